@@ -343,6 +343,96 @@ fs_status fs_hvp_x(const float* X, const float* a, int64_t n,
 int64_t fs_hvp_workspace_bytes(int64_t n, int64_t m, int32_t d, const fs_options* opt);
 
 /*
+ * Cross attention.  The plan of fs_apply_plan is normalised over both sides;
+ * softmax attention is the same streamed, biased dot-product weighting
+ * normalised over the keys alone, for each head, in 16-bit types, and these
+ * entry points give it with its gradients.  With queries q (batch x n x heads
+ * x d) and an encoder's keys and values k, v (batch x m x kv_heads x d; query
+ * head h reads key head g = h / (heads / kv_heads)):
+ *     z_ij  = scale q_i . k_j + bias[h][ bucket(j - (q_pos[b] + i)) ]
+ *     lse_i = log sum_j exp(z_ij),   out_i = sum_j exp(z_ij - lse_i) v_j
+ * over the keys j that count: j < kv_len[b] and key_mask[b][j] != 0.  A query
+ * that no key counts for (or whose scores are all -inf) has out = 0 and
+ * lse = -inf.  Keys and values that do not count are never used, whatever
+ * they hold (NaN and infinities included).
+ *
+ * Relative position bias.  bucket(r) = bias_buckets[clamp(r, -D, D) + D] with
+ * D = max_distance; bias is heads x n_buckets (or one row that all heads
+ * share, bias_stride = 0) of the type of q.  Its n x m form is never stored,
+ * and neither are the scores nor their gradients.  Bucket numbers outside
+ * [0, n_buckets) are taken to the nearest end.  A bias below -1e30 forbids
+ * its pairs, as -inf does.
+ *
+ * Numerics: products of 16-bit operands are summed in float32; the softmax,
+ * lse and every sum over keys or queries are float32; the probabilities (and
+ * the score gradients) are rounded once to the type of q as operands of the
+ * next product, results once at the end.  Results are bitwise deterministic.
+ */
+typedef enum {
+    FS_DTYPE_BF16 = 0,
+    FS_DTYPE_F16 = 1
+} fs_dtype;
+
+/*
+ * Description of one attention call.  All arrays are DEVICE memory.  Strides
+ * are in elements, {batch, token, head}; the d elements of a head are
+ * contiguous; strides are not negative, and an input may repeat (stride 0).
+ * Tensors whose address and strides are multiples of 16 bytes and whose d is
+ * a multiple of 8 are read in place; others are first copied to the
+ * workspace.
+ */
+typedef struct fs_attention {
+    int32_t dtype;            /* fs_dtype of q, k, v, bias and every result but lse */
+    int32_t heads, kv_heads;  /* heads is a multiple of kv_heads */
+    int32_t d;                /* elements per head, 1 .. 128 */
+    int64_t batch, n, m;      /* sequences, queries and keys of each; 0 allowed */
+    float scale;              /* > 0, finite */
+    int32_t n_buckets;        /* 0: no bias; at most 1024 */
+    int32_t max_distance;     /* D, 1 .. 2048, with a bias */
+    int32_t reserved;         /* must be zero */
+    int64_t q_stride[3], k_stride[3], v_stride[3], out_stride[3];
+    int64_t dout_stride[3], dq_stride[3], dk_stride[3], dv_stride[3]; /* gradients only */
+    const int32_t* kv_len;        /* [batch], taken into [0, m]; NULL: m */
+    const uint8_t* key_mask;      /* batch rows of m, mask_stride apart; NULL: ones */
+    int64_t mask_stride;
+    const void* bias;             /* heads (or 1) rows of n_buckets, bias_stride apart */
+    int64_t bias_stride;
+    const int32_t* bias_buckets;  /* [2 max_distance + 1] */
+    const int32_t* q_pos;         /* [batch] position of the first query; NULL: 0 */
+} fs_attention;
+
+/*
+ * fs_cross_attention -- forward pass: out (batch x n x heads x d) and lse
+ * (float32, batch x heads x n, contiguous; natural logarithm).  Few queries
+ * against many keys (single tokens against a cache) take a kernel that splits
+ * the keys over the GPU.
+ * Enqueued on `stream`; can be captured in a CUDA graph after one call of
+ * the same sizes outside the capture.
+ * Errors: FS_ERR_INVALID_ARG for null or host pointers, sizes, strides or
+ * options out of range; FS_ERR_UNSUPPORTED for more than 2^31 - 1 tiles of
+ * work; FS_ERR_OOM, FS_ERR_CUDA, FS_ERR_TIMEOUT (from fs_check) as above.
+ */
+fs_status fs_cross_attention(const fs_attention* at, const void* q, const void* k, const void* v,
+                             void* out, float* lse, void* stream);
+
+/*
+ * fs_cross_attention_grad -- gradients of fs_cross_attention for the gradient
+ * dout of out, with out and lse as the forward pass wrote them:
+ *     D_i = dout_i . out_i,  ds_ij = p_ij (dout_i . v_j - D_i),  p_ij = exp(z_ij - lse_i)
+ *     dq_i = scale sum_j ds_ij k_j,   dk_j = scale sum_{h of g, i} ds_ij q_i,
+ *     dv_j = sum_{h of g, i} p_ij dout_i,
+ *     dbias[h][u] = sum of ds_ij over batches and pairs of bucket u
+ * (the sum over all heads too, one row, when bias_stride = 0).  dq, dk, dv as
+ * q, k, v (their own strides); dbias rows of n_buckets, contiguous, of the
+ * type of q, or NULL when its gradient is not wanted.  Keys that do not count
+ * get zero gradients.  Errors as fs_cross_attention.
+ */
+fs_status fs_cross_attention_grad(const fs_attention* at, const void* q, const void* k,
+                                  const void* v, const void* out, const float* lse,
+                                  const void* dout, void* dq, void* dk, void* dv, void* dbias,
+                                  void* stream);
+
+/*
  * fs_unit_rates -- measure, on the current GPU, the per-SM issue rates that
  * bound the exponent-heavy half-updates (no counterpart on the pages: it
  * supplies the denominators of the ALU roofline).  Throughput kernels with

@@ -37,7 +37,8 @@ EXPORTED = ("fs_sinkhorn_solve", "fs_apply_plan", "fs_barycentric", "fs_grad_x",
             "fs_timing_read", "fs_sinkhorn_solve_noalloc", "fs_unit_rates", "fs_hvp_x",
             "fs_sparse_solve", "fs_morton_order", "fs_sparse_screen", "fs_wait_selftest",
             "fs_debug_bounds", "fs_shard_unit", "fs_shard_range", "fs_fixup_stats",
-            "fs_hvp_workspace_bytes", "fs_barrier_selftest")
+            "fs_hvp_workspace_bytes", "fs_barrier_selftest", "fs_cross_attention",
+            "fs_cross_attention_grad")
 
 
 class FlashSinkhornError(RuntimeError):
@@ -70,6 +71,21 @@ class fs_sparse_report(ctypes.Structure):
                 ("kept_pairs", ctypes.c_double), ("exact_bounds", ctypes.c_double),
                 ("fixed_rows", ctypes.c_double), ("lift_checks", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("lift_error", ctypes.c_double)]
+
+
+class fs_attention(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("d", ctypes.c_int32), ("batch", ctypes.c_int64),
+                ("n", ctypes.c_int64), ("m", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("n_buckets", ctypes.c_int32), ("max_distance", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("q_stride", ctypes.c_int64 * 3),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("out_stride", ctypes.c_int64 * 3), ("dout_stride", ctypes.c_int64 * 3),
+                ("dq_stride", ctypes.c_int64 * 3), ("dk_stride", ctypes.c_int64 * 3),
+                ("dv_stride", ctypes.c_int64 * 3), ("kv_len", ctypes.c_void_p),
+                ("key_mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64),
+                ("bias", ctypes.c_void_p), ("bias_stride", ctypes.c_int64),
+                ("bias_buckets", ctypes.c_void_p), ("q_pos", ctypes.c_void_p)]
 
 
 _lib = None
@@ -145,6 +161,11 @@ def load_library(path: Optional[str] = None):
         lib.fs_hvp_workspace_bytes.restype = i64
         lib.fs_barrier_selftest.argtypes = [i64, vp]
         lib.fs_barrier_selftest.restype = ctypes.c_int
+        att = ctypes.POINTER(fs_attention)
+        lib.fs_cross_attention.argtypes = [att] + [vp] * 6
+        lib.fs_cross_attention.restype = ctypes.c_int
+        lib.fs_cross_attention_grad.argtypes = [att] + [vp] * 11
+        lib.fs_cross_attention_grad.restype = ctypes.c_int
         if path is None:
             _lib = lib
         return lib
@@ -568,3 +589,175 @@ def fs_barrier_selftest(timeout_ns: int = 1_000_000, *, stream=None) -> None:
     """Run the one-launch solve's grid barrier with a block that never
     arrives (see the C header); the next fs_check() raises FS_ERR_TIMEOUT."""
     _raise(load_library().fs_barrier_selftest(int(timeout_ns), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# cross attention (16-bit CUDA tensors)
+
+def fs_relative_buckets(num_buckets: int, max_distance: int, bidirectional: bool = True):
+    """Buckets of the relative positions -max_distance .. max_distance (int32
+    numpy array of 2 max_distance + 1 entries, the `bias_buckets` of
+    fs_cross_attention once on the GPU).
+
+    A relative position is key minus query.  Bidirectional: half of the
+    buckets for keys up to the query, half for later ones.  Otherwise later
+    keys share bucket 0 with the query's own position.  Of a side's buckets
+    the first half hold one distance each; the rest widen geometrically up to
+    max_distance, the last holding all beyond.  The boundaries are those of
+    exact (integer) arithmetic.
+    """
+    nb, far = int(num_buckets), int(max_distance)
+    side = nb // 2 if bidirectional else nb
+    near = side // 2
+    if nb < 2 or (bidirectional and nb % 2) or near < 1 or far <= near:
+        raise ValueError(f"num_buckets={num_buckets}, max_distance={max_distance}: need an even "
+                         "number of at least 4 (2 with bidirectional=False) buckets and a "
+                         "max_distance above the single distances")
+    wide = side - near
+    one_side = []
+    step = 0
+    for a in range(far + 1):
+        if a < near:
+            one_side.append(a)
+            continue
+        # largest step < wide with near (far / near)^(step / wide) <= a
+        while step + 1 < wide and near ** wide * far ** (step + 1) <= a ** wide * near ** (step + 1):
+            step += 1
+        one_side.append(near + step)
+    below = one_side[:0:-1]
+    above = [side + b for b in one_side[1:]] if bidirectional else [0] * far
+    return np.array(below + [0] + above, dtype=np.int32)
+
+
+def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos) -> fs_attention:
+    """Checked description of a call (see the C header for each field)."""
+    import torch
+    if not (_is_torch(q) and q.is_cuda and q.dtype in (torch.bfloat16, torch.float16)):
+        raise TypeError("q must be a bfloat16 or float16 CUDA tensor")
+    if q.dim() != 4:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected (batch, n, heads, d)")
+    batch, n, heads, d = q.shape
+    if k.dim() != 4:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected (batch, m, kv_heads, d)")
+    m, kv_heads = k.shape[1], k.shape[2]
+    at = fs_attention()
+    at.dtype = 0 if q.dtype == torch.bfloat16 else 1
+    at.heads, at.kv_heads, at.d, at.batch, at.n, at.m = heads, kv_heads, d, batch, n, m
+    at.scale = d ** -0.5 if scale is None else scale
+    at.q_stride = _att_strides(q, "q", q.shape, q)
+    at.k_stride = _att_strides(k, "k", (batch, m, kv_heads, d), q)
+    at.v_stride = _att_strides(v, "v", (batch, m, kv_heads, d), q)
+    if kv_len is not None:
+        at.kv_len = _i_ptr(kv_len, "kv_len", (batch,), torch.int32)
+    if key_mask is not None:
+        if not (key_mask.is_cuda and key_mask.dtype in (torch.bool, torch.uint8)):
+            raise TypeError("key_mask must be a bool or uint8 CUDA tensor")
+        if tuple(key_mask.shape) != (batch, m):
+            raise ValueError(f"key_mask has shape {tuple(key_mask.shape)}, expected {(batch, m)}")
+        if m > 1 and key_mask.stride(1) != 1:
+            raise TypeError("the keys of key_mask must be contiguous")
+        at.key_mask, at.mask_stride = key_mask.data_ptr(), key_mask.stride(0)
+    if (bias is None) != (bias_buckets is None):
+        raise TypeError("bias and bias_buckets come together")
+    if bias is not None:
+        if not (bias.is_cuda and bias.dtype == q.dtype):
+            raise TypeError(f"bias must be a CUDA tensor of {q.dtype}")
+        if bias.dim() != 2 or bias.shape[0] not in (1, heads) or bias.shape[1] < 1:
+            raise ValueError(f"bias has shape {tuple(bias.shape)}, expected ({heads} or 1, buckets)")
+        if bias.shape[1] > 1 and bias.stride(1) != 1:
+            raise TypeError("the buckets of bias must be contiguous")
+        size = bias_buckets.numel()
+        if size % 2 == 0:
+            raise ValueError("bias_buckets must have 2 max_distance + 1 entries")
+        at.n_buckets, at.max_distance = bias.shape[1], size // 2
+        at.bias = bias.data_ptr()
+        at.bias_stride = 0 if bias.shape[0] == 1 else bias.stride(0)
+        at.bias_buckets = _i_ptr(bias_buckets, "bias_buckets", (size,), torch.int32)
+        if q_pos is not None:
+            at.q_pos = _i_ptr(q_pos, "q_pos", (batch,), torch.int32)
+    return at
+
+
+_strides3 = ctypes.c_int64 * 3
+
+
+def _att_strides(x, name: str, shape, like):
+    if not (_is_torch(x) and x.is_cuda and x.dtype == like.dtype and x.device == like.device):
+        raise TypeError(f"{name} must be a {like.dtype} tensor on {like.device}")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    sb, st, sh, sd = x.stride()
+    if sd != 1 and x.shape[3] > 1:
+        raise TypeError(f"the last dimension of {name} must be contiguous")
+    return _strides3(sb, st, sh)
+
+
+def _att_empty(shape, dtype, like, stream):
+    """A result, allocated for the stream that writes it."""
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=like.device)
+    return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def fs_cross_attention(q, k, v, *, scale: Optional[float] = None, kv_len=None, key_mask=None,
+                       bias=None, bias_buckets=None, q_pos=None, out=None, lse=None,
+                       stream=None) -> Tuple:
+    """Softmax attention of q (batch, n, heads, d) over an encoder's k and v
+    (batch, m, kv_heads, d), bfloat16 or float16, any strides with contiguous
+    d <= 128.  Returns (out, lse): out as q, lse float32 (batch, heads, n).
+
+    scale         factor of the dot products, d ** -0.5 if None
+    kv_len        int32 (batch,): keys j >= kv_len[b] do not count
+    key_mask      bool or uint8 (batch, m): keys with 0 do not count
+    bias          learned relative position bias, (heads or 1, buckets) of q's
+                  type: z_ij += bias[h, bias_buckets[clamp(j - (q_pos[b] + i), -D, D) + D]]
+    bias_buckets  int32 (2 D + 1,), e.g. from fs_relative_buckets, D <= 2048
+    q_pos         int32 (batch,): position of each sequence's first query (0 if
+                  None), e.g. the step of a decoder that sends one token at a time
+    A query without a counted key has out 0 and lse -inf; keys and values that
+    do not count may hold anything.
+    """
+    import torch
+    at = _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos)
+    if out is None:
+        out = _att_empty(q.shape, q.dtype, q, stream)
+    if lse is None:
+        lse = _att_empty((at.batch, at.heads, at.n), torch.float32, q, stream)
+    at.out_stride = _att_strides(out, "out", q.shape, q)
+    st = load_library().fs_cross_attention(
+        ctypes.byref(at), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+        _ptr(lse, "lse", (at.batch, at.heads, at.n)), _stream(stream, q))
+    _raise(st)
+    return out, lse
+
+
+def fs_cross_attention_grad(q, k, v, out, lse, dout, *, scale: Optional[float] = None,
+                            kv_len=None, key_mask=None, bias=None, bias_buckets=None, q_pos=None,
+                            dq=None, dk=None, dv=None, dbias=None, stream=None) -> Tuple:
+    """Gradients of fs_cross_attention for the gradient dout of its out; out
+    and lse as it returned them, the other arguments as it got them.  Returns
+    (dq, dk, dv, dbias), each as its input (dbias None without a bias)."""
+    at = _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos)
+    at.out_stride = _att_strides(out, "out", q.shape, q)
+    at.dout_stride = _att_strides(dout, "dout", q.shape, q)
+    dq = _att_empty(q.shape, q.dtype, q, stream) if dq is None else dq
+    dk = _att_empty(k.shape, q.dtype, q, stream) if dk is None else dk
+    dv = _att_empty(v.shape, q.dtype, q, stream) if dv is None else dv
+    at.dq_stride = _att_strides(dq, "dq", q.shape, q)
+    at.dk_stride = _att_strides(dk, "dk", k.shape, q)
+    at.dv_stride = _att_strides(dv, "dv", v.shape, q)
+    if bias is not None:
+        dbias = _att_empty(bias.shape, q.dtype, q, stream) if dbias is None else dbias
+        if not (dbias.is_cuda and dbias.dtype == q.dtype and dbias.is_contiguous()
+                and dbias.shape == bias.shape):
+            raise TypeError(f"dbias must be a contiguous {q.dtype} tensor of shape "
+                            f"{tuple(bias.shape)}")
+    st = load_library().fs_cross_attention_grad(
+        ctypes.byref(at), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+        _ptr(lse, "lse", (at.batch, at.heads, at.n)), dout.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), dbias.data_ptr() if bias is not None else None,
+        _stream(stream, q))
+    _raise(st)
+    return dq, dk, dv, dbias if bias is not None else None

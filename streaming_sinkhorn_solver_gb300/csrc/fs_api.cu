@@ -34,7 +34,7 @@ fs_status fail(fs_status st, const char* fmt, ...) {
     return st;
 }
 
-fs_status begin_call(Call& c, void* stream) {
+fs_status begin_call(Call& c, void* stream, bool scratch) {
     FS_CUDA(cudaGetDevice(&c.dev));
     if (c.dev < 0 || c.dev >= kMaxDevices) return fail(FS_ERR_UNSUPPORTED, "device index %d", c.dev);
     c.stream = static_cast<cudaStream_t>(stream);
@@ -55,7 +55,7 @@ fs_status begin_call(Call& c, void* stream) {
     }
     // order this call after the previous one if that ran on another stream (a
     // captured call is ordered by the graph's user instead)
-    if (!c.capturing && w.used && w.last_stream != c.stream)
+    if (scratch && !c.capturing && w.used && w.last_stream != c.stream)
         FS_CUDA(cudaStreamWaitEvent(c.stream, w.done, 0));
     return FS_OK;
 }

@@ -1,7 +1,7 @@
 // C ABI of cross attention: argument checks, workspace, choice of kernels.
-#include "fs_host.cuh"
-#include "fs_attn.cuh"
+#include "fs_attn_host.cuh"
 
+#include <algorithm>
 #include <cmath>
 
 namespace fs {
@@ -109,10 +109,79 @@ fs_status check_tiles(double tiles) {
     return FS_OK;
 }
 
+bool aligned16(const View& w, int B, int tokens, int heads) {
+    return (reinterpret_cast<uintptr_t>(w.p) & 15) == 0 && (tokens <= 1 || w.st % 8 == 0) &&
+           (heads <= 1 || w.sh % 8 == 0) && (B <= 1 || w.sb % 8 == 0);
+}
+
+// What a tensor map can describe: 16-byte steps, below 2^40 bytes, and tokens
+// that differ.
+bool mappable(const View& w, int B, int tokens, int heads, int d) {
+    constexpr int64_t far = int64_t(1) << 39;
+    return d % 8 == 0 && aligned16(w, B, tokens, heads) && (tokens <= 1 || w.st > 0) && w.st < far &&
+           w.sh < far && w.sb < far;
+}
+
+// An input that the kernels read through a tensor map: in place, or from a
+// copy in the workspace with rows of 16-byte multiples.
+struct Input {
+    View* w;
+    int tokens, heads;
+    bool copy = false;
+    size_t off = 0;
+    Input(View& v, int t, int h) : w(&v), tokens(t), heads(h) {}
+    void plan(const Args& a, Layout& L) {
+        copy = !mappable(*w, a.B, tokens, heads, a.d);
+        if (copy) off = L.take(2 * (size_t)a.B * tokens * heads * pitch(a));
+    }
+    static int pitch(const Args& a) { return (a.d + 7) / 8 * 8; }
+    fs_status run(const Call& c, const Args& a) {
+        if (!copy) return FS_OK;
+        const int dp = pitch(a);
+        void* to = c.at<void>(off);
+        FS_CUDA(launch_pack(*w, to, a.B, tokens, heads, a.d, dp, c.stream));
+        w->p = to;
+        w->sh = dp;
+        w->st = (int64_t)heads * dp;
+        w->sb = (int64_t)tokens * heads * dp;
+        return FS_OK;
+    }
+};
+
+// The key tiles of a mask.
+struct TilePlan {
+    KeyTiles kt = {};
+    size_t words = 0, list = 0, count = 0;
+    void plan(const Args& a, Layout& L) {
+        kt.tiles = (a.m + kTile - 1) / kTile;
+        if (!a.mask) return;
+        words = L.take(sizeof(uint4) * (size_t)a.B * kt.tiles);
+        list = L.take(sizeof(int) * (size_t)a.B * kt.tiles);
+        count = L.take(sizeof(int) * (size_t)a.B);
+    }
+    fs_status run(const Call& c, const Args& a) {
+        if (!a.mask) return FS_OK;
+        kt.words = c.at<uint4>(words);
+        kt.list = c.at<int>(list);
+        kt.count = c.at<int>(count);
+        FS_CUDA(launch_key_tiles(a, c.at<uint4>(words), c.at<int>(list), c.at<int>(count), kt.tiles,
+                                 c.stream));
+        return FS_OK;
+    }
+};
+
+// Splits of the keys: enough blocks for every SM, of two key tiles at least.
+int choose_key_splits(int64_t blocks, int tiles, int sms) {
+    int64_t s = blocks >= sms ? 1 : sms / blocks;
+    s = std::min<int64_t>(s, (tiles + 1) / 2);
+    return (int)std::max<int64_t>(s, 1);
+}
+
 fs_status forward_entry(const fs_attention* at, const void* q, const void* k, const void* v,
                         void* out, float* lse, void* stream) {
     FS_TRY(check_desc(at));
-    Args a = {};
+    FwdArgs p = {};
+    Args& a = p.a;
     FS_TRY(fill(a, at));
     FS_TRY(view(a.q, q, at->q_stride, at->batch, at->n, a.H, a.d, false, "q"));
     FS_TRY(view(a.k, k, at->k_stride, at->batch, at->m, a.G, a.d, false, "k"));
@@ -121,18 +190,55 @@ fs_status forward_entry(const fs_attention* at, const void* q, const void* k, co
     FS_TRY(check_ptr(lse, at->batch * at->n, "lse"));
     a.lse = lse;
     FS_TRY(check_tiles((double)at->batch * a.H * at->n));
+    FS_TRY(check_tiles((double)at->batch * a.G * at->m));
     const int64_t rows = at->batch * a.H * at->n;
     if (rows == 0) return FS_OK;
     NvtxRange range("fs_cross_attention");
-    FS_CUDA(launch_forward_simple(a, static_cast<cudaStream_t>(stream)));
-    return FS_OK;
+    Call c;
+    if (a.m == 0) {
+        FS_TRY(begin_call(c, stream, false));
+        FS_CUDA(launch_zero(a, a.o, a.n, a.H, lse, c.stream));
+        return FS_OK;
+    }
+    Input inputs[3] = {{a.q, a.n, a.H}, {a.k, a.m, a.G}, {a.v, a.m, a.G}};
+    TilePlan tiles;
+    for (Input& x : inputs) x.plan(a, c.L);
+    tiles.plan(a, c.L);
+    int dev = 0, sms = 0;
+    FS_CUDA(cudaGetDevice(&dev));
+    FS_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    p.row_blocks = (a.n + 2 * kTile - 1) / (2 * kTile);
+    p.splits = choose_key_splits((int64_t)p.row_blocks * a.H * a.B, tiles.kt.tiles, sms);
+    size_t part_out = 0, part_lse = 0;
+    if (p.splits > 1) {
+        part_out = c.L.take(sizeof(float) * (size_t)p.splits * rows * a.d);
+        part_lse = c.L.take(sizeof(float) * (size_t)p.splits * rows);
+    }
+    const bool scratch = c.L.off > 0;
+    FS_TRY(begin_call(c, stream, scratch));
+    FS_TRY(ensure_capacity(c));
+    for (Input& x : inputs) FS_TRY(x.run(c, a));
+    FS_TRY(tiles.run(c, a));
+    p.kt = tiles.kt;
+    p.part.rows = rows;
+    p.part.out = p.splits > 1 ? c.at<float>(part_out) : nullptr;
+    p.part.lse2 = p.splits > 1 ? c.at<float>(part_lse) : nullptr;
+    p.out_vec = a.d % 8 == 0 && aligned16(a.o, a.B, a.n, a.H);
+    a.err = c.ws->err_word;
+    FS_TRY(make_tensor_map(p.q, a.q, a.B, a.n, a.H, a.d, a.bf16));
+    FS_TRY(make_tensor_map(p.k, a.k, a.B, a.m, a.G, a.d, a.bf16));
+    FS_TRY(make_tensor_map(p.v, a.v, a.B, a.m, a.G, a.d, a.bf16));
+    FS_CUDA(launch_forward_tc(p, c.stream));
+    if (p.splits > 1) FS_CUDA(launch_combine(a, p.part, p.splits, c.stream));
+    return scratch ? end_call(c) : FS_OK;
 }
 
 fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const void* v,
                      const void* out, const float* lse, const void* dout, void* dq, void* dk,
                      void* dv, void* dbias, void* stream) {
     FS_TRY(check_desc(at));
-    Args a = {};
+    GradArgs p = {};
+    Args& a = p.a;
     FS_TRY(fill(a, at));
     FS_TRY(view(a.q, q, at->q_stride, at->batch, at->n, a.H, a.d, false, "q"));
     FS_TRY(view(a.k, k, at->k_stride, at->batch, at->m, a.G, a.d, false, "k"));
@@ -147,18 +253,49 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     if (dbias) FS_TRY(check_ptr(dbias, 1, "dbias"));
     a.lse = const_cast<float*>(lse);
     FS_TRY(check_tiles((double)at->batch * a.H * at->n));
-    const int64_t rows = at->batch * a.H * at->n;
     FS_TRY(check_tiles((double)at->batch * a.G * at->m));
     NvtxRange range("fs_cross_attention_grad");
     Call c;
+    if (a.n == 0 || a.m == 0 || a.B == 0) {
+        FS_TRY(begin_call(c, stream, false));
+        FS_CUDA(launch_zero(a, a.dq, a.n, a.H, nullptr, c.stream));
+        FS_CUDA(launch_zero(a, a.dk, a.m, a.G, nullptr, c.stream));
+        FS_CUDA(launch_zero(a, a.dv, a.m, a.G, nullptr, c.stream));
+        if (dbias)
+            FS_CUDA(cudaMemsetAsync(dbias, 0, 2 * (size_t)(a.table_stride ? a.H : 1) * a.nb, c.stream));
+        return FS_OK;
+    }
+    Input inputs[4] = {{a.q, a.n, a.H}, {a.k, a.m, a.G}, {a.v, a.m, a.G}, {a.dout, a.n, a.H}};
+    TilePlan tiles;
+    for (Input& x : inputs) x.plan(a, c.L);
+    tiles.plan(a, c.L);
+    p.q_tiles = (a.n + kTile - 1) / kTile;
+    p.k_tiles = tiles.kt.tiles;
+    const size_t blocks = (size_t)a.B * a.H * p.q_tiles;
+    const size_t rows = c.L.take(sizeof(float) * blocks * 2 * kTile);
+    const size_t part = c.L.take(dbias ? sizeof(float) * blocks * (2 * (size_t)a.D + 1) : 0);
     FS_TRY(begin_call(c, stream));
-    const size_t o_delta = c.L.take(sizeof(float) * (size_t)rows);
-    const size_t o_part = c.L.take(dbias ? sizeof(float) * (size_t)rows * a.nb : 0);
     FS_TRY(ensure_capacity(c));
-    a.delta = c.at<float>(o_delta);
-    a.bias_part = dbias ? c.at<float>(o_part) : nullptr;
+    for (Input& x : inputs) FS_TRY(x.run(c, a));
+    FS_TRY(tiles.run(c, a));
+    p.kt = tiles.kt;
+    p.rows = c.at<float>(rows);
+    a.bias_part = dbias ? c.at<float>(part) : nullptr;
     a.err = c.ws->err_word;
-    FS_CUDA(launch_grad_simple(a, dbias, c.stream));
+    auto vec = [&](const View& w, int tokens, int heads) {
+        return a.d % 8 == 0 && aligned16(w, a.B, tokens, heads);
+    };
+    p.q_vec = vec(a.q, a.n, a.H);
+    p.dout_vec = vec(a.dout, a.n, a.H);
+    p.o_vec = vec(a.o, a.n, a.H);
+    p.dq_vec = vec(a.dq, a.n, a.H);
+    p.dk_vec = vec(a.dk, a.m, a.G);
+    p.dv_vec = vec(a.dv, a.m, a.G);
+    FS_TRY(make_tensor_map(p.q, a.q, a.B, a.n, a.H, a.d, a.bf16));
+    FS_TRY(make_tensor_map(p.k, a.k, a.B, a.m, a.G, a.d, a.bf16));
+    FS_TRY(make_tensor_map(p.v, a.v, a.B, a.m, a.G, a.d, a.bf16));
+    FS_TRY(make_tensor_map(p.dout, a.dout, a.B, a.n, a.H, a.d, a.bf16));
+    FS_CUDA(launch_grad_tc(p, dbias, c.stream));
     return end_call(c);
 }
 

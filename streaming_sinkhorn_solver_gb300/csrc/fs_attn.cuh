@@ -36,8 +36,7 @@ struct Args {
     const int32_t* buckets;      // [2 D + 1]
     int nb, D;
     const int32_t* q_pos;        // [B] or nullptr
-    float* delta;                // [B][H][n]: dout_i . out_i (gradients)
-    float* bias_part;            // partial sums of the bias gradient
+    float* bias_part;            // [H][B][query tiles][2 D + 1] sums of the bias gradient, or nullptr
     uint32_t* err;               // device error word
 };
 
@@ -60,9 +59,6 @@ __device__ __forceinline__ int key_end(const Args& a, int b) {
     const int l = __ldg(a.kv_len + b);
     return l < 0 ? 0 : (l < a.m ? l : a.m);
 }
-__device__ __forceinline__ bool key_counts(const Args& a, int b, int j, int end) {
-    return j < end && (a.mask == nullptr || __ldg(a.mask + (int64_t)b * a.mask_stride + j) != 0);
-}
 
 __device__ __forceinline__ int bucket_of(const Args& a, int64_t rel) {
     const int64_t r = rel < -a.D ? -a.D : (rel > a.D ? a.D : rel);
@@ -76,9 +72,6 @@ __device__ __forceinline__ int bucket_of(const Args& a, int64_t rel) {
 __device__ __forceinline__ float bias2(float v) {
     return v < -1e30f ? -INFINITY : v * (float)kLog2e;
 }
-
-cudaError_t launch_forward_simple(const Args& a, cudaStream_t s);
-cudaError_t launch_grad_simple(const Args& a, void* dbias, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace fs

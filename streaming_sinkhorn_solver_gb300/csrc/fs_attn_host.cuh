@@ -1,0 +1,58 @@
+// Launch interfaces of the cross-attention kernels.
+#pragma once
+
+#include "fs_attn_tc.cuh"
+#include "fs_host.cuh"
+
+namespace fs {
+namespace attn {
+
+// A tensor as 64 x 128 boxes of (d, token, head, batch); a repeated (stride 0)
+// head or batch is one entry of the map, its index multiplied by 0.
+struct TensorMap {
+    CUtensorMap map;
+    int head, batch;   // index factors, 0 or 1
+};
+
+// Row sums over part of the keys, joined by k_combine: rows are (b, h, i)
+struct Partials {
+    float* out;        // [splits][rows][d], divided by its own sum
+    float* lse2;       // [splits][rows], base 2
+    int64_t rows;
+};
+
+struct FwdArgs {
+    TensorMap q, k, v;
+    Args a;
+    KeyTiles kt;
+    Partials part;
+    int row_blocks, splits;
+    int out_vec;       // the rows of out take 16-byte stores
+};
+
+struct GradArgs {
+    TensorMap q, k, v, dout;
+    Args a;
+    KeyTiles kt;
+    float* rows;       // [B][H][q_tiles][-lse2 of 128 queries, delta of 128 queries]
+    int q_tiles, k_tiles;
+    int stages, kv_stages;     // set at launch
+    int q_vec, dout_vec, o_vec, dq_vec, dk_vec, dv_vec;   // rows take 16-byte accesses
+};
+
+// dq, then dk and dv, then dbias (nullptr: none)
+cudaError_t launch_grad_tc(const GradArgs& p, void* dbias, cudaStream_t s);
+cudaError_t launch_forward_tc(const FwdArgs& p, cudaStream_t s);
+cudaError_t launch_combine(const Args& a, const Partials& part, int splits, cudaStream_t s);
+cudaError_t launch_key_tiles(const Args& a, uint4* words, int* list, int* count, int tiles,
+                             cudaStream_t s);
+// out = 0, lse = -inf (no keys), or zero gradients
+cudaError_t launch_zero(const Args& a, const View& w, int tokens, int heads, float* lse, cudaStream_t s);
+// contiguous copy of a (batch, token, head, d) tensor with rows of dp elements, zero beyond d
+cudaError_t launch_pack(const View& from, void* to, int B, int tokens, int heads, int d, int dp,
+                        cudaStream_t s);
+
+fs_status make_tensor_map(TensorMap& t, const View& w, int B, int tokens, int heads, int d, bool bf16);
+
+}  // namespace attn
+}  // namespace fs

@@ -1,0 +1,227 @@
+// Tensor-core building blocks of the cross-attention kernels, beyond those of
+// fs_tc.cuh: tensor-map copies of 64 x 128 boxes of a (batch, token, head, d)
+// tensor, tcgen05.mma with its A operand in TMEM, and operand tiles read with
+// their rows as the summed dimension.
+//
+// Shared-memory tiles: 128 tokens x 64 elements, one 128-byte row per token in
+// the 128-byte swizzle (tc::CHUNK_BYTES); a head of d > 64 takes two, one after
+// the other.  Such a tile is an operand over d (K-major) for the score
+// products, and over tokens (MN-major: the d elements are contiguous) for the
+// products that sum over tokens.
+#pragma once
+
+#include "fs_attn.cuh"
+#include "fs_tc.cuh"
+
+#include <cuda.h>
+
+namespace fs {
+namespace attn {
+
+using namespace fs::tc;
+
+constexpr int kTile = 128;   // tokens of a tile
+
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int c0, int token, int head,
+                                         int batch, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(token), "r"(head), "r"(batch), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// A whole warp waits (mbar_wait's branches are uniform, so its result is made so
+// and the warp joined before the warp-collective instructions that follow).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code) {
+    __syncwarp();
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, err, code);
+    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+    // every lane observes the completed phase itself
+    if (ok) ok = mbar_try_wait(bar, parity);
+    return __all_sync(0xffffffffu, ok);
+}
+
+// one lane of a converged warp: the issuer of its copies and products
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]; A holds two 16-bit elements of a row per column
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Operand summed over the tokens of a tile: element (token, c) at row token of
+// the 64-element chunk c / 64.  Groups of 8 tokens are 1024 bytes apart, the
+// next 64 elements a chunk apart; 16 tokens on, the start address is 2048 bytes up.
+__device__ __forceinline__ uint64_t sdesc_tokens(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(CHUNK_BYTES >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// kind::f16 with float32 sums; b_tokens: B is summed over its rows
+__host__ __device__ constexpr uint32_t idesc_16(bool bf16, int N, bool b_tokens) {
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
+           ((b_tokens ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// 32 lanes x 16 columns: thread t gets lane t
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]),
+          "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+}
+
+// D[tmem] = A * B^T over the d elements of two 128-token tiles (chunks of 64), `steps`
+// products of 16 elements.  One elected thread.
+__device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                           int steps) {
+#pragma unroll 1
+    for (int x = 0; x < steps; ++x) {
+        const uint64_t o = (uint64_t)((x >> 2) * (CHUNK_BYTES >> 4) + 2 * (x & 3));
+        mma_f16(d_tmem, a + o, b + o, idesc, x != 0);
+    }
+}
+// the same with A in TMEM
+__device__ __forceinline__ void mma_over_d_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                              int steps) {
+#pragma unroll 1
+    for (int x = 0; x < steps; ++x)
+        mma_f16_ts(d_tmem, a_tmem + 8 * x, b + (uint64_t)((x >> 2) * (CHUNK_BYTES >> 4) + 2 * (x & 3)),
+                   idesc, x != 0);
+}
+// D[tmem] (+)= A[tmem] * B over the 128 tokens of B's tile; tokens 64..127 of A
+// are `half` columns on from its first.  One elected thread.
+__device__ __forceinline__ void mma_over_tokens(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                                uint32_t idesc, bool accumulate, uint32_t half = 32) {
+#pragma unroll
+    for (int x = 0; x < kTile / 16; ++x)
+        mma_f16_ts(d_tmem, a_tmem + (x >> 2) * half + 8 * (x & 3), b + 128 * x, idesc,
+                   accumulate || x != 0);
+}
+
+// Position in a ring of `n` stages: slot, and the parity its next use completes with.
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step(int by, int n) {
+        slot += by;
+        if (slot >= n) {
+            slot -= n;
+            phase ^= 1u;
+        }
+    }
+};
+
+// warp: 32 registers into 32 consecutive columns of the warp's lanes
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+        "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+        "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                     taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// two floats rounded to one register, x in the low half
+template <bool BF>
+__device__ __forceinline__ uint32_t pack16(float x, float y) {
+    uint32_t r;
+    if (BF)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+    return r;
+}
+
+// Tiles of 128 keys a sequence visits, and which of a tile's keys count.
+struct KeyTiles {
+    const uint4* words;     // [B][tiles] bits of counted keys, or nullptr (no mask)
+    const int* list;        // [B][tiles] tiles with a counted key, in order
+    const int* count;       // [B]
+    int tiles;              // ceil(m / 128)
+};
+__device__ __forceinline__ int tile_count(const KeyTiles& kt, int b, int end) {
+    return kt.list ? __ldg(kt.count + b) : (end + kTile - 1) / kTile;
+}
+__device__ __forceinline__ int tile_at(const KeyTiles& kt, int b, int j) {
+    return kt.list ? __ldg(kt.list + (int64_t)b * kt.tiles + j) : j;
+}
+// counted keys of a tile as 128 bits
+__device__ __forceinline__ uint4 tile_words(const KeyTiles& kt, int b, int tile, int end) {
+    if (kt.words) return __ldg(kt.words + (int64_t)b * kt.tiles + tile);
+    const int left = end - tile * kTile;   // >= 1
+    auto w = [&](int k) -> uint32_t {
+        const int c = left - 32 * k;
+        return c <= 0 ? 0u : (c >= 32 ? 0xffffffffu : (1u << c) - 1u);
+    };
+    return make_uint4(w(0), w(1), w(2), w(3));
+}
+__device__ __forceinline__ bool all_count(const uint4& w) {
+    return (w.x & w.y & w.z & w.w) == 0xffffffffu;
+}
+
+// One whole warp: zeroes the rows of a landed tile whose keys do not count (what
+// such keys hold would otherwise enter sums as 0 * NaN).
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int chunks, const uint4& w, int lane) {
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t gone = ~words[k];
+        while (gone) {
+            const int r = 32 * k + __ffs(gone) - 1;
+            gone &= gone - 1;
+            // 8 lanes clear a 128-byte row; up to 4 chunks at a time
+            const int c = lane >> 3;
+            if (c < chunks)
+                *reinterpret_cast<uint4*>(tile + c * CHUNK_BYTES + r * 128 + (lane & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+}  // namespace attn
+}  // namespace fs

@@ -86,7 +86,9 @@ struct Call {
     T* at(size_t off) const { return reinterpret_cast<T*>(ws->base + off); }
 };
 
-fs_status begin_call(Call& c, void* stream);
+// scratch = false: the call uses nothing of the workspace but the error word, so
+// it is not ordered after the workspace's last user (and needs no end_call)
+fs_status begin_call(Call& c, void* stream, bool scratch = true);
 fs_status end_call(Call& c);
 fs_status ensure_capacity(Call& c);                 // grows to c.L.off bytes
 fs_status classify(Call& c, Arr& a, const float* p, size_t count);
@@ -114,6 +116,11 @@ void timing_end(int slot, int kind, cudaStream_t s, int units = 1);
 
 // TMA tensor map (128 bytes) over `rows` rows of 64 fp16 at `base`, box 64 x 128.
 fs_status make_chunk_tmap(void* map128, const void* base, uint64_t rows);
+
+// TMA tensor map of a 4-D 16-bit tensor (strides in bytes of dimensions 1..3),
+// its boxes of 64 elements by box[1] rows in the 128-byte swizzle
+fs_status make_tmap_4d(void* map128, const void* base, const uint64_t* dims, const uint64_t* strides,
+                       const uint32_t* box, bool bf16);
 
 // sm_balance: cost by the blocks per SM (dynamic scheduling over several
 // waves) instead of full waves.

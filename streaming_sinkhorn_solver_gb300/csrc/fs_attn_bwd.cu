@@ -813,7 +813,7 @@ cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
     if (a.n > 0) {
         const size_t fixed = 1024 + sizeof(GradBars) + sizeof(float) * (kTile + 2 * kElemWarps) + bias +
                              (a.bias_part ? sizeof(float) * kBands * width : 0);
-        p.stages = ring_stages(fixed, tile);
+        p.stages = 2 * (ring_stages(fixed, tile) / 2);     // even: K keeps its slots, and their clean bars
         if ((e = raise_smem(k_grad_q<HD, BF>, kSmemLimit, ready_q)) != cudaSuccess) return e;
         k_grad_q<HD, BF><<<(unsigned)((int64_t)p.q_tiles * a.H * a.B), kGradThreads,
                            fixed + p.stages * tile, s>>>(p);

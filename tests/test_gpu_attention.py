@@ -101,6 +101,14 @@ def test_bias(n, m, nb, far, shared):
     check(*make(2, n, m, 4, 2, 64, BF, nb=nb, far=far, shared=shared, pos=[m // 2, 3], seed=11))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("drop", [0.0, 0.2])
+def test_many_key_tiles_with_partial_ones(d, drop):
+    """Sequences of more key tiles than the kernels keep in flight, with masked tiles."""
+    check(*make(2, 130, 2300, 2, 1, d, BF, lens=[2300, 1900], drop=drop, seed=22))
+    fs.fs_check()
+
+
 def test_bias_with_masks_and_wide_heads():
     check(*make(3, 200, 333, 6, 3, 128, HF, lens=[333, 130, 0], drop=0.3, nb=48, far=300, seed=3))
 

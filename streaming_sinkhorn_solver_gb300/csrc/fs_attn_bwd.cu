@@ -40,19 +40,8 @@ struct GradBars {
     uint32_t tmem, pad;
 };
 
-// The issuing thread's wait for a barrier, ordered before its products.
-__device__ __forceinline__ bool mma_wait(uint32_t* err, uint64_t* bar, uint32_t phase) {
-    const bool ok = mbar_wait(bar, phase, err, ERR_TIMEOUT_MMA);
-    tc_fence_after();
-    return ok;
-}
-
 template <bool BF>
 using Elem = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-
-__device__ __forceinline__ void named_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
 
 // Two 16-bit values of a register as floats
 template <bool BF>
@@ -282,10 +271,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
         if (partial_keys) {
             Ring r;
             for (int j = 0; j < nt; ++j) {
-                const uint4 w = tile_words(P.kt, b, tile_at(P.kt, b, j), end);
+                const KeyBits<kTile> w(P.kt, b, j, end);
                 if (!warp_wait(&bar.full[r.slot], r.phase, a.err, ERR_TIMEOUT_PRODUCER)) break;
-                if (!all_count(w)) {
-                    clear_rows(sKV + r.slot * kTileBytes, kChunks, w, lane);
+                if (!w.all()) {
+                    clear_rows(sKV + r.slot * kTileBytes, kChunks, CHUNK_BYTES, w, lane);
                     fence_proxy_async_smem();
                 }
                 __syncwarp();

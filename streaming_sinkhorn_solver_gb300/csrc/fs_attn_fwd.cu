@@ -2,13 +2,19 @@
 //
 // A block takes 256 queries of one head in two tiles of 128 and streams the
 // keys in tiles of 128:
-//   S_t = Q_t K^T (TMEM), p = 2^{x - ref} in 16 bits over S_t in TMEM,
+//   S_t = Q_t K^T (TMEM), p = 2^{x - ref} in 16 bits in TMEM,
 //   O_t += P_t V (TMEM, P as the A operand read from TMEM).
-// One warp issues the copies, one thread the products, four warps per query
-// tile hold a row per thread and keep its running sum and reference.  While
-// one tile's rows are in the softmax, the tensor core works on the other's
-// products; V is read as an operand summed over its rows, so nothing is
-// transposed.
+// V is read as an operand summed over its rows, so nothing is transposed.
+//
+// Four warps hold a query tile, a row per thread, and one thread issues its
+// products, so neither tile waits for the other's.  From the last P of a tile to
+// its next scores the tensor core would take its products' time and about 450
+// cycles of latency; so P has TMEM columns of its own, and the next scores are
+// formed while this tile's are still in the softmax.  That fills TMEM with two S,
+// two P and two O for heads up to 64; wider heads take the keys 64 at a time, with
+// two P each (their score products then read Q twice as often as keys of 128
+// would: 48 cycles of shared memory for 32 of arithmetic, and still less than the
+// wait that P over S costs: 3950 cycles a step of 256 x 128 then, see below).
 //
 // The reference is the running maximum, moved only when a row's maximum grew
 // by more than 2^8 (p then stays below 256, which both types and the float32
@@ -24,88 +30,53 @@ namespace attn {
 
 namespace {
 
-constexpr int kFwdThreads = 384;
+constexpr int kSoftWarps = 8;              // 4 per query tile
+constexpr int kFwdThreads = 32 * (kSoftWarps + 4);
+constexpr int kMma0 = kSoftWarps, kLoad = kSoftWarps + 2, kClean = kSoftWarps + 3;
 constexpr int kSlack = 2 * kTile;          // bias table entries beyond +-D on each side
 constexpr float kRefSlack = 8.f;
 
+// Key tiles, TMEM columns and shared memory by the width of the heads
 template <int HD>
 struct Fwd {
     static constexpr int kChunks = HD / 64;
-    static constexpr int kTileBytes = kChunks * CHUNK_BYTES;
-    static constexpr int kStages = HD == 64 ? 6 : 4;   // K and V tiles in turn
-    static constexpr int kBars = 1 + 3 * kStages + 2 + 2 + 1 + 1;
-    static constexpr size_t kFixed = 1024 + (size_t)(2 + kStages) * kTileBytes + 8 * kBars + 16;
+    static constexpr int kKeys = forward_keys(HD);               // keys of a tile
+    static constexpr int kChunkBytes = kKeys * 128;              // 64 elements of each
+    static constexpr int kTileBytes = kChunks * kChunkBytes;     // 16 KB
+    static constexpr int kQBytes = kChunks * CHUNK_BYTES;
+    static constexpr int kStages = 8;                            // K and V tiles in turn
+    static constexpr int kPBufs = HD == 64 ? 1 : 2;
+    static constexpr uint32_t kPCols = kKeys / 2;
+    __host__ __device__ static constexpr uint32_t S(int t) { return 256 * t; }
+    __host__ __device__ static constexpr uint32_t P(int t) { return S(t) + kKeys; }
+    __host__ __device__ static constexpr uint32_t O(int t) { return P(t) + kPBufs * kPCols; }
+    static_assert(kKeys + kPBufs * (int)kPCols + HD == 256, "TMEM");
 };
 
-// One row's result from its sum and O in TMEM: out and lse, or the partial of
-// this split.  Whole warps.
-template <bool BF>
-__device__ __forceinline__ void write_row(const FwdArgs& P, uint32_t tO, int b, int h, int i, int split,
-                                          bool any, int dsteps, float ref, float sum) {
-    using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-    const Args& a = P.a;
-    const bool live = i < a.n;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const float lse2 = sum == 0.f ? -INFINITY : ref + lg2(sum);
-    const int64_t row = ((int64_t)b * a.H + h) * a.n + i;
-    float* part = P.splits > 1 ? P.part.out + (split * P.part.rows + row) * a.d : nullptr;
-    T* out = static_cast<T*>(a.o.p) + b * a.o.sb + (int64_t)i * a.o.st + h * a.o.sh;
-    for (int c = 0; c < dsteps * 16; c += 16) {
-        float o[16];
-        if (any) {
-            tmem_ld16(tO + c, o);
-            tmem_wait_ld();
-            tmem_reg_fence(o);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = sum == 0.f ? 0.f : o[e] * inv;
-        if (part) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (live && c + e < a.d) part[c + e] = o[e];
-        } else if (P.out_vec) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-                if (live && c + e < a.d)
-                    *reinterpret_cast<uint4*>(out + c + e) =
-                        make_uint4(pack16<BF>(o[e], o[e + 1]), pack16<BF>(o[e + 2], o[e + 3]),
-                                   pack16<BF>(o[e + 4], o[e + 5]), pack16<BF>(o[e + 6], o[e + 7]));
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (live && c + e < a.d) out[c + e] = from_f<T>(o[e]);
-        }
-        __syncwarp();
-    }
-    if (!live) return;
-    if (part)
-        P.part.lse2[split * P.part.rows + row] = lse2;
-    else
-        a.lse[row] = lse2 * (float)kLn2;
-}
+struct FwdBars {
+    uint64_t full[8], empty[8], clean[8];
+    uint64_t qfull, sfull[2], sfree[2], pfull[2][2], pfree[2][2], drain[2];
+    uint32_t tmem, pad;
+};
+template <int HD>
+constexpr size_t kFwdFixed =
+    1024 + 2 * (size_t)Fwd<HD>::kQBytes + Fwd<HD>::kStages * (size_t)Fwd<HD>::kTileBytes + sizeof(FwdBars);
 
 template <int HD, bool BF>
 __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_constant__ FwdArgs P) {
     using C = Fwd<HD>;
-    constexpr int NS = C::kStages;
+    using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+    constexpr int NS = C::kStages, KT = C::kKeys;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     const Args& a = P.a;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    uint8_t* sQ = smem;
-    uint8_t* sKV = sQ + 2 * C::kTileBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(sKV + NS * C::kTileBytes);
-    uint64_t* empty = full + NS;
-    uint64_t* clean = empty + NS;     // a V tile whose uncounted rows are zero
-    uint64_t* qfull = clean + NS;
-    uint64_t* sfull = qfull + 1;
-    uint64_t* pfull = sfull + 2;
-    uint64_t* ofull = pfull + 2;
-    uint64_t* drain = ofull + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-    float* sBias = reinterpret_cast<float*>(tmem_slot + 4);
+    uint8_t* sQ = smem;                                  // at the end the rows of out
+    uint8_t* sKV = sQ + 2 * C::kQBytes;
+    FwdBars& bar = *reinterpret_cast<FwdBars*>(sKV + NS * C::kTileBytes);
+    float* sBias = reinterpret_cast<float*>(&bar + 1);
 
     int blk = blockIdx.x;
     const int split = blk % P.splits;
@@ -117,33 +88,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
     const int i0 = qt * 2 * kTile;
     const bool two = i0 + kTile < a.n;
     const int end = key_end(a, b);
-    const int nt_all = tile_count(P.kt, b, end);
+    const int nt_all = step_count<KT>(P.kt, b, end);
     const int per = (nt_all + P.splits - 1) / P.splits;
     const int t0 = min(nt_all, split * per);
     const int nt = min(nt_all, t0 + per) - t0;
     const bool partial_keys = P.kt.words != nullptr || end < a.m;
-    const int64_t pos = a.q_pos ? (int64_t)__ldg(a.q_pos + b) : 0;
     const int dsteps = (a.d + 15) >> 4;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-            mbar_init(&clean[s], 1);
+            mbar_init(&bar.full[s], 1);
+            mbar_init(&bar.empty[s], two ? 2 : 1);
+            mbar_init(&bar.clean[s], 1);
         }
-        mbar_init(qfull, 1);
+        mbar_init(&bar.qfull, 1);
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&sfull[t], 1);
-            mbar_init(&pfull[t], 4);
+            mbar_init(&bar.sfull[t], 1);
+            mbar_init(&bar.sfree[t], 4);
+            mbar_init(&bar.pfull[t][0], 4);
+            mbar_init(&bar.pfull[t][1], 4);
+            mbar_init(&bar.pfree[t][0], 1);
+            mbar_init(&bar.pfree[t][1], 1);
+            mbar_init(&bar.drain[t], 1);
         }
-        mbar_init(ofull, 1);
-        mbar_init(drain, 1);
         fence_mbar_init();
     }
-    if (warp == 9) tmem_alloc(tmem_slot, 512);
+    if (warp == kMma0) tmem_alloc(&bar.tmem, 512);
     if (a.table) {
         // base-2 bias by relative position -D - kSlack .. D + kSlack of this head
-        using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
         const T* row = static_cast<const T*>(a.table) + h * a.table_stride;
         for (int e = threadIdx.x; e < 2 * (a.D + kSlack) + 1; e += kFwdThreads)
             sBias[e] = bias2(to_f<T>(row[bucket_of(a, (int64_t)e - a.D - kSlack)]));
@@ -151,158 +123,148 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = bar.tmem;
 
-    if (warp == 8) {
+    if (warp == kLoad) {
         if (nt > 0 && elect_one()) {
             const int g = h / a.R;
-            mbar_arrive_expect_tx(qfull, (two ? 2 : 1) * C::kTileBytes);
+            mbar_arrive_expect_tx(&bar.qfull, (two ? 2 : 1) * C::kQBytes);
             for (int t = 0; t < (two ? 2 : 1); ++t)
                 for (int c = 0; c < C::kChunks; ++c)
-                    tma_load(sQ + t * C::kTileBytes + c * CHUNK_BYTES, &P.q.map, c * 64, i0 + t * kTile,
-                             h * P.q.head, b * P.q.batch, qfull);
+                    tma_load(sQ + t * C::kQBytes + c * CHUNK_BYTES, &P.q.map, c * 64, i0 + t * kTile,
+                             h * P.q.head, b * P.q.batch, &bar.qfull);
+            Ring r;
             int issued = 0;
             bool ok = true;
             for (int it = 0; it < 2 * nt; ++it) {
-                const int s = it % NS;
-                if (!mbar_wait(&empty[s], ((it / NS) & 1) ^ 1, a.err, ERR_TIMEOUT_PRODUCER)) {
+                if (!mbar_wait(&bar.empty[r.slot], r.phase ^ 1u, a.err, ERR_TIMEOUT_PRODUCER)) {
                     ok = false;
                     break;
                 }
-                const int tile = tile_at(P.kt, b, t0 + (it >> 1));
+                const int key = step_key<KT>(P.kt, b, t0 + (it >> 1));
                 const TensorMap& src = it & 1 ? P.v : P.k;
-                mbar_arrive_expect_tx(&full[s], C::kTileBytes);
+                mbar_arrive_expect_tx(&bar.full[r.slot], C::kTileBytes);
                 for (int c = 0; c < C::kChunks; ++c)
-                    tma_load(sKV + s * C::kTileBytes + c * CHUNK_BYTES, &src.map, c * 64, tile * kTile,
-                             g * src.head, b * src.batch, &full[s]);
+                    tma_load(sKV + r.slot * C::kTileBytes + c * C::kChunkBytes, &src.map, c * 64, key,
+                             g * src.head, b * src.batch, &bar.full[r.slot]);
                 ++issued;
+                r.step(1, NS);
             }
             if (!ok) {   // every copy lands before the block can exit
-                mbar_wait(qfull, 0, a.err, ERR_TIMEOUT_PRODUCER);
-                for (int it = max(0, issued - NS); it < issued; ++it)
-                    mbar_wait(&full[it % NS], (it / NS) & 1, a.err, ERR_TIMEOUT_PRODUCER);
+                mbar_wait(&bar.qfull, 0, a.err, ERR_TIMEOUT_PRODUCER);
+                Ring l;
+                for (int it = 0; it < issued; ++it) {
+                    if (it + NS >= issued)
+                        mbar_wait(&bar.full[l.slot], l.phase, a.err, ERR_TIMEOUT_PRODUCER);
+                    l.step(1, NS);
+                }
             }
         }
-    } else if (warp == 9) {
-        if (nt > 0 && elect_one()) {
-            const uint32_t idS = idesc_16(BF, kTile, false);
+    } else if (warp == kMma0 || warp == kMma0 + 1) {
+        const int t = warp - kMma0;
+        if (nt > 0 && (t == 0 || two) && elect_one()) {
+            const uint32_t idS = idesc_16(BF, KT, false);
             const uint32_t idO = idesc_16(BF, dsteps * 16, true);
-            const uint64_t dQ = sdesc_sw128(smem_u32(sQ)), dK = sdesc_sw128(smem_u32(sKV));
-            const uint64_t dV = sdesc_tokens(smem_u32(sKV));
             constexpr uint64_t kTileU = C::kTileBytes >> 4;    // descriptors count 16 bytes
-            bool ok = mbar_wait(qfull, 0, a.err, ERR_TIMEOUT_MMA) &&
-                      mbar_wait(&full[0], 0, a.err, ERR_TIMEOUT_MMA);
-            if (ok) {
-                tc_fence_after();
-                mma_over_d(tmem, dQ, dK, idS, dsteps);
-                mma_commit(&sfull[0]);
-                if (two) {
-                    mma_over_d(tmem + kTile, dQ + kTileU, dK, idS, dsteps);
-                    mma_commit(&sfull[1]);
-                }
-                mma_commit(&empty[0]);
-            }
-            for (int j = 0; j < nt && ok; ++j) {
-                const int vs = (2 * j + 1) % NS, ks = (2 * j + 2) % NS;
-                if (!mbar_wait(partial_keys ? &clean[vs] : &full[vs], ((2 * j + 1) / NS) & 1, a.err,
-                               ERR_TIMEOUT_MMA)) {
-                    ok = false;
-                    break;
-                }
-                const bool more = j + 1 < nt;
-                if (more && !mbar_wait(&full[ks], ((2 * j + 2) / NS) & 1, a.err, ERR_TIMEOUT_MMA)) {
-                    ok = false;
-                    break;
-                }
-                for (int t = 0; t < (two ? 2 : 1); ++t) {
-                    if (!mbar_wait(&pfull[t], j & 1, a.err, ERR_TIMEOUT_MMA)) {
-                        ok = false;
+            const uint64_t dQ = sdesc_sw128(smem_u32(sQ)) + t * (C::kQBytes >> 4);
+            const uint64_t dK = sdesc_sw128(smem_u32(sKV));
+            const uint64_t dV = sdesc_tokens(smem_u32(sKV), C::kChunkBytes);
+            const uint32_t cS = tmem + C::S(t), cP = tmem + C::P(t), cO = tmem + C::O(t);
+            uint64_t* vbar = partial_keys ? bar.clean : bar.full;
+            Ring rk, rv;
+            rv.step(1, NS);
+            bool ok = mma_wait(a.err, &bar.qfull, 0);
+            for (int j = -1; j < nt && ok; ++j) {
+                if (j + 1 < nt) {
+                    if (!(ok = mma_wait(a.err, &bar.full[rk.slot], rk.phase) &&
+                               (j < 0 || mma_wait(a.err, &bar.sfree[t], j & 1))))
                         break;
-                    }
-                    tc_fence_after();
-                    mma_over_tokens(tmem + (2 + t) * kTile, tmem + t * kTile, dV + vs * kTileU, idO, j > 0);
-                    if (more) {
-                        mma_over_d(tmem + t * kTile, dQ + t * kTileU, dK + ks * kTileU, idS, dsteps);
-                        mma_commit(&sfull[t]);
-                    }
+                    mma_over_d<C::kChunkBytes>(cS, dQ, dK + rk.slot * kTileU, idS, dsteps);
+                    mma_commit(&bar.sfull[t]);
+                    mma_commit(&bar.empty[rk.slot]);
+                    rk.step(2, NS);
                 }
-                if (!ok) break;
-                mma_commit(&empty[vs]);
-                if (more) mma_commit(&empty[ks]);
+                if (j < 0) continue;
+                const int buf = C::kPBufs == 2 ? j & 1 : 0;
+                if (!(ok = mma_wait(a.err, &vbar[rv.slot], rv.phase) &&
+                           mma_wait(a.err, &bar.pfull[t][buf], C::kPBufs == 2 ? (j >> 1) & 1 : j & 1)))
+                    break;
+                mma_over_tokens<KT>(cO, cP + buf * C::kPCols, dV + rv.slot * kTileU, idO, j > 0, 32);
+                mma_commit(&bar.pfree[t][buf]);
+                mma_commit(&bar.empty[rv.slot]);
+                rv.step(2, NS);
             }
-            mma_commit(ofull);
-            mma_commit(drain);
-            mbar_wait(drain, 0, a.err, ERR_TIMEOUT_MMA);
+            mma_commit(&bar.drain[t]);
+            mbar_wait(&bar.drain[t], 0, a.err, ERR_TIMEOUT_MMA);
         }
-    } else if (warp == 10) {
+    } else if (warp == kClean) {
         if (partial_keys) {
+            Ring r;
+            r.step(1, NS);
             for (int j = 0; j < nt; ++j) {
-                const int vs = (2 * j + 1) % NS;
-                const uint4 w = tile_words(P.kt, b, tile_at(P.kt, b, t0 + j), end);
-                if (!warp_wait(&full[vs], ((2 * j + 1) / NS) & 1, a.err, ERR_TIMEOUT_PRODUCER)) break;
-                if (!all_count(w)) {
-                    clear_rows(sKV + vs * C::kTileBytes, C::kChunks, w, lane);
+                const KeyBits<KT> w(P.kt, b, t0 + j, end);
+                if (!warp_wait(&bar.full[r.slot], r.phase, a.err, ERR_TIMEOUT_PRODUCER)) break;
+                if (!w.all()) {
+                    clear_rows(sKV + r.slot * C::kTileBytes, C::kChunks, C::kChunkBytes, w, lane);
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&clean[vs]);
+                if (lane == 0) mbar_arrive(&bar.clean[r.slot]);
+                r.step(2, NS);
             }
         }
-    } else if (warp < 8) {
-        const int t = warp >> 2;
+    } else {
+        const int t = warp >> 2, quarter = warp & 3;
         if (t == 0 || two) {
-            const int r = (warp & 3) * 32 + lane;
+            const int r = quarter * 32 + lane;
             const int i = i0 + t * kTile + r;
-            const uint32_t lofs = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t tS = tmem + t * kTile + lofs, tO = tmem + (2 + t) * kTile + lofs;
-            const int64_t first = pos + i0 + t * kTile;          // position of the tile's first query
+            const uint32_t lofs = (uint32_t)(quarter * 32) << 16;
+            const uint32_t tS = tmem + C::S(t) + lofs, tP = tmem + C::P(t) + lofs, tO = tmem + C::O(t) + lofs;
+            // position of the tile's first query
+            const int64_t first = (a.q_pos ? (int64_t)__ldg(a.q_pos + b) : 0) + i0 + t * kTile;
             float ref = -INFINITY, sum = 0.f;
             bool ok = true;
             for (int j = 0; j < nt; ++j) {
-                const int tile = tile_at(P.kt, b, t0 + j);
-                const uint4 w = tile_words(P.kt, b, tile, end);
-                const int64_t rel0 = (int64_t)tile * kTile - first;   // of the tile's first row and key
-                if (!warp_wait(&sfull[t], j & 1, a.err, ERR_TIMEOUT_EPILOGUE)) {
-                    ok = false;
-                    break;
-                }
+                if (!(ok = warp_wait(&bar.sfull[t], j & 1, a.err, ERR_TIMEOUT_EPILOGUE))) break;
                 tc_fence_after();
-                float v[kTile];
+                float v[KT];
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32) tmem_ld32(tS + c, v + c);
+                for (int c = 0; c < KT; c += 32) tmem_ld32(tS + c, v + c);
                 tmem_wait_ld();
                 tmem_reg_fence(v);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.sfree[t]);
                 float mul = a.scale2, add = 0.f;
                 if (a.table) {
+                    // relative position of the first row and key
+                    const int64_t rel0 = step_key<KT>(P.kt, b, t0 + j) - first;
                     if (rel0 - (kTile - 1) >= a.D) {
                         add = sBias[2 * a.D + kSlack];
-                    } else if (rel0 + (kTile - 1) <= -a.D) {
+                    } else if (rel0 + (KT - 1) <= -a.D) {
                         add = sBias[kSlack];
                     } else {
                         // |rel| < D + 2 * 128 here
                         const float* e = sBias + (int)rel0 - r + a.D + kSlack;
 #pragma unroll
-                        for (int c = 0; c < kTile; ++c) v[c] = fmaf(v[c], mul, e[c]);
+                        for (int c = 0; c < KT; ++c) v[c] = fmaf(v[c], mul, e[c]);
                         mul = 1.f;
                     }
                 }
-                if (!all_count(w)) {
-                    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+                if (P.kt.words || (t0 + j + 1) * KT > end) {
+                    const KeyBits<KT> w(P.kt, b, t0 + j, end);
 #pragma unroll
-                    for (int c = 0; c < kTile; ++c)
-                        if (!((words[c >> 5] >> (c & 31)) & 1u)) v[c] = -INFINITY;
+                    for (int c = 0; c < KT; ++c)
+                        if (!((w.w[c >> 5] >> (c & 31)) & 1u)) v[c] = -INFINITY;
                 }
-                float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
+                float m[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                for (int c = 4; c < kTile - 4; c += 8) {
-                    m0 = max3(m0, v[c], v[c + 1]);
-                    m1 = max3(m1, v[c + 2], v[c + 3]);
-                    m2 = max3(m2, v[c + 4], v[c + 5]);
-                    m3 = max3(m3, v[c + 6], v[c + 7]);
-                }
-                m0 = max3(m0, v[kTile - 4], v[kTile - 3]);
-                m1 = max3(m1, v[kTile - 2], v[kTile - 1]);
-                const float top = fmaf(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), mul, add);
+                for (int c = 4; c + 8 <= KT; c += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) m[k] = max3(m[k], v[c + 2 * k], v[c + 2 * k + 1]);
+                m[0] = max3(m[0], v[KT - 4], v[KT - 3]);
+                m[1] = max3(m[1], v[KT - 2], v[KT - 1]);
+                const float top = fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), mul, add);
                 float alpha = 1.f;
                 if (top > ref + kRefSlack) {
                     // (up to its first counted key a row's sum and O are zero)
@@ -310,8 +272,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
                     sum *= alpha;
                     ref = top;
                 }
+                const int buf = C::kPBufs == 2 ? j & 1 : 0;
                 if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                    // the products of tile j - 1 are complete: S of tile j came after them
+                    // O is still once the products of tile j - 1 are done (j > 0 here)
+                    if (!(ok = warp_wait(&bar.pfree[t][C::kPBufs == 2 ? buf ^ 1 : 0],
+                                         C::kPBufs == 2 ? ((j - 1) >> 1) & 1 : (j - 1) & 1, a.err,
+                                         ERR_TIMEOUT_EPILOGUE)))
+                        break;
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < dsteps * 16; c += 16) {
                         float o[16];
@@ -328,11 +296,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
                 const uint64_t mul2 = pk(mul, mul), base2 = pk(base, base);
                 uint64_t s0 = 0, s1 = 0;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                for (int q = 0; q < KT / 64; ++q) {
                     uint32_t p[32];
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        const int x = half * 64 + 2 * c;
+                        const int x = q * 64 + 2 * c;
                         float e0, e1, e2, e3;
                         upk(fma2(pk(v[x], v[x + 1]), mul2, base2), e0, e1);
                         upk(fma2(pk(v[x + 2], v[x + 3]), mul2, base2), e2, e3);
@@ -345,28 +313,89 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
                         p[c] = pack16<BF>(e0, e1);
                         p[c + 1] = pack16<BF>(e2, e3);
                     }
-                    tmem_st32(tS + half * 32, p);
+                    // the buffer's last P has been read
+                    if (q == 0 && j >= C::kPBufs) {
+                        ok = warp_wait(&bar.pfree[t][buf],
+                                       C::kPBufs == 2 ? ((j - 2) >> 1) & 1 : (j - 1) & 1, a.err,
+                                       ERR_TIMEOUT_EPILOGUE);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    tmem_st32(tP + buf * C::kPCols + q * 32, p);
                 }
-                float a0, a1, b0, b1;
-                upk(s0, a0, a1);
-                upk(s1, b0, b1);
-                sum += (a0 + a1) + (b0 + b1);
+                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&pfull[t]);
+                if (lane == 0) mbar_arrive(&bar.pfull[t][buf]);
+                float f0, f1, f2, f3;
+                upk(s0, f0, f1);
+                upk(s1, f2, f3);
+                sum += (f0 + f1) + (f2 + f3);
             }
-            if (nt > 0 && ok) ok = warp_wait(ofull, 0, a.err, ERR_TIMEOUT_EPILOGUE);
-            if (ok) {
-                tc_fence_after();
-                write_row<BF>(P, tO, b, h, i, split, nt > 0, dsteps, ref, sum);
+            if (nt > 0 && ok) {
+                const int j = nt - 1;
+                ok = warp_wait(&bar.pfree[t][C::kPBufs == 2 ? j & 1 : 0],
+                               C::kPBufs == 2 ? (j >> 1) & 1 : j & 1, a.err, ERR_TIMEOUT_EPILOGUE);
+            }
+            const bool live = i < a.n;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int64_t row = ((int64_t)b * a.H + h) * a.n + i;
+            if (live) {
+                const float lse2 = sum == 0.f ? -INFINITY : ref + lg2(sum);
+                if (P.splits > 1)
+                    P.part.lse2[split * P.part.rows + row] = lse2;
+                else
+                    a.lse[row] = lse2 * (float)kLn2;
+            }
+            tc_fence_after();
+            // the rows of out: through shared memory in whole boxes, or directly
+            float* part = P.splits > 1 ? P.part.out + (split * P.part.rows + row) * a.d : nullptr;
+            T* out = static_cast<T*>(a.o.p) + b * a.o.sb + (int64_t)i * a.o.st + h * a.o.sh;
+            uint8_t* stage = sQ + t * C::kQBytes;
+            for (int c = 0; c < dsteps * 16 && ok; c += 16) {
+                float o[16];
+                if (nt > 0) {
+                    tmem_ld16(tO + c, o);
+                    tmem_wait_ld();
+                    tmem_reg_fence(o);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = sum == 0.f ? 0.f : o[e] * inv;
+                if (part) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (live && c + e < a.d) part[c + e] = o[e];
+                } else if (P.out_box) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8)
+                        *reinterpret_cast<uint4*>(stage + (c >> 6) * CHUNK_BYTES +
+                                                  swz_offset(r, (c & 63) + e)) =
+                            make_uint4(pack16<BF>(o[e], o[e + 1]), pack16<BF>(o[e + 2], o[e + 3]),
+                                       pack16<BF>(o[e + 4], o[e + 5]), pack16<BF>(o[e + 6], o[e + 7]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (live && c + e < a.d) out[c + e] = from_f<T>(o[e]);
+                }
+                __syncwarp();
+            }
+            if (P.out_box && !part) {
+                fence_proxy_async_smem();
+                named_sync(1 + t, kTile);
+                if (quarter == 0 && elect_one()) {
+                    for (int c = 0; c < C::kChunks; ++c)
+                        if (c * 64 < a.d)
+                            tma_store(&P.o.map, stage + c * CHUNK_BYTES, c * 64, i0 + t * kTile, h, b);
+                    tma_store_wait();
+                }
             }
         }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kMma0) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -375,7 +404,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
 template <int HD, bool BF>
 cudaError_t launch_forward(const FwdArgs& p, cudaStream_t s) {
     const size_t bias = p.a.table ? sizeof(float) * (2 * (size_t)(p.a.D + kSlack) + 1) : 0;
-    constexpr size_t most = Fwd<HD>::kFixed + sizeof(float) * (2 * (size_t)(kMaxDistance + kSlack) + 1);
+    constexpr size_t most = kFwdFixed<HD> + sizeof(float) * (2 * (size_t)(kMaxDistance + kSlack) + 1);
     static_assert(most <= kSmemLimit, "forward kernel does not fit in shared memory");
     static std::atomic<uint64_t> ready{0};    // devices whose shared-memory limit is raised
     int dev = 0;
@@ -388,7 +417,7 @@ cudaError_t launch_forward(const FwdArgs& p, cudaStream_t s) {
         ready.fetch_or(1ull << dev);
     }
     const unsigned blocks = (unsigned)((int64_t)p.row_blocks * p.a.H * p.a.B * p.splits);
-    k_forward_tc<HD, BF><<<blocks, kFwdThreads, Fwd<HD>::kFixed + bias, s>>>(p);
+    k_forward_tc<HD, BF><<<blocks, kFwdThreads, kFwdFixed<HD> + bias, s>>>(p);
     count_launch();
     return cudaGetLastError();
 }

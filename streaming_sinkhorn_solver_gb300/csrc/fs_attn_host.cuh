@@ -22,12 +22,12 @@ struct Partials {
 };
 
 struct FwdArgs {
-    TensorMap q, k, v;
+    TensorMap q, k, v, o;
     Args a;
     KeyTiles kt;
     Partials part;
     int row_blocks, splits;
-    int out_vec;       // the rows of out take 16-byte stores
+    int out_box;       // out is written through its tensor map
 };
 
 struct GradArgs {
@@ -52,7 +52,11 @@ cudaError_t launch_zero(const Args& a, const View& w, int tokens, int heads, flo
 cudaError_t launch_pack(const View& from, void* to, int B, int tokens, int heads, int d, int dp,
                         cudaStream_t s);
 
-fs_status make_tensor_map(TensorMap& t, const View& w, int B, int tokens, int heads, int d, bool bf16);
+// boxes of `rows` tokens
+fs_status make_tensor_map(TensorMap& t, const View& w, int B, int tokens, int heads, int d, bool bf16,
+                          int rows = kTile);
+// keys of a tile of the forward kernel
+constexpr int forward_keys(int d) { return d <= 64 ? 128 : 64; }
 
 }  // namespace attn
 }  // namespace fs

@@ -142,7 +142,8 @@ cudaError_t launch_pack(const View& from, void* to, int B, int tokens, int heads
     return cudaGetLastError();
 }
 
-fs_status make_tensor_map(TensorMap& t, const View& w, int B, int tokens, int heads, int d, bool bf16) {
+fs_status make_tensor_map(TensorMap& t, const View& w, int B, int tokens, int heads, int d, bool bf16,
+                          int rows) {
     // (d, token, head, batch); an axis of one entry or of stride 0 has one entry
     const uint64_t row = 2 * (uint64_t)((d + 7) / 8 * 8);
     t.head = heads > 1 && w.sh != 0;
@@ -151,7 +152,7 @@ fs_status make_tensor_map(TensorMap& t, const View& w, int B, int tokens, int he
                               t.batch ? (uint64_t)B : 1};
     const uint64_t strides[3] = {tokens > 1 ? 2 * (uint64_t)w.st : row, t.head ? 2 * (uint64_t)w.sh : row,
                                  t.batch ? 2 * (uint64_t)w.sb : row};
-    const uint32_t box[4] = {64, kTile, 1, 1};
+    const uint32_t box[4] = {64, (uint32_t)rows, 1, 1};
     return make_tmap_4d(&t.map, w.p, dims, strides, box, bf16);
 }
 

@@ -31,16 +31,33 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
         : "memory");
 }
 
-// A whole warp waits (mbar_wait's branches are uniform, so its result is made so
-// and the warp joined before the warp-collective instructions that follow).
+// A whole warp waits; its lanes agree on the result and are joined for the
+// warp-collective instructions that follow.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err, uint32_t code) {
-    __syncwarp();
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, err, code);
-    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-    // every lane observes the completed phase itself
-    if (ok) ok = mbar_try_wait(bar, parity);
-    return __all_sync(0xffffffffu, ok);
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, code));
+}
+// The issuing thread's wait for a barrier, ordered before its products.
+__device__ __forceinline__ bool mma_wait(uint32_t* err, uint64_t* bar, uint32_t phase) {
+    const bool ok = mbar_wait(bar, phase, err, ERR_TIMEOUT_MMA);
+    tc_fence_after();
+    return ok;
+}
+
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// copy of a box from shared memory, rows and elements beyond the tensor left out
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int c0, int token,
+                                          int head, int batch) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(map),
+        "r"(smem_u32(src)), "r"(c0), "r"(token), "r"(head), "r"(batch)
+        : "memory");
+}
+// the issuing thread's stores have read their shared memory
+__device__ __forceinline__ void tma_store_wait() {
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // one lane of a converged warp: the issuer of its copies and products
@@ -68,10 +85,10 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
 // Operand summed over the tokens of a tile: element (token, c) at row token of
 // the 64-element chunk c / 64.  Groups of 8 tokens are 1024 bytes apart, the
 // next 64 elements a chunk apart; 16 tokens on, the start address is 2048 bytes up.
-__device__ __forceinline__ uint64_t sdesc_tokens(uint32_t saddr) {
+__device__ __forceinline__ uint64_t sdesc_tokens(uint32_t saddr, uint32_t chunk_bytes = CHUNK_BYTES) {
     uint64_t d = 0;
     d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(CHUNK_BYTES >> 4) << 16;
+    d |= (uint64_t)(chunk_bytes >> 4) << 16;
     d |= (uint64_t)(1024 >> 4) << 32;
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
@@ -95,15 +112,17 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
         : "r"(taddr));
 }
 
-// D[tmem] = A * B^T over the d elements of two 128-token tiles (chunks of 64), `steps`
-// products of 16 elements.  One elected thread.
+// D[tmem] = A * B^T over the d elements of a 128-token tile (A) and a tile of
+// B_CHUNK / 128 tokens (B), in chunks of 64; `steps` products of 16 elements.  One
+// elected thread.  (The count is a loop bound, not a condition around each product:
+// products under a data-dependent condition ended in illegal accesses.)
+template <int B_CHUNK = CHUNK_BYTES>
 __device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                            int steps) {
 #pragma unroll 1
-    for (int x = 0; x < steps; ++x) {
-        const uint64_t o = (uint64_t)((x >> 2) * (CHUNK_BYTES >> 4) + 2 * (x & 3));
-        mma_f16(d_tmem, a + o, b + o, idesc, x != 0);
-    }
+    for (int x = 0; x < steps; ++x)
+        mma_f16(d_tmem, a + (uint64_t)((x >> 2) * (CHUNK_BYTES >> 4) + 2 * (x & 3)),
+                b + (uint64_t)((x >> 2) * (B_CHUNK >> 4) + 2 * (x & 3)), idesc, x != 0);
 }
 // the same with A in TMEM
 __device__ __forceinline__ void mma_over_d_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
@@ -113,12 +132,13 @@ __device__ __forceinline__ void mma_over_d_ts(uint32_t d_tmem, uint32_t a_tmem, 
         mma_f16_ts(d_tmem, a_tmem + 8 * x, b + (uint64_t)((x >> 2) * (CHUNK_BYTES >> 4) + 2 * (x & 3)),
                    idesc, x != 0);
 }
-// D[tmem] (+)= A[tmem] * B over the 128 tokens of B's tile; tokens 64..127 of A
-// are `half` columns on from its first.  One elected thread.
+// D[tmem] (+)= A[tmem] * B over the KEYS tokens of B's tile; tokens 64 and on of A are
+// `half` columns from its first.  One elected thread.
+template <int KEYS = kTile>
 __device__ __forceinline__ void mma_over_tokens(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                                uint32_t idesc, bool accumulate, uint32_t half = 32) {
+                                                uint32_t idesc, bool accumulate, uint32_t half) {
 #pragma unroll
-    for (int x = 0; x < kTile / 16; ++x)
+    for (int x = 0; x < KEYS / 16; ++x)
         mma_f16_ts(d_tmem, a_tmem + (x >> 2) * half + 8 * (x & 3), b + 128 * x, idesc,
                    accumulate || x != 0);
 }
@@ -204,20 +224,56 @@ __device__ __forceinline__ bool all_count(const uint4& w) {
     return (w.x & w.y & w.z & w.w) == 0xffffffffu;
 }
 
+// The same in steps of KT = 128 or 64 keys: their count, first key, and bits.
+template <int KT>
+__device__ __forceinline__ int step_count(const KeyTiles& kt, int b, int end) {
+    return kt.list ? __ldg(kt.count + b) * (kTile / KT) : (end + KT - 1) / KT;
+}
+template <int KT>
+__device__ __forceinline__ int step_key(const KeyTiles& kt, int b, int j) {
+    if (!kt.list) return j * KT;
+    constexpr int per = kTile / KT;
+    return __ldg(kt.list + (int64_t)b * kt.tiles + j / per) * kTile + (j % per) * KT;
+}
+template <int KT>
+struct KeyBits {
+    uint32_t w[KT / 32];
+    __device__ __forceinline__ KeyBits(const KeyTiles& kt, int b, int j, int end) {
+        const int key = step_key<KT>(kt, b, j);
+        const uint4 all = tile_words(kt, b, key / kTile, end);
+        if (KT == kTile) {
+            w[0] = all.x;
+            w[1] = all.y;
+            w[KT / 32 - 2] = all.z;
+            w[KT / 32 - 1] = all.w;
+        } else {
+            w[0] = key & 64 ? all.z : all.x;
+            w[1] = key & 64 ? all.w : all.y;
+        }
+    }
+    __device__ __forceinline__ bool all() const {
+        uint32_t x = w[0];
+#pragma unroll
+        for (int k = 1; k < KT / 32; ++k) x &= w[k];
+        return x == 0xffffffffu;
+    }
+};
+
 // One whole warp: zeroes the rows of a landed tile whose keys do not count (what
 // such keys hold would otherwise enter sums as 0 * NaN).
-__device__ __forceinline__ void clear_rows(uint8_t* tile, int chunks, const uint4& w, int lane) {
-    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+template <int KT>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int chunks, int chunk_bytes, const KeyBits<KT>& w,
+                                           int lane) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        uint32_t gone = ~words[k];
+    for (int k = 0; k < KT / 32; ++k) {
+        uint32_t gone = ~w.w[k];
         while (gone) {
             const int r = 32 * k + __ffs(gone) - 1;
             gone &= gone - 1;
             // 8 lanes clear a 128-byte row; up to 4 chunks at a time
             const int c = lane >> 3;
             if (c < chunks)
-                *reinterpret_cast<uint4*>(tile + c * CHUNK_BYTES + r * 128 + (lane & 7) * 16) =
+                *reinterpret_cast<uint4*>(tile + c * chunk_bytes + r * 128 + (lane & 7) * 16) =
                     make_uint4(0, 0, 0, 0);
         }
     }

@@ -17,6 +17,10 @@ BF, HF = torch.bfloat16, torch.float16
 def _lib():
     assert torch.cuda.is_available()
     fs.load_library()
+
+
+@pytest.fixture(autouse=True)
+def _no_wait_gave_up():
     yield
     fs.fs_check()
 

@@ -223,8 +223,7 @@ fs_status forward_entry(const fs_attention* at, const void* q, const void* k, co
     p.part.rows = rows;
     p.part.out = p.splits > 1 ? c.at<float>(part_out) : nullptr;
     p.part.lse2 = p.splits > 1 ? c.at<float>(part_lse) : nullptr;
-    p.out_box = mappable(a.o, a.B, a.n, a.H, a.d);
-    if (p.out_box) FS_TRY(make_tensor_map(p.o, a.o, a.B, a.n, a.H, a.d, a.bf16));
+    p.out_vec = a.d % 8 == 0 && aligned16(a.o, a.B, a.n, a.H);
     a.err = c.ws->err_word;
     FS_TRY(make_tensor_map(p.q, a.q, a.B, a.n, a.H, a.d, a.bf16));
     FS_TRY(make_tensor_map(p.k, a.k, a.B, a.m, a.G, a.d, a.bf16, forward_keys(a.d)));

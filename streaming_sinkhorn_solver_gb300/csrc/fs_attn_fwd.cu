@@ -95,14 +95,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
     const bool partial_keys = P.kt.words != nullptr || end < a.m;
     const int dsteps = (a.d + 15) >> 4;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(&bar.full[s], 1);
-            mbar_init(&bar.empty[s], two ? 2 : 1);
-            mbar_init(&bar.clean[s], 1);
-        }
-        mbar_init(&bar.qfull, 1);
-        for (int t = 0; t < 2; ++t) {
+    // The loading warp's barriers are its own until the block meets below: it starts
+    // its copies before that.
+    if (warp == kLoad) {
+        if (lane < NS) mbar_init(&bar.full[lane], 1);
+        if (lane == NS) mbar_init(&bar.qfull, 1);
+        fence_mbar_init();
+        __syncwarp();
+    } else if (warp == kClean) {
+        if (lane < NS) {
+            mbar_init(&bar.empty[lane], two ? 2 : 1);
+            mbar_init(&bar.clean[lane], 1);
+        } else if (lane < NS + 2) {
+            const int t = lane - NS;
             mbar_init(&bar.sfull[t], 1);
             mbar_init(&bar.sfree[t], 4);
             mbar_init(&bar.pfull[t][0], 4);
@@ -114,6 +119,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
         fence_mbar_init();
     }
     if (warp == kMma0) tmem_alloc(&bar.tmem, 512);
+    // the copy of step it (K and V in turn) into its slot
+    const auto load = [&](int it, int slot) {
+        const int g = h / a.R;
+        const int key = step_key<KT>(P.kt, b, t0 + (it >> 1));
+        const TensorMap& src = it & 1 ? P.v : P.k;
+        mbar_arrive_expect_tx(&bar.full[slot], C::kTileBytes);
+        for (int c = 0; c < C::kChunks; ++c)
+            tma_load(sKV + slot * C::kTileBytes + c * C::kChunkBytes, &src.map, c * 64, key, g * src.head,
+                     b * src.batch, &bar.full[slot]);
+    };
+    const int early = min(2 * nt, NS);     // copies that need no free slot
+    if (warp == kLoad && nt > 0 && elect_one()) {
+        mbar_arrive_expect_tx(&bar.qfull, (two ? 2 : 1) * C::kQBytes);
+        for (int t = 0; t < (two ? 2 : 1); ++t)
+            for (int c = 0; c < C::kChunks; ++c)
+                tma_load(sQ + t * C::kQBytes + c * CHUNK_BYTES, &P.q.map, c * 64, i0 + t * kTile,
+                         h * P.q.head, b * P.q.batch, &bar.qfull);
+        for (int it = 0; it < early; ++it) load(it, it);
+    }
     if (a.table) {
         // base-2 bias by relative position -D - kSlack .. D + kSlack of this head
         const T* row = static_cast<const T*>(a.table) + h * a.table_stride;
@@ -127,26 +151,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
 
     if (warp == kLoad) {
         if (nt > 0 && elect_one()) {
-            const int g = h / a.R;
-            mbar_arrive_expect_tx(&bar.qfull, (two ? 2 : 1) * C::kQBytes);
-            for (int t = 0; t < (two ? 2 : 1); ++t)
-                for (int c = 0; c < C::kChunks; ++c)
-                    tma_load(sQ + t * C::kQBytes + c * CHUNK_BYTES, &P.q.map, c * 64, i0 + t * kTile,
-                             h * P.q.head, b * P.q.batch, &bar.qfull);
             Ring r;
-            int issued = 0;
+            r.step(early, NS);
+            int issued = early;
             bool ok = true;
-            for (int it = 0; it < 2 * nt; ++it) {
+            for (int it = early; it < 2 * nt; ++it) {
                 if (!mbar_wait(&bar.empty[r.slot], r.phase ^ 1u, a.err, ERR_TIMEOUT_PRODUCER)) {
                     ok = false;
                     break;
                 }
-                const int key = step_key<KT>(P.kt, b, t0 + (it >> 1));
-                const TensorMap& src = it & 1 ? P.v : P.k;
-                mbar_arrive_expect_tx(&bar.full[r.slot], C::kTileBytes);
-                for (int c = 0; c < C::kChunks; ++c)
-                    tma_load(sKV + r.slot * C::kTileBytes + c * C::kChunkBytes, &src.map, c * 64, key,
-                             g * src.head, b * src.batch, &bar.full[r.slot]);
+                load(it, r.slot);
                 ++issued;
                 r.step(1, NS);
             }
@@ -313,11 +327,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
                         p[c] = pack16<BF>(e0, e1);
                         p[c + 1] = pack16<BF>(e2, e3);
                     }
-                    // the buffer's last P has been read
-                    if (q == 0 && j >= C::kPBufs) {
-                        ok = warp_wait(&bar.pfree[t][buf],
-                                       C::kPBufs == 2 ? ((j - 2) >> 1) & 1 : (j - 1) & 1, a.err,
-                                       ERR_TIMEOUT_EPILOGUE);
+                    // the buffer's last P has been read: of two, the one of tile j - 2 was when
+                    // S of this tile was done (its products were issued before it)
+                    if (q == 0 && j > 0 && C::kPBufs == 1) {
+                        ok = warp_wait(&bar.pfree[t][0], (j - 1) & 1, a.err, ERR_TIMEOUT_EPILOGUE);
                         if (!ok) break;
                         tc_fence_after();
                     }
@@ -349,10 +362,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
                     a.lse[row] = lse2 * (float)kLn2;
             }
             tc_fence_after();
-            // the rows of out: through shared memory in whole boxes, or directly
+            // the rows of out, through this warp's rows of the tile's Q
             float* part = P.splits > 1 ? P.part.out + (split * P.part.rows + row) * a.d : nullptr;
-            T* out = static_cast<T*>(a.o.p) + b * a.o.sb + (int64_t)i * a.o.st + h * a.o.sh;
             uint8_t* stage = sQ + t * C::kQBytes;
+#pragma unroll 2
             for (int c = 0; c < dsteps * 16 && ok; c += 16) {
                 float o[16];
                 if (nt > 0) {
@@ -366,29 +379,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         if (live && c + e < a.d) part[c + e] = o[e];
-                } else if (P.out_box) {
-#pragma unroll
-                    for (int e = 0; e < 16; e += 8)
-                        *reinterpret_cast<uint4*>(stage + (c >> 6) * CHUNK_BYTES +
-                                                  swz_offset(r, (c & 63) + e)) =
-                            make_uint4(pack16<BF>(o[e], o[e + 1]), pack16<BF>(o[e + 2], o[e + 3]),
-                                       pack16<BF>(o[e + 4], o[e + 5]), pack16<BF>(o[e + 6], o[e + 7]));
+                    __syncwarp();
                 } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (live && c + e < a.d) out[c + e] = from_f<T>(o[e]);
+                    stage16<BF>(stage, r, c, o);
                 }
-                __syncwarp();
             }
-            if (P.out_box && !part) {
-                fence_proxy_async_smem();
-                named_sync(1 + t, kTile);
-                if (quarter == 0 && elect_one()) {
-                    for (int c = 0; c < C::kChunks; ++c)
-                        if (c * 64 < a.d)
-                            tma_store(&P.o.map, stage + c * CHUNK_BYTES, c * 64, i0 + t * kTile, h, b);
-                    tma_store_wait();
-                }
+            if (!part) {
+                const int w0 = i - lane;      // the warp's first query
+                unstage_rows<32>(stage, quarter * 32, a.n - w0, a.d,
+                             static_cast<uint16_t*>(a.o.p) + b * a.o.sb + (int64_t)w0 * a.o.st + h * a.o.sh,
+                             a.o.st, P.out_vec, lane);
             }
         }
     }

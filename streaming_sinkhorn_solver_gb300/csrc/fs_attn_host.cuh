@@ -22,12 +22,12 @@ struct Partials {
 };
 
 struct FwdArgs {
-    TensorMap q, k, v, o;
+    TensorMap q, k, v;
     Args a;
     KeyTiles kt;
     Partials part;
     int row_blocks, splits;
-    int out_box;       // out is written through its tensor map
+    int out_vec;       // the rows of out take 16-byte stores
 };
 
 struct GradArgs {

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Tuple
 
@@ -629,26 +630,34 @@ def fs_relative_buckets(num_buckets: int, max_distance: int, bidirectional: bool
     return np.array(below + [0] + above, dtype=np.int32)
 
 
-def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos) -> fs_attention:
-    """Checked description of a call (see the C header for each field)."""
+# the fields of fs_attention, packed in one go (a ctypes field costs 0.1 us to set)
+_ATTENTION = struct.Struct("=4i3qf3i24q2QqQq2Q")
+assert _ATTENTION.size == ctypes.sizeof(fs_attention)
+_NO_STRIDES = (0, 0, 0)
+_DTYPES = {}
+
+
+def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, strides) -> fs_attention:
+    """Checked description of a call (see the C header for each field);
+    `strides` are those of out, dout, dq, dk and dv."""
     import torch
-    if not (_is_torch(q) and q.is_cuda and q.dtype in (torch.bfloat16, torch.float16)):
+    if not _DTYPES:
+        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1})
+    dtype = _DTYPES.get(getattr(q, "dtype", None))
+    if dtype is None or not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise TypeError("q must be a bfloat16 or float16 CUDA tensor")
     if q.dim() != 4:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected (batch, n, heads, d)")
-    batch, n, heads, d = q.shape
     if k.dim() != 4:
         raise ValueError(f"k has shape {tuple(k.shape)}, expected (batch, m, kv_heads, d)")
+    batch, n, heads, d = q.shape
     m, kv_heads = k.shape[1], k.shape[2]
-    at = fs_attention()
-    at.dtype = 0 if q.dtype == torch.bfloat16 else 1
-    at.heads, at.kv_heads, at.d, at.batch, at.n, at.m = heads, kv_heads, d, batch, n, m
-    at.scale = d ** -0.5 if scale is None else scale
-    at.q_stride = _att_strides(q, "q", q.shape, q)
-    at.k_stride = _att_strides(k, "k", (batch, m, kv_heads, d), q)
-    at.v_stride = _att_strides(v, "v", (batch, m, kv_heads, d), q)
+    qs = _att_strides(q, "q", q.shape, q)
+    ks = _att_strides(k, "k", (batch, m, kv_heads, d), q)
+    vs = _att_strides(v, "v", (batch, m, kv_heads, d), q)
+    len_p = mask_p = mask_stride = bias_p = bias_stride = buckets_p = pos_p = nb = far = 0
     if kv_len is not None:
-        at.kv_len = _i_ptr(kv_len, "kv_len", (batch,), torch.int32)
+        len_p = _i_ptr(kv_len, "kv_len", (batch,), torch.int32)
     if key_mask is not None:
         if not (key_mask.is_cuda and key_mask.dtype in (torch.bool, torch.uint8)):
             raise TypeError("key_mask must be a bool or uint8 CUDA tensor")
@@ -656,7 +665,7 @@ def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos) -> f
             raise ValueError(f"key_mask has shape {tuple(key_mask.shape)}, expected {(batch, m)}")
         if m > 1 and key_mask.stride(1) != 1:
             raise TypeError("the keys of key_mask must be contiguous")
-        at.key_mask, at.mask_stride = key_mask.data_ptr(), key_mask.stride(0)
+        mask_p, mask_stride = key_mask.data_ptr(), key_mask.stride(0)
     if (bias is None) != (bias_buckets is None):
         raise TypeError("bias and bias_buckets come together")
     if bias is not None:
@@ -664,35 +673,46 @@ def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos) -> f
             raise TypeError(f"bias must be a CUDA tensor of {q.dtype}")
         if bias.dim() != 2 or bias.shape[0] not in (1, heads) or bias.shape[1] < 1:
             raise ValueError(f"bias has shape {tuple(bias.shape)}, expected ({heads} or 1, buckets)")
-        if bias.shape[1] > 1 and bias.stride(1) != 1:
+        nb = bias.shape[1]
+        if nb > 1 and bias.stride(1) != 1:
             raise TypeError("the buckets of bias must be contiguous")
         size = bias_buckets.numel()
         if size % 2 == 0:
             raise ValueError("bias_buckets must have 2 max_distance + 1 entries")
-        at.n_buckets, at.max_distance = bias.shape[1], size // 2
-        at.bias = bias.data_ptr()
-        at.bias_stride = 0 if bias.shape[0] == 1 else bias.stride(0)
-        at.bias_buckets = _i_ptr(bias_buckets, "bias_buckets", (size,), torch.int32)
+        far = size // 2
+        bias_p = bias.data_ptr()
+        bias_stride = 0 if bias.shape[0] == 1 else bias.stride(0)
+        buckets_p = _i_ptr(bias_buckets, "bias_buckets", (size,), torch.int32)
         if q_pos is not None:
-            at.q_pos = _i_ptr(q_pos, "q_pos", (batch,), torch.int32)
+            pos_p = _i_ptr(q_pos, "q_pos", (batch,), torch.int32)
+    at = fs_attention()
+    _ATTENTION.pack_into(at, 0, dtype, heads, kv_heads, d, batch, n, m,
+                         d ** -0.5 if scale is None else scale, nb, far, 0, *qs, *ks, *vs, *strides,
+                         len_p, mask_p, mask_stride, bias_p, bias_stride, buckets_p, pos_p)
     return at
 
 
-_strides3 = ctypes.c_int64 * 3
-
-
 def _att_strides(x, name: str, shape, like):
-    if not (_is_torch(x) and x.is_cuda and x.dtype == like.dtype and x.device == like.device):
+    if getattr(x, "dtype", None) != like.dtype or x.device != like.device:
         raise TypeError(f"{name} must be a {like.dtype} tensor on {like.device}")
-    if tuple(x.shape) != tuple(shape):
+    if x.shape != shape:
         raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
     sb, st, sh, sd = x.stride()
     if sd != 1 and x.shape[3] > 1:
         raise TypeError(f"the last dimension of {name} must be contiguous")
-    return _strides3(sb, st, sh)
+    return sb, st, sh
 
 
-def _att_empty(shape, dtype, like, stream):
+def _att_stream(stream, like) -> int:
+    """The cudaStream_t of a call: explicit, else torch's current one."""
+    if stream is not None:
+        return int(getattr(stream, "cuda_stream", stream))
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without a Stream object
+    return raw(like.get_device()) if raw else torch.cuda.current_stream(like.device).cuda_stream
+
+
+def _att_empty(like, shape, dtype, stream):
     """A result, allocated for the stream that writes it."""
     import torch
     if isinstance(stream, torch.cuda.Stream):
@@ -720,15 +740,19 @@ def fs_cross_attention(q, k, v, *, scale: Optional[float] = None, kv_len=None, k
     do not count may hold anything.
     """
     import torch
-    at = _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos)
     if out is None:
-        out = _att_empty(q.shape, q.dtype, q, stream)
+        out = _att_empty(q, q.shape, q.dtype, stream) if _is_torch(q) else q
+    at = _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos,
+                    (*_att_strides(out, "out", q.shape, q), *_NO_STRIDES * 4))
+    rows = (q.shape[0], q.shape[2], q.shape[1])
     if lse is None:
-        lse = _att_empty((at.batch, at.heads, at.n), torch.float32, q, stream)
-    at.out_stride = _att_strides(out, "out", q.shape, q)
+        lse = _att_empty(q, rows, torch.float32, stream)
+        lse_p = lse.data_ptr()
+    else:
+        lse_p = _ptr(lse, "lse", rows)
     st = load_library().fs_cross_attention(
-        ctypes.byref(at), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-        _ptr(lse, "lse", (at.batch, at.heads, at.n)), _stream(stream, q))
+        ctypes.byref(at), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse_p,
+        _att_stream(stream, q))
     _raise(st)
     return out, lse
 
@@ -739,25 +763,25 @@ def fs_cross_attention_grad(q, k, v, out, lse, dout, *, scale: Optional[float] =
     """Gradients of fs_cross_attention for the gradient dout of its out; out
     and lse as it returned them, the other arguments as it got them.  Returns
     (dq, dk, dv, dbias), each as its input (dbias None without a bias)."""
-    at = _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos)
-    at.out_stride = _att_strides(out, "out", q.shape, q)
-    at.dout_stride = _att_strides(dout, "dout", q.shape, q)
-    dq = _att_empty(q.shape, q.dtype, q, stream) if dq is None else dq
-    dk = _att_empty(k.shape, q.dtype, q, stream) if dk is None else dk
-    dv = _att_empty(v.shape, q.dtype, q, stream) if dv is None else dv
-    at.dq_stride = _att_strides(dq, "dq", q.shape, q)
-    at.dk_stride = _att_strides(dk, "dk", k.shape, q)
-    at.dv_stride = _att_strides(dv, "dv", v.shape, q)
-    if bias is not None:
-        dbias = _att_empty(bias.shape, q.dtype, q, stream) if dbias is None else dbias
+    dq = _att_empty(q, q.shape, q.dtype, stream) if dq is None else dq
+    dk = _att_empty(k, k.shape, q.dtype, stream) if dk is None else dk
+    dv = _att_empty(v, v.shape, q.dtype, stream) if dv is None else dv
+    at = _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos,
+                    (*_att_strides(out, "out", q.shape, q), *_att_strides(dout, "dout", q.shape, q),
+                     *_att_strides(dq, "dq", q.shape, q), *_att_strides(dk, "dk", k.shape, q),
+                     *_att_strides(dv, "dv", v.shape, q)))
+    if bias is None:
+        dbias = None
+    else:
+        dbias = _att_empty(q, bias.shape, q.dtype, stream) if dbias is None else dbias
         if not (dbias.is_cuda and dbias.dtype == q.dtype and dbias.is_contiguous()
                 and dbias.shape == bias.shape):
             raise TypeError(f"dbias must be a contiguous {q.dtype} tensor of shape "
                             f"{tuple(bias.shape)}")
     st = load_library().fs_cross_attention_grad(
         ctypes.byref(at), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-        _ptr(lse, "lse", (at.batch, at.heads, at.n)), dout.data_ptr(), dq.data_ptr(),
-        dk.data_ptr(), dv.data_ptr(), dbias.data_ptr() if bias is not None else None,
-        _stream(stream, q))
+        _ptr(lse, "lse", (q.shape[0], q.shape[2], q.shape[1])), dout.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), None if dbias is None else dbias.data_ptr(),
+        _att_stream(stream, q))
     _raise(st)
-    return dq, dk, dv, dbias if bias is not None else None
+    return dq, dk, dv, dbias

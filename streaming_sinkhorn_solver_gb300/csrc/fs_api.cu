@@ -48,8 +48,9 @@ fs_status begin_call(Call& c, void* stream, bool scratch) {
         return fail(FS_ERR_UNSUPPORTED, "make one call on this device before capturing a graph");
     if (w.done == nullptr) {
         FS_CUDA(cudaDeviceGetAttribute(&w.sms, cudaDevAttrMultiProcessorCount, c.dev));
-        FS_CUDA(cudaMalloc(&w.err_word, kErrWordBytes));
-        FS_CUDA(cudaMemset(w.err_word, 0, kErrWordBytes));
+        FS_CUDA(cudaMalloc(&w.err_word, kErrWordBytes + sizeof(unsigned) * kCounters));
+        FS_CUDA(cudaMemset(w.err_word, 0, kErrWordBytes + sizeof(unsigned) * kCounters));
+        w.counters = reinterpret_cast<unsigned*>(reinterpret_cast<char*>(w.err_word) + kErrWordBytes);
         FS_CUDA(cudaDeviceSynchronize());
         FS_CUDA(cudaEventCreateWithFlags(&w.done, cudaEventDisableTiming));
     }

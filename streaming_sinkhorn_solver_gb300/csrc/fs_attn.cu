@@ -122,16 +122,17 @@ bool mappable(const View& w, int B, int tokens, int heads, int d) {
            w.sh < far && w.sb < far;
 }
 
-// An input that the kernels read through a tensor map: in place, or from a
-// copy in the workspace with rows of 16-byte multiples.
+// An input that the kernels read through a tensor map (or 16 bytes at a time):
+// in place, or from a copy in the workspace with rows of 16-byte multiples.
 struct Input {
     View* w;
     int tokens, heads;
     bool copy = false;
     size_t off = 0;
     Input(View& v, int t, int h) : w(&v), tokens(t), heads(h) {}
-    void plan(const Args& a, Layout& L) {
-        copy = !mappable(*w, a.B, tokens, heads, a.d);
+    void plan(const Args& a, Layout& L, bool map = true) {
+        copy = map ? !mappable(*w, a.B, tokens, heads, a.d)
+                   : a.d % 8 != 0 || !aligned16(*w, a.B, tokens, heads);
         if (copy) off = L.take(2 * (size_t)a.B * tokens * heads * pitch(a));
     }
     static int pitch(const Args& a) { return (a.d + 7) / 8 * 8; }
@@ -177,6 +178,36 @@ int choose_key_splits(int64_t blocks, int tiles, int sms) {
     return (int)std::max<int64_t>(s, 1);
 }
 
+// Whether the few-query kernel takes a call: one tile of its 16 rows per key head, or
+// two where query heads share keys (the 128-row tiles of the other kernel then read
+// the keys once per query head; with a head of its own each they read them once
+// too).  8 heads of 64, 21 queries and 77 keys: 8.0 us here, 7.0 us there; 4 queries
+// of 8 heads to a key head, 20000 keys: twice as fast here.
+bool few_rows(const Args& a) {
+    const int64_t rows = (int64_t)a.R * a.n;
+    return rows <= 16 || (rows <= 32 && a.R > 1);
+}
+
+// Its splits of the keys.  A split costs its keys and a fixed part (set-up, its share
+// of the join) worth about 512 keys; blocks beyond the resident ones wait for a
+// whole turn.  The fewest splits of the least cost.
+int choose_decode_splits(int64_t blocks, int m, int64_t resident) {
+    constexpr double kFixedKeys = 512.0;
+    if (blocks > kCounters) return 1;
+    const int64_t most = std::min<int64_t>((m + kDecodeKeys - 1) / kDecodeKeys, 4 * resident / blocks + 1);
+    int best = 1;
+    double least = 0.0;
+    for (int64_t s = 1; s <= most; ++s) {
+        const double turns = (double)((blocks * s + resident - 1) / resident);
+        const double cost = turns * ((double)m / (double)s + kFixedKeys);
+        if (s == 1 || cost < 0.999 * least) {
+            least = cost;
+            best = (int)s;
+        }
+    }
+    return best;
+}
+
 fs_status forward_entry(const fs_attention* at, const void* q, const void* k, const void* v,
                         void* out, float* lse, void* stream) {
     FS_TRY(check_desc(at));
@@ -200,36 +231,61 @@ fs_status forward_entry(const fs_attention* at, const void* q, const void* k, co
         FS_CUDA(launch_zero(a, a.o, a.n, a.H, lse, c.stream));
         return FS_OK;
     }
-    Input inputs[3] = {{a.q, a.n, a.H}, {a.k, a.m, a.G}, {a.v, a.m, a.G}};
-    TilePlan tiles;
-    for (Input& x : inputs) x.plan(a, c.L);
-    tiles.plan(a, c.L);
     int dev = 0, sms = 0;
     FS_CUDA(cudaGetDevice(&dev));
     FS_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    p.row_blocks = (a.n + 2 * kTile - 1) / (2 * kTile);
-    p.splits = choose_key_splits((int64_t)p.row_blocks * a.H * a.B, tiles.kt.tiles, sms);
+    Input inputs[3] = {{a.q, a.n, a.H}, {a.k, a.m, a.G}, {a.v, a.m, a.G}};
+    const bool few = few_rows(a);
+    for (Input& x : inputs) x.plan(a, c.L, !few);
+    TilePlan tiles;
+    DecodeArgs dp = {};
+    int splits;
+    if (few) {
+        dp.row_blocks = a.R * a.n <= 8 ? 1 : 2;
+        dp.groups = (a.R * a.n + 8 * dp.row_blocks - 1) / (8 * dp.row_blocks);
+        dp.dp = (a.d + 3) / 4 * 4;
+        int resident = 0;
+        FS_CUDA(decode_resident(a, dp.row_blocks, &resident));
+        splits = choose_decode_splits((int64_t)a.B * a.G * dp.groups, a.m, (int64_t)sms * resident);
+    } else {
+        tiles.plan(a, c.L);
+        p.row_blocks = (a.n + 2 * kTile - 1) / (2 * kTile);
+        splits = choose_key_splits((int64_t)p.row_blocks * a.H * a.B, tiles.kt.tiles, sms);
+    }
+    Partials part = {};
+    part.rows = rows;
     size_t part_out = 0, part_lse = 0;
-    if (p.splits > 1) {
-        part_out = c.L.take(sizeof(float) * (size_t)p.splits * rows * a.d);
-        part_lse = c.L.take(sizeof(float) * (size_t)p.splits * rows);
+    if (splits > 1) {
+        part_out = c.L.take(sizeof(float) * (size_t)splits * rows * ((a.d + 3) / 4 * 4));
+        part_lse = c.L.take(sizeof(float) * (size_t)splits * rows);
     }
     const bool scratch = c.L.off > 0;
     FS_TRY(begin_call(c, stream, scratch));
     FS_TRY(ensure_capacity(c));
     for (Input& x : inputs) FS_TRY(x.run(c, a));
+    if (splits > 1) {
+        part.out = c.at<float>(part_out);
+        part.lse2 = c.at<float>(part_lse);
+    }
+    a.err = c.ws->err_word;
+    if (few) {
+        dp.a = a;
+        dp.part = part;
+        dp.splits = splits;
+        dp.counters = c.ws->counters;
+        FS_CUDA(launch_decode(dp, c.stream));
+        return scratch ? end_call(c) : FS_OK;
+    }
     FS_TRY(tiles.run(c, a));
     p.kt = tiles.kt;
-    p.part.rows = rows;
-    p.part.out = p.splits > 1 ? c.at<float>(part_out) : nullptr;
-    p.part.lse2 = p.splits > 1 ? c.at<float>(part_lse) : nullptr;
+    p.part = part;
+    p.splits = splits;
     p.out_vec = a.d % 8 == 0 && aligned16(a.o, a.B, a.n, a.H);
-    a.err = c.ws->err_word;
     FS_TRY(make_tensor_map(p.q, a.q, a.B, a.n, a.H, a.d, a.bf16));
     FS_TRY(make_tensor_map(p.k, a.k, a.B, a.m, a.G, a.d, a.bf16, forward_keys(a.d)));
     FS_TRY(make_tensor_map(p.v, a.v, a.B, a.m, a.G, a.d, a.bf16, forward_keys(a.d)));
     FS_CUDA(launch_forward_tc(p, c.stream));
-    if (p.splits > 1) FS_CUDA(launch_combine(a, p.part, p.splits, c.stream));
+    if (splits > 1) FS_CUDA(launch_combine(a, part, splits, c.stream));
     return scratch ? end_call(c) : FS_OK;
 }
 

@@ -773,19 +773,6 @@ __global__ void __launch_bounds__(kBiasThreads) k_grad_bias(const __grid_constan
 
 // ---------------------------------------------------------------------------
 
-template <typename K>
-cudaError_t raise_smem(K kernel, size_t bytes, std::atomic<uint64_t>& ready) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (!(ready.load() >> dev & 1)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(1ull << dev);
-    }
-    return cudaSuccess;
-}
-
 int ring_stages(size_t fixed, size_t per_stage) {
     const int s = (int)((kSmemLimit - fixed) / per_stage);
     return s < kMaxRing ? s : kMaxRing;

@@ -407,15 +407,7 @@ cudaError_t launch_forward(const FwdArgs& p, cudaStream_t s) {
     constexpr size_t most = kFwdFixed<HD> + sizeof(float) * (2 * (size_t)(kMaxDistance + kSlack) + 1);
     static_assert(most <= kSmemLimit, "forward kernel does not fit in shared memory");
     static std::atomic<uint64_t> ready{0};    // devices whose shared-memory limit is raised
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (!(ready.load() >> dev & 1)) {
-        e = cudaFuncSetAttribute(k_forward_tc<HD, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)most);
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(1ull << dev);
-    }
+    if (cudaError_t e = raise_smem(k_forward_tc<HD, BF>, most, ready); e != cudaSuccess) return e;
     const unsigned blocks = (unsigned)((int64_t)p.row_blocks * p.a.H * p.a.B * p.splits);
     k_forward_tc<HD, BF><<<blocks, kFwdThreads, kFwdFixed<HD> + bias, s>>>(p);
     count_launch();

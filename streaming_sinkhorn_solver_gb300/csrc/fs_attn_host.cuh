@@ -4,6 +4,9 @@
 #include "fs_attn_tc.cuh"
 #include "fs_host.cuh"
 
+#include <algorithm>
+#include <atomic>
+
 namespace fs {
 namespace attn {
 
@@ -43,6 +46,19 @@ struct GradArgs {
 // dq, then dk and dv, then dbias (nullptr: none)
 cudaError_t launch_grad_tc(const GradArgs& p, void* dbias, cudaStream_t s);
 cudaError_t launch_forward_tc(const FwdArgs& p, cudaStream_t s);
+
+// Few query rows per key head: row_blocks of 8 rows to a block (1 or 2), in `groups`.
+struct DecodeArgs {
+    Args a;
+    Partials part;
+    int splits, groups, row_blocks;
+    int dp;                // elements of a partial row: d, to a multiple of 4
+    unsigned* counters;    // [batch x key heads x groups], zero between calls
+};
+constexpr int kDecodeKeys = 128;           // the splits are whole multiples of these keys
+cudaError_t launch_decode(const DecodeArgs& p, cudaStream_t s);
+// blocks of it that an SM holds
+cudaError_t decode_resident(const Args& a, int row_blocks, int* blocks);
 cudaError_t launch_combine(const Args& a, const Partials& part, int splits, cudaStream_t s);
 cudaError_t launch_key_tiles(const Args& a, uint4* words, int* list, int* count, int tiles,
                              cudaStream_t s);
@@ -51,6 +67,20 @@ cudaError_t launch_zero(const Args& a, const View& w, int tokens, int heads, flo
 // contiguous copy of a (batch, token, head, d) tensor with rows of dp elements, zero beyond d
 cudaError_t launch_pack(const View& from, void* to, int B, int tokens, int heads, int d, int dp,
                         cudaStream_t s);
+
+// Raises a kernel's limit of dynamic shared memory, once per device.
+template <typename K>
+cudaError_t raise_smem(K kernel, size_t bytes, std::atomic<uint64_t>& ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!(ready.load() >> dev & 1)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(1ull << dev);
+    }
+    return cudaSuccess;
+}
 
 // boxes of `rows` tokens
 fs_status make_tensor_map(TensorMap& t, const View& w, int B, int tokens, int heads, int d, bool bf16,

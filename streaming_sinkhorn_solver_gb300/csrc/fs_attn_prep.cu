@@ -50,32 +50,35 @@ __global__ void __launch_bounds__(128) k_combine(Args a, Partials part, int spli
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (row >= part.rows) return;
+    const int i = (int)(row % a.n);
+    const int64_t bh = row / a.n;
+    const int h = (int)(bh % a.H), b = (int)(bh / a.H);
+    T* out = static_cast<T*>(a.o.p) + b * a.o.sb + (int64_t)i * a.o.st + h * a.o.sh;
     float top = -INFINITY;
     for (int s = lane; s < splits; s += 32) top = fmaxf(top, part.lse2[s * part.rows + row]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float use = top == -INFINITY ? 0.f : top;
-    float total = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const float base = top == -INFINITY ? 0.f : top;
+    float total = 0.f, acc[kMaxHeadDim / 32];
+#pragma unroll
+    for (int e = 0; e < kMaxHeadDim / 32; ++e) acc[e] = 0.f;
     for (int s0 = 0; s0 < splits; s0 += 32) {
-        const float mine = s0 + lane < splits ? ex2(part.lse2[(s0 + lane) * part.rows + row] - use) : 0.f;
+        const float mine = s0 + lane < splits ? ex2(part.lse2[(s0 + lane) * part.rows + row] - base) : 0.f;
         const int some = min(32, splits - s0);
+#pragma unroll 4
         for (int s = 0; s < some; ++s) {
             const float w = __shfl_sync(0xffffffffu, mine, s);
             total += w;
             const float* src = part.out + ((s0 + s) * part.rows + row) * a.d;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < kMaxHeadDim / 32; ++e)
                 if (lane + 32 * e < a.d) acc[e] = fmaf(w, src[lane + 32 * e], acc[e]);
         }
     }
-    const int i = (int)(row % a.n);
-    const int64_t bh = row / a.n;
-    const int h = (int)(bh % a.H), b = (int)(bh / a.H);
-    T* out = static_cast<T*>(a.o.p) + b * a.o.sb + (int64_t)i * a.o.st + h * a.o.sh;
     const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (lane + 32 * e < a.d) out[lane + 32 * e] = from_f<T>(acc[e] * inv);
+    for (int e = 0; e < kMaxHeadDim / 32; ++e)
+        if (lane + 32 * e < a.d) out[lane + 32 * e] = from_f<T>(total == 0.f ? 0.f : acc[e] * inv);
     if (lane == 0) a.lse[row] = total == 0.f ? -INFINITY : (top + lg2(total)) * (float)kLn2;
 }
 

@@ -35,6 +35,7 @@ constexpr int kShiftBlocks = 1024;
 
 // One workspace per device: a single cudaMalloc'd arena carved per call.
 constexpr size_t kErrWordBytes = 32;
+constexpr int kCounters = 4096;
 inline unsigned long long* fix_stats_of(uint32_t* err_word) {
     return reinterpret_cast<unsigned long long*>(err_word + 2);
 }
@@ -50,6 +51,8 @@ struct Workspace {
     // error bits; bytes 8..23 hold the cumulative fixup statistics (two
     // 64-bit counters: fixup launches, rows recomputed)
     uint32_t* err_word = nullptr;
+    // arrival counters of blocks that join their results (kCounters, zero between calls)
+    unsigned* counters = nullptr;
     int sms = 0;
 };
 

@@ -5,17 +5,19 @@
 //
 // k_grad_q: a block takes 128 queries of one head and streams the keys.
 //     S = Q K^T, dP = dO V^T, p = 2^{x - lse2}, ds = p (dP - delta),
-//     dQ += ds K;   Q and dO stay in TMEM as the A operands of S and dP, ds
-//     replaces dP there as the A operand of dQ.
-//   Also delta_i = dO_i . O_i, the padded rows (lse2, delta) that k_grad_kv
-//   reads, and the sums of ds by relative position for the bias gradient.
+//     dQ += ds K;   Q, dO and ds are A operands in TMEM.
+//   Also delta_i = dO_i . O_i, the rows (-lse2, -delta) that k_grad_kv reads, and
+//   the sums of ds by relative position for the bias gradient.
 // k_grad_kv: a block takes 128 keys of one key head and streams the queries of
 //   all its heads, with keys as rows:
-//     S = K Q^T, dP = V dO^T, dV += p dO, dK += ds Q;   p replaces S in TMEM
-//     and ds replaces dP, each the A operand of its product.
-// In both, eight warps hold the elementwise part: warps w and w + 4 the same 32
-// rows, 64 columns each; one thread issues the products in an order that keeps
-// the tensor core at the next tile's scores while this tile's are in registers.
+//     S = K Q^T, dP = V dO^T, dV += p dO, dK += ds Q;   p and ds in TMEM.
+// In both, eight warps hold the elementwise part (warps w and w + 4 the same 32
+// rows, 64 columns of a tile each), and one thread issues the products in an order
+// that keeps the tensor core at other products while a tile is in registers: p
+// replaces S and ds replaces dP in TMEM as operands.  (Columns of their own for p
+// and ds, as in the forward kernel, leave room for tiles of 64 only with wide heads:
+// at batch 4, 2048 x 2048, 16 heads the gradients then took 374 instead of 341 us
+// with heads of 64, 550 instead of 446 us with heads of 128.)
 #include "fs_attn_host.cuh"
 
 #include <atomic>
@@ -26,17 +28,16 @@ namespace attn {
 
 namespace {
 
-constexpr int kGradThreads = 384;
+constexpr int kElemWarps = 8;
+constexpr int kLoad = kElemWarps, kIssue = kElemWarps + 1, kClean = kElemWarps + 2;   // and one idle
+constexpr int kGradThreads = 32 * (kElemWarps + 4);
 constexpr int kSlack = 2 * kTile;
 constexpr int kMaxRing = 8;
-constexpr int kElemWarps = 8;
 constexpr int kBands = 4;           // rows of bias sums: one per 32 queries
 
-// barriers, then the TMEM address
 struct GradBars {
     uint64_t full[kMaxRing], empty[kMaxRing], clean[kMaxRing];
-    uint64_t ready, sfull, sfree, done, drain, pfull, dsfull;
-    uint64_t dpfull[2];
+    uint64_t ready, sfull, sfree, dpfull[2], pfull, dsfull, done, drain;
     uint32_t tmem, pad;
 };
 
@@ -74,13 +75,12 @@ __device__ __forceinline__ void load16(const View& w, int64_t off, int c, int d,
     }
 }
 
-// Columns [c0, c1) of a row of sums in TMEM, times `mul`, rounded, to a row in memory
-// (zero where !keep).  Whole warps.
+// Columns [c0, c1) of a row of sums in TMEM, times `mul` (zero where !keep), rounded into
+// a staged tile.  Whole warps.
 template <bool BF>
-__device__ __forceinline__ void store_row(const View& w, int64_t off, uint32_t tmem_row, int c0, int c1,
-                                          int d, float mul, bool any, bool live, bool keep, bool vec) {
-    using T = Elem<BF>;
-    T* out = static_cast<T*>(w.p) + off;
+__device__ __forceinline__ void stage_row(uint8_t* tile, int r, uint32_t tmem_row, int c0, int c1, float mul,
+                                          bool any, bool keep) {
+#pragma unroll 2
     for (int c = c0; c < c1; c += 16) {
         float o[16];
         if (any) {
@@ -90,19 +90,7 @@ __device__ __forceinline__ void store_row(const View& w, int64_t off, uint32_t t
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[e] = any && keep ? o[e] * mul : 0.f;
-        if (vec) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-                if (live && c + e < d)
-                    *reinterpret_cast<uint4*>(out + c + e) =
-                        make_uint4(pack16<BF>(o[e], o[e + 1]), pack16<BF>(o[e + 2], o[e + 3]),
-                                   pack16<BF>(o[e + 4], o[e + 5]), pack16<BF>(o[e + 6], o[e + 7]));
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (live && c + e < d) out[c + e] = from_f<T>(o[e]);
-        }
-        __syncwarp();
+        stage16<BF>(tile, r, c, o);
     }
 }
 
@@ -116,10 +104,38 @@ __device__ __forceinline__ void fill_bias(const Args& a, int h, float* sBias, in
 
 // ---------------------------------------------------------------------------
 
-// TMEM columns of k_grad_q.  ds of tile j replaces dP of tile j; with heads of 64
-// there is room for two dP tiles, so the next one does not wait for dQ.
+// Sums of a 32 x 32 block (a row per lane) along its diagonals, column - row = lane
+// (upper) and lane - 32 (lower), through shared memory, ROWS rows of 33 floats at a
+// time: in step s lane l reads column (s + l) mod 32 of row s.
+template <int ROWS>
+__device__ __forceinline__ void diagonals(const float* v, float* scratch, int lane, float& upper,
+                                          float& lower) {
+#pragma unroll
+    for (int s0 = 0; s0 < 32; s0 += ROWS) {
+        if (ROWS == 32 || lane / ROWS == s0 / ROWS) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) scratch[(lane - s0) * 33 + c] = v[c];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int s = s0; s < s0 + ROWS; ++s) {
+            const float x = scratch[(s - s0) * 33 + ((s + lane) & 31)];
+            if (s + lane < 32)
+                upper += x;
+            else
+                lower += x;
+        }
+        __syncwarp();
+    }
+}
+
 template <int HD>
-struct QCols {
+struct GradQ {
+    static constexpr int kKeys = kTile, kCols = kTile / 2;       // keys of a tile, of a warp
+    static constexpr int kChunks = HD / 64, kChunkBytes = CHUNK_BYTES;
+    static constexpr int kTileBytes = kChunks * CHUNK_BYTES;
+    // TMEM columns; with heads of 64 there is room for two dP (and ds) tiles, so the
+    // next dP does not wait for dQ
     static constexpr int kDp = HD == 64 ? 2 : 1;
     static constexpr uint32_t S = 0, DP = kTile, DQ = DP + kDp * kTile, Q = DQ + HD, DO = Q + HD / 2;
     static_assert(DO + HD / 2 <= 512, "TMEM");
@@ -127,22 +143,23 @@ struct QCols {
 
 template <int HD, bool BF>
 __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constant__ GradArgs P) {
-    using Cols = QCols<HD>;
-    constexpr int kChunks = HD / 64, kTileBytes = kChunks * CHUNK_BYTES;
-    constexpr uint64_t kTileU = kTileBytes >> 4;
+    using C = GradQ<HD>;
+    constexpr int KT = C::kKeys, NC = C::kCols;
+    constexpr uint64_t kTileU = C::kTileBytes >> 4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
     const Args& a = P.a;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int NS = P.stages;
-    uint8_t* sKV = smem;
-    GradBars& bar = *reinterpret_cast<GradBars*>(sKV + NS * kTileBytes);
+    const int NS = P.stages;                // even: K and V keep their slots
+    uint8_t* sKV = smem;                    // at the end the rows of dq
+    GradBars& bar = *reinterpret_cast<GradBars*>(sKV + NS * C::kTileBytes);
     float* sDelta = reinterpret_cast<float*>(&bar + 1);          // [128]
     float* sFar = sDelta + kTile;                                // [8][2]
     float* sBias = sFar + 2 * kElemWarps;                        // [2 (D + kSlack) + 1]
     float* sSums = sBias + (a.table ? 2 * (a.D + kSlack) + 1 : 0);   // [4][2 D + 1]
+    float* sScratch = sSums + kBands * (2 * a.D + 1);            // [8][scratch_rows][33], with bias sums
 
     int blk = blockIdx.x;
     const int qt = blk % P.q_tiles;
@@ -151,54 +168,65 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
     const int b = blk / a.H;
     const int i0 = qt * kTile;
     const int end = key_end(a, b);
-    const int nt = tile_count(P.kt, b, end);
+    const int nt = step_count<KT>(P.kt, b, end);
     const bool partial_keys = P.kt.words != nullptr || end < a.m;
     const int64_t first = (a.q_pos ? (int64_t)__ldg(a.q_pos + b) : 0) + i0;
     const int dsteps = (a.d + 15) >> 4;
     const int width = 2 * a.D + 1;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(&bar.full[s], 1);
-            mbar_init(&bar.empty[s], 1);
-            mbar_init(&bar.clean[s], 1);
+    if (warp == kLoad) {
+        if (lane < NS) mbar_init(&bar.full[lane], 1);
+        fence_mbar_init();
+        __syncwarp();
+    } else if (warp == kClean) {
+        if (lane < NS) {
+            mbar_init(&bar.empty[lane], 1);
+            mbar_init(&bar.clean[lane], 1);
+        } else if (lane == NS) {
+            mbar_init(&bar.ready, kElemWarps);
+            mbar_init(&bar.sfull, 1);
+            mbar_init(&bar.sfree, kElemWarps);
+            mbar_init(&bar.dpfull[0], 1);
+            mbar_init(&bar.dpfull[1], 1);
+            mbar_init(&bar.dsfull, kElemWarps);
+            mbar_init(&bar.done, 1);
+            mbar_init(&bar.drain, 1);
         }
-        mbar_init(&bar.ready, kElemWarps);
-        mbar_init(&bar.sfull, 1);
-        mbar_init(&bar.sfree, kElemWarps);
-        mbar_init(&bar.dpfull[0], 1);
-        mbar_init(&bar.dpfull[1], 1);
-        mbar_init(&bar.dsfull, kElemWarps);
-        mbar_init(&bar.done, 1);
-        mbar_init(&bar.drain, 1);
         fence_mbar_init();
     }
-    if (warp == 9) tmem_alloc(&bar.tmem, 512);
+    if (warp == kIssue) tmem_alloc(&bar.tmem, 512);
+    const auto load = [&](int it, int slot) {      // K and V tiles in turn
+        const int g = h / a.R;
+        const int key = step_key<KT>(P.kt, b, it >> 1);
+        const TensorMap& src = it & 1 ? P.v : P.k;
+        mbar_arrive_expect_tx(&bar.full[slot], C::kTileBytes);
+        for (int c = 0; c < C::kChunks; ++c)
+            tma_load(sKV + slot * C::kTileBytes + c * C::kChunkBytes, &src.map, c * 64, key, g * src.head,
+                     b * src.batch, &bar.full[slot]);
+    };
+    const int early = min(2 * nt, NS);             // copies that need no free slot
+    if (warp == kLoad && nt > 0 && elect_one())
+        for (int it = 0; it < early; ++it) load(it, it);
     if (a.table) fill_bias<BF>(a, h, sBias, threadIdx.x, kGradThreads);
     if (a.bias_part)
-        for (int e = threadIdx.x; e < 4 * width; e += kGradThreads) sSums[e] = 0.f;
+        for (int e = threadIdx.x; e < kBands * width; e += kGradThreads) sSums[e] = 0.f;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
 
-    if (warp == 8) {
+    if (warp == kLoad) {
         if (nt > 0 && elect_one()) {
-            const int g = h / a.R;
             Ring r;
-            int issued = 0;
+            r.step(early, NS);
+            int issued = early;
             bool ok = true;
-            for (int it = 0; it < 2 * nt; ++it) {
+            for (int it = early; it < 2 * nt; ++it) {
                 if (!mbar_wait(&bar.empty[r.slot], r.phase ^ 1u, a.err, ERR_TIMEOUT_PRODUCER)) {
                     ok = false;
                     break;
                 }
-                const int tile = tile_at(P.kt, b, it >> 1);
-                const TensorMap& src = it & 1 ? P.v : P.k;
-                mbar_arrive_expect_tx(&bar.full[r.slot], kTileBytes);
-                for (int c = 0; c < kChunks; ++c)
-                    tma_load(sKV + r.slot * kTileBytes + c * CHUNK_BYTES, &src.map, c * 64, tile * kTile,
-                             g * src.head, b * src.batch, &bar.full[r.slot]);
+                load(it, r.slot);
                 ++issued;
                 r.step(1, NS);
             }
@@ -211,70 +239,68 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
                 }
             }
         }
-    } else if (warp == 9) {
+    } else if (warp == kIssue) {
         if (nt > 0 && elect_one()) {
             const uint32_t idS = idesc_16(BF, kTile, false);
             const uint32_t idQ = idesc_16(BF, dsteps * 16, true);
             const uint64_t dKV = sdesc_sw128(smem_u32(sKV)), dKVt = sdesc_tokens(smem_u32(sKV));
-            Ring rk, rv, rq;     // K of the next scores, V of the next dP, K of the next dQ
-            rv.step(1, NS);
             uint64_t* kbar = partial_keys ? bar.clean : bar.full;
-            bool ok = mma_wait(a.err, &bar.ready, 0) && mma_wait(a.err, &kbar[rk.slot], rk.phase);
-            if (ok) {
-                mma_over_d_ts(tmem + Cols::S, tmem + Cols::Q, dKV + rk.slot * kTileU, idS, dsteps);
+            Ring rs, rq;         // K (and V beside it) of the next scores, K of the next dQ
+            uint32_t sph = 0;    // phase of the slot of the next dP
+            int sslot = 0;
+            const auto scores = [&]() {
+                mma_over_d_ts<CHUNK_BYTES>(tmem + C::S, tmem + C::Q, dKV + rs.slot * kTileU, idS, dsteps);
                 mma_commit(&bar.sfull);
-                rk.step(2, NS);
-                ok = mma_wait(a.err, &bar.full[rv.slot], rv.phase);
-            }
+                sslot = rs.slot + 1;
+                sph = rs.phase;
+                rs.step(2, NS);
+            };
+            const auto grads = [&](int buf) {
+                mma_over_d_ts<CHUNK_BYTES>(tmem + C::DP + buf * kTile, tmem + C::DO, dKV + sslot * kTileU, idS,
+                                           dsteps);
+                mma_commit(&bar.dpfull[buf]);
+                mma_commit(&bar.empty[sslot]);
+            };
+            bool ok = mma_wait(a.err, &bar.ready, 0) && mma_wait(a.err, &kbar[0], 0);
             if (ok) {
-                mma_over_d_ts(tmem + Cols::DP, tmem + Cols::DO, dKV + rv.slot * kTileU, idS, dsteps);
-                mma_commit(&bar.dpfull[0]);
-                mma_commit(&bar.empty[rv.slot]);
-                rv.step(2, NS);
+                scores();
+                ok = mma_wait(a.err, &bar.full[sslot], sph);
             }
+            if (ok) grads(0);
             for (int j = 0; j < nt && ok; ++j) {
                 const bool more = j + 1 < nt;
-                const uint32_t next = Cols::kDp == 2 ? (j + 1) & 1 : 0;
                 if (more) {
                     // scores of the next tile, once this one's are in registers
-                    if (!(ok = mma_wait(a.err, &kbar[rk.slot], rk.phase) && mma_wait(a.err, &bar.sfree, j & 1))) break;
-                    mma_over_d_ts(tmem + Cols::S, tmem + Cols::Q, dKV + rk.slot * kTileU, idS, dsteps);
-                    mma_commit(&bar.sfull);
-                    rk.step(2, NS);
-                }
-                if (more && Cols::kDp == 2) {
-                    if (!(ok = mma_wait(a.err, &bar.full[rv.slot], rv.phase))) break;
-                    mma_over_d_ts(tmem + Cols::DP + next * kTile, tmem + Cols::DO, dKV + rv.slot * kTileU,
-                                  idS, dsteps);
-                    mma_commit(&bar.dpfull[next]);
-                    mma_commit(&bar.empty[rv.slot]);
-                    rv.step(2, NS);
+                    // (copies that have long landed are waited for before the warps)
+                    if (!(ok = mma_wait(a.err, &kbar[rs.slot], rs.phase) &&
+                               (C::kDp == 1 || mma_wait(a.err, &bar.full[rs.slot + 1], rs.phase)) &&
+                               mma_wait(a.err, &bar.sfree, j & 1)))
+                        break;
+                    scores();
+                    if (C::kDp == 2)
+                        grads((j + 1) & 1);
+                    else if (!(ok = mma_wait(a.err, &bar.full[sslot], sph)))
+                        break;
                 }
                 if (!(ok = mma_wait(a.err, &bar.dsfull, j & 1))) break;
-                mma_over_tokens(tmem + Cols::DQ, tmem + Cols::DP + (Cols::kDp == 2 ? (j & 1) * kTile : 0),
+                mma_over_tokens(tmem + C::DQ, tmem + C::DP + (C::kDp == 2 ? (j & 1) * kTile : 0),
                                 dKVt + rq.slot * kTileU, idQ, j > 0, 64);
                 mma_commit(&bar.empty[rq.slot]);
                 rq.step(2, NS);
-                if (more && Cols::kDp == 1) {
-                    if (!(ok = mma_wait(a.err, &bar.full[rv.slot], rv.phase))) break;
-                    mma_over_d_ts(tmem + Cols::DP, tmem + Cols::DO, dKV + rv.slot * kTileU, idS, dsteps);
-                    mma_commit(&bar.dpfull[0]);
-                    mma_commit(&bar.empty[rv.slot]);
-                    rv.step(2, NS);
-                }
+                if (more && C::kDp == 1) grads(0);
             }
             mma_commit(&bar.done);
             mma_commit(&bar.drain);
             mbar_wait(&bar.drain, 0, a.err, ERR_TIMEOUT_MMA);
         }
-    } else if (warp == 10) {
+    } else if (warp == kClean) {
         if (partial_keys) {
             Ring r;
             for (int j = 0; j < nt; ++j) {
-                const KeyBits<kTile> w(P.kt, b, j, end);
+                const KeyBits<KT> w(P.kt, b, j, end);
                 if (!warp_wait(&bar.full[r.slot], r.phase, a.err, ERR_TIMEOUT_PRODUCER)) break;
                 if (!w.all()) {
-                    clear_rows(sKV + r.slot * kTileBytes, kChunks, CHUNK_BYTES, w, lane);
+                    clear_rows(sKV + r.slot * C::kTileBytes, C::kChunks, C::kChunkBytes, w, lane);
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
@@ -295,6 +321,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
             const int64_t off = b * w.sb + (int64_t)i * w.st + h * w.sh;
             const int64_t oo = b * a.o.sb + (int64_t)i * a.o.st + h * a.o.sh;
             float dot = 0.f;
+#pragma unroll 2
             for (int x = 0; x < dsteps; ++x) {
                 uint32_t u[8];
                 load16<BF>(w, off, 16 * x, a.d, live, half ? P.dout_vec : P.q_vec, u);
@@ -309,7 +336,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
                     }
                 }
                 __syncwarp();
-                tmem_st8u(tmem + lofs + (half ? Cols::DO : Cols::Q) + 8 * x, u);
+                tmem_st8u(tmem + lofs + (half ? C::DO : C::Q) + 8 * x, u);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -323,24 +350,26 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
         named_sync(1, 32 * kElemWarps);
         const float delta = sDelta[r];
         if (half == 0) {
-            float* pad = P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * 2 * kTile;
-            pad[r] = -lse2;
-            pad[kTile + r] = delta;
+            float* pad = P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * 2 * kTile + r;
+            pad[0] = -lse2;
+            pad[kTile] = -delta;
         }
         const float nlse = -lse2;
+        const uint32_t tS = tmem + lofs + C::S + half * NC;
+        float* scratch = sScratch + warp * P.scratch_rows * 33;
         float far_lo = 0.f, far_hi = 0.f;
         bool ok = true;
         for (int j = 0; j < nt; ++j) {
-            const int tile = tile_at(P.kt, b, j);
-            const uint4 w = tile_words(P.kt, b, tile, end);
+            const int buf = C::kDp == 2 ? j & 1 : 0;
+            const uint32_t tDP = tmem + lofs + C::DP + buf * kTile + half * NC;
             // relative position of the warp's first row and column
-            const int64_t rel0 = (int64_t)tile * kTile + half * 64 - first - quarter * 32;
-            const int buf = Cols::kDp == 2 ? j & 1 : 0;
+            const int64_t rel0 =
+                a.table ? step_key<KT>(P.kt, b, j) + half * NC - first - quarter * 32 : (int64_t)0;
             if (!(ok = warp_wait(&bar.sfull, j & 1, a.err, ERR_TIMEOUT_EPILOGUE))) break;
             tc_fence_after();
-            float v[64];
-            tmem_ld32(tmem + lofs + Cols::S + half * 64, v);
-            tmem_ld32(tmem + lofs + Cols::S + half * 64 + 32, v + 32);
+            float v[NC];
+#pragma unroll
+            for (int c = 0; c < NC; c += 32) tmem_ld32(tS + c, v + c);
             tmem_wait_ld();
             tmem_reg_fence(v);
             tc_fence_before();
@@ -352,48 +381,51 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
                 if (rel0 - 31 >= a.D) {
                     add = sBias[2 * a.D + kSlack];
                     where = 1;
-                } else if (rel0 + 63 <= -a.D) {
+                } else if (rel0 + (NC - 1) <= -a.D) {
                     add = sBias[kSlack];
                     where = -1;
                 } else {
                     const float* e = sBias + (int)rel0 - lane + a.D + kSlack;
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) v[c] = fmaf(v[c], mul, e[c]);
+                    for (int c = 0; c < NC; ++c) v[c] = fmaf(v[c], mul, e[c]);
                     mul = 1.f;
                 }
             }
             const float base = add + nlse;
             const uint64_t mul2 = pk(mul, mul), base2 = pk(base, base);
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
+            for (int c = 0; c < NC; c += 2) {
                 upk(fma2(pk(v[c], v[c + 1]), mul2, base2), v[c], v[c + 1]);
                 v[c] = ex2(v[c]);
                 v[c + 1] = ex2(v[c + 1]);
             }
-            if (!(ok = warp_wait(&bar.dpfull[buf], Cols::kDp == 2 ? (j >> 1) & 1 : j & 1, a.err,
+            if (!(ok = warp_wait(&bar.dpfull[buf], C::kDp == 2 ? (j >> 1) & 1 : j & 1, a.err,
                                  ERR_TIMEOUT_EPILOGUE)))
                 break;
             tc_fence_after();
-            const uint32_t tDP = tmem + lofs + Cols::DP + buf * kTile + half * 64;
+            {
+                float g[NC];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                float g[32];
-                tmem_ld32(tDP + 32 * q, g);
+                for (int c = 0; c < NC; c += 32) tmem_ld32(tDP + c, g + c);
                 tmem_wait_ld();
                 tmem_reg_fence(g);
+                const uint64_t nd = pk(-delta, -delta);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[32 * q + c] *= g[c] - delta;
+                for (int c = 0; c < NC; c += 2)
+                    upk(mul2f(pk(v[c], v[c + 1]), add2(pk(g[c], g[c + 1]), nd)), v[c], v[c + 1]);
             }
-            if (!all_count(w)) {
-                const uint32_t lo = half ? w.z : w.x, hi = half ? w.w : w.y;
+            if (P.kt.words || (j + 1) * KT > end) {
+                const KeyBits<KT> w(P.kt, b, j, end);
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    if (!(((c < 32 ? lo : hi) >> (c & 31)) & 1u)) v[c] = 0.f;
+                for (int c = 0; c < NC; ++c) {
+                    const uint32_t bits = half ? w.w[2 + (c >> 5)] : w.w[c >> 5];
+                    if (!((bits >> (c & 31)) & 1u)) v[c] = 0.f;
+                }
             }
             {
-                uint32_t u[32];
+                uint32_t u[NC / 2];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) u[c] = pack16<BF>(v[2 * c], v[2 * c + 1]);
+                for (int c = 0; c < NC / 2; ++c) u[c] = pack16<BF>(v[2 * c], v[2 * c + 1]);
                 tmem_st32(tDP, u);
                 tmem_wait_st();
                 tc_fence_before();
@@ -404,7 +436,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
                 if (where != 0) {
                     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                    for (int c = 0; c < 64; c += 2) {
+                    for (int c = 0; c < NC; c += 2) {
                         s0 += v[c];
                         s1 += v[c + 1];
                     }
@@ -413,12 +445,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
                     else
                         far_lo += s0 + s1;
                 } else {
-                    // sums along the diagonals: each lane's running sum moves one row down
-                    // per column; lane 31's is complete.  A diagonal of these 32 rows meets
-                    // two 64-column strips at most, so no entry gets more than two terms and
-                    // the order of the additions does not matter.
+                    // A diagonal of these 32 rows meets two 32 x 32 blocks at most, so no entry of
+                    // the sums gets more than two terms and the order of the additions does
+                    // not matter.
                     float* sums = sSums + quarter * width;
-                    auto put = [&](int64_t rel, float x) {
+                    const auto put = [&](int64_t rel, float x) {
                         if (rel >= a.D)
                             far_hi += x;
                         else if (rel <= -a.D)
@@ -426,26 +457,32 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
                         else
                             atomicAdd(sums + (int)rel + a.D, x);
                     };
-                    float run = 0.f;
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        run = __shfl_up_sync(0xffffffffu, run, 1);
-                        run = (lane == 0 ? 0.f : run) + v[c];
-                        if (lane == 31) put(rel0 + c - 31, run);
-                        __syncwarp();
+                    for (int q = 0; q < NC / 32; ++q) {
+                        float upper = 0.f, lower = 0.f;
+                        if (P.scratch_rows == 32)
+                            diagonals<32>(v + 32 * q, scratch, lane, upper, lower);
+                        else
+                            diagonals<8>(v + 32 * q, scratch, lane, upper, lower);
+                        put(rel0 + 32 * q + lane, upper);
+                        if (lane > 0) put(rel0 + 32 * q + lane - 32, lower);
                     }
-                    if (lane != 31) put(rel0 + 63 - lane, run);
-                    __syncwarp();
                 }
             }
         }
         if (nt > 0 && ok) ok = warp_wait(&bar.done, 0, a.err, ERR_TIMEOUT_EPILOGUE);
+        tc_fence_after();
         if (ok) {
-            tc_fence_after();
             const int mid = (dsteps * 16 + 31) / 32 * 16;
-            store_row<BF>(a.dq, b * a.dq.sb + (int64_t)i * a.dq.st + h * a.dq.sh, tmem + lofs + Cols::DQ,
-                          half ? mid : 0, half ? dsteps * 16 : mid, a.d, a.scale, nt > 0, live, true,
-                          P.dq_vec);
+            stage_row<BF>(sKV, r, tmem + lofs + C::DQ, half ? mid : 0, half ? dsteps * 16 : mid, a.scale,
+                          nt > 0, true);
+        }
+        named_sync(2 + quarter, 64);
+        if (ok) {
+            const int w0 = i - lane + half * 16;
+            unstage_rows<16>(sKV, quarter * 32 + half * 16, a.n - w0, a.d,
+                             static_cast<uint16_t*>(a.dq.p) + b * a.dq.sb + (int64_t)w0 * a.dq.st + h * a.dq.sh,
+                             a.dq.st, P.dq_vec, lane);
         }
         if (a.bias_part) {
 #pragma unroll
@@ -466,7 +503,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
                     for (int k = 0; k < kElemWarps; ++k) s += sFar[2 * k + (e ? 1 : 0)];
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) s += sSums[k * width + e];
+                    for (int k = 0; k < kBands; ++k) s += sSums[k * width + e];
                 }
                 out[e] = s;
             }
@@ -475,7 +512,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kIssue) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -483,11 +520,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
 
 // ---------------------------------------------------------------------------
 
+template <int HD>
+struct GradKV {
+    static constexpr int kQueries = kTile, kCols = kTile / 2;    // queries of a tile, of a warp
+    static constexpr int kChunks = HD / 64, kChunkBytes = CHUNK_BYTES;
+    static constexpr int kTileBytes = kChunks * CHUNK_BYTES;
+    static constexpr int kOwnBytes = kTileBytes;                 // the block's K or V
+    static constexpr uint32_t S = 0, DP = kTile, DV = 2 * kTile, DK = 3 * kTile;     // TMEM columns
+};
+
 template <int HD, bool BF>
 __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_constant__ GradArgs P) {
-    constexpr uint32_t cS = 0, cDP = kTile, cDV = 2 * kTile, cDK = 3 * kTile;
-    constexpr int kChunks = HD / 64, kTileBytes = kChunks * CHUNK_BYTES;
-    constexpr uint64_t kTileU = kTileBytes >> 4;
+    using C = GradKV<HD>;
+    constexpr int QT = C::kQueries, NC = C::kCols;
+    constexpr uint64_t kTileU = C::kTileBytes >> 4;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -495,11 +541,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int NS = P.kv_stages;           // even: Q and dO tiles in turn
-    uint8_t* sK = smem;
-    uint8_t* sV = sK + kTileBytes;
-    uint8_t* sR = sV + kTileBytes;
-    float* sRow = reinterpret_cast<float*>(sR + NS * kTileBytes);   // [NS / 2][-lse2 128, delta 128]
-    GradBars& bar = *reinterpret_cast<GradBars*>(sRow + (NS / 2) * 2 * kTile);
+    uint8_t* sK = smem;                   // at the end the rows of dk and dv
+    uint8_t* sV = sK + C::kOwnBytes;
+    uint8_t* sR = sV + C::kOwnBytes;
+    float* sRow = reinterpret_cast<float*>(sR + NS * C::kTileBytes);   // [NS / 2][-lse2, -delta][QT]
+    GradBars& bar = *reinterpret_cast<GradBars*>(sRow + NS * QT);
     float* sBias = reinterpret_cast<float*>(&bar + 1);
 
     int blk = blockIdx.x;
@@ -514,61 +560,70 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
     const bool any = (w.x | w.y | w.z | w.w) != 0;
     const int64_t pos = a.q_pos ? (int64_t)__ldg(a.q_pos + b) : 0;
     const int dsteps = (a.d + 15) >> 4;
-    const int nt = any ? a.R * P.q_tiles : 0;       // query tiles of every head
+    const int per_head = (a.n + QT - 1) / QT;        // query tiles of a head
+    const int nt = any ? a.R * per_head : 0;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(&bar.full[s], 1);
-            mbar_init(&bar.empty[s], 1);
+    if (warp == kLoad) {
+        if (lane < NS) mbar_init(&bar.full[lane], 1);
+        if (lane == NS) mbar_init(&bar.ready, 1);
+        fence_mbar_init();
+        __syncwarp();
+    } else if (warp == kClean) {
+        if (lane < NS) {
+            mbar_init(&bar.empty[lane], 1);
+        } else if (lane == NS) {
+            mbar_init(&bar.sfull, 1);
+            mbar_init(&bar.dpfull[0], 1);
+            mbar_init(&bar.pfull, kElemWarps);
+            mbar_init(&bar.dsfull, kElemWarps);
+            mbar_init(&bar.done, 1);
+            mbar_init(&bar.drain, 1);
         }
-        mbar_init(&bar.ready, 1);
-        mbar_init(&bar.sfull, 1);
-        mbar_init(&bar.dpfull[0], 1);
-        mbar_init(&bar.pfull, kElemWarps);
-        mbar_init(&bar.dsfull, kElemWarps);
-        mbar_init(&bar.done, 1);
-        mbar_init(&bar.drain, 1);
         fence_mbar_init();
     }
-    if (warp == 9) tmem_alloc(&bar.tmem, 512);
+    if (warp == kIssue) tmem_alloc(&bar.tmem, 512);
+    // Q tiles (with the row values of their queries) and dO tiles in turn
+    const auto load = [&](int it, int slot) {
+        const int t = it >> 1, h = g * a.R + t / per_head, qt = t % per_head;
+        const bool second = it & 1;
+        const TensorMap& src = second ? P.dout : P.q;
+        mbar_arrive_expect_tx(&bar.full[slot], C::kTileBytes + (second ? 0 : 8 * QT));
+        for (int c = 0; c < C::kChunks; ++c)
+            tma_load(sR + slot * C::kTileBytes + c * C::kChunkBytes, &src.map, c * 64, qt * QT, h * src.head,
+                     b * src.batch, &bar.full[slot]);
+        if (!second)
+            bulk_g2s(sRow + (slot >> 1) * 2 * QT,
+                     P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * 2 * QT, 8 * QT,
+                     &bar.full[slot]);
+    };
+    const int early = min(2 * nt, NS);
+    if (warp == kLoad && nt > 0 && elect_one()) {
+        mbar_arrive_expect_tx(&bar.ready, 2 * C::kOwnBytes);
+        for (int c = 0; c < C::kChunks; ++c) {
+            tma_load(sK + c * CHUNK_BYTES, &P.k.map, c * 64, j0, g * P.k.head, b * P.k.batch, &bar.ready);
+            tma_load(sV + c * CHUNK_BYTES, &P.v.map, c * 64, j0, g * P.v.head, b * P.v.batch, &bar.ready);
+        }
+        for (int it = 0; it < early; ++it) load(it, it);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
 
-    if (warp == 8) {
+    if (warp == kLoad) {
         if (nt > 0 && elect_one()) {
-            mbar_arrive_expect_tx(&bar.ready, 2 * kTileBytes);
-            for (int c = 0; c < kChunks; ++c) {
-                tma_load(sK + c * CHUNK_BYTES, &P.k.map, c * 64, j0, g * P.k.head, b * P.k.batch, &bar.ready);
-                tma_load(sV + c * CHUNK_BYTES, &P.v.map, c * 64, j0, g * P.v.head, b * P.v.batch, &bar.ready);
-            }
             Ring r;
-            int issued = 0;
+            r.step(early, NS);
+            int issued = early;
             bool ok = true;
-            int h = g * a.R, qt = 0;
-            for (int it = 0; it < 2 * nt; ++it) {
+            for (int it = early; it < 2 * nt; ++it) {
                 if (!mbar_wait(&bar.empty[r.slot], r.phase ^ 1u, a.err, ERR_TIMEOUT_PRODUCER)) {
                     ok = false;
                     break;
                 }
-                const bool second = it & 1;
-                const TensorMap& src = second ? P.dout : P.q;
-                // the row values come with Q: -lse2 and delta of the tile's queries
-                mbar_arrive_expect_tx(&bar.full[r.slot], kTileBytes + (second ? 0 : 8 * kTile));
-                for (int c = 0; c < kChunks; ++c)
-                    tma_load(sR + r.slot * kTileBytes + c * CHUNK_BYTES, &src.map, c * 64, qt * kTile,
-                             h * src.head, b * src.batch, &bar.full[r.slot]);
-                if (!second)
-                    bulk_g2s(sRow + (r.slot >> 1) * 2 * kTile,
-                             P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * 2 * kTile, 8 * kTile,
-                             &bar.full[r.slot]);
+                load(it, r.slot);
                 ++issued;
                 r.step(1, NS);
-                if (second && ++qt == P.q_tiles) {
-                    qt = 0;
-                    ++h;
-                }
             }
             if (!ok) {
                 mbar_wait(&bar.ready, 0, a.err, ERR_TIMEOUT_PRODUCER);
@@ -580,42 +635,41 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
                 }
             }
         }
-    } else if (warp == 9) {
+    } else if (warp == kIssue) {
         if (nt > 0 && elect_one()) {
             const uint32_t idS = idesc_16(BF, kTile, false);
             const uint32_t idD = idesc_16(BF, dsteps * 16, true);
             const uint64_t dK = sdesc_sw128(smem_u32(sK)), dV = sdesc_sw128(smem_u32(sV));
             const uint64_t dR = sdesc_sw128(smem_u32(sR)), dRt = sdesc_tokens(smem_u32(sR));
-            Ring rs;               // the tile whose scores come next: Q at slot, dO at slot + 1
-            Ring rd;               // the tile whose dV and dK come next
+            Ring rs, rd;      // tiles whose scores, and whose dV and dK, come next: Q at slot, dO at slot + 1
             bool ok = mma_wait(a.err, &bar.ready, 0) && mma_wait(a.err, &bar.full[0], 0);
             if (ok) {
-                mma_over_d(tmem + cS, dK, dR, idS, dsteps);
+                mma_over_d(tmem + C::S, dK, dR, idS, dsteps);
                 mma_commit(&bar.sfull);
                 ok = mma_wait(a.err, &bar.full[1], 0);
             }
             if (ok) {
-                mma_over_d(tmem + cDP, dV, dR + kTileU, idS, dsteps);
+                mma_over_d(tmem + C::DP, dV, dR + kTileU, idS, dsteps);
                 mma_commit(&bar.dpfull[0]);
                 rs.step(2, NS);
             }
             for (int t = 0; t < nt && ok; ++t) {
                 const bool more = t + 1 < nt;
                 if (!(ok = mma_wait(a.err, &bar.pfull, t & 1))) break;
-                mma_over_tokens(tmem + cDV, tmem + cS, dRt + (rd.slot + 1) * kTileU, idD, t > 0, 64);
+                mma_over_tokens(tmem + C::DV, tmem + C::S, dRt + (rd.slot + 1) * kTileU, idD, t > 0, 64);
                 mma_commit(&bar.empty[rd.slot + 1]);
                 if (more) {
                     if (!(ok = mma_wait(a.err, &bar.full[rs.slot], rs.phase))) break;
-                    mma_over_d(tmem + cS, dK, dR + rs.slot * kTileU, idS, dsteps);
+                    mma_over_d(tmem + C::S, dK, dR + rs.slot * kTileU, idS, dsteps);
                     mma_commit(&bar.sfull);
                 }
                 if (!(ok = mma_wait(a.err, &bar.dsfull, t & 1))) break;
-                mma_over_tokens(tmem + cDK, tmem + cDP, dRt + rd.slot * kTileU, idD, t > 0, 64);
+                mma_over_tokens(tmem + C::DK, tmem + C::DP, dRt + rd.slot * kTileU, idD, t > 0, 64);
                 mma_commit(&bar.empty[rd.slot]);
                 rd.step(2, NS);
                 if (more) {
                     if (!(ok = mma_wait(a.err, &bar.full[rs.slot + 1], rs.phase))) break;
-                    mma_over_d(tmem + cDP, dV, dR + (rs.slot + 1) * kTileU, idS, dsteps);
+                    mma_over_d(tmem + C::DP, dV, dR + (rs.slot + 1) * kTileU, idS, dsteps);
                     mma_commit(&bar.dpfull[0]);
                     rs.step(2, NS);
                 }
@@ -629,7 +683,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
         const int r = quarter * 32 + lane;
         const int j = j0 + r;
         const uint32_t lofs = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tS = tmem + lofs + cS + half * 64, tDP = tmem + lofs + cDP + half * 64;
+        const uint32_t tS = tmem + lofs + C::S + half * NC, tDP = tmem + lofs + C::DP + half * NC;
         Ring ring;
         bool ok = true;
         int h = g * a.R, qt = 0;
@@ -639,105 +693,111 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
                 fill_bias<BF>(a, h, sBias, threadIdx.x, 32 * kElemWarps);
                 named_sync(1, 32 * kElemWarps);
             }
-            // relative position of the tile's first key and the strip's first query
-            const int64_t rel0 = (int64_t)j0 - pos - (int64_t)qt * kTile - half * 64;
-            const float* rows = sRow + (ring.slot >> 1) * 2 * kTile + half * 64;
+            const float* rows = sRow + (ring.slot >> 1) * 2 * QT + half * NC;
             // (a warp that gave up still meets the others at the barriers above)
-            ok = ok && warp_wait(&bar.full[ring.slot], ring.phase, a.err, ERR_TIMEOUT_EPILOGUE) &&
-                 warp_wait(&bar.sfull, t & 1, a.err, ERR_TIMEOUT_EPILOGUE);
+            ok = ok && warp_wait(&bar.full[ring.slot], ring.phase, a.err, ERR_TIMEOUT_EPILOGUE);
+            // the row values go to registers ahead of the tiles they are used with
+            float v[NC];
+            float4 l[NC / 4];
+#pragma unroll
+            for (int c = 0; c < NC / 4; ++c) l[c] = *reinterpret_cast<const float4*>(rows + 4 * c);
+            ok = ok && warp_wait(&bar.sfull, t & 1, a.err, ERR_TIMEOUT_EPILOGUE);
             if (ok) {
                 tc_fence_after();
-                float v[64];
-                tmem_ld32(tS, v);
-                tmem_ld32(tS + 32, v + 32);
+#pragma unroll
+                for (int c = 0; c < NC; c += 32) tmem_ld32(tS + c, v + c);
                 tmem_wait_ld();
                 tmem_reg_fence(v);
-                float mul = a.scale2, add = 0.f;
+                float mul = a.scale2;
                 if (a.table) {
-                    if (rel0 - 63 >= a.D) {
-                        add = sBias[2 * a.D + kSlack];
-                    } else if (rel0 + (kTile - 1) <= -a.D) {
-                        add = sBias[kSlack];
-                    } else {
-                        const float* e = sBias + (int)rel0 + r + a.D + kSlack;
+                    // relative position of the tile's first key and the strip's first query
+                    const int64_t rel0 = (int64_t)j0 - pos - (int64_t)qt * QT - half * NC;
+                    const bool above = rel0 - (NC - 1) >= a.D, below = rel0 + (kTile - 1) <= -a.D;
+                    const float* e = sBias + (above || below ? 0 : (int)rel0 + r + a.D + kSlack);
+                    const float add = sBias[above ? 2 * a.D + kSlack : kSlack];
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) v[c] = fmaf(v[c], mul, e[-c]);
-                        mul = 1.f;
-                    }
+                    for (int c = 0; c < NC; ++c) v[c] = fmaf(v[c], mul, above || below ? add : e[-c]);
+                    mul = 1.f;
                 }
-                const uint64_t mul2 = pk(mul, mul), add2_ = pk(add, add);
+                const uint64_t mul2 = pk(mul, mul);
 #pragma unroll
-                for (int c = 0; c < 64; c += 4) {
-                    const float4 l = *reinterpret_cast<const float4*>(rows + c);
-                    upk(fma2(pk(v[c], v[c + 1]), mul2, add2(pk(l.x, l.y), add2_)), v[c], v[c + 1]);
-                    upk(fma2(pk(v[c + 2], v[c + 3]), mul2, add2(pk(l.z, l.w), add2_)), v[c + 2], v[c + 3]);
+                for (int c = 0; c < NC; c += 4) {
+                    upk(fma2(pk(v[c], v[c + 1]), mul2, pk(l[c / 4].x, l[c / 4].y)), v[c], v[c + 1]);
+                    upk(fma2(pk(v[c + 2], v[c + 3]), mul2, pk(l[c / 4].z, l[c / 4].w)), v[c + 2], v[c + 3]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[c + e] = ex2(v[c + e]);
                 }
                 {
-                    uint32_t u[32];
+                    uint32_t u[NC / 2];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) u[c] = pack16<BF>(v[2 * c], v[2 * c + 1]);
+                    for (int c = 0; c < NC / 2; ++c) u[c] = pack16<BF>(v[2 * c], v[2 * c + 1]);
                     tmem_st32(tS, u);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.pfull);
                 }
-                ok = warp_wait(&bar.dpfull[0], t & 1, a.err, ERR_TIMEOUT_EPILOGUE);
-                if (ok) {
-                    tc_fence_after();
+            }
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float d[32];
-                        tmem_ld32(tDP + 32 * q, d);
-                        tmem_wait_ld();
-                        tmem_reg_fence(d);
+            for (int c = 0; c < NC / 4; ++c) l[c] = *reinterpret_cast<const float4*>(rows + QT + 4 * c);
+            ok = ok && warp_wait(&bar.dpfull[0], t & 1, a.err, ERR_TIMEOUT_EPILOGUE);
+            if (ok) {
+                tc_fence_after();
+                uint32_t u[NC / 2];
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            const float4 l = *reinterpret_cast<const float4*>(rows + kTile + 32 * q + c);
-                            v[32 * q + c] *= d[c] - l.x;
-                            v[32 * q + c + 1] *= d[c + 1] - l.y;
-                            v[32 * q + c + 2] *= d[c + 2] - l.z;
-                            v[32 * q + c + 3] *= d[c + 3] - l.w;
-                        }
-                    }
-                    {
-                        uint32_t u[32];
+                for (int q = 0; q < NC; q += 32) {
+                    float d[32];
+                    tmem_ld32(tDP + q, d);
+                    tmem_wait_ld();
+                    tmem_reg_fence(d);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) u[c] = pack16<BF>(v[2 * c], v[2 * c + 1]);
-                        tmem_st32(tDP, u);
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.dsfull);
+                    for (int c = 0; c < 32; c += 4) {
+                        const float4 x = l[(q + c) / 4];
+                        float f0, f1, f2, f3;
+                        upk(mul2f(pk(v[q + c], v[q + c + 1]), add2(pk(d[c], d[c + 1]), pk(x.x, x.y))), f0, f1);
+                        upk(mul2f(pk(v[q + c + 2], v[q + c + 3]), add2(pk(d[c + 2], d[c + 3]), pk(x.z, x.w))),
+                            f2, f3);
+                        u[(q + c) / 2] = pack16<BF>(f0, f1);
+                        u[(q + c) / 2 + 1] = pack16<BF>(f2, f3);
                     }
                 }
+                tmem_st32(tDP, u);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.dsfull);
             }
             ring.step(2, NS);
-            if (++qt == P.q_tiles) {
+            if (++qt == per_head) {
                 qt = 0;
                 ++h;
             }
         }
         if (nt > 0 && ok) ok = warp_wait(&bar.done, 0, a.err, ERR_TIMEOUT_EPILOGUE);
+        tc_fence_after();
+        const uint32_t word = quarter == 0 ? w.x : quarter == 1 ? w.y : quarter == 2 ? w.z : w.w;
+        const bool keep = (word >> lane) & 1u;
         if (ok) {
-            tc_fence_after();
-            const uint32_t word = quarter == 0 ? w.x : quarter == 1 ? w.y : quarter == 2 ? w.z : w.w;
-            const bool keep = (word >> lane) & 1u;
-            const bool live = j < a.m;
             const int mid = (dsteps * 16 + 31) / 32 * 16;
             const int c0 = half ? mid : 0, c1 = half ? dsteps * 16 : mid;
-            store_row<BF>(a.dv, b * a.dv.sb + (int64_t)j * a.dv.st + g * a.dv.sh, tmem + lofs + cDV, c0, c1,
-                          a.d, 1.f, nt > 0, live, keep, P.dv_vec);
-            store_row<BF>(a.dk, b * a.dk.sb + (int64_t)j * a.dk.st + g * a.dk.sh, tmem + lofs + cDK, c0, c1,
-                          a.d, a.scale, nt > 0, live, keep, P.dk_vec);
+            stage_row<BF>(sV, r, tmem + lofs + C::DV, c0, c1, 1.f, nt > 0, keep);
+            stage_row<BF>(sK, r, tmem + lofs + C::DK, c0, c1, a.scale, nt > 0, keep);
+        }
+        named_sync(2 + quarter, 64);
+        if (ok) {
+            const int w0 = j - lane + half * 16, r0 = quarter * 32 + half * 16;
+            unstage_rows<16>(sV, r0, a.m - w0, a.d,
+                             static_cast<uint16_t*>(a.dv.p) + b * a.dv.sb + (int64_t)w0 * a.dv.st + g * a.dv.sh,
+                             a.dv.st, P.dv_vec, lane);
+            unstage_rows<16>(sK, r0, a.m - w0, a.d,
+                             static_cast<uint16_t*>(a.dk.p) + b * a.dk.sb + (int64_t)w0 * a.dk.st + g * a.dk.sh,
+                             a.dk.st, P.dk_vec, lane);
         }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kIssue) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -747,27 +807,45 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
 // dbias of one row of the table: the blocks' sums by relative position, in
 // their order, then the positions of each bucket in theirs.
 
-constexpr int kBiasThreads = 512;
+constexpr int kBiasThreads = 1024;
+constexpr int kBiasSplit = 8;      // most shares of the blocks' sums
 
 template <bool BF>
-__global__ void __launch_bounds__(kBiasThreads) k_grad_bias(const __grid_constant__ GradArgs P,
+__global__ void __launch_bounds__(kBiasThreads) k_grad_bias(const __grid_constant__ GradArgs P, int shares,
                                                             Elem<BF>* __restrict__ dbias) {
-    extern __shared__ float sSum[];
+    extern __shared__ float sSum[];                 // [shares][width], then the buckets
     const Args& a = P.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int width = 2 * a.D + 1;
+    int* sBucket = reinterpret_cast<int*>(sSum + shares * width);
     const int64_t parts = (int64_t)a.B * P.q_tiles * (a.table_stride ? 1 : a.H);
     const float* src = a.bias_part + blockIdx.x * parts * width;
-    for (int e = threadIdx.x; e < width; e += kBiasThreads) {
+    const int64_t per = (parts + shares - 1) / shares;
+    const int strips = (width + 31) / 32;
+    for (int x = warp; x < strips * shares; x += kBiasThreads / 32) {
+        const int share = x / strips, e = (x % strips) * 32 + lane;
+        if (e >= width) continue;
+        const int64_t p0 = share * per, p1 = min(parts, p0 + per);
         float s = 0.f;
-        for (int64_t p = 0; p < parts; ++p) s += src[p * width + e];
+#pragma unroll 8
+        for (int64_t p = p0; p < p1; ++p) s += src[p * width + e];
+        sSum[share * width + e] = s;
+    }
+    for (int e = threadIdx.x; e < width; e += kBiasThreads) sBucket[e] = bucket_of(a, e - a.D);
+    __syncthreads();
+    for (int e = threadIdx.x; e < width; e += kBiasThreads) {
+        float s = sSum[e];
+        for (int k = 1; k < shares; ++k) s += sSum[k * width + e];
         sSum[e] = s;
     }
     __syncthreads();
-    for (int u = threadIdx.x; u < a.nb; u += kBiasThreads) {
+    for (int u = warp; u < a.nb; u += kBiasThreads / 32) {
         float s = 0.f;
-        for (int e = 0; e < width; ++e)
-            if (bucket_of(a, e - a.D) == u) s += sSum[e];
-        dbias[(int64_t)blockIdx.x * a.nb + u] = from_f<Elem<BF>>(s);
+        for (int e = lane; e < width; e += 32)
+            if (sBucket[e] == u) s += sSum[e];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) dbias[(int64_t)blockIdx.x * a.nb + u] = from_f<Elem<BF>>(s);
     }
 }
 
@@ -778,35 +856,47 @@ int ring_stages(size_t fixed, size_t per_stage) {
     return s < kMaxRing ? s : kMaxRing;
 }
 
+// the least shared memory of the largest call leaves four tiles
+static_assert(1024 + sizeof(GradBars) + 4 * (kTile + 2 * kElemWarps) + 4 * (2 * (kMaxDistance + kSlack) + 1) +
+                      4 * kBands * (2 * kMaxDistance + 1) + 4 * kElemWarps * 8 * 33 + 4 * 2 * CHUNK_BYTES <=
+                  kSmemLimit,
+              "k_grad_q does not fit in shared memory");
+
 template <int HD, bool BF>
 cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
     const Args& a = p.a;
-    constexpr size_t tile = (HD / 64) * CHUNK_BYTES;
+    using Q = GradQ<HD>;
+    using KV = GradKV<HD>;
     const size_t bias = a.table ? sizeof(float) * (2 * (size_t)(a.D + kSlack) + 1) : 0;
     const size_t width = 2 * (size_t)a.D + 1;
     static std::atomic<uint64_t> ready_q{0}, ready_kv{0};
     cudaError_t e;
-    if (a.n > 0) {
-        const size_t fixed = 1024 + sizeof(GradBars) + sizeof(float) * (kTile + 2 * kElemWarps) + bias +
-                             (a.bias_part ? sizeof(float) * kBands * width : 0);
-        p.stages = 2 * (ring_stages(fixed, tile) / 2);     // even: K keeps its slots, and their clean bars
-        if ((e = raise_smem(k_grad_q<HD, BF>, kSmemLimit, ready_q)) != cudaSuccess) return e;
-        k_grad_q<HD, BF><<<(unsigned)((int64_t)p.q_tiles * a.H * a.B), kGradThreads,
-                           fixed + p.stages * tile, s>>>(p);
-        count_launch();
-    }
-    if (a.m > 0) {
-        // K and V, then stages of which each pair has a row of (-lse2, delta)
-        const size_t fixed = 1024 + sizeof(GradBars) + bias + 2 * tile;
-        p.kv_stages = 2 * (ring_stages(fixed, tile + 4 * kTile) / 2);
-        if ((e = raise_smem(k_grad_kv<HD, BF>, kSmemLimit, ready_kv)) != cudaSuccess) return e;
-        k_grad_kv<HD, BF><<<(unsigned)((int64_t)p.k_tiles * a.G * a.B), kGradThreads,
-                            fixed + p.kv_stages * (tile + 4 * kTile), s>>>(p);
-        count_launch();
-    }
+    size_t fixed = 1024 + sizeof(GradBars) + sizeof(float) * (kTile + 2 * kElemWarps) + bias +
+                   (a.bias_part ? sizeof(float) * kBands * width : 0);
+    // shared memory for the diagonals of ds, 32 rows at a time; 8 where that would leave
+    // fewer than the four tiles in flight that the order of the products needs (wide
+    // heads and distances from about 1500)
+    const auto scratch = [&](int rows) { return a.bias_part ? sizeof(float) * kElemWarps * rows * 33 : 0; };
+    p.scratch_rows = ring_stages(fixed + scratch(32), Q::kTileBytes) >= 4 ? 32 : 8;
+    fixed += scratch(p.scratch_rows);
+    p.stages = 2 * (ring_stages(fixed, Q::kTileBytes) / 2);
+    if ((e = raise_smem(k_grad_q<HD, BF>, kSmemLimit, ready_q)) != cudaSuccess) return e;
+    k_grad_q<HD, BF><<<(unsigned)((int64_t)p.q_tiles * a.H * a.B), kGradThreads,
+                       fixed + p.stages * Q::kTileBytes, s>>>(p);
+    count_launch();
+    // K and V, then stages of which each pair has a row of (-lse2, -delta)
+    constexpr size_t stage = KV::kTileBytes + 4 * KV::kQueries;
+    fixed = 1024 + sizeof(GradBars) + bias + 2 * KV::kOwnBytes;
+    p.kv_stages = 2 * (ring_stages(fixed, stage) / 2);
+    if ((e = raise_smem(k_grad_kv<HD, BF>, kSmemLimit, ready_kv)) != cudaSuccess) return e;
+    k_grad_kv<HD, BF><<<(unsigned)((int64_t)p.k_tiles * a.G * a.B), kGradThreads,
+                        fixed + p.kv_stages * stage, s>>>(p);
+    count_launch();
     if (dbias) {
-        k_grad_bias<BF><<<a.table_stride ? a.H : 1, kBiasThreads, sizeof(float) * width, s>>>(
-            p, static_cast<Elem<BF>*>(dbias));
+        // shares of the sums and the buckets in 48 KB
+        const int shares = std::max(1, std::min<int>(kBiasSplit, (int)(12288 / width) - 1));
+        k_grad_bias<BF><<<a.table_stride ? a.H : 1, kBiasThreads, 4 * (shares + 1) * width, s>>>(
+            p, shares, static_cast<Elem<BF>*>(dbias));
         count_launch();
     }
     return cudaGetLastError();

@@ -10,6 +10,9 @@
 namespace fs {
 namespace attn {
 
+// keys of a tile of the forward kernel
+constexpr int forward_keys(int d) { return d <= 64 ? 128 : 64; }
+
 // A tensor as 64 x 128 boxes of (d, token, head, batch); a repeated (stride 0)
 // head or batch is one entry of the map, its index multiplied by 0.
 struct TensorMap {
@@ -37,9 +40,9 @@ struct GradArgs {
     TensorMap q, k, v, dout;
     Args a;
     KeyTiles kt;
-    float* rows;       // [B][H][q_tiles][-lse2 of 128 queries, delta of 128 queries]
+    float* rows;       // [B][H][q_tiles][-lse2 of 128 queries, -delta of 128 queries]
     int q_tiles, k_tiles;
-    int stages, kv_stages;     // set at launch
+    int stages, kv_stages, scratch_rows;     // set at launch
     int q_vec, dout_vec, o_vec, dq_vec, dk_vec, dv_vec;   // rows take 16-byte accesses
 };
 
@@ -85,8 +88,5 @@ cudaError_t raise_smem(K kernel, size_t bytes, std::atomic<uint64_t>& ready) {
 // boxes of `rows` tokens
 fs_status make_tensor_map(TensorMap& t, const View& w, int B, int tokens, int heads, int d, bool bf16,
                           int rows = kTile);
-// keys of a tile of the forward kernel
-constexpr int forward_keys(int d) { return d <= 64 ? 128 : 64; }
-
 }  // namespace attn
 }  // namespace fs

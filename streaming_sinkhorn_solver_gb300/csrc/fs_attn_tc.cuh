@@ -22,6 +22,12 @@ using namespace fs::tc;
 
 constexpr int kTile = 128;   // tokens of a tile
 
+__device__ __forceinline__ uint64_t mul2f(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int c0, int token, int head,
                                          int batch, uint64_t* bar) {
     asm volatile(
@@ -117,12 +123,13 @@ __device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint64_t a, uint64_t
                 b + (uint64_t)((x >> 2) * (B_CHUNK >> 4) + 2 * (x & 3)), idesc, x != 0);
 }
 // the same with A in TMEM
+template <int B_CHUNK>
 __device__ __forceinline__ void mma_over_d_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                               int steps) {
 #pragma unroll 1
     for (int x = 0; x < steps; ++x)
-        mma_f16_ts(d_tmem, a_tmem + 8 * x, b + (uint64_t)((x >> 2) * (CHUNK_BYTES >> 4) + 2 * (x & 3)),
-                   idesc, x != 0);
+        mma_f16_ts(d_tmem, a_tmem + 8 * x, b + (uint64_t)((x >> 2) * (B_CHUNK >> 4) + 2 * (x & 3)), idesc,
+                   x != 0);
 }
 // D[tmem] (+)= A[tmem] * B over the KEYS tokens of B's tile; tokens 64 and on of A are
 // `half` columns from its first.  One elected thread.

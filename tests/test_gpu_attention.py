@@ -117,6 +117,11 @@ def test_bias_with_masks_and_wide_heads():
     check(*make(3, 200, 333, 6, 3, 128, HF, lens=[333, 130, 0], drop=0.3, nb=48, far=300, seed=3))
 
 
+def test_widest_bias_with_wide_heads():
+    """The largest max_distance, where the gradient's shared memory is tightest."""
+    check(*make(1, 300, 900, 2, 1, 128, BF, nb=64, far=2048, pos=[400], seed=23))
+
+
 def test_positions_far_outside_the_keys():
     check(*make(2, 70, 260, 2, 2, 64, BF, nb=32, far=128, pos=[100000, -2000], seed=4))
 

@@ -328,20 +328,19 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     p.q_tiles = (a.n + kTile - 1) / kTile;
     p.k_tiles = tiles.kt.tiles;
     const size_t blocks = (size_t)a.B * a.H * p.q_tiles;
-    const size_t rows = c.L.take(sizeof(float) * blocks * 2 * kTile);
+    const size_t rows = c.L.take(blocks * kRowBytes);
     const size_t part = c.L.take(dbias ? sizeof(float) * blocks * (2 * (size_t)a.D + 1) : 0);
     FS_TRY(begin_call(c, stream));
     FS_TRY(ensure_capacity(c));
     for (Input& x : inputs) FS_TRY(x.run(c, a));
     FS_TRY(tiles.run(c, a));
     p.kt = tiles.kt;
-    p.rows = c.at<float>(rows);
+    p.rows = c.at<uint8_t>(rows);
     a.bias_part = dbias ? c.at<float>(part) : nullptr;
     a.err = c.ws->err_word;
     auto vec = [&](const View& w, int tokens, int heads) {
         return a.d % 8 == 0 && aligned16(w, a.B, tokens, heads);
     };
-    p.q_vec = vec(a.q, a.n, a.H);
     p.dout_vec = vec(a.dout, a.n, a.H);
     p.o_vec = vec(a.o, a.n, a.H);
     p.dq_vec = vec(a.dq, a.n, a.H);

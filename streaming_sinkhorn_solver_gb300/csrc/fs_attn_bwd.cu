@@ -35,9 +35,11 @@ constexpr int kSlack = 2 * kTile;
 constexpr int kMaxRing = 8;
 constexpr int kBands = 4;           // rows of bias sums: one per 32 queries
 
+constexpr int kOnesBytes = 384 * kTile / 8;
+
 struct GradBars {
     uint64_t full[kMaxRing], empty[kMaxRing], clean[kMaxRing];
-    uint64_t ready, sfull, sfree, dpfull[2], pfull, dsfull, done, drain;
+    uint64_t own, ready, sfull, sfree, dpfull[2], pfull, dsfull, done, drain;
     uint32_t tmem, pad;
 };
 
@@ -52,27 +54,23 @@ __device__ __forceinline__ float2 unpack16(uint32_t u) {
     return __half22float2(h);
 }
 
-// The row's elements [c, c + 16) as 8 registers, zero beyond d; `vec`: 16-byte loads
-template <bool BF>
-__device__ __forceinline__ void load16(const View& w, int64_t off, int c, int d, bool live, bool vec,
-                                       uint32_t* u) {
+// The row's elements [c, c + 8) as 4 registers, zero beyond d; `vec`: 16-byte loads
+__device__ __forceinline__ void load8(const View& w, int64_t off, int c, int d, bool live, bool vec,
+                                      uint32_t* u) {
     const uint16_t* p = static_cast<const uint16_t*>(w.p) + off;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (live && vec) {
+        if (c < d) x = __ldg(reinterpret_cast<const uint4*>(p + c));
+    } else if (live) {
+        uint32_t* xs = &x.x;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (live && vec) {
-            if (c + 8 * e < d) x = __ldg(reinterpret_cast<const uint4*>(p + c + 8 * e));
-        } else if (live) {
-            uint32_t* xs = &x.x;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (c + 8 * e + k < d) xs[k >> 1] |= (uint32_t)__ldg(p + c + 8 * e + k) << (16 * (k & 1));
-        }
-        u[4 * e] = x.x;
-        u[4 * e + 1] = x.y;
-        u[4 * e + 2] = x.z;
-        u[4 * e + 3] = x.w;
+        for (int k = 0; k < 8; ++k)
+            if (c + k < d) xs[k >> 1] |= (uint32_t)__ldg(p + c + k) << (16 * (k & 1));
     }
+    u[0] = x.x;
+    u[1] = x.y;
+    u[2] = x.z;
+    u[3] = x.w;
 }
 
 // Columns [c0, c1) of a row of sums in TMEM, times `mul` (zero where !keep), rounded into
@@ -129,6 +127,22 @@ __device__ __forceinline__ void diagonals(const float* v, float* scratch, int la
     }
 }
 
+// k_grad_kv divides lse2 by scale2, which must not overflow: its scale2 is 2^-96 where it
+// is less (the scores' share of x is below 2^-32 then), and a quotient stays within
+// 2^120, where p = 0 for any finite bias that does not forbid its key.
+constexpr float kRowLimit = 1.329227995784916e36f;      // 2^120
+__device__ __forceinline__ float least_scale(const Args& a) { return fmaxf(a.scale2, 1.262177448353619e-29f); }
+
+// x as three bfloat16 terms (24 bits), then five zeros
+__device__ __forceinline__ uint4 three_terms(float x) {
+    const float hi = __bfloat162float(__float2bfloat16_rn(x)), y = x - hi;
+    const float mid = __bfloat162float(__float2bfloat16_rn(y));
+    return make_uint4(pack16<true>(hi, mid), pack16<true>(y - mid, 0.f), 0u, 0u);
+}
+
+// Q and dO are copied to TMEM once (as A operands in shared memory they are read with
+// every product: 94 instead of 67 us for 304 blocks of 16 key tiles, heads of 128,
+// although TMEM then has room for two dP tiles).
 template <int HD>
 struct GradQ {
     static constexpr int kKeys = kTile, kCols = kTile / 2;       // keys of a tile, of a warp
@@ -153,7 +167,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int NS = P.stages;                // even: K and V keep their slots
-    uint8_t* sKV = smem;                    // at the end the rows of dq
+    uint8_t* sKV = smem;                    // at first Q and dO in the last two tiles, at the end dq
+    uint8_t* sOwn = sKV + (NS - 2) * C::kTileBytes;
     GradBars& bar = *reinterpret_cast<GradBars*>(sKV + NS * C::kTileBytes);
     float* sDelta = reinterpret_cast<float*>(&bar + 1);          // [128]
     float* sFar = sDelta + kTile;                                // [8][2]
@@ -171,11 +186,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
     const int nt = step_count<KT>(P.kt, b, end);
     const bool partial_keys = P.kt.words != nullptr || end < a.m;
     const int64_t first = (a.q_pos ? (int64_t)__ldg(a.q_pos + b) : 0) + i0;
-    const int dsteps = (a.d + 15) >> 4;
+    const int dsteps = (a.d + 15) >> 4, dpairs = (a.d + 31) >> 5;
     const int width = 2 * a.D + 1;
 
     if (warp == kLoad) {
         if (lane < NS) mbar_init(&bar.full[lane], 1);
+        if (lane == NS) mbar_init(&bar.own, 1);
+        if (lane == NS + 1) mbar_init(&bar.ready, kElemWarps);
         fence_mbar_init();
         __syncwarp();
     } else if (warp == kClean) {
@@ -183,7 +200,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
             mbar_init(&bar.empty[lane], 1);
             mbar_init(&bar.clean[lane], 1);
         } else if (lane == NS) {
-            mbar_init(&bar.ready, kElemWarps);
             mbar_init(&bar.sfull, 1);
             mbar_init(&bar.sfree, kElemWarps);
             mbar_init(&bar.dpfull[0], 1);
@@ -204,9 +220,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
             tma_load(sKV + slot * C::kTileBytes + c * C::kChunkBytes, &src.map, c * 64, key, g * src.head,
                      b * src.batch, &bar.full[slot]);
     };
-    const int early = min(2 * nt, NS);             // copies that need no free slot
-    if (warp == kLoad && nt > 0 && elect_one())
+    const int early = min(2 * nt, NS - 2);         // copies that need no free slot
+    if (warp == kLoad && nt > 0 && elect_one()) {
+        mbar_arrive_expect_tx(&bar.own, 2 * C::kTileBytes);
+        for (int c = 0; c < C::kChunks; ++c) {
+            tma_load(sOwn + c * CHUNK_BYTES, &P.q.map, c * 64, i0, h * P.q.head, b * P.q.batch, &bar.own);
+            tma_load(sOwn + C::kTileBytes + c * CHUNK_BYTES, &P.dout.map, c * 64, i0, h * P.dout.head,
+                     b * P.dout.batch, &bar.own);
+        }
         for (int it = 0; it < early; ++it) load(it, it);
+    }
     if (a.table) fill_bias<BF>(a, h, sBias, threadIdx.x, kGradThreads);
     if (a.bias_part)
         for (int e = threadIdx.x; e < kBands * width; e += kGradThreads) sSums[e] = 0.f;
@@ -222,15 +245,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
             int issued = early;
             bool ok = true;
             for (int it = early; it < 2 * nt; ++it) {
-                if (!mbar_wait(&bar.empty[r.slot], r.phase ^ 1u, a.err, ERR_TIMEOUT_PRODUCER)) {
-                    ok = false;
-                    break;
-                }
+                // (Q and dO have left the last two slots before their first use)
+                if (it == NS - 2) ok = mbar_wait(&bar.ready, 0, a.err, ERR_TIMEOUT_PRODUCER);
+                ok = ok && mbar_wait(&bar.empty[r.slot], r.phase ^ 1u, a.err, ERR_TIMEOUT_PRODUCER);
+                if (!ok) break;
                 load(it, r.slot);
                 ++issued;
                 r.step(1, NS);
             }
             if (!ok) {   // every copy lands before the block can exit
+                mbar_wait(&bar.own, 0, a.err, ERR_TIMEOUT_PRODUCER);
                 Ring l;
                 for (int it = 0; it < issued; ++it) {
                     if (it + NS >= issued)
@@ -249,7 +273,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
             uint32_t sph = 0;    // phase of the slot of the next dP
             int sslot = 0;
             const auto scores = [&]() {
-                mma_over_d_ts<CHUNK_BYTES>(tmem + C::S, tmem + C::Q, dKV + rs.slot * kTileU, idS, dsteps);
+                mma_over_d_ts<CHUNK_BYTES>(tmem + C::S, tmem + C::Q, dKV + rs.slot * kTileU, idS, dpairs);
                 mma_commit(&bar.sfull);
                 sslot = rs.slot + 1;
                 sph = rs.phase;
@@ -257,7 +281,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
             };
             const auto grads = [&](int buf) {
                 mma_over_d_ts<CHUNK_BYTES>(tmem + C::DP + buf * kTile, tmem + C::DO, dKV + sslot * kTileU, idS,
-                                           dsteps);
+                                           dpairs);
                 mma_commit(&bar.dpfull[buf]);
                 mma_commit(&bar.empty[sslot]);
             };
@@ -315,51 +339,69 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
         const bool live = i < a.n;
         const uint32_t lofs = (uint32_t)(quarter * 32) << 16;
         const int64_t row = ((int64_t)b * a.H + h) * a.n + i;
-        // operands into TMEM: warps 0..3 the rows of Q, warps 4..7 those of dO with delta
-        {
-            const View& w = half ? a.dout : a.q;
-            const int64_t off = b * w.sb + (int64_t)i * w.st + h * w.sh;
-            const int64_t oo = b * a.o.sb + (int64_t)i * a.o.st + h * a.o.sh;
-            float dot = 0.f;
-#pragma unroll 2
-            for (int x = 0; x < dsteps; ++x) {
-                uint32_t u[8];
-                load16<BF>(w, off, 16 * x, a.d, live, half ? P.dout_vec : P.q_vec, u);
-                if (half) {
-                    uint32_t v[8];
-                    load16<BF>(a.o, oo, 16 * x, a.d, live, P.o_vec, v);
+        {       // delta of 16 rows a warp, kLanes lanes to a row
+            constexpr int kLanes = HD / 8, kRows = 32 / kLanes;
+            const int c = 8 * (lane % kLanes);
+            float dot[16 / kRows];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 f = unpack16<BF>(u[e]), g = unpack16<BF>(v[e]);
-                        dot = fmaf(f.x, g.x, dot);
-                        dot = fmaf(f.y, g.y, dot);
-                    }
+            for (int k = 0; k < 16 / kRows; ++k) {
+                const int ri = i0 + warp * 16 + k * kRows + lane / kLanes;
+                uint32_t u[4], v[4];
+                load8(a.dout, b * a.dout.sb + (int64_t)ri * a.dout.st + h * a.dout.sh, c, a.d, ri < a.n,
+                      P.dout_vec, u);
+                load8(a.o, b * a.o.sb + (int64_t)ri * a.o.st + h * a.o.sh, c, a.d, ri < a.n, P.o_vec, v);
+                dot[k] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = unpack16<BF>(u[e]), g = unpack16<BF>(v[e]);
+                    dot[k] = fmaf(f.x, g.x, dot[k]);
+                    dot[k] = fmaf(f.y, g.y, dot[k]);
                 }
-                __syncwarp();
+            }
+#pragma unroll
+            for (int k = 0; k < 16 / kRows; ++k) {
+#pragma unroll
+                for (int o = kLanes / 2; o; o >>= 1) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], o);
+                if (lane % kLanes == 0) sDelta[warp * 16 + k * kRows + lane / kLanes] = dot[k];
+            }
+        }
+        bool ok = true;
+        if (nt > 0) {     // operands into TMEM: warps 0..3 the rows of Q, warps 4..7 those of dO
+            ok = warp_wait(&bar.own, 0, a.err, ERR_TIMEOUT_EPILOGUE);
+            const uint8_t* src = sOwn + half * C::kTileBytes;
+#pragma unroll 4
+            for (int x = 0; x < 2 * dpairs; ++x) {
+                uint32_t u[8];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 y = *reinterpret_cast<const uint4*>(
+                        src + (x >> 2) * CHUNK_BYTES + swz_offset(r, (x & 3) * 16 + 8 * e));
+                    u[4 * e] = y.x;
+                    u[4 * e + 1] = y.y;
+                    u[4 * e + 2] = y.z;
+                    u[4 * e + 3] = y.w;
+                }
                 tmem_st8u(tmem + lofs + (half ? C::DO : C::Q) + 8 * x, u);
             }
             tmem_wait_st();
             tc_fence_before();
+            fence_proxy_async_smem();      // the slots are copied over next
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.ready);
-            if (half) sDelta[r] = dot;
         }
         // a row without a counted key has p = 0, as if its lse were +inf
         float lse2 = live ? a.lse[row] * (float)kLog2e : INFINITY;
         if (lse2 == -INFINITY) lse2 = INFINITY;
         named_sync(1, 32 * kElemWarps);
         const float delta = sDelta[r];
-        if (half == 0) {
-            float* pad = P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * 2 * kTile + r;
-            pad[0] = -lse2;
-            pad[kTile] = -delta;
-        }
+        *reinterpret_cast<uint4*>(P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowBytes +
+                                  (r >> 3) * 256 + half * 128 + (r & 7) * 16) =
+            three_terms(half ? -delta : fminf(fmaxf(-lse2 / least_scale(a), -kRowLimit), kRowLimit));
         const float nlse = -lse2;
         const uint32_t tS = tmem + lofs + C::S + half * NC;
         float* scratch = sScratch + warp * P.scratch_rows * 33;
         float far_lo = 0.f, far_hi = 0.f;
-        bool ok = true;
-        for (int j = 0; j < nt; ++j) {
+        for (int j = 0; j < nt && ok; ++j) {
             const int buf = C::kDp == 2 ? j & 1 : 0;
             const uint32_t tDP = tmem + lofs + C::DP + buf * kTile + half * NC;
             // relative position of the warp's first row and column
@@ -544,8 +586,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
     uint8_t* sK = smem;                   // at the end the rows of dk and dv
     uint8_t* sV = sK + C::kOwnBytes;
     uint8_t* sR = sV + C::kOwnBytes;
-    float* sRow = reinterpret_cast<float*>(sR + NS * C::kTileBytes);   // [NS / 2][-lse2, -delta][QT]
-    GradBars& bar = *reinterpret_cast<GradBars*>(sRow + NS * QT);
+    uint8_t* sRow = sR + NS * C::kTileBytes;       // [NS / 2][kRowBytes], the queries' row values
+    uint8_t* sOnes = sRow + NS / 2 * kRowBytes;    // [128][8 zeros, 1 1 1 0 0 0 0 0, 8 zeros]
+    GradBars& bar = *reinterpret_cast<GradBars*>(sOnes + kOnesBytes);
     float* sBias = reinterpret_cast<float*>(&bar + 1);
 
     int blk = blockIdx.x;
@@ -559,7 +602,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
     if (j0 < end) w = tile_words(P.kt, b, kt, end);
     const bool any = (w.x | w.y | w.z | w.w) != 0;
     const int64_t pos = a.q_pos ? (int64_t)__ldg(a.q_pos + b) : 0;
-    const int dsteps = (a.d + 15) >> 4;
+    const int dsteps = (a.d + 15) >> 4, dpairs = (a.d + 31) >> 5;
     const int per_head = (a.n + QT - 1) / QT;        // query tiles of a head
     const int nt = any ? a.R * per_head : 0;
 
@@ -587,13 +630,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
         const int t = it >> 1, h = g * a.R + t / per_head, qt = t % per_head;
         const bool second = it & 1;
         const TensorMap& src = second ? P.dout : P.q;
-        mbar_arrive_expect_tx(&bar.full[slot], C::kTileBytes + (second ? 0 : 8 * QT));
+        mbar_arrive_expect_tx(&bar.full[slot], C::kTileBytes + (second ? 0 : kRowBytes));
         for (int c = 0; c < C::kChunks; ++c)
             tma_load(sR + slot * C::kTileBytes + c * C::kChunkBytes, &src.map, c * 64, qt * QT, h * src.head,
                      b * src.batch, &bar.full[slot]);
         if (!second)
-            bulk_g2s(sRow + (slot >> 1) * 2 * QT,
-                     P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * 2 * QT, 8 * QT,
+            bulk_g2s(sRow + (slot >> 1) * kRowBytes,
+                     P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowBytes, kRowBytes,
                      &bar.full[slot]);
     };
     const int early = min(2 * nt, NS);
@@ -605,6 +648,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
         }
         for (int it = 0; it < early; ++it) load(it, it);
     }
+    for (int e = threadIdx.x; e < kOnesBytes / 16; e += kGradThreads)
+        reinterpret_cast<uint4*>(sOnes)[e] =
+            (e / 8) % 3 == 1 ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -641,18 +688,27 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
             const uint32_t idD = idesc_16(BF, dsteps * 16, true);
             const uint64_t dK = sdesc_sw128(smem_u32(sK)), dV = sdesc_sw128(smem_u32(sV));
             const uint64_t dR = sdesc_sw128(smem_u32(sR)), dRt = sdesc_tokens(smem_u32(sR));
+            const uint32_t idR = idesc_16(true, kTile, false);
+            const uint64_t dRow = sdesc_flat(smem_u32(sRow), 256), dOnes = sdesc_flat(smem_u32(sOnes), 384);
             Ring rs, rd;      // tiles whose scores, and whose dV and dK, come next: Q at slot, dO at slot + 1
-            bool ok = mma_wait(a.err, &bar.ready, 0) && mma_wait(a.err, &bar.full[0], 0);
-            if (ok) {
-                mma_over_d(tmem + C::S, dK, dR, idS, dsteps);
+            // K Q^T - lse2 / scale2, V dO^T - delta: the row values are a last product's sums
+            const auto scores = [&]() {
+                mma_over_d(tmem + C::S, dK, dR + rs.slot * kTileU, idS, dpairs);
+                mma_f16(tmem + C::S, dOnes + (128 >> 4), dRow + (rs.slot >> 1) * (kRowBytes >> 4), idR, true);
                 mma_commit(&bar.sfull);
-                ok = mma_wait(a.err, &bar.full[1], 0);
-            }
-            if (ok) {
-                mma_over_d(tmem + C::DP, dV, dR + kTileU, idS, dsteps);
+            };
+            const auto grads = [&]() {
+                mma_over_d(tmem + C::DP, dV, dR + (rs.slot + 1) * kTileU, idS, dpairs);
+                mma_f16(tmem + C::DP, dOnes, dRow + (rs.slot >> 1) * (kRowBytes >> 4), idR, true);
                 mma_commit(&bar.dpfull[0]);
                 rs.step(2, NS);
+            };
+            bool ok = mma_wait(a.err, &bar.ready, 0) && mma_wait(a.err, &bar.full[0], 0);
+            if (ok) {
+                scores();
+                ok = mma_wait(a.err, &bar.full[1], 0);
             }
+            if (ok) grads();
             for (int t = 0; t < nt && ok; ++t) {
                 const bool more = t + 1 < nt;
                 if (!(ok = mma_wait(a.err, &bar.pfull, t & 1))) break;
@@ -660,8 +716,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
                 mma_commit(&bar.empty[rd.slot + 1]);
                 if (more) {
                     if (!(ok = mma_wait(a.err, &bar.full[rs.slot], rs.phase))) break;
-                    mma_over_d(tmem + C::S, dK, dR + rs.slot * kTileU, idS, dsteps);
-                    mma_commit(&bar.sfull);
+                    scores();
                 }
                 if (!(ok = mma_wait(a.err, &bar.dsfull, t & 1))) break;
                 mma_over_tokens(tmem + C::DK, tmem + C::DP, dRt + rd.slot * kTileU, idD, t > 0, 64);
@@ -669,9 +724,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
                 rd.step(2, NS);
                 if (more) {
                     if (!(ok = mma_wait(a.err, &bar.full[rs.slot + 1], rs.phase))) break;
-                    mma_over_d(tmem + C::DP, dV, dR + (rs.slot + 1) * kTileU, idS, dsteps);
-                    mma_commit(&bar.dpfull[0]);
-                    rs.step(2, NS);
+                    grads();
                 }
             }
             mma_commit(&bar.done);
@@ -684,7 +737,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
         const int j = j0 + r;
         const uint32_t lofs = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lofs + C::S + half * NC, tDP = tmem + lofs + C::DP + half * NC;
-        Ring ring;
+        const float scale2 = least_scale(a);
         bool ok = true;
         int h = g * a.R, qt = 0;
         for (int t = 0; t < nt; ++t) {
@@ -693,14 +746,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
                 fill_bias<BF>(a, h, sBias, threadIdx.x, 32 * kElemWarps);
                 named_sync(1, 32 * kElemWarps);
             }
-            const float* rows = sRow + (ring.slot >> 1) * 2 * QT + half * NC;
             // (a warp that gave up still meets the others at the barriers above)
-            ok = ok && warp_wait(&bar.full[ring.slot], ring.phase, a.err, ERR_TIMEOUT_EPILOGUE);
-            // the row values go to registers ahead of the tiles they are used with
             float v[NC];
-            float4 l[NC / 4];
-#pragma unroll
-            for (int c = 0; c < NC / 4; ++c) l[c] = *reinterpret_cast<const float4*>(rows + 4 * c);
             ok = ok && warp_wait(&bar.sfull, t & 1, a.err, ERR_TIMEOUT_EPILOGUE);
             if (ok) {
                 tc_fence_after();
@@ -708,24 +755,27 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
                 for (int c = 0; c < NC; c += 32) tmem_ld32(tS + c, v + c);
                 tmem_wait_ld();
                 tmem_reg_fence(v);
-                float mul = a.scale2;
+                float mul = scale2, add = 0.f;
                 if (a.table) {
                     // relative position of the tile's first key and the strip's first query
                     const int64_t rel0 = (int64_t)j0 - pos - (int64_t)qt * QT - half * NC;
-                    const bool above = rel0 - (NC - 1) >= a.D, below = rel0 + (kTile - 1) <= -a.D;
-                    const float* e = sBias + (above || below ? 0 : (int)rel0 + r + a.D + kSlack);
-                    const float add = sBias[above ? 2 * a.D + kSlack : kSlack];
+                    if (rel0 - (NC - 1) >= a.D) {
+                        add = sBias[2 * a.D + kSlack];
+                    } else if (rel0 + (kTile - 1) <= -a.D) {
+                        add = sBias[kSlack];
+                    } else {
+                        const float* e = sBias + (int)rel0 + r + a.D + kSlack;
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) v[c] = fmaf(v[c], mul, above || below ? add : e[-c]);
-                    mul = 1.f;
+                        for (int c = 0; c < NC; ++c) v[c] = fmaf(v[c], mul, e[-c]);
+                        mul = 1.f;
+                    }
                 }
-                const uint64_t mul2 = pk(mul, mul);
+                const uint64_t mul2 = pk(mul, mul), add2 = pk(add, add);
 #pragma unroll
-                for (int c = 0; c < NC; c += 4) {
-                    upk(fma2(pk(v[c], v[c + 1]), mul2, pk(l[c / 4].x, l[c / 4].y)), v[c], v[c + 1]);
-                    upk(fma2(pk(v[c + 2], v[c + 3]), mul2, pk(l[c / 4].z, l[c / 4].w)), v[c + 2], v[c + 3]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[c + e] = ex2(v[c + e]);
+                for (int c = 0; c < NC; c += 2) {
+                    upk(fma2(pk(v[c], v[c + 1]), mul2, add2), v[c], v[c + 1]);
+                    v[c] = ex2(v[c]);
+                    v[c + 1] = ex2(v[c + 1]);
                 }
                 {
                     uint32_t u[NC / 2];
@@ -738,8 +788,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
                     if (lane == 0) mbar_arrive(&bar.pfull);
                 }
             }
-#pragma unroll
-            for (int c = 0; c < NC / 4; ++c) l[c] = *reinterpret_cast<const float4*>(rows + QT + 4 * c);
             ok = ok && warp_wait(&bar.dpfull[0], t & 1, a.err, ERR_TIMEOUT_EPILOGUE);
             if (ok) {
                 tc_fence_after();
@@ -751,14 +799,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
                     tmem_wait_ld();
                     tmem_reg_fence(d);
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const float4 x = l[(q + c) / 4];
-                        float f0, f1, f2, f3;
-                        upk(mul2f(pk(v[q + c], v[q + c + 1]), add2(pk(d[c], d[c + 1]), pk(x.x, x.y))), f0, f1);
-                        upk(mul2f(pk(v[q + c + 2], v[q + c + 3]), add2(pk(d[c + 2], d[c + 3]), pk(x.z, x.w))),
-                            f2, f3);
+                    for (int c = 0; c < 32; c += 2) {
+                        float f0, f1;
+                        upk(mul2f(pk(v[q + c], v[q + c + 1]), pk(d[c], d[c + 1])), f0, f1);
                         u[(q + c) / 2] = pack16<BF>(f0, f1);
-                        u[(q + c) / 2 + 1] = pack16<BF>(f2, f3);
                     }
                 }
                 tmem_st32(tDP, u);
@@ -767,7 +811,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.dsfull);
             }
-            ring.step(2, NS);
             if (++qt == per_head) {
                 qt = 0;
                 ++h;
@@ -856,11 +899,15 @@ int ring_stages(size_t fixed, size_t per_stage) {
     return s < kMaxRing ? s : kMaxRing;
 }
 
-// the least shared memory of the largest call leaves four tiles
+// the least shared memory of the largest calls leaves four tiles
 static_assert(1024 + sizeof(GradBars) + 4 * (kTile + 2 * kElemWarps) + 4 * (2 * (kMaxDistance + kSlack) + 1) +
                       4 * kBands * (2 * kMaxDistance + 1) + 4 * kElemWarps * 8 * 33 + 4 * 2 * CHUNK_BYTES <=
                   kSmemLimit,
               "k_grad_q does not fit in shared memory");
+static_assert(1024 + sizeof(GradBars) + 4 * (2 * (kMaxDistance + kSlack) + 1) + kOnesBytes +
+                      6 * 2 * CHUNK_BYTES + 2 * kRowBytes <=
+                  kSmemLimit,
+              "k_grad_kv does not fit in shared memory");
 
 template <int HD, bool BF>
 cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
@@ -884,9 +931,9 @@ cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
     k_grad_q<HD, BF><<<(unsigned)((int64_t)p.q_tiles * a.H * a.B), kGradThreads,
                        fixed + p.stages * Q::kTileBytes, s>>>(p);
     count_launch();
-    // K and V, then stages of which each pair has a row of (-lse2, -delta)
-    constexpr size_t stage = KV::kTileBytes + 4 * KV::kQueries;
-    fixed = 1024 + sizeof(GradBars) + bias + 2 * KV::kOwnBytes;
+    // K and V, then stages of which each pair has the row values of its queries
+    constexpr size_t stage = KV::kTileBytes + kRowBytes / 2;
+    fixed = 1024 + sizeof(GradBars) + bias + 2 * KV::kOwnBytes + kOnesBytes;
     p.kv_stages = 2 * (ring_stages(fixed, stage) / 2);
     if ((e = raise_smem(k_grad_kv<HD, BF>, kSmemLimit, ready_kv)) != cudaSuccess) return e;
     k_grad_kv<HD, BF><<<(unsigned)((int64_t)p.k_tiles * a.G * a.B), kGradThreads,

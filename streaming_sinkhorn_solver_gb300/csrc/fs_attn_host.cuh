@@ -36,14 +36,18 @@ struct FwdArgs {
     int out_vec;       // the rows of out take 16-byte stores
 };
 
+// -lse2 / scale2 and -delta of 128 queries, each as three bfloat16 terms, in the form
+// of an operand of 16 elements a row (sdesc_flat)
+constexpr int kRowBytes = kTile * 32;
+
 struct GradArgs {
     TensorMap q, k, v, dout;
     Args a;
     KeyTiles kt;
-    float* rows;       // [B][H][q_tiles][-lse2 of 128 queries, -delta of 128 queries]
+    uint8_t* rows;     // [B][H][q_tiles][kRowBytes]: what k_grad_q leaves for k_grad_kv
     int q_tiles, k_tiles;
     int stages, kv_stages, scratch_rows;     // set at launch
-    int q_vec, dout_vec, o_vec, dq_vec, dk_vec, dv_vec;   // rows take 16-byte accesses
+    int dout_vec, o_vec, dq_vec, dk_vec, dv_vec;   // rows take 16-byte accesses
 };
 
 // dq, then dk and dv, then dbias (nullptr: none)

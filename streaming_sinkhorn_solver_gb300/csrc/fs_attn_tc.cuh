@@ -93,6 +93,17 @@ __device__ __forceinline__ uint64_t sdesc_tokens(uint32_t saddr, uint32_t chunk_
     return d;
 }
 
+// Operand of 16 elements a row without swizzle: 8 x 8 element blocks of 128 bytes
+// (rows of 16 bytes), the two of a row group 128 bytes apart, row groups `group` bytes.
+__device__ __forceinline__ uint64_t sdesc_flat(uint32_t saddr, uint32_t group) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(128 >> 4) << 16;
+    d |= (uint64_t)(group >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    return d;
+}
+
 // kind::f16 with float32 sums; b_tokens: B is summed over its rows
 __host__ __device__ constexpr uint32_t idesc_16(bool bf16, int N, bool b_tokens) {
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
@@ -111,25 +122,32 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
 }
 
 // D[tmem] = A * B^T over the d elements of a 128-token tile (A) and a tile of
-// B_CHUNK / 128 tokens (B), in chunks of 64; `steps` products of 16 elements.  One
-// elected thread.  (The count is a loop bound, not a condition around each product:
-// products under a data-dependent condition ended in illegal accesses.)
+// B_CHUNK / 128 tokens (B), in chunks of 64, both zero beyond d; `pairs` times two
+// products of 16 elements (the issuing thread takes 80 cycles for one product a turn
+// of the loop, more than the products themselves).  One elected thread.  (The count is
+// a loop bound, not a condition around each product: products under a data-dependent
+// condition ended in illegal accesses.)
 template <int B_CHUNK = CHUNK_BYTES>
 __device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                           int steps) {
+                                           int pairs) {
 #pragma unroll 1
-    for (int x = 0; x < steps; ++x)
-        mma_f16(d_tmem, a + (uint64_t)((x >> 2) * (CHUNK_BYTES >> 4) + 2 * (x & 3)),
-                b + (uint64_t)((x >> 2) * (B_CHUNK >> 4) + 2 * (x & 3)), idesc, x != 0);
+    for (int x = 0; x < pairs; ++x) {
+        const uint64_t da = a + (uint64_t)((x >> 1) * (CHUNK_BYTES >> 4) + 4 * (x & 1));
+        const uint64_t db = b + (uint64_t)((x >> 1) * (B_CHUNK >> 4) + 4 * (x & 1));
+        mma_f16(d_tmem, da, db, idesc, x != 0);
+        mma_f16(d_tmem, da + 2, db + 2, idesc, true);
+    }
 }
 // the same with A in TMEM
 template <int B_CHUNK>
 __device__ __forceinline__ void mma_over_d_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                              int steps) {
+                                              int pairs) {
 #pragma unroll 1
-    for (int x = 0; x < steps; ++x)
-        mma_f16_ts(d_tmem, a_tmem + 8 * x, b + (uint64_t)((x >> 2) * (B_CHUNK >> 4) + 2 * (x & 3)), idesc,
-                   x != 0);
+    for (int x = 0; x < pairs; ++x) {
+        const uint64_t db = b + (uint64_t)((x >> 1) * (B_CHUNK >> 4) + 4 * (x & 1));
+        mma_f16_ts(d_tmem, a_tmem + 16 * x, db, idesc, x != 0);
+        mma_f16_ts(d_tmem, a_tmem + 16 * x + 8, db + 2, idesc, true);
+    }
 }
 // D[tmem] (+)= A[tmem] * B over the KEYS tokens of B's tile; tokens 64 and on of A are
 // `half` columns from its first.  One elected thread.

@@ -328,7 +328,7 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     p.q_tiles = (a.n + kTile - 1) / kTile;
     p.k_tiles = tiles.kt.tiles;
     const size_t blocks = (size_t)a.B * a.H * p.q_tiles;
-    const size_t rows = c.L.take(blocks * kRowBytes);
+    const size_t rows = c.L.take(blocks * kRowStride);
     const size_t part = c.L.take(dbias ? sizeof(float) * blocks * (2 * (size_t)a.D + 1) : 0);
     FS_TRY(begin_call(c, stream));
     FS_TRY(ensure_capacity(c));

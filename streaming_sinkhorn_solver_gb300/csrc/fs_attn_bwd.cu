@@ -54,25 +54,6 @@ __device__ __forceinline__ float2 unpack16(uint32_t u) {
     return __half22float2(h);
 }
 
-// The row's elements [c, c + 8) as 4 registers, zero beyond d; `vec`: 16-byte loads
-__device__ __forceinline__ void load8(const View& w, int64_t off, int c, int d, bool live, bool vec,
-                                      uint32_t* u) {
-    const uint16_t* p = static_cast<const uint16_t*>(w.p) + off;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (live && vec) {
-        if (c < d) x = __ldg(reinterpret_cast<const uint4*>(p + c));
-    } else if (live) {
-        uint32_t* xs = &x.x;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (c + k < d) xs[k >> 1] |= (uint32_t)__ldg(p + c + k) << (16 * (k & 1));
-    }
-    u[0] = x.x;
-    u[1] = x.y;
-    u[2] = x.z;
-    u[3] = x.w;
-}
-
 // Columns [c0, c1) of a row of sums in TMEM, times `mul` (zero where !keep), rounded into
 // a staged tile.  Whole warps.
 template <bool BF>
@@ -127,7 +108,7 @@ __device__ __forceinline__ void diagonals(const float* v, float* scratch, int la
     }
 }
 
-// k_grad_kv divides lse2 by scale2, which must not overflow: its scale2 is 2^-96 where it
+// grad_keys divides lse2 by scale2, which must not overflow: its scale2 is 2^-96 where it
 // is less (the scores' share of x is below 2^-32 then), and a quotient stays within
 // 2^120, where p = 0 for any finite bias that does not forbid its key.
 constexpr float kRowLimit = 1.329227995784916e36f;      // 2^120
@@ -139,6 +120,86 @@ __device__ __forceinline__ uint4 three_terms(float x) {
     const float mid = __bfloat162float(__float2bfloat16_rn(y));
     return make_uint4(pack16<true>(hi, mid), pack16<true>(y - mid, 0.f), 0u, 0u);
 }
+
+// ---------------------------------------------------------------------------
+// The row values of 128 queries a block: delta_i = dO_i . O_i and lse_i.  Reads dO and O
+// once, LANES lanes of 8 elements to a row; bound by memory.
+
+constexpr int kRowThreads = 256;
+
+// The row's elements [c, c + 8) as 4 registers, zero beyond d; `vec`: 16-byte loads
+__device__ __forceinline__ void load8(const View& w, int64_t off, int c, int d, bool live, bool vec,
+                                      uint32_t* u) {
+    const uint16_t* p = static_cast<const uint16_t*>(w.p) + off;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (live && vec) {
+        if (c < d) x = __ldg(reinterpret_cast<const uint4*>(p + c));
+    } else if (live) {
+        uint32_t* xs = &x.x;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (c + k < d) xs[k >> 1] |= (uint32_t)__ldg(p + c + k) << (16 * (k & 1));
+    }
+    u[0] = x.x;
+    u[1] = x.y;
+    u[2] = x.z;
+    u[3] = x.w;
+}
+
+template <int LANES, bool BF>
+__global__ void __launch_bounds__(kRowThreads) k_grad_rows(const __grid_constant__ GradArgs P) {
+    constexpr int kRows = 32 / LANES, kTurns = 16 / kRows;      // rows of a warp at a time, of 16
+    __shared__ float sDelta[kTile];
+    const Args& a = P.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int blk = blockIdx.x;
+    const int qt = blk % P.q_tiles;
+    blk /= P.q_tiles;
+    const int h = blk % a.H, b = blk / a.H;
+    const int c = 8 * (lane % LANES);
+    uint32_t u[kTurns][4], v[kTurns][4];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int64_t i = qt * kTile + warp * 16 + k * kRows + lane / LANES;
+        load8(a.dout, b * a.dout.sb + i * a.dout.st + h * a.dout.sh, c, a.d, i < a.n, P.dout_vec, u[k]);
+        load8(a.o, b * a.o.sb + i * a.o.st + h * a.o.sh, c, a.d, i < a.n, P.o_vec, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        float dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack16<BF>(u[k][e]), g = unpack16<BF>(v[k][e]);
+            dot = fmaf(f.x, g.x, dot);
+            dot = fmaf(f.y, g.y, dot);
+        }
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane % LANES == 0) sDelta[warp * 16 + k * kRows + lane / LANES] = dot;
+    }
+    __syncthreads();
+    const int r = threadIdx.x & (kTile - 1);
+    const bool second = threadIdx.x >= kTile;         // -delta, else -lse2
+    const int64_t i = qt * kTile + r;
+    float x;
+    if (second) {
+        x = -sDelta[r];
+    } else {
+        x = i < a.n ? -a.lse[((int64_t)b * a.H + h) * a.n + i] * (float)kLog2e : -INFINITY;
+        // a row without a counted key has p = 0, as if its lse were +inf
+        if (x == INFINITY) x = -INFINITY;
+    }
+    uint8_t* out = P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowStride;
+    reinterpret_cast<float*>(out + kRowBytes)[threadIdx.x] = x;
+    if (!second) {
+        x /= least_scale(a);
+        if (x < -kRowLimit) x = -kRowLimit;
+        if (x > kRowLimit) x = kRowLimit;
+    }
+    *reinterpret_cast<uint4*>(out + (r >> 3) * 256 + (second ? 128 : 0) + (r & 7) * 16) = three_terms(x);
+}
+
+// ---------------------------------------------------------------------------
 
 // Q and dO are copied to TMEM once (as A operands in shared memory they are read with
 // every product: 94 instead of 67 us for 304 blocks of 16 key tiles, heads of 128,
@@ -156,7 +217,7 @@ struct GradQ {
 };
 
 template <int HD, bool BF>
-__global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constant__ GradArgs P) {
+__device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
     using C = GradQ<HD>;
     constexpr int KT = C::kKeys, NC = C::kCols;
     constexpr uint64_t kTileU = C::kTileBytes >> 4;
@@ -170,13 +231,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
     uint8_t* sKV = smem;                    // at first Q and dO in the last two tiles, at the end dq
     uint8_t* sOwn = sKV + (NS - 2) * C::kTileBytes;
     GradBars& bar = *reinterpret_cast<GradBars*>(sKV + NS * C::kTileBytes);
-    float* sDelta = reinterpret_cast<float*>(&bar + 1);          // [128]
-    float* sFar = sDelta + kTile;                                // [8][2]
+    float* sFar = reinterpret_cast<float*>(&bar + 1);            // [8][2]
     float* sBias = sFar + 2 * kElemWarps;                        // [2 (D + kSlack) + 1]
     float* sSums = sBias + (a.table ? 2 * (a.D + kSlack) + 1 : 0);   // [4][2 D + 1]
     float* sScratch = sSums + kBands * (2 * a.D + 1);            // [8][scratch_rows][33], with bias sums
 
-    int blk = blockIdx.x;
     const int qt = blk % P.q_tiles;
     blk /= P.q_tiles;
     const int h = blk % a.H;
@@ -336,35 +395,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
         const int quarter = warp & 3, half = warp >> 2;
         const int r = quarter * 32 + lane;
         const int i = i0 + r;
-        const bool live = i < a.n;
         const uint32_t lofs = (uint32_t)(quarter * 32) << 16;
-        const int64_t row = ((int64_t)b * a.H + h) * a.n + i;
-        {       // delta of 16 rows a warp, kLanes lanes to a row
-            constexpr int kLanes = HD / 8, kRows = 32 / kLanes;
-            const int c = 8 * (lane % kLanes);
-            float dot[16 / kRows];
-#pragma unroll
-            for (int k = 0; k < 16 / kRows; ++k) {
-                const int ri = i0 + warp * 16 + k * kRows + lane / kLanes;
-                uint32_t u[4], v[4];
-                load8(a.dout, b * a.dout.sb + (int64_t)ri * a.dout.st + h * a.dout.sh, c, a.d, ri < a.n,
-                      P.dout_vec, u);
-                load8(a.o, b * a.o.sb + (int64_t)ri * a.o.st + h * a.o.sh, c, a.d, ri < a.n, P.o_vec, v);
-                dot[k] = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = unpack16<BF>(u[e]), g = unpack16<BF>(v[e]);
-                    dot[k] = fmaf(f.x, g.x, dot[k]);
-                    dot[k] = fmaf(f.y, g.y, dot[k]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 16 / kRows; ++k) {
-#pragma unroll
-                for (int o = kLanes / 2; o; o >>= 1) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], o);
-                if (lane % kLanes == 0) sDelta[warp * 16 + k * kRows + lane / kLanes] = dot[k];
-            }
-        }
+        const float* row =
+            reinterpret_cast<const float*>(P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowStride + kRowBytes);
+        const float nlse = row[r], ndelta = row[kTile + r];
         bool ok = true;
         if (nt > 0) {     // operands into TMEM: warps 0..3 the rows of Q, warps 4..7 those of dO
             ok = warp_wait(&bar.own, 0, a.err, ERR_TIMEOUT_EPILOGUE);
@@ -389,15 +423,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.ready);
         }
-        // a row without a counted key has p = 0, as if its lse were +inf
-        float lse2 = live ? a.lse[row] * (float)kLog2e : INFINITY;
-        if (lse2 == -INFINITY) lse2 = INFINITY;
-        named_sync(1, 32 * kElemWarps);
-        const float delta = sDelta[r];
-        *reinterpret_cast<uint4*>(P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowBytes +
-                                  (r >> 3) * 256 + half * 128 + (r & 7) * 16) =
-            three_terms(half ? -delta : fminf(fmaxf(-lse2 / least_scale(a), -kRowLimit), kRowLimit));
-        const float nlse = -lse2;
         const uint32_t tS = tmem + lofs + C::S + half * NC;
         float* scratch = sScratch + warp * P.scratch_rows * 33;
         float far_lo = 0.f, far_hi = 0.f;
@@ -451,7 +476,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_q(const __grid_constan
                 for (int c = 0; c < NC; c += 32) tmem_ld32(tDP + c, g + c);
                 tmem_wait_ld();
                 tmem_reg_fence(g);
-                const uint64_t nd = pk(-delta, -delta);
+                const uint64_t nd = pk(ndelta, ndelta);
 #pragma unroll
                 for (int c = 0; c < NC; c += 2)
                     upk(mul2f(pk(v[c], v[c + 1]), add2(pk(g[c], g[c + 1]), nd)), v[c], v[c + 1]);
@@ -572,7 +597,7 @@ struct GradKV {
 };
 
 template <int HD, bool BF>
-__global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_constant__ GradArgs P) {
+__device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
     using C = GradKV<HD>;
     constexpr int QT = C::kQueries, NC = C::kCols;
     constexpr uint64_t kTileU = C::kTileBytes >> 4;
@@ -591,7 +616,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
     GradBars& bar = *reinterpret_cast<GradBars*>(sOnes + kOnesBytes);
     float* sBias = reinterpret_cast<float*>(&bar + 1);
 
-    int blk = blockIdx.x;
     const int kt = blk % P.k_tiles;
     blk /= P.k_tiles;
     const int g = blk % a.G;
@@ -636,7 +660,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
                      b * src.batch, &bar.full[slot]);
         if (!second)
             bulk_g2s(sRow + (slot >> 1) * kRowBytes,
-                     P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowBytes, kRowBytes,
+                     P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowStride, kRowBytes,
                      &bar.full[slot]);
     };
     const int early = min(2 * nt, NS);
@@ -846,6 +870,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad_kv(const __grid_consta
     }
 }
 
+// Both in one launch: the blocks of the keys, which take longer, first; those of the
+// queries fill the GPU's last wave.
+template <int HD, bool BF>
+__global__ void __launch_bounds__(kGradThreads, 1) k_grad(const __grid_constant__ GradArgs P) {
+    const int keys = P.k_tiles * P.a.G * P.a.B;
+    if ((int)blockIdx.x < keys)
+        grad_keys<HD, BF>(P, blockIdx.x);
+    else
+        grad_queries<HD, BF>(P, blockIdx.x - keys);
+}
+
 // ---------------------------------------------------------------------------
 // dbias of one row of the table: the blocks' sums by relative position, in
 // their order, then the positions of each bucket in theirs.
@@ -900,14 +935,14 @@ int ring_stages(size_t fixed, size_t per_stage) {
 }
 
 // the least shared memory of the largest calls leaves four tiles
-static_assert(1024 + sizeof(GradBars) + 4 * (kTile + 2 * kElemWarps) + 4 * (2 * (kMaxDistance + kSlack) + 1) +
+static_assert(1024 + sizeof(GradBars) + 4 * 2 * kElemWarps + 4 * (2 * (kMaxDistance + kSlack) + 1) +
                       4 * kBands * (2 * kMaxDistance + 1) + 4 * kElemWarps * 8 * 33 + 4 * 2 * CHUNK_BYTES <=
                   kSmemLimit,
-              "k_grad_q does not fit in shared memory");
+              "grad_queries does not fit in shared memory");
 static_assert(1024 + sizeof(GradBars) + 4 * (2 * (kMaxDistance + kSlack) + 1) + kOnesBytes +
                       6 * 2 * CHUNK_BYTES + 2 * kRowBytes <=
                   kSmemLimit,
-              "k_grad_kv does not fit in shared memory");
+              "grad_keys does not fit in shared memory");
 
 template <int HD, bool BF>
 cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
@@ -916,9 +951,9 @@ cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
     using KV = GradKV<HD>;
     const size_t bias = a.table ? sizeof(float) * (2 * (size_t)(a.D + kSlack) + 1) : 0;
     const size_t width = 2 * (size_t)a.D + 1;
-    static std::atomic<uint64_t> ready_q{0}, ready_kv{0};
+    static std::atomic<uint64_t> ready{0};
     cudaError_t e;
-    size_t fixed = 1024 + sizeof(GradBars) + sizeof(float) * (kTile + 2 * kElemWarps) + bias +
+    size_t fixed = 1024 + sizeof(GradBars) + sizeof(float) * 2 * kElemWarps + bias +
                    (a.bias_part ? sizeof(float) * kBands * width : 0);
     // shared memory for the diagonals of ds, 32 rows at a time; 8 where that would leave
     // fewer than the four tiles in flight that the order of the products needs (wide
@@ -927,17 +962,17 @@ cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
     p.scratch_rows = ring_stages(fixed + scratch(32), Q::kTileBytes) >= 4 ? 32 : 8;
     fixed += scratch(p.scratch_rows);
     p.stages = 2 * (ring_stages(fixed, Q::kTileBytes) / 2);
-    if ((e = raise_smem(k_grad_q<HD, BF>, kSmemLimit, ready_q)) != cudaSuccess) return e;
-    k_grad_q<HD, BF><<<(unsigned)((int64_t)p.q_tiles * a.H * a.B), kGradThreads,
-                       fixed + p.stages * Q::kTileBytes, s>>>(p);
-    count_launch();
+    size_t smem = fixed + p.stages * Q::kTileBytes;
     // K and V, then stages of which each pair has the row values of its queries
     constexpr size_t stage = KV::kTileBytes + kRowBytes / 2;
     fixed = 1024 + sizeof(GradBars) + bias + 2 * KV::kOwnBytes + kOnesBytes;
     p.kv_stages = 2 * (ring_stages(fixed, stage) / 2);
-    if ((e = raise_smem(k_grad_kv<HD, BF>, kSmemLimit, ready_kv)) != cudaSuccess) return e;
-    k_grad_kv<HD, BF><<<(unsigned)((int64_t)p.k_tiles * a.G * a.B), kGradThreads,
-                        fixed + p.kv_stages * stage, s>>>(p);
+    smem = std::max(smem, fixed + p.kv_stages * stage);
+    if ((e = raise_smem(k_grad<HD, BF>, kSmemLimit, ready)) != cudaSuccess) return e;
+    const int64_t q_blocks = (int64_t)p.q_tiles * a.H * a.B, k_blocks = (int64_t)p.k_tiles * a.G * a.B;
+    k_grad_rows<HD / 8, BF><<<(unsigned)q_blocks, kRowThreads, 0, s>>>(p);
+    count_launch();
+    k_grad<HD, BF><<<(unsigned)(q_blocks + k_blocks), kGradThreads, smem, s>>>(p);
     count_launch();
     if (dbias) {
         // shares of the sums and the buckets in 48 KB

@@ -37,14 +37,15 @@ struct FwdArgs {
 };
 
 // -lse2 / scale2 and -delta of 128 queries, each as three bfloat16 terms, in the form
-// of an operand of 16 elements a row (sdesc_flat)
-constexpr int kRowBytes = kTile * 32;
+// of an operand of 16 elements a row (sdesc_flat), kRowBytes; then -lse2 and -delta in
+// float32
+constexpr int kRowBytes = kTile * 32, kRowStride = kRowBytes + 8 * kTile;
 
 struct GradArgs {
     TensorMap q, k, v, dout;
     Args a;
     KeyTiles kt;
-    uint8_t* rows;     // [B][H][q_tiles][kRowBytes]: what k_grad_q leaves for k_grad_kv
+    uint8_t* rows;     // [B][H][q_tiles][kRowStride]: row values of the queries
     int q_tiles, k_tiles;
     int stages, kv_stages, scratch_rows;     // set at launch
     int dout_vec, o_vec, dq_vec, dk_vec, dv_vec;   // rows take 16-byte accesses

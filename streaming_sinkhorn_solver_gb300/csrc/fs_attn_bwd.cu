@@ -39,7 +39,8 @@ constexpr int kOnesBytes = 384 * kTile / 8;
 
 struct GradBars {
     uint64_t full[kMaxRing], empty[kMaxRing], clean[kMaxRing];
-    uint64_t own, ready, sfull, sfree, dpfull[2], pfull, dsfull, done, drain;
+    uint64_t own, ready, dvdone, done, drain;
+    uint64_t sfull[2], sfree[2], dpfull[2], pfull, dsfull[2];    // grad_queries: of each half of a tile's keys
     uint32_t tmem, pad;
 };
 
@@ -54,23 +55,25 @@ __device__ __forceinline__ float2 unpack16(uint32_t u) {
     return __half22float2(h);
 }
 
-// Columns [c0, c1) of a row of sums in TMEM, times `mul` (zero where !keep), rounded into
-// a staged tile.  Whole warps.
-template <bool BF>
-__device__ __forceinline__ void stage_row(uint8_t* tile, int r, uint32_t tmem_row, int c0, int c1, float mul,
-                                          bool any, bool keep) {
-#pragma unroll 2
-    for (int c = c0; c < c1; c += 16) {
-        float o[16];
-        if (any) {
-            tmem_ld16(tmem_row + c, o);
-            tmem_wait_ld();
-            tmem_reg_fence(o);
-        }
+// The half of a row of dsteps x 16 sums in TMEM, times `mul` (zero where !keep), rounded
+// into a staged tile.  Whole warps.
+template <int HD, bool BF>
+__device__ __forceinline__ void stage_row(uint8_t* tile, int r, uint32_t tmem_row, int half, int dsteps,
+                                          float mul, bool any, bool keep) {
+    const int mid = (dsteps + 1) / 2 * 16;
+    const int c0 = half ? mid : 0, c1 = half ? dsteps * 16 : mid;
+    float o[HD / 2];
+    if (any) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = any && keep ? o[e] * mul : 0.f;
-        stage16<BF>(tile, r, c, o);
+        for (int c = 0; c < HD / 2; c += 32) tmem_ld32(tmem_row + c0 + c, o + c);
+        tmem_wait_ld();
+        tmem_reg_fence(o);
     }
+#pragma unroll
+    for (int c = 0; c < HD / 2; ++c) o[c] = any && keep ? o[c] * mul : 0.f;
+#pragma unroll
+    for (int c = 0; c < HD / 2; c += 16)
+        if (c0 + c < c1) stage16<BF>(tile, r, c0 + c, o + c);
 }
 
 // base-2 bias of head h by relative position -D - kSlack .. D + kSlack
@@ -209,10 +212,7 @@ struct GradQ {
     static constexpr int kKeys = kTile, kCols = kTile / 2;       // keys of a tile, of a warp
     static constexpr int kChunks = HD / 64, kChunkBytes = CHUNK_BYTES;
     static constexpr int kTileBytes = kChunks * CHUNK_BYTES;
-    // TMEM columns; with heads of 64 there is room for two dP (and ds) tiles, so the
-    // next dP does not wait for dQ
-    static constexpr int kDp = HD == 64 ? 2 : 1;
-    static constexpr uint32_t S = 0, DP = kTile, DQ = DP + kDp * kTile, Q = DQ + HD, DO = Q + HD / 2;
+    static constexpr uint32_t S = 0, DP = kTile, DQ = DP + kTile, Q = DQ + HD, DO = Q + HD / 2;    // TMEM columns
     static_assert(DO + HD / 2 <= 512, "TMEM");
 };
 
@@ -220,7 +220,7 @@ template <int HD, bool BF>
 __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
     using C = GradQ<HD>;
     constexpr int KT = C::kKeys, NC = C::kCols;
-    constexpr uint64_t kTileU = C::kTileBytes >> 4;
+    constexpr uint64_t kTileU = C::kTileBytes >> 4, kHalfU = (uint64_t)(NC * 128) >> 4;   // descriptor units
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -245,7 +245,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
     const int nt = step_count<KT>(P.kt, b, end);
     const bool partial_keys = P.kt.words != nullptr || end < a.m;
     const int64_t first = (a.q_pos ? (int64_t)__ldg(a.q_pos + b) : 0) + i0;
-    const int dsteps = (a.d + 15) >> 4, dpairs = (a.d + 31) >> 5;
+    const int dsteps = (a.d + 15) >> 4, dchunks = (a.d + 63) >> 6;
     const int width = 2 * a.D + 1;
 
     if (warp == kLoad) {
@@ -259,11 +259,12 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
             mbar_init(&bar.empty[lane], 1);
             mbar_init(&bar.clean[lane], 1);
         } else if (lane == NS) {
-            mbar_init(&bar.sfull, 1);
-            mbar_init(&bar.sfree, kElemWarps);
-            mbar_init(&bar.dpfull[0], 1);
-            mbar_init(&bar.dpfull[1], 1);
-            mbar_init(&bar.dsfull, kElemWarps);
+            for (int u = 0; u < 2; ++u) {
+                mbar_init(&bar.sfull[u], 1);
+                mbar_init(&bar.sfree[u], kElemWarps / 2);
+                mbar_init(&bar.dpfull[u], 1);
+                mbar_init(&bar.dsfull[u], kElemWarps / 2);
+            }
             mbar_init(&bar.done, 1);
             mbar_init(&bar.drain, 1);
         }
@@ -324,53 +325,53 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
         }
     } else if (warp == kIssue) {
         if (nt > 0 && elect_one()) {
-            const uint32_t idS = idesc_16(BF, kTile, false);
+            const uint32_t idS = idesc_16(BF, NC, false);
             const uint32_t idQ = idesc_16(BF, dsteps * 16, true);
             const uint64_t dKV = sdesc_sw128(smem_u32(sKV)), dKVt = sdesc_tokens(smem_u32(sKV));
             uint64_t* kbar = partial_keys ? bar.clean : bar.full;
-            Ring rs, rq;         // K (and V beside it) of the next scores, K of the next dQ
-            uint32_t sph = 0;    // phase of the slot of the next dP
-            int sslot = 0;
-            const auto scores = [&]() {
-                mma_over_d_ts<CHUNK_BYTES>(tmem + C::S, tmem + C::Q, dKV + rs.slot * kTileU, idS, dpairs);
-                mma_commit(&bar.sfull);
-                sslot = rs.slot + 1;
-                sph = rs.phase;
-                rs.step(2, NS);
+            Ring r;
+            // scores of half u of the tile at r, and its dP from the V tile beside it
+            const auto scores = [&](int u) {
+                mma_over_d_ts(tmem + C::S + u * NC, tmem + C::Q, dKV + r.slot * kTileU + u * kHalfU,
+                                           idS, dchunks);
+                mma_commit(&bar.sfull[u]);
             };
-            const auto grads = [&](int buf) {
-                mma_over_d_ts<CHUNK_BYTES>(tmem + C::DP + buf * kTile, tmem + C::DO, dKV + sslot * kTileU, idS,
-                                           dpairs);
-                mma_commit(&bar.dpfull[buf]);
-                mma_commit(&bar.empty[sslot]);
+            const auto grads = [&](int u) {
+                mma_over_d_ts(tmem + C::DP + u * NC, tmem + C::DO,
+                                           dKV + (r.slot + 1) * kTileU + u * kHalfU, idS, dchunks);
+                mma_commit(&bar.dpfull[u]);
+                if (u) mma_commit(&bar.empty[r.slot + 1]);
             };
-            bool ok = mma_wait(a.err, &bar.ready, 0) && mma_wait(a.err, &kbar[0], 0);
+            bool ok = mma_wait(a.err, &bar.ready, 0) && mma_wait(a.err, &kbar[0], 0) &&
+                      mma_wait(a.err, &bar.full[1], 0);
             if (ok) {
-                scores();
-                ok = mma_wait(a.err, &bar.full[sslot], sph);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    scores(u);
+                    grads(u);
+                }
             }
-            if (ok) grads(0);
             for (int j = 0; j < nt && ok; ++j) {
                 const bool more = j + 1 < nt;
-                if (more) {
-                    // scores of the next tile, once this one's are in registers
-                    // (copies that have long landed are waited for before the warps)
-                    if (!(ok = mma_wait(a.err, &kbar[rs.slot], rs.phase) &&
-                               (C::kDp == 1 || mma_wait(a.err, &bar.full[rs.slot + 1], rs.phase)) &&
-                               mma_wait(a.err, &bar.sfree, j & 1)))
-                        break;
-                    scores();
-                    if (C::kDp == 2)
-                        grads((j + 1) & 1);
-                    else if (!(ok = mma_wait(a.err, &bar.full[sslot], sph)))
-                        break;
+                const uint64_t dTile = dKVt + r.slot * kTileU;
+                uint64_t* const done_with = &bar.empty[r.slot];
+                r.step(2, NS);
+                // (copies that have long landed are waited for before the warps)
+                if (more && !(ok = mma_wait(a.err, &kbar[r.slot], r.phase) &&
+                                   mma_wait(a.err, &bar.full[r.slot + 1], r.phase)))
+                    break;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (more) {      // scores of the next tile, once this one's are in registers
+                        if (!(ok = mma_wait(a.err, &bar.sfree[u], j & 1))) break;
+                        scores(u);
+                    }
+                    if (!(ok = mma_wait(a.err, &bar.dsfull[u], j & 1))) break;
+                    mma_over_tokens<NC>(tmem + C::DQ, tmem + C::DP + u * NC, dTile + u * kHalfU, idQ,
+                                        j > 0 || u > 0, 0);
+                    if (u) mma_commit(done_with);
+                    if (more) grads(u);
                 }
-                if (!(ok = mma_wait(a.err, &bar.dsfull, j & 1))) break;
-                mma_over_tokens(tmem + C::DQ, tmem + C::DP + (C::kDp == 2 ? (j & 1) * kTile : 0),
-                                dKVt + rq.slot * kTileU, idQ, j > 0, 64);
-                mma_commit(&bar.empty[rq.slot]);
-                rq.step(2, NS);
-                if (more && C::kDp == 1) grads(0);
             }
             mma_commit(&bar.done);
             mma_commit(&bar.drain);
@@ -404,7 +405,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
             ok = warp_wait(&bar.own, 0, a.err, ERR_TIMEOUT_EPILOGUE);
             const uint8_t* src = sOwn + half * C::kTileBytes;
 #pragma unroll 4
-            for (int x = 0; x < 2 * dpairs; ++x) {
+            for (int x = 0; x < 4 * dchunks; ++x) {
                 uint32_t u[8];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -423,16 +424,14 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.ready);
         }
-        const uint32_t tS = tmem + lofs + C::S + half * NC;
+        const uint32_t tS = tmem + lofs + C::S + half * NC, tDP = tmem + lofs + C::DP + half * NC;
         float* scratch = sScratch + warp * P.scratch_rows * 33;
         float far_lo = 0.f, far_hi = 0.f;
         for (int j = 0; j < nt && ok; ++j) {
-            const int buf = C::kDp == 2 ? j & 1 : 0;
-            const uint32_t tDP = tmem + lofs + C::DP + buf * kTile + half * NC;
             // relative position of the warp's first row and column
             const int64_t rel0 =
                 a.table ? step_key<KT>(P.kt, b, j) + half * NC - first - quarter * 32 : (int64_t)0;
-            if (!(ok = warp_wait(&bar.sfull, j & 1, a.err, ERR_TIMEOUT_EPILOGUE))) break;
+            if (!(ok = warp_wait(&bar.sfull[half], j & 1, a.err, ERR_TIMEOUT_EPILOGUE))) break;
             tc_fence_after();
             float v[NC];
 #pragma unroll
@@ -441,7 +440,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
             tmem_reg_fence(v);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.sfree);
+            if (lane == 0) mbar_arrive(&bar.sfree[half]);
             float mul = a.scale2, add = 0.f;
             int where = 0;                       // -1, 1: every pair beyond -D or D
             if (a.table) {
@@ -466,9 +465,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                 v[c] = ex2(v[c]);
                 v[c + 1] = ex2(v[c + 1]);
             }
-            if (!(ok = warp_wait(&bar.dpfull[buf], C::kDp == 2 ? (j >> 1) & 1 : j & 1, a.err,
-                                 ERR_TIMEOUT_EPILOGUE)))
-                break;
+            if (!(ok = warp_wait(&bar.dpfull[half], j & 1, a.err, ERR_TIMEOUT_EPILOGUE))) break;
             tc_fence_after();
             {
                 float g[NC];
@@ -497,7 +494,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.dsfull);
+                if (lane == 0) mbar_arrive(&bar.dsfull[half]);
             }
             if (a.bias_part) {
                 if (where != 0) {
@@ -529,6 +526,8 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                         float upper = 0.f, lower = 0.f;
                         if (P.scratch_rows == 32)
                             diagonals<32>(v + 32 * q, scratch, lane, upper, lower);
+                        else if (P.scratch_rows == 16)
+                            diagonals<16>(v + 32 * q, scratch, lane, upper, lower);
                         else
                             diagonals<8>(v + 32 * q, scratch, lane, upper, lower);
                         put(rel0 + 32 * q + lane, upper);
@@ -540,9 +539,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
         if (nt > 0 && ok) ok = warp_wait(&bar.done, 0, a.err, ERR_TIMEOUT_EPILOGUE);
         tc_fence_after();
         if (ok) {
-            const int mid = (dsteps * 16 + 31) / 32 * 16;
-            stage_row<BF>(sKV, r, tmem + lofs + C::DQ, half ? mid : 0, half ? dsteps * 16 : mid, a.scale,
-                          nt > 0, true);
+            stage_row<HD, BF>(sKV, r, tmem + lofs + C::DQ, half, dsteps, a.scale, nt > 0, true);
         }
         named_sync(2 + quarter, 64);
         if (ok) {
@@ -639,10 +636,11 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
         if (lane < NS) {
             mbar_init(&bar.empty[lane], 1);
         } else if (lane == NS) {
-            mbar_init(&bar.sfull, 1);
+            mbar_init(&bar.sfull[0], 1);
             mbar_init(&bar.dpfull[0], 1);
             mbar_init(&bar.pfull, kElemWarps);
-            mbar_init(&bar.dsfull, kElemWarps);
+            mbar_init(&bar.dsfull[0], kElemWarps);
+            mbar_init(&bar.dvdone, 1);
             mbar_init(&bar.done, 1);
             mbar_init(&bar.drain, 1);
         }
@@ -717,12 +715,12 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
             Ring rs, rd;      // tiles whose scores, and whose dV and dK, come next: Q at slot, dO at slot + 1
             // K Q^T - lse2 / scale2, V dO^T - delta: the row values are a last product's sums
             const auto scores = [&]() {
-                mma_over_d(tmem + C::S, dK, dR + rs.slot * kTileU, idS, dpairs);
+                mma_over_d<2>(tmem + C::S, dK, dR + rs.slot * kTileU, idS, dpairs);
                 mma_f16(tmem + C::S, dOnes + (128 >> 4), dRow + (rs.slot >> 1) * (kRowBytes >> 4), idR, true);
-                mma_commit(&bar.sfull);
+                mma_commit(&bar.sfull[0]);
             };
             const auto grads = [&]() {
-                mma_over_d(tmem + C::DP, dV, dR + (rs.slot + 1) * kTileU, idS, dpairs);
+                mma_over_d<2>(tmem + C::DP, dV, dR + (rs.slot + 1) * kTileU, idS, dpairs);
                 mma_f16(tmem + C::DP, dOnes, dRow + (rs.slot >> 1) * (kRowBytes >> 4), idR, true);
                 mma_commit(&bar.dpfull[0]);
                 rs.step(2, NS);
@@ -737,12 +735,12 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
                 const bool more = t + 1 < nt;
                 if (!(ok = mma_wait(a.err, &bar.pfull, t & 1))) break;
                 mma_over_tokens(tmem + C::DV, tmem + C::S, dRt + (rd.slot + 1) * kTileU, idD, t > 0, 64);
-                mma_commit(&bar.empty[rd.slot + 1]);
+                mma_commit(more ? &bar.empty[rd.slot + 1] : &bar.dvdone);
                 if (more) {
                     if (!(ok = mma_wait(a.err, &bar.full[rs.slot], rs.phase))) break;
                     scores();
                 }
-                if (!(ok = mma_wait(a.err, &bar.dsfull, t & 1))) break;
+                if (!(ok = mma_wait(a.err, &bar.dsfull[0], t & 1))) break;
                 mma_over_tokens(tmem + C::DK, tmem + C::DP, dRt + rd.slot * kTileU, idD, t > 0, 64);
                 mma_commit(&bar.empty[rd.slot]);
                 rd.step(2, NS);
@@ -772,7 +770,7 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
             }
             // (a warp that gave up still meets the others at the barriers above)
             float v[NC];
-            ok = ok && warp_wait(&bar.sfull, t & 1, a.err, ERR_TIMEOUT_EPILOGUE);
+            ok = ok && warp_wait(&bar.sfull[0], t & 1, a.err, ERR_TIMEOUT_EPILOGUE);
             if (ok) {
                 tc_fence_after();
 #pragma unroll
@@ -833,33 +831,32 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.dsfull);
+                if (lane == 0) mbar_arrive(&bar.dsfull[0]);
             }
             if (++qt == per_head) {
                 qt = 0;
                 ++h;
             }
         }
-        if (nt > 0 && ok) ok = warp_wait(&bar.done, 0, a.err, ERR_TIMEOUT_EPILOGUE);
-        tc_fence_after();
         const uint32_t word = quarter == 0 ? w.x : quarter == 1 ? w.y : quarter == 2 ? w.z : w.w;
         const bool keep = (word >> lane) & 1u;
-        if (ok) {
-            const int mid = (dsteps * 16 + 31) / 32 * 16;
-            const int c0 = half ? mid : 0, c1 = half ? dsteps * 16 : mid;
-            stage_row<BF>(sV, r, tmem + lofs + C::DV, c0, c1, 1.f, nt > 0, keep);
-            stage_row<BF>(sK, r, tmem + lofs + C::DK, c0, c1, a.scale, nt > 0, keep);
-        }
+        const int w0 = j - lane + half * 16, r0 = quarter * 32 + half * 16;
+        if (nt > 0 && ok) ok = warp_wait(&bar.dvdone, 0, a.err, ERR_TIMEOUT_EPILOGUE);
+        tc_fence_after();
+        if (ok) stage_row<HD, BF>(sV, r, tmem + lofs + C::DV, half, dsteps, 1.f, nt > 0, keep);
         named_sync(2 + quarter, 64);
-        if (ok) {
-            const int w0 = j - lane + half * 16, r0 = quarter * 32 + half * 16;
+        if (ok)
             unstage_rows<16>(sV, r0, a.m - w0, a.d,
                              static_cast<uint16_t*>(a.dv.p) + b * a.dv.sb + (int64_t)w0 * a.dv.st + g * a.dv.sh,
                              a.dv.st, P.dv_vec, lane);
+        if (nt > 0 && ok) ok = warp_wait(&bar.done, 0, a.err, ERR_TIMEOUT_EPILOGUE);
+        tc_fence_after();
+        if (ok) stage_row<HD, BF>(sK, r, tmem + lofs + C::DK, half, dsteps, a.scale, nt > 0, keep);
+        named_sync(2 + quarter, 64);
+        if (ok)
             unstage_rows<16>(sK, r0, a.m - w0, a.d,
                              static_cast<uint16_t*>(a.dk.p) + b * a.dk.sb + (int64_t)w0 * a.dk.st + g * a.dk.sh,
                              a.dk.st, P.dk_vec, lane);
-        }
     }
 
     tc_fence_before();
@@ -955,11 +952,13 @@ cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
     cudaError_t e;
     size_t fixed = 1024 + sizeof(GradBars) + sizeof(float) * 2 * kElemWarps + bias +
                    (a.bias_part ? sizeof(float) * kBands * width : 0);
-    // shared memory for the diagonals of ds, 32 rows at a time; 8 where that would leave
-    // fewer than the four tiles in flight that the order of the products needs (wide
-    // heads and distances from about 1500)
+    // shared memory for the diagonals of ds, 32 rows at a time.  16 where that leaves six
+    // tiles in flight instead of four, so that the next key tile has landed in time (batch
+    // 4, 2048 x 2048, 16 heads of 128, distance 128: 453 us for 501); 8 where fewer than
+    // the four are left that the order of the products needs (distances from about 1500)
     const auto scratch = [&](int rows) { return a.bias_part ? sizeof(float) * kElemWarps * rows * 33 : 0; };
-    p.scratch_rows = ring_stages(fixed + scratch(32), Q::kTileBytes) >= 4 ? 32 : 8;
+    const auto stages = [&](int rows) { return ring_stages(fixed + scratch(rows), Q::kTileBytes); };
+    p.scratch_rows = stages(32) >= 6 ? 32 : stages(16) >= 6 ? 16 : stages(32) >= 4 ? 32 : 8;
     fixed += scratch(p.scratch_rows);
     p.stages = 2 * (ring_stages(fixed, Q::kTileBytes) / 2);
     size_t smem = fixed + p.stages * Q::kTileBytes;

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
                     if (!(ok = mma_wait(a.err, &bar.full[rk.slot], rk.phase) &&
                                (j < 0 || mma_wait(a.err, &bar.sfree[t], j & 1))))
                         break;
-                    mma_over_d<C::kChunkBytes>(cS, dQ, dK + rk.slot * kTileU, idS, (dsteps + 1) / 2);
+                    mma_over_d<4, C::kChunkBytes>(cS, dQ, dK + rk.slot * kTileU, idS, (dsteps + 3) / 4);
                     mma_commit(&bar.sfull[t]);
                     mma_commit(&bar.empty[rk.slot]);
                     rk.step(2, NS);

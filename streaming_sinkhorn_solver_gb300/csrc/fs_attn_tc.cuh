@@ -122,32 +122,34 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
 }
 
 // D[tmem] = A * B^T over the d elements of a 128-token tile (A) and a tile of
-// B_CHUNK / 128 tokens (B), in chunks of 64, both zero beyond d; `pairs` times two
-// products of 16 elements (the issuing thread takes 80 cycles for one product a turn
-// of the loop, more than the products themselves).  One elected thread.  (The count is
-// a loop bound, not a condition around each product: products under a data-dependent
-// condition ended in illegal accesses.)
-template <int B_CHUNK = CHUNK_BYTES>
+// B_CHUNK / 128 tokens (B), in chunks of 64, both zero beyond d; `turns` times U products
+// of 16 elements.  The issuing thread takes 80 cycles for a product a turn, 45 with two,
+// 32 with four: with U = 4 the forward pass of heads of 128 takes 120 us for 128 (U = 1)
+// and 124 (U = 2), of heads of 80 114 for 120, although it adds zeros there.  U = 2 where
+// a product takes longer than that anyway.  One elected thread.  (The count is a loop
+// bound, not a condition around each product: products under a data-dependent condition
+// ended in illegal accesses.)
+template <int U, int B_CHUNK = CHUNK_BYTES>
 __device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                           int pairs) {
+                                           int turns) {
 #pragma unroll 1
-    for (int x = 0; x < pairs; ++x) {
-        const uint64_t da = a + (uint64_t)((x >> 1) * (CHUNK_BYTES >> 4) + 4 * (x & 1));
-        const uint64_t db = b + (uint64_t)((x >> 1) * (B_CHUNK >> 4) + 4 * (x & 1));
-        mma_f16(d_tmem, da, db, idesc, x != 0);
-        mma_f16(d_tmem, da + 2, db + 2, idesc, true);
+    for (int x = 0; x < turns; ++x) {
+        const int chunk = x * U / 4, step = x * U % 4;
+        const uint64_t da = a + (uint64_t)(chunk * (CHUNK_BYTES >> 4) + 2 * step);
+        const uint64_t db = b + (uint64_t)(chunk * (B_CHUNK >> 4) + 2 * step);
+#pragma unroll
+        for (int y = 0; y < U; ++y) mma_f16(d_tmem, da + 2 * y, db + 2 * y, idesc, x != 0 || y != 0);
     }
 }
-// the same with A in TMEM
-template <int B_CHUNK>
+// the same with A in TMEM, a chunk of 64 a turn
 __device__ __forceinline__ void mma_over_d_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                              int pairs) {
+                                              int chunks) {
 #pragma unroll 1
-    for (int x = 0; x < pairs; ++x) {
-        const uint64_t db = b + (uint64_t)((x >> 1) * (B_CHUNK >> 4) + 4 * (x & 1));
-        mma_f16_ts(d_tmem, a_tmem + 16 * x, db, idesc, x != 0);
-        mma_f16_ts(d_tmem, a_tmem + 16 * x + 8, db + 2, idesc, true);
-    }
+    for (int x = 0; x < chunks; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            mma_f16_ts(d_tmem, a_tmem + 32 * x + 8 * y, b + (uint64_t)(x * (CHUNK_BYTES >> 4) + 2 * y), idesc,
+                       x != 0 || y != 0);
 }
 // D[tmem] (+)= A[tmem] * B over the KEYS tokens of B's tile; tokens 64 and on of A are
 // `half` columns from its first.  One elected thread.

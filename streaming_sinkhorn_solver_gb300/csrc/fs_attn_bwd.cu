@@ -357,16 +357,26 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                 uint64_t* const done_with = &bar.empty[r.slot];
                 r.step(2, NS);
                 // (copies that have long landed are waited for before the warps)
-                if (more && !(ok = mma_wait(a.err, &kbar[r.slot], r.phase) &&
-                                   mma_wait(a.err, &bar.full[r.slot + 1], r.phase)))
-                    break;
+                bool seen = false;
+                if (more) {
+                    const bool k_seen = mbar_test(&kbar[r.slot], r.phase);
+                    const bool v_seen = mbar_test(&bar.full[r.slot + 1], r.phase);
+                    seen = mbar_test(&bar.sfree[0], j & 1);
+                    ok = (k_seen || mma_wait(a.err, &kbar[r.slot], r.phase)) &&
+                         (v_seen || mma_wait(a.err, &bar.full[r.slot + 1], r.phase));
+                    if (!ok) break;
+                }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     if (more) {      // scores of the next tile, once this one's are in registers
-                        if (!(ok = mma_wait(a.err, &bar.sfree[u], j & 1))) break;
+                        if (!(ok = seen || mma_wait(a.err, &bar.sfree[u], j & 1))) break;
+                        tc_fence_after();
                         scores(u);
                     }
-                    if (!(ok = mma_wait(a.err, &bar.dsfull[u], j & 1))) break;
+                    const bool ds_seen = mbar_test(&bar.dsfull[u], j & 1);
+                    seen = u == 0 && more && mbar_test(&bar.sfree[1], j & 1);
+                    if (!(ok = ds_seen || mma_wait(a.err, &bar.dsfull[u], j & 1))) break;
+                    tc_fence_after();
                     mma_over_tokens<NC>(tmem + C::DQ, tmem + C::DP + u * NC, dTile + u * kHalfU, idQ,
                                         j > 0 || u > 0, 0);
                     if (u) mma_commit(done_with);
@@ -441,6 +451,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.sfree[half]);
+            const bool dp_seen = mbar_test(&bar.dpfull[half], j & 1);
             float mul = a.scale2, add = 0.f;
             int where = 0;                       // -1, 1: every pair beyond -D or D
             if (a.table) {
@@ -465,7 +476,9 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                 v[c] = ex2(v[c]);
                 v[c + 1] = ex2(v[c + 1]);
             }
-            if (!(ok = warp_wait(&bar.dpfull[half], j & 1, a.err, ERR_TIMEOUT_EPILOGUE))) break;
+            if (!(ok = __all_sync(0xffffffffu, dp_seen) ||
+                       warp_wait(&bar.dpfull[half], j & 1, a.err, ERR_TIMEOUT_EPILOGUE)))
+                break;
             tc_fence_after();
             {
                 float g[NC];
@@ -733,11 +746,15 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
             if (ok) grads();
             for (int t = 0; t < nt && ok; ++t) {
                 const bool more = t + 1 < nt;
-                if (!(ok = mma_wait(a.err, &bar.pfull, t & 1))) break;
+                const bool p_seen = mbar_test(&bar.pfull, t & 1);
+                const bool q_seen = more && mbar_test(&bar.full[rs.slot], rs.phase);
+                const bool do_seen = more && mbar_test(&bar.full[rs.slot + 1], rs.phase);
+                if (!(ok = p_seen || mma_wait(a.err, &bar.pfull, t & 1))) break;
+                tc_fence_after();
                 mma_over_tokens(tmem + C::DV, tmem + C::S, dRt + (rd.slot + 1) * kTileU, idD, t > 0, 64);
                 mma_commit(more ? &bar.empty[rd.slot + 1] : &bar.dvdone);
                 if (more) {
-                    if (!(ok = mma_wait(a.err, &bar.full[rs.slot], rs.phase))) break;
+                    if (!(ok = q_seen || mma_wait(a.err, &bar.full[rs.slot], rs.phase))) break;
                     scores();
                 }
                 if (!(ok = mma_wait(a.err, &bar.dsfull[0], t & 1))) break;
@@ -745,7 +762,7 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
                 mma_commit(&bar.empty[rd.slot]);
                 rd.step(2, NS);
                 if (more) {
-                    if (!(ok = mma_wait(a.err, &bar.full[rs.slot + 1], rs.phase))) break;
+                    if (!(ok = do_seen || mma_wait(a.err, &bar.full[rs.slot + 1], rs.phase))) break;
                     grads();
                 }
             }

@@ -724,7 +724,8 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
             const uint64_t dK = sdesc_sw128(smem_u32(sK)), dV = sdesc_sw128(smem_u32(sV));
             const uint64_t dR = sdesc_sw128(smem_u32(sR)), dRt = sdesc_tokens(smem_u32(sR));
             const uint32_t idR = idesc_16(true, kTile, false);
-            const uint64_t dRow = sdesc_flat(smem_u32(sRow), 256), dOnes = sdesc_flat(smem_u32(sOnes), 384);
+            const uint64_t dRow = sdesc_flat(smem_u32(sRow), 128, 256);
+            const uint64_t dOnes = sdesc_flat(smem_u32(sOnes), 128, 384);
             Ring rs, rd;      // tiles whose scores, and whose dV and dK, come next: Q at slot, dO at slot + 1
             // K Q^T - lse2 / scale2, V dO^T - delta: the row values are a last product's sums
             const auto scores = [&]() {

@@ -54,15 +54,18 @@ struct Fwd {
 };
 
 struct FwdBars {
-    uint64_t full[8], empty[8], clean[8];
+    uint64_t full[8], empty[8], clean[8], last[2];
     uint64_t qfull, sfull[2], sfree[2], pfull[2][2], pfree[2][2], drain[2];
     uint32_t tmem, pad;
 };
 template <int HD>
-constexpr size_t kFwdFixed =
-    1024 + 2 * (size_t)Fwd<HD>::kQBytes + Fwd<HD>::kStages * (size_t)Fwd<HD>::kTileBytes + sizeof(FwdBars);
+using FwdMask = KeyMask<Fwd<HD>::kKeys, Fwd<HD>::kStages / 2>;
+template <int HD>
+constexpr size_t kFwdFixed = 1024 + 2 * (size_t)Fwd<HD>::kQBytes + Fwd<HD>::kStages * (size_t)Fwd<HD>::kTileBytes +
+                             FwdMask<HD>::kBytes + sizeof(FwdBars);
 
-template <int HD, bool BF>
+// MASK: tiles may hold keys that do not count
+template <int HD, bool BF, bool MASK>
 __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_constant__ FwdArgs P) {
     using C = Fwd<HD>;
     using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
@@ -75,7 +78,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
     const int lane = threadIdx.x & 31;
     uint8_t* sQ = smem;                                  // at the end the rows of out
     uint8_t* sKV = sQ + 2 * C::kQBytes;
-    FwdBars& bar = *reinterpret_cast<FwdBars*>(sKV + NS * C::kTileBytes);
+    const FwdMask<HD> mask{sKV + NS * C::kTileBytes};
+    FwdBars& bar = *reinterpret_cast<FwdBars*>(mask.p + FwdMask<HD>::kBytes);
     float* sBias = reinterpret_cast<float*>(&bar + 1);
 
     int blk = blockIdx.x;
@@ -92,14 +96,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
     const int per = (nt_all + P.splits - 1) / P.splits;
     const int t0 = min(nt_all, split * per);
     const int nt = min(nt_all, t0 + per) - t0;
-    const bool partial_keys = P.kt.words != nullptr || end < a.m;
     const int dsteps = (a.d + 15) >> 4;
+    // Tiles with keys that do not count are waited for at their cleaning.  Under a mask
+    // any tile may be one; else the one that the keys end in, whose copies have barriers
+    // of their own (the cleaning warp then follows no other tile's).
+    const bool every = MASK && P.kt.words;
+    const int tail = MASK && !every && (t0 + nt) * KT > end ? nt - 1 : nt;
 
     // The loading warp's barriers are its own until the block meets below: it starts
     // its copies before that.
     if (warp == kLoad) {
         if (lane < NS) mbar_init(&bar.full[lane], 1);
         if (lane == NS) mbar_init(&bar.qfull, 1);
+        if (lane > NS && lane <= NS + 2) mbar_init(&bar.last[lane - NS - 1], 1);
         fence_mbar_init();
         __syncwarp();
     } else if (warp == kClean) {
@@ -121,13 +130,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
     if (warp == kMma0) tmem_alloc(&bar.tmem, 512);
     // the copy of step it (K and V in turn) into its slot
     const auto load = [&](int it, int slot) {
+        uint64_t* const full = (it >> 1) == tail ? &bar.last[it & 1] : &bar.full[slot];
         const int g = h / a.R;
         const int key = step_key<KT>(P.kt, b, t0 + (it >> 1));
         const TensorMap& src = it & 1 ? P.v : P.k;
-        mbar_arrive_expect_tx(&bar.full[slot], C::kTileBytes);
+        mbar_arrive_expect_tx(full, C::kTileBytes);
         for (int c = 0; c < C::kChunks; ++c)
             tma_load(sKV + slot * C::kTileBytes + c * C::kChunkBytes, &src.map, c * 64, key, g * src.head,
-                     b * src.batch, &bar.full[slot]);
+                     b * src.batch, full);
     };
     const int early = min(2 * nt, NS);     // copies that need no free slot
     if (warp == kLoad && nt > 0 && elect_one()) {
@@ -144,6 +154,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
         for (int e = threadIdx.x; e < 2 * (a.D + kSlack) + 1; e += kFwdThreads)
             sBias[e] = bias2(to_f<T>(row[bucket_of(a, (int64_t)e - a.D - kSlack)]));
     }
+    if (MASK) mask.init(threadIdx.x, kFwdThreads);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -168,7 +179,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
                 mbar_wait(&bar.qfull, 0, a.err, ERR_TIMEOUT_PRODUCER);
                 Ring l;
                 for (int it = 0; it < issued; ++it) {
-                    if (it + NS >= issued)
+                    if ((it >> 1) == tail)
+                        mbar_wait(&bar.last[it & 1], 0, a.err, ERR_TIMEOUT_PRODUCER);
+                    else if (it + NS >= issued)
                         mbar_wait(&bar.full[l.slot], l.phase, a.err, ERR_TIMEOUT_PRODUCER);
                     l.step(1, NS);
                 }
@@ -177,30 +190,41 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
     } else if (warp == kMma0 || warp == kMma0 + 1) {
         const int t = warp - kMma0;
         if (nt > 0 && (t == 0 || two) && elect_one()) {
-            const uint32_t idS = idesc_16(BF, KT, false);
+            const uint32_t idS = idesc_16(BF, KT, false), idM = idesc_16(true, KT, false);
             const uint32_t idO = idesc_16(BF, dsteps * 16, true);
             constexpr uint64_t kTileU = C::kTileBytes >> 4;    // descriptors count 16 bytes
             const uint64_t dQ = sdesc_sw128(smem_u32(sQ)) + t * (C::kQBytes >> 4);
             const uint64_t dK = sdesc_sw128(smem_u32(sKV));
             const uint64_t dV = sdesc_tokens(smem_u32(sKV), C::kChunkBytes);
             const uint32_t cS = tmem + C::S(t), cP = tmem + C::P(t), cO = tmem + C::O(t);
-            uint64_t* vbar = partial_keys ? bar.clean : bar.full;
+            uint64_t* const kvbar = every ? bar.clean : bar.full;
+            const auto landed = [&](const Ring& r, int j) {
+                return mma_wait(a.err, (MASK && j == tail ? bar.clean : kvbar) + r.slot,
+                                MASK && j == tail ? 0 : r.phase);
+            };
+            const uint64_t dOnes = mask.ones(), dMask = mask.tile(0);
             Ring rk, rv;
             rv.step(1, NS);
             bool ok = mma_wait(a.err, &bar.qfull, 0);
             for (int j = -1; j < nt && ok; ++j) {
                 if (j + 1 < nt) {
-                    if (!(ok = mma_wait(a.err, &bar.full[rk.slot], rk.phase) &&
+                    if (!(ok = landed(rk, j + 1) &&
                                (j < 0 || mma_wait(a.err, &bar.sfree[t], j & 1))))
                         break;
                     mma_over_d<4, C::kChunkBytes>(cS, dQ, dK + rk.slot * kTileU, idS, (dsteps + 3) / 4);
+                    if (MASK) {
+                        const uint64_t dTile = dMask + (rk.slot >> 1) * FwdMask<HD>::kStep;
+                        const int times = every || j + 1 == tail;     // a loop bound, as above
+#pragma unroll 1
+                        for (int x = 0; x < times; ++x) mma_f16(cS, dOnes, dTile, idM, true);
+                    }
                     mma_commit(&bar.sfull[t]);
                     mma_commit(&bar.empty[rk.slot]);
                     rk.step(2, NS);
                 }
                 if (j < 0) continue;
                 const int buf = C::kPBufs == 2 ? j & 1 : 0;
-                if (!(ok = mma_wait(a.err, &vbar[rv.slot], rv.phase) &&
+                if (!(ok = landed(rv, j) &&
                            mma_wait(a.err, &bar.pfull[t][buf], C::kPBufs == 2 ? (j >> 1) & 1 : j & 1)))
                     break;
                 mma_over_tokens<KT>(cO, cP + buf * C::kPCols, dV + rv.slot * kTileU, idO, j > 0, 32);
@@ -212,19 +236,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
             mbar_wait(&bar.drain[t], 0, a.err, ERR_TIMEOUT_MMA);
         }
     } else if (warp == kClean) {
-        if (partial_keys) {
+        if (MASK && nt > 0) {
+            const int j0 = every ? 0 : tail;
             Ring r;
-            r.step(1, NS);
-            for (int j = 0; j < nt; ++j) {
-                const KeyBits<KT> w(P.kt, b, t0 + j, end);
-                if (!warp_wait(&bar.full[r.slot], r.phase, a.err, ERR_TIMEOUT_PRODUCER)) break;
-                if (!w.all()) {
+            r.slot = 2 * j0 % NS;
+            bool ok = true;
+            KeyBits<KT> next(P.kt, b, t0 + min(j0, nt - 1), end);
+            for (int j = j0; j < nt && ok; ++j) {
+                const KeyBits<KT> w = next;
+                if (j + 1 < nt) next = KeyBits<KT>(P.kt, b, t0 + j + 1, end);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    ok = ok && warp_wait(every ? &bar.full[r.slot] : &bar.last[kv], r.phase, a.err,
+                                         ERR_TIMEOUT_PRODUCER);
+                    if (!ok) break;
+                    if (!kv) mask.write(r.slot >> 1, w, lane);
                     clear_rows(sKV + r.slot * C::kTileBytes, C::kChunks, C::kChunkBytes, w, lane);
                     fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.clean[r.slot]);
+                    r.step(1, NS);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.clean[r.slot]);
-                r.step(2, NS);
             }
         }
     } else {
@@ -264,12 +296,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
                         for (int c = 0; c < KT; ++c) v[c] = fmaf(v[c], mul, e[c]);
                         mul = 1.f;
                     }
-                }
-                if (P.kt.words || (t0 + j + 1) * KT > end) {
-                    const KeyBits<KT> w(P.kt, b, t0 + j, end);
-#pragma unroll
-                    for (int c = 0; c < KT; ++c)
-                        if (!((w.w[c >> 5] >> (c & 31)) & 1u)) v[c] = -INFINITY;
                 }
                 float m[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
@@ -401,17 +427,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
     }
 }
 
-template <int HD, bool BF>
-cudaError_t launch_forward(const FwdArgs& p, cudaStream_t s) {
+template <int HD, bool BF, bool MASK>
+cudaError_t launch_masked(const FwdArgs& p, cudaStream_t s) {
     const size_t bias = p.a.table ? sizeof(float) * (2 * (size_t)(p.a.D + kSlack) + 1) : 0;
     constexpr size_t most = kFwdFixed<HD> + sizeof(float) * (2 * (size_t)(kMaxDistance + kSlack) + 1);
     static_assert(most <= kSmemLimit, "forward kernel does not fit in shared memory");
     static std::atomic<uint64_t> ready{0};    // devices whose shared-memory limit is raised
-    if (cudaError_t e = raise_smem(k_forward_tc<HD, BF>, most, ready); e != cudaSuccess) return e;
+    if (cudaError_t e = raise_smem(k_forward_tc<HD, BF, MASK>, most, ready); e != cudaSuccess) return e;
     const unsigned blocks = (unsigned)((int64_t)p.row_blocks * p.a.H * p.a.B * p.splits);
-    k_forward_tc<HD, BF><<<blocks, kFwdThreads, kFwdFixed<HD> + bias, s>>>(p);
+    k_forward_tc<HD, BF, MASK><<<blocks, kFwdThreads, kFwdFixed<HD> + bias, s>>>(p);
     count_launch();
     return cudaGetLastError();
+}
+
+template <int HD, bool BF>
+cudaError_t launch_forward(const FwdArgs& p, cudaStream_t s) {
+    const bool whole = !p.kt.words && !p.a.kv_len && p.a.m % Fwd<HD>::kKeys == 0;
+    return whole ? launch_masked<HD, BF, false>(p, s) : launch_masked<HD, BF, true>(p, s);
 }
 
 }  // namespace

@@ -104,11 +104,11 @@ __device__ __forceinline__ uint64_t sdesc_tokens(uint32_t saddr, uint32_t chunk_
 }
 
 // Operand of 16 elements a row without swizzle: 8 x 8 element blocks of 128 bytes
-// (rows of 16 bytes), the two of a row group 128 bytes apart, row groups `group` bytes.
-__device__ __forceinline__ uint64_t sdesc_flat(uint32_t saddr, uint32_t group) {
+// (rows of 16 bytes), the two of a row group `second` bytes apart, row groups `group`.
+__device__ __forceinline__ uint64_t sdesc_flat(uint32_t saddr, uint32_t second, uint32_t group) {
     uint64_t d = 0;
     d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(128 >> 4) << 16;
+    d |= (uint64_t)(second >> 4) << 16;
     d |= (uint64_t)(group >> 4) << 32;
     d |= (uint64_t)1 << 46;
     return d;
@@ -328,20 +328,56 @@ struct KeyBits {
 template <int KT>
 __device__ __forceinline__ void clear_rows(uint8_t* tile, int chunks, int chunk_bytes, const KeyBits<KT>& w,
                                            int lane) {
+    // 8 lanes clear a 128-byte row, stores under a predicate (branches take four times as long)
+    const uint32_t at = smem_u32(tile) + (lane >> 3) * 128 + (lane & 7) * 16;
 #pragma unroll
     for (int k = 0; k < KT / 32; ++k) {
-        uint32_t gone = ~w.w[k];
-        while (gone) {
-            const int r = 32 * k + __ffs(gone) - 1;
-            gone &= gone - 1;
-            // 8 lanes clear a 128-byte row; up to 4 chunks at a time
-            const int c = lane >> 3;
-            if (c < chunks)
-                *reinterpret_cast<uint4*>(tile + c * chunk_bytes + r * 128 + (lane & 7) * 16) =
-                    make_uint4(0, 0, 0, 0);
+        if (w.w[k] == 0xffffffffu) continue;
+        const uint32_t bits = w.w[k] >> (lane >> 3);
+        for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+            for (int r4 = 0; r4 < 32; r4 += 4)
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %0, 0;\n\t"
+                    "@p st.shared.v4.u32 [%1], {%2, %2, %2, %2};\n\t}" ::"r"((bits >> r4) & 1u),
+                    "r"(at + c * chunk_bytes + (32 * k + r4) * 128), "r"(0)
+                    : "memory");
         }
     }
 }
+
+// A tile's mask as an operand: a product with it adds -inf to the scores of the keys
+// that do not count, so the softmax has no test per score (batch 4, 2048 x 2048, 16 heads
+// with 3 % of the keys masked: 100 us for 125 with heads of 64, 135 for 157 with 128).  Rows of 16 elements, bfloat16 whatever
+// the type: 0 or -inf, then zeros; the second half of every row is one block of zeros
+// that all tiles share.  The other operand has ones in the first column.
+template <int KT, int TILES>
+struct KeyMask {
+    static constexpr int kTileBytes = KT * 16, kOnes = TILES * kTileBytes, kZeros = kOnes + kTile * 16;
+    static constexpr int kBytes = kZeros + kTile * 16;
+    uint8_t* p;
+    // every thread of the block, before it meets
+    __device__ __forceinline__ void init(int t, int threads) const {
+        for (int e = t; e < 2 * kTile; e += threads)
+            reinterpret_cast<uint4*>(p + kOnes)[e] = make_uint4(e < kTile ? 0x3f80u : 0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+    }
+    // One whole warp, before the fence and the arrival that publish the tile
+    __device__ __forceinline__ void write(int slot, const KeyBits<KT>& w, int lane) const {
+#pragma unroll
+        for (int k = 0; k < KT / 32; ++k)
+            reinterpret_cast<uint4*>(p + slot * kTileBytes)[32 * k + lane] =
+                make_uint4((w.w[k] >> lane) & 1u ? 0u : 0xff80u, 0u, 0u, 0u);
+    }
+    // descriptors of the ones and of a tile's mask, kStep more from a tile to the next
+    static constexpr uint64_t kStep = (uint64_t)(kTileBytes >> 4) - ((uint64_t)(kTileBytes >> 4) << 16);
+    __device__ __forceinline__ uint64_t ones() const {
+        return sdesc_flat(smem_u32(p) + kOnes, kZeros - kOnes, 128);
+    }
+    __device__ __forceinline__ uint64_t tile(int slot) const {
+        return sdesc_flat(smem_u32(p), kZeros, 128) + slot * kStep;
+    }
+};
 
 }  // namespace attn
 }  // namespace fs

@@ -23,8 +23,8 @@ fs_status check_desc(const fs_attention* a) {
         a->m > kMaxTokens)
         return fail(FS_ERR_INVALID_ARG, "batch=%lld n=%lld m=%lld out of range [0, %lld]",
                     (long long)a->batch, (long long)a->n, (long long)a->m, (long long)kMaxTokens);
-    if (!(a->scale > 0.f) || !std::isfinite(a->scale))
-        return fail(FS_ERR_INVALID_ARG, "scale must be positive and finite (got %g)",
+    if (!(a->scale > 0.f) || !std::isfinite((float)(a->scale * kLog2e)))
+        return fail(FS_ERR_INVALID_ARG, "scale must be positive and finite in base 2 (got %g)",
                     (double)a->scale);
     if (a->reserved) return fail(FS_ERR_INVALID_ARG, "fs_attention.reserved must be zero");
     if (a->n_buckets < 0 || a->n_buckets > kMaxBuckets)
@@ -43,8 +43,8 @@ fs_status check_desc(const fs_attention* a) {
     return FS_OK;
 }
 
-// a device array of the current device (empty tensors may be null)
-fs_status check_ptr(const void* p, int64_t count, const char* name) {
+// a device array of device dev, the current one (empty tensors may be null)
+fs_status check_ptr(int dev, const void* p, int64_t count, const char* name) {
     if (count == 0) return FS_OK;
     if (!p) return fail(FS_ERR_INVALID_ARG, "null %s", name);
     cudaPointerAttributes attr;
@@ -54,12 +54,14 @@ fs_status check_ptr(const void* p, int64_t count, const char* name) {
     }
     if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged)
         return fail(FS_ERR_INVALID_ARG, "%s must be device memory", name);
+    if (attr.type == cudaMemoryTypeDevice && attr.device != dev)
+        return fail(FS_ERR_INVALID_ARG, "%s on device %d, current is %d", name, attr.device, dev);
     return FS_OK;
 }
 
-fs_status view(View& w, const void* p, const int64_t* stride, int64_t batch, int64_t tokens,
+fs_status view(int dev, View& w, const void* p, const int64_t* stride, int64_t batch, int64_t tokens,
                int heads, int d, bool out, const char* name) {
-    FS_TRY(check_ptr(p, batch * tokens, name));
+    FS_TRY(check_ptr(dev, p, batch * tokens, name));
     w.p = const_cast<void*>(p);
     w.sb = stride[0];
     w.st = stride[1];
@@ -73,7 +75,7 @@ fs_status view(View& w, const void* p, const int64_t* stride, int64_t batch, int
     return FS_OK;
 }
 
-fs_status fill(Args& w, const fs_attention* a) {
+fs_status fill(int dev, Args& w, const fs_attention* a) {
     w.B = (int)a->batch;
     w.H = a->heads;
     w.G = a->kv_heads;
@@ -84,15 +86,15 @@ fs_status fill(Args& w, const fs_attention* a) {
     w.bf16 = a->dtype == FS_DTYPE_BF16;
     w.scale = a->scale;
     w.scale2 = (float)((double)a->scale * kLog2e);
-    FS_TRY(check_ptr(a->kv_len, a->kv_len ? a->batch : 0, "kv_len"));
-    FS_TRY(check_ptr(a->key_mask, a->key_mask ? a->batch * a->m : 0, "key_mask"));
-    FS_TRY(check_ptr(a->q_pos, a->q_pos ? a->batch : 0, "q_pos"));
+    FS_TRY(check_ptr(dev, a->kv_len, a->kv_len ? a->batch : 0, "kv_len"));
+    FS_TRY(check_ptr(dev, a->key_mask, a->key_mask ? a->batch * a->m : 0, "key_mask"));
+    FS_TRY(check_ptr(dev, a->q_pos, a->q_pos ? a->batch : 0, "q_pos"));
     w.kv_len = a->kv_len;
     w.mask = a->key_mask;
     w.mask_stride = a->mask_stride;
     if (a->n_buckets) {
-        FS_TRY(check_ptr(a->bias, 1, "bias"));
-        FS_TRY(check_ptr(a->bias_buckets, 1, "bias_buckets"));
+        FS_TRY(check_ptr(dev, a->bias, 1, "bias"));
+        FS_TRY(check_ptr(dev, a->bias_buckets, 1, "bias_buckets"));
         w.table = a->bias;
         w.table_stride = a->bias_stride;
         w.buckets = a->bias_buckets;
@@ -213,12 +215,14 @@ fs_status forward_entry(const fs_attention* at, const void* q, const void* k, co
     FS_TRY(check_desc(at));
     FwdArgs p = {};
     Args& a = p.a;
-    FS_TRY(fill(a, at));
-    FS_TRY(view(a.q, q, at->q_stride, at->batch, at->n, a.H, a.d, false, "q"));
-    FS_TRY(view(a.k, k, at->k_stride, at->batch, at->m, a.G, a.d, false, "k"));
-    FS_TRY(view(a.v, v, at->v_stride, at->batch, at->m, a.G, a.d, false, "v"));
-    FS_TRY(view(a.o, out, at->out_stride, at->batch, at->n, a.H, a.d, true, "out"));
-    FS_TRY(check_ptr(lse, at->batch * at->n, "lse"));
+    int dev = 0;
+    FS_CUDA(cudaGetDevice(&dev));
+    FS_TRY(fill(dev, a, at));
+    FS_TRY(view(dev, a.q, q, at->q_stride, at->batch, at->n, a.H, a.d, false, "q"));
+    FS_TRY(view(dev, a.k, k, at->k_stride, at->batch, at->m, a.G, a.d, false, "k"));
+    FS_TRY(view(dev, a.v, v, at->v_stride, at->batch, at->m, a.G, a.d, false, "v"));
+    FS_TRY(view(dev, a.o, out, at->out_stride, at->batch, at->n, a.H, a.d, true, "out"));
+    FS_TRY(check_ptr(dev, lse, at->batch * at->n, "lse"));
     a.lse = lse;
     FS_TRY(check_tiles((double)at->batch * a.H * at->n));
     FS_TRY(check_tiles((double)at->batch * a.G * at->m));
@@ -231,8 +235,7 @@ fs_status forward_entry(const fs_attention* at, const void* q, const void* k, co
         FS_CUDA(launch_zero(a, a.o, a.n, a.H, lse, c.stream));
         return FS_OK;
     }
-    int dev = 0, sms = 0;
-    FS_CUDA(cudaGetDevice(&dev));
+    int sms = 0;
     FS_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     Input inputs[3] = {{a.q, a.n, a.H}, {a.k, a.m, a.G}, {a.v, a.m, a.G}};
     const bool few = few_rows(a);
@@ -295,18 +298,20 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     FS_TRY(check_desc(at));
     GradArgs p = {};
     Args& a = p.a;
-    FS_TRY(fill(a, at));
-    FS_TRY(view(a.q, q, at->q_stride, at->batch, at->n, a.H, a.d, false, "q"));
-    FS_TRY(view(a.k, k, at->k_stride, at->batch, at->m, a.G, a.d, false, "k"));
-    FS_TRY(view(a.v, v, at->v_stride, at->batch, at->m, a.G, a.d, false, "v"));
-    FS_TRY(view(a.o, out, at->out_stride, at->batch, at->n, a.H, a.d, false, "out"));
-    FS_TRY(view(a.dout, dout, at->dout_stride, at->batch, at->n, a.H, a.d, false, "dout"));
-    FS_TRY(view(a.dq, dq, at->dq_stride, at->batch, at->n, a.H, a.d, true, "dq"));
-    FS_TRY(view(a.dk, dk, at->dk_stride, at->batch, at->m, a.G, a.d, true, "dk"));
-    FS_TRY(view(a.dv, dv, at->dv_stride, at->batch, at->m, a.G, a.d, true, "dv"));
-    FS_TRY(check_ptr(lse, at->batch * at->n, "lse"));
+    int dev = 0;
+    FS_CUDA(cudaGetDevice(&dev));
+    FS_TRY(fill(dev, a, at));
+    FS_TRY(view(dev, a.q, q, at->q_stride, at->batch, at->n, a.H, a.d, false, "q"));
+    FS_TRY(view(dev, a.k, k, at->k_stride, at->batch, at->m, a.G, a.d, false, "k"));
+    FS_TRY(view(dev, a.v, v, at->v_stride, at->batch, at->m, a.G, a.d, false, "v"));
+    FS_TRY(view(dev, a.o, out, at->out_stride, at->batch, at->n, a.H, a.d, false, "out"));
+    FS_TRY(view(dev, a.dout, dout, at->dout_stride, at->batch, at->n, a.H, a.d, false, "dout"));
+    FS_TRY(view(dev, a.dq, dq, at->dq_stride, at->batch, at->n, a.H, a.d, true, "dq"));
+    FS_TRY(view(dev, a.dk, dk, at->dk_stride, at->batch, at->m, a.G, a.d, true, "dk"));
+    FS_TRY(view(dev, a.dv, dv, at->dv_stride, at->batch, at->m, a.G, a.d, true, "dv"));
+    FS_TRY(check_ptr(dev, lse, at->batch * at->n, "lse"));
     if (dbias && !at->n_buckets) return fail(FS_ERR_INVALID_ARG, "dbias without a bias");
-    if (dbias) FS_TRY(check_ptr(dbias, 1, "dbias"));
+    if (dbias) FS_TRY(check_ptr(dev, dbias, 1, "dbias"));
     a.lse = const_cast<float*>(lse);
     FS_TRY(check_tiles((double)at->batch * a.H * at->n));
     FS_TRY(check_tiles((double)at->batch * a.G * at->m));

@@ -92,20 +92,24 @@ __device__ __forceinline__ void fill_bias(const Args& a, int h, float* sBias, in
 template <int ROWS>
 __device__ __forceinline__ void diagonals(const float* v, float* scratch, int lane, float& upper,
                                           float& lower) {
-#pragma unroll
+#pragma unroll 1
     for (int s0 = 0; s0 < 32; s0 += ROWS) {
         if (ROWS == 32 || lane / ROWS == s0 / ROWS) {
 #pragma unroll
             for (int c = 0; c < 32; ++c) scratch[(lane - s0) * 33 + c] = v[c];
         }
         __syncwarp();
+#pragma unroll 1
+        for (int t = 0; t < ROWS; t += 8) {
 #pragma unroll
-        for (int s = s0; s < s0 + ROWS; ++s) {
-            const float x = scratch[(s - s0) * 33 + ((s + lane) & 31)];
-            if (s + lane < 32)
-                upper += x;
-            else
-                lower += x;
+            for (int u = 0; u < 8; ++u) {
+                const int c = s0 + t + u + lane;
+                const float x = scratch[(t + u) * 33 + (c & 31)];
+                if (c < 32)
+                    upper += x;
+                else
+                    lower += x;
+            }
         }
         __syncwarp();
     }
@@ -522,30 +526,37 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                     else
                         far_lo += s0 + s1;
                 } else {
-                    // A diagonal of these 32 rows meets two 32 x 32 blocks at most, so no entry of
-                    // the sums gets more than two terms and the order of the additions does
-                    // not matter.
-                    float* sums = sSums + quarter * width;
-                    const auto put = [&](int64_t rel, float x) {
+                    // upper[q] and lower[q] of lane l are at relative position rel0 + 32 q + l and
+                    // 32 less.  A diagonal of these 32 rows meets two 32 x 32 blocks at most, so no
+                    // entry of the sums gets more than two terms, and the order of the two
+                    // additions between warps does not matter.
+                    float* sums = sSums + quarter * width + a.D;
+                    const auto put = [&](int rel, float x, bool alone) {
                         if (rel >= a.D)
                             far_hi += x;
                         else if (rel <= -a.D)
                             far_lo += x;
+                        else if (alone)
+                            sums[rel] = x;
                         else
-                            atomicAdd(sums + (int)rel + a.D, x);
+                            atomicAdd(sums + rel, x);
                     };
+                    float upper[NC / 32], lower[NC / 32];
 #pragma unroll
                     for (int q = 0; q < NC / 32; ++q) {
-                        float upper = 0.f, lower = 0.f;
+                        upper[q] = lower[q] = 0.f;
                         if (P.scratch_rows == 32)
-                            diagonals<32>(v + 32 * q, scratch, lane, upper, lower);
+                            diagonals<32>(v + 32 * q, scratch, lane, upper[q], lower[q]);
                         else if (P.scratch_rows == 16)
-                            diagonals<16>(v + 32 * q, scratch, lane, upper, lower);
+                            diagonals<16>(v + 32 * q, scratch, lane, upper[q], lower[q]);
                         else
-                            diagonals<8>(v + 32 * q, scratch, lane, upper, lower);
-                        put(rel0 + 32 * q + lane, upper);
-                        if (lane > 0) put(rel0 + 32 * q + lane - 32, lower);
+                            diagonals<8>(v + 32 * q, scratch, lane, upper[q], lower[q]);
                     }
+                    static_assert(NC == 64, "two blocks a warp");
+                    const int rel = (int)rel0 + lane;
+                    if (lane > 0) put(rel - 32, lower[0], false);
+                    put(rel, upper[0] + lower[1], true);
+                    put(rel + 32, upper[1], lane == 0);
                 }
             }
         }

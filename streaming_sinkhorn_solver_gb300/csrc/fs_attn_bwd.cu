@@ -128,6 +128,22 @@ __device__ __forceinline__ uint4 three_terms(float x) {
     return make_uint4(pack16<true>(hi, mid), pack16<true>(y - mid, 0.f), 0u, 0u);
 }
 
+// -lse2 of a query; a row without a counted key has p = 0, as if its lse were +inf
+__device__ __forceinline__ float row_lse(const Args& a, int b, int h, int64_t i) {
+    const float x = i < a.n ? -a.lse[((int64_t)b * a.H + h) * a.n + i] * (float)kLog2e : -INFINITY;
+    return x == INFINITY ? -INFINITY : x;
+}
+// row values of query r of its tile: x is -lse2, or -delta
+__device__ __forceinline__ void put_row(const Args& a, uint8_t* out, int r, float x, bool is_delta) {
+    reinterpret_cast<float*>(out + kRowBytes)[(is_delta ? kTile : 0) + r] = x;
+    if (!is_delta) {
+        x /= least_scale(a);
+        if (x < -kRowLimit) x = -kRowLimit;
+        if (x > kRowLimit) x = kRowLimit;
+    }
+    *reinterpret_cast<uint4*>(out + (r >> 3) * 256 + (is_delta ? 128 : 0) + (r & 7) * 16) = three_terms(x);
+}
+
 // ---------------------------------------------------------------------------
 // The row values of 128 queries a block: delta_i = dO_i . O_i and lse_i.  Reads dO and O
 // once, LANES lanes of 8 elements to a row; bound by memory.
@@ -186,24 +202,9 @@ __global__ void __launch_bounds__(kRowThreads) k_grad_rows(const __grid_constant
     }
     __syncthreads();
     const int r = threadIdx.x & (kTile - 1);
-    const bool second = threadIdx.x >= kTile;         // -delta, else -lse2
-    const int64_t i = qt * kTile + r;
-    float x;
-    if (second) {
-        x = -sDelta[r];
-    } else {
-        x = i < a.n ? -a.lse[((int64_t)b * a.H + h) * a.n + i] * (float)kLog2e : -INFINITY;
-        // a row without a counted key has p = 0, as if its lse were +inf
-        if (x == INFINITY) x = -INFINITY;
-    }
-    uint8_t* out = P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowStride;
-    reinterpret_cast<float*>(out + kRowBytes)[threadIdx.x] = x;
-    if (!second) {
-        x /= least_scale(a);
-        if (x < -kRowLimit) x = -kRowLimit;
-        if (x > kRowLimit) x = kRowLimit;
-    }
-    *reinterpret_cast<uint4*>(out + (r >> 3) * 256 + (second ? 128 : 0) + (r & 7) * 16) = three_terms(x);
+    const bool second = threadIdx.x >= kTile;
+    put_row(a, P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowStride, r,
+            second ? -sDelta[r] : row_lse(a, b, h, (int64_t)qt * kTile + r), second);
 }
 
 // ---------------------------------------------------------------------------
@@ -220,7 +221,13 @@ struct GradQ {
     static_assert(DO + HD / 2 <= 512, "TMEM");
 };
 
-template <int HD, bool BF>
+// DELTA: no gradients, only the row values, with delta_i = sum_j p_ij dP_ij in float32.
+// With delta from the 16-bit O, sum_j ds_ij is dO_i . (error of O_i) instead of 0, and a
+// bucket that holds nearly all of its rows' weight sums nothing but that: its gradient
+// came out up to 1.2 % off (2-norm of dbias against 64 bits, 0.24 % with this pass).  It
+// costs a quarter of the gradients' time, so only a bias gradient takes it; without one dq
+// and dk are 0.25 % off for 0.17 % of rounding alone.
+template <int HD, bool BF, bool DELTA>
 __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
     using C = GradQ<HD>;
     constexpr int KT = C::kKeys, NC = C::kCols;
@@ -231,12 +238,12 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
     const Args& a = P.a;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int NS = P.stages;                // even: K and V keep their slots
+    const int NS = DELTA ? P.delta_stages : P.stages;                // even: K and V keep their slots
     uint8_t* sKV = smem;                    // at first Q and dO in the last two tiles, at the end dq
     uint8_t* sOwn = sKV + (NS - 2) * C::kTileBytes;
     GradBars& bar = *reinterpret_cast<GradBars*>(sKV + NS * C::kTileBytes);
-    float* sFar = reinterpret_cast<float*>(&bar + 1);            // [8][2]
-    float* sBias = sFar + 2 * kElemWarps;                        // [2 (D + kSlack) + 1]
+    float* sFar = reinterpret_cast<float*>(&bar + 1);            // [8][2], or half sums of delta
+    float* sBias = sFar + (DELTA ? kTile : 2 * kElemWarps);      // [2 (D + kSlack) + 1]
     float* sSums = sBias + (a.table ? 2 * (a.D + kSlack) + 1 : 0);   // [4][2 D + 1]
     float* sScratch = sSums + kBands * (2 * a.D + 1);            // [8][scratch_rows][33], with bias sums
 
@@ -247,7 +254,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
     const int i0 = qt * kTile;
     const int end = key_end(a, b);
     const int nt = step_count<KT>(P.kt, b, end);
-    const bool partial_keys = P.kt.words != nullptr || end < a.m;
+    const bool partial_keys = !DELTA && (P.kt.words != nullptr || end < a.m);
     const int64_t first = (a.q_pos ? (int64_t)__ldg(a.q_pos + b) : 0) + i0;
     const int dsteps = (a.d + 15) >> 4, dchunks = (a.d + 63) >> 6;
     const int width = 2 * a.D + 1;
@@ -295,7 +302,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
         for (int it = 0; it < early; ++it) load(it, it);
     }
     if (a.table) fill_bias<BF>(a, h, sBias, threadIdx.x, kGradThreads);
-    if (a.bias_part)
+    if (!DELTA && a.bias_part)
         for (int e = threadIdx.x; e < kBands * width; e += kGradThreads) sSums[e] = 0.f;
     tc_fence_before();
     __syncthreads();
@@ -339,6 +346,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                 mma_over_d_ts(tmem + C::S + u * NC, tmem + C::Q, dKV + r.slot * kTileU + u * kHalfU,
                                            idS, dchunks);
                 mma_commit(&bar.sfull[u]);
+                if (DELTA && u) mma_commit(&bar.empty[r.slot]);
             };
             const auto grads = [&](int u) {
                 mma_over_d_ts(tmem + C::DP + u * NC, tmem + C::DO,
@@ -381,9 +389,11 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                     seen = u == 0 && more && mbar_test(&bar.sfree[1], j & 1);
                     if (!(ok = ds_seen || mma_wait(a.err, &bar.dsfull[u], j & 1))) break;
                     tc_fence_after();
-                    mma_over_tokens<NC>(tmem + C::DQ, tmem + C::DP + u * NC, dTile + u * kHalfU, idQ,
-                                        j > 0 || u > 0, 0);
-                    if (u) mma_commit(done_with);
+                    if (!DELTA) {
+                        mma_over_tokens<NC>(tmem + C::DQ, tmem + C::DP + u * NC, dTile + u * kHalfU, idQ,
+                                            j > 0 || u > 0, 0);
+                        if (u) mma_commit(done_with);
+                    }
                     if (more) grads(u);
                 }
             }
@@ -411,9 +421,10 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
         const int r = quarter * 32 + lane;
         const int i = i0 + r;
         const uint32_t lofs = (uint32_t)(quarter * 32) << 16;
-        const float* row =
-            reinterpret_cast<const float*>(P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowStride + kRowBytes);
-        const float nlse = row[r], ndelta = row[kTile + r];
+        uint8_t* const values = P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowStride;
+        const float* row = reinterpret_cast<const float*>(values + kRowBytes);
+        const float nlse = DELTA ? row_lse(a, b, h, i) : row[r];
+        const float ndelta = DELTA ? 0.f : row[kTile + r];
         bool ok = true;
         if (nt > 0) {     // operands into TMEM: warps 0..3 the rows of Q, warps 4..7 those of dO
             ok = warp_wait(&bar.own, 0, a.err, ERR_TIMEOUT_EPILOGUE);
@@ -440,7 +451,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
         }
         const uint32_t tS = tmem + lofs + C::S + half * NC, tDP = tmem + lofs + C::DP + half * NC;
         float* scratch = sScratch + warp * P.scratch_rows * 33;
-        float far_lo = 0.f, far_hi = 0.f;
+        float far_lo = 0.f, far_hi = 0.f, total = 0.f;
         for (int j = 0; j < nt && ok; ++j) {
             // relative position of the warp's first row and column
             const int64_t rel0 =
@@ -490,6 +501,11 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                 for (int c = 0; c < NC; c += 32) tmem_ld32(tDP + c, g + c);
                 tmem_wait_ld();
                 tmem_reg_fence(g);
+                if (DELTA) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.dsfull[half]);
+                }
                 const uint64_t nd = pk(ndelta, ndelta);
 #pragma unroll
                 for (int c = 0; c < NC; c += 2)
@@ -503,7 +519,15 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                     if (!((bits >> (c & 31)) & 1u)) v[c] = 0.f;
                 }
             }
-            {
+            if (DELTA) {
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int c = 0; c < NC; c += 2) {
+                    s0 += v[c];
+                    s1 += v[c + 1];
+                }
+                total += s0 + s1;
+            } else {
                 uint32_t u[NC / 2];
 #pragma unroll
                 for (int c = 0; c < NC / 2; ++c) u[c] = pack16<BF>(v[2 * c], v[2 * c + 1]);
@@ -513,7 +537,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.dsfull[half]);
             }
-            if (a.bias_part) {
+            if (!DELTA && a.bias_part) {
                 if (where != 0) {
                     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -560,19 +584,24 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                 }
             }
         }
-        if (nt > 0 && ok) ok = warp_wait(&bar.done, 0, a.err, ERR_TIMEOUT_EPILOGUE);
+        if (DELTA) {       // the two halves of a row, to its row values
+            if (half) sFar[r] = total;
+            named_sync(2 + quarter, 64);
+            if (ok) put_row(a, values, r, half ? nlse : -(total + sFar[r]), !half);
+        }
+        if (!DELTA && nt > 0 && ok) ok = warp_wait(&bar.done, 0, a.err, ERR_TIMEOUT_EPILOGUE);
         tc_fence_after();
-        if (ok) {
+        if (!DELTA && ok) {
             stage_row<HD, BF>(sKV, r, tmem + lofs + C::DQ, half, dsteps, a.scale, nt > 0, true);
         }
         named_sync(2 + quarter, 64);
-        if (ok) {
+        if (!DELTA && ok) {
             const int w0 = i - lane + half * 16;
             unstage_rows<16>(sKV, quarter * 32 + half * 16, a.n - w0, a.d,
                              static_cast<uint16_t*>(a.dq.p) + b * a.dq.sb + (int64_t)w0 * a.dq.st + h * a.dq.sh,
                              a.dq.st, P.dq_vec, lane);
         }
-        if (a.bias_part) {
+        if (!DELTA && a.bias_part) {
 #pragma unroll
             for (int o = 16; o; o >>= 1) {
                 far_lo += __shfl_xor_sync(0xffffffffu, far_lo, o);
@@ -904,7 +933,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad(const __grid_constant_
     if ((int)blockIdx.x < keys)
         grad_keys<HD, BF>(P, blockIdx.x);
     else
-        grad_queries<HD, BF>(P, blockIdx.x - keys);
+        grad_queries<HD, BF, false>(P, blockIdx.x - keys);
+}
+
+template <int HD, bool BF>
+__global__ void __launch_bounds__(kGradThreads, 1) k_grad_delta(const __grid_constant__ GradArgs P) {
+    grad_queries<HD, BF, true>(P, blockIdx.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -977,7 +1011,7 @@ cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
     using KV = GradKV<HD>;
     const size_t bias = a.table ? sizeof(float) * (2 * (size_t)(a.D + kSlack) + 1) : 0;
     const size_t width = 2 * (size_t)a.D + 1;
-    static std::atomic<uint64_t> ready{0};
+    static std::atomic<uint64_t> ready{0}, delta_ready{0};
     cudaError_t e;
     size_t fixed = 1024 + sizeof(GradBars) + sizeof(float) * 2 * kElemWarps + bias +
                    (a.bias_part ? sizeof(float) * kBands * width : 0);
@@ -998,7 +1032,14 @@ cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
     smem = std::max(smem, fixed + p.kv_stages * stage);
     if ((e = raise_smem(k_grad<HD, BF>, kSmemLimit, ready)) != cudaSuccess) return e;
     const int64_t q_blocks = (int64_t)p.q_tiles * a.H * a.B, k_blocks = (int64_t)p.k_tiles * a.G * a.B;
-    k_grad_rows<HD / 8, BF><<<(unsigned)q_blocks, kRowThreads, 0, s>>>(p);
+    if (a.bias_part) {
+        const size_t least = 1024 + sizeof(GradBars) + sizeof(float) * kTile + bias;
+        p.delta_stages = 2 * (ring_stages(least, Q::kTileBytes) / 2);
+        if ((e = raise_smem(k_grad_delta<HD, BF>, kSmemLimit, delta_ready)) != cudaSuccess) return e;
+        k_grad_delta<HD, BF><<<(unsigned)q_blocks, kGradThreads, least + p.delta_stages * Q::kTileBytes, s>>>(p);
+    } else {
+        k_grad_rows<HD / 8, BF><<<(unsigned)q_blocks, kRowThreads, 0, s>>>(p);
+    }
     count_launch();
     k_grad<HD, BF><<<(unsigned)(q_blocks + k_blocks), kGradThreads, smem, s>>>(p);
     count_launch();

@@ -47,7 +47,7 @@ struct GradArgs {
     KeyTiles kt;
     uint8_t* rows;     // [B][H][q_tiles][kRowStride]: row values of the queries
     int q_tiles, k_tiles;
-    int stages, kv_stages, scratch_rows;     // set at launch
+    int stages, kv_stages, delta_stages, scratch_rows;     // set at launch
     int dout_vec, o_vec, dq_vec, dk_vec, dv_vec;   // rows take 16-byte accesses
 };
 

@@ -17,6 +17,11 @@
 // does not show; the products are idle anyway.  The warps' results are joined in
 // shared memory, the blocks' by the last block of a (batch, key head) to finish,
 // in the order of the splits.
+//
+// Measured: 64 sequences, 32 heads on 8 of 128, one token each against 4096 keys: 170 us,
+// 6.3 TB/s (0.93 of the measured copy rate), 140 us with lengths from half of that on;
+// 2 x 2 tokens of 16 heads on 4 of 64 against 200001 keys with a position bias: 77 us,
+// 4.9 TB/s; one token of 16 heads of 64 against 1500 keys: 11.6 us, latency.
 #include "fs_attn_host.cuh"
 
 #include <type_traits>

@@ -1,10 +1,11 @@
 // Cross attention, forward, on the tensor cores.
 //
 // A block takes 256 queries of one head in two tiles of 128 and streams the
-// keys in tiles of 128:
+// keys in tiles of 128 (64 for heads wider than 64):
 //   S_t = Q_t K^T (TMEM), p = 2^{x - ref} in 16 bits in TMEM,
 //   O_t += P_t V (TMEM, P as the A operand read from TMEM).
-// V is read as an operand summed over its rows, so nothing is transposed.
+// V is read as an operand summed over its rows, so nothing is transposed; keys that
+// do not count get -inf by one more product (KeyMask), and their rows are zeroed.
 //
 // Four warps hold a query tile, a row per thread, and one thread issues its
 // products, so neither tile waits for the other's.  From the last P of a tile to
@@ -14,12 +15,18 @@
 // two P and two O for heads up to 64; wider heads take the keys 64 at a time, with
 // two P each (their score products then read Q twice as often as keys of 128
 // would: 48 cycles of shared memory for 32 of arithmetic, and still less than the
-// wait that P over S costs: 3950 cycles a step of 256 x 128 then, see below).
+// wait that P in the columns of S costs).
 //
 // The reference is the running maximum, moved only when a row's maximum grew
 // by more than 2^8 (p then stays below 256, which both types and the float32
 // sums hold with the same relative precision); the rare move rescales O_t in
-// TMEM.
+// TMEM.  P is rounded to the operands' 16 bits, the sum of p is not: out is 0.22 % off
+// in the 2-norm in bfloat16, of which 0.17 % is the rounding of out itself.
+//
+// Bound: heads of 128 by the products (4 x 4096 x 8192, 16 heads, bfloat16: 725 us,
+// 1510 TFLOP/s, 0.80 of the measured burst rate and 0.89 of the sustained one), heads of
+// 64 by the softmax (4 x 2048 x 2048, 16 heads: 92 us, 745 TFLOP/s; 16 exponentials a
+// cycle and SM, half of what the unit gives, and 47 % of the issue slots).
 #include "fs_attn_host.cuh"
 
 #include <atomic>

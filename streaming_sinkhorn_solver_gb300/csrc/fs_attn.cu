@@ -43,6 +43,13 @@ fs_status check_desc(const fs_attention* a) {
     return FS_OK;
 }
 
+// -1 without one (every pointer then fails its check)
+int current_device() {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+    return dev;
+}
+
 // a device array of device dev, the current one (empty tensors may be null)
 fs_status check_ptr(int dev, const void* p, int64_t count, const char* name) {
     if (count == 0) return FS_OK;
@@ -215,8 +222,7 @@ fs_status forward_entry(const fs_attention* at, const void* q, const void* k, co
     FS_TRY(check_desc(at));
     FwdArgs p = {};
     Args& a = p.a;
-    int dev = 0;
-    FS_CUDA(cudaGetDevice(&dev));
+    const int dev = current_device();
     FS_TRY(fill(dev, a, at));
     FS_TRY(view(dev, a.q, q, at->q_stride, at->batch, at->n, a.H, a.d, false, "q"));
     FS_TRY(view(dev, a.k, k, at->k_stride, at->batch, at->m, a.G, a.d, false, "k"));
@@ -298,8 +304,7 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     FS_TRY(check_desc(at));
     GradArgs p = {};
     Args& a = p.a;
-    int dev = 0;
-    FS_CUDA(cudaGetDevice(&dev));
+    const int dev = current_device();
     FS_TRY(fill(dev, a, at));
     FS_TRY(view(dev, a.q, q, at->q_stride, at->batch, at->n, a.H, a.d, false, "q"));
     FS_TRY(view(dev, a.k, k, at->k_stride, at->batch, at->m, a.G, a.d, false, "k"));

@@ -95,6 +95,7 @@ __device__ __forceinline__ void stage_row(uint8_t* tile, int r, uint32_t tmem_ro
 template <bool BF>
 __device__ __forceinline__ void fill_bias(const Args& a, int h, float* sBias, int t, int threads) {
     const Elem<BF>* row = static_cast<const Elem<BF>*>(a.table) + h * a.table_stride;
+#pragma unroll 4      // two loads that depend on one another an entry
     for (int e = t; e < 2 * (a.D + kSlack) + 1; e += threads)
         sBias[e] = bias2(to_f<Elem<BF>>(row[bucket_of(a, (int64_t)e - a.D - kSlack)]));
 }
@@ -266,7 +267,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
     const int qt = blk % P.q_tiles;
     blk /= P.q_tiles;
     const int h = blk % a.H;
-    const int b = blk / a.H;
+    const int b = longest_first<KT>(P.kt, a, blk / a.H);
     const int i0 = qt * kTile;
     const int end = key_end(a, b);
     const int nt = step_count<KT>(P.kt, b, end);

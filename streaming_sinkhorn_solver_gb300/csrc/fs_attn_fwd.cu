@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
     const int qt = blk % P.row_blocks;
     blk /= P.row_blocks;
     const int h = blk % a.H;
-    const int b = blk / a.H;
+    const int b = longest_first<KT>(P.kt, a, blk / a.H);
     const int i0 = qt * 2 * kTile;
     const bool two = i0 + kTile < a.n;
     const int end = key_end(a, b);
@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
     if (a.table) {
         // base-2 bias by relative position -D - kSlack .. D + kSlack of this head
         const T* row = static_cast<const T*>(a.table) + h * a.table_stride;
+#pragma unroll 4      // two loads that depend on one another an entry
         for (int e = threadIdx.x; e < 2 * (a.D + kSlack) + 1; e += kFwdThreads)
             sBias[e] = bias2(to_f<T>(row[bucket_of(a, (int64_t)e - a.D - kSlack)]));
     }

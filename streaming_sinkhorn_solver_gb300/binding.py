@@ -703,19 +703,24 @@ def _att_strides(x, name: str, shape, like):
     return sb, st, sh
 
 
+_RAW_STREAM = []
+
+
 def _att_stream(stream, like) -> int:
     """The cudaStream_t of a call: explicit, else torch's current one."""
     if stream is not None:
         return int(getattr(stream, "cuda_stream", stream))
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without a Stream object
-    return raw(like.get_device()) if raw else torch.cuda.current_stream(like.device).cuda_stream
+    if not _RAW_STREAM:
+        import torch
+        _RAW_STREAM.append(getattr(torch._C, "_cuda_getCurrentRawStream", None) or   # no Stream object
+                           (lambda device: torch.cuda.current_stream(device).cuda_stream))
+    return _RAW_STREAM[0](like.get_device())
 
 
 def _att_empty(like, shape, dtype, stream):
     """A result, allocated for the stream that writes it."""
     import torch
-    if isinstance(stream, torch.cuda.Stream):
+    if stream is not None and isinstance(stream, torch.cuda.Stream):
         with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=like.device)
     return torch.empty(shape, dtype=dtype, device=like.device)

@@ -187,6 +187,24 @@ int choose_key_splits(int64_t blocks, int tiles, int sms) {
     return (int)std::max<int64_t>(s, 1);
 }
 
+// Splits of the gradients' tiles, at most so: as many as a block's tiles outlast the whole
+// call's when those are spread evenly (a block's fixed part counts as 2.5 of them).  With a
+// bias gradient a pass over the queries' blocks alone comes first, so their number counts
+// alone.  2 x 60 queries, 6171 keys, 16 heads on 8 of 112: 93 us for 102, with a bias 153 for
+// 234; 3230 queries, 140 keys, 2 heads on 1 of 128, bias: 72 for 99; 4 x 351 queries, 157
+// keys, 64 heads on 8 of 64 (64 blocks of keys beside 768 of queries): 123 us, and 143 with
+// the keys' blocks split.
+void choose_grad_splits(GradArgs& p, bool bias, int sms) {
+    const Args& a = p.a;
+    const int64_t q_blocks = (int64_t)p.q_tiles * a.H * a.B, k_blocks = (int64_t)p.k_tiles * a.G * a.B;
+    const int q_steps = p.k_tiles, k_steps = a.R * p.q_tiles;
+    const double even = (q_blocks * (q_steps + 2.5) + k_blocks * (k_steps + 2.5)) / sms;
+    p.q_splits = choose_key_splits(q_blocks, q_steps, sms);
+    p.k_splits = choose_key_splits(k_blocks, k_steps, sms);
+    if (!bias) p.q_splits = std::min(p.q_splits, (int)std::ceil(q_steps / even));
+    p.k_splits = std::min(p.k_splits, (int)std::ceil(k_steps / even));
+}
+
 // Whether the few-query kernel takes a call: one tile of its 16 rows per key head, or
 // two where query heads share keys (the 128-row tiles of the other kernel then read
 // the keys once per query head; with a head of its own each they read them once
@@ -338,8 +356,16 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     p.q_tiles = (a.n + kTile - 1) / kTile;
     p.k_tiles = tiles.kt.tiles;
     const size_t blocks = (size_t)a.B * a.H * p.q_tiles;
+    int sms = 0;
+    FS_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    choose_grad_splits(p, dbias != nullptr, sms);
     const size_t rows = c.L.take(blocks * kRowStride);
-    const size_t part = c.L.take(dbias ? sizeof(float) * blocks * (2 * (size_t)a.D + 1) : 0);
+    const size_t part = c.L.take(dbias ? sizeof(float) * blocks * p.q_splits * (2 * (size_t)a.D + 1) : 0);
+    const size_t q_part = p.q_splits > 1 ? sizeof(float) * p.q_splits : 0;
+    const size_t k_part = p.k_splits > 1 ? sizeof(float) * p.k_splits * a.B * a.G * a.m * a.d : 0;
+    const size_t part_dq = c.L.take(q_part * a.B * a.H * a.n * a.d);
+    const size_t part_delta = c.L.take(dbias ? q_part * blocks * kTile : 0);
+    const size_t part_dk = c.L.take(k_part), part_dv = c.L.take(k_part);
     FS_TRY(begin_call(c, stream));
     FS_TRY(ensure_capacity(c));
     for (Input& x : inputs) FS_TRY(x.run(c, a));
@@ -347,6 +373,10 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     p.kt = tiles.kt;
     p.rows = c.at<uint8_t>(rows);
     a.bias_part = dbias ? c.at<float>(part) : nullptr;
+    p.part_dq = c.at<float>(part_dq);
+    p.part_delta = c.at<float>(part_delta);
+    p.part_dk = c.at<float>(part_dk);
+    p.part_dv = c.at<float>(part_dv);
     a.err = c.ws->err_word;
     auto vec = [&](const View& w, int tokens, int heads) {
         return a.d % 8 == 0 && aligned16(w, a.B, tokens, heads);

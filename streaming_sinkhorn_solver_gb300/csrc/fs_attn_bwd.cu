@@ -13,7 +13,9 @@
 //   There a row value belongs to a column, and reading 128 of each kind for every
 //   thread took as long as the exponentials: they enter as one more product of 16 elements
 //   (ones by three bfloat16 terms of each, 24 bits).
-// Both run in one launch, after k_grad_rows (delta = dO . O) or k_grad_delta.
+// Both run in one launch, after k_grad_rows (delta = dO . O) or k_grad_delta.  Where few
+// blocks have many tiles, shares of them go to blocks of their own and k_grad_join adds
+// the float32 sums in order.
 //
 // In both, eight warps hold the elementwise part (warps w and w + 4 the same 32
 // rows, 64 columns of a tile each), and one thread issues the products in an order
@@ -89,6 +91,25 @@ __device__ __forceinline__ void stage_row(uint8_t* tile, int r, uint32_t tmem_ro
 #pragma unroll
     for (int c = 0; c < HD / 2; c += 16)
         if (c0 + c < c1) stage16<BF>(tile, r, c0 + c, o + c);
+}
+
+// The same, unrounded, to a row in memory: one share of the sum.
+template <int HD>
+__device__ __forceinline__ void part_row(float* out, bool live, uint32_t tmem_row, int half, int dsteps,
+                                         float mul, bool any, int d) {
+    const int mid = (dsteps + 1) / 2 * 16;
+    const int c0 = half ? mid : 0, c1 = half ? d : min(mid, d);
+    float o[HD / 2];
+    if (any) {
+#pragma unroll
+        for (int c = 0; c < HD / 2; c += 32) tmem_ld32(tmem_row + c0 + c, o + c);
+        tmem_wait_ld();
+        tmem_reg_fence(o);
+    }
+#pragma unroll
+    for (int c = 0; c < HD / 2; ++c)
+        if (live && c0 + c < c1) out[c0 + c] = any ? o[c] * mul : 0.f;
+    __syncwarp();
 }
 
 // base-2 bias of head h by relative position -D - kSlack .. D + kSlack
@@ -264,13 +285,16 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
     float* sSums = sBias + (a.table ? 2 * (a.D + kSlack) + 1 : 0);   // [4][2 D + 1]
     float* sScratch = sSums + kBands * (2 * a.D + 1);            // [8][scratch_rows][33], with bias sums
 
+    const int split = blk % P.q_splits;
+    blk /= P.q_splits;
     const int qt = blk % P.q_tiles;
     blk /= P.q_tiles;
     const int h = blk % a.H;
     const int b = longest_first<KT>(P.kt, a, blk / a.H);
     const int i0 = qt * kTile;
     const int end = key_end(a, b);
-    const int nt = step_count<KT>(P.kt, b, end);
+    const int nt_all = step_count<KT>(P.kt, b, end), per = (nt_all + P.q_splits - 1) / P.q_splits;
+    const int t0 = min(nt_all, split * per), nt = min(nt_all, t0 + per) - t0;
     const bool partial_keys = !DELTA && (P.kt.words != nullptr || end < a.m);
     const int64_t first = (a.q_pos ? (int64_t)__ldg(a.q_pos + b) : 0) + i0;
     const int dsteps = (a.d + 15) >> 4, dchunks = (a.d + 63) >> 6;
@@ -301,7 +325,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
     if (warp == kIssue) tmem_alloc(&bar.tmem, 512);
     const auto load = [&](int it, int slot) {      // K and V tiles in turn
         const int g = h / a.R;
-        const int key = step_key<KT>(P.kt, b, it >> 1);
+        const int key = step_key<KT>(P.kt, b, t0 + (it >> 1));
         const TensorMap& src = it & 1 ? P.v : P.k;
         mbar_arrive_expect_tx(&bar.full[slot], C::kTileBytes);
         for (int c = 0; c < C::kChunks; ++c)
@@ -422,7 +446,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
         if (partial_keys) {
             Ring r;
             for (int j = 0; j < nt; ++j) {
-                const KeyBits<KT> w(P.kt, b, j, end);
+                const KeyBits<KT> w(P.kt, b, t0 + j, end);
                 if (!warp_wait(&bar.full[r.slot], r.phase, a.err, ERR_TIMEOUT_PRODUCER)) break;
                 if (!w.all()) {
                     clear_rows(sKV + r.slot * C::kTileBytes, C::kChunks, C::kChunkBytes, w, lane);
@@ -472,7 +496,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
         for (int j = 0; j < nt && ok; ++j) {
             // relative position of the warp's first row and column
             const int64_t rel0 =
-                a.table ? step_key<KT>(P.kt, b, j) + half * NC - first - quarter * 32 : (int64_t)0;
+                a.table ? step_key<KT>(P.kt, b, t0 + j) + half * NC - first - quarter * 32 : (int64_t)0;
             if (!(ok = warp_wait(&bar.sfull[half], j & 1, a.err, ERR_TIMEOUT_EPILOGUE))) break;
             tc_fence_after();
             float v[NC];
@@ -528,8 +552,8 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                 for (int c = 0; c < NC; c += 2)
                     upk(mul2f(pk(v[c], v[c + 1]), add2(pk(g[c], g[c + 1]), nd)), v[c], v[c + 1]);
             }
-            if (P.kt.words || (j + 1) * KT > end) {
-                const KeyBits<KT> w(P.kt, b, j, end);
+            if (P.kt.words || (t0 + j + 1) * KT > end) {
+                const KeyBits<KT> w(P.kt, b, t0 + j, end);
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
                     const uint32_t bits = half ? w.w[2 + (c >> 5)] : w.w[c >> 5];
@@ -604,15 +628,26 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
         if (DELTA) {       // the two halves of a row, to its row values
             if (half) sFar[r] = total;
             named_sync(2 + quarter, 64);
-            if (ok) put_row(a, values, r, half ? nlse : -(total + sFar[r]), !half);
+            if (P.q_splits > 1) {
+                if (ok && !half)
+                    P.part_delta[((int64_t)split * a.B * a.H + (int64_t)b * a.H + h) * P.q_tiles * kTile +
+                                 qt * kTile + r] = total + sFar[r];
+            } else if (ok) {
+                put_row(a, values, r, half ? nlse : -(total + sFar[r]), !half);
+            }
         }
         if (!DELTA && nt > 0 && ok) ok = warp_wait(&bar.done, 0, a.err, ERR_TIMEOUT_EPILOGUE);
         tc_fence_after();
+        const bool whole = P.q_splits == 1;
         if (!DELTA && ok) {
-            stage_row<HD, BF>(sKV, r, tmem + lofs + C::DQ, half, dsteps, a.scale, nt > 0, true);
+            if (whole)
+                stage_row<HD, BF>(sKV, r, tmem + lofs + C::DQ, half, dsteps, a.scale, nt > 0, true);
+            else
+                part_row<HD>(P.part_dq + (((int64_t)split * a.B + b) * a.H + h) * a.n * a.d + (int64_t)i * a.d,
+                             i < a.n, tmem + lofs + C::DQ, half, dsteps, a.scale, nt > 0, a.d);
         }
         named_sync(2 + quarter, 64);
-        if (!DELTA && ok) {
+        if (!DELTA && ok && whole) {
             const int w0 = i - lane + half * 16;
             unstage_rows<16>(sKV, quarter * 32 + half * 16, a.n - w0, a.d,
                              static_cast<uint16_t*>(a.dq.p) + b * a.dq.sb + (int64_t)w0 * a.dq.st + h * a.dq.sh,
@@ -629,7 +664,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                 sFar[2 * warp + 1] = far_hi;
             }
             named_sync(1, 32 * kElemWarps);
-            float* out = a.bias_part + ((int64_t)h * a.B * P.q_tiles + (int64_t)b * P.q_tiles + qt) * width;
+            float* out = a.bias_part + ((((int64_t)h * a.B + b) * P.q_tiles + qt) * P.q_splits + split) * width;
             for (int e = threadIdx.x; e < width; e += 32 * kElemWarps) {
                 float s = 0.f;
                 if (e == 0 || e == width - 1) {
@@ -683,6 +718,8 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
     GradBars& bar = *reinterpret_cast<GradBars*>(sOnes + kOnesBytes);
     float* sBias = reinterpret_cast<float*>(&bar + 1);
 
+    const int split = blk % P.k_splits;
+    blk /= P.k_splits;
     const int kt = blk % P.k_tiles;
     blk /= P.k_tiles;
     const int g = blk % a.G;
@@ -695,7 +732,8 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
     const int64_t pos = a.q_pos ? (int64_t)__ldg(a.q_pos + b) : 0;
     const int dsteps = (a.d + 15) >> 4, dpairs = (a.d + 31) >> 5;
     const int per_head = (a.n + QT - 1) / QT;        // query tiles of a head
-    const int nt = any ? a.R * per_head : 0;
+    const int nt_all = any ? a.R * per_head : 0, per = (nt_all + P.k_splits - 1) / P.k_splits;
+    const int t0 = min(nt_all, split * per), nt = min(nt_all, t0 + per) - t0;
 
     if (warp == kLoad) {
         if (lane < NS) mbar_init(&bar.full[lane], 1);
@@ -719,7 +757,7 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
     if (warp == kIssue) tmem_alloc(&bar.tmem, 512);
     // Q tiles (with the row values of their queries) and dO tiles in turn
     const auto load = [&](int it, int slot) {
-        const int t = it >> 1, h = g * a.R + t / per_head, qt = t % per_head;
+        const int t = t0 + (it >> 1), h = g * a.R + t / per_head, qt = t % per_head;
         const bool second = it & 1;
         const TensorMap& src = second ? P.dout : P.q;
         mbar_arrive_expect_tx(&bar.full[slot], C::kTileBytes + (second ? 0 : kRowBytes));
@@ -836,9 +874,9 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
         const uint32_t tS = tmem + lofs + C::S + half * NC, tDP = tmem + lofs + C::DP + half * NC;
         const float scale2 = least_scale(a);
         bool ok = true;
-        int h = g * a.R, qt = 0;
+        int h = g * a.R + t0 / per_head, qt = t0 % per_head;
         for (int t = 0; t < nt; ++t) {
-            if (a.table && qt == 0) {
+            if (a.table && (qt == 0 || t == 0)) {
                 named_sync(1, 32 * kElemWarps);
                 fill_bias<BF>(a, h, sBias, threadIdx.x, 32 * kElemWarps);
                 named_sync(1, 32 * kElemWarps);
@@ -918,17 +956,25 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
         const int w0 = j - lane + half * 16, r0 = quarter * 32 + half * 16;
         if (nt > 0 && ok) ok = warp_wait(&bar.dvdone, 0, a.err, ERR_TIMEOUT_EPILOGUE);
         tc_fence_after();
-        if (ok) stage_row<HD, BF>(sV, r, tmem + lofs + C::DV, half, dsteps, 1.f, nt > 0, keep);
+        const bool whole = P.k_splits == 1;
+        const int64_t part = ((((int64_t)split * a.B + b) * a.G + g) * a.m + j) * a.d;
+        if (ok && whole)
+            stage_row<HD, BF>(sV, r, tmem + lofs + C::DV, half, dsteps, 1.f, nt > 0, keep);
+        else if (ok)
+            part_row<HD>(P.part_dv + part, j < a.m, tmem + lofs + C::DV, half, dsteps, 1.f, nt > 0, a.d);
         named_sync(2 + quarter, 64);
-        if (ok)
+        if (ok && whole)
             unstage_rows<16>(sV, r0, a.m - w0, a.d,
                              static_cast<uint16_t*>(a.dv.p) + b * a.dv.sb + (int64_t)w0 * a.dv.st + g * a.dv.sh,
                              a.dv.st, P.dv_vec, lane);
         if (nt > 0 && ok) ok = warp_wait(&bar.done, 0, a.err, ERR_TIMEOUT_EPILOGUE);
         tc_fence_after();
-        if (ok) stage_row<HD, BF>(sK, r, tmem + lofs + C::DK, half, dsteps, a.scale, nt > 0, keep);
+        if (ok && whole)
+            stage_row<HD, BF>(sK, r, tmem + lofs + C::DK, half, dsteps, a.scale, nt > 0, keep);
+        else if (ok)
+            part_row<HD>(P.part_dk + part, j < a.m, tmem + lofs + C::DK, half, dsteps, a.scale, nt > 0, a.d);
         named_sync(2 + quarter, 64);
-        if (ok)
+        if (ok && whole)
             unstage_rows<16>(sK, r0, a.m - w0, a.d,
                              static_cast<uint16_t*>(a.dk.p) + b * a.dk.sb + (int64_t)w0 * a.dk.st + g * a.dk.sh,
                              a.dk.st, P.dk_vec, lane);
@@ -946,7 +992,7 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
 // queries fill the GPU's last wave.
 template <int HD, bool BF>
 __global__ void __launch_bounds__(kGradThreads, 1) k_grad(const __grid_constant__ GradArgs P) {
-    const int keys = P.k_tiles * P.a.G * P.a.B;
+    const int keys = P.k_tiles * P.a.G * P.a.B * P.k_splits;
     if ((int)blockIdx.x < keys)
         grad_keys<HD, BF>(P, blockIdx.x);
     else
@@ -956,6 +1002,53 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_grad(const __grid_constant_
 template <int HD, bool BF>
 __global__ void __launch_bounds__(kGradThreads, 1) k_grad_delta(const __grid_constant__ GradArgs P) {
     grad_queries<HD, BF, true>(P, blockIdx.x);
+}
+
+// The shares of a gradient added in their order: a row (b, head, token) a warp.  A key that
+// does not count has a zero gradient whatever its row holds.
+template <bool BF>
+__global__ void __launch_bounds__(128) k_grad_join(Args a, View w, View w1, const float* part, const float* part1,
+                                                   int splits, int tokens, int heads,
+                                                   const uint4* __restrict__ words, int tiles, bool keys) {
+    if (blockIdx.y) {
+        w = w1;
+        part = part1;
+    }
+    const int64_t rows = (int64_t)a.B * heads * tokens, row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    const int t = (int)(row % tokens), h = (int)(row / tokens % heads), b = (int)(row / tokens / heads);
+    bool counts = true;
+    if (keys) {
+        counts = t < key_end(a, b);
+        if (counts && words) {
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(words + (int64_t)b * tiles + t / kTile);
+            counts = (u[(t % kTile) / 32] >> (t % 32)) & 1u;
+        }
+    }
+    Elem<BF>* out = static_cast<Elem<BF>*>(w.p) + b * w.sb + (int64_t)t * w.st + h * w.sh;
+    for (int c = lane; c < a.d; c += 32) {
+        float s = 0.f;
+        if (counts)
+#pragma unroll 8
+            for (int k = 0; k < splits; ++k) s += __ldg(part + (k * rows + row) * a.d + c);
+        out[c] = from_f<Elem<BF>>(s);
+    }
+}
+
+// Row values of the queries from the shares of delta: a row a thread.
+__global__ void __launch_bounds__(kTile) k_delta_join(const __grid_constant__ GradArgs P) {
+    const Args& a = P.a;
+    int blk = blockIdx.x;
+    const int qt = blk % P.q_tiles;
+    blk /= P.q_tiles;
+    const int h = blk % a.H, b = blk / a.H, r = threadIdx.x;
+    const int64_t tile = (int64_t)blockIdx.x;
+    float s = 0.f;
+    for (int k = 0; k < P.q_splits; ++k) s += P.part_delta[(k * (int64_t)gridDim.x + tile) * kTile + r];
+    uint8_t* values = P.rows + tile * kRowStride;
+    put_row(a, values, r, -s, true);
+    put_row(a, values, r, row_lse(a, b, h, (int64_t)qt * kTile + r), false);
 }
 
 // ---------------------------------------------------------------------------
@@ -973,7 +1066,7 @@ __global__ void __launch_bounds__(kBiasThreads) k_grad_bias(const __grid_constan
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int width = 2 * a.D + 1;
     int* sBucket = reinterpret_cast<int*>(sSum + shares * width);
-    const int64_t parts = (int64_t)a.B * P.q_tiles * (a.table_stride ? 1 : a.H);
+    const int64_t parts = (int64_t)a.B * P.q_tiles * P.q_splits * (a.table_stride ? 1 : a.H);
     const float* src = a.bias_part + blockIdx.x * parts * width;
     const int64_t per = (parts + shares - 1) / shares;
     const int strips = (width + 31) / 32;
@@ -1053,13 +1146,27 @@ cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
         const size_t least = 1024 + sizeof(GradBars) + sizeof(float) * kTile + bias;
         p.delta_stages = 2 * (ring_stages(least, Q::kTileBytes) / 2);
         if ((e = raise_smem(k_grad_delta<HD, BF>, kSmemLimit, delta_ready)) != cudaSuccess) return e;
-        k_grad_delta<HD, BF><<<(unsigned)q_blocks, kGradThreads, least + p.delta_stages * Q::kTileBytes, s>>>(p);
+        k_grad_delta<HD, BF><<<(unsigned)(q_blocks * p.q_splits), kGradThreads,
+                               least + p.delta_stages * Q::kTileBytes, s>>>(p);
+        if (p.q_splits > 1) {
+            k_delta_join<<<(unsigned)q_blocks, kTile, 0, s>>>(p);
+            count_launch();
+        }
     } else {
         k_grad_rows<HD / 8, BF><<<(unsigned)q_blocks, kRowThreads, 0, s>>>(p);
     }
     count_launch();
-    k_grad<HD, BF><<<(unsigned)(q_blocks + k_blocks), kGradThreads, smem, s>>>(p);
+    k_grad<HD, BF><<<(unsigned)(q_blocks * p.q_splits + k_blocks * p.k_splits), kGradThreads, smem, s>>>(p);
     count_launch();
+    const auto join = [&](const View& w, const View& w1, const float* part, const float* part1, int splits,
+                          int tokens, int heads, bool keys) {
+        const dim3 grid((unsigned)(((int64_t)a.B * heads * tokens + 3) / 4), keys ? 2 : 1);
+        k_grad_join<BF><<<grid, 128, 0, s>>>(a, w, w1, part, part1, splits, tokens, heads, p.kt.words, p.kt.tiles,
+                                             keys);
+        count_launch();
+    };
+    if (p.q_splits > 1) join(a.dq, a.dq, p.part_dq, p.part_dq, p.q_splits, a.n, a.H, false);
+    if (p.k_splits > 1) join(a.dk, a.dv, p.part_dk, p.part_dv, p.k_splits, a.m, a.G, true);
     if (dbias) {
         // shares of the sums and the buckets in 48 KB
         const int shares = std::max(1, std::min<int>(kBiasSplit, (int)(12288 / width) - 1));

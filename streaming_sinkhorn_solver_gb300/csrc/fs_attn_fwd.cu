@@ -23,8 +23,8 @@
 // TMEM.  P is rounded to the operands' 16 bits, the sum of p is not: out is 0.22 % off
 // in the 2-norm in bfloat16, of which 0.17 % is the rounding of out itself.
 //
-// Bound: heads of 128 by the products (4 x 4096 x 8192, 16 heads, bfloat16: 725 us,
-// 1510 TFLOP/s, 0.80 of the measured burst rate and 0.89 of the sustained one), heads of
+// Bound: heads of 128 by the products (4 x 4096 x 8192, 16 heads, bfloat16: 720 us,
+// 1530 TFLOP/s, 0.81 of the measured burst rate and 0.90 of the sustained one), heads of
 // 64 by the softmax (4 x 2048 x 2048, 16 heads: 92 us, 745 TFLOP/s; 16 exponentials a
 // cycle and SM, half of what the unit gives, and 47 % of the issue slots).
 #include "fs_attn_host.cuh"

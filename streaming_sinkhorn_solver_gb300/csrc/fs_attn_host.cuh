@@ -47,6 +47,10 @@ struct GradArgs {
     KeyTiles kt;
     uint8_t* rows;     // [B][H][q_tiles][kRowStride]: row values of the queries
     int q_tiles, k_tiles;
+    // where few blocks have many tiles: shares of a block's tiles, and their sums in float32
+    // (rows (b, head, token); delta: rows of rows), joined in order
+    int q_splits, k_splits;
+    float *part_dq, *part_dk, *part_dv, *part_delta;
     int stages, kv_stages, delta_stages, scratch_rows;     // set at launch
     int dout_vec, o_vec, dq_vec, dk_vec, dv_vec;   // rows take 16-byte accesses
 };

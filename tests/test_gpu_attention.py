@@ -389,3 +389,10 @@ def test_bias_gradient_where_one_bucket_holds_most_of_the_weight(n, m, nb, far):
     dbias = fs.fs_cross_attention_grad(c["q"], c["k"], c["v"], out, lse, dout, **how)[3]
     want = reference(c, how, dout)["dbias"]
     assert float((dbias.cpu().double() - want).norm()) <= 2.0 ** -8 * float(want.norm())
+
+
+@pytest.mark.parametrize("n,m,H,G,d,nb", [(40, 3100, 4, 2, 80, 16), (40, 3100, 2, 2, 64, 0),
+                                          (2600, 100, 4, 1, 128, 0), (2600, 140, 2, 1, 64, 16)])
+def test_gradients_of_few_blocks_with_many_tiles(n, m, H, G, d, nb):
+    """Shares of the tiles in blocks of their own, with a share that no key counts in."""
+    check(*make(2, n, m, H, G, d, BF, lens=[m, m // 3], drop=0.2, nb=nb, far=90, seed=32))

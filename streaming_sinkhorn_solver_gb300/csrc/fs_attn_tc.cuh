@@ -268,12 +268,6 @@ struct KeyTiles {
     const int* count;       // [B]
     int tiles;              // ceil(m / 128)
 };
-__device__ __forceinline__ int tile_count(const KeyTiles& kt, int b, int end) {
-    return kt.list ? __ldg(kt.count + b) : (end + kTile - 1) / kTile;
-}
-__device__ __forceinline__ int tile_at(const KeyTiles& kt, int b, int j) {
-    return kt.list ? __ldg(kt.list + (int64_t)b * kt.tiles + j) : j;
-}
 // counted keys of a tile as 128 bits
 __device__ __forceinline__ uint4 tile_words(const KeyTiles& kt, int b, int tile, int end) {
     if (kt.words) return __ldg(kt.words + (int64_t)b * kt.tiles + tile);
@@ -283,9 +277,6 @@ __device__ __forceinline__ uint4 tile_words(const KeyTiles& kt, int b, int tile,
         return c <= 0 ? 0u : (c >= 32 ? 0xffffffffu : (1u << c) - 1u);
     };
     return make_uint4(w(0), w(1), w(2), w(3));
-}
-__device__ __forceinline__ bool all_count(const uint4& w) {
-    return (w.x & w.y & w.z & w.w) == 0xffffffffu;
 }
 
 // The same in steps of KT = 128 or 64 keys: their count, first key, and bits.

@@ -1075,7 +1075,7 @@ __global__ void __launch_bounds__(kBiasThreads) k_grad_bias(const __grid_constan
         if (e >= width) continue;
         const int64_t p0 = share * per, p1 = min(parts, p0 + per);
         float s = 0.f;
-#pragma unroll 8
+#pragma unroll 16
         for (int64_t p = p0; p < p1; ++p) s += src[p * width + e];
         sSum[share * width + e] = s;
     }
@@ -1168,8 +1168,10 @@ cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
     if (p.q_splits > 1) join(a.dq, a.dq, p.part_dq, p.part_dq, p.q_splits, a.n, a.H, false);
     if (p.k_splits > 1) join(a.dk, a.dv, p.part_dk, p.part_dv, p.k_splits, a.m, a.G, true);
     if (dbias) {
-        // shares of the sums and the buckets in 48 KB
-        const int shares = std::max(1, std::min<int>(kBiasSplit, (int)(12288 / width) - 1));
+        // shares of the sums and the buckets in 48 KB; no more than the warps take in one turn
+        const int strips = (int)(width + 31) / 32;
+        const int shares =
+            std::max(1, std::min({kBiasSplit, (int)(12288 / width) - 1, kBiasThreads / 32 / strips}));
         k_grad_bias<BF><<<a.table_stride ? a.H : 1, kBiasThreads, 4 * (shares + 1) * width, s>>>(
             p, shares, static_cast<Elem<BF>*>(dbias));
         count_launch();

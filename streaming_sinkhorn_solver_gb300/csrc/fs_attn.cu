@@ -187,21 +187,26 @@ int choose_key_splits(int64_t blocks, int tiles, int sms) {
     return (int)std::max<int64_t>(s, 1);
 }
 
+// Key tiles up to which delta comes from the scores without a bias gradient too: the fewer
+// keys share a row's weight, the more the rounding of O counts.  In bfloat16 dq is 0.28 %
+// off with delta from O at 150 to 830 keys, 0.25 % at 4096; with it from the scores 0.24 %
+// (3 x 2644 queries, 478 keys, 16 heads on 8 of 32, forward and gradients: 169 us for 128).
+constexpr int kExactTiles = 8;
+
 // Splits of the gradients' tiles, at most so: as many as a block's tiles outlast the whole
-// call's when those are spread evenly (a block's fixed part counts as 2.5 of them).  With a
-// bias gradient a pass over the queries' blocks alone comes first, so their number counts
-// alone.  2 x 60 queries, 6171 keys, 16 heads on 8 of 112: 93 us for 102, with a bias 153 for
+// call's when those are spread evenly (a block's fixed part counts as 2.5 of them).  Where
+// k_grad_delta, of the queries' blocks alone, comes first, their number counts alone.  2 x 60 queries, 6171 keys, 16 heads on 8 of 112: 93 us for 102, with a bias 153 for
 // 234; 3230 queries, 140 keys, 2 heads on 1 of 128, bias: 72 for 99; 4 x 351 queries, 157
 // keys, 64 heads on 8 of 64 (64 blocks of keys beside 768 of queries): 123 us, and 143 with
 // the keys' blocks split.
-void choose_grad_splits(GradArgs& p, bool bias, int sms) {
+void choose_grad_splits(GradArgs& p, int sms) {
     const Args& a = p.a;
     const int64_t q_blocks = (int64_t)p.q_tiles * a.H * a.B, k_blocks = (int64_t)p.k_tiles * a.G * a.B;
     const int q_steps = p.k_tiles, k_steps = a.R * p.q_tiles;
     const double even = (q_blocks * (q_steps + 2.5) + k_blocks * (k_steps + 2.5)) / sms;
     p.q_splits = choose_key_splits(q_blocks, q_steps, sms);
     p.k_splits = choose_key_splits(k_blocks, k_steps, sms);
-    if (!bias) p.q_splits = std::min(p.q_splits, (int)std::ceil(q_steps / even));
+    if (!p.exact_delta) p.q_splits = std::min(p.q_splits, (int)std::ceil(q_steps / even));
     p.k_splits = std::min(p.k_splits, (int)std::ceil(k_steps / even));
 }
 
@@ -358,13 +363,14 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     const size_t blocks = (size_t)a.B * a.H * p.q_tiles;
     int sms = 0;
     FS_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    choose_grad_splits(p, dbias != nullptr, sms);
+    p.exact_delta = dbias || p.k_tiles <= kExactTiles;
+    choose_grad_splits(p, sms);
     const size_t rows = c.L.take(blocks * kRowStride);
     const size_t part = c.L.take(dbias ? sizeof(float) * blocks * p.q_splits * (2 * (size_t)a.D + 1) : 0);
     const size_t q_part = p.q_splits > 1 ? sizeof(float) * p.q_splits : 0;
     const size_t k_part = p.k_splits > 1 ? sizeof(float) * p.k_splits * a.B * a.G * a.m * a.d : 0;
     const size_t part_dq = c.L.take(q_part * a.B * a.H * a.n * a.d);
-    const size_t part_delta = c.L.take(dbias ? q_part * blocks * kTile : 0);
+    const size_t part_delta = c.L.take(p.exact_delta ? q_part * blocks * kTile : 0);
     const size_t part_dk = c.L.take(k_part), part_dv = c.L.take(k_part);
     FS_TRY(begin_call(c, stream));
     FS_TRY(ensure_capacity(c));

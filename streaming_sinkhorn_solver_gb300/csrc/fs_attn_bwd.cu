@@ -263,8 +263,8 @@ struct GradQ {
 // With delta from the 16-bit O, sum_j ds_ij is dO_i . (error of O_i) instead of 0, and a
 // bucket that holds nearly all of its rows' weight sums nothing but that: its gradient
 // came out up to 1.2 % off (2-norm of dbias against 64 bits, 0.24 % with this pass).  It
-// costs a quarter of the gradients' time, so only a bias gradient takes it; without one dq
-// and dk are 0.25 % off for 0.17 % of rounding alone.
+// costs a quarter of the gradients' time, so only a bias gradient and calls with few keys
+// take it (exact_delta).
 template <int HD, bool BF, bool DELTA>
 __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
     using C = GradQ<HD>;
@@ -1142,7 +1142,7 @@ cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
     smem = std::max(smem, fixed + p.kv_stages * stage);
     if ((e = raise_smem(k_grad<HD, BF>, kSmemLimit, ready)) != cudaSuccess) return e;
     const int64_t q_blocks = (int64_t)p.q_tiles * a.H * a.B, k_blocks = (int64_t)p.k_tiles * a.G * a.B;
-    if (a.bias_part) {
+    if (p.exact_delta) {
         const size_t least = 1024 + sizeof(GradBars) + sizeof(float) * kTile + bias;
         p.delta_stages = 2 * (ring_stages(least, Q::kTileBytes) / 2);
         if ((e = raise_smem(k_grad_delta<HD, BF>, kSmemLimit, delta_ready)) != cudaSuccess) return e;

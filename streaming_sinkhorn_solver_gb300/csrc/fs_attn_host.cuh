@@ -47,6 +47,7 @@ struct GradArgs {
     KeyTiles kt;
     uint8_t* rows;     // [B][H][q_tiles][kRowStride]: row values of the queries
     int q_tiles, k_tiles;
+    bool exact_delta;  // from the scores (k_grad_delta), not from O
     // where few blocks have many tiles: shares of a block's tiles, and their sums in float32
     // (rows (b, head, token); delta: rows of rows), joined in order
     int q_splits, k_splits;

@@ -637,7 +637,8 @@ _NO_STRIDES = (0, 0, 0)
 _DTYPES = {}
 
 
-def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, strides) -> fs_attention:
+def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, strides,
+               stream) -> fs_attention:
     """Checked description of a call (see the C header for each field);
     `strides` are those of out, dout, dq, dk and dv."""
     import torch
@@ -680,6 +681,10 @@ def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, stri
         if size % 2 == 0:
             raise ValueError("bias_buckets must have 2 max_distance + 1 entries")
         far = size // 2
+        if bias.shape[0] > 1 and bias.stride(0) == 0:
+            # stride 0 is one row with one gradient; an expanded row has one for each head
+            with _att_on(stream):
+                bias = bias.contiguous()
         bias_p = bias.data_ptr()
         bias_stride = 0 if bias.shape[0] == 1 else bias.stride(0)
         buckets_p = _i_ptr(bias_buckets, "bias_buckets", (size,), torch.int32)
@@ -689,6 +694,7 @@ def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, stri
     _ATTENTION.pack_into(at, 0, dtype, heads, kv_heads, d, batch, n, m,
                          d ** -0.5 if scale is None else scale, nb, far, 0, *qs, *ks, *vs, *strides,
                          len_p, mask_p, mask_stride, bias_p, bias_stride, buckets_p, pos_p)
+    at.table = bias      # a copy lives until the call is enqueued
     return at
 
 
@@ -717,13 +723,19 @@ def _att_stream(stream, like) -> int:
     return _RAW_STREAM[0](like.get_device())
 
 
+def _att_on(stream):
+    """Where torch allocates and runs what belongs to a call on `stream`."""
+    import torch
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None)
+
+
 def _att_empty(like, shape, dtype, stream):
     """A result, allocated for the stream that writes it."""
     import torch
-    if stream is not None and isinstance(stream, torch.cuda.Stream):
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=like.device)
-    return torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with _att_on(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def fs_cross_attention(q, k, v, *, scale: Optional[float] = None, kv_len=None, key_mask=None,
@@ -748,7 +760,7 @@ def fs_cross_attention(q, k, v, *, scale: Optional[float] = None, kv_len=None, k
     if out is None:
         out = _att_empty(q, q.shape, q.dtype, stream) if _is_torch(q) else q
     at = _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos,
-                    (*_att_strides(out, "out", q.shape, q), *_NO_STRIDES * 4))
+                    (*_att_strides(out, "out", q.shape, q), *_NO_STRIDES * 4), stream)
     rows = (q.shape[0], q.shape[2], q.shape[1])
     if lse is None:
         lse = _att_empty(q, rows, torch.float32, stream)
@@ -774,7 +786,7 @@ def fs_cross_attention_grad(q, k, v, out, lse, dout, *, scale: Optional[float] =
     at = _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos,
                     (*_att_strides(out, "out", q.shape, q), *_att_strides(dout, "dout", q.shape, q),
                      *_att_strides(dq, "dq", q.shape, q), *_att_strides(dk, "dk", k.shape, q),
-                     *_att_strides(dv, "dv", v.shape, q)))
+                     *_att_strides(dv, "dv", v.shape, q)), stream)
     if bias is None:
         dbias = None
     else:

@@ -372,6 +372,8 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     const size_t part_dq = c.L.take(q_part * a.B * a.H * a.n * a.d);
     const size_t part_delta = c.L.take(p.exact_delta ? q_part * blocks * kTile : 0);
     const size_t part_dk = c.L.take(k_part), part_dv = c.L.take(k_part);
+    const size_t q_range = c.L.take(a.bf16 ? 0 : sizeof(float) * blocks);
+    const size_t v_range = c.L.take(a.bf16 ? 0 : sizeof(float) * a.B * a.G * (size_t)p.k_tiles);
     FS_TRY(begin_call(c, stream));
     FS_TRY(ensure_capacity(c));
     for (Input& x : inputs) FS_TRY(x.run(c, a));
@@ -383,6 +385,8 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     p.part_delta = c.at<float>(part_delta);
     p.part_dk = c.at<float>(part_dk);
     p.part_dv = c.at<float>(part_dv);
+    p.q_range = c.at<float>(q_range);
+    p.v_range = c.at<float>(v_range);
     a.err = c.ws->err_word;
     auto vec = [&](const View& w, int tokens, int heads) {
         return a.d % 8 == 0 && aligned16(w, a.B, tokens, heads);

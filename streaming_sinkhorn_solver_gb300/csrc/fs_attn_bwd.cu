@@ -29,7 +29,10 @@
 // grad_keys products half as wide read shared memory half again as much, and lost.
 //
 // p and ds are rounded to the operands' 16 bits, sums are float32: in bfloat16 dq, dk and
-// dv are 0.25 % off in the 2-norm, of which 0.17 % is their own rounding.
+// dv are 0.25 % off in the 2-norm, of which 0.17 % is their own rounding.  In float16 both
+// are multiplied by powers of two first (kProbShift, range_shift), which the results' last
+// factors take back: ds goes with dO, whose size is the training's choice, and as it is would
+// be subnormal (dq and dk 0.8 % off at |dO| = 1e-4) or infinite.
 //
 // Measured: batch 4, 2048 x 2048, 16 heads, bfloat16: 264 us with heads of 64 (650
 // TFLOP/s of the five products; the chain of waits, exponentials and conversions of a
@@ -244,6 +247,78 @@ __global__ void __launch_bounds__(kRowThreads) k_grad_rows(const __grid_constant
     put_row(a, P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowStride, r,
             second ? -sDelta[r] : row_lse(a, b, h, (int64_t)qt * kTile + r), second);
 }
+
+// float16: the largest norm of a row in each tile of dO and of a counted row in each of V,
+// for range_shift.  Rows that are not finite set no range: they are lost whatever it is.
+template <int LANES>
+__global__ void __launch_bounds__(kRowThreads) k_grad_range(const __grid_constant__ GradArgs P) {
+    constexpr int kRows = 32 / LANES, kTurns = 16 / kRows;      // rows of a warp at a time, of 16
+    __shared__ float sTop[kRowThreads / 32];
+    const Args& a = P.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int queries = P.q_tiles * a.H * a.B;
+    const bool keys = (int)blockIdx.x >= queries;
+    const int blk = blockIdx.x - (keys ? queries : 0);
+    const int tiles = keys ? P.k_tiles : P.q_tiles, heads = keys ? a.G : a.H;
+    const int tile = blk % tiles, h = blk / tiles % heads, b = blk / tiles / heads;
+    const View& w = keys ? a.v : a.dout;      // in place or copied, their rows take 16-byte loads
+    const uint4 bits = keys ? tile_words(P.kt, b, tile, key_end(a, b)) : make_uint4(0, 0, 0, 0);
+    uint32_t u[kTurns][4];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int r = warp * 16 + k * kRows + lane / LANES;     // a warp's rows are of one word
+        const int64_t t = (int64_t)tile * kTile + r;
+        const uint32_t word = warp < 2 ? bits.x : warp < 4 ? bits.y : warp < 6 ? bits.z : bits.w;
+        const bool live = keys ? (word >> (r & 31)) & 1u : t < a.n;
+        load8(w, b * w.sb + t * w.st + h * w.sh, 8 * (lane % LANES), a.d, live, true, u[k]);
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        float x = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack16<false>(u[k][e]);
+            x = fmaf(f.x, f.x, x);
+            x = fmaf(f.y, f.y, x);
+        }
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (x < INFINITY) top = fmaxf(top, x);
+    }
+#pragma unroll
+    for (int o = 16; o >= LANES; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) sTop[warp] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int k = 1; k < kRowThreads / 32; ++k) top = fmaxf(top, sTop[k]);
+        (keys ? P.v_range : P.q_range)[blk] = sqrtf(top);
+    }
+}
+
+// |ds_ij| = p_ij |dO_i . v_j - sum_k p_ik dO_i . v_k| <= 2 max |dO_i| max |v_j|.  The power of two
+// that takes this bound, over `nq` tiles of dO and all counted values of the key head, to
+// [2^14, 2^15): float16 then holds in full what is down to 2^-29 of it.  A whole warp.
+__device__ __forceinline__ int range_shift(const float* q, int nq, const float* v, int nv) {
+    const int lane = threadIdx.x & 31;
+    float x = 0.f, y = 0.f;
+    for (int e = lane; e < nq; e += 32) x = fmaxf(x, __ldg(q + e));
+#pragma unroll 4
+    for (int e = lane; e < nv; e += 32) y = fmaxf(y, __ldg(v + e));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+    }
+    const float bound = 2.f * x * y;      // 0 or a normal number, 2^-48 to 2^41
+    return bound > 0.f ? 14 + 127 - (int)(__float_as_uint(bound) >> 23) : 0;
+}
+__device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// p of grad_keys in float16 is multiplied by 2^kProbShift: in full down to 2^-28, and no more
+// than the rounding of x can take it past 1 would make it infinite
+constexpr int kProbShift = 14;
 
 // ---------------------------------------------------------------------------
 
@@ -464,7 +539,13 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
         const uint32_t lofs = (uint32_t)(quarter * 32) << 16;
         uint8_t* const values = P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowStride;
         const float* row = reinterpret_cast<const float*>(values + kRowBytes);
-        const float nlse = DELTA ? row_lse(a, b, h, i) : row[r];
+        // float16: ds, and the sums of the bias gradient, are 2^shift times as large
+        const float* v_range = P.v_range + ((int64_t)b * a.G + h / a.R) * P.k_tiles;
+        const int shift = BF || DELTA ? 0
+                                      : range_shift(P.q_range + ((int64_t)b * a.H + h) * P.q_tiles + qt, 1,
+                                                    v_range, P.k_tiles);
+        float nlse = DELTA ? row_lse(a, b, h, i) : row[r];
+        if (!BF && !DELTA) nlse += (float)shift;
         const float ndelta = DELTA ? 0.f : row[kTile + r];
         bool ok = true;
         if (nt > 0) {     // operands into TMEM: warps 0..3 the rows of Q, warps 4..7 those of dO
@@ -639,12 +720,13 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
         if (!DELTA && nt > 0 && ok) ok = warp_wait(&bar.done, 0, a.err, ERR_TIMEOUT_EPILOGUE);
         tc_fence_after();
         const bool whole = P.q_splits == 1;
+        const float scale = BF ? a.scale : a.scale * power2(-shift);
         if (!DELTA && ok) {
             if (whole)
-                stage_row<HD, BF>(sKV, r, tmem + lofs + C::DQ, half, dsteps, a.scale, nt > 0, true);
+                stage_row<HD, BF>(sKV, r, tmem + lofs + C::DQ, half, dsteps, scale, nt > 0, true);
             else
                 part_row<HD>(P.part_dq + (((int64_t)split * a.B + b) * a.H + h) * a.n * a.d + (int64_t)i * a.d,
-                             i < a.n, tmem + lofs + C::DQ, half, dsteps, a.scale, nt > 0, a.d);
+                             i < a.n, tmem + lofs + C::DQ, half, dsteps, scale, nt > 0, a.d);
         }
         named_sync(2 + quarter, 64);
         if (!DELTA && ok && whole) {
@@ -674,7 +756,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
 #pragma unroll
                     for (int k = 0; k < kBands; ++k) s += sSums[k * width + e];
                 }
-                out[e] = s;
+                out[e] = BF ? s : s * power2(-shift);
             }
         }
     }
@@ -873,6 +955,12 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
         const uint32_t lofs = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lofs + C::S + half * NC, tDP = tmem + lofs + C::DP + half * NC;
         const float scale2 = least_scale(a);
+        // float16: p and ds are 2^kProbShift and 2^shift times as large
+        const float* q_range = P.q_range + ((int64_t)b * a.H + g * a.R) * P.q_tiles;
+        const int shift = BF ? 0
+                             : range_shift(q_range, a.R * P.q_tiles,
+                                           P.v_range + ((int64_t)b * a.G + g) * P.k_tiles, P.k_tiles);
+        const float ds_over_p = power2(shift - (BF ? 0 : kProbShift));
         bool ok = true;
         int h = g * a.R + t0 / per_head, qt = t0 % per_head;
         for (int t = 0; t < nt; ++t) {
@@ -905,6 +993,7 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
                         mul = 1.f;
                     }
                 }
+                if (!BF) add += (float)kProbShift;
                 const uint64_t mul2 = pk(mul, mul), add2 = pk(add, add);
 #pragma unroll
                 for (int c = 0; c < NC; c += 2) {
@@ -936,7 +1025,9 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
                         float f0, f1;
-                        upk(mul2f(pk(v[q + c], v[q + c + 1]), pk(d[c], d[c + 1])), f0, f1);
+                        uint64_t ds = mul2f(pk(v[q + c], v[q + c + 1]), pk(d[c], d[c + 1]));
+                        if (!BF) ds = mul2f(ds, pk(ds_over_p, ds_over_p));
+                        upk(ds, f0, f1);
                         u[(q + c) / 2] = pack16<BF>(f0, f1);
                     }
                 }
@@ -958,10 +1049,12 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
         tc_fence_after();
         const bool whole = P.k_splits == 1;
         const int64_t part = ((((int64_t)split * a.B + b) * a.G + g) * a.m + j) * a.d;
+        const float dv_scale = BF ? 1.f : power2(-kProbShift);
+        const float dk_scale = BF ? a.scale : a.scale * power2(-shift);
         if (ok && whole)
-            stage_row<HD, BF>(sV, r, tmem + lofs + C::DV, half, dsteps, 1.f, nt > 0, keep);
+            stage_row<HD, BF>(sV, r, tmem + lofs + C::DV, half, dsteps, dv_scale, nt > 0, keep);
         else if (ok)
-            part_row<HD>(P.part_dv + part, j < a.m, tmem + lofs + C::DV, half, dsteps, 1.f, nt > 0, a.d);
+            part_row<HD>(P.part_dv + part, j < a.m, tmem + lofs + C::DV, half, dsteps, dv_scale, nt > 0, a.d);
         named_sync(2 + quarter, 64);
         if (ok && whole)
             unstage_rows<16>(sV, r0, a.m - w0, a.d,
@@ -970,9 +1063,9 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
         if (nt > 0 && ok) ok = warp_wait(&bar.done, 0, a.err, ERR_TIMEOUT_EPILOGUE);
         tc_fence_after();
         if (ok && whole)
-            stage_row<HD, BF>(sK, r, tmem + lofs + C::DK, half, dsteps, a.scale, nt > 0, keep);
+            stage_row<HD, BF>(sK, r, tmem + lofs + C::DK, half, dsteps, dk_scale, nt > 0, keep);
         else if (ok)
-            part_row<HD>(P.part_dk + part, j < a.m, tmem + lofs + C::DK, half, dsteps, a.scale, nt > 0, a.d);
+            part_row<HD>(P.part_dk + part, j < a.m, tmem + lofs + C::DK, half, dsteps, dk_scale, nt > 0, a.d);
         named_sync(2 + quarter, 64);
         if (ok && whole)
             unstage_rows<16>(sK, r0, a.m - w0, a.d,
@@ -1142,6 +1235,10 @@ cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
     smem = std::max(smem, fixed + p.kv_stages * stage);
     if ((e = raise_smem(k_grad<HD, BF>, kSmemLimit, ready)) != cudaSuccess) return e;
     const int64_t q_blocks = (int64_t)p.q_tiles * a.H * a.B, k_blocks = (int64_t)p.k_tiles * a.G * a.B;
+    if (!BF) {
+        k_grad_range<HD / 8><<<(unsigned)(q_blocks + k_blocks), kRowThreads, 0, s>>>(p);
+        count_launch();
+    }
     if (p.exact_delta) {
         const size_t least = 1024 + sizeof(GradBars) + sizeof(float) * kTile + bias;
         p.delta_stages = 2 * (ring_stages(least, Q::kTileBytes) / 2);

@@ -52,6 +52,9 @@ struct GradArgs {
     // (rows (b, head, token); delta: rows of rows), joined in order
     int q_splits, k_splits;
     float *part_dq, *part_dk, *part_dv, *part_delta;
+    // float16: the largest norm of a row in each tile of dO, [B][H][q_tiles], and of a counted
+    // row in each tile of V, [B][G][k_tiles] (k_grad_range)
+    float *q_range, *v_range;
     int stages, kv_stages, delta_stages, scratch_rows;     // set at launch
     int dout_vec, o_vec, dq_vec, dk_vec, dv_vec;   // rows take 16-byte accesses
 };

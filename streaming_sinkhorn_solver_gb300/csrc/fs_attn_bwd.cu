@@ -30,7 +30,7 @@
 //
 // p and ds are rounded to the operands' 16 bits, sums are float32: in bfloat16 dq, dk and
 // dv are 0.25 % off in the 2-norm, of which 0.17 % is their own rounding.  In float16 both
-// are multiplied by powers of two first (kProbShift, range_shift), which the results' last
+// are multiplied by powers of two first (kGradShift, range_shift), which the results' last
 // factors take back: ds goes with dO, whose size is the training's choice, and as it is would
 // be subnormal (dq and dk 0.8 % off at |dO| = 1e-4) or infinite.
 //
@@ -316,9 +316,9 @@ __device__ __forceinline__ int range_shift(const float* q, int nq, const float* 
 }
 __device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// p of grad_keys in float16 is multiplied by 2^kProbShift: in full down to 2^-28, and no more
+// p of grad_keys in float16 is multiplied by 2^kGradShift: in full down to 2^-28, and no more
 // than the rounding of x can take it past 1 would make it infinite
-constexpr int kProbShift = 14;
+constexpr int kGradShift = 14;
 
 // ---------------------------------------------------------------------------
 
@@ -955,12 +955,12 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
         const uint32_t lofs = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + lofs + C::S + half * NC, tDP = tmem + lofs + C::DP + half * NC;
         const float scale2 = least_scale(a);
-        // float16: p and ds are 2^kProbShift and 2^shift times as large
+        // float16: p and ds are 2^kGradShift and 2^shift times as large
         const float* q_range = P.q_range + ((int64_t)b * a.H + g * a.R) * P.q_tiles;
         const int shift = BF ? 0
                              : range_shift(q_range, a.R * P.q_tiles,
                                            P.v_range + ((int64_t)b * a.G + g) * P.k_tiles, P.k_tiles);
-        const float ds_over_p = power2(shift - (BF ? 0 : kProbShift));
+        const float ds_over_p = power2(shift - (BF ? 0 : kGradShift));
         bool ok = true;
         int h = g * a.R + t0 / per_head, qt = t0 % per_head;
         for (int t = 0; t < nt; ++t) {
@@ -993,7 +993,7 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
                         mul = 1.f;
                     }
                 }
-                if (!BF) add += (float)kProbShift;
+                if (!BF) add += (float)kGradShift;
                 const uint64_t mul2 = pk(mul, mul), add2 = pk(add, add);
 #pragma unroll
                 for (int c = 0; c < NC; c += 2) {
@@ -1049,7 +1049,7 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
         tc_fence_after();
         const bool whole = P.k_splits == 1;
         const int64_t part = ((((int64_t)split * a.B + b) * a.G + g) * a.m + j) * a.d;
-        const float dv_scale = BF ? 1.f : power2(-kProbShift);
+        const float dv_scale = BF ? 1.f : power2(-kGradShift);
         const float dk_scale = BF ? a.scale : a.scale * power2(-shift);
         if (ok && whole)
             stage_row<HD, BF>(sV, r, tmem + lofs + C::DV, half, dsteps, dv_scale, nt > 0, keep);

@@ -18,9 +18,9 @@
 // wait that P in the columns of S costs).
 //
 // The reference is the running maximum, moved only when a row's maximum grew
-// by more than 2^8 (p then stays below 256, which both types and the float32
-// sums hold with the same relative precision); the rare move rescales O_t in
-// TMEM.  P is rounded to the operands' 16 bits, the sum of p is not: out is 0.22 % off
+// by more than 2^8 (p then stays below 256 times the power of two that
+// kProbShift<BF> adds, which the types and the float32 sums hold); the rare move rescales
+// O_t in TMEM.  P is rounded to the operands' 16 bits, the sum of p is not: out is 0.22 % off
 // in the 2-norm in bfloat16, of which 0.17 % is the rounding of out itself.
 //
 // Bound: heads of 128 by the products (4 x 4096 x 8192, 16 heads, bfloat16: 720 us,
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
                         tmem_st16(tO + c, u);
                     }
                 }
-                const float base = add - (ref == -INFINITY ? 0.f : ref);
+                const float base = add + kProbShift<BF> - (ref == -INFINITY ? 0.f : ref);
                 const uint64_t mul2 = pk(mul, mul), base2 = pk(base, base);
                 uint64_t s0 = 0, s1 = 0;
 #pragma unroll
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int64_t row = ((int64_t)b * a.H + h) * a.n + i;
             if (live) {
-                const float lse2 = sum == 0.f ? -INFINITY : ref + lg2(sum);
+                const float lse2 = sum == 0.f ? -INFINITY : ref - kProbShift<BF> + lg2(sum);
                 if (P.splits > 1)
                     P.part.lse2[split * P.part.rows + row] = lse2;
                 else

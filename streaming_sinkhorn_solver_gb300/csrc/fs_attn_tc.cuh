@@ -172,6 +172,14 @@ __device__ __forceinline__ void mma_over_tokens(uint32_t d_tmem, uint32_t a_tmem
                    accumulate || x != 0);
 }
 
+// Forward, p = 2^{x - ref + kProbShift}: up to 2^8 without the shift, whose largest value
+// float16 would use half of its range for.  With it float16 holds p in full from 2^-21 of
+// the reference's weight on and rounds to multiples of 2^-31 of it below (without it from
+// 2^-14, and weights below 2^-25 were in the sum of p but not in out: all that 200000 keys 18
+// below one other bring).  The type's end, 65504, is above 2^15.  bfloat16 has float32's range.
+template <bool BF>
+constexpr float kProbShift = BF ? 0.f : 7.f;
+
 // two floats rounded to one register, x in the low half
 template <bool BF>
 __device__ __forceinline__ uint32_t pack16(float x, float y) {

@@ -59,6 +59,40 @@ def exact(c, how, dout=None):
     return r
 
 
+def check_out(c, how, one=None):
+    """`one`: the same call with the entries that c repeats once."""
+    out, lse = fs.fs_cross_attention(c["q"], c["k"], c["v"], **how)
+    want = exact(one or c, how)
+    u = 2.0 ** -11
+    # relative error of p from scores of up to 32, summed in float32 over d <= 128 terms
+    e = 2 * (128 + 8) * 2.0 ** -24 * 32 + 2.0 ** -16
+    tol = u * want["out"].abs() + (u + e) * want["pv"] + 2.0 ** -32 * want["v"] + 2.0 ** -24
+    over = (out.to(F64) - want["out"]).abs() - tol
+    assert float(over.max()) <= 0, f"{float(over.max()):.3g} over the bound, out about {float(want['out'].mean()):.3g}"
+    assert float((lse.to(F64) - want["lse"]).abs().max()) <= e
+
+
+@pytest.mark.parametrize("B,n,H", [(1, 1, 1), (4097, 1, 1), (1, 300, 1), (1, 300, 80)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_small_weights_reach_the_output(B, n, H, d):
+    """One heavy key with value 0 at the start, 200000 keys 18 below it: they bring all that
+    `out` holds, 0.3 % of the weight.  (2^-32 each is 1.6 % of that.)  With 4097 sequences
+    or 80 heads the keys are not split, and all are weighted against the heavy one."""
+    m = 200001
+    g = torch.Generator(device="cuda").manual_seed(51)
+    c = {x: torch.zeros(1, t, 1, d, dtype=HF, device="cuda") for x, t in (("q", n), ("k", m), ("v", m))}
+    c["q"][..., 0], c["k"][:, 0, :, 0] = 6.0, 3.0
+    c["v"][:, 1:] = (0.5 + torch.rand(1, m - 1, 1, d, generator=g, device="cuda")).to(HF)
+    many = {x: y.expand(B, -1, H if x == "q" else 1, -1) for x, y in c.items()}
+    check_out(many, dict(scale=1.0), c)
+
+
+@pytest.mark.parametrize("n,H,G", [(2, 4, 2), (200, 4, 2)])
+def test_spread_scores(n, H, G):
+    c, how, _ = make(2, n, 3000, H, G, 64, HF, lens=[3000, 2900], drop=0.1, seed=52, gain=6.0)
+    check_out(c, how)
+
+
 # (n, m): delta from the scores, from out, few blocks with many tiles, sums that many tiles share
 SHAPES = [(200, 300, 4, 2, 64, 0), (200, 300, 4, 2, 64, 16), (130, 1500, 4, 2, 128, 0),
           (130, 1500, 4, 2, 80, 16), (40, 3100, 4, 2, 80, 16), (40, 3100, 2, 2, 64, 0),

@@ -144,6 +144,9 @@ fs_status fs_shard_range(int64_t rows, int64_t unit, int32_t shards, int32_t s, 
  * (FS_ERR_UNSUPPORTED otherwise), and the library does not order the
  * captured work against its other calls: replays share the workspace with
  * every call on the device, so the caller orders them (one stream, or events).
+ * A later call may outgrow the workspace: the memory that captured calls use is
+ * then kept beside the larger one.  fs_release frees both, so graphs are not
+ * replayed after it.
  * The reports, fs_hvp_x and fs_check synchronise and cannot be captured.
  */
 
@@ -409,7 +412,7 @@ typedef struct fs_attention {
  * against many keys (single tokens against a cache) take a kernel that splits
  * the keys over the GPU.
  * Enqueued on `stream`; can be captured in a CUDA graph after one call of
- * the same sizes outside the capture.
+ * the same sizes outside the capture (see "CUDA graphs" above).
  * Errors: FS_ERR_INVALID_ARG for null or host pointers, sizes, strides or
  * options out of range; FS_ERR_UNSUPPORTED for more than 2^31 - 1 tiles of
  * work; FS_ERR_OOM, FS_ERR_CUDA, FS_ERR_TIMEOUT (from fs_check) as above.
@@ -627,7 +630,8 @@ int64_t fs_workspace_bytes(int64_t n, int64_t m, int32_t d, int32_t k, const fs_
  * device.  Returns FS_OK, FS_ERR_TIMEOUT or FS_ERR_CUDA. */
 fs_status fs_check(void* stream);
 
-/* Free the workspaces of every device (synchronises each). */
+/* Free the workspaces of every device (synchronises each).  Graphs with captured
+ * calls must not be replayed afterwards. */
 fs_status fs_release(void);
 
 /* Message for the calling thread's last non-OK status ("" if none). */

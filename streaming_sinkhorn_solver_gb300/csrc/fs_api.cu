@@ -73,7 +73,10 @@ fs_status end_call(Call& c) {
 fs_status ensure_capacity(Call& c) {
     Workspace& w = *c.ws;
     const size_t bytes = c.L.off;
-    if (bytes <= w.cap) return FS_OK;
+    if (bytes <= w.cap) {
+        w.captured = w.captured || (c.capturing && bytes > 0);
+        return FS_OK;
+    }
     if (c.capturing)
         return fail(FS_ERR_UNSUPPORTED,
                     "the workspace (%zu bytes) must be grown before graph capture: make one call "
@@ -81,9 +84,13 @@ fs_status ensure_capacity(Call& c) {
     // grow: wait for every user of the old arena, then replace it
     if (w.base) {
         FS_CUDA(cudaDeviceSynchronize());
-        FS_CUDA(cudaFree(w.base));
+        if (w.captured)
+            w.kept.push_back(w.base);
+        else
+            FS_CUDA(cudaFree(w.base));
         w.base = nullptr;
         w.cap = 0;
+        w.captured = false;
     }
     const size_t want = bytes + bytes / 8;
     cudaError_t e = cudaMalloc(&w.base, want);
@@ -538,6 +545,12 @@ fs_status fs_release(void) {
         if (w.base) FS_CUDA(cudaFree(w.base));
         w.base = nullptr;
         w.cap = 0;
+        w.captured = false;
+        while (!w.kept.empty()) {
+            char* p = w.kept.back();
+            w.kept.pop_back();
+            FS_CUDA(cudaFree(p));
+        }
     }
     FS_CUDA(cudaSetDevice(cur));
     return FS_OK;

@@ -44,6 +44,10 @@ struct Workspace {
     std::mutex mu;
     char* base = nullptr;
     size_t cap = 0;
+    // A captured call leaves addresses of the arena in its graph: such an arena is kept
+    // when a larger one takes its place (until fs_release).
+    bool captured = false;
+    std::vector<char*> kept;
     cudaEvent_t done = nullptr;        // recorded at the end of every call
     cudaStream_t last_stream = nullptr;
     bool used = false;

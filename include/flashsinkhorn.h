@@ -382,6 +382,8 @@ typedef enum {
  * Description of one attention call.  All arrays are DEVICE memory.  Strides
  * are in elements, {batch, token, head}; the d elements of a head are
  * contiguous; strides are not negative, and an input may repeat (stride 0).
+ * The rows of a result do not overlap: of its axes of more than one entry, taken
+ * by rising stride, each steps over all that the ones before it span.
  * Tensors whose address and strides are multiples of 16 bytes and whose d is
  * a multiple of 8 are read in place; others are first copied to the
  * workspace.

@@ -73,11 +73,19 @@ fs_status view(int dev, View& w, const void* p, const int64_t* stride, int64_t b
     w.sb = stride[0];
     w.st = stride[1];
     w.sh = stride[2];
-    const int64_t size[3] = {batch, tokens, heads};
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 3; ++i)
         if (stride[i] < 0) return fail(FS_ERR_INVALID_ARG, "%s has a negative stride", name);
-        if (out && size[i] > 1 && stride[i] < d)
-            return fail(FS_ERR_INVALID_ARG, "the rows of %s overlap", name);
+    if (!out || batch == 0 || tokens == 0) return FS_OK;
+    // A result's axes by rising stride: each steps over all that the ones before it span.
+    struct Axis {
+        int64_t size, stride;
+    } axis[3] = {{batch, stride[0]}, {tokens, stride[1]}, {heads, stride[2]}};
+    std::sort(axis, axis + 3, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
+    double span = d;        // (products of two sizes may pass 64 bits)
+    for (const Axis& x : axis) {
+        if (x.size == 1) continue;
+        if ((double)x.stride < span) return fail(FS_ERR_INVALID_ARG, "the rows of %s overlap", name);
+        span += (double)x.stride * (double)(x.size - 1);
     }
     return FS_OK;
 }

@@ -1,4 +1,5 @@
-"""Cross attention on the GPU where a result could be lost or stale: expanded tables."""
+"""Cross attention on the GPU where a result could be lost or stale: expanded tables, results
+that overlap."""
 import math
 
 import pytest
@@ -51,3 +52,41 @@ def test_an_expanded_row_has_a_gradient_for_each_head(n, m, side):
     if n and m:
         check(c, stored, dout)
         check(c, how, dout)
+
+
+# (batch, token, head) strides of (2, 3, 4, 64) tensors
+OVERLAPS = [(2048, 64, 64), (2048, 192, 64), (2048, 256, 32), (256, 256, 64), (64, 256, 128), (700, 256, 64),
+            (0, 256, 64), (2048, 64, 0), (1024, 63, 2048)]
+APART = [(768, 256, 64), (2048, 256, 64), (64, 512, 128), (64, 128, 384), (768, 64, 192), (256, 512, 64),
+         (5000, 1000, 101)]
+
+
+@pytest.mark.parametrize("name", ["out", "dq", "dk", "dv"])
+def test_results_that_overlap_are_refused(name):
+    c, how, dout = make(2, 3, 3, 4, 4, 64, BF, seed=42)
+    a = fs.fs_cross_attention(c["q"], c["k"], c["v"], **how)
+    want = dict(zip(("out", "lse", "dq", "dk", "dv"),
+                    (*a, *fs.fs_cross_attention_grad(c["q"], c["k"], c["v"], *a, dout, **how))))
+
+    def call(strides):
+        store = torch.zeros(20000, dtype=BF, device="cuda")
+        x = store.as_strided((2, 3, 4, 64), strides + (1,))
+        if name == "out":
+            fs.fs_cross_attention(c["q"], c["k"], c["v"], out=x, **how)
+        else:
+            fs.fs_cross_attention_grad(c["q"], c["k"], c["v"], *a, dout, **{name: x}, **how)
+        return x
+
+    for strides in OVERLAPS:
+        with pytest.raises(fs.FlashSinkhornError, match="overlap"):
+            call(strides)
+    for strides in APART:
+        assert torch.equal(call(strides), want[name])
+
+
+def test_a_result_of_one_entry_may_have_any_stride_there():
+    c, how, _ = make(1, 3, 5, 1, 1, 64, BF, seed=43)
+    store = torch.zeros(1000, dtype=BF, device="cuda")
+    x = store.as_strided((1, 3, 1, 64), (0, 64, 0, 1))
+    want, _ = fs.fs_cross_attention(c["q"], c["k"], c["v"], **how)
+    assert torch.equal(fs.fs_cross_attention(c["q"], c["k"], c["v"], out=x, **how)[0], want)

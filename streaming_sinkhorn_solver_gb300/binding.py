@@ -683,7 +683,7 @@ def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, stri
         far = size // 2
         if bias.shape[0] > 1 and bias.stride(0) == 0:
             # stride 0 is one row with one gradient; an expanded row has one for each head
-            with _att_on(stream):
+            with _att_on(stream, q):
                 bias = bias.contiguous()
         bias_p = bias.data_ptr()
         bias_stride = 0 if bias.shape[0] == 1 else bias.stride(0)
@@ -723,18 +723,24 @@ def _att_stream(stream, like) -> int:
     return _RAW_STREAM[0](like.get_device())
 
 
-def _att_on(stream):
-    """Where torch allocates and runs what belongs to a call on `stream`."""
+def _att_on(stream, like):
+    """Where torch allocates and runs what belongs to a call on `stream`: the same stream,
+    so that memory goes to and comes from its own work alone."""
     import torch
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None)
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    handle = int(getattr(stream, "cuda_stream", stream))
+    if handle in (0, 1):         # both the legacy default stream
+        return torch.cuda.stream(torch.cuda.default_stream(like.device))
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, device=like.device))
 
 
 def _att_empty(like, shape, dtype, stream):
     """A result, allocated for the stream that writes it."""
     import torch
-    if stream is None:
+    if stream is None or not like.is_cuda:
         return torch.empty(shape, dtype=dtype, device=like.device)
-    with _att_on(stream):
+    with _att_on(stream, like):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 

@@ -1,5 +1,5 @@
 """Cross attention on the GPU where a result could be lost or stale: expanded tables, results
-that overlap."""
+that overlap, streams of other libraries."""
 import math
 
 import pytest
@@ -90,3 +90,40 @@ def test_a_result_of_one_entry_may_have_any_stride_there():
     x = store.as_strided((1, 3, 1, 64), (0, 64, 0, 1))
     want, _ = fs.fs_cross_attention(c["q"], c["k"], c["v"], **how)
     assert torch.equal(fs.fs_cross_attention(c["q"], c["k"], c["v"], out=x, **how)[0], want)
+
+
+class Foreign:
+    """What other libraries' stream objects have in common with torch's."""
+
+    def __init__(self, stream):
+        self.cuda_stream = stream.cuda_stream
+
+
+@pytest.mark.parametrize("kind", [lambda s: s, lambda s: s.cuda_stream, Foreign])
+def test_results_belong_to_the_stream_that_writes_them(kind):
+    """Memory that pending work of the current stream still writes to, although it was freed
+    there, is not handed to a call on another stream."""
+    c, how, dout = make(2, 150, 300, 4, 2, 64, BF, nb=16, far=50, seed=44)
+    a = fs.fs_cross_attention(c["q"], c["k"], c["v"], **how)
+    want = [*a, *fs.fs_cross_attention_grad(c["q"], c["k"], c["v"], *a, dout, **how)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    pending = [torch.empty_like(x) for x in want for _ in range(4)]
+    torch.cuda._sleep(200_000_000)         # 0.1 s of the current stream
+    for x in pending:
+        x.fill_(math.nan)
+    del pending, x
+    b = fs.fs_cross_attention(c["q"], c["k"], c["v"], stream=kind(side), **how)
+    got = [*b, *fs.fs_cross_attention_grad(c["q"], c["k"], c["v"], *b, dout, stream=kind(side), **how)]
+    torch.cuda.synchronize()
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_the_default_stream_by_its_handle(handle):
+    c, how, _ = make(1, 20, 40, 2, 2, 64, BF, seed=45)
+    want = fs.fs_cross_attention(c["q"], c["k"], c["v"], **how)
+    got = fs.fs_cross_attention(c["q"], c["k"], c["v"], stream=handle, **how)
+    torch.cuda.synchronize()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])

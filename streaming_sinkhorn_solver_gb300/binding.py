@@ -639,18 +639,10 @@ _DTYPES = {}
 
 def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, strides,
                stream) -> fs_attention:
-    """Checked description of a call (see the C header for each field);
+    """Checked description of a call of _att_inputs (see the C header for each field);
     `strides` are those of out, dout, dq, dk and dv."""
     import torch
-    if not _DTYPES:
-        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1})
-    dtype = _DTYPES.get(getattr(q, "dtype", None))
-    if dtype is None or not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise TypeError("q must be a bfloat16 or float16 CUDA tensor")
-    if q.dim() != 4:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected (batch, n, heads, d)")
-    if k.dim() != 4:
-        raise ValueError(f"k has shape {tuple(k.shape)}, expected (batch, m, kv_heads, d)")
+    dtype = _DTYPES[q.dtype]
     batch, n, heads, d = q.shape
     m, kv_heads = k.shape[1], k.shape[2]
     qs = _att_strides(q, "q", q.shape, q)
@@ -660,7 +652,7 @@ def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, stri
     if kv_len is not None:
         len_p = _i_ptr(kv_len, "kv_len", (batch,), torch.int32)
     if key_mask is not None:
-        if not (key_mask.is_cuda and key_mask.dtype in (torch.bool, torch.uint8)):
+        if not (isinstance(key_mask, torch.Tensor) and key_mask.is_cuda and key_mask.dtype in (torch.bool, torch.uint8)):
             raise TypeError("key_mask must be a bool or uint8 CUDA tensor")
         if tuple(key_mask.shape) != (batch, m):
             raise ValueError(f"key_mask has shape {tuple(key_mask.shape)}, expected {(batch, m)}")
@@ -670,8 +662,10 @@ def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, stri
     if (bias is None) != (bias_buckets is None):
         raise TypeError("bias and bias_buckets come together")
     if bias is not None:
-        if not (bias.is_cuda and bias.dtype == q.dtype):
+        if not (isinstance(bias, torch.Tensor) and bias.is_cuda and bias.dtype == q.dtype):
             raise TypeError(f"bias must be a CUDA tensor of {q.dtype}")
+        if not isinstance(bias_buckets, torch.Tensor):
+            raise TypeError("bias_buckets must be an int32 CUDA tensor")
         if bias.dim() != 2 or bias.shape[0] not in (1, heads) or bias.shape[1] < 1:
             raise ValueError(f"bias has shape {tuple(bias.shape)}, expected ({heads} or 1, buckets)")
         nb = bias.shape[1]
@@ -696,6 +690,23 @@ def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, stri
                          len_p, mask_p, mask_stride, bias_p, bias_stride, buckets_p, pos_p)
     at.table = bias      # a copy lives until the call is enqueued
     return at
+
+
+def _att_inputs(q, k, v) -> None:
+    """Refuses what no result could be made like."""
+    import torch
+    if not _DTYPES:
+        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1})
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES or not q.is_cuda:
+        raise TypeError("q must be a bfloat16 or float16 CUDA tensor")
+    if q.dim() != 4:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected (batch, n, heads, d)")
+    if q.shape[3] < 1:
+        raise ValueError("q has heads of no elements")
+    if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor):
+        raise TypeError(f"k and v must be {q.dtype} tensors on {q.device}")
+    if k.dim() != 4:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected (batch, m, kv_heads, d)")
 
 
 def _att_strides(x, name: str, shape, like):
@@ -738,7 +749,7 @@ def _att_on(stream, like):
 def _att_empty(like, shape, dtype, stream):
     """A result, allocated for the stream that writes it."""
     import torch
-    if stream is None or not like.is_cuda:
+    if stream is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
     with _att_on(stream, like):
         return torch.empty(shape, dtype=dtype, device=like.device)
@@ -763,8 +774,8 @@ def fs_cross_attention(q, k, v, *, scale: Optional[float] = None, kv_len=None, k
     do not count may hold anything.
     """
     import torch
-    if out is None:
-        out = _att_empty(q, q.shape, q.dtype, stream) if _is_torch(q) else q
+    _att_inputs(q, k, v)
+    out = _att_empty(q, q.shape, q.dtype, stream) if out is None else out
     at = _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos,
                     (*_att_strides(out, "out", q.shape, q), *_NO_STRIDES * 4), stream)
     rows = (q.shape[0], q.shape[2], q.shape[1])
@@ -786,6 +797,7 @@ def fs_cross_attention_grad(q, k, v, out, lse, dout, *, scale: Optional[float] =
     """Gradients of fs_cross_attention for the gradient dout of its out; out
     and lse as it returned them, the other arguments as it got them.  Returns
     (dq, dk, dv, dbias), each as its input (dbias None without a bias)."""
+    _att_inputs(q, k, v)
     dq = _att_empty(q, q.shape, q.dtype, stream) if dq is None else dq
     dk = _att_empty(k, k.shape, q.dtype, stream) if dk is None else dk
     dv = _att_empty(v, v.shape, q.dtype, stream) if dv is None else dv
@@ -797,7 +809,7 @@ def fs_cross_attention_grad(q, k, v, out, lse, dout, *, scale: Optional[float] =
         dbias = None
     else:
         dbias = _att_empty(q, bias.shape, q.dtype, stream) if dbias is None else dbias
-        if not (dbias.is_cuda and dbias.dtype == q.dtype and dbias.is_contiguous()
+        if not (_is_torch(dbias) and dbias.is_cuda and dbias.dtype == q.dtype and dbias.is_contiguous()
                 and dbias.shape == bias.shape):
             raise TypeError(f"dbias must be a contiguous {q.dtype} tensor of shape "
                             f"{tuple(bias.shape)}")

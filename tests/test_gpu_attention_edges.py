@@ -1,7 +1,8 @@
 """Cross attention on the GPU where a result could be lost or stale: expanded tables, results
-that overlap, streams of other libraries."""
+that overlap, streams of other libraries, arguments of other kinds."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -127,3 +128,44 @@ def test_the_default_stream_by_its_handle(handle):
     got = fs.fs_cross_attention(c["q"], c["k"], c["v"], stream=handle, **how)
     torch.cuda.synchronize()
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+class Tagged(torch.Tensor):
+    """A tensor of a user's own class."""
+
+
+@pytest.mark.parametrize("n", [2, 150])
+def test_tensors_of_a_subclass_are_read_and_not_written(n):
+    c, how, dout = make(2, n, 300, 4, 2, 64, BF, nb=16, far=50, seed=46)
+    a = fs.fs_cross_attention(c["q"], c["k"], c["v"], **how)
+    want = [*a, *fs.fs_cross_attention_grad(c["q"], c["k"], c["v"], *a, dout, **how)]
+    own = {x: y.clone().as_subclass(Tagged) for x, y in c.items()}
+    b = fs.fs_cross_attention(own["q"], own["k"], own["v"], **how)
+    got = [*b, *fs.fs_cross_attention_grad(own["q"], own["k"], own["v"], *b, dout, **how)]
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
+    for x, y in c.items():
+        assert torch.equal(y, own[x].as_subclass(torch.Tensor))
+    assert b[0].data_ptr() != own["q"].data_ptr()
+
+
+def test_arguments_of_other_kinds_are_refused():
+    c, how, dout = make(2, 3, 5, 4, 2, 64, BF, nb=8, far=9)
+    q, k, v = c["q"], c["k"], c["v"]
+    out, lse = fs.fs_cross_attention(q, k, v, **how)
+    for other in (np.zeros((2, 5, 2, 64), np.float16), [1.0], None):
+        for args in ((other, k, v), (q, other, v), (q, k, other)):
+            with pytest.raises(TypeError):
+                fs.fs_cross_attention(*args, **how)
+            with pytest.raises(TypeError):
+                fs.fs_cross_attention_grad(*args, out, lse, dout, **how)
+    for name, other in (("key_mask", np.ones((2, 5), bool)), ("key_mask", [[1] * 5] * 2),
+                        ("bias", np.zeros((4, 8), np.float16)), ("bias_buckets", [0] * 19),
+                        ("kv_len", [5, 5]), ("q_pos", 3)):
+        with pytest.raises(TypeError):
+            fs.fs_cross_attention(q, k, v, **dict(how, **{name: other}))
+    with pytest.raises(TypeError):
+        fs.fs_cross_attention_grad(q, k, v, out, lse, dout, dbias=np.zeros((4, 8), np.float16), **how)
+    for shape in ((2, 3, 4, 0), (3, 4, 64)):
+        with pytest.raises(ValueError):
+            fs.fs_cross_attention(q.new_zeros(shape), k, v, **how)

@@ -642,6 +642,7 @@ def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, stri
     """Checked description of a call of _att_inputs (see the C header for each field);
     `strides` are those of out, dout, dq, dk and dv."""
     import torch
+    at = fs_attention()
     dtype = _DTYPES[q.dtype]
     batch, n, heads, d = q.shape
     m, kv_heads = k.shape[1], k.shape[2]
@@ -652,7 +653,8 @@ def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, stri
     if kv_len is not None:
         len_p = _i_ptr(kv_len, "kv_len", (batch,), torch.int32)
     if key_mask is not None:
-        if not (isinstance(key_mask, torch.Tensor) and key_mask.is_cuda and key_mask.dtype in (torch.bool, torch.uint8)):
+        if not (isinstance(key_mask, torch.Tensor) and key_mask.is_cuda
+                and key_mask.dtype in (torch.bool, torch.uint8)):
             raise TypeError("key_mask must be a bool or uint8 CUDA tensor")
         if tuple(key_mask.shape) != (batch, m):
             raise ValueError(f"key_mask has shape {tuple(key_mask.shape)}, expected {(batch, m)}")
@@ -675,20 +677,19 @@ def _attention(q, k, v, scale, kv_len, key_mask, bias, bias_buckets, q_pos, stri
         if size % 2 == 0:
             raise ValueError("bias_buckets must have 2 max_distance + 1 entries")
         far = size // 2
-        if bias.shape[0] > 1 and bias.stride(0) == 0:
+        bias_stride = 0 if bias.shape[0] == 1 else bias.stride(0)
+        if bias_stride == 0 and bias.shape[0] > 1:
             # stride 0 is one row with one gradient; an expanded row has one for each head
             with _att_on(stream, q):
-                bias = bias.contiguous()
+                bias = at.table = bias.contiguous()     # lives until the call is enqueued
+            bias_stride = nb
         bias_p = bias.data_ptr()
-        bias_stride = 0 if bias.shape[0] == 1 else bias.stride(0)
         buckets_p = _i_ptr(bias_buckets, "bias_buckets", (size,), torch.int32)
         if q_pos is not None:
             pos_p = _i_ptr(q_pos, "q_pos", (batch,), torch.int32)
-    at = fs_attention()
     _ATTENTION.pack_into(at, 0, dtype, heads, kv_heads, d, batch, n, m,
                          d ** -0.5 if scale is None else scale, nb, far, 0, *qs, *ks, *vs, *strides,
                          len_p, mask_p, mask_stride, bias_p, bias_stride, buckets_p, pos_p)
-    at.table = bias      # a copy lives until the call is enqueued
     return at
 
 
@@ -697,13 +698,13 @@ def _att_inputs(q, k, v) -> None:
     import torch
     if not _DTYPES:
         _DTYPES.update({torch.bfloat16: 0, torch.float16: 1})
-    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES or not q.is_cuda:
+    Tensor = torch.Tensor
+    if not isinstance(q, Tensor) or q.dtype not in _DTYPES or not q.is_cuda:
         raise TypeError("q must be a bfloat16 or float16 CUDA tensor")
-    if q.dim() != 4:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected (batch, n, heads, d)")
-    if q.shape[3] < 1:
-        raise ValueError("q has heads of no elements")
-    if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor):
+    shape = q.shape
+    if len(shape) != 4 or shape[3] < 1:
+        raise ValueError(f"q has shape {tuple(shape)}, expected (batch, n, heads, d)")
+    if not isinstance(k, Tensor) or not isinstance(v, Tensor):
         raise TypeError(f"k and v must be {q.dtype} tensors on {q.device}")
     if k.dim() != 4:
         raise ValueError(f"k has shape {tuple(k.shape)}, expected (batch, m, kv_heads, d)")

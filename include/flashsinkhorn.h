@@ -364,7 +364,9 @@ int64_t fs_hvp_workspace_bytes(int64_t n, int64_t m, int32_t d, const fs_options
  * share, bias_stride = 0) of the type of q.  Its n x m form is never stored,
  * and neither are the scores nor their gradients.  Bucket numbers outside
  * [0, n_buckets) are taken to the nearest end.  A bias below -1e30 forbids
- * its pairs, as -inf does.
+ * its pairs, as -inf does; in float16 only -inf does, as its lowest value,
+ * -65504, is a finite bias (a row with no other one is a softmax of its scores,
+ * which float32 then rounds to multiples of 2^-7).
  *
  * Numerics: products of 16-bit operands are summed in float32; the softmax,
  * lse and every sum over keys or queries are float32; the probabilities (and

@@ -767,7 +767,8 @@ def fs_cross_attention(q, k, v, *, scale: Optional[float] = None, kv_len=None, k
     kv_len        int32 (batch,): keys j >= kv_len[b] do not count
     key_mask      bool or uint8 (batch, m): keys with 0 do not count
     bias          learned relative position bias, (heads or 1, buckets) of q's
-                  type: z_ij += bias[h, bias_buckets[clamp(j - (q_pos[b] + i), -D, D) + D]]
+                  type: z_ij += bias[h, bias_buckets[clamp(j - (q_pos[b] + i), -D, D) + D]];
+                  -inf forbids its pairs (in bfloat16 anything below -1e30 too)
     bias_buckets  int32 (2 D + 1,), e.g. from fs_relative_buckets, D <= 2048
     q_pos         int32 (batch,): position of each sequence's first query (0 if
                   None), e.g. the step of a decoder that sends one token at a time

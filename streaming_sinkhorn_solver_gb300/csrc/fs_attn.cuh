@@ -66,9 +66,10 @@ __device__ __forceinline__ int bucket_of(const Args& a, int64_t rel) {
     return u < 0 ? 0 : (u < a.nb ? u : a.nb - 1);
 }
 
-// bias entry in base 2; entries below -1e30 (a type's lowest value stands for
+// bias entry in base 2; entries below -1e30 (bfloat16's lowest value stands for
 // "never" in additive masks) forbid their pairs as -inf does, so that such
-// rows stay empty instead of losing their scores to rounding
+// rows stay empty instead of losing their scores to rounding.  float16 ends at -65504, a
+// number like others: a row that has no other bias keeps its scores to 2^-7 in base 2.
 __device__ __forceinline__ float bias2(float v) {
     return v < -1e30f ? -INFINITY : v * (float)kLog2e;
 }

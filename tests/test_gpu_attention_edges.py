@@ -1,5 +1,5 @@
 """Cross attention on the GPU where a result could be lost or stale: expanded tables, results
-that overlap, streams of other libraries, arguments of other kinds."""
+that overlap, streams of other libraries, arguments of other kinds, lowest values."""
 import math
 
 import numpy as np
@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from streaming_sinkhorn_solver_gb300 import binding as fs
-from tests.test_gpu_attention import BF, HF, check, make
+from tests.test_gpu_attention import BF, HF, check, make, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +169,36 @@ def test_arguments_of_other_kinds_are_refused():
     for shape in ((2, 3, 4, 0), (3, 4, 64)):
         with pytest.raises(ValueError):
             fs.fs_cross_attention(q.new_zeros(shape), k, v, **how)
+
+
+@pytest.mark.parametrize("n", [2, 150])
+def test_rows_that_have_nothing_but_the_lowest_bias(n):
+    """In bfloat16 they are empty.  In float16 -65504 is a finite bias: a softmax of the scores,
+    which next to -94503 in base 2 are rounded to multiples of 2^-7.  p is then off by a
+    factor of up to 2^(4 * 2^-8) (its score, its row's, lse and its product with log2 e), 1.1 %,
+    ds too, and delta by as much of sum |dout v|; lse by its own rounding, 2^-8, twice."""
+    for dtype in (BF, HF):
+        c, how, dout = make(2, n, 300, 2, 2, 64, dtype, nb=8, far=20, seed=47)
+        how["bias"][1] = torch.finfo(dtype).min
+        out, lse = fs.fs_cross_attention(c["q"], c["k"], c["v"], **how)
+        dq, dk, dv, dbias = fs.fs_cross_attention_grad(c["q"], c["k"], c["v"], out, lse, dout, **how)
+        if dtype == BF:
+            assert bool((out[:, :, 1] == 0).all()) and bool((lse[:, 1] == -math.inf).all())
+            assert all(bool((x[:, :, 1] == 0).all()) for x in (dq, dk, dv)) and bool((dbias[1] == 0).all())
+            continue
+        ref = reference(c, how, dout)
+        p, do = 0.011, dout.cpu().double()
+        v = c["v"].cpu().double()[:, :, 1]
+        z = how["scale"] * torch.einsum("bic,bjc->bij", c["q"].cpu().double()[:, :, 1], c["k"].cpu().double()[:, :, 1])
+        w = z.softmax(-1)
+        tol = ref["tol"]["out"][:, :, 1] + p * 2 * torch.einsum("bij,bjc->bic", w, v.abs())
+        assert float(((out.cpu().double() - ref["out"])[:, :, 1].abs() - tol).max()) <= 0
+        assert float((lse.cpu().double() - ref["lse"])[:, 1].abs().max()) <= 2 * 2.0 ** -8
+        tol = ref["tol"]["dv"][:, :, 1] + p * torch.einsum("bij,bic->bjc", w, do[:, :, 1].abs())
+        assert float(((dv.cpu().double() - ref["dv"])[:, :, 1].abs() - tol).max()) <= 0
+        ds = p * 4 * w * torch.einsum("bic,bijc->bij", do[:, :, 1].abs(),
+                                      v.abs()[:, None] + (w @ v.abs())[:, :, None])
+        for name, x, tol in (("dq", dq, torch.einsum("bij,bjc->bic", ds, c["k"].cpu().double()[:, :, 1].abs())),
+                             ("dk", dk, torch.einsum("bij,bic->bjc", ds, c["q"].cpu().double()[:, :, 1].abs()))):
+            tol = ref["tol"][name][:, :, 1] + how["scale"] * tol
+            assert float(((x.cpu().double() - ref[name])[:, :, 1].abs() - tol).max()) <= 0, name

@@ -372,8 +372,8 @@ int64_t fs_hvp_workspace_bytes(int64_t n, int64_t m, int32_t d, const fs_options
  * lse and every sum over keys or queries are float32; the probabilities (and
  * the score gradients) are rounded once to the type of q as operands of the
  * next product, results once at the end.  In float16 the gradients' operands are
- * multiplied by powers of two for that, from the largest norms of the rows of
- * dout and v, so dout may be of any size.  Results are bitwise deterministic.
+ * multiplied by powers of two for that, from a bound on the score gradients, so
+ * dout may be of any size.  Results are bitwise deterministic.
  */
 typedef enum {
     FS_DTYPE_BF16 = 0,

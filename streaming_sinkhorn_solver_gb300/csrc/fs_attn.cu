@@ -380,8 +380,10 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     const size_t part_dq = c.L.take(q_part * a.B * a.H * a.n * a.d);
     const size_t part_delta = c.L.take(p.exact_delta ? q_part * blocks * kTile : 0);
     const size_t part_dk = c.L.take(k_part), part_dv = c.L.take(k_part);
-    const size_t q_range = c.L.take(a.bf16 ? 0 : sizeof(float) * blocks);
-    const size_t v_range = c.L.take(a.bf16 ? 0 : sizeof(float) * a.B * a.G * (size_t)p.k_tiles);
+    const size_t entry = a.bf16 ? 0 : sizeof(float);
+    const size_t q_range = c.L.take(entry * blocks * 4);
+    const size_t v_range = c.L.take(p.exact_delta ? 0 : entry * a.B * a.G * p.k_tiles);
+    const size_t part_top = c.L.take(p.exact_delta && p.q_splits > 1 ? entry * p.q_splits * blocks * kTile : 0);
     FS_TRY(begin_call(c, stream));
     FS_TRY(ensure_capacity(c));
     for (Input& x : inputs) FS_TRY(x.run(c, a));
@@ -395,6 +397,7 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     p.part_dv = c.at<float>(part_dv);
     p.q_range = c.at<float>(q_range);
     p.v_range = c.at<float>(v_range);
+    p.part_top = c.at<float>(part_top);
     a.err = c.ws->err_word;
     auto vec = [&](const View& w, int tokens, int heads) {
         return a.d % 8 == 0 && aligned16(w, a.B, tokens, heads);

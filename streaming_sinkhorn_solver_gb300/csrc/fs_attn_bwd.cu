@@ -32,12 +32,13 @@
 // dv are 0.25 % off in the 2-norm, of which 0.17 % is their own rounding.  In float16 both
 // are multiplied by powers of two first (kGradShift, range_shift), which the results' last
 // factors take back: ds goes with dO, whose size is the training's choice, and as it is would
-// be subnormal (dq and dk 0.8 % off at |dO| = 1e-4) or infinite.
+// be subnormal (dq and dk 0.8 % off at |dO| = 1e-4, 1500 keys) or infinite.  With the
+// bounds on ds that takes 1 to 6 % of the gradients' time.
 //
 // Measured: batch 4, 2048 x 2048, 16 heads, bfloat16: 264 us with heads of 64 (650
 // TFLOP/s of the five products; the chain of waits, exponentials and conversions of a
 // tile, 2000 cycles for 1100 of products), 370 us with heads of 128 (930 TFLOP/s of the
-// five, 1300 of the seven, 0.69 of the measured burst rate).
+// five, 1300 of the seven, 0.69 of the measured burst rate); in float16 283 and 401 us.
 #include "fs_attn_host.cuh"
 
 #include <atomic>
@@ -184,10 +185,45 @@ __device__ __forceinline__ void put_row(const Args& a, uint8_t* out, int r, floa
     *reinterpret_cast<uint4*>(out + (r >> 3) * 256 + (is_delta ? 128 : 0) + (r & 7) * 16) = three_terms(x);
 }
 
+// float16: the power of two that ds is multiplied with, over whole tiles, so that a bound on it
+// comes to [2^14, 2^15): the type then holds in full what is down to 2^-29 of that.  The
+// bound is 2 max |dO_i| max |v_j| of the queries and values that meet, or, where
+// k_grad_delta has formed all p dP, max |p_ij dP_ij| + |delta_i|.  Rows that are not finite
+// set none: they are lost with any.  A whole warp.
+__device__ __forceinline__ float range_max(const float* x, int count) {
+    float top = 0.f;
+#pragma unroll 4
+    for (int e = threadIdx.x & 31; e < count; e += 32) top = fmaxf(top, __ldg(x + e));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return top;
+}
+__device__ __forceinline__ int range_shift(const GradArgs& P, int b, int h, int tile, int tiles) {
+    const Args& a = P.a;
+    float bound = range_max(P.q_range + (((int64_t)b * a.H + h) * P.q_tiles + tile) * 4, 4 * tiles);
+    if (!P.exact_delta)
+        bound *= 2.f * range_max(P.v_range + ((int64_t)b * a.G + h / a.R) * P.k_tiles, P.k_tiles);
+    return bound > 0.f ? min(14 + 127 - (int)(__float_as_uint(bound) >> 23), 100) : 0;
+}
+__device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ float finite_or_0(float x) { return x < INFINITY ? x : 0.f; }
+// the entry of a warp's 32 queries of a tile
+__device__ __forceinline__ void put_range(const GradArgs& P, int64_t tile, int quarter, int lane, float x) {
+    x = finite_or_0(x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    if (lane == 0) P.q_range[tile * 4 + quarter] = x;
+}
+
+// p of grad_keys in float16 is multiplied by 2^kGradShift: in full down to 2^-28, and no more
+// than the rounding of x can take it past 1 would make it infinite
+constexpr int kGradShift = 14;
+
 // ---------------------------------------------------------------------------
 // The row values of 128 queries a block: delta_i = dO_i . O_i and lse_i.  Reads dO and O
 // once, LANES lanes of 8 elements to a row; bound by memory (4 x 2048 x 16 rows of 128: 68 MB
-// in 18 us from a cold cache).
+// in 18 us from a cold cache).  In float16 also the norms of dO and, in blocks of their own
+// behind those, of V.
 
 constexpr int kRowThreads = 256;
 
@@ -210,12 +246,62 @@ __device__ __forceinline__ void load8(const View& w, int64_t off, int c, int d, 
     u[3] = x.w;
 }
 
+// The largest norm of a counted value of a key tile
+template <int LANES>
+__device__ __forceinline__ void value_range(const GradArgs& P, int64_t blk) {
+    constexpr int kRows = 32 / LANES, kTurns = 16 / kRows;
+    __shared__ float sTop[kRowThreads / 32];
+    const Args& a = P.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tile = (int)(blk % P.k_tiles), g = (int)(blk / P.k_tiles % a.G), b = (int)(blk / P.k_tiles / a.G);
+    const uint4 w = tile_words(P.kt, b, tile, key_end(a, b));
+    const uint32_t word = warp < 2 ? w.x : warp < 4 ? w.y : warp < 6 ? w.z : w.w;    // of the warp's 16 keys
+    uint32_t u[kTurns][4];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int r = warp * 16 + k * kRows + lane / LANES;
+        // (V as the tensor map reads it: its rows take 16-byte loads)
+        load8(a.v, b * a.v.sb + ((int64_t)tile * kTile + r) * a.v.st + g * a.v.sh, 8 * (lane % LANES), a.d,
+              (word >> (r & 31)) & 1u, true, u[k]);
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        float x = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack16<false>(u[k][e]);
+            x = fmaf(f.x, f.x, x);
+            x = fmaf(f.y, f.y, x);
+        }
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        top = fmaxf(top, finite_or_0(x));
+    }
+#pragma unroll
+    for (int o = 16; o >= LANES; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) sTop[warp] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int k = 1; k < kRowThreads / 32; ++k) top = fmaxf(top, sTop[k]);
+        P.v_range[blk] = sqrtf(top);
+    }
+}
+
 template <int LANES, bool BF>
 __global__ void __launch_bounds__(kRowThreads) k_grad_rows(const __grid_constant__ GradArgs P) {
     constexpr int kRows = 32 / LANES, kTurns = 16 / kRows;      // rows of a warp at a time, of 16
-    __shared__ float sDelta[kTile];
+    __shared__ float sDelta[kTile], sNorm[BF ? 1 : kTile];
     const Args& a = P.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (!BF) {
+        const int queries = P.q_tiles * a.H * a.B;
+        if ((int)blockIdx.x >= queries) {
+            value_range<LANES>(P, (int)blockIdx.x - queries);
+            return;
+        }
+    }
     int blk = blockIdx.x;
     const int qt = blk % P.q_tiles;
     blk /= P.q_tiles;
@@ -230,95 +316,31 @@ __global__ void __launch_bounds__(kRowThreads) k_grad_rows(const __grid_constant
     }
 #pragma unroll
     for (int k = 0; k < kTurns; ++k) {
-        float dot = 0.f;
+        float dot = 0.f, norm = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float2 f = unpack16<BF>(u[k][e]), g = unpack16<BF>(v[k][e]);
             dot = fmaf(f.x, g.x, dot);
             dot = fmaf(f.y, g.y, dot);
+            if (!BF) norm = fmaf(f.x, f.x, fmaf(f.y, f.y, norm));
         }
+        const int r = warp * 16 + k * kRows + lane / LANES;
 #pragma unroll
-        for (int o = LANES / 2; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane % LANES == 0) sDelta[warp * 16 + k * kRows + lane / LANES] = dot;
+        for (int o = LANES / 2; o; o >>= 1) {
+            dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            if (!BF) norm += __shfl_xor_sync(0xffffffffu, norm, o);
+        }
+        if (lane % LANES == 0) sDelta[r] = dot;
+        if (!BF && lane % LANES == 0) sNorm[r] = norm;
     }
     __syncthreads();
     const int r = threadIdx.x & (kTile - 1);
     const bool second = threadIdx.x >= kTile;
-    put_row(a, P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowStride, r,
-            second ? -sDelta[r] : row_lse(a, b, h, (int64_t)qt * kTile + r), second);
+    const int64_t tile = ((int64_t)b * a.H + h) * P.q_tiles + qt;
+    put_row(a, P.rows + tile * kRowStride, r, second ? -sDelta[r] : row_lse(a, b, h, (int64_t)qt * kTile + r),
+            second);
+    if (!BF && !second) put_range(P, tile, warp, lane, sqrtf(sNorm[r]));
 }
-
-// float16: the largest norm of a row in each tile of dO and of a counted row in each of V,
-// for range_shift.  Rows that are not finite set no range: they are lost whatever it is.
-template <int LANES>
-__global__ void __launch_bounds__(kRowThreads) k_grad_range(const __grid_constant__ GradArgs P) {
-    constexpr int kRows = 32 / LANES, kTurns = 16 / kRows;      // rows of a warp at a time, of 16
-    __shared__ float sTop[kRowThreads / 32];
-    const Args& a = P.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int queries = P.q_tiles * a.H * a.B;
-    const bool keys = (int)blockIdx.x >= queries;
-    const int blk = blockIdx.x - (keys ? queries : 0);
-    const int tiles = keys ? P.k_tiles : P.q_tiles, heads = keys ? a.G : a.H;
-    const int tile = blk % tiles, h = blk / tiles % heads, b = blk / tiles / heads;
-    const View& w = keys ? a.v : a.dout;      // in place or copied, their rows take 16-byte loads
-    const uint4 bits = keys ? tile_words(P.kt, b, tile, key_end(a, b)) : make_uint4(0, 0, 0, 0);
-    uint32_t u[kTurns][4];
-#pragma unroll
-    for (int k = 0; k < kTurns; ++k) {
-        const int r = warp * 16 + k * kRows + lane / LANES;     // a warp's rows are of one word
-        const int64_t t = (int64_t)tile * kTile + r;
-        const uint32_t word = warp < 2 ? bits.x : warp < 4 ? bits.y : warp < 6 ? bits.z : bits.w;
-        const bool live = keys ? (word >> (r & 31)) & 1u : t < a.n;
-        load8(w, b * w.sb + t * w.st + h * w.sh, 8 * (lane % LANES), a.d, live, true, u[k]);
-    }
-    float top = 0.f;
-#pragma unroll
-    for (int k = 0; k < kTurns; ++k) {
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack16<false>(u[k][e]);
-            x = fmaf(f.x, f.x, x);
-            x = fmaf(f.y, f.y, x);
-        }
-#pragma unroll
-        for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (x < INFINITY) top = fmaxf(top, x);
-    }
-#pragma unroll
-    for (int o = 16; o >= LANES; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) sTop[warp] = top;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-#pragma unroll
-        for (int k = 1; k < kRowThreads / 32; ++k) top = fmaxf(top, sTop[k]);
-        (keys ? P.v_range : P.q_range)[blk] = sqrtf(top);
-    }
-}
-
-// |ds_ij| = p_ij |dO_i . v_j - sum_k p_ik dO_i . v_k| <= 2 max |dO_i| max |v_j|.  The power of two
-// that takes this bound, over `nq` tiles of dO and all counted values of the key head, to
-// [2^14, 2^15): float16 then holds in full what is down to 2^-29 of it.  A whole warp.
-__device__ __forceinline__ int range_shift(const float* q, int nq, const float* v, int nv) {
-    const int lane = threadIdx.x & 31;
-    float x = 0.f, y = 0.f;
-    for (int e = lane; e < nq; e += 32) x = fmaxf(x, __ldg(q + e));
-#pragma unroll 4
-    for (int e = lane; e < nv; e += 32) y = fmaxf(y, __ldg(v + e));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-    }
-    const float bound = 2.f * x * y;      // 0 or a normal number, 2^-48 to 2^41
-    return bound > 0.f ? 14 + 127 - (int)(__float_as_uint(bound) >> 23) : 0;
-}
-__device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-
-// p of grad_keys in float16 is multiplied by 2^kGradShift: in full down to 2^-28, and no more
-// than the rounding of x can take it past 1 would make it infinite
-constexpr int kGradShift = 14;
 
 // ---------------------------------------------------------------------------
 
@@ -355,8 +377,8 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
     uint8_t* sKV = smem;                    // at first Q and dO in the last two tiles, at the end dq
     uint8_t* sOwn = sKV + (NS - 2) * C::kTileBytes;
     GradBars& bar = *reinterpret_cast<GradBars*>(sKV + NS * C::kTileBytes);
-    float* sFar = reinterpret_cast<float*>(&bar + 1);            // [8][2], or half sums of delta
-    float* sBias = sFar + (DELTA ? kTile : 2 * kElemWarps);      // [2 (D + kSlack) + 1]
+    float* sFar = reinterpret_cast<float*>(&bar + 1);            // [8][2], or the second halves' sums and largest
+    float* sBias = sFar + (DELTA ? 2 * kTile : 2 * kElemWarps);      // [2 (D + kSlack) + 1]
     float* sSums = sBias + (a.table ? 2 * (a.D + kSlack) + 1 : 0);   // [4][2 D + 1]
     float* sScratch = sSums + kBands * (2 * a.D + 1);            // [8][scratch_rows][33], with bias sums
 
@@ -540,10 +562,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
         uint8_t* const values = P.rows + (((int64_t)b * a.H + h) * P.q_tiles + qt) * kRowStride;
         const float* row = reinterpret_cast<const float*>(values + kRowBytes);
         // float16: ds, and the sums of the bias gradient, are 2^shift times as large
-        const float* v_range = P.v_range + ((int64_t)b * a.G + h / a.R) * P.k_tiles;
-        const int shift = BF || DELTA ? 0
-                                      : range_shift(P.q_range + ((int64_t)b * a.H + h) * P.q_tiles + qt, 1,
-                                                    v_range, P.k_tiles);
+        const int shift = BF || DELTA ? 0 : range_shift(P, b, h, qt, 1);
         float nlse = DELTA ? row_lse(a, b, h, i) : row[r];
         if (!BF && !DELTA) nlse += (float)shift;
         const float ndelta = DELTA ? 0.f : row[kTile + r];
@@ -573,7 +592,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
         }
         const uint32_t tS = tmem + lofs + C::S + half * NC, tDP = tmem + lofs + C::DP + half * NC;
         float* scratch = sScratch + warp * P.scratch_rows * 33;
-        float far_lo = 0.f, far_hi = 0.f, total = 0.f;
+        float far_lo = 0.f, far_hi = 0.f, total = 0.f, top = 0.f;      // DELTA: sum, and largest, of p dP
         for (int j = 0; j < nt && ok; ++j) {
             // relative position of the warp's first row and column
             const int64_t rel0 =
@@ -647,6 +666,7 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
                 for (int c = 0; c < NC; c += 2) {
                     s0 += v[c];
                     s1 += v[c + 1];
+                    if (!BF) top = max3(top, fabsf(v[c]), fabsf(v[c + 1]));
                 }
                 total += s0 + s1;
             } else {
@@ -707,14 +727,23 @@ __device__ __forceinline__ void grad_queries(const GradArgs& P, int blk) {
             }
         }
         if (DELTA) {       // the two halves of a row, to its row values
-            if (half) sFar[r] = total;
+            if (half) {
+                sFar[r] = total;
+                if (!BF) sFar[kTile + r] = top;
+            }
             named_sync(2 + quarter, 64);
+            total += sFar[r];
+            if (!BF) top = fmaxf(top, sFar[kTile + r]);
+            const int64_t tile = ((int64_t)b * a.H + h) * P.q_tiles + qt;
             if (P.q_splits > 1) {
-                if (ok && !half)
-                    P.part_delta[((int64_t)split * a.B * a.H + (int64_t)b * a.H + h) * P.q_tiles * kTile +
-                                 qt * kTile + r] = total + sFar[r];
+                const int64_t at = ((int64_t)split * a.B * a.H * P.q_tiles + tile) * kTile + r;
+                if (ok && !half) {
+                    P.part_delta[at] = total;
+                    if (!BF) P.part_top[at] = top;
+                }
             } else if (ok) {
-                put_row(a, values, r, half ? nlse : -(total + sFar[r]), !half);
+                put_row(a, values, r, half ? nlse : -total, !half);
+                if (!BF && !half) put_range(P, tile, quarter, lane, top + fabsf(total));
             }
         }
         if (!DELTA && nt > 0 && ok) ok = warp_wait(&bar.done, 0, a.err, ERR_TIMEOUT_EPILOGUE);
@@ -956,10 +985,7 @@ __device__ __forceinline__ void grad_keys(const GradArgs& P, int blk) {
         const uint32_t tS = tmem + lofs + C::S + half * NC, tDP = tmem + lofs + C::DP + half * NC;
         const float scale2 = least_scale(a);
         // float16: p and ds are 2^kGradShift and 2^shift times as large
-        const float* q_range = P.q_range + ((int64_t)b * a.H + g * a.R) * P.q_tiles;
-        const int shift = BF ? 0
-                             : range_shift(q_range, a.R * P.q_tiles,
-                                           P.v_range + ((int64_t)b * a.G + g) * P.k_tiles, P.k_tiles);
+        const int shift = BF ? 0 : range_shift(P, b, g * a.R, 0, a.R * P.q_tiles);
         const float ds_over_p = power2(shift - (BF ? 0 : kGradShift));
         bool ok = true;
         int h = g * a.R + t0 / per_head, qt = t0 % per_head;
@@ -1130,6 +1156,7 @@ __global__ void __launch_bounds__(128) k_grad_join(Args a, View w, View w1, cons
 }
 
 // Row values of the queries from the shares of delta: a row a thread.
+template <bool BF>
 __global__ void __launch_bounds__(kTile) k_delta_join(const __grid_constant__ GradArgs P) {
     const Args& a = P.a;
     int blk = blockIdx.x;
@@ -1137,11 +1164,16 @@ __global__ void __launch_bounds__(kTile) k_delta_join(const __grid_constant__ Gr
     blk /= P.q_tiles;
     const int h = blk % a.H, b = blk / a.H, r = threadIdx.x;
     const int64_t tile = (int64_t)blockIdx.x;
-    float s = 0.f;
-    for (int k = 0; k < P.q_splits; ++k) s += P.part_delta[(k * (int64_t)gridDim.x + tile) * kTile + r];
+    float s = 0.f, top = 0.f;
+    for (int k = 0; k < P.q_splits; ++k) {
+        const int64_t at = (k * (int64_t)gridDim.x + tile) * kTile + r;
+        s += P.part_delta[at];
+        if (!BF) top = fmaxf(top, P.part_top[at]);
+    }
     uint8_t* values = P.rows + tile * kRowStride;
     put_row(a, values, r, -s, true);
     put_row(a, values, r, row_lse(a, b, h, (int64_t)qt * kTile + r), false);
+    if (!BF) put_range(P, tile, r >> 5, r & 31, top + fabsf(s));
 }
 
 // ---------------------------------------------------------------------------
@@ -1235,22 +1267,18 @@ cudaError_t launch_grad(GradArgs p, void* dbias, cudaStream_t s) {
     smem = std::max(smem, fixed + p.kv_stages * stage);
     if ((e = raise_smem(k_grad<HD, BF>, kSmemLimit, ready)) != cudaSuccess) return e;
     const int64_t q_blocks = (int64_t)p.q_tiles * a.H * a.B, k_blocks = (int64_t)p.k_tiles * a.G * a.B;
-    if (!BF) {
-        k_grad_range<HD / 8><<<(unsigned)(q_blocks + k_blocks), kRowThreads, 0, s>>>(p);
-        count_launch();
-    }
     if (p.exact_delta) {
-        const size_t least = 1024 + sizeof(GradBars) + sizeof(float) * kTile + bias;
+        const size_t least = 1024 + sizeof(GradBars) + sizeof(float) * 2 * kTile + bias;
         p.delta_stages = 2 * (ring_stages(least, Q::kTileBytes) / 2);
         if ((e = raise_smem(k_grad_delta<HD, BF>, kSmemLimit, delta_ready)) != cudaSuccess) return e;
         k_grad_delta<HD, BF><<<(unsigned)(q_blocks * p.q_splits), kGradThreads,
                                least + p.delta_stages * Q::kTileBytes, s>>>(p);
         if (p.q_splits > 1) {
-            k_delta_join<<<(unsigned)q_blocks, kTile, 0, s>>>(p);
+            k_delta_join<BF><<<(unsigned)q_blocks, kTile, 0, s>>>(p);
             count_launch();
         }
     } else {
-        k_grad_rows<HD / 8, BF><<<(unsigned)q_blocks, kRowThreads, 0, s>>>(p);
+        k_grad_rows<HD / 8, BF><<<(unsigned)(q_blocks + (BF ? 0 : k_blocks)), kRowThreads, 0, s>>>(p);
     }
     count_launch();
     k_grad<HD, BF><<<(unsigned)(q_blocks * p.q_splits + k_blocks * p.k_splits), kGradThreads, smem, s>>>(p);

@@ -52,9 +52,10 @@ struct GradArgs {
     // (rows (b, head, token); delta: rows of rows), joined in order
     int q_splits, k_splits;
     float *part_dq, *part_dk, *part_dv, *part_delta;
-    // float16: the largest norm of a row in each tile of dO, [B][H][q_tiles], and of a counted
-    // row in each tile of V, [B][G][k_tiles] (k_grad_range)
-    float *q_range, *v_range;
+    // float16: what bounds |ds| (range_shift).  For every 32 queries, [B][H][q_tiles][4]: a
+    // bound on theirs with exact_delta, else the largest norm of their dO; that goes with
+    // the largest norm of a counted value of each key tile, [B][G][k_tiles]
+    float *q_range, *v_range, *part_top;
     int stages, kv_stages, delta_stages, scratch_rows;     // set at launch
     int dout_vec, o_vec, dq_vec, dk_vec, dv_vec;   // rows take 16-byte accesses
 };

@@ -47,6 +47,10 @@
  *     pairs) run in Morton order with per-block exponent offsets, so
  *     reordering the caller's points changes the potentials (reordered the
  *     same way) only by rounding.
+ *   - The library links the CUDA runtime of the toolkit that built it as a
+ *     shared library (libcudart.so, which a process that has loaded one of the
+ *     same version shares, and else the toolkit's path): a machine without that
+ *     toolkit needs it on the loader's path.
  *   - Errors are returned as fs_status codes, never as C++ exceptions.  A
  *     human-readable message for the last non-OK status of the calling
  *     thread is available from fs_last_error().
@@ -418,8 +422,8 @@ typedef struct fs_attention {
  * Enqueued on `stream`; can be captured in a CUDA graph after one call of
  * the same sizes outside the capture (see "CUDA graphs" above).
  * Errors: FS_ERR_INVALID_ARG for null or host pointers, sizes, strides or
- * options out of range; FS_ERR_UNSUPPORTED for more than 2^31 - 1 tiles of
- * work; FS_ERR_OOM, FS_ERR_CUDA, FS_ERR_TIMEOUT (from fs_check) as above.
+ * options out of range; FS_ERR_UNSUPPORTED for more than 2^31 - 1 rows of
+ * queries or of keys (batch x heads x n, batch x kv_heads x m); FS_ERR_OOM, FS_ERR_CUDA, FS_ERR_TIMEOUT (from fs_check) as above.
  */
 fs_status fs_cross_attention(const fs_attention* at, const void* q, const void* k, const void* v,
                              void* out, float* lse, void* stream);

@@ -773,7 +773,9 @@ def fs_cross_attention(q, k, v, *, scale: Optional[float] = None, kv_len=None, k
     q_pos         int32 (batch,): position of each sequence's first query (0 if
                   None), e.g. the step of a decoder that sends one token at a time
     A query without a counted key has out 0 and lse -inf; keys and values that
-    do not count may hold anything.
+    do not count may hold anything.  Like every call here it leaves no autograd
+    history; examples/distill_plan.py wraps it with its gradients as a
+    torch.autograd.Function.
     """
     import torch
     _att_inputs(q, k, v)

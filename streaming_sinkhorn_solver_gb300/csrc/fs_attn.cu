@@ -120,9 +120,9 @@ fs_status fill(int dev, Args& w, const fs_attention* a) {
     return FS_OK;
 }
 
-fs_status check_tiles(double tiles) {
-    if (tiles > (double)INT32_MAX)
-        return fail(FS_ERR_UNSUPPORTED, "%.3g tiles of work in one call", tiles);
+fs_status check_rows(double rows) {
+    if (rows > (double)INT32_MAX)
+        return fail(FS_ERR_UNSUPPORTED, "%.3g rows of queries or keys in one call", rows);
     return FS_OK;
 }
 
@@ -203,7 +203,8 @@ constexpr int kExactTiles = 8;
 
 // Splits of the gradients' tiles, at most so: as many as a block's tiles outlast the whole
 // call's when those are spread evenly (a block's fixed part counts as 2.5 of them).  Where
-// k_grad_delta, of the queries' blocks alone, comes first, their number counts alone.  2 x 60 queries, 6171 keys, 16 heads on 8 of 112: 93 us for 102, with a bias 153 for
+// k_grad_delta, of the queries' blocks alone, comes first, their number counts alone.
+// 2 x 60 queries, 6171 keys, 16 heads on 8 of 112: 93 us for 102, with a bias 153 for
 // 234; 3230 queries, 140 keys, 2 heads on 1 of 128, bias: 72 for 99; 4 x 351 queries, 157
 // keys, 64 heads on 8 of 64 (64 blocks of keys beside 768 of queries): 123 us, and 143 with
 // the keys' blocks split.
@@ -261,8 +262,8 @@ fs_status forward_entry(const fs_attention* at, const void* q, const void* k, co
     FS_TRY(view(dev, a.o, out, at->out_stride, at->batch, at->n, a.H, a.d, true, "out"));
     FS_TRY(check_ptr(dev, lse, at->batch * at->n, "lse"));
     a.lse = lse;
-    FS_TRY(check_tiles((double)at->batch * a.H * at->n));
-    FS_TRY(check_tiles((double)at->batch * a.G * at->m));
+    FS_TRY(check_rows((double)at->batch * a.H * at->n));
+    FS_TRY(check_rows((double)at->batch * a.G * at->m));
     const int64_t rows = at->batch * a.H * at->n;
     if (rows == 0) return FS_OK;
     NvtxRange range("fs_cross_attention");
@@ -349,8 +350,8 @@ fs_status grad_entry(const fs_attention* at, const void* q, const void* k, const
     if (dbias && !at->n_buckets) return fail(FS_ERR_INVALID_ARG, "dbias without a bias");
     if (dbias) FS_TRY(check_ptr(dev, dbias, 1, "dbias"));
     a.lse = const_cast<float*>(lse);
-    FS_TRY(check_tiles((double)at->batch * a.H * at->n));
-    FS_TRY(check_tiles((double)at->batch * a.G * at->m));
+    FS_TRY(check_rows((double)at->batch * a.H * at->n));
+    FS_TRY(check_rows((double)at->batch * a.G * at->m));
     NvtxRange range("fs_cross_attention_grad");
     Call c;
     if (a.n == 0 || a.m == 0 || a.B == 0) {

@@ -38,7 +38,7 @@
 // Measured: batch 4, 2048 x 2048, 16 heads, bfloat16: 264 us with heads of 64 (650
 // TFLOP/s of the five products; the chain of waits, exponentials and conversions of a
 // tile, 2000 cycles for 1100 of products), 370 us with heads of 128 (930 TFLOP/s of the
-// five, 1300 of the seven, 0.69 of the measured burst rate); in float16 283 and 401 us.
+// five, 1300 of the seven, 0.69 of the measured burst rate); in float16 4 to 5 % longer.
 #include "fs_attn_host.cuh"
 
 #include <atomic>

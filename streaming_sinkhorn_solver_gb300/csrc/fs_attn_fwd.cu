@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_forward_tc(const __grid_cons
                     mma_over_d<4, C::kChunkBytes>(cS, dQ, dK + rk.slot * kTileU, idS, (dsteps + 3) / 4);
                     if (MASK) {
                         const uint64_t dTile = dMask + (rk.slot >> 1) * FwdMask<HD>::kStep;
-                        const int times = every || j + 1 == tail;     // a loop bound, as above
+                        const int times = every || j + 1 == tail;     // a loop bound (mma_over_d)
 #pragma unroll 1
                         for (int x = 0; x < times; ++x) mma_f16(cS, dOnes, dTile, idM, true);
                     }

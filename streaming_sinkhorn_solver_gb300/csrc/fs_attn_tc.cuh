@@ -136,9 +136,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
 // of 16 elements.  The issuing thread takes 80 cycles for a product a turn, 45 with two,
 // 32 with four: with U = 4 the forward pass of heads of 128 takes 120 us for 128 (U = 1)
 // and 124 (U = 2), of heads of 80 114 for 120, although it adds zeros there.  U = 2 where
-// a product takes longer than that anyway.  One elected thread.  (The count is a loop
-// bound, not a condition around each product: products under a data-dependent condition
-// ended in illegal accesses.)
+// a product takes longer than that anyway.
+//
+// Every product is issued by the one lane that elect.sync names, in code inlined into that
+// lane's branch, and the sizes of a product's operands are constants of the code; run-time
+// counts are loop bounds, and conditions stand around whole groups of products and their
+// commit.  (A first version issued them from a function that was not inlined, under
+// `lane == 0`, with a condition around each product, and ended in illegal accesses with
+// the operands that are right here.  All three went at once; which of them it was is not known.)
 template <int U, int B_CHUNK = CHUNK_BYTES>
 __device__ __forceinline__ void mma_over_d(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                            int turns) {

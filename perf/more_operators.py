@@ -10,7 +10,7 @@ Cache: (pages, kv_heads, page_size, d) for keys and values each, in the type of 
 or in 8 bits with a float32 scale for every token and head; position p of sequence b lies at
 place p % page_size of page table[b, p // page_size].  In 8 bits a row x is held as
 x * (top / amax), quotient and product in float32, rounded to the type, with the scale
-amax / top; amax is its largest magnitude, 2^-100 at least, and top the type's largest number
+amax / top; amax is its largest magnitude, 2^-80 at least, and top the type's largest number
 that is used: 448 (e4m3) or 127 (whole numbers).
 
 Tree attention: token t of a sequence is at position ctx_len + t of its cache.  It sees the
@@ -25,7 +25,7 @@ import torch
 own = False
 
 TOP = {"float8_e4m3fn": 448.0, "int8": 127.0}
-FLOOR = 2.0 ** -100
+FLOOR = 2.0 ** -80
 
 # kind: "rotate" turns queries and keys, "rotate-train" their gradients too, "store" writes
 # a chunk of tokens and reads the sequences back, "tree" attends.

@@ -381,7 +381,9 @@ int64_t fs_hvp_workspace_bytes(int64_t n, int64_t m, int32_t d, const fs_options
  */
 typedef enum {
     FS_DTYPE_BF16 = 0,
-    FS_DTYPE_F16 = 1
+    FS_DTYPE_F16 = 1,
+    FS_DTYPE_E4M3 = 2,        /* caches alone: 8-bit floats of 4 exponent and 3 mantissa bits */
+    FS_DTYPE_I8 = 3           /* caches alone: whole numbers -127 .. 127 */
 } fs_dtype;
 
 /*
@@ -444,6 +446,146 @@ fs_status fs_cross_attention_grad(const fs_attention* at, const void* q, const v
                                   const void* v, const void* out, const float* lse,
                                   const void* dout, void* dq, void* dk, void* dv, void* dbias,
                                   void* stream);
+
+/*
+ * Answering from a cache of keys and values.  Single tokens against an
+ * encoder's states (fs_cross_attention) read keys and values that lie together
+ * in 16 bits; the entry points below hold them in pages, in 16 or 8 bits, give
+ * queries and keys their positions by rotation, and attend to them with several
+ * drafted tokens of a sequence at once.  Conventions as for fs_attention: device
+ * memory, strides in elements, results whose rows do not overlap.
+ *
+ * fs_rotary -- rotary positions.  Of each head the first `rotary_dim` elements
+ * are pairs: (i, i + rotary_dim / 2), or (2 i, 2 i + 1) if `interleaved`.  The pair
+ * (x, y) of a token at position p becomes
+ *     amplitude (x cos(p w_i) - y sin(p w_i),  x sin(p w_i) + y cos(p w_i)),
+ * w_i = freqs[i] (radians a position; longer contexts take other freqs and
+ * amplitude), the rest of the head is copied.  p w_i is reduced in whole numbers
+ * of 2^-64 turns, so far positions lose nothing (freqs as large as they like);
+ * products are float32, results rounded once.  A result may be its own input.
+ * fs_rotary_grad -- the gradient: the same turned back, of dq, dk (arguments in
+ * the places of q, k; results in those of q_out, k_out, with their strides).
+ * k and k_out may be NULL (kv_heads 0): queries alone.  FS_ERR_INVALID_ARG as
+ * fs_cross_attention.  Neither call uses the workspace: they may overlap with others
+ * and be captured in a CUDA graph at any time.
+ */
+typedef struct fs_rotation {
+    int32_t dtype;            /* fs_dtype of q and k: FS_DTYPE_BF16 or FS_DTYPE_F16 */
+    int32_t heads, kv_heads;  /* of q (>= 1) and k (>= 0) */
+    int32_t d;                /* elements per head, 1 .. 4096 */
+    int32_t rotary_dim;       /* even, 2 .. d, at most 512 */
+    int32_t interleaved;      /* 0 or 1 */
+    int64_t batch, n;         /* sequences, tokens of each; 0 allowed */
+    float amplitude;          /* finite */
+    int32_t reserved;         /* must be zero */
+    int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
+    const double* freqs;      /* [rotary_dim / 2] */
+    const int32_t* pos;       /* position of token t of sequence b at b pos_stride[0] + t pos_stride[1] */
+    int64_t pos_stride[2];    /* 0 repeats */
+} fs_rotation;
+
+fs_status fs_rotary(const fs_rotation* rot, const void* q, const void* k, void* q_out,
+                    void* k_out, void* stream);
+fs_status fs_rotary_grad(const fs_rotation* rot, const void* dq, const void* dk, void* dq_out,
+                         void* dk_out, void* stream);
+
+/*
+ * A cache in pages.  Position p of sequence b is row p % page_size of page
+ * table[b][p / page_size]; an entry outside [0, pages) is no page: its positions
+ * are not written, are read as zeros and do not count as keys.  Several
+ * sequences may share pages.
+ *
+ * In 8 bits a row x (one token of one key head, d elements) is held as
+ * x (top / amax), quotient and product in float32, rounded to nearest (ties to
+ * even) in the type, and scale = amax / top in float32, where
+ * amax = max(max |x_c|, 2^-80) and top = 448 (FS_DTYPE_E4M3) or 127 (FS_DTYPE_I8).
+ * The value it stands for is code x scale.  A row with a NaN or an infinity gets
+ * zero codes and a NaN scale: all of it is read as NaN.  A caller that writes
+ * scales itself keeps them positive, 2^-89 at least.  FS_DTYPE_BF16 and
+ * FS_DTYPE_F16 hold the rows as they are, without scales.
+ */
+typedef struct fs_cache {
+    int32_t dtype;            /* fs_dtype: any of the four */
+    int32_t kv_heads;         /* >= 1 */
+    int32_t d;                /* a multiple of 8, 8 .. 128 */
+    int32_t page_size;        /* a power of two, 8 .. 2^20 */
+    int64_t pages;            /* of the pool; 0 .. 2^31 - 1 */
+    int64_t batch;            /* sequences: rows of the table */
+    int64_t table_pages;      /* entries of a row; table_pages x page_size < 2^31 - 4096 */
+    int64_t table_stride;     /* from one row to the next */
+    void *k, *v;              /* rows at page s[0] + head s[1] + token s[2], s = k_stride, v_stride */
+    float *k_scale, *v_scale; /* 8 bits: scales at page s[0] + head s[1] + token; else ignored */
+    int64_t k_stride[3], v_stride[3]; /* rows start at multiples of 16 bytes, in 8 bits of 8 */
+    int64_t k_scale_stride[2], v_scale_stride[2];
+    const int32_t* table;     /* batch rows of table_pages */
+} fs_cache;
+
+/* Tokens that go into a cache or come out of it: k, v (batch x n x kv_heads x d). */
+typedef struct fs_cache_rows {
+    int32_t dtype;            /* fs_dtype of k and v: FS_DTYPE_BF16 or FS_DTYPE_F16, and that of a
+                                 cache in 16 bits */
+    int32_t reserved;         /* must be zero */
+    int64_t n;                /* tokens of each sequence; 0 allowed */
+    int64_t k_stride[3], v_stride[3];
+    const int32_t* at;        /* write: [batch][n] positions, at_stride apart; read: [batch] lengths */
+    int64_t at_stride;
+} fs_cache_rows;
+
+/*
+ * fs_cache_write -- writes token t of sequence b at position at[b][t]; tokens at
+ * negative positions, beyond the table or without a page are left out, and every
+ * other row of the cache is left as it is.  The rows that a call writes are
+ * distinct: of two tokens at one place, parts of either may be left there.
+ * Captured as fs_rotary.
+ */
+fs_status fs_cache_write(const fs_cache* cache, const fs_cache_rows* rows, const void* k,
+                         const void* v, void* stream);
+
+/*
+ * fs_cache_read -- positions 0 .. n - 1 of every sequence, rounded once to
+ * rows->dtype, as the k and v of fs_cross_attention; zeros from at[b] on (at NULL:
+ * none) and where there is no page.  Captured as fs_rotary.
+ */
+fs_status fs_cache_read(const fs_cache* cache, const fs_cache_rows* rows, void* k, void* v,
+                        void* stream);
+
+/*
+ * fs_tree_attention -- attention of a tree of n drafted tokens a sequence to its
+ * cache, in which the tree's own keys and values lie behind the ctx_len[b] positions
+ * before it, token t at position ctx_len[b] + t.  Token t sees every position below
+ * ctx_len[b], itself, its parent parents[b][t], that one's parent and so on up to a
+ * parent of -1.  A parent is a lower token of the tree or -1; a token whose chain does
+ * not end in -1 is not there (padding).  parents NULL: a chain, t after t - 1; one
+ * token alone (n = 1) is ordinary decoding.
+ *     z_tj = scale q_t . k_j,  lse_t = log sum_j exp(z_tj),  out_t = sum_j exp(z_tj - lse_t) v_j
+ * over what t sees, for each head (query head h reads key head h / (heads /
+ * kv_heads)).  A token that is not there, or sees no key, has out 0 and lse -inf.
+ * ctx_len is taken into [0, table_pages x page_size]; positions beyond the table do
+ * not count.  Keys and values that a token does not see never reach its results,
+ * whatever they hold; of the tree's own values that it sees, one that is not finite
+ * makes the whole of its row NaN.
+ *
+ * out (batch x n x heads x d) of the type of q, lse float32 (batch x heads x n),
+ * contiguous.  Numerics as fs_cross_attention; a cache in 8 bits is multiplied as
+ * float16 holds its codes (exactly), keys' scales enter the scores, values' the
+ * weights, in float32.  Bitwise deterministic.  Captured as fs_cross_attention;
+ * errors as there.
+ */
+typedef struct fs_tree {
+    int32_t dtype;            /* fs_dtype of q and out: FS_DTYPE_BF16 or FS_DTYPE_F16, and that of
+                                 a cache in 16 bits */
+    int32_t heads;            /* a multiple of the cache's kv_heads */
+    int64_t n;                /* tokens of a tree, 0 .. 256 */
+    float scale;              /* > 0, finite */
+    int32_t reserved;         /* must be zero */
+    int64_t q_stride[3], out_stride[3];
+    const int32_t* ctx_len;   /* [batch] */
+    const int32_t* parents;   /* batch rows of n, parents_stride apart (0: one tree for all); NULL */
+    int64_t parents_stride;
+} fs_tree;
+
+fs_status fs_tree_attention(const fs_cache* cache, const fs_tree* tree, const void* q, void* out,
+                            float* lse, void* stream);
 
 /*
  * fs_unit_rates -- measure, on the current GPU, the per-SM issue rates that

@@ -16,7 +16,7 @@ import ctypes
 import os
 import struct
 import threading
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import numpy as np
 
@@ -39,7 +39,8 @@ EXPORTED = ("fs_sinkhorn_solve", "fs_apply_plan", "fs_barycentric", "fs_grad_x",
             "fs_sparse_solve", "fs_morton_order", "fs_sparse_screen", "fs_wait_selftest",
             "fs_debug_bounds", "fs_shard_unit", "fs_shard_range", "fs_fixup_stats",
             "fs_hvp_workspace_bytes", "fs_barrier_selftest", "fs_cross_attention",
-            "fs_cross_attention_grad")
+            "fs_cross_attention_grad", "fs_rotary", "fs_rotary_grad", "fs_cache_write",
+            "fs_cache_read", "fs_tree_attention")
 
 
 class FlashSinkhornError(RuntimeError):
@@ -87,6 +88,42 @@ class fs_attention(ctypes.Structure):
                 ("key_mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64),
                 ("bias", ctypes.c_void_p), ("bias_stride", ctypes.c_int64),
                 ("bias_buckets", ctypes.c_void_p), ("q_pos", ctypes.c_void_p)]
+
+
+class fs_rotation(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("batch", ctypes.c_int64), ("n", ctypes.c_int64), ("amplitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("q_stride", ctypes.c_int64 * 3),
+                ("k_stride", ctypes.c_int64 * 3), ("q_out_stride", ctypes.c_int64 * 3),
+                ("k_out_stride", ctypes.c_int64 * 3), ("freqs", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p), ("pos_stride", ctypes.c_int64 * 2)]
+
+
+class fs_cache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("pages", ctypes.c_int64),
+                ("batch", ctypes.c_int64), ("table_pages", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("k_scale_stride", ctypes.c_int64 * 2), ("v_scale_stride", ctypes.c_int64 * 2),
+                ("table", ctypes.c_void_p)]
+
+
+class fs_cache_rows(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("n", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("at", ctypes.c_void_p), ("at_stride", ctypes.c_int64)]
+
+
+class fs_tree(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("n", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3),
+                ("ctx_len", ctypes.c_void_p), ("parents", ctypes.c_void_p),
+                ("parents_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -167,6 +204,15 @@ def load_library(path: Optional[str] = None):
         lib.fs_cross_attention.restype = ctypes.c_int
         lib.fs_cross_attention_grad.argtypes = [att] + [vp] * 11
         lib.fs_cross_attention_grad.restype = ctypes.c_int
+        for fn in ("fs_rotary", "fs_rotary_grad"):
+            getattr(lib, fn).argtypes = [ctypes.POINTER(fs_rotation)] + [vp] * 5
+            getattr(lib, fn).restype = ctypes.c_int
+        cache, rows = ctypes.POINTER(fs_cache), ctypes.POINTER(fs_cache_rows)
+        for fn in ("fs_cache_write", "fs_cache_read"):
+            getattr(lib, fn).argtypes = [cache, rows, vp, vp, vp]
+            getattr(lib, fn).restype = ctypes.c_int
+        lib.fs_tree_attention.argtypes = [cache, ctypes.POINTER(fs_tree), vp, vp, vp, vp]
+        lib.fs_tree_attention.restype = ctypes.c_int
         if path is None:
             _lib = lib
         return lib
@@ -824,3 +870,298 @@ def fs_cross_attention_grad(q, k, v, out, lse, dout, *, scale: Optional[float] =
         _att_stream(stream, q))
     _raise(st)
     return dq, dk, dv, dbias
+
+
+# ---------------------------------------------------------------------------
+# rotary positions, a cache in pages, attention of drafted trees (CUDA tensors)
+
+def fs_rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, factor: float = 1.0,
+                          trained: Optional[int] = None, low: float = 1.0, high: float = 4.0):
+    """Radians a position of the rotary_dim / 2 pairs of fs_rotary, base^(-2 i / rotary_dim)
+    (float64 numpy array; its `freqs` once on the GPU).
+
+    Contexts `factor` times longer than the `trained` positions: with trained = None every
+    frequency is divided by factor; else those that turn less than `low` times over the
+    trained positions are, those that turn more than `high` times are kept, and the ones
+    between go over evenly.  (A raised base is the third way.)
+    """
+    half = int(rotary_dim) // 2
+    if rotary_dim < 2 or rotary_dim % 2 or not (base > 0 and factor > 0 and high > low):
+        raise ValueError(f"rotary_dim={rotary_dim} must be even and at least 2, base={base} and "
+                         f"factor={factor} positive, high={high} above low={low}")
+    f = float(base) ** (-np.arange(half, dtype=np.float64) / half)
+    if trained is None:
+        return f / factor
+    keep = np.clip((trained * f / (2 * np.pi) - low) / (high - low), 0.0, 1.0)
+    return f * keep + f / factor * (1.0 - keep)
+
+
+_ROTATION = struct.Struct("=6i2qfi12q2Q2q")
+_CACHE = struct.Struct("=4i4q4Q10qQ")
+_CACHE_ROWS = struct.Struct("=2iq6qQq")
+_TREE = struct.Struct("=2iqfi6q2Qq")
+for _packed, _desc in ((_ROTATION, fs_rotation), (_CACHE, fs_cache), (_CACHE_ROWS, fs_cache_rows),
+                       (_TREE, fs_tree)):
+    assert _packed.size == ctypes.sizeof(_desc)
+
+
+def _rows16(x, name: str):
+    """Refuses what is no (batch, n, heads, d) tensor of a 16-bit type on the GPU."""
+    import torch
+    if not _DTYPES:
+        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1})
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES or not x.is_cuda:
+        raise TypeError(f"{name} must be a bfloat16 or float16 CUDA tensor")
+    if x.dim() != 4 or x.shape[3] < 1:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected (batch, n, heads, d)")
+
+
+def _rotate(fn: str, q, k, freqs, pos, interleaved, amplitude, q_out, k_out, stream) -> Tuple:
+    import torch
+    _rows16(q, "q")
+    batch, n, heads, d = q.shape
+    qs = _att_strides(q, "q", q.shape, q)
+    kv_heads, ks, kos, k_p, ko_p = 0, _NO_STRIDES, _NO_STRIDES, None, None
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise TypeError("k must be a tensor (batch, n, kv_heads, d) or None")
+        kv_heads = k.shape[2]
+        ks = _att_strides(k, "k", (batch, n, kv_heads, d), q)
+        k_p = k.data_ptr()
+    elif k_out is not None:
+        raise TypeError("k_out without k")
+    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+        raise TypeError("freqs must be a float64 CUDA tensor (rotary_dim / 2,)")
+    half = freqs.shape[0]
+    freqs_p = _i_ptr(freqs, "freqs", (half,), torch.float64)
+    if not (isinstance(pos, torch.Tensor) and pos.is_cuda and pos.dtype == torch.int32):
+        raise TypeError("pos must be an int32 CUDA tensor")
+    if tuple(pos.shape) not in ((n,), (batch, n)):
+        raise ValueError(f"pos has shape {tuple(pos.shape)}, expected {(batch, n)} or {(n,)}")
+    step = pos.stride() if pos.dim() == 2 else (0, pos.stride(0))
+    q_out = _att_empty(q, q.shape, q.dtype, stream) if q_out is None else q_out
+    qos = _att_strides(q_out, "q_out", q.shape, q)
+    if kv_heads:
+        k_out = _att_empty(q, k.shape, q.dtype, stream) if k_out is None else k_out
+        kos = _att_strides(k_out, "k_out", k.shape, q)
+        ko_p = k_out.data_ptr()
+    elif k is not None and k_out is None:
+        k_out = _att_empty(q, k.shape, q.dtype, stream)
+    r = fs_rotation()
+    _ROTATION.pack_into(r, 0, _DTYPES[q.dtype], heads, kv_heads, d, 2 * half,
+                        1 if interleaved else 0, batch, n, amplitude, 0, *qs, *ks, *qos, *kos,
+                        freqs_p, pos.data_ptr(), *step)
+    _raise(getattr(load_library(), fn)(ctypes.byref(r), q.data_ptr(), k_p, q_out.data_ptr(), ko_p,
+                                       _att_stream(stream, q)))
+    return q_out, k_out
+
+
+def fs_rotary(q, k, freqs, pos, *, interleaved: bool = False, amplitude: float = 1.0, q_out=None,
+              k_out=None, stream=None) -> Tuple:
+    """Rotary positions: turns the first 2 len(freqs) elements of each head of q (batch, n,
+    heads, d) and k (batch, n, kv_heads, d) or None, bfloat16 or float16, any strides with
+    contiguous d.  Returns (q_out, k_out), new or as given (their inputs themselves, too).
+
+    freqs        float64 (pairs,): radians a position, e.g. from fs_rotary_frequencies
+    pos          int32 (batch, n) or (n,): position of each token
+    interleaved  pairs are neighbours (2 i, 2 i + 1); else (i, i + pairs)
+    amplitude    factor of the turned elements
+    """
+    return _rotate("fs_rotary", q, k, freqs, pos, interleaved, amplitude, q_out, k_out, stream)
+
+
+def fs_rotary_grad(dq, dk, freqs, pos, *, interleaved: bool = False, amplitude: float = 1.0,
+                   dq_out=None, dk_out=None, stream=None) -> Tuple:
+    """Gradients of fs_rotary with respect to its q and k, for those of its results."""
+    return _rotate("fs_rotary_grad", dq, dk, freqs, pos, interleaved, amplitude, dq_out, dk_out,
+                   stream)
+
+
+class KVCache(NamedTuple):
+    """Keys and values in pages: k and v (pages, kv_heads, page_size, d), bfloat16, float16,
+    float8_e4m3fn or int8; 8-bit ones with float32 scales (pages, kv_heads, page_size).  Any
+    strides whose rows start at multiples of 16 bytes (8 bits: of 8)."""
+    k: object
+    v: object
+    k_scale: object = None
+    v_scale: object = None
+
+
+def fs_cache_new(pages: int, kv_heads: int, page_size: int, d: int, dtype, device="cuda") -> KVCache:
+    """An empty cache (zeros) of `dtype`; in 8 bits its rows start at multiples of 16 bytes."""
+    import torch
+    held = _cache_dtypes()
+    if dtype not in held:
+        raise TypeError(f"dtype must be one of {', '.join(map(str, held))}")
+    eight = held[dtype] >= 2
+    wide = (d + 15) // 16 * 16 if eight else d
+
+    def rows():
+        return torch.zeros((pages, kv_heads, page_size, wide), dtype=torch.int8 if eight else dtype,
+                           device=device).view(dtype)[..., :d]
+
+    def scale():
+        return torch.ones((pages, kv_heads, page_size), dtype=torch.float32, device=device)
+
+    return KVCache(rows(), rows(), *((scale(), scale()) if eight else ()))
+
+
+_CACHE_DTYPES = {}
+
+
+def _cache_dtypes():
+    import torch
+    if not _CACHE_DTYPES:
+        _CACHE_DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2,
+                              torch.int8: 3})
+    return _CACHE_DTYPES
+
+
+def _cache(cache, table, like) -> fs_cache:
+    """Checked description of a KVCache with its page table, for tensors on like's device."""
+    import torch
+    k, v, k_scale, v_scale = cache
+    held = _cache_dtypes().get(getattr(k, "dtype", None))
+    if held is None or not isinstance(k, torch.Tensor) or k.device != like.device:
+        raise TypeError(f"cache.k must be a 16-bit, float8_e4m3fn or int8 tensor on {like.device}")
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"cache.k has shape {tuple(shape)}, expected (pages, kv_heads, page_size, d)")
+    ks = _att_strides(k, "cache.k", shape, k)
+    vs = _att_strides(v, "cache.v", shape, k)
+    ks_p = vs_p = 0
+    kss = vss = (0, 0)
+    if held >= 2:
+        for x, name in ((k_scale, "cache.k_scale"), (v_scale, "cache.v_scale")):
+            if not (isinstance(x, torch.Tensor) and x.dtype == torch.float32 and x.device == k.device
+                    and x.shape == shape[:3]):
+                raise TypeError(f"{name} must be a float32 tensor of shape {tuple(shape[:3])} on {k.device}")
+            if shape[2] > 1 and x.stride(2) != 1:
+                raise TypeError(f"the tokens of {name} must be contiguous")
+        ks_p, vs_p, kss, vss = k_scale.data_ptr(), v_scale.data_ptr(), k_scale.stride()[:2], v_scale.stride()[:2]
+    elif k_scale is not None or v_scale is not None:
+        raise TypeError("a cache in 16 bits has no scales")
+    if not (isinstance(table, torch.Tensor) and table.dtype == torch.int32 and table.device == k.device
+            and table.dim() == 2):
+        raise TypeError(f"table must be an int32 tensor (batch, pages of a sequence) on {k.device}")
+    if table.shape[0] != like.shape[0]:
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected {like.shape[0]} rows")
+    if table.shape[1] > 1 and table.stride(1) != 1:
+        raise TypeError("the rows of table must be contiguous")
+    c = fs_cache()
+    _CACHE.pack_into(c, 0, held, shape[1], shape[3], shape[2], shape[0], table.shape[0], table.shape[1],
+                     table.stride(0), k.data_ptr(), v.data_ptr(), ks_p, vs_p, *ks, *vs, *kss, *vss,
+                     table.data_ptr())
+    return c
+
+
+def fs_cache_write(cache: KVCache, table, positions, k, v, *, stream=None) -> None:
+    """Writes keys and values k, v (batch, n, kv_heads, d) into the cache, in its type.
+
+    table      int32 (batch, pages of a sequence): position p of sequence b is row
+               p % page_size of page table[b, p // page_size]; entries outside
+               [0, pages) are no page
+    positions  int32 (batch, n): where each token goes; tokens with a negative position,
+               beyond the table or without a page are left out.  The rows that one call
+               writes are distinct: of two tokens at one place, parts of either may be left.
+    """
+    import torch
+    _rows16(k, "k")
+    batch, n, _, _ = k.shape
+    c = _cache(cache, table, k)
+    want = (batch, n, cache.k.shape[1], cache.k.shape[3])
+    ks, vs = _att_strides(k, "k", want, k), _att_strides(v, "v", want, k)
+    if not (isinstance(positions, torch.Tensor) and positions.dtype == torch.int32
+            and positions.device == k.device and tuple(positions.shape) == (batch, n)):
+        raise TypeError(f"positions must be an int32 tensor of shape {(batch, n)} on {k.device}")
+    if n > 1 and positions.stride(1) != 1:
+        raise TypeError("the rows of positions must be contiguous")
+    r = fs_cache_rows()
+    _CACHE_ROWS.pack_into(r, 0, _DTYPES[k.dtype], 0, n, *ks, *vs, positions.data_ptr(),
+                          positions.stride(0))
+    _raise(load_library().fs_cache_write(ctypes.byref(c), ctypes.byref(r), k.data_ptr(), v.data_ptr(),
+                                         _att_stream(stream, k)))
+
+
+def fs_cache_read(cache: KVCache, table, lens=None, n: Optional[int] = None, *, dtype=None, k=None,
+                  v=None, stream=None) -> Tuple:
+    """Positions 0 .. n - 1 (None: all that the table has) of every sequence as k and v
+    (batch, n, kv_heads, d) for fs_cross_attention: new ones of `dtype` (None: the cache's,
+    bfloat16 for 8 bits) or as given.  Zeros from lens[b] (int32 (batch,)) on and where
+    there is no page."""
+    import torch
+    like = cache.k
+    if not isinstance(like, torch.Tensor) or not like.is_cuda or like.dim() != 4:
+        raise TypeError("cache.k must be a CUDA tensor (pages, kv_heads, page_size, d)")
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise TypeError("table must be an int32 tensor (batch, pages of a sequence)")
+    n = table.shape[1] * like.shape[2] if n is None else int(n)
+    if dtype is None:
+        dtype = k.dtype if k is not None else like.dtype if like.element_size() == 2 else torch.bfloat16
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("dtype must be bfloat16 or float16")
+    if n < 0:
+        raise ValueError(f"n={n}")
+    want = (table.shape[0], n, like.shape[1], like.shape[3])
+    k = _att_empty(like, want, dtype, stream) if k is None else k
+    v = _att_empty(like, want, dtype, stream) if v is None else v
+    _rows16(k, "k")
+    if k.dtype != dtype:
+        raise TypeError(f"k must be a {dtype} tensor")
+    c = _cache(cache, table, k)
+    ks, vs = _att_strides(k, "k", want, k), _att_strides(v, "v", want, k)
+    lens_p = 0 if lens is None else _i_ptr(lens, "lens", (table.shape[0],), torch.int32)
+    r = fs_cache_rows()
+    _CACHE_ROWS.pack_into(r, 0, _DTYPES[dtype], 0, n, *ks, *vs, lens_p, 0)
+    _raise(load_library().fs_cache_read(ctypes.byref(c), ctypes.byref(r), k.data_ptr(), v.data_ptr(),
+                                        _att_stream(stream, k)))
+    return k, v
+
+
+def fs_tree_attention(q, cache: KVCache, table, ctx_len, parents=None, *,
+                      scale: Optional[float] = None, out=None, lse=None, stream=None) -> Tuple:
+    """Attention of a tree of drafted tokens, q (batch, n <= 256, heads, d), to each
+    sequence's cache, in which its own keys and values lie at positions ctx_len[b] + t
+    (fs_cache_write them first).  Returns (out, lse): out as q, lse float32 (batch, heads, n).
+
+    cache, table  as fs_cache_write has them; of q's type, or in 8 bits
+    ctx_len       int32 (batch,): positions before the tree, which every token sees
+    parents       int32 (batch, n) or (n,): the parent of each token of the tree, lower than
+                  it, or -1; a token sees itself and its chain of parents.  A token whose
+                  chain does not end in -1 (-2, for padding) is not there: out 0, lse -inf.
+                  None: a chain of tokens; n = 1 is ordinary decoding.
+    scale         factor of the dot products, d ** -0.5 if None
+    Positions beyond the table or without a page do not count.
+    """
+    import torch
+    _rows16(q, "q")
+    batch, n, heads, d = q.shape
+    c = _cache(cache, table, q)
+    if cache.k.shape[3] != d:
+        raise ValueError(f"q has heads of {d}, the cache of {cache.k.shape[3]}")
+    qs = _att_strides(q, "q", q.shape, q)
+    ctx_p = _i_ptr(ctx_len, "ctx_len", (batch,), torch.int32)
+    par_p = par_s = 0
+    if parents is not None:
+        if not (isinstance(parents, torch.Tensor) and parents.dtype == torch.int32
+                and parents.device == q.device):
+            raise TypeError(f"parents must be an int32 tensor on {q.device}")
+        if tuple(parents.shape) not in ((n,), (batch, n)):
+            raise ValueError(f"parents has shape {tuple(parents.shape)}, expected {(batch, n)} or {(n,)}")
+        if n > 1 and parents.stride(-1) != 1:
+            raise TypeError("the rows of parents must be contiguous")
+        par_p, par_s = parents.data_ptr(), parents.stride(0) if parents.dim() == 2 else 0
+    out = _att_empty(q, q.shape, q.dtype, stream) if out is None else out
+    os_ = _att_strides(out, "out", q.shape, q)
+    rows = (batch, heads, n)
+    if lse is None:
+        lse = _att_empty(q, rows, torch.float32, stream)
+        lse_p = lse.data_ptr()
+    else:
+        lse_p = _ptr(lse, "lse", rows)
+    t = fs_tree()
+    _TREE.pack_into(t, 0, _DTYPES[q.dtype], heads, n, d ** -0.5 if scale is None else scale, 0, *qs,
+                    *os_, ctx_p, par_p, par_s)
+    _raise(load_library().fs_tree_attention(ctypes.byref(c), ctypes.byref(t), q.data_ptr(),
+                                            out.data_ptr(), lse_p, _att_stream(stream, q)))
+    return out, lse

@@ -7,42 +7,6 @@
 namespace fs {
 namespace attn {
 
-namespace {
-
-fs_status check_desc(const fs_attention* a) {
-    if (!a) return fail(FS_ERR_INVALID_ARG, "null fs_attention");
-    if (a->dtype != FS_DTYPE_BF16 && a->dtype != FS_DTYPE_F16)
-        return fail(FS_ERR_INVALID_ARG, "fs_attention.dtype=%d", a->dtype);
-    if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads != 0)
-        return fail(FS_ERR_INVALID_ARG, "heads=%d is not a multiple of kv_heads=%d", a->heads,
-                    a->kv_heads);
-    if (a->d < 1 || a->d > kMaxHeadDim)
-        return fail(FS_ERR_INVALID_ARG, "d=%d out of range [1, %d]", a->d, kMaxHeadDim);
-    constexpr int64_t kMaxTokens = INT32_MAX - 4096;   // tile ends stay in 32 bits
-    if (a->batch < 0 || a->n < 0 || a->m < 0 || a->batch > kMaxTokens || a->n > kMaxTokens ||
-        a->m > kMaxTokens)
-        return fail(FS_ERR_INVALID_ARG, "batch=%lld n=%lld m=%lld out of range [0, %lld]",
-                    (long long)a->batch, (long long)a->n, (long long)a->m, (long long)kMaxTokens);
-    if (!(a->scale > 0.f) || !std::isfinite((float)(a->scale * kLog2e)))
-        return fail(FS_ERR_INVALID_ARG, "scale must be positive and finite in base 2 (got %g)",
-                    (double)a->scale);
-    if (a->reserved) return fail(FS_ERR_INVALID_ARG, "fs_attention.reserved must be zero");
-    if (a->n_buckets < 0 || a->n_buckets > kMaxBuckets)
-        return fail(FS_ERR_INVALID_ARG, "n_buckets=%d out of range [0, %d]", a->n_buckets,
-                    kMaxBuckets);
-    if (a->n_buckets) {
-        if (!a->bias || !a->bias_buckets) return fail(FS_ERR_INVALID_ARG, "null bias or bias_buckets");
-        if (a->max_distance < 1 || a->max_distance > kMaxDistance)
-            return fail(FS_ERR_INVALID_ARG, "max_distance=%d out of range [1, %d]", a->max_distance,
-                        kMaxDistance);
-        if (a->bias_stride != 0 && a->bias_stride < a->n_buckets)
-            return fail(FS_ERR_INVALID_ARG, "bias_stride=%lld is less than n_buckets=%d",
-                        (long long)a->bias_stride, a->n_buckets);
-    }
-    if (a->key_mask && a->mask_stride < 0) return fail(FS_ERR_INVALID_ARG, "negative mask_stride");
-    return FS_OK;
-}
-
 // -1 without one (every pointer then fails its check)
 int current_device() {
     int dev = -1;
@@ -90,6 +54,47 @@ fs_status view(int dev, View& w, const void* p, const int64_t* stride, int64_t b
     return FS_OK;
 }
 
+bool aligned16(const View& w, int B, int tokens, int heads) {
+    return (reinterpret_cast<uintptr_t>(w.p) & 15) == 0 && (tokens <= 1 || w.st % 8 == 0) &&
+           (heads <= 1 || w.sh % 8 == 0) && (B <= 1 || w.sb % 8 == 0);
+}
+
+namespace {
+
+fs_status check_desc(const fs_attention* a) {
+    if (!a) return fail(FS_ERR_INVALID_ARG, "null fs_attention");
+    if (a->dtype != FS_DTYPE_BF16 && a->dtype != FS_DTYPE_F16)
+        return fail(FS_ERR_INVALID_ARG, "fs_attention.dtype=%d", a->dtype);
+    if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads != 0)
+        return fail(FS_ERR_INVALID_ARG, "heads=%d is not a multiple of kv_heads=%d", a->heads,
+                    a->kv_heads);
+    if (a->d < 1 || a->d > kMaxHeadDim)
+        return fail(FS_ERR_INVALID_ARG, "d=%d out of range [1, %d]", a->d, kMaxHeadDim);
+    constexpr int64_t kMaxTokens = INT32_MAX - 4096;   // tile ends stay in 32 bits
+    if (a->batch < 0 || a->n < 0 || a->m < 0 || a->batch > kMaxTokens || a->n > kMaxTokens ||
+        a->m > kMaxTokens)
+        return fail(FS_ERR_INVALID_ARG, "batch=%lld n=%lld m=%lld out of range [0, %lld]",
+                    (long long)a->batch, (long long)a->n, (long long)a->m, (long long)kMaxTokens);
+    if (!(a->scale > 0.f) || !std::isfinite((float)(a->scale * kLog2e)))
+        return fail(FS_ERR_INVALID_ARG, "scale must be positive and finite in base 2 (got %g)",
+                    (double)a->scale);
+    if (a->reserved) return fail(FS_ERR_INVALID_ARG, "fs_attention.reserved must be zero");
+    if (a->n_buckets < 0 || a->n_buckets > kMaxBuckets)
+        return fail(FS_ERR_INVALID_ARG, "n_buckets=%d out of range [0, %d]", a->n_buckets,
+                    kMaxBuckets);
+    if (a->n_buckets) {
+        if (!a->bias || !a->bias_buckets) return fail(FS_ERR_INVALID_ARG, "null bias or bias_buckets");
+        if (a->max_distance < 1 || a->max_distance > kMaxDistance)
+            return fail(FS_ERR_INVALID_ARG, "max_distance=%d out of range [1, %d]", a->max_distance,
+                        kMaxDistance);
+        if (a->bias_stride != 0 && a->bias_stride < a->n_buckets)
+            return fail(FS_ERR_INVALID_ARG, "bias_stride=%lld is less than n_buckets=%d",
+                        (long long)a->bias_stride, a->n_buckets);
+    }
+    if (a->key_mask && a->mask_stride < 0) return fail(FS_ERR_INVALID_ARG, "negative mask_stride");
+    return FS_OK;
+}
+
 fs_status fill(int dev, Args& w, const fs_attention* a) {
     w.B = (int)a->batch;
     w.H = a->heads;
@@ -124,11 +129,6 @@ fs_status check_rows(double rows) {
     if (rows > (double)INT32_MAX)
         return fail(FS_ERR_UNSUPPORTED, "%.3g rows of queries or keys in one call", rows);
     return FS_OK;
-}
-
-bool aligned16(const View& w, int B, int tokens, int heads) {
-    return (reinterpret_cast<uintptr_t>(w.p) & 15) == 0 && (tokens <= 1 || w.st % 8 == 0) &&
-           (heads <= 1 || w.sh % 8 == 0) && (B <= 1 || w.sb % 8 == 0);
 }
 
 // What a tensor map can describe: 16-byte steps, below 2^40 bytes, and tokens

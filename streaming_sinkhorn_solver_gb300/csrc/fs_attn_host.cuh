@@ -99,6 +99,13 @@ cudaError_t raise_smem(K kernel, size_t bytes, std::atomic<uint64_t>& ready) {
     return cudaSuccess;
 }
 
+// Argument checks of the entry points over (batch, token, head, d) tensors.
+int current_device();
+fs_status check_ptr(int dev, const void* p, int64_t count, const char* name);
+fs_status view(int dev, View& w, const void* p, const int64_t* stride, int64_t batch, int64_t tokens,
+               int heads, int d, bool out, const char* name);
+bool aligned16(const View& w, int B, int tokens, int heads);
+
 // boxes of `rows` tokens
 fs_status make_tensor_map(TensorMap& t, const View& w, int B, int tokens, int heads, int d, bool bf16,
                           int rows = kTile);

@@ -1,0 +1,250 @@
+// Rotary positions of queries and keys, and their gradient (the same turned back).
+//
+// Bound by memory: every element is read and written once.  A block takes a few tokens:
+// first the sines and cosines of each into shared memory, where all their heads find
+// them, then the heads, 16 bytes an access.
+//
+// Angles.  A frequency is kept as a 64-bit fraction of a turn, F = frac(w / 2 pi) 2^64, so
+// that a position's angle is the low 64 bits of p F: whole turns fall away by themselves,
+// with no reduction and no double arithmetic per token, and a position of 2^31 is off by
+// the rounding of w alone (2^-22 turns; float32 angles would be off by many).
+#include "fs_attn_host.cuh"
+
+#include <cmath>
+
+namespace fs {
+namespace rotary {
+
+namespace {
+
+using attn::View;
+
+constexpr int kThreads = 256;
+constexpr int kMaxRotary = 512;
+
+struct Args {
+    View x[2], y[2];             // queries and keys: input, output
+    int heads[2];
+    int B, n, d, half;
+    float amplitude;
+    const double* freqs;
+    const int32_t* pos;
+    int64_t pos_b, pos_t;
+    int tokens;                  // of a block
+    int back;                    // turned back
+    int vec;                     // every row takes 16-byte accesses
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(uint32_t w, float& x, float& y) {
+    const uint16_t a = (uint16_t)w, b = (uint16_t)(w >> 16);
+    x = attn::to_f<T>(*reinterpret_cast<const T*>(&a));
+    y = attn::to_f<T>(*reinterpret_cast<const T*>(&b));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+    const T a = attn::from_f<T>(x), b = attn::from_f<T>(y);
+    return (uint32_t)*reinterpret_cast<const uint16_t*>(&b) << 16 | *reinterpret_cast<const uint16_t*>(&a);
+}
+
+// PAIRS: neighbours (2 i, 2 i + 1) are pairs, else (i, i + half)
+template <typename T, bool PAIRS>
+__global__ void __launch_bounds__(kThreads) k_rotary(const __grid_constant__ Args P) {
+    extern __shared__ float2 turn[];         // [tokens][half] amplitude (cos, sin)
+    const int64_t all = (int64_t)P.B * P.n;
+    const int64_t first = (int64_t)blockIdx.x * P.tokens;
+    const int count = (int)min((int64_t)P.tokens, all - first);
+    for (int e = threadIdx.x; e < count * P.half; e += kThreads) {
+        const int t = e / P.half, i = e - t * P.half;
+        const int64_t tok = first + t;
+        const int b = (int)(tok / P.n);
+        const int64_t p = __ldg(P.pos + b * P.pos_b + (tok - (int64_t)b * P.n) * P.pos_t);
+        const double turns = __ldg(P.freqs + i) * 0.15915494309189533577;     // 1 / (2 pi)
+        const uint64_t f = __double2ull_rz((turns - floor(turns)) * 0x1p64);
+        const int32_t top = (int32_t)(((uint64_t)p * f) >> 32);
+        float sn, cs;
+        sincospif((float)top * 0x1p-31f, &sn, &cs);
+        turn[e] = make_float2(P.amplitude * cs, P.amplitude * (P.back ? -sn : sn));
+    }
+    __syncthreads();
+    const int heads = P.heads[0] + P.heads[1];
+    if (P.vec) {
+        // units of a head: the turned ones (8 elements, or 8 of each half), then copies of 8
+        const int turned = PAIRS ? P.half / 4 : P.half / 8;
+        const int units = turned + (P.d - 2 * P.half) / 8;
+        for (int e = threadIdx.x; e < count * heads * units; e += kThreads) {
+            const int row = e / units, u = e - row * units;
+            const int t = row / heads;
+            int h = row - t * heads;
+            const int64_t tok = first + t;
+            const int b = (int)(tok / P.n);
+            const int64_t i = tok - (int64_t)b * P.n;
+            const int which = h >= P.heads[0];
+            if (which) h -= P.heads[0];
+            const View &from = P.x[which], &to = P.y[which];
+            const uint16_t* src = static_cast<const uint16_t*>(from.p) + b * from.sb + i * from.st + h * from.sh;
+            uint16_t* dst = static_cast<uint16_t*>(to.p) + b * to.sb + i * to.st + h * to.sh;
+            if (u >= turned) {
+                const int c = 2 * P.half + 8 * (u - turned);
+                *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
+                continue;
+            }
+            const float2* w = turn + t * P.half;
+            if (PAIRS) {
+                const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * u);
+                uint32_t o[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float a, c;
+                    unpack<T>(o[k], a, c);
+                    const float2 z = w[4 * u + k];
+                    o[k] = pack<T>(a * z.x - c * z.y, a * z.y + c * z.x);
+                }
+                *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+                const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * u);
+                const uint4 y = *reinterpret_cast<const uint4*>(src + P.half + 8 * u);
+                uint32_t o[4] = {x.x, x.y, x.z, x.w}, r[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float a0, a1, c0, c1;
+                    unpack<T>(o[k], a0, a1);
+                    unpack<T>(r[k], c0, c1);
+                    const float4 z = reinterpret_cast<const float4*>(w + 8 * u)[k];
+                    o[k] = pack<T>(a0 * z.x - c0 * z.y, a1 * z.z - c1 * z.w);
+                    r[k] = pack<T>(a0 * z.y + c0 * z.x, a1 * z.w + c1 * z.z);
+                }
+                *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(dst + P.half + 8 * u) = make_uint4(r[0], r[1], r[2], r[3]);
+            }
+        }
+        return;
+    }
+    // one pair, or one element behind the pairs, a thread
+    const int units = P.d - P.half;
+    for (int e = threadIdx.x; e < count * heads * units; e += kThreads) {
+        const int row = e / units, u = e - row * units;
+        const int t = row / heads;
+        int h = row - t * heads;
+        const int64_t tok = first + t;
+        const int b = (int)(tok / P.n);
+        const int64_t i = tok - (int64_t)b * P.n;
+        const int which = h >= P.heads[0];
+        if (which) h -= P.heads[0];
+        const View &from = P.x[which], &to = P.y[which];
+        const T* src = static_cast<const T*>(from.p) + b * from.sb + i * from.st + h * from.sh;
+        T* dst = static_cast<T*>(to.p) + b * to.sb + i * to.st + h * to.sh;
+        if (u >= P.half) {
+            dst[P.half + u] = src[P.half + u];
+            continue;
+        }
+        const int c0 = PAIRS ? 2 * u : u, c1 = PAIRS ? 2 * u + 1 : u + P.half;
+        const float a = attn::to_f<T>(src[c0]), c = attn::to_f<T>(src[c1]);
+        const float2 z = turn[t * P.half + u];
+        dst[c0] = attn::from_f<T>(a * z.x - c * z.y);
+        dst[c1] = attn::from_f<T>(a * z.y + c * z.x);
+    }
+}
+
+template <typename T>
+cudaError_t launch(const Args& p, bool pairs, cudaStream_t s) {
+    const int64_t blocks = ((int64_t)p.B * p.n + p.tokens - 1) / p.tokens;
+    const size_t smem = sizeof(float2) * (size_t)p.tokens * p.half;
+    if (pairs)
+        k_rotary<T, true><<<(unsigned)blocks, kThreads, smem, s>>>(p);
+    else
+        k_rotary<T, false><<<(unsigned)blocks, kThreads, smem, s>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+fs_status rotary_entry(const fs_rotation* r, const void* q, const void* k, void* q_out, void* k_out,
+                       void* stream, bool back) {
+    if (!r) return fail(FS_ERR_INVALID_ARG, "null fs_rotation");
+    if (r->dtype != FS_DTYPE_BF16 && r->dtype != FS_DTYPE_F16)
+        return fail(FS_ERR_INVALID_ARG, "fs_rotation.dtype=%d", r->dtype);
+    constexpr int kMostHeads = 1 << 16;
+    if (r->heads < 1 || r->heads > kMostHeads || r->kv_heads < 0 || r->kv_heads > kMostHeads)
+        return fail(FS_ERR_INVALID_ARG, "heads=%d kv_heads=%d out of range", r->heads, r->kv_heads);
+    if (r->d < 1 || r->d > 4096) return fail(FS_ERR_INVALID_ARG, "d=%d out of range [1, 4096]", r->d);
+    if (r->rotary_dim < 2 || r->rotary_dim % 2 || r->rotary_dim > r->d || r->rotary_dim > kMaxRotary)
+        return fail(FS_ERR_INVALID_ARG, "rotary_dim=%d is not even in [2, min(d, %d)]", r->rotary_dim,
+                    kMaxRotary);
+    if (r->interleaved != 0 && r->interleaved != 1)
+        return fail(FS_ERR_INVALID_ARG, "interleaved=%d", r->interleaved);
+    constexpr int64_t kMaxTokens = INT32_MAX - 4096;
+    if (r->batch < 0 || r->n < 0 || r->batch > kMaxTokens || r->n > kMaxTokens)
+        return fail(FS_ERR_INVALID_ARG, "batch=%lld n=%lld out of range [0, %lld]", (long long)r->batch,
+                    (long long)r->n, (long long)kMaxTokens);
+    if (!std::isfinite(r->amplitude)) return fail(FS_ERR_INVALID_ARG, "amplitude must be finite");
+    if (r->reserved) return fail(FS_ERR_INVALID_ARG, "fs_rotation.reserved must be zero");
+    if (r->pos_stride[0] < 0 || r->pos_stride[1] < 0)
+        return fail(FS_ERR_INVALID_ARG, "pos has a negative stride");
+    const int dev = attn::current_device();
+    Args p = {};
+    FS_TRY(attn::view(dev, p.x[0], q, r->q_stride, r->batch, r->n, r->heads, r->d, false, "q"));
+    FS_TRY(attn::view(dev, p.y[0], q_out, r->q_out_stride, r->batch, r->n, r->heads, r->d, true, "q_out"));
+    if (r->kv_heads) {
+        FS_TRY(attn::view(dev, p.x[1], k, r->k_stride, r->batch, r->n, r->kv_heads, r->d, false, "k"));
+        FS_TRY(attn::view(dev, p.y[1], k_out, r->k_out_stride, r->batch, r->n, r->kv_heads, r->d, true,
+                          "k_out"));
+    }
+    const int64_t tokens = r->batch * r->n;
+    FS_TRY(attn::check_ptr(dev, r->freqs, 1, "freqs"));
+    FS_TRY(attn::check_ptr(dev, r->pos, tokens, "pos"));
+    if ((double)r->batch * r->n > (double)kMaxTokens)
+        return fail(FS_ERR_UNSUPPORTED, "%.3g tokens in one call", (double)r->batch * r->n);
+    if (tokens == 0) return FS_OK;
+    p.heads[0] = r->heads;
+    p.heads[1] = r->kv_heads;
+    p.B = (int)r->batch;
+    p.n = (int)r->n;
+    p.d = r->d;
+    p.half = r->rotary_dim / 2;
+    p.amplitude = r->amplitude;
+    p.freqs = r->freqs;
+    p.pos = r->pos;
+    p.pos_b = r->pos_stride[0];
+    p.pos_t = r->pos_stride[1];
+    p.back = back;
+    // the turned part and each half of it in whole pieces of 16 bytes
+    p.vec = p.d % 8 == 0 && (r->interleaved ? p.half % 4 == 0 : p.half % 8 == 0);
+    for (int w = 0; w < (r->kv_heads ? 2 : 1); ++w)
+        p.vec = p.vec && attn::aligned16(p.x[w], p.B, p.n, p.heads[w]) &&
+                attn::aligned16(p.y[w], p.B, p.n, p.heads[w]);
+    p.tokens = tokens >= 4096 ? 4 : 1;
+    NvtxRange range(back ? "fs_rotary_grad" : "fs_rotary");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    FS_CUDA(r->dtype == FS_DTYPE_BF16 ? launch<__nv_bfloat16>(p, r->interleaved, s)
+                                      : launch<__half>(p, r->interleaved, s));
+    return FS_OK;
+}
+
+}  // namespace
+
+}  // namespace rotary
+}  // namespace fs
+
+using namespace fs;
+
+extern "C" {
+
+fs_status fs_rotary(const fs_rotation* rot, const void* q, const void* k, void* q_out,
+                    void* k_out, void* stream) {
+    try {
+        return rotary::rotary_entry(rot, q, k, q_out, k_out, stream, false);
+    } catch (...) {
+        return fail(FS_ERR_CUDA, "unexpected host exception");
+    }
+}
+
+fs_status fs_rotary_grad(const fs_rotation* rot, const void* dq, const void* dk, void* dq_out,
+                         void* dk_out, void* stream) {
+    try {
+        return rotary::rotary_entry(rot, dq, dk, dq_out, dk_out, stream, true);
+    } catch (...) {
+        return fail(FS_ERR_CUDA, "unexpected host exception");
+    }
+}
+
+}  // extern "C"

@@ -1,0 +1,115 @@
+// C ABI of the tree attention: argument checks, workspace, choice of kernels.
+#include "fs_tree.cuh"
+
+#include <cmath>
+
+namespace fs {
+namespace tree {
+
+namespace {
+
+// Splits of the keys of the few-row kernel.  A split costs its keys and a fixed part
+// (set-up, its share of the join) worth about 512 keys of 16 bits; blocks beyond the
+// resident ones wait for a whole turn.  The fewest splits of the least cost.
+int choose_few_splits(int64_t blocks, int m, int64_t resident) {
+    constexpr double kFixedKeys = 512.0;
+    if (blocks > kCounters) return 1;
+    const int64_t most = std::min<int64_t>((m + kFewKeys - 1) / kFewKeys, 4 * resident / blocks + 1);
+    int best = 1;
+    double least = 0.0;
+    for (int64_t s = 1; s <= most; ++s) {
+        const double turns = (double)((blocks * s + resident - 1) / resident);
+        const double cost = turns * ((double)m / (double)s + kFixedKeys);
+        if (s == 1 || cost < 0.999 * least) {
+            least = cost;
+            best = (int)s;
+        }
+    }
+    return best;
+}
+
+fs_status tree_entry(const fs_cache* cache, const fs_tree* t, const void* q, void* out, float* lse,
+                     void* stream) {
+    const int dev = attn::current_device();
+    FewArgs p = {};
+    Args& a = p.a;
+    FS_TRY(kv::fill_cache(dev, a.c, cache, false));
+    if (!t) return fail(FS_ERR_INVALID_ARG, "null fs_tree");
+    if (t->dtype != FS_DTYPE_BF16 && t->dtype != FS_DTYPE_F16)
+        return fail(FS_ERR_INVALID_ARG, "fs_tree.dtype=%d", t->dtype);
+    if (cache->dtype < FS_DTYPE_E4M3 && t->dtype != cache->dtype)
+        return fail(FS_ERR_INVALID_ARG, "queries of dtype %d for a cache of dtype %d", t->dtype, cache->dtype);
+    constexpr int kMostHeads = 1 << 16;
+    if (t->heads < 1 || t->heads > kMostHeads || t->heads % a.c.G != 0)
+        return fail(FS_ERR_INVALID_ARG, "heads=%d is not a multiple of kv_heads=%d", t->heads, a.c.G);
+    if (t->n < 0 || t->n > kv::kMaxTree)
+        return fail(FS_ERR_INVALID_ARG, "n=%lld out of range [0, %d]", (long long)t->n, kv::kMaxTree);
+    if (!(t->scale > 0.f) || !std::isfinite((float)(t->scale * kLog2e)))
+        return fail(FS_ERR_INVALID_ARG, "scale must be positive and finite in base 2 (got %g)",
+                    (double)t->scale);
+    if (t->reserved) return fail(FS_ERR_INVALID_ARG, "fs_tree.reserved must be zero");
+    if (t->parents && t->parents_stride < 0) return fail(FS_ERR_INVALID_ARG, "negative parents_stride");
+    a.H = t->heads;
+    a.R = t->heads / a.c.G;
+    a.n = (int)t->n;
+    a.d = a.c.d;
+    a.bf16 = t->dtype == FS_DTYPE_BF16;
+    a.scale2 = (float)((double)t->scale * kLog2e);
+    const int64_t B = a.c.B;
+    FS_TRY(attn::view(dev, a.q, q, t->q_stride, B, t->n, a.H, a.d, false, "q"));
+    FS_TRY(attn::view(dev, a.o, out, t->out_stride, B, t->n, a.H, a.d, true, "out"));
+    FS_TRY(attn::check_ptr(dev, lse, B * t->n, "lse"));
+    FS_TRY(attn::check_ptr(dev, t->ctx_len, B * t->n, "ctx_len"));
+    FS_TRY(attn::check_ptr(dev, t->parents, t->parents ? B * t->n : 0, "parents"));
+    if ((double)B * a.H * a.n > (double)INT32_MAX)
+        return fail(FS_ERR_UNSUPPORTED, "%.3g rows of queries in one call", (double)B * a.H * a.n);
+    const int64_t rows = B * a.H * a.n;
+    if (rows == 0) return FS_OK;
+    a.lse = lse;
+    a.ctx_len = t->ctx_len;
+    a.parents = t->parents;
+    a.parents_stride = t->parents_stride;
+    a.q_vec = attn::aligned16(a.q, a.c.B, a.n, a.H);
+    NvtxRange range("fs_tree_attention");
+    Call c;
+    int sms = 0, resident = 0;
+    FS_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    p.row_blocks = a.R * a.n <= 8 ? 1 : 2;
+    p.groups = (a.R * a.n + 8 * p.row_blocks - 1) / (8 * p.row_blocks);
+    p.dp = (a.d + 3) / 4 * 4;
+    FS_CUDA(few_resident(a, p.row_blocks, &resident));
+    p.splits = choose_few_splits(B * a.c.G * p.groups, a.c.reach(), (int64_t)sms * resident);
+    p.part.rows = rows;
+    size_t part_out = 0, part_lse = 0;
+    if (p.splits > 1) {
+        part_out = c.L.take(sizeof(float) * (size_t)p.splits * rows * p.dp);
+        part_lse = c.L.take(sizeof(float) * (size_t)p.splits * rows);
+    }
+    const bool scratch = c.L.off > 0;
+    FS_TRY(begin_call(c, stream, scratch));
+    FS_TRY(ensure_capacity(c));
+    if (scratch) {
+        p.part.out = c.at<float>(part_out);
+        p.part.lse2 = c.at<float>(part_lse);
+    }
+    a.err = c.ws->err_word;
+    p.counters = c.ws->counters;
+    FS_CUDA(launch_few(p, c.stream));
+    return scratch ? end_call(c) : FS_OK;
+}
+
+}  // namespace
+
+}  // namespace tree
+}  // namespace fs
+
+using namespace fs;
+
+extern "C" fs_status fs_tree_attention(const fs_cache* cache, const fs_tree* tree, const void* q, void* out,
+                                       float* lse, void* stream) {
+    try {
+        return tree::tree_entry(cache, tree, q, out, lse, stream);
+    } catch (...) {
+        return fail(FS_ERR_CUDA, "unexpected host exception");
+    }
+}

@@ -1,0 +1,81 @@
+// Launch interfaces of the tree attention's kernels.
+//
+// Rows of a sequence and key head are (token t, query head r of the R that share it),
+// row = t R + r.  Keys are positions: below `ctx` all rows see them, from there on they are
+// the tree's tokens, and bits say which of them a token sees.
+#pragma once
+
+#include "fs_kv.cuh"
+
+namespace fs {
+namespace tree {
+
+using attn::Partials;
+using attn::View;
+using kv::Cache;
+
+struct Args {
+    Cache c;
+    View q, o;
+    int H, R, n, d;
+    int bf16;
+    int q_vec;                   // the rows of q take 16-byte loads
+    float scale2;                // scale log2(e)
+    float* lse;                  // [B][H][n], natural logarithm
+    const int32_t* ctx_len;      // [B]
+    const int32_t* parents;      // rows of n, or nullptr (a chain)
+    int64_t parents_stride;
+    uint32_t* err;               // device error word
+};
+
+__device__ __forceinline__ int context(const Args& a, int b) {
+    const int l = __ldg(a.ctx_len + b);
+    return l < 0 ? 0 : min(l, a.c.reach());
+}
+
+// What a token of the tree sees of it: bit u for token u, none if it is not there.
+constexpr int kTreeWords = kv::kMaxTree / 32;
+// parents: in shared memory, or nullptr for a chain
+__device__ __forceinline__ void tree_row(const int* parents, int t, uint32_t* words) {
+#pragma unroll
+    for (int w = 0; w < kTreeWords; ++w) words[w] = 0;
+    if (parents == nullptr) {
+        for (int w = 0; w <= t >> 5; ++w) words[w] = w < t >> 5 ? 0xffffffffu : (2u << (t & 31)) - 1u;
+        return;
+    }
+    int u = t;
+    while (u >= 0) {
+        words[u >> 5] |= 1u << (u & 31);
+        const int up = parents[u];
+        if (up >= u || up < -1) {         // no parent: the token is not there
+#pragma unroll
+            for (int w = 0; w < kTreeWords; ++w) words[w] = 0;
+            return;
+        }
+        u = up;
+    }
+}
+// 32 keys from key `at` of the tree on (above -32), as a row sees them; the keys before
+// the tree too, where the row is there.  words: kTreeWords + 1 of them, the last zero.
+__device__ __forceinline__ uint32_t tree_window(const uint32_t* words, bool there, int at) {
+    if (!there) return 0;
+    if (at < 0) return at <= -32 ? 0xffffffffu : words[0] << -at | ((1u << -at) - 1u);
+    if (at >= kv::kMaxTree) return 0;
+    return __funnelshift_r(words[at >> 5], words[(at >> 5) + 1], at & 31);
+}
+
+// Few rows: row_blocks of 8 rows to a block (1 or 2), in `groups`.
+struct FewArgs {
+    Args a;
+    Partials part;
+    int splits, groups, row_blocks;
+    int dp;                // elements of a partial row: d, to a multiple of 4
+    unsigned* counters;    // [batch x key heads x groups], zero between calls
+};
+constexpr int kFewKeys = 128;          // the splits are whole multiples of these keys
+cudaError_t launch_few(const FewArgs& p, cudaStream_t s);
+// blocks of it that an SM holds
+cudaError_t few_resident(const Args& a, int row_blocks, int* blocks);
+
+}  // namespace tree
+}  // namespace fs

@@ -1,0 +1,638 @@
+// Tree attention, few query rows per key head: bound by reading the cache once.
+//
+// As in the cross attention of few queries, the rows that share a key head are one tile of
+// 8 or 16, blocks split the keys, and a warp takes 32 keys at a time straight from memory
+// into the operand registers of mma.sync (S = Q K^T with any 16 of the d elements in a
+// product, the same for both operands; O^T += V^T P^T, with P^T in S's own layout).
+//
+// A cache in 8 bits is widened to float16 in registers, which is exact: a lane's 16 bytes
+// of a key row are 4 products' worth of its operand, and of four value rows a byte permute
+// pairs two keys before they are widened.  Scales stay in float32:
+//   x_ij = q_i . code_j (scale2 ks_j) + log2 vs_j,   P_ij = 2^{x_ij - ref_i},
+//   O_i = sum_j P_ij code_j,   sum_i = sum_j P_ij / vs_j,
+// so that the largest P of a row is the one that counts most in O, whatever the scales,
+// and float16 holds them all as it holds weights.  Queries in bfloat16 are multiplied by a
+// power of two for each row, which float16 then holds to all their bits.
+#include "fs_tree.cuh"
+
+#include <type_traits>
+
+namespace fs {
+namespace tree {
+
+namespace {
+
+using namespace fs::attn;
+using kv::HELD_16;
+using kv::HELD_E4M3;
+using kv::HELD_I8;
+
+constexpr int kWarps = 4;
+constexpr int kWords = kTreeWords + 1;
+
+template <bool BF>
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    if (BF)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ld16(const uint8_t* p, bool on, uint32_t* x) {
+    x[0] = x[1] = x[2] = x[3] = 0;
+    if (on)
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "l"(p));
+}
+__device__ __forceinline__ void ld8(const uint8_t* p, bool on, uint32_t* x) {
+    x[0] = x[1] = 0;
+    if (on)
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+                     : "=r"(x[0]), "=r"(x[1])
+                     : "l"(p));
+}
+// 16 codes from element c on, zero from d on
+__device__ __forceinline__ void ld_codes16(const uint8_t* row, int c, int d, bool on, bool vec16, uint32_t* x) {
+    if (vec16) {
+        ld16(row + c, on && c < d, x);
+    } else {
+        ld8(row + c, on && c < d, x);
+        ld8(row + c + 8, on && c + 8 < d, x + 2);
+    }
+}
+
+// whether a register of the held type has an element that is not finite
+template <int HELD, bool BF>
+__device__ __forceinline__ bool nonfinite(uint32_t w) {
+    if (HELD == HELD_I8) return false;
+    if (HELD == HELD_E4M3) {
+        const uint32_t m = w & 0x7f7f7f7fu;       // a byte of 0x7f
+        return ((m + 0x01010101u) & 0x80808080u) != 0;
+    }
+    constexpr uint32_t kExp = BF ? 0x7f80u : 0x7c00u;
+    return (w & kExp) == kExp || ((w >> 16) & kExp) == kExp;
+}
+
+// RB: blocks of 8 query rows
+template <int HD, int RB>
+constexpr size_t kFewSmem = sizeof(float) * kWarps * 8 * RB * (HD + 2);
+
+template <int HD, int HELD, bool BF, int RB>
+__global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant__ FewArgs P) {
+    using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+    constexpr bool Q8 = HELD != HELD_16;
+    constexpr bool MB = BF && !Q8;                    // products in bfloat16
+    constexpr int EB = Q8 ? 1 : 2;                    // bytes of an element
+    constexpr int PIECE = 16 / EB;                    // elements of a key piece
+    constexpr int U = HD / (4 * PIECE);               // key pieces of a lane
+    constexpr int VW = HD * EB / 32;                  // registers of a lane's part of a value row
+    constexpr int NT = HD / 16;                       // O tiles: two elements of d to a lane
+    constexpr int KB = !Q8 && HD == 64 ? 1 : 2, KEYS = 16 * KB;
+    constexpr int RP = (RB + 1) / 2, ROWS = 8 * RB;
+    constexpr float kShift = kProbShift<MB>;
+    extern __shared__ float smem[];
+    float* sO = smem;                                   // [warp][row][HD]
+    float* sRef = sO + kWarps * ROWS * HD;              // [warp][row]
+    float* sSum = sRef + kWarps * ROWS;
+    __shared__ int sParents[kv::kMaxTree];
+    __shared__ uint32_t sTree[ROWS][kWords];
+    __shared__ int sLast;
+    const Args& a = P.a;
+    const Cache& c = a.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+
+    int blk = blockIdx.x;
+    const int split = blk % P.splits;
+    blk /= P.splits;
+    const int group = blk % P.groups;
+    blk /= P.groups;
+    const int kh = blk % c.G;
+    const int b = blk / c.G;
+    const int nrows = min(ROWS, a.R * a.n - group * ROWS);
+    const int ctx = context(a, b);
+    const int end = min(ctx + a.n, c.reach());
+    // this split's keys, in whole steps of the block
+    const int steps = (end + kFewKeys - 1) / kFewKeys;
+    const int per = (steps + P.splits - 1) / P.splits;
+    const int k0 = (int)min((int64_t)end, (int64_t)split * per * kFewKeys);
+    const int k1 = (int)min((int64_t)end, k0 + (int64_t)per * kFewKeys);
+
+    // what each row sees of the tree
+    if (a.parents) {
+        const int32_t* p = a.parents + b * a.parents_stride;
+        for (int e = threadIdx.x; e < a.n; e += 32 * kWarps) sParents[e] = __ldg(p + e);
+        __syncthreads();
+    }
+    if (threadIdx.x < ROWS) {
+        const int row = group * ROWS + min((int)threadIdx.x, nrows - 1);
+        tree_row(a.parents ? sParents : nullptr, row / a.R, sTree[threadIdx.x]);
+        sTree[threadIdx.x][kTreeWords] = 0;
+    }
+
+    // Row 8 rb + g of the tile: its queries as the products' operand
+    uint32_t q[RB][U][4 * (Q8 ? 2 : 1)];
+    float mul[RB];                        // scale2, times what the row was divided by
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int row = group * ROWS + min(8 * rb + g, nrows - 1);
+        const int tok = row / a.R, r = row - tok * a.R;
+        const uint16_t* p = static_cast<const uint16_t*>(a.q.p) + b * a.q.sb + tok * a.q.st +
+                            (int64_t)(kh * a.R + r) * a.q.sh;
+        mul[rb] = a.scale2;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int x = 0; x < (Q8 ? 2 : 1); ++x) {
+                const int e = PIECE * (t + 4 * u) + 8 * x;
+                uint32_t* w = q[rb][u] + 4 * x;
+                if (a.q_vec) {
+                    ld16(reinterpret_cast<const uint8_t*>(p + e), e < a.d, w);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = e < a.d ? (uint32_t)p[e + 2 * k] | (uint32_t)p[e + 2 * k + 1] << 16 : 0u;
+                }
+            }
+        if (Q8 && BF) {
+            // the row's largest magnitude to [1, 2), then float16
+            uint32_t top = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    top = max(top, max(q[rb][u][k] & 0x7fffu, q[rb][u][k] >> 16 & 0x7fffu));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int ex = top >> 7;          // biased exponent; 0 and 255 are left alone
+            const int by = ex == 0 || ex == 255 ? 127 : min(ex, 253);
+            const float down = __uint_as_float((uint32_t)(254 - by) << 23);
+            mul[rb] = a.scale2 * __uint_as_float((uint32_t)by << 23);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t w = q[rb][u][k];
+                    q[rb][u][k] = pack16<false>(__uint_as_float(w << 16) * down,
+                                                __uint_as_float(w & 0xffff0000u) * down);
+                }
+        }
+    }
+    __syncthreads();
+    bool there[RB];
+    const uint32_t* words[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int row = group * ROWS + min(8 * rb + g, nrows - 1), tok = row / a.R;
+        words[rb] = sTree[min(8 * rb + g, nrows - 1)];
+        there[rb] = words[rb][tok >> 5] >> (tok & 31) & 1u;
+    }
+    float ref[RB], sum[RB], o[RB][NT][4];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        ref[rb] = -INFINITY;
+        sum[rb] = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT; ++w)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[rb][w][e] = 0.f;
+    }
+    const uint8_t* kp = c.k.p + kh * c.k.head;
+    const uint8_t* vp = c.v.p + kh * c.v.head;
+
+    for (int key = k0 + KEYS * warp; key < k1; key += KEYS * kWarps) {
+        // pages of each 8 of these keys (which none of them leaves), and what counts
+        int page[2 * KB];
+        uint32_t bits = 0;
+#pragma unroll
+        for (int nb = 0; nb < 2 * KB; ++nb) {
+            const int at = key + 8 * nb;
+            page[nb] = at < k1 ? c.page_of(b, at) : -1;
+            if (page[nb] >= 0) bits |= (at + 8 <= k1 ? 255u : (1u << (k1 - at)) - 1u) << (8 * nb);
+        }
+        if (bits == 0) continue;
+        uint32_t k[2 * KB][U][4], v[KB][4][VW];
+        float ks[4 * KB], lv[4 * KB], iv[4 * KB];      // of keys 8 nb + 2 t + {0, 1}
+#pragma unroll
+        for (int nb = 0; nb < 2 * KB; ++nb) {
+            const int j = 8 * nb + g;
+            const bool on = (bits >> j) & 1u;
+            const uint8_t* p = kp + page[nb] * c.k.page + c.slot_of(key + j) * c.k.token;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (Q8)
+                    ld_codes16(p, PIECE * (t + 4 * u), a.d, on, c.vec16, k[nb][u]);
+                else
+                    ld16(p + 16 * (t + 4 * u), on && PIECE * (t + 4 * u) < a.d, k[nb][u]);
+            }
+        }
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int j = 16 * kb + 2 * t + (x & 1) + 8 * (x >> 1);
+                const bool on = (bits >> j) & 1u;
+                const uint8_t* p = vp + page[2 * kb + (x >> 1)] * c.v.page + c.slot_of(key + j) * c.v.token;
+                if (Q8) {
+                    if (HD == 128)
+                        ld_codes16(p, 16 * g, a.d, on, c.vec16, v[kb][x]);
+                    else
+                        ld8(p + 8 * g, on && 8 * g < a.d, v[kb][x]);
+                } else {
+#pragma unroll
+                    for (int w = 0; w < HD / 64; ++w)
+                        ld16(p + 16 * g + 128 * w, on && 8 * g + 64 * w < a.d, v[kb][x] + 4 * w);
+                }
+            }
+        if (Q8) {
+#pragma unroll
+            for (int e = 0; e < 4 * KB; ++e) {
+                const int nb = e >> 1, j = 8 * nb + 2 * t + (e & 1);
+                const bool on = (bits >> j) & 1u;
+                const int slot = c.slot_of(key + j);
+                ks[e] = on ? __ldg(c.k.scale + page[nb] * c.k.s_page + kh * c.k.s_head + slot) : 0.f;
+                lv[e] = on ? __ldg(c.v.scale + page[nb] * c.v.s_page + kh * c.v.s_head + slot) : 1.f;
+            }
+        }
+        float s[RP][2 * KB][4];
+#pragma unroll
+        for (int rp = 0; rp < RP; ++rp)
+#pragma unroll
+            for (int nb = 0; nb < 2 * KB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[rp][nb][e] = 0.f;
+        constexpr bool pair = RB > 1;
+#pragma unroll
+        for (int nb = 0; nb < 2 * KB; ++nb)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                // the products' second operand: two registers each
+                uint32_t w[4 * (Q8 ? 2 : 1)];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    if (Q8)
+                        kv::widen4<HELD>(k[nb][u][y], w[2 * y], w[2 * y + (Q8 ? 1 : 0)]);
+                    else
+                        w[y] = k[nb][u][y];
+                }
+#pragma unroll
+                for (int y = 0; y < (Q8 ? 8 : 4); y += 2)
+#pragma unroll
+                    for (int rp = 0; rp < RP; ++rp)
+                        mma16816<MB>(s[rp][nb], q[2 * rp][u][y], pair ? q[pair ? 2 * rp + 1 : 0][u][y] : 0u,
+                                     q[2 * rp][u][y + 1], pair ? q[pair ? 2 * rp + 1 : 0][u][y + 1] : 0u,
+                                     w[y], w[y + 1]);
+            }
+        // Among the tree's keys a row may not see some that others do, and a value of theirs
+        // that is not finite would reach it as 0 * NaN: such rows of V are zeroed, and
+        // their keys make the rows that see them NaN.
+        uint32_t poison = 0;                  // of keys 16 kb + 2 t + (x & 1) + 8 (x >> 1), bit 4 kb + x
+        const bool mixed = key + KEYS > ctx;
+        if (mixed) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int j = 16 * kb + 2 * t + (x & 1) + 8 * (x >> 1);
+                    if (key + j < ctx) continue;
+                    bool bad = false;
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) bad |= nonfinite<HELD, BF>(v[kb][x][w]);
+                    if (Q8) bad |= !(lv[4 * kb + x] < INFINITY);
+                    poison |= (uint32_t)bad << (4 * kb + x);
+                }
+            poison |= __shfl_xor_sync(0xffffffffu, poison, 4);
+            poison |= __shfl_xor_sync(0xffffffffu, poison, 8);
+            poison |= __shfl_xor_sync(0xffffffffu, poison, 16);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (poison >> (4 * kb + x) & 1u) {
+#pragma unroll
+                        for (int w = 0; w < VW; ++w) v[kb][x][w] = 0;
+                        if (Q8) lv[4 * kb + x] = 1.f;
+                    }
+        }
+        if (Q8) {
+#pragma unroll
+            for (int e = 0; e < 4 * KB; ++e) {
+                iv[e] = __fdividef(1.f, lv[e]);
+                lv[e] = lg2(lv[e]);
+            }
+        }
+        // scores of row 8 rb + g and keys 8 nb + 2 t + {0, 1}
+        uint32_t ph[RB][2 * KB], pl[RB][2 * KB];
+        float alpha[RB];
+        bool moved = false;
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            float x[4 * KB], top = -INFINITY;
+            const uint32_t sees = bits & (mixed ? tree_window(words[rb], there[rb], key - ctx)
+                                                : there[rb] ? 0xffffffffu : 0u);
+#pragma unroll
+            for (int e = 0; e < 4 * KB; ++e) {
+                const int j = 8 * (e >> 1) + 2 * t + (e & 1);
+                const float z = s[rb >> 1][e >> 1][2 * (rb & 1) + (e & 1)];
+                float y = Q8 ? fmaf(z * mul[rb], ks[e], lv[e]) : z * mul[rb];
+                // bit 4 kb + x, e = 4 kb + 2 (nb & 1) + (e & 1) and x = (j & 1) + 2 (nb & 1)
+                if (poison >> e & 1u) y = __uint_as_float(0x7fc00000u);
+                x[e] = (sees >> j) & 1u ? y : -INFINITY;
+                top = fmaxf(top, x[e]);
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            alpha[rb] = 1.f;
+            if (top > ref[rb] + 8.f) {
+                if (ref[rb] != -INFINITY) alpha[rb] = ex2(ref[rb] - top);
+                sum[rb] *= alpha[rb];
+                ref[rb] = top;
+                moved |= alpha[rb] != 1.f;
+            }
+            const float base = (ref[rb] == -INFINITY ? 0.f : ref[rb]) - kShift;
+#pragma unroll
+            for (int e = 0; e < 4 * KB; ++e) {
+                x[e] = ex2(x[e] - base);
+                sum[rb] = Q8 ? fmaf(x[e], iv[e], sum[rb]) : sum[rb] + x[e];
+            }
+#pragma unroll
+            for (int nb = 0; nb < 2 * KB; ++nb) {
+                const uint32_t h = pack16<MB>(x[2 * nb], x[2 * nb + 1]);
+                ph[rb][nb] = h;
+                if (MB)
+                    pl[rb][nb] = pack16<MB>(x[2 * nb] - __uint_as_float(h << 16),
+                                            x[2 * nb + 1] - __uint_as_float(h & 0xffff0000u));
+            }
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) {
+                // O's columns are rows 2 t and 2 t + 1 of the block
+                const float a0 = __shfl_sync(0xffffffffu, alpha[rb], 8 * t);
+                const float a1 = __shfl_sync(0xffffffffu, alpha[rb], 8 * t + 4);
+#pragma unroll
+                for (int w = 0; w < NT; ++w) {
+                    o[rb][w][0] *= a0;
+                    o[rb][w][1] *= a1;
+                    o[rb][w][2] *= a0;
+                    o[rb][w][3] *= a1;
+                }
+            }
+        }
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+                const uint32_t x0 = v[kb][0][w], x1 = v[kb][1][w], x2 = v[kb][2][w], x3 = v[kb][3][w];
+                uint32_t m[2][4];             // operands of the products of this register
+                if (Q8) {
+                    kv::widen4<HELD>(__byte_perm(x0, x1, 0x5140), m[0][0], m[0][1]);
+                    kv::widen4<HELD>(__byte_perm(x2, x3, 0x5140), m[0][2], m[0][3]);
+                    kv::widen4<HELD>(__byte_perm(x0, x1, 0x7362), m[1][0], m[1][1]);
+                    kv::widen4<HELD>(__byte_perm(x2, x3, 0x7362), m[1][2], m[1][3]);
+                } else {
+                    m[0][0] = __byte_perm(x0, x1, 0x5410);
+                    m[0][1] = __byte_perm(x0, x1, 0x7632);
+                    m[0][2] = __byte_perm(x2, x3, 0x5410);
+                    m[0][3] = __byte_perm(x2, x3, 0x7632);
+                }
+#pragma unroll
+                for (int i = 0; i < (Q8 ? 2 : 1); ++i)
+#pragma unroll
+                    for (int rb = 0; rb < RB; ++rb) {
+                        float* to = o[rb][Q8 ? 2 * w + i : w];
+                        mma16816<MB>(to, m[i][0], m[i][1], m[i][2], m[i][3], ph[rb][2 * kb],
+                                     ph[rb][2 * kb + 1]);
+                        if (MB)
+                            mma16816<MB>(to, m[i][0], m[i][1], m[i][2], m[i][3], pl[rb][2 * kb],
+                                         pl[rb][2 * kb + 1]);
+                    }
+            }
+    }
+
+    // each warp's rows, then their join
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        sum[rb] += __shfl_xor_sync(0xffffffffu, sum[rb], 1);
+        sum[rb] += __shfl_xor_sync(0xffffffffu, sum[rb], 2);
+        if (t == 0) {
+            sRef[warp * ROWS + 8 * rb + g] = ref[rb];
+            sSum[warp * ROWS + 8 * rb + g] = sum[rb];
+        }
+#pragma unroll
+        for (int w = 0; w < NT; ++w) {
+            const int col = Q8 ? HD / 8 * g + 2 * w : 8 * (g + 8 * (w >> 2)) + 2 * (w & 3);
+            float* p = sO + (size_t)(warp * ROWS + 8 * rb + 2 * t) * HD + col;
+            *reinterpret_cast<float2*>(p) = make_float2(o[rb][w][0], o[rb][w][2]);
+            *reinterpret_cast<float2*>(p + HD) = make_float2(o[rb][w][1], o[rb][w][3]);
+        }
+    }
+    __syncthreads();
+    const int64_t head0 = (int64_t)b * a.H + kh * a.R;
+    // the place of a row of the tile among the results, rows (b, head, token)
+    const auto place = [&](int row) {
+        const int all = group * ROWS + row, tok = all / a.R;
+        return (head0 + (all - tok * a.R)) * a.n + tok;
+    };
+    const auto out_row = [&](int row) {
+        const int all = group * ROWS + row, tok = all / a.R;
+        return static_cast<T*>(a.o.p) + b * a.o.sb + tok * a.o.st + (int64_t)(kh * a.R + all - tok * a.R) * a.o.sh;
+    };
+    for (int row = warp; row < nrows; row += kWarps) {
+        const int64_t at = place(row);
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sRef[w * ROWS + row]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float total = 0.f, f[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            f[w] = ex2(sRef[w * ROWS + row] - base);
+            total = fmaf(f[w], sSum[w * ROWS + row], total);
+        }
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        const float lse2 = total == 0.f ? -INFINITY : top - kShift + lg2(total);
+        T* out = out_row(row);
+        float* part = P.part.out + (split * P.part.rows + at) * P.dp;
+        for (int e = lane; e < P.dp; e += 32) {
+            float x = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) x = fmaf(f[w], sO[(size_t)(w * ROWS + row) * HD + e], x);
+            x = total == 0.f ? 0.f : x * inv;
+            if (P.splits > 1)
+                part[e] = x;
+            else if (e < a.d)
+                out[e] = from_f<T>(x);
+        }
+        if (lane == 0) {
+            if (P.splits > 1)
+                P.part.lse2[split * P.part.rows + at] = lse2;
+            else
+                a.lse[at] = lse2 * (float)kLn2;
+        }
+    }
+    if (P.splits == 1) return;
+
+    // the last block of these rows joins the splits, in their order
+    __threadfence();
+    __syncthreads();
+    unsigned* count = P.counters + blockIdx.x / P.splits;
+    if (threadIdx.x == 0) {
+        const unsigned before = atomicAdd(count, 1u);
+        sLast = before == (unsigned)P.splits - 1;
+        if (sLast) *count = 0;        // ready for the next call
+    }
+    __syncthreads();
+    if (!sLast) return;
+    __threadfence();
+    // Weights of 256 splits at a time into shared memory (over sO), a row's in one warp;
+    // then a thread sums four elements of a row over them.
+    constexpr int kSome = 256;
+    constexpr int kQuads = HD / 4, kSums = ROWS * kQuads / (32 * kWarps);
+    static_assert(ROWS * kSome <= kWarps * ROWS * HD, "weights fit over the rows");
+    float top[ROWS / kWarps], total[ROWS / kWarps];
+#pragma unroll
+    for (int x = 0; x < ROWS / kWarps; ++x) {
+        const int row = warp + kWarps * x;
+        top[x] = -INFINITY;
+        total[x] = 0.f;
+        if (row < nrows) {
+            const float* l = P.part.lse2 + place(row);
+            for (int i = lane; i < P.splits; i += 32) top[x] = fmaxf(top[x], l[i * P.part.rows]);
+        }
+#pragma unroll
+        for (int y = 16; y; y >>= 1) top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], y));
+    }
+    float4 acc[kSums];
+#pragma unroll
+    for (int x = 0; x < kSums; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < P.splits; s0 += kSome) {
+        const int some = min(kSome, P.splits - s0);
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < ROWS / kWarps; ++x) {
+            const int row = warp + kWarps * x;
+            if (row >= nrows) continue;
+            const float* l = P.part.lse2 + place(row);
+            float w_sum = 0.f;
+            for (int i = lane; i < some; i += 32) {
+                const float w = ex2(l[(s0 + i) * P.part.rows] - (top[x] == -INFINITY ? 0.f : top[x]));
+                sO[row * kSome + i] = w;
+                w_sum += w;
+            }
+#pragma unroll
+            for (int y = 16; y; y >>= 1) w_sum += __shfl_xor_sync(0xffffffffu, w_sum, y);
+            total[x] += w_sum;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kSums; ++x) {
+            const int e = threadIdx.x + x * 32 * kWarps, row = e / kQuads, col = 4 * (e % kQuads);
+            if (row >= nrows || col >= a.d) continue;
+            const float* src = P.part.out + (s0 * P.part.rows + place(row)) * P.dp + col;
+            const float* w = sO + row * kSome;
+            const int64_t step = P.part.rows * P.dp;
+#pragma unroll 16
+            for (int i = 0; i < some; ++i) {
+                const float4 y = *reinterpret_cast<const float4*>(src + i * step);
+                acc[x].x = fmaf(w[i], y.x, acc[x].x);
+                acc[x].y = fmaf(w[i], y.y, acc[x].y);
+                acc[x].z = fmaf(w[i], y.z, acc[x].z);
+                acc[x].w = fmaf(w[i], y.w, acc[x].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < ROWS / kWarps; ++x) {
+        const int row = warp + kWarps * x;
+        if (lane == 0 && row < nrows) {
+            sSum[row] = total[x];
+            a.lse[place(row)] = total[x] == 0.f ? -INFINITY : (top[x] + lg2(total[x])) * (float)kLn2;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kSums; ++x) {
+        const int e = threadIdx.x + x * 32 * kWarps, row = e / kQuads, col = 4 * (e % kQuads);
+        if (row >= nrows || col >= a.d) continue;
+        T* out = out_row(row) + col;
+        const float inv = sSum[row] == 0.f ? 0.f : 1.f / sSum[row];
+        const float y[4] = {acc[x].x * inv, acc[x].y * inv, acc[x].z * inv, acc[x].w * inv};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (col + i < a.d) out[i] = from_f<T>(y[i]);
+    }
+}
+
+template <int HD, int HELD, bool BF, int RB>
+cudaError_t launch(const FewArgs& p, cudaStream_t s) {
+    static std::atomic<uint64_t> ready{0};    // devices whose shared-memory limit is raised
+    if (cudaError_t e = raise_smem(k_tree_few<HD, HELD, BF, RB>, kFewSmem<HD, RB>, ready); e != cudaSuccess)
+        return e;
+    const unsigned blocks = (unsigned)((int64_t)p.a.c.B * p.a.c.G * p.groups * p.splits);
+    k_tree_few<HD, HELD, BF, RB><<<blocks, 32 * kWarps, kFewSmem<HD, RB>, s>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <int HD, int HELD, bool BF, int RB>
+cudaError_t resident(int* blocks) {
+    static std::atomic<int> held{0};
+    *blocks = held.load();
+    if (*blocks > 0) return cudaSuccess;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, k_tree_few<HD, HELD, BF, RB>,
+                                                                        32 * kWarps, kFewSmem<HD, RB>);
+    if (e == cudaSuccess) held.store(*blocks);
+    return e;
+}
+
+// the kernel of a call, for `f` to run
+template <int HD, int HELD, typename F>
+cudaError_t pick_rows(const Args& a, int row_blocks, F f) {
+    if (a.bf16)
+        return row_blocks == 1 ? f.template run<HD, HELD, true, 1>() : f.template run<HD, HELD, true, 2>();
+    return row_blocks == 1 ? f.template run<HD, HELD, false, 1>() : f.template run<HD, HELD, false, 2>();
+}
+template <int HD, typename F>
+cudaError_t pick_held(const Args& a, int row_blocks, F f) {
+    if (a.c.held == HELD_16) return pick_rows<HD, HELD_16>(a, row_blocks, f);
+    return a.c.held == HELD_E4M3 ? pick_rows<HD, HELD_E4M3>(a, row_blocks, f)
+                                 : pick_rows<HD, HELD_I8>(a, row_blocks, f);
+}
+template <typename F>
+cudaError_t pick(const Args& a, int row_blocks, F f) {
+    return a.d <= 64 ? pick_held<64>(a, row_blocks, f) : pick_held<128>(a, row_blocks, f);
+}
+
+struct Launch {
+    const FewArgs& p;
+    cudaStream_t s;
+    template <int HD, int HELD, bool BF, int RB>
+    cudaError_t run() const { return launch<HD, HELD, BF, RB>(p, s); }
+};
+struct Resident {
+    int* blocks;
+    template <int HD, int HELD, bool BF, int RB>
+    cudaError_t run() const { return resident<HD, HELD, BF, RB>(blocks); }
+};
+
+}  // namespace
+
+cudaError_t launch_few(const FewArgs& p, cudaStream_t s) { return pick(p.a, p.row_blocks, Launch{p, s}); }
+
+cudaError_t few_resident(const Args& a, int row_blocks, int* blocks) {
+    return pick(a, row_blocks, Resident{blocks});
+}
+
+}  // namespace tree
+}  // namespace fs

@@ -128,6 +128,9 @@ fs_status make_chunk_tmap(void* map128, const void* base, uint64_t rows);
 // its boxes of 64 elements by box[1] rows in the 128-byte swizzle
 fs_status make_tmap_4d(void* map128, const void* base, const uint64_t* dims, const uint64_t* strides,
                        const uint32_t* box, bool bf16);
+// the same of a tensor of bytes, its boxes as they are
+fs_status make_tmap_4d_bytes(void* map128, const void* base, const uint64_t* dims, const uint64_t* strides,
+                             const uint32_t* box);
 
 // sm_balance: cost by the blocks per SM (dynamic scheduling over several
 // waves) instead of full waves.

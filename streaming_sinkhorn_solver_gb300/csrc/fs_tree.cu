@@ -28,6 +28,29 @@ int choose_few_splits(int64_t blocks, int m, int64_t resident) {
     return best;
 }
 
+// Splits of the keys of the tensor-core kernel, one block to an SM: a split costs its tiles
+// and a fixed part worth about 8 of them (set-up, its results); the join of several about
+// 12.  The fewest splits of the least cost.
+int choose_tc_splits(int64_t blocks, int m, int sms) {
+    constexpr double kFixed = 8.0, kJoin = 12.0;
+    const int tiles = (m + kTcKeys - 1) / kTcKeys;
+    const int64_t most = std::min<int64_t>((tiles + 3) / 4, 4 * (int64_t)sms / blocks + 1);
+    int best = 1;
+    double least = 0.0;
+    for (int64_t s = 1; s <= most; ++s) {
+        const double turns = (double)((blocks * s + sms - 1) / sms);
+        const double cost = turns * ((double)((tiles + s - 1) / s) + kFixed) + (s > 1 ? kJoin : 0.0);
+        if (s == 1 || cost < 0.999 * least) {
+            least = cost;
+            best = (int)s;
+        }
+    }
+    return best;
+}
+
+// Rows of a key head from which the tensor-core kernel takes a call.
+constexpr int kFewRows = 16;
+
 fs_status tree_entry(const fs_cache* cache, const fs_tree* t, const void* q, void* out, float* lse,
                      void* stream) {
     const int dev = attn::current_device();
@@ -72,29 +95,63 @@ fs_status tree_entry(const fs_cache* cache, const fs_tree* t, const void* q, voi
     a.q_vec = attn::aligned16(a.q, a.c.B, a.n, a.H);
     NvtxRange range("fs_tree_attention");
     Call c;
-    int sms = 0, resident = 0;
+    int sms = 0;
     FS_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    p.row_blocks = a.R * a.n <= 8 ? 1 : 2;
-    p.groups = (a.R * a.n + 8 * p.row_blocks - 1) / (8 * p.row_blocks);
-    p.dp = (a.d + 3) / 4 * 4;
-    FS_CUDA(few_resident(a, p.row_blocks, &resident));
-    p.splits = choose_few_splits(B * a.c.G * p.groups, a.c.reach(), (int64_t)sms * resident);
-    p.part.rows = rows;
+    const int per_head = a.R * a.n;
+    const bool few = per_head <= kFewRows || !tc_copies(a.c);
+    TcArgs tc = {};
+    int splits;
+    if (few) {
+        int resident = 0;
+        p.row_blocks = per_head <= 8 ? 1 : 2;
+        p.groups = (per_head + 8 * p.row_blocks - 1) / (8 * p.row_blocks);
+        FS_CUDA(few_resident(a, p.row_blocks, &resident));
+        splits = choose_few_splits(B * a.c.G * p.groups, a.c.reach(), (int64_t)sms * resident);
+    } else {
+        tc.keys = per_head <= 128;
+        tc.groups = (per_head + (tc.keys ? 127 : 255)) / (tc.keys ? 128 : 256);
+        tc.o_vec = attn::aligned16(a.o, a.c.B, a.n, a.H);
+        splits = choose_tc_splits(B * a.c.G * tc.groups, a.c.reach(), sms);
+    }
+    Partials part = {};
+    part.rows = rows;
     size_t part_out = 0, part_lse = 0;
-    if (p.splits > 1) {
-        part_out = c.L.take(sizeof(float) * (size_t)p.splits * rows * p.dp);
-        part_lse = c.L.take(sizeof(float) * (size_t)p.splits * rows);
+    if (splits > 1) {
+        part_out = c.L.take(sizeof(float) * (size_t)splits * rows * a.d);
+        part_lse = c.L.take(sizeof(float) * (size_t)splits * rows);
     }
     const bool scratch = c.L.off > 0;
     FS_TRY(begin_call(c, stream, scratch));
     FS_TRY(ensure_capacity(c));
     if (scratch) {
-        p.part.out = c.at<float>(part_out);
-        p.part.lse2 = c.at<float>(part_lse);
+        part.out = c.at<float>(part_out);
+        part.lse2 = c.at<float>(part_lse);
     }
     a.err = c.ws->err_word;
-    p.counters = c.ws->counters;
-    FS_CUDA(launch_few(p, c.stream));
+    if (few) {
+        p.part = part;
+        p.splits = splits;
+        p.dp = a.d;
+        p.counters = c.ws->counters;
+        FS_CUDA(launch_few(p, c.stream));
+    } else {
+        tc.a = a;
+        tc.part = part;
+        tc.splits = splits;
+        FS_TRY(tc_maps(tc, a.bf16));
+        FS_CUDA(launch_tc(tc, c.stream));
+        if (splits > 1) {
+            attn::Args j = {};
+            j.o = a.o;
+            j.B = a.c.B;
+            j.H = a.H;
+            j.n = a.n;
+            j.d = a.d;
+            j.bf16 = a.bf16;
+            j.lse = a.lse;
+            FS_CUDA(attn::launch_combine(j, part, splits, c.stream));
+        }
+    }
     return scratch ? end_call(c) : FS_OK;
 }
 

@@ -64,18 +64,43 @@ __device__ __forceinline__ uint32_t tree_window(const uint32_t* words, bool ther
     return __funnelshift_r(words[at >> 5], words[(at >> 5) + 1], at & 31);
 }
 
+// the same from words without the last, zero one
+__device__ __forceinline__ uint32_t tree_window8(const uint32_t* words, bool there, int at) {
+    if (!there) return 0;
+    if (at < 0) return at <= -32 ? 0xffffffffu : words[0] << -at | ((1u << -at) - 1u);
+    if (at >= kv::kMaxTree) return 0;
+    const int w = at >> 5;
+    return __funnelshift_r(words[w], w + 1 < kTreeWords ? words[w + 1] : 0u, at & 31);
+}
+
 // Few rows: row_blocks of 8 rows to a block (1 or 2), in `groups`.
 struct FewArgs {
     Args a;
     Partials part;
     int splits, groups, row_blocks;
-    int dp;                // elements of a partial row: d, to a multiple of 4
+    int dp;                // elements of a partial row: d, a multiple of 8
     unsigned* counters;    // [batch x key heads x groups], zero between calls
 };
 constexpr int kFewKeys = 128;          // the splits are whole multiples of these keys
 cudaError_t launch_few(const FewArgs& p, cudaStream_t s);
 // blocks of it that an SM holds
 cudaError_t few_resident(const Args& a, int row_blocks, int* blocks);
+
+// Many rows, on the tensor cores: `groups` of 128 rows (keys: the keys' tiles alternate
+// between two streams of scores) or of 256 (two tiles of rows).
+struct TcArgs {
+    CUtensorMap k, v;      // (d, token, head, page)
+    Args a;
+    Partials part;         // rows of d floats
+    int splits, groups;
+    int keys;
+    int o_vec;             // the rows of out take 16-byte stores
+};
+constexpr int kTcKeys = 64;            // keys of a tile
+// whether the cache's copies can be described to it
+bool tc_copies(const Cache& c);
+fs_status tc_maps(TcArgs& p, bool bf16);
+cudaError_t launch_tc(const TcArgs& p, cudaStream_t s);
 
 }  // namespace tree
 }  // namespace fs

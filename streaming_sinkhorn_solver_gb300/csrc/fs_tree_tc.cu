@@ -1,0 +1,899 @@
+// Tree attention, many query rows per key head, on the tensor cores.
+//
+// A block streams the keys of its share in tiles of 64 through two streams of scores:
+//   S_t = Q_t K^T (TMEM), P = 2^{x - ref} in 16 bits in TMEM, O_t += P V (TMEM),
+// either two tiles of 128 query rows that share every key tile (ROWS), or, where there are
+// 128 rows or fewer, one tile of rows whose key tiles go to the streams in turn (KEYS), joined at
+// the end; so the softmax of one stream runs beside the products of the other.
+//
+// Pages come by tensor copies, a page (or 64 keys of one) at a time; an entry without a
+// page is copied from beyond the end of the pool, which gives zeros.  Keys and values in 16
+// bits land as operand tiles.  Those in 8 bits land as they are, and four warps widen them to
+// float16 (exact).  Scales stay in float32:
+//   x_ij = q_i . code_j (scale2 ks_j) + log2 vs_j,   P_ij = 2^{x_ij - ref_i},
+//   O_i = sum_j P_ij code_j,   sum_i = sum_j P_ij / vs_j.
+// Queries in bfloat16 become float16 for that, the block's multiplied by one power of two that
+// brings the largest to 2^14: what the others lose, 2^-25 at most, is 2^-39 of it.
+//
+// A softmax thread holds 16 keys of each of 4 rows (the 16 x 256-bit form of TMEM loads), not
+// a row: the scales of its keys are then 24 loads of 8 bytes instead of 48 of 16 that
+// every lane reads alike, which took most of the shared memory's time.
+#include "fs_tree.cuh"
+
+#include <type_traits>
+
+namespace fs {
+namespace tree {
+
+namespace {
+
+using namespace fs::attn;
+using kv::HELD_16;
+using kv::HELD_E4M3;
+using kv::HELD_I8;
+
+constexpr int kSoftWarps = 8;              // 4 per stream
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kMma0 = kSoftWarps, kFit0 = kSoftWarps + 2, kFitWarps = 4;   // 2 for keys, 2 for values
+constexpr int kCopy = kFit0 + kFitWarps;
+constexpr int kTcThreads = 32 * (kCopy + 1);
+constexpr int kFitters = 32 * kFitWarps / 2;   // threads that fit the keys of a tile, and its values
+constexpr int kKeys = kTcKeys;
+constexpr float kRefSlack = 8.f;
+
+template <int HD, int HELD, bool KEYS>
+struct Tc {
+    static constexpr bool Q8 = HELD != HELD_16;
+    static constexpr int kChunks = HD / 64;
+    static constexpr int kChunkBytes = kKeys * 128;               // 64 elements of each key
+    static constexpr int kSlotBytes = kChunks * kChunkBytes;      // a tile of keys, or of values
+    static constexpr int kQBytes = kChunks * CHUNK_BYTES;
+    static constexpr int kQTiles = KEYS ? 1 : 2;
+    static constexpr int kRows = 128 * kQTiles;
+    static constexpr int kRing = Q8 ? (HD == 64 ? 4 : 3) : (HD == 64 ? 8 : 4);   // tiles of each
+    static constexpr int kRaw = !Q8 ? 0 : HD == 64 ? 8 : KEYS ? 4 : 3;           // as they land
+    static constexpr int kRawBytes = kKeys * HD;
+    // Descriptions of tiles are kept while the softmax may read them: it is behind the tile
+    // that a slot was last used for by up to 3 (alternating streams: 5), and 8-bit tiles are
+    // described when they are asked for, kRaw before that.
+    static constexpr int kScales = kRing + (KEYS ? 5 : 3);
+    static constexpr int kBits = kScales + kRaw;
+    __host__ __device__ static constexpr uint32_t S(int t) { return 256 * t; }
+    __host__ __device__ static constexpr uint32_t P(int t) { return S(t) + kKeys; }    // two of 32 columns
+    __host__ __device__ static constexpr uint32_t O(int t) { return P(t) + kKeys; }
+    static_assert(2 * kKeys + HD <= 256, "TMEM");
+};
+
+// What the softmax needs to know of a tile.
+struct TileBits {
+    uint32_t counted[2];
+    uint8_t poison_scale[kKeys], poison_value[kKeys];    // of the tree's keys
+};
+struct TileScales {
+    float kc[kKeys], lv[kKeys], iv[kKeys];   // of the scores; log2 and inverse of the value scale
+};
+struct TcBars {
+    uint64_t full[2][8], free_raw[2][8];     // copies landed; 8 bits: the ring they land in
+    uint64_t ready[2][8], empty[2][8];       // operand tiles (16 bits: values that were looked through)
+    uint64_t sfull[2], sfree[2], pfull[2][2], pfree[2][2], drain[2];
+    uint32_t tmem, pad;
+};
+
+template <int HD, int HELD, bool KEYS>
+struct Smem {
+    using C = Tc<HD, HELD, KEYS>;
+    static constexpr int q = 0;
+    static constexpr int ring = q + C::kQTiles * C::kQBytes;                  // [keys, values][slot]
+    static constexpr int raw = ring + 2 * C::kRing * C::kSlotBytes;           // [keys, values][slot][key][HD]
+    static constexpr int raw_scale = raw + 2 * C::kRaw * C::kRawBytes;        // [slot][keys, values][key]
+    static constexpr int scales = raw_scale + C::kRaw * 2 * kKeys * 4;
+    static constexpr int bits = scales + (C::Q8 ? C::kScales * (int)sizeof(TileScales) : 0);
+    static constexpr int words = bits + C::kBits * (int)sizeof(TileBits);     // [row's token][kTreeWords]
+    static constexpr int join = words + C::kRows * 4 * kTreeWords;            // [ref, sum][stream][row]
+    static constexpr int parents = join + (KEYS ? 4 * 4 * 128 : 0);
+    static constexpr int bars = parents + 4 * kv::kMaxTree;
+    static constexpr int top = bars + (int)sizeof(TcBars);                    // of the queries, by warps
+    static constexpr int bytes = top + 4 * kSoftWarps;
+    static_assert(bits % 16 == 0 && bars % 8 == 0, "alignment");
+    static_assert(1024 + bytes <= kSmemLimit, "shared memory");
+};
+
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at)
+                 : "memory");
+    return x;
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// 16 lanes x 64 columns (16 x 256-bit form): thread t gets, for i = 0..7, columns 8 i + 2 (t % 4) +
+// {0, 1} of lane t / 4 (v[4 i], v[4 i + 1]) and of lane t / 4 + 8 (v[4 i + 2], v[4 i + 3])
+__device__ __forceinline__ void tmem_ld16x64(uint32_t taddr, float* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]),
+          "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
+          "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]),
+          "=f"(v[31])
+        : "r"(taddr));
+}
+// 16 lanes x 32 columns (16 x 128-bit form): column 4 i + t % 4 of lane t / 4 (v[2 i]) and of
+// lane t / 4 + 8 (v[2 i + 1])
+__device__ __forceinline__ void tmem_st16x32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15])
+        : "memory");
+}
+
+// whether 16 bytes hold an element that is not finite
+template <int HELD, bool BF>
+__device__ __forceinline__ bool nonfinite16(const uint4& x) {
+    if (HELD == HELD_I8) return false;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (HELD == HELD_E4M3) {
+            bad |= (((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+        } else {
+            constexpr uint32_t kExp = BF ? 0x7f80u : 0x7c00u;
+            bad |= (w[k] & kExp) == kExp || (w[k] >> 16 & kExp) == kExp;
+        }
+    }
+    return bad;
+}
+
+// 2^n, -126 <= n <= 127
+__device__ __forceinline__ float two_to(int n) { return __int_as_float((127 + n) << 23); }
+
+// A block's share of the work.
+struct Share {
+    int b, kh, ctx, end, tile0, nt;
+    __device__ __forceinline__ int key_of(int j) const { return (tile0 + j) * kKeys; }
+    // first tile with keys of the tree, or behind the end
+    __device__ __forceinline__ int mixed_from() const { return min(max(ctx / kKeys - tile0, 0), nt); }
+};
+
+// The copying warp.
+template <int HD, int HELD, bool KEYS>
+__device__ __forceinline__ void copy_tiles(const TcArgs& P, const Share& w, uint8_t* smem, TcBars& bar, int& asked,
+                                           int to, int& entry, int& entry2, Ring& r, int& bits) {
+    using C = Tc<HD, HELD, KEYS>;
+    using M = Smem<HD, HELD, KEYS>;
+    constexpr int kSlots = C::Q8 ? C::kRaw : C::kRing;
+    const Args& a = P.a;
+    const int lane = threadIdx.x & 31;
+    const int rows = min(kKeys, 1 << a.c.log_page);            // of a copy
+    const auto load_entry = [&](int j) {
+        // of the tile's keys 8 (lane & 7) on
+        const int i = (w.key_of(j) + 8 * (lane & 7)) >> a.c.log_page;
+        int x = -1;
+        if (i < a.c.table_pages)
+            asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(a.c.table + w.b * a.c.table_stride + i));
+        return x;
+    };
+    if (asked == 0) {
+        entry = load_entry(0);
+        entry2 = load_entry(1);
+    }
+#pragma unroll 1
+    for (; asked < to; ++asked) {
+        const int j = asked;
+        const int key0 = w.key_of(j), key = key0 + 8 * (lane & 7);
+        const bool on = (unsigned)entry < a.c.pages && key < w.end;
+        const int page = on ? entry : (int)a.c.pages;          // (one behind the last: zeros)
+        entry = entry2;
+        entry2 = load_entry(j + 2);
+        if (j >= kSlots) {
+            uint64_t* const gone = C::Q8 ? &bar.free_raw[0][0] : &bar.empty[0][0];
+            if (!warp_wait(gone + r.slot, r.phase ^ 1u, a.err, ERR_TIMEOUT_PRODUCER) ||
+                !warp_wait(gone + 8 + r.slot, r.phase ^ 1u, a.err, ERR_TIMEOUT_PRODUCER))
+                return;
+        }
+        // keys that count, 8 to a lane
+        const int left = w.end - key;
+        const uint32_t byte = !on ? 0u : left >= 8 ? 255u : (1u << left) - 1u;
+        const uint32_t lo = __reduce_or_sync(0xffffffffu, lane < 4 ? byte << (8 * lane) : 0u);
+        const uint32_t hi = __reduce_or_sync(0xffffffffu, lane >= 4 && lane < 8 ? byte << (8 * (lane - 4)) : 0u);
+        const uint32_t pages = __ballot_sync(0xffffffffu, on) & 255u;
+        if (lane == 0)
+            *reinterpret_cast<uint2*>(reinterpret_cast<TileBits*>(smem + M::bits)[bits].counted) = make_uint2(lo, hi);
+        __syncwarp();
+        if (C::Q8) {
+            // scales, only where there is a page
+            int copies = 0;
+            for (int c = 0; c < kKeys; c += rows) copies += pages >> (c >> 3) & 1;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&bar.full[0][r.slot], C::kRawBytes + 2 * 4 * rows * copies);
+                mbar_arrive_expect_tx(&bar.full[1][r.slot], C::kRawBytes);
+            }
+        } else if (elect_one()) {
+            mbar_arrive_expect_tx(&bar.full[0][r.slot], C::kSlotBytes);
+            mbar_arrive_expect_tx(&bar.full[1][r.slot], C::kSlotBytes);
+        }
+        __syncwarp();
+        for (int c = 0; c < kKeys; c += rows) {
+            const int pg = __shfl_sync(0xffffffffu, page, c >> 3);
+            const int slot = a.c.slot_of(key0 + c);
+            if (elect_one()) {
+                if (C::Q8) {
+                    uint8_t* k = smem + M::raw + r.slot * C::kRawBytes + c * HD;
+                    tma_load(k, &P.k, 0, slot, w.kh, pg, &bar.full[0][r.slot]);
+                    tma_load(k + C::kRaw * C::kRawBytes, &P.v, 0, slot, w.kh, pg,
+                             &bar.full[1][r.slot]);
+                    if (pages >> (c >> 3) & 1) {
+                        float* s = reinterpret_cast<float*>(smem + M::raw_scale) + r.slot * 2 * kKeys + c;
+                        const kv::Pool &pk = a.c.k, &pv = a.c.v;
+                        bulk_g2s(s, pk.scale + pg * pk.s_page + w.kh * pk.s_head + slot, 4 * rows,
+                                 &bar.full[0][r.slot]);
+                        bulk_g2s(s + kKeys, pv.scale + pg * pv.s_page + w.kh * pv.s_head + slot, 4 * rows,
+                                 &bar.full[0][r.slot]);
+                    }
+                } else {
+                    uint8_t* k = smem + M::ring + r.slot * C::kSlotBytes + c * 128;
+#pragma unroll
+                    for (int x = 0; x < C::kChunks; ++x) {
+                        tma_load(k + x * C::kChunkBytes, &P.k, 64 * x, slot, w.kh, pg,
+                                 &bar.full[0][r.slot]);
+                        tma_load(k + C::kRing * C::kSlotBytes + x * C::kChunkBytes, &P.v, 64 * x, slot,
+                                 w.kh, pg, &bar.full[1][r.slot]);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        r.step(1, kSlots);
+        if (++bits == C::kBits) bits = 0;
+    }
+}
+
+// The fitting warps of keys (KV = 0) or values (1).  8 bits: every tile is widened into an
+// operand tile.  16 bits: of the values, tiles with keys of the tree are looked through.
+template <int HD, int HELD, bool BF, bool KEYS, int KV>
+__device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8_t* smem, TcBars& bar, int tid,
+                                          float mul) {
+    using C = Tc<HD, HELD, KEYS>;
+    using M = Smem<HD, HELD, KEYS>;
+    constexpr bool Q8 = C::Q8;
+    constexpr int kPer = HD / (Q8 ? 16 : 8);            // 16-byte pieces of a row
+    constexpr int kMine = kKeys * kPer / kFitters;      // of a thread: rows kStep apart
+    constexpr int kStep = kFitters / kPer;
+    if (!Q8 && KV == 0) return;
+    const Args& a = P.a;
+    const int lane = threadIdx.x & 31;
+    const int u = tid % kPer, row0 = tid / kPer;
+    const int mixed_from = w.mixed_from(), j0 = Q8 ? 0 : mixed_from;
+    Ring from, to;
+    if (!Q8) {
+        to.slot = j0 % C::kRing;
+        to.phase = j0 / C::kRing & 1;
+    }
+    int scales = 0, bits = j0 % C::kBits;
+    // pieces of a row are in neighbouring lanes
+    const auto look = [&](const uint4& x, int key0, int row, uint8_t* flags) {
+        uint32_t bad = key0 + row >= w.ctx && nonfinite16<HELD, BF>(x);
+#pragma unroll
+        for (int o = kPer / 2; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+        if (u == 0) flags[row] = (uint8_t)bad;
+        return bad != 0;
+    };
+#pragma unroll 1
+    for (int j = j0; j < w.nt; ++j) {
+        const int key0 = w.key_of(j);
+        TileBits& tb = reinterpret_cast<TileBits*>(smem + M::bits)[bits];
+        // Of the tree's keys: a value row with an element that is not finite is zeroed, and told
+        // to the softmax (0 * NaN would reach the rows that do not see it).  Rows behind the
+        // end may hold anything: they are zeroed too.
+        const bool mixed = j >= mixed_from;
+        const uint32_t slot = smem_u32(smem) + M::ring + (KV * C::kRing + to.slot) * C::kSlotBytes;
+        if (Q8) {
+            if (!warp_wait(&bar.full[KV][from.slot], from.phase, a.err, ERR_TIMEOUT_PRODUCER)) return;
+            const uint32_t raw = smem_u32(smem) + M::raw + (KV * C::kRaw + from.slot) * C::kRawBytes + 16 * tid;
+            uint4 x[kMine];
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) x[i] = lds16(raw + i * (16 * kFitters));
+            if (mixed) {
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    const int row = row0 + i * kStep;
+                    const bool out = key0 + row >= w.end;
+                    if (out) x[i] = make_uint4(0, 0, 0, 0);
+                    if (KV == 1 && HELD == HELD_E4M3 && look(x[i], key0, row, tb.poison_value))
+                        x[i] = make_uint4(0, 0, 0, 0);
+                }
+            }
+            float ks = 0.f, vs = 0.f;
+            if (KV == 0) {
+                const float* s = reinterpret_cast<const float*>(smem + M::raw_scale) + from.slot * 2 * kKeys + tid;
+                if (tb.counted[tid >> 5] >> (tid & 31) & 1u) {
+                    ks = s[0];
+                    vs = s[kKeys];
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.free_raw[KV][from.slot]);
+            if (j >= C::kRing && !warp_wait(&bar.empty[KV][to.slot], to.phase ^ 1u, a.err, ERR_TIMEOUT_PRODUCER))
+                return;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int row = row0 + i * kStep;
+                constexpr int kHeld = HELD == HELD_16 ? HELD_I8 : HELD;
+                uint32_t y[8];
+                kv::widen4<kHeld>(x[i].x, y[0], y[1]);
+                kv::widen4<kHeld>(x[i].y, y[2], y[3]);
+                kv::widen4<kHeld>(x[i].z, y[4], y[5]);
+                kv::widen4<kHeld>(x[i].w, y[6], y[7]);
+                const uint32_t at = slot + (u >> 2) * C::kChunkBytes;
+                sts16(at + swz_offset(row, (u & 3) * 16), y[0], y[1], y[2], y[3]);
+                sts16(at + swz_offset(row, (u & 3) * 16 + 8), y[4], y[5], y[6], y[7]);
+            }
+            if (KV == 0) {
+                TileScales& ts = reinterpret_cast<TileScales*>(smem + M::scales)[scales];
+                const bool bad = mixed && key0 + tid >= w.ctx && !(vs < INFINITY);
+                const bool none = vs == 0.f || bad;            // (0: the key does not count)
+                ts.kc[tid] = ks * mul;
+                ts.lv[tid] = none ? 0.f : lg2(vs);
+                ts.iv[tid] = none ? 0.f : __fdividef(1.f, vs);
+                tb.poison_scale[tid] = bad;
+            }
+        } else {
+            if (!warp_wait(&bar.full[1][to.slot], to.phase, a.err, ERR_TIMEOUT_PRODUCER)) return;
+#pragma unroll 4
+            for (int i = 0; i < kMine; ++i) {
+                const int row = row0 + i * kStep;
+                const uint32_t at = slot + (u >> 3) * C::kChunkBytes + swz_offset(row, (u & 7) * 8);
+                const bool bad = look(lds16(at), key0, row, tb.poison_value);
+                if (bad || key0 + row >= w.end) sts16(at, 0, 0, 0, 0);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.ready[KV][to.slot]);
+        if (Q8) from.step(1, Q8 ? C::kRaw : 1);
+        to.step(1, C::kRing);
+        if (++scales == C::kScales) scales = 0;
+        if (++bits == C::kBits) bits = 0;
+    }
+}
+
+template <int HD, int HELD, bool BF, bool KEYS>
+__global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant__ TcArgs P) {
+    using C = Tc<HD, HELD, KEYS>;
+    using M = Smem<HD, HELD, KEYS>;
+    using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+    constexpr bool Q8 = C::Q8;
+    constexpr bool MB = BF && !Q8;             // products in bfloat16
+    constexpr int NR = C::kRing;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    const Args& a = P.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    TcBars& bar = *reinterpret_cast<TcBars*>(smem + M::bars);
+    uint32_t* sWords = reinterpret_cast<uint32_t*>(smem + M::words);
+    uint32_t* sTop = reinterpret_cast<uint32_t*>(smem + M::top);
+    int* sParents = reinterpret_cast<int*>(smem + M::parents);
+
+    int blk = blockIdx.x;
+    const int split = blk % P.splits;
+    blk /= P.splits;
+    const int group = blk % P.groups;
+    blk /= P.groups;
+    Share w;
+    w.kh = blk % a.c.G;
+    w.b = blk / a.c.G;
+    const int b = w.b, kh = w.kh;
+    const int ctx = w.ctx = context(a, b);
+    w.end = min(ctx + a.n, a.c.reach());
+    const int nt_all = (w.end + kKeys - 1) / kKeys;
+    const int per = (nt_all + P.splits - 1) / P.splits;
+    const int t0 = w.tile0 = min(nt_all, split * per);
+    const int nt = w.nt = min(nt_all, t0 + per) - t0;
+    const int mixed_from = w.mixed_from();
+    const int rows = a.R * a.n;
+    const int row0 = group * C::kRows;                 // the block's first row
+    const bool two = KEYS || row0 + 128 < rows;
+    const int tok0 = row0 / a.R, tok1 = min(rows - 1, row0 + C::kRows - 1) / a.R;
+    const int dsteps = (a.d + 15) >> 4;
+    // warps of a stream's softmax that have rows (the others leave their rows of P as they are)
+    const auto warps_of = [&](int t) { return min(4, (rows - row0 - (KEYS ? 0 : 128 * t) + 31) >> 5); };
+    float mul = a.scale2;
+    constexpr int kSlots = Q8 ? C::kRaw : NR;          // that copies land in
+    int asked = 0, entry = -1, entry2 = -1, bits = 0;
+    Ring copied;
+
+    if (warp == kCopy) {
+        // its barriers are its own until the block meets: it starts its copies before that
+        if (lane < 16) mbar_init(&bar.full[lane >> 3][lane & 7], 1);
+        fence_mbar_init();
+        __syncwarp();
+        copy_tiles<HD, HELD, KEYS>(P, w, smem, bar, asked, min(nt, kSlots), entry, entry2, copied, bits);
+    } else if (warp < kSoftWarps) {
+        // what the block's tokens see of the tree, then their queries as operand tiles
+        if (a.parents) {
+            const int32_t* p = a.parents + b * a.parents_stride;
+            for (int e = threadIdx.x; e < a.n; e += kSoftThreads) sParents[e] = __ldg(p + e);
+            named_sync(1, kSoftThreads);
+        }
+        if ((int)threadIdx.x <= tok1 - tok0) {
+            uint32_t x[kTreeWords];
+            tree_row(a.parents ? sParents : nullptr, tok0 + threadIdx.x, x);
+#pragma unroll
+            for (int k = 0; k < kTreeWords; ++k) sWords[threadIdx.x * kTreeWords + k] = x[k];
+        }
+        named_sync(1, kSoftThreads);
+        constexpr int kPieces = HD / 8;        // of a row, in neighbouring lanes
+        constexpr int kMine = C::kRows * kPieces / kSoftThreads, kStep = kSoftThreads / kPieces;
+        const int u = threadIdx.x % kPieces;
+        uint32_t x[kMine][4], top = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int all = row0 + threadIdx.x / kPieces + i * kStep;
+            x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0;
+            if (all < rows && 8 * u < a.d) {
+                const int tok = all / a.R;
+                const uint32_t* s = sWords + (tok - tok0) * kTreeWords;
+                if (s[tok >> 5] >> (tok & 31) & 1u) {
+                    const uint16_t* p = static_cast<const uint16_t*>(a.q.p) + b * a.q.sb + tok * a.q.st +
+                                        (int64_t)(kh * a.R + all - tok * a.R) * a.q.sh + 8 * u;
+                    if (a.q_vec) {
+                        const uint4 y = __ldg(reinterpret_cast<const uint4*>(p));
+                        x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[i][k] = (uint32_t)p[2 * k] | (uint32_t)p[2 * k + 1] << 16;
+                    }
+                }
+            }
+        }
+        if (Q8 && BF) {
+            // The largest finite magnitude of the block to [2^14, 2^15), then float16.
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t l = x[i][k] & 0x7fffu, h = x[i][k] >> 16 & 0x7fffu;
+                    top = max(top, max(l < 0x7f80u ? l : 0u, h < 0x7f80u ? h : 0u));
+                }
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (lane == 0) sTop[warp] = top;
+            named_sync(1, kSoftThreads);
+#pragma unroll
+            for (int k = 0; k < kSoftWarps; ++k) top = max(top, sTop[k]);
+            // times 2^(14 + 127 - exponent), in two factors that float32 holds
+            const int up = 14 + 127 - (int)(top >> 7);
+            const float f0 = two_to(up / 2), f1 = two_to(up - up / 2);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x[i][k] = pack16<false>(__uint_as_float(x[i][k] << 16) * f0 * f1,
+                                            __uint_as_float(x[i][k] & 0xffff0000u) * f0 * f1);
+        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int r = threadIdx.x / kPieces + i * kStep;
+            sts16(smem_u32(smem) + M::q + (r >> 7) * C::kQBytes + (u >> 3) * CHUNK_BYTES +
+                      swz_offset(r & 127, (u & 7) * 8),
+                  x[i][0], x[i][1], x[i][2], x[i][3]);
+        }
+        fence_proxy_async_smem();
+    } else if (warp == kMma0) {
+        if (lane < 16) {
+            mbar_init(&bar.ready[lane >> 3][lane & 7], kFitWarps / 2);
+            mbar_init(&bar.empty[lane >> 3][lane & 7], !KEYS && two ? 2 : 1);
+            mbar_init(&bar.free_raw[lane >> 3][lane & 7], kFitWarps / 2);
+        } else if (lane >= 30) {
+            const int t = lane - 30;
+            mbar_init(&bar.sfull[t], 1);
+            const int warps = max(1, warps_of(t));
+            mbar_init(&bar.sfree[t], warps);
+            mbar_init(&bar.pfull[t][0], warps);
+            mbar_init(&bar.pfull[t][1], warps);
+            mbar_init(&bar.pfree[t][0], 1);
+            mbar_init(&bar.pfree[t][1], 1);
+            mbar_init(&bar.drain[t], 1);
+        }
+        fence_mbar_init();
+    } else if (warp == kMma0 + 1) {
+        tmem_alloc(&bar.tmem, 512);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem;
+
+    if (warp == kCopy) {
+        copy_tiles<HD, HELD, KEYS>(P, w, smem, bar, asked, nt, entry, entry2, copied, bits);
+        // every copy lands before the block can exit, also where a wait above ran out
+        for (int x = 0; x < min(asked, kSlots); ++x) {
+            const uint32_t phase = (asked - 1 - x) / kSlots & 1;       // of the slot's last copy
+            for (int kvs = 0; kvs < 2; ++kvs) warp_wait(&bar.full[kvs][x], phase, a.err, ERR_TIMEOUT_PRODUCER);
+        }
+    } else if (warp >= kFit0) {
+        if (Q8 && BF) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < kSoftWarps; ++k) top = max(top, sTop[k]);
+            const int down = (int)(top >> 7) - 14 - 127;
+            mul = mul * two_to(down / 2) * two_to(down - down / 2);
+        }
+        const int tid = (threadIdx.x - 32 * kFit0) & (kFitters - 1);
+        if (warp < kFit0 + kFitWarps / 2)
+            fit_tiles<HD, HELD, BF, KEYS, 0>(P, w, smem, bar, tid, mul);
+        else
+            fit_tiles<HD, HELD, BF, KEYS, 1>(P, w, smem, bar, tid, mul);
+    } else if (warp >= kMma0) {
+        const int t = warp - kMma0;
+        const int n_mine = KEYS ? (nt + 1 - t) / 2 : nt;
+        if (n_mine > 0 && (KEYS || t == 0 || two) && elect_one()) {
+            constexpr int kBy = KEYS ? 2 : 1;
+            const uint32_t idS = idesc_16(MB, kKeys, false), idO = idesc_16(MB, dsteps * 16, true);
+            constexpr uint64_t kSlotU = C::kSlotBytes >> 4;    // descriptors count 16 bytes
+            const uint64_t dQ = sdesc_sw128(smem_u32(smem + M::q)) + (KEYS ? 0 : t) * (C::kQBytes >> 4);
+            const uint64_t dK = sdesc_sw128(smem_u32(smem + M::ring));
+            const uint64_t dV = sdesc_tokens(smem_u32(smem + M::ring) + NR * C::kSlotBytes, C::kChunkBytes);
+            const uint32_t cS = tmem + C::S(t), cP = tmem + C::P(t), cO = tmem + C::O(t);
+            uint64_t* const k_in = Q8 ? bar.ready[0] : bar.full[0];
+            Ring rk, rv;
+            if (KEYS) rk.step(t, NR), rv.step(t, NR);
+            bool ok = true;
+            for (int j = -1; j < n_mine && ok; ++j) {
+                if (j + 1 < n_mine) {
+                    if (!(ok = mma_wait(a.err, k_in + rk.slot, rk.phase) &&
+                               (j < 0 || mma_wait(a.err, &bar.sfree[t], j & 1))))
+                        break;
+                    mma_over_d<4, C::kChunkBytes>(cS, dQ, dK + rk.slot * kSlotU, idS, (dsteps + 3) / 4);
+                    mma_commit(&bar.sfull[t]);
+                    mma_commit(&bar.empty[0][rk.slot]);
+                    rk.step(kBy, NR);
+                }
+                if (j < 0) continue;
+                const int buf = j & 1, tile = KEYS ? 2 * j + t : j;
+                const bool looked = Q8 || tile >= mixed_from;
+                if (!(ok = mma_wait(a.err, looked ? &bar.ready[1][rv.slot] : &bar.full[1][rv.slot],
+                                    Q8 || !looked ? rv.phase : (tile - mixed_from) / NR & 1) &&
+                           mma_wait(a.err, &bar.pfull[t][buf], (j >> 1) & 1)))
+                    break;
+                mma_over_tokens<kKeys>(cO, cP + buf * (kKeys / 2), dV + rv.slot * kSlotU, idO, j > 0, 32);
+                mma_commit(&bar.pfree[t][buf]);
+                mma_commit(&bar.empty[1][rv.slot]);
+                rv.step(kBy, NR);
+            }
+            mma_commit(&bar.drain[t]);
+            mbar_wait(&bar.drain[t], 0, a.err, ERR_TIMEOUT_MMA);
+        }
+    } else {
+        const int t = warp >> 2, quarter = warp & 3;
+        const uint32_t lofs = (uint32_t)(quarter * 32) << 16;
+        const uint32_t tS = tmem + C::S(t) + lofs, tP = tmem + C::P(t) + lofs, tO = tmem + C::O(t) + lofs;
+        const int n_mine = quarter >= warps_of(t) ? 0 : KEYS ? (nt + 1 - t) / 2 : nt;
+        const int g = lane >> 2, t4 = lane & 3;
+        const int row_t = row0 + (KEYS ? 0 : 128 * t) + quarter * 32;    // the warp's first row
+        const uint64_t mul2 = pk(mul, mul);
+        // of rows g + 8 k of the warp; a lane's part of the sum
+        float ref[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sum[4] = {0.f, 0.f, 0.f, 0.f};
+        bool ok = true;
+        for (int j = 0; j < n_mine; ++j) {
+            const int tile = KEYS ? 2 * j + t : j;
+            const int key0 = (t0 + tile) * kKeys;
+            if (!(ok = warp_wait(&bar.sfull[t], j & 1, a.err, ERR_TIMEOUT_EPILOGUE))) break;
+            tc_fence_after();
+            // v[32 h + 4 i + e]: column 8 i + 2 t4 + (e & 1) of row g + 8 (2 h + (e >> 1))
+            float v[kKeys];
+            tmem_ld16x64(tS, v);
+            tmem_ld16x64(tS + (16u << 16), v + 32);
+            tmem_wait_ld();
+            tmem_reg_fence(v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.sfree[t]);
+            const TileBits& tb = reinterpret_cast<const TileBits*>(smem + M::bits)[tile % C::kBits];
+            const TileScales& ts = reinterpret_cast<const TileScales*>(smem + M::scales)[tile % C::kScales];
+            if (Q8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint64_t kc = *reinterpret_cast<const uint64_t*>(ts.kc + 8 * i + 2 * t4);
+                    const uint64_t lv = *reinterpret_cast<const uint64_t*>(ts.lv + 8 * i + 2 * t4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float* x = v + 32 * (k >> 1) + 4 * i + 2 * (k & 1);
+                        upk(fma2(pk(x[0], x[1]), kc, lv), x[0], x[1]);
+                    }
+                }
+            }
+            const uint2 counted = *reinterpret_cast<const uint2*>(tb.counted);
+            const bool mixed = tile >= mixed_from;
+            if (mixed || (counted.x & counted.y) != 0xffffffffu) {
+                uint32_t bad[2] = {0, 0};
+                if (mixed) {
+                    // the values' check comes with their tile
+                    if (!(ok = warp_wait(&bar.ready[1][tile % NR],
+                                         (Q8 ? tile / NR : (tile - mixed_from) / NR) & 1, a.err,
+                                         ERR_TIMEOUT_EPILOGUE)))
+                        break;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t f = HELD == HELD_I8 ? 0u : tb.poison_value[32 * x + lane];
+                        if (Q8) f |= tb.poison_scale[32 * x + lane];
+                        bad[x] = __ballot_sync(0xffffffffu, f != 0);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t sees[2] = {counted.x, counted.y};
+                    if (mixed) {
+                        const int tok = min(row_t + g + 8 * k, rows - 1) / a.R;
+                        const uint32_t* words = sWords + (tok - tok0) * kTreeWords;
+                        const bool there = words[tok >> 5] >> (tok & 31) & 1u;
+                        sees[0] &= tree_window8(words, there, key0 - ctx);
+                        sees[1] &= tree_window8(words, there, key0 + 32 - ctx);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int at = (8 * i & 31) + 2 * t4 + e;
+                            float& x = v[32 * (k >> 1) + 4 * i + 2 * (k & 1) + e];
+                            if (bad[i >> 2] >> at & 1u) x = __uint_as_float(0x7fc00000u);
+                            if (!(sees[i >> 2] >> at & 1u)) x = -INFINITY;
+                        }
+                }
+            }
+            float alpha[4], base[4];
+            bool moved = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float* x = v + 32 * (k >> 1) + 2 * (k & 1);
+                float m = fmaxf(x[0], x[1]), m1 = fmaxf(x[4], x[5]);
+#pragma unroll
+                for (int i = 2; i < 8; i += 2) {
+                    m = max3(m, x[4 * i], x[4 * i + 1]);
+                    m1 = max3(m1, x[4 * i + 4], x[4 * i + 5]);
+                }
+                m = fmaxf(m, m1);
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                const float top = Q8 ? m : m * mul;
+                alpha[k] = 1.f;
+                if (top > ref[k] + kRefSlack) {
+                    // (up to its first counted key a row's sum and O are zero)
+                    if (ref[k] != -INFINITY) alpha[k] = ex2(ref[k] - top);
+                    sum[k] *= alpha[k];
+                    ref[k] = top;
+                    moved |= alpha[k] != 1.f;
+                }
+                base[k] = kProbShift<MB> - (ref[k] == -INFINITY ? 0.f : ref[k]);
+            }
+            const int buf = j & 1;
+            if (__any_sync(0xffffffffu, moved)) {
+                // O is still once the products of tile j - 1 are done (j > 0 here)
+                if (!(ok = warp_wait(&bar.pfree[t][buf ^ 1], ((j - 1) >> 1) & 1, a.err, ERR_TIMEOUT_EPILOGUE)))
+                    break;
+                tc_fence_after();
+                float f = 1.f;                 // of row `lane`
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float x = __shfl_sync(0xffffffffu, alpha[k], 4 * (lane & 7));
+                    f = lane >> 3 == k ? x : f;
+                }
+#pragma unroll 1
+                for (int c = 0; c < dsteps * 16; c += 16) {
+                    float o[16];
+                    tmem_ld16(tO + c, o);
+                    tmem_wait_ld();
+                    tmem_reg_fence(o);
+                    uint32_t y[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * f);
+                    tmem_st16(tO + c, y);
+                }
+            }
+            uint64_t s[4] = {0, 0, 0, 0};
+            uint32_t p[32];                    // p[16 h + 2 i + (k & 1)]
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t iv = Q8 ? *reinterpret_cast<const uint64_t*>(ts.iv + 8 * i + 2 * t4) : 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float* x = v + 32 * (k >> 1) + 4 * i + 2 * (k & 1);
+                    const uint64_t base2 = pk(base[k], base[k]);
+                    float e0, e1;
+                    upk(Q8 ? add2(pk(x[0], x[1]), base2) : fma2(pk(x[0], x[1]), mul2, base2), e0, e1);
+                    e0 = ex2(e0);
+                    e1 = ex2(e1);
+                    s[k] = Q8 ? fma2(pk(e0, e1), iv, s[k]) : add2(s[k], pk(e0, e1));
+                    p[16 * (k >> 1) + 2 * i + (k & 1)] = pack16<MB>(e0, e1);
+                }
+            }
+            // this buffer's last P, of tile j - 2, was read when S of this tile was done
+            tmem_st16x32(tP + buf * (kKeys / 2), p);
+            tmem_st16x32(tP + buf * (kKeys / 2) + (16u << 16), p + 16);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.pfull[t][buf]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float f0, f1;
+                upk(s[k], f0, f1);
+                sum[k] += f0 + f1;
+            }
+        }
+        if (n_mine > 0 && ok) {
+            const int j = n_mine - 1;
+            ok = warp_wait(&bar.pfree[t][j & 1], (j >> 1) & 1, a.err, ERR_TIMEOUT_EPILOGUE);
+        }
+        tc_fence_after();
+        // from here on a row to a thread
+        float total = 0.f, top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
+            sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
+            const float x = __shfl_sync(0xffffffffu, sum[k], 4 * (lane & 7));
+            const float y = __shfl_sync(0xffffffffu, ref[k], 4 * (lane & 7));
+            if (lane >> 3 == k) {
+                total = x;
+                top = y;
+            }
+        }
+        const int r = quarter * 32 + lane;                 // of the stream's tile
+        const int all = min(row_t + lane, rows - 1);
+        const bool live = row_t + lane < rows;
+        const int tok = all / a.R, head = kh * a.R + all - tok * a.R;
+        const bool there = sWords[(tok - tok0) * kTreeWords + (tok >> 5)] >> (tok & 31) & 1u;
+        // KEYS: both streams' sums of the row, each stream then half of its columns
+        float f[2] = {1.f, 0.f};
+        int c0 = 0, c1 = dsteps * 16;
+        if (KEYS) {
+            float* join = reinterpret_cast<float*>(smem + M::join);
+            join[t * 128 + r] = top;
+            join[256 + t * 128 + r] = total;
+            tc_fence_before();
+            named_sync(1, kSoftThreads);
+            tc_fence_after();
+            top = fmaxf(join[r], join[128 + r]);
+            const float base = top == -INFINITY ? 0.f : top;
+            total = 0.f;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                f[x] = ex2(join[128 * x + r] - base);
+                total = fmaf(f[x], join[256 + 128 * x + r], total);
+            }
+            c0 = t ? (dsteps + 1) / 2 * 16 : 0;
+            c1 = t ? dsteps * 16 : (dsteps + 1) / 2 * 16;
+        }
+        const bool none = total == 0.f || !there;
+        const float inv = none ? 0.f : 1.f / total;
+        const int64_t row = ((int64_t)b * a.H + head) * a.n + tok;
+        if (live && (!KEYS || t == 0)) {
+            const float lse2 = none ? -INFINITY : top - kProbShift<MB> + lg2(total);
+            if (P.splits > 1)
+                P.part.lse2[split * P.part.rows + row] = lse2;
+            else
+                a.lse[row] = lse2 * (float)kLn2;
+        }
+        // Each thread writes 16 elements of its row at a time.
+        T* out = static_cast<T*>(a.o.p) + b * a.o.sb + tok * a.o.st + (int64_t)head * a.o.sh;
+        float* part = P.splits > 1 ? P.part.out + (split * P.part.rows + row) * a.d : nullptr;
+        const uint32_t o_at[2] = {tmem + C::O(KEYS ? 0 : t) + lofs, tmem + C::O(1) + lofs};
+        const int streams = KEYS ? (nt > 1 ? 2 : nt) : nt > 0;
+        const bool any = quarter < warps_of(t);
+#pragma unroll 1
+        for (int c = c0; c < c1 && any; c += 16) {
+            __syncwarp();
+            float o[16], y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = y[e] = 0.f;
+            if (streams > 0) tmem_ld16(o_at[0] + c, o);
+            if (KEYS && streams > 1) tmem_ld16(o_at[1] + c, y);
+            tmem_wait_ld();
+            tmem_reg_fence(o);
+            tmem_reg_fence(y);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                o[e] = KEYS ? (f[0] == 0.f ? 0.f : f[0] * o[e]) + (f[1] == 0.f ? 0.f : f[1] * y[e]) : o[e];
+                o[e] = none ? 0.f : o[e] * inv;
+            }
+            if (!live || !ok) {
+                // nothing to write
+            } else if (part) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    if (c + e < a.d)
+                        *reinterpret_cast<float4*>(part + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            } else if (P.o_vec) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 8)
+                    if (c + e < a.d)
+                        *reinterpret_cast<uint4*>(out + c + e) =
+                            make_uint4(pack16<BF>(o[e], o[e + 1]), pack16<BF>(o[e + 2], o[e + 3]),
+                                       pack16<BF>(o[e + 4], o[e + 5]), pack16<BF>(o[e + 6], o[e + 7]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (c + e < a.d) out[c + e] = from_f<T>(o[e]);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMma0 + 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int HD, int HELD, bool BF, bool KEYS>
+cudaError_t launch(const TcArgs& p, cudaStream_t s) {
+    constexpr size_t bytes = 1024 + Smem<HD, HELD, KEYS>::bytes;
+    static std::atomic<uint64_t> ready{0};    // devices whose shared-memory limit is raised
+    if (cudaError_t e = raise_smem(k_tree_tc<HD, HELD, BF, KEYS>, bytes, ready); e != cudaSuccess) return e;
+    const unsigned blocks = (unsigned)((int64_t)p.a.c.B * p.a.c.G * p.groups * p.splits);
+    k_tree_tc<HD, HELD, BF, KEYS><<<blocks, kTcThreads, bytes, s>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+template <int HD, int HELD>
+cudaError_t launch_held(const TcArgs& p, cudaStream_t s) {
+    if (p.keys) return p.a.bf16 ? launch<HD, HELD, true, true>(p, s) : launch<HD, HELD, false, true>(p, s);
+    return p.a.bf16 ? launch<HD, HELD, true, false>(p, s) : launch<HD, HELD, false, false>(p, s);
+}
+template <int HD>
+cudaError_t launch_width(const TcArgs& p, cudaStream_t s) {
+    if (p.a.c.held == HELD_16) return launch_held<HD, HELD_16>(p, s);
+    return p.a.c.held == HELD_E4M3 ? launch_held<HD, HELD_E4M3>(p, s) : launch_held<HD, HELD_I8>(p, s);
+}
+
+}  // namespace
+
+bool tc_copies(const Cache& c) {
+    constexpr int64_t kFar = int64_t(1) << 39;
+    if (c.pages == 0) return false;
+    for (const kv::Pool* w : {&c.k, &c.v}) {
+        const auto step = [&](int64_t size, int64_t s) { return size <= 1 || (s > 0 && s % 16 == 0 && s < kFar); };
+        if (reinterpret_cast<uintptr_t>(w->p) % 16 || !step(2, w->token) || !step(c.G, w->head) ||
+            !step(c.pages, w->page))
+            return false;
+        if (c.held != HELD_16 && (reinterpret_cast<uintptr_t>(w->scale) % 16 || (c.G > 1 && w->s_head % 4) ||
+                                  (c.pages > 1 && w->s_page % 4)))
+            return false;
+    }
+    return true;
+}
+
+fs_status tc_maps(TcArgs& p, bool bf16) {
+    const Cache& c = p.a.c;
+    const bool bytes = c.held != HELD_16;
+    const uint64_t row = (uint64_t)(c.d * (bytes ? 1 : 2) + 15) / 16 * 16;
+    const uint64_t dims[4] = {(uint64_t)c.d, uint64_t(1) << c.log_page, (uint64_t)c.G, c.pages};
+    const uint32_t box[4] = {bytes ? (c.d <= 64 ? 64u : 128u) : 64u, (uint32_t)std::min(kKeys, 1 << c.log_page),
+                             1, 1};
+    for (int x = 0; x < 2; ++x) {
+        const kv::Pool& w = x ? c.v : c.k;
+        const uint64_t strides[3] = {(uint64_t)w.token, c.G > 1 ? (uint64_t)w.head : row,
+                                     c.pages > 1 ? (uint64_t)w.page : row};
+        FS_TRY(bytes ? make_tmap_4d_bytes(x ? &p.v : &p.k, w.p, dims, strides, box)
+                     : make_tmap_4d(x ? &p.v : &p.k, w.p, dims, strides, box, bf16));
+    }
+    return FS_OK;
+}
+
+cudaError_t launch_tc(const TcArgs& p, cudaStream_t s) {
+    return p.a.d <= 64 ? launch_width<64>(p, s) : launch_width<128>(p, s);
+}
+
+}  // namespace tree
+}  // namespace fs

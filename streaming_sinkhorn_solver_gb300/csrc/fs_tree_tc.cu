@@ -36,10 +36,12 @@ constexpr int kSoftWarps = 8;              // 4 per stream
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kMma0 = kSoftWarps, kFit0 = kSoftWarps + 2, kFitWarps = 4;   // 2 for keys, 2 for values
 constexpr int kCopy = kFit0 + kFitWarps;
-constexpr int kTcThreads = 32 * (kCopy + 1);
+constexpr int kTcThreads = 32 * (kCopy + 2);   // one copies keys, one values
 constexpr int kFitters = 32 * kFitWarps / 2;   // threads that fit the keys of a tile, and its values
 constexpr int kKeys = kTcKeys;
 constexpr float kRefSlack = 8.f;
+// tiles that the tree's keys may lie in
+constexpr int kMixed = (kv::kMaxTree + kKeys - 2) / kKeys + 1;
 
 template <int HD, int HELD, bool KEYS>
 struct Tc {
@@ -50,8 +52,14 @@ struct Tc {
     static constexpr int kQBytes = kChunks * CHUNK_BYTES;
     static constexpr int kQTiles = KEYS ? 1 : 2;
     static constexpr int kRows = 128 * kQTiles;
-    static constexpr int kRing = Q8 ? (HD == 64 ? 4 : 3) : (HD == 64 ? 8 : 4);   // tiles of each
-    static constexpr int kRaw = !Q8 ? 0 : HD == 64 ? 8 : KEYS ? 4 : 3;           // as they land
+    static constexpr int kRing = Q8 ? (HD == 64 ? 4 : 3) : HD == 64 ? 8 : 4;     // tiles of each
+    // Alternating streams that wait for the copies themselves (16 bits): a slot's tiles are all of
+    // one stream, which waits for them in their order.  (Copies land in any: with 5 slots a
+    // stream could find a slot's barrier still before the other stream's tile, take it for past
+    // its own, and have the slot asked for again with a copy under way, a fault.  Widened
+    // tiles are handed on in order.)
+    static_assert(!KEYS || Q8 || kRing % 2 == 0, "slots of one stream");
+    static constexpr int kRaw = !Q8 ? 0 : HD == 64 ? 8 : KEYS ? 5 : 3;           // as they land
     static constexpr int kRawBytes = kKeys * HD;
     // Descriptions of tiles are kept while the softmax may read them: it is behind the tile
     // that a slot was last used for by up to 3 (alternating streams: 5), and 8-bit tiles are
@@ -74,7 +82,10 @@ struct TileScales {
 };
 struct TcBars {
     uint64_t full[2][8], free_raw[2][8];     // copies landed; 8 bits: the ring they land in
-    uint64_t ready[2][8], empty[2][8];       // operand tiles (16 bits: values that were looked through)
+    uint64_t ready[2][8], empty[2][8];       // 8 bits: widened tiles; operand tiles done with
+    // 16 bits: values of the tiles with keys of the tree (the block's last), each of which has
+    // barriers of its own: landed, and looked through
+    uint64_t last[kMixed], looked[kMixed];
     uint64_t sfull[2], sfree[2], pfull[2][2], pfree[2][2], drain[2];
     uint32_t tmem, pad;
 };
@@ -164,16 +175,17 @@ struct Share {
     __device__ __forceinline__ int mixed_from() const { return min(max(ctx / kKeys - tile0, 0), nt); }
 };
 
-// The copying warp.
-template <int HD, int HELD, bool KEYS>
-__device__ __forceinline__ void copy_tiles(const TcArgs& P, const Share& w, uint8_t* smem, TcBars& bar, int& asked,
-                                           int to, int& entry, int& entry2, Ring& r, int& bits) {
+// The copying warps, of keys (KV = 0, with what describes a tile) and values (1): they and the
+// rings they fill are apart, as keys leave theirs two or three tiles before the values do.
+template <int HD, int HELD, bool KEYS, int KV>
+__device__ __forceinline__ void copy_tiles(const TcArgs& P, const Share& w, uint8_t* smem, TcBars& bar) {
     using C = Tc<HD, HELD, KEYS>;
     using M = Smem<HD, HELD, KEYS>;
     constexpr int kSlots = C::Q8 ? C::kRaw : C::kRing;
     const Args& a = P.a;
     const int lane = threadIdx.x & 31;
     const int rows = min(kKeys, 1 << a.c.log_page);            // of a copy
+    const CUtensorMap* const map = KV ? &P.v : &P.k;
     const auto load_entry = [&](int j) {
         // of the tile's keys 8 (lane & 7) on
         const int i = (w.key_of(j) + 8 * (lane & 7)) >> a.c.log_page;
@@ -182,79 +194,76 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& P, const Share& w, uint
             asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(a.c.table + w.b * a.c.table_stride + i));
         return x;
     };
-    if (asked == 0) {
-        entry = load_entry(0);
-        entry2 = load_entry(1);
-    }
+    int entry = load_entry(0), entry2 = load_entry(1), bits = 0, asked = 0;
+    const int mixed_from = w.mixed_from();
+    Ring r;
 #pragma unroll 1
-    for (; asked < to; ++asked) {
-        const int j = asked;
-        const int key0 = w.key_of(j), key = key0 + 8 * (lane & 7);
+    for (; asked < w.nt; ++asked) {
+        const int key0 = w.key_of(asked), key = key0 + 8 * (lane & 7);
         const bool on = (unsigned)entry < a.c.pages && key < w.end;
         const int page = on ? entry : (int)a.c.pages;          // (one behind the last: zeros)
         entry = entry2;
-        entry2 = load_entry(j + 2);
-        if (j >= kSlots) {
-            uint64_t* const gone = C::Q8 ? &bar.free_raw[0][0] : &bar.empty[0][0];
-            if (!warp_wait(gone + r.slot, r.phase ^ 1u, a.err, ERR_TIMEOUT_PRODUCER) ||
-                !warp_wait(gone + 8 + r.slot, r.phase ^ 1u, a.err, ERR_TIMEOUT_PRODUCER))
-                return;
+        entry2 = load_entry(asked + 2);
+        // the other warps' barriers are not needed before the ring is full
+        if (asked == min(w.nt, kSlots)) {
+            __syncthreads();
         }
-        // keys that count, 8 to a lane
-        const int left = w.end - key;
-        const uint32_t byte = !on ? 0u : left >= 8 ? 255u : (1u << left) - 1u;
-        const uint32_t lo = __reduce_or_sync(0xffffffffu, lane < 4 ? byte << (8 * lane) : 0u);
-        const uint32_t hi = __reduce_or_sync(0xffffffffu, lane >= 4 && lane < 8 ? byte << (8 * (lane - 4)) : 0u);
+        if (asked >= kSlots &&
+            !warp_wait((C::Q8 ? bar.free_raw[KV] : bar.empty[KV]) + r.slot, r.phase ^ 1u, a.err,
+                       ERR_TIMEOUT_PRODUCER))
+            break;
         const uint32_t pages = __ballot_sync(0xffffffffu, on) & 255u;
-        if (lane == 0)
-            *reinterpret_cast<uint2*>(reinterpret_cast<TileBits*>(smem + M::bits)[bits].counted) = make_uint2(lo, hi);
-        __syncwarp();
-        if (C::Q8) {
+        uint64_t* const full = !C::Q8 && KV == 1 && asked >= mixed_from ? &bar.last[asked - mixed_from]
+                                                                       : &bar.full[KV][r.slot];
+        uint32_t bytes = C::Q8 ? C::kRawBytes : C::kSlotBytes;
+        if (KV == 0) {
+            // keys that count, 8 to a lane
+            const int left = w.end - key;
+            const uint32_t byte = !on ? 0u : left >= 8 ? 255u : (1u << left) - 1u;
+            const uint32_t lo = __reduce_or_sync(0xffffffffu, lane < 4 ? byte << (8 * lane) : 0u);
+            const uint32_t hi = __reduce_or_sync(0xffffffffu, lane >= 4 && lane < 8 ? byte << (8 * (lane - 4)) : 0u);
+            if (lane == 0)
+                *reinterpret_cast<uint2*>(reinterpret_cast<TileBits*>(smem + M::bits)[bits].counted) =
+                    make_uint2(lo, hi);
             // scales, only where there is a page
-            int copies = 0;
-            for (int c = 0; c < kKeys; c += rows) copies += pages >> (c >> 3) & 1;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&bar.full[0][r.slot], C::kRawBytes + 2 * 4 * rows * copies);
-                mbar_arrive_expect_tx(&bar.full[1][r.slot], C::kRawBytes);
-            }
-        } else if (elect_one()) {
-            mbar_arrive_expect_tx(&bar.full[0][r.slot], C::kSlotBytes);
-            mbar_arrive_expect_tx(&bar.full[1][r.slot], C::kSlotBytes);
+            if (C::Q8)
+                for (int c = 0; c < kKeys; c += rows) bytes += (pages >> (c >> 3) & 1) * 2 * 4 * rows;
+            if (++bits == C::kBits) bits = 0;
         }
+        __syncwarp();
+        if (elect_one()) mbar_arrive_expect_tx(full, bytes);
         __syncwarp();
         for (int c = 0; c < kKeys; c += rows) {
             const int pg = __shfl_sync(0xffffffffu, page, c >> 3);
             const int slot = a.c.slot_of(key0 + c);
             if (elect_one()) {
                 if (C::Q8) {
-                    uint8_t* k = smem + M::raw + r.slot * C::kRawBytes + c * HD;
-                    tma_load(k, &P.k, 0, slot, w.kh, pg, &bar.full[0][r.slot]);
-                    tma_load(k + C::kRaw * C::kRawBytes, &P.v, 0, slot, w.kh, pg,
-                             &bar.full[1][r.slot]);
-                    if (pages >> (c >> 3) & 1) {
+                    tma_load(smem + M::raw + (KV * C::kRaw + r.slot) * C::kRawBytes + c * HD, map, 0, slot, w.kh,
+                             pg, full);
+                    if (KV == 0 && (pages >> (c >> 3) & 1)) {
                         float* s = reinterpret_cast<float*>(smem + M::raw_scale) + r.slot * 2 * kKeys + c;
                         const kv::Pool &pk = a.c.k, &pv = a.c.v;
-                        bulk_g2s(s, pk.scale + pg * pk.s_page + w.kh * pk.s_head + slot, 4 * rows,
-                                 &bar.full[0][r.slot]);
-                        bulk_g2s(s + kKeys, pv.scale + pg * pv.s_page + w.kh * pv.s_head + slot, 4 * rows,
-                                 &bar.full[0][r.slot]);
+                        bulk_g2s(s, pk.scale + pg * pk.s_page + w.kh * pk.s_head + slot, 4 * rows, full);
+                        bulk_g2s(s + kKeys, pv.scale + pg * pv.s_page + w.kh * pv.s_head + slot, 4 * rows, full);
                     }
                 } else {
-                    uint8_t* k = smem + M::ring + r.slot * C::kSlotBytes + c * 128;
 #pragma unroll
-                    for (int x = 0; x < C::kChunks; ++x) {
-                        tma_load(k + x * C::kChunkBytes, &P.k, 64 * x, slot, w.kh, pg,
-                                 &bar.full[0][r.slot]);
-                        tma_load(k + C::kRing * C::kSlotBytes + x * C::kChunkBytes, &P.v, 64 * x, slot,
-                                 w.kh, pg, &bar.full[1][r.slot]);
-                    }
+                    for (int x = 0; x < C::kChunks; ++x)
+                        tma_load(smem + M::ring + (KV * C::kRing + r.slot) * C::kSlotBytes + x * C::kChunkBytes +
+                                     c * 128,
+                                 map, 64 * x, slot, w.kh, pg, full);
                 }
             }
             __syncwarp();
         }
         r.step(1, kSlots);
-        if (++bits == C::kBits) bits = 0;
     }
+    if (w.nt <= kSlots) __syncthreads();
+    // every copy lands before the block can exit, also where a wait above ran out
+    const int plain = !C::Q8 && KV == 1 ? min(asked, mixed_from) : asked;
+    for (int x = 0; x < min(plain, kSlots); ++x)
+        warp_wait(&bar.full[KV][x], (plain - 1 - x) / kSlots & 1, a.err, ERR_TIMEOUT_PRODUCER);   // the slot's last
+    for (int x = plain; x < asked; ++x) warp_wait(&bar.last[x - mixed_from], 0, a.err, ERR_TIMEOUT_PRODUCER);
 }
 
 // The fitting warps of keys (KV = 0) or values (1).  8 bits: every tile is widened into an
@@ -274,10 +283,7 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
     const int u = tid % kPer, row0 = tid / kPer;
     const int mixed_from = w.mixed_from(), j0 = Q8 ? 0 : mixed_from;
     Ring from, to;
-    if (!Q8) {
-        to.slot = j0 % C::kRing;
-        to.phase = j0 / C::kRing & 1;
-    }
+    to.slot = j0 % C::kRing;
     int scales = 0, bits = j0 % C::kBits;
     // pieces of a row are in neighbouring lanes
     const auto look = [&](const uint4& x, int key0, int row, uint8_t* flags) {
@@ -347,7 +353,7 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
                 tb.poison_scale[tid] = bad;
             }
         } else {
-            if (!warp_wait(&bar.full[1][to.slot], to.phase, a.err, ERR_TIMEOUT_PRODUCER)) return;
+            if (!warp_wait(&bar.last[j - mixed_from], 0, a.err, ERR_TIMEOUT_PRODUCER)) return;
 #pragma unroll 4
             for (int i = 0; i < kMine; ++i) {
                 const int row = row0 + i * kStep;
@@ -358,7 +364,7 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.ready[KV][to.slot]);
+        if (lane == 0) mbar_arrive(Q8 ? &bar.ready[KV][to.slot] : &bar.looked[j - mixed_from]);
         if (Q8) from.step(1, Q8 ? C::kRaw : 1);
         to.step(1, C::kRing);
         if (++scales == C::kScales) scales = 0;
@@ -408,16 +414,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
     // warps of a stream's softmax that have rows (the others leave their rows of P as they are)
     const auto warps_of = [&](int t) { return min(4, (rows - row0 - (KEYS ? 0 : 128 * t) + 31) >> 5); };
     float mul = a.scale2;
-    constexpr int kSlots = Q8 ? C::kRaw : NR;          // that copies land in
-    int asked = 0, entry = -1, entry2 = -1, bits = 0;
-    Ring copied;
 
-    if (warp == kCopy) {
-        // its barriers are its own until the block meets: it starts its copies before that
-        if (lane < 16) mbar_init(&bar.full[lane >> 3][lane & 7], 1);
+    if (warp >= kCopy) {
+        // Their barriers are their own until the block meets: they start their copies before
+        // that, and meet the block once their ring is full.
+        if (lane < 8) mbar_init(&bar.full[warp - kCopy][lane], 1);
+        if (warp > kCopy && lane >= 8 && lane < 8 + kMixed) mbar_init(&bar.last[lane - 8], 1);
         fence_mbar_init();
         __syncwarp();
-        copy_tiles<HD, HELD, KEYS>(P, w, smem, bar, asked, min(nt, kSlots), entry, entry2, copied, bits);
+        if (warp == kCopy)
+            copy_tiles<HD, HELD, KEYS, 0>(P, w, smem, bar);
+        else
+            copy_tiles<HD, HELD, KEYS, 1>(P, w, smem, bar);
+        __syncthreads();
+        return;
     } else if (warp < kSoftWarps) {
         // what the block's tokens see of the tree, then their queries as operand tiles
         if (a.parents) {
@@ -493,6 +503,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
             mbar_init(&bar.ready[lane >> 3][lane & 7], kFitWarps / 2);
             mbar_init(&bar.empty[lane >> 3][lane & 7], !KEYS && two ? 2 : 1);
             mbar_init(&bar.free_raw[lane >> 3][lane & 7], kFitWarps / 2);
+        } else if (lane < 16 + kMixed) {
+            mbar_init(&bar.looked[lane - 16], kFitWarps / 2);
         } else if (lane >= 30) {
             const int t = lane - 30;
             mbar_init(&bar.sfull[t], 1);
@@ -513,14 +525,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
 
-    if (warp == kCopy) {
-        copy_tiles<HD, HELD, KEYS>(P, w, smem, bar, asked, nt, entry, entry2, copied, bits);
-        // every copy lands before the block can exit, also where a wait above ran out
-        for (int x = 0; x < min(asked, kSlots); ++x) {
-            const uint32_t phase = (asked - 1 - x) / kSlots & 1;       // of the slot's last copy
-            for (int kvs = 0; kvs < 2; ++kvs) warp_wait(&bar.full[kvs][x], phase, a.err, ERR_TIMEOUT_PRODUCER);
-        }
-    } else if (warp >= kFit0) {
+    if (warp >= kFit0) {
         if (Q8 && BF) {
             uint32_t top = 0;
 #pragma unroll
@@ -560,9 +565,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
                 }
                 if (j < 0) continue;
                 const int buf = j & 1, tile = KEYS ? 2 * j + t : j;
-                const bool looked = Q8 || tile >= mixed_from;
-                if (!(ok = mma_wait(a.err, looked ? &bar.ready[1][rv.slot] : &bar.full[1][rv.slot],
-                                    Q8 || !looked ? rv.phase : (tile - mixed_from) / NR & 1) &&
+                const bool own = !Q8 && tile >= mixed_from;
+                uint64_t* const v_in = Q8 ? &bar.ready[1][rv.slot]
+                                          : own ? &bar.looked[tile - mixed_from] : &bar.full[1][rv.slot];
+                if (!(ok = mma_wait(a.err, v_in, own ? 0 : rv.phase) &&
                            mma_wait(a.err, &bar.pfull[t][buf], (j >> 1) & 1)))
                     break;
                 mma_over_tokens<kKeys>(cO, cP + buf * (kKeys / 2), dV + rv.slot * kSlotU, idO, j > 0, 32);
@@ -593,34 +599,38 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
             float v[kKeys];
             tmem_ld16x64(tS, v);
             tmem_ld16x64(tS + (16u << 16), v + 32);
+            const TileBits& tb = reinterpret_cast<const TileBits*>(smem + M::bits)[tile % C::kBits];
+            const TileScales& ts = reinterpret_cast<const TileScales*>(smem + M::scales)[tile % C::kScales];
+            uint64_t kc[Q8 ? 8 : 1], lv[Q8 ? 8 : 1];
+            if (Q8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    kc[Q8 ? i : 0] = *reinterpret_cast<const uint64_t*>(ts.kc + 8 * i + 2 * t4);
+                    lv[Q8 ? i : 0] = *reinterpret_cast<const uint64_t*>(ts.lv + 8 * i + 2 * t4);
+                }
+            }
+            const uint2 counted = *reinterpret_cast<const uint2*>(tb.counted);
             tmem_wait_ld();
             tmem_reg_fence(v);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.sfree[t]);
-            const TileBits& tb = reinterpret_cast<const TileBits*>(smem + M::bits)[tile % C::kBits];
-            const TileScales& ts = reinterpret_cast<const TileScales*>(smem + M::scales)[tile % C::kScales];
             if (Q8) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint64_t kc = *reinterpret_cast<const uint64_t*>(ts.kc + 8 * i + 2 * t4);
-                    const uint64_t lv = *reinterpret_cast<const uint64_t*>(ts.lv + 8 * i + 2 * t4);
+                for (int i = 0; i < 8; ++i)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         float* x = v + 32 * (k >> 1) + 4 * i + 2 * (k & 1);
-                        upk(fma2(pk(x[0], x[1]), kc, lv), x[0], x[1]);
+                        upk(fma2(pk(x[0], x[1]), kc[Q8 ? i : 0], lv[Q8 ? i : 0]), x[0], x[1]);
                     }
-                }
             }
-            const uint2 counted = *reinterpret_cast<const uint2*>(tb.counted);
             const bool mixed = tile >= mixed_from;
             if (mixed || (counted.x & counted.y) != 0xffffffffu) {
                 uint32_t bad[2] = {0, 0};
                 if (mixed) {
                     // the values' check comes with their tile
-                    if (!(ok = warp_wait(&bar.ready[1][tile % NR],
-                                         (Q8 ? tile / NR : (tile - mixed_from) / NR) & 1, a.err,
-                                         ERR_TIMEOUT_EPILOGUE)))
+                    if (!(ok = warp_wait(Q8 ? &bar.ready[1][tile % NR] : &bar.looked[tile - mixed_from],
+                                         Q8 ? tile / NR & 1 : 0, a.err, ERR_TIMEOUT_EPILOGUE)))
                         break;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
@@ -650,54 +660,62 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
                         }
                 }
             }
-            float alpha[4], base[4];
-            bool moved = false;
+            float m[4];                        // over this lane's keys
+            bool moves = false;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float* x = v + 32 * (k >> 1) + 2 * (k & 1);
-                float m = fmaxf(x[0], x[1]), m1 = fmaxf(x[4], x[5]);
+                float m0 = fmaxf(x[0], x[1]), m1 = fmaxf(x[4], x[5]);
 #pragma unroll
                 for (int i = 2; i < 8; i += 2) {
-                    m = max3(m, x[4 * i], x[4 * i + 1]);
+                    m0 = max3(m0, x[4 * i], x[4 * i + 1]);
                     m1 = max3(m1, x[4 * i + 4], x[4 * i + 5]);
                 }
-                m = fmaxf(m, m1);
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const float top = Q8 ? m : m * mul;
-                alpha[k] = 1.f;
-                if (top > ref[k] + kRefSlack) {
-                    // (up to its first counted key a row's sum and O are zero)
-                    if (ref[k] != -INFINITY) alpha[k] = ex2(ref[k] - top);
-                    sum[k] *= alpha[k];
-                    ref[k] = top;
-                    moved |= alpha[k] != 1.f;
-                }
-                base[k] = kProbShift<MB> - (ref[k] == -INFINITY ? 0.f : ref[k]);
+                m[k] = fmaxf(m0, m1);
+                if (!Q8) m[k] *= mul;
+                moves |= m[k] > ref[k] + kRefSlack;
             }
             const int buf = j & 1;
-            if (__any_sync(0xffffffffu, moved)) {
-                // O is still once the products of tile j - 1 are done (j > 0 here)
-                if (!(ok = warp_wait(&bar.pfree[t][buf ^ 1], ((j - 1) >> 1) & 1, a.err, ERR_TIMEOUT_EPILOGUE)))
-                    break;
-                tc_fence_after();
+            // Rarely: references move, and O and the sums with them.
+            if (__any_sync(0xffffffffu, moves)) {
                 float f = 1.f;                 // of row `lane`
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float x = __shfl_sync(0xffffffffu, alpha[k], 4 * (lane & 7));
+                    float top = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    float alpha = 1.f;
+                    if (top > ref[k] + kRefSlack) {
+                        // (up to its first counted key a row's sum and O are zero)
+                        if (ref[k] != -INFINITY) alpha = ex2(ref[k] - top);
+                        sum[k] *= alpha;
+                        ref[k] = top;
+                    }
+                    const float x = __shfl_sync(0xffffffffu, alpha, 4 * (lane & 7));
                     f = lane >> 3 == k ? x : f;
                 }
+                if (__any_sync(0xffffffffu, f != 1.f)) {
+                    // O is still once the products of tile j - 1 are done (j > 0 here)
+                    if (!(ok = warp_wait(&bar.pfree[t][buf ^ 1], ((j - 1) >> 1) & 1, a.err, ERR_TIMEOUT_EPILOGUE)))
+                        break;
+                    tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < dsteps * 16; c += 16) {
-                    float o[16];
-                    tmem_ld16(tO + c, o);
-                    tmem_wait_ld();
-                    tmem_reg_fence(o);
-                    uint32_t y[16];
+                    for (int c = 0; c < dsteps * 16; c += 16) {
+                        float o[16];
+                        tmem_ld16(tO + c, o);
+                        tmem_wait_ld();
+                        tmem_reg_fence(o);
+                        uint32_t y[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * f);
-                    tmem_st16(tO + c, y);
+                        for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * f);
+                        tmem_st16(tO + c, y);
+                    }
                 }
+            }
+            uint64_t base2[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float base = kProbShift<MB> - (ref[k] == -INFINITY ? 0.f : ref[k]);
+                base2[k] = pk(base, base);
             }
             uint64_t s[4] = {0, 0, 0, 0};
             uint32_t p[32];                    // p[16 h + 2 i + (k & 1)]
@@ -707,9 +725,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float* x = v + 32 * (k >> 1) + 4 * i + 2 * (k & 1);
-                    const uint64_t base2 = pk(base[k], base[k]);
                     float e0, e1;
-                    upk(Q8 ? add2(pk(x[0], x[1]), base2) : fma2(pk(x[0], x[1]), mul2, base2), e0, e1);
+                    upk(Q8 ? add2(pk(x[0], x[1]), base2[k]) : fma2(pk(x[0], x[1]), mul2, base2[k]), e0, e1);
                     e0 = ex2(e0);
                     e1 = ex2(e1);
                     s[k] = Q8 ? fma2(pk(e0, e1), iv, s[k]) : add2(s[k], pk(e0, e1));

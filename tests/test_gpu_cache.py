@@ -423,6 +423,20 @@ def test_long_contexts_are_split_and_joined(held, n):
     assert torch.equal(a, b) and torch.equal(la, lb)
 
 
+@pytest.mark.parametrize("held", [BF, HALF, E4M3, I8])
+@pytest.mark.parametrize("n,R,d", [(9, 4, 128), (9, 4, 64), (20, 8, 128), (20, 8, 64), (1, 2, 128)])
+def test_blocks_of_many_tiles(held, n, R, d):
+    """As many sequences and key heads as the GPU has SMs: every ring of a block goes round
+    several times, with contexts that end anywhere."""
+    G = 4
+    B = torch.cuda.get_device_properties(0).multi_processor_count // G
+    dtype = held if held in (BF, HALF) else BF
+    ctx = [1300 - 19 * b for b in range(B)]
+    s = setting(16, B, n, ctx, R * G, G, d, dtype, held, 32)
+    parents = random_parents(gen(5), 1, n)[0]
+    check(*s, ctx, parents)
+
+
 @pytest.mark.parametrize("n", [1, 32])
 def test_scales_that_differ_widely(n):
     """Values of a key may be 2^30 times those of another: each weighs in by its own."""

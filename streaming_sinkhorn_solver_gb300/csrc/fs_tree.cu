@@ -108,8 +108,7 @@ fs_status tree_entry(const fs_cache* cache, const fs_tree* t, const void* q, voi
         FS_CUDA(few_resident(a, p.row_blocks, &resident));
         splits = choose_few_splits(B * a.c.G * p.groups, a.c.reach(), (int64_t)sms * resident);
     } else {
-        tc.keys = per_head <= 128;
-        tc.groups = (per_head + (tc.keys ? 127 : 255)) / (tc.keys ? 128 : 256);
+        tc.groups = (per_head + 255) / 256;
         tc.o_vec = attn::aligned16(a.o, a.c.B, a.n, a.H);
         splits = choose_tc_splits(B * a.c.G * tc.groups, a.c.reach(), sms);
     }

@@ -86,14 +86,12 @@ cudaError_t launch_few(const FewArgs& p, cudaStream_t s);
 // blocks of it that an SM holds
 cudaError_t few_resident(const Args& a, int row_blocks, int* blocks);
 
-// Many rows, on the tensor cores: `groups` of 128 rows (keys: the keys' tiles alternate
-// between two streams of scores) or of 256 (two tiles of rows).
+// Many rows, on the tensor cores: `groups` of 256 rows, or one of up to 128.
 struct TcArgs {
     CUtensorMap k, v;      // (d, token, head, page)
     Args a;
     Partials part;         // rows of d floats
     int splits, groups;
-    int keys;
     int o_vec;             // the rows of out take 16-byte stores
 };
 constexpr int kTcKeys = 64;            // keys of a tile

@@ -4,7 +4,9 @@
 //   S_t = Q_t K^T (TMEM), P = 2^{x - ref} in 16 bits in TMEM, O_t += P V (TMEM),
 // either two tiles of 128 query rows that share every key tile (ROWS), or, where there are
 // 128 rows or fewer, one tile of rows whose key tiles go to the streams in turn (KEYS), joined at
-// the end; so the softmax of one stream runs beside the products of the other.
+// the end; so the softmax of one stream runs beside the products of the other.  64 rows or
+// fewer (HALF) lie 16 by 16 in the four quarters of the tile: each of its four warps then has
+// some, on a scheduler of its own, and half the work.
 //
 // Pages come by tensor copies, a page (or 64 keys of one) at a time; an entry without a
 // page is copied from beyond the end of the pool, which gives zeros.  Keys and values in 16
@@ -34,37 +36,41 @@ using kv::HELD_I8;
 
 constexpr int kSoftWarps = 8;              // 4 per stream
 constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kMma0 = kSoftWarps, kFit0 = kSoftWarps + 2, kFitWarps = 4;   // 2 for keys, 2 for values
-constexpr int kCopy = kFit0 + kFitWarps;
-constexpr int kTcThreads = 32 * (kCopy + 2);   // one copies keys, one values
-constexpr int kFitters = 32 * kFitWarps / 2;   // threads that fit the keys of a tile, and its values
+constexpr int kMma0 = kSoftWarps, kFit0 = kSoftWarps + 2;
+enum Mode : int { ROWS = 0, KEYS = 1, HALF = 2 };
 constexpr int kKeys = kTcKeys;
 constexpr float kRefSlack = 8.f;
 // tiles that the tree's keys may lie in
 constexpr int kMixed = (kv::kMaxTree + kKeys - 2) / kKeys + 1;
 
-template <int HD, int HELD, bool KEYS>
+template <int HD, int HELD, int MODE>
 struct Tc {
     static constexpr bool Q8 = HELD != HELD_16;
+    static constexpr bool kAlternate = MODE != ROWS;     // key tiles to the streams in turn
+    // Half of the warps fit the keys of a tile, half its values; HALF leaves the registers for more
+    static constexpr int kFitWarps = Q8 && MODE == HALF ? 8 : 4, kFitters = 16 * kFitWarps;
+    static constexpr int kCopy = kFit0 + kFitWarps;      // two warps: one copies keys, one values
+    static constexpr int kThreads = 32 * (kCopy + 2);
+    static constexpr int kQuarter = MODE == HALF ? 16 : 32;     // rows of a softmax warp
     static constexpr int kChunks = HD / 64;
     static constexpr int kChunkBytes = kKeys * 128;               // 64 elements of each key
     static constexpr int kSlotBytes = kChunks * kChunkBytes;      // a tile of keys, or of values
     static constexpr int kQBytes = kChunks * CHUNK_BYTES;
-    static constexpr int kQTiles = KEYS ? 1 : 2;
-    static constexpr int kRows = 128 * kQTiles;
+    static constexpr int kQTiles = kAlternate ? 1 : 2;
+    static constexpr int kRows = 4 * kQuarter * kQTiles;
     static constexpr int kRing = Q8 ? (HD == 64 ? 4 : 3) : HD == 64 ? 8 : 4;     // tiles of each
     // Alternating streams that wait for the copies themselves (16 bits): a slot's tiles are all of
     // one stream, which waits for them in their order.  (Copies land in any: with 5 slots a
     // stream could find a slot's barrier still before the other stream's tile, take it for past
     // its own, and have the slot asked for again with a copy under way, a fault.  Widened
     // tiles are handed on in order.)
-    static_assert(!KEYS || Q8 || kRing % 2 == 0, "slots of one stream");
-    static constexpr int kRaw = !Q8 ? 0 : HD == 64 ? 8 : KEYS ? 5 : 3;           // as they land
+    static_assert(!kAlternate || Q8 || kRing % 2 == 0, "slots of one stream");
+    static constexpr int kRaw = !Q8 ? 0 : HD == 64 ? 8 : kAlternate ? 5 : 3;     // as they land
     static constexpr int kRawBytes = kKeys * HD;
     // Descriptions of tiles are kept while the softmax may read them: it is behind the tile
     // that a slot was last used for by up to 3 (alternating streams: 5), and 8-bit tiles are
     // described when they are asked for, kRaw before that.
-    static constexpr int kScales = kRing + (KEYS ? 5 : 3);
+    static constexpr int kScales = kRing + (kAlternate ? 5 : 3);
     static constexpr int kBits = kScales + kRaw;
     __host__ __device__ static constexpr uint32_t S(int t) { return 256 * t; }
     __host__ __device__ static constexpr uint32_t P(int t) { return S(t) + kKeys; }    // two of 32 columns
@@ -90,9 +96,9 @@ struct TcBars {
     uint32_t tmem, pad;
 };
 
-template <int HD, int HELD, bool KEYS>
+template <int HD, int HELD, int MODE>
 struct Smem {
-    using C = Tc<HD, HELD, KEYS>;
+    using C = Tc<HD, HELD, MODE>;
     static constexpr int q = 0;
     static constexpr int ring = q + C::kQTiles * C::kQBytes;                  // [keys, values][slot]
     static constexpr int raw = ring + 2 * C::kRing * C::kSlotBytes;           // [keys, values][slot][key][HD]
@@ -101,7 +107,7 @@ struct Smem {
     static constexpr int bits = scales + (C::Q8 ? C::kScales * (int)sizeof(TileScales) : 0);
     static constexpr int words = bits + C::kBits * (int)sizeof(TileBits);     // [row's token][kTreeWords]
     static constexpr int join = words + C::kRows * 4 * kTreeWords;            // [ref, sum][stream][row]
-    static constexpr int parents = join + (KEYS ? 4 * 4 * 128 : 0);
+    static constexpr int parents = join + (C::kAlternate ? 4 * 4 * 128 : 0);
     static constexpr int bars = parents + 4 * kv::kMaxTree;
     static constexpr int top = bars + (int)sizeof(TcBars);                    // of the queries, by warps
     static constexpr int bytes = top + 4 * kSoftWarps;
@@ -177,10 +183,10 @@ struct Share {
 
 // The copying warps, of keys (KV = 0, with what describes a tile) and values (1): they and the
 // rings they fill are apart, as keys leave theirs two or three tiles before the values do.
-template <int HD, int HELD, bool KEYS, int KV>
+template <int HD, int HELD, int MODE, int KV>
 __device__ __forceinline__ void copy_tiles(const TcArgs& P, const Share& w, uint8_t* smem, TcBars& bar) {
-    using C = Tc<HD, HELD, KEYS>;
-    using M = Smem<HD, HELD, KEYS>;
+    using C = Tc<HD, HELD, MODE>;
+    using M = Smem<HD, HELD, MODE>;
     constexpr int kSlots = C::Q8 ? C::kRaw : C::kRing;
     const Args& a = P.a;
     const int lane = threadIdx.x & 31;
@@ -268,12 +274,13 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& P, const Share& w, uint
 
 // The fitting warps of keys (KV = 0) or values (1).  8 bits: every tile is widened into an
 // operand tile.  16 bits: of the values, tiles with keys of the tree are looked through.
-template <int HD, int HELD, bool BF, bool KEYS, int KV>
+template <int HD, int HELD, bool BF, int MODE, int KV>
 __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8_t* smem, TcBars& bar, int tid,
                                           float mul) {
-    using C = Tc<HD, HELD, KEYS>;
-    using M = Smem<HD, HELD, KEYS>;
+    using C = Tc<HD, HELD, MODE>;
+    using M = Smem<HD, HELD, MODE>;
     constexpr bool Q8 = C::Q8;
+    constexpr int kFitters = C::kFitters;
     constexpr int kPer = HD / (Q8 ? 16 : 8);            // 16-byte pieces of a row
     constexpr int kMine = kKeys * kPer / kFitters;      // of a thread: rows kStep apart
     constexpr int kStep = kFitters / kPer;
@@ -319,7 +326,8 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
                 }
             }
             float ks = 0.f, vs = 0.f;
-            if (KV == 0) {
+            const bool scaled = KV == 0 && tid < kKeys;
+            if (scaled) {
                 const float* s = reinterpret_cast<const float*>(smem + M::raw_scale) + from.slot * 2 * kKeys + tid;
                 if (tb.counted[tid >> 5] >> (tid & 31) & 1u) {
                     ks = s[0];
@@ -343,7 +351,7 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
                 sts16(at + swz_offset(row, (u & 3) * 16), y[0], y[1], y[2], y[3]);
                 sts16(at + swz_offset(row, (u & 3) * 16 + 8), y[4], y[5], y[6], y[7]);
             }
-            if (KV == 0) {
+            if (scaled) {
                 TileScales& ts = reinterpret_cast<TileScales*>(smem + M::scales)[scales];
                 const bool bad = mixed && key0 + tid >= w.ctx && !(vs < INFINITY);
                 const bool none = vs == 0.f || bad;            // (0: the key does not count)
@@ -372,14 +380,16 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
     }
 }
 
-template <int HD, int HELD, bool BF, bool KEYS>
-__global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant__ TcArgs P) {
-    using C = Tc<HD, HELD, KEYS>;
-    using M = Smem<HD, HELD, KEYS>;
+template <int HD, int HELD, bool BF, int MODE>
+__global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(const __grid_constant__ TcArgs P) {
+    using C = Tc<HD, HELD, MODE>;
+    using M = Smem<HD, HELD, MODE>;
     using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
     constexpr bool Q8 = C::Q8;
     constexpr bool MB = BF && !Q8;             // products in bfloat16
-    constexpr int NR = C::kRing;
+    constexpr bool kAlternate = C::kAlternate;
+    constexpr int NR = C::kRing, kCopy = C::kCopy, kFitWarps = C::kFitWarps, kFitters = C::kFitters;
+    constexpr int kQuarter = C::kQuarter, kLaneRows = kQuarter / 8;     // rows of a lane: 8 apart
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
@@ -408,11 +418,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
     const int mixed_from = w.mixed_from();
     const int rows = a.R * a.n;
     const int row0 = group * C::kRows;                 // the block's first row
-    const bool two = KEYS || row0 + 128 < rows;
+    const bool two = kAlternate || row0 + 128 < rows;
     const int tok0 = row0 / a.R, tok1 = min(rows - 1, row0 + C::kRows - 1) / a.R;
     const int dsteps = (a.d + 15) >> 4;
     // warps of a stream's softmax that have rows (the others leave their rows of P as they are)
-    const auto warps_of = [&](int t) { return min(4, (rows - row0 - (KEYS ? 0 : 128 * t) + 31) >> 5); };
+    const auto warps_of = [&](int t) {
+        return min(4, (rows - row0 - (kAlternate ? 0 : 128 * t) + kQuarter - 1) / kQuarter);
+    };
     float mul = a.scale2;
 
     if (warp >= kCopy) {
@@ -423,9 +435,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
         fence_mbar_init();
         __syncwarp();
         if (warp == kCopy)
-            copy_tiles<HD, HELD, KEYS, 0>(P, w, smem, bar);
+            copy_tiles<HD, HELD, MODE, 0>(P, w, smem, bar);
         else
-            copy_tiles<HD, HELD, KEYS, 1>(P, w, smem, bar);
+            copy_tiles<HD, HELD, MODE, 1>(P, w, smem, bar);
         __syncthreads();
         return;
     } else if (warp < kSoftWarps) {
@@ -492,7 +504,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
         }
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            const int r = threadIdx.x / kPieces + i * kStep;
+            int r = threadIdx.x / kPieces + i * kStep;
+            if (MODE == HALF) r = r / kQuarter * 32 + r % kQuarter;    // (what the other rows hold stays in them)
             sts16(smem_u32(smem) + M::q + (r >> 7) * C::kQBytes + (u >> 3) * CHUNK_BYTES +
                       swz_offset(r & 127, (u & 7) * 8),
                   x[i][0], x[i][1], x[i][2], x[i][3]);
@@ -501,7 +514,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
     } else if (warp == kMma0) {
         if (lane < 16) {
             mbar_init(&bar.ready[lane >> 3][lane & 7], kFitWarps / 2);
-            mbar_init(&bar.empty[lane >> 3][lane & 7], !KEYS && two ? 2 : 1);
+            mbar_init(&bar.empty[lane >> 3][lane & 7], !kAlternate && two ? 2 : 1);
             mbar_init(&bar.free_raw[lane >> 3][lane & 7], kFitWarps / 2);
         } else if (lane < 16 + kMixed) {
             mbar_init(&bar.looked[lane - 16], kFitWarps / 2);
@@ -535,23 +548,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
         }
         const int tid = (threadIdx.x - 32 * kFit0) & (kFitters - 1);
         if (warp < kFit0 + kFitWarps / 2)
-            fit_tiles<HD, HELD, BF, KEYS, 0>(P, w, smem, bar, tid, mul);
+            fit_tiles<HD, HELD, BF, MODE, 0>(P, w, smem, bar, tid, mul);
         else
-            fit_tiles<HD, HELD, BF, KEYS, 1>(P, w, smem, bar, tid, mul);
+            fit_tiles<HD, HELD, BF, MODE, 1>(P, w, smem, bar, tid, mul);
     } else if (warp >= kMma0) {
         const int t = warp - kMma0;
-        const int n_mine = KEYS ? (nt + 1 - t) / 2 : nt;
-        if (n_mine > 0 && (KEYS || t == 0 || two) && elect_one()) {
-            constexpr int kBy = KEYS ? 2 : 1;
+        const int n_mine = kAlternate ? (nt + 1 - t) / 2 : nt;
+        if (n_mine > 0 && (t == 0 || two) && elect_one()) {
+            constexpr int kBy = kAlternate ? 2 : 1;
             const uint32_t idS = idesc_16(MB, kKeys, false), idO = idesc_16(MB, dsteps * 16, true);
             constexpr uint64_t kSlotU = C::kSlotBytes >> 4;    // descriptors count 16 bytes
-            const uint64_t dQ = sdesc_sw128(smem_u32(smem + M::q)) + (KEYS ? 0 : t) * (C::kQBytes >> 4);
+            const uint64_t dQ = sdesc_sw128(smem_u32(smem + M::q)) + (kAlternate ? 0 : t) * (C::kQBytes >> 4);
             const uint64_t dK = sdesc_sw128(smem_u32(smem + M::ring));
             const uint64_t dV = sdesc_tokens(smem_u32(smem + M::ring) + NR * C::kSlotBytes, C::kChunkBytes);
             const uint32_t cS = tmem + C::S(t), cP = tmem + C::P(t), cO = tmem + C::O(t);
             uint64_t* const k_in = Q8 ? bar.ready[0] : bar.full[0];
             Ring rk, rv;
-            if (KEYS) rk.step(t, NR), rv.step(t, NR);
+            if (kAlternate) rk.step(t, NR), rv.step(t, NR);
             bool ok = true;
             for (int j = -1; j < n_mine && ok; ++j) {
                 if (j + 1 < n_mine) {
@@ -564,7 +577,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
                     rk.step(kBy, NR);
                 }
                 if (j < 0) continue;
-                const int buf = j & 1, tile = KEYS ? 2 * j + t : j;
+                const int buf = j & 1, tile = kAlternate ? 2 * j + t : j;
                 const bool own = !Q8 && tile >= mixed_from;
                 uint64_t* const v_in = Q8 ? &bar.ready[1][rv.slot]
                                           : own ? &bar.looked[tile - mixed_from] : &bar.full[1][rv.slot];
@@ -583,22 +596,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
         const int t = warp >> 2, quarter = warp & 3;
         const uint32_t lofs = (uint32_t)(quarter * 32) << 16;
         const uint32_t tS = tmem + C::S(t) + lofs, tP = tmem + C::P(t) + lofs, tO = tmem + C::O(t) + lofs;
-        const int n_mine = quarter >= warps_of(t) ? 0 : KEYS ? (nt + 1 - t) / 2 : nt;
+        const int n_mine = quarter >= warps_of(t) ? 0 : kAlternate ? (nt + 1 - t) / 2 : nt;
         const int g = lane >> 2, t4 = lane & 3;
-        const int row_t = row0 + (KEYS ? 0 : 128 * t) + quarter * 32;    // the warp's first row
+        const int row_t = row0 + (kAlternate ? 0 : 128 * t) + quarter * kQuarter;    // the warp's first row
         const uint64_t mul2 = pk(mul, mul);
         // of rows g + 8 k of the warp; a lane's part of the sum
-        float ref[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float ref[kLaneRows], sum[kLaneRows];
+#pragma unroll
+        for (int k = 0; k < kLaneRows; ++k) {
+            ref[k] = -INFINITY;
+            sum[k] = 0.f;
+        }
         bool ok = true;
         for (int j = 0; j < n_mine; ++j) {
-            const int tile = KEYS ? 2 * j + t : j;
+            const int tile = kAlternate ? 2 * j + t : j;
             const int key0 = (t0 + tile) * kKeys;
             if (!(ok = warp_wait(&bar.sfull[t], j & 1, a.err, ERR_TIMEOUT_EPILOGUE))) break;
             tc_fence_after();
             // v[32 h + 4 i + e]: column 8 i + 2 t4 + (e & 1) of row g + 8 (2 h + (e >> 1))
-            float v[kKeys];
+            float v[16 * kLaneRows];
             tmem_ld16x64(tS, v);
-            tmem_ld16x64(tS + (16u << 16), v + 32);
+            if (kLaneRows > 2) tmem_ld16x64(tS + (16u << 16), v + (kLaneRows > 2 ? 32 : 0));
             const TileBits& tb = reinterpret_cast<const TileBits*>(smem + M::bits)[tile % C::kBits];
             const TileScales& ts = reinterpret_cast<const TileScales*>(smem + M::scales)[tile % C::kScales];
             uint64_t kc[Q8 ? 8 : 1], lv[Q8 ? 8 : 1];
@@ -619,7 +637,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < kLaneRows; ++k) {
                         float* x = v + 32 * (k >> 1) + 4 * i + 2 * (k & 1);
                         upk(fma2(pk(x[0], x[1]), kc[Q8 ? i : 0], lv[Q8 ? i : 0]), x[0], x[1]);
                     }
@@ -640,7 +658,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kLaneRows; ++k) {
                     uint32_t sees[2] = {counted.x, counted.y};
                     if (mixed) {
                         const int tok = min(row_t + g + 8 * k, rows - 1) / a.R;
@@ -660,10 +678,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
                         }
                 }
             }
-            float m[4];                        // over this lane's keys
+            float m[kLaneRows];                // over this lane's keys
             bool moves = false;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kLaneRows; ++k) {
                 const float* x = v + 32 * (k >> 1) + 2 * (k & 1);
                 float m0 = fmaxf(x[0], x[1]), m1 = fmaxf(x[4], x[5]);
 #pragma unroll
@@ -680,7 +698,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
             if (__any_sync(0xffffffffu, moves)) {
                 float f = 1.f;                 // of row `lane`
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kLaneRows; ++k) {
                     float top = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     float alpha = 1.f;
@@ -711,19 +729,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
                     }
                 }
             }
-            uint64_t base2[4];
+            uint64_t base2[kLaneRows];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kLaneRows; ++k) {
                 const float base = kProbShift<MB> - (ref[k] == -INFINITY ? 0.f : ref[k]);
                 base2[k] = pk(base, base);
             }
-            uint64_t s[4] = {0, 0, 0, 0};
-            uint32_t p[32];                    // p[16 h + 2 i + (k & 1)]
+            uint64_t s[kLaneRows];
+#pragma unroll
+            for (int k = 0; k < kLaneRows; ++k) s[k] = 0;
+            uint32_t p[8 * kLaneRows];         // p[16 h + 2 i + (k & 1)]
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint64_t iv = Q8 ? *reinterpret_cast<const uint64_t*>(ts.iv + 8 * i + 2 * t4) : 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < kLaneRows; ++k) {
                     const float* x = v + 32 * (k >> 1) + 4 * i + 2 * (k & 1);
                     float e0, e1;
                     upk(Q8 ? add2(pk(x[0], x[1]), base2[k]) : fma2(pk(x[0], x[1]), mul2, base2[k]), e0, e1);
@@ -735,13 +755,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
             }
             // this buffer's last P, of tile j - 2, was read when S of this tile was done
             tmem_st16x32(tP + buf * (kKeys / 2), p);
-            tmem_st16x32(tP + buf * (kKeys / 2) + (16u << 16), p + 16);
+            if (kLaneRows > 2) tmem_st16x32(tP + buf * (kKeys / 2) + (16u << 16), p + (kLaneRows > 2 ? 16 : 0));
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.pfull[t][buf]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < kLaneRows; ++k) {
                 float f0, f1;
                 upk(s[k], f0, f1);
                 sum[k] += f0 + f1;
@@ -755,7 +775,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
         // from here on a row to a thread
         float total = 0.f, top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kLaneRows; ++k) {
             sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
             sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
             const float x = __shfl_sync(0xffffffffu, sum[k], 4 * (lane & 7));
@@ -767,13 +787,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
         }
         const int r = quarter * 32 + lane;                 // of the stream's tile
         const int all = min(row_t + lane, rows - 1);
-        const bool live = row_t + lane < rows;
+        const bool live = lane < kQuarter && row_t + lane < rows;
         const int tok = all / a.R, head = kh * a.R + all - tok * a.R;
         const bool there = sWords[(tok - tok0) * kTreeWords + (tok >> 5)] >> (tok & 31) & 1u;
-        // KEYS: both streams' sums of the row, each stream then half of its columns
+        // Alternating streams: both sums of the row, each stream then half of its columns
         float f[2] = {1.f, 0.f};
         int c0 = 0, c1 = dsteps * 16;
-        if (KEYS) {
+        if (kAlternate) {
             float* join = reinterpret_cast<float*>(smem + M::join);
             join[t * 128 + r] = top;
             join[256 + t * 128 + r] = total;
@@ -794,7 +814,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
         const bool none = total == 0.f || !there;
         const float inv = none ? 0.f : 1.f / total;
         const int64_t row = ((int64_t)b * a.H + head) * a.n + tok;
-        if (live && (!KEYS || t == 0)) {
+        if (live && (!kAlternate || t == 0)) {
             const float lse2 = none ? -INFINITY : top - kProbShift<MB> + lg2(total);
             if (P.splits > 1)
                 P.part.lse2[split * P.part.rows + row] = lse2;
@@ -804,8 +824,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
         // Each thread writes 16 elements of its row at a time.
         T* out = static_cast<T*>(a.o.p) + b * a.o.sb + tok * a.o.st + (int64_t)head * a.o.sh;
         float* part = P.splits > 1 ? P.part.out + (split * P.part.rows + row) * a.d : nullptr;
-        const uint32_t o_at[2] = {tmem + C::O(KEYS ? 0 : t) + lofs, tmem + C::O(1) + lofs};
-        const int streams = KEYS ? (nt > 1 ? 2 : nt) : nt > 0;
+        const uint32_t o_at[2] = {tmem + C::O(kAlternate ? 0 : t) + lofs, tmem + C::O(1) + lofs};
+        const int streams = kAlternate ? (nt > 1 ? 2 : nt) : nt > 0;
         const bool any = quarter < warps_of(t);
 #pragma unroll 1
         for (int c = c0; c < c1 && any; c += 16) {
@@ -814,13 +834,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = y[e] = 0.f;
             if (streams > 0) tmem_ld16(o_at[0] + c, o);
-            if (KEYS && streams > 1) tmem_ld16(o_at[1] + c, y);
+            if (kAlternate && streams > 1) tmem_ld16(o_at[1] + c, y);
             tmem_wait_ld();
             tmem_reg_fence(o);
             tmem_reg_fence(y);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                o[e] = KEYS ? (f[0] == 0.f ? 0.f : f[0] * o[e]) + (f[1] == 0.f ? 0.f : f[1] * y[e]) : o[e];
+                o[e] = kAlternate ? (f[0] == 0.f ? 0.f : f[0] * o[e]) + (f[1] == 0.f ? 0.f : f[1] * y[e]) : o[e];
                 o[e] = none ? 0.f : o[e] * inv;
             }
             if (!live || !ok) {
@@ -853,20 +873,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_tree_tc(const __grid_constant
     }
 }
 
-template <int HD, int HELD, bool BF, bool KEYS>
+template <int HD, int HELD, bool BF, int MODE>
 cudaError_t launch(const TcArgs& p, cudaStream_t s) {
-    constexpr size_t bytes = 1024 + Smem<HD, HELD, KEYS>::bytes;
+    constexpr size_t bytes = 1024 + Smem<HD, HELD, MODE>::bytes;
     static std::atomic<uint64_t> ready{0};    // devices whose shared-memory limit is raised
-    if (cudaError_t e = raise_smem(k_tree_tc<HD, HELD, BF, KEYS>, bytes, ready); e != cudaSuccess) return e;
+    if (cudaError_t e = raise_smem(k_tree_tc<HD, HELD, BF, MODE>, bytes, ready); e != cudaSuccess) return e;
     const unsigned blocks = (unsigned)((int64_t)p.a.c.B * p.a.c.G * p.groups * p.splits);
-    k_tree_tc<HD, HELD, BF, KEYS><<<blocks, kTcThreads, bytes, s>>>(p);
+    k_tree_tc<HD, HELD, BF, MODE><<<blocks, Tc<HD, HELD, MODE>::kThreads, bytes, s>>>(p);
     count_launch();
     return cudaGetLastError();
 }
+template <int HD, int HELD, bool BF>
+cudaError_t launch_mode(const TcArgs& p, cudaStream_t s) {
+    const int rows = p.a.R * p.a.n;
+    if (rows > 128) return launch<HD, HELD, BF, ROWS>(p, s);
+    return rows > 64 ? launch<HD, HELD, BF, KEYS>(p, s) : launch<HD, HELD, BF, HALF>(p, s);
+}
 template <int HD, int HELD>
 cudaError_t launch_held(const TcArgs& p, cudaStream_t s) {
-    if (p.keys) return p.a.bf16 ? launch<HD, HELD, true, true>(p, s) : launch<HD, HELD, false, true>(p, s);
-    return p.a.bf16 ? launch<HD, HELD, true, false>(p, s) : launch<HD, HELD, false, false>(p, s);
+    return p.a.bf16 ? launch_mode<HD, HELD, true>(p, s) : launch_mode<HD, HELD, false>(p, s);
 }
 template <int HD>
 cudaError_t launch_width(const TcArgs& p, cudaStream_t s) {

@@ -47,15 +47,22 @@ template <int HD, int HELD, int MODE>
 struct Tc {
     static constexpr bool Q8 = HELD != HELD_16;
     static constexpr bool kAlternate = MODE != ROWS;     // key tiles to the streams in turn
-    // Half of the warps fit the keys of a tile, half its values; HALF leaves the registers for more
-    static constexpr int kFitWarps = Q8 && MODE == HALF ? 8 : 4, kFitters = 16 * kFitWarps;
+    // Half of the warps fit keys, half values, two warps to a tile.  HALF leaves the registers for
+    // more, which take the tiles in turn: a tile takes a warp as long as its waits and latencies do,
+    // whatever its share of it.
+    static constexpr int kFitWarps = Q8 && MODE == HALF ? 8 : 4, kGroups = kFitWarps / 4, kFitters = 64;
     static constexpr int kCopy = kFit0 + kFitWarps;      // two warps: one copies keys, one values
     static constexpr int kThreads = 32 * (kCopy + 2);
+    // HALF: products of 64 rows, whose rows 16 q .. 16 q + 15 are in lanes 32 q .. 32 q + 15
+    __device__ static constexpr uint32_t tile_of(uint32_t idesc) {
+        return MODE == HALF ? (idesc & ~(31u << 24)) | ((64u >> 4) << 24) : idesc;
+    }
     static constexpr int kQuarter = MODE == HALF ? 16 : 32;     // rows of a softmax warp
     static constexpr int kChunks = HD / 64;
     static constexpr int kChunkBytes = kKeys * 128;               // 64 elements of each key
     static constexpr int kSlotBytes = kChunks * kChunkBytes;      // a tile of keys, or of values
-    static constexpr int kQBytes = kChunks * CHUNK_BYTES;
+    static constexpr int kQChunk = MODE == HALF ? CHUNK_BYTES / 2 : CHUNK_BYTES;     // 64 or 128 rows
+    static constexpr int kQBytes = kChunks * kQChunk;
     static constexpr int kQTiles = kAlternate ? 1 : 2;
     static constexpr int kRows = 4 * kQuarter * kQTiles;
     static constexpr int kRing = Q8 ? (HD == 64 ? 4 : 3) : HD == 64 ? 8 : 4;     // tiles of each
@@ -65,12 +72,13 @@ struct Tc {
     // its own, and have the slot asked for again with a copy under way, a fault.  Widened
     // tiles are handed on in order.)
     static_assert(!kAlternate || Q8 || kRing % 2 == 0, "slots of one stream");
-    static constexpr int kRaw = !Q8 ? 0 : HD == 64 ? 8 : kAlternate ? 5 : 3;     // as they land
+    static constexpr int kRaw = !Q8 ? 0 : HD == 64 ? 8 : MODE == HALF ? 6 : MODE == KEYS ? 5 : 3;    // as they land
+    static_assert(kRaw % kGroups == 0, "slots of one group, which waits for them in their order");
     static constexpr int kRawBytes = kKeys * HD;
     // Descriptions of tiles are kept while the softmax may read them: it is behind the tile
-    // that a slot was last used for by up to 3 (alternating streams: 5), and 8-bit tiles are
-    // described when they are asked for, kRaw before that.
-    static constexpr int kScales = kRing + (kAlternate ? 5 : 3);
+    // that a slot was last used for by up to 3 (alternating streams: 5, with two groups 6), and
+    // 8-bit tiles are described when they are asked for, kRaw before that.
+    static constexpr int kScales = kRing + (!kAlternate ? 3 : kGroups == 1 ? 5 : 7);
     static constexpr int kBits = kScales + kRaw;
     __host__ __device__ static constexpr uint32_t S(int t) { return 256 * t; }
     __host__ __device__ static constexpr uint32_t P(int t) { return S(t) + kKeys; }    // two of 32 columns
@@ -107,8 +115,9 @@ struct Smem {
     static constexpr int bits = scales + (C::Q8 ? C::kScales * (int)sizeof(TileScales) : 0);
     static constexpr int words = bits + C::kBits * (int)sizeof(TileBits);     // [row's token][kTreeWords]
     static constexpr int join = words + C::kRows * 4 * kTreeWords;            // [ref, sum][stream][row]
-    static constexpr int parents = join + (C::kAlternate ? 4 * 4 * 128 : 0);
-    static constexpr int bars = parents + 4 * kv::kMaxTree;
+    static constexpr int parents = join;                                      // (done with before the join)
+    static constexpr int bars = join + (C::kAlternate ? 4 * 4 * 128 : 4 * kv::kMaxTree);
+    static_assert(4 * 4 * 128 >= 4 * kv::kMaxTree, "parents");
     static constexpr int top = bars + (int)sizeof(TcBars);                    // of the queries, by warps
     static constexpr int bytes = top + 4 * kSoftWarps;
     static_assert(bits % 16 == 0 && bars % 8 == 0, "alignment");
@@ -150,6 +159,17 @@ __device__ __forceinline__ void tmem_st16x32(uint32_t taddr, const uint32_t* v) 
         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
         "r"(v[15])
         : "memory");
+}
+
+// D[tmem] = A * B^T over the d elements, chunks of 64 a turn (as mma_over_d)
+template <int A_CHUNK, int B_CHUNK>
+__device__ __forceinline__ void mma_over_chunks(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, int chunks) {
+#pragma unroll 1
+    for (int x = 0; x < chunks; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            mma_f16(d_tmem, a + (uint64_t)(x * (A_CHUNK >> 4) + 2 * y), b + (uint64_t)(x * (B_CHUNK >> 4) + 2 * y),
+                    idesc, x != 0 || y != 0);
 }
 
 // whether 16 bytes hold an element that is not finite
@@ -276,7 +296,7 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& P, const Share& w, uint
 // operand tile.  16 bits: of the values, tiles with keys of the tree are looked through.
 template <int HD, int HELD, bool BF, int MODE, int KV>
 __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8_t* smem, TcBars& bar, int tid,
-                                          float mul) {
+                                          int group, float mul) {
     using C = Tc<HD, HELD, MODE>;
     using M = Smem<HD, HELD, MODE>;
     constexpr bool Q8 = C::Q8;
@@ -291,7 +311,16 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
     const int mixed_from = w.mixed_from(), j0 = Q8 ? 0 : mixed_from;
     Ring from, to;
     to.slot = j0 % C::kRing;
-    int scales = 0, bits = j0 % C::kBits;
+    constexpr int kGroups = C::kGroups;
+    int j_at = j0;
+    if (Q8 && kGroups > 1) {
+        j_at = group;
+        from.step(group, Q8 ? C::kRaw : 1);
+        to.step(group, C::kRing);
+    }
+    int scales = j_at % C::kScales, bits = j_at % C::kBits;
+    Ring before;               // the tile before this one: they are handed on in their order
+    if (kGroups > 1 && group == 0) before.step(1, C::kRing);
     // pieces of a row are in neighbouring lanes
     const auto look = [&](const uint4& x, int key0, int row, uint8_t* flags) {
         uint32_t bad = key0 + row >= w.ctx && nonfinite16<HELD, BF>(x);
@@ -301,7 +330,7 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
         return bad != 0;
     };
 #pragma unroll 1
-    for (int j = j0; j < w.nt; ++j) {
+    for (int j = j_at; j < w.nt; j += kGroups) {
         const int key0 = w.key_of(j);
         TileBits& tb = reinterpret_cast<TileBits*>(smem + M::bits)[bits];
         // Of the tree's keys: a value row with an element that is not finite is zeroed, and told
@@ -371,12 +400,18 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
             }
         }
         fence_proxy_async_smem();
+        if (kGroups > 1 && j > 0) {
+            if (!warp_wait(&bar.ready[KV][before.slot], before.phase, a.err, ERR_TIMEOUT_PRODUCER)) return;
+            before.step(kGroups, C::kRing);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(Q8 ? &bar.ready[KV][to.slot] : &bar.looked[j - mixed_from]);
-        if (Q8) from.step(1, Q8 ? C::kRaw : 1);
-        to.step(1, C::kRing);
-        if (++scales == C::kScales) scales = 0;
-        if (++bits == C::kBits) bits = 0;
+        if (Q8) from.step(kGroups, Q8 ? C::kRaw : 1);
+        to.step(kGroups, C::kRing);
+        scales += kGroups;
+        if (scales >= C::kScales) scales -= C::kScales;
+        bits += kGroups;
+        if (bits >= C::kBits) bits -= C::kBits;
     }
 }
 
@@ -388,7 +423,7 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
     constexpr bool Q8 = C::Q8;
     constexpr bool MB = BF && !Q8;             // products in bfloat16
     constexpr bool kAlternate = C::kAlternate;
-    constexpr int NR = C::kRing, kCopy = C::kCopy, kFitWarps = C::kFitWarps, kFitters = C::kFitters;
+    constexpr int NR = C::kRing, kCopy = C::kCopy, kFitters = C::kFitters;
     constexpr int kQuarter = C::kQuarter, kLaneRows = kQuarter / 8;     // rows of a lane: 8 apart
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -504,20 +539,19 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
         }
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
-            int r = threadIdx.x / kPieces + i * kStep;
-            if (MODE == HALF) r = r / kQuarter * 32 + r % kQuarter;    // (what the other rows hold stays in them)
-            sts16(smem_u32(smem) + M::q + (r >> 7) * C::kQBytes + (u >> 3) * CHUNK_BYTES +
+            const int r = threadIdx.x / kPieces + i * kStep;
+            sts16(smem_u32(smem) + M::q + (r >> 7) * C::kQBytes + (u >> 3) * C::kQChunk +
                       swz_offset(r & 127, (u & 7) * 8),
                   x[i][0], x[i][1], x[i][2], x[i][3]);
         }
         fence_proxy_async_smem();
     } else if (warp == kMma0) {
         if (lane < 16) {
-            mbar_init(&bar.ready[lane >> 3][lane & 7], kFitWarps / 2);
+            mbar_init(&bar.ready[lane >> 3][lane & 7], 2);
             mbar_init(&bar.empty[lane >> 3][lane & 7], !kAlternate && two ? 2 : 1);
-            mbar_init(&bar.free_raw[lane >> 3][lane & 7], kFitWarps / 2);
+            mbar_init(&bar.free_raw[lane >> 3][lane & 7], 2);
         } else if (lane < 16 + kMixed) {
-            mbar_init(&bar.looked[lane - 16], kFitWarps / 2);
+            mbar_init(&bar.looked[lane - 16], 2);
         } else if (lane >= 30) {
             const int t = lane - 30;
             mbar_init(&bar.sfull[t], 1);
@@ -546,17 +580,17 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
             const int down = (int)(top >> 7) - 14 - 127;
             mul = mul * two_to(down / 2) * two_to(down - down / 2);
         }
-        const int tid = (threadIdx.x - 32 * kFit0) & (kFitters - 1);
-        if (warp < kFit0 + kFitWarps / 2)
-            fit_tiles<HD, HELD, BF, MODE, 0>(P, w, smem, bar, tid, mul);
+        const int tid = (threadIdx.x - 32 * kFit0) & (kFitters - 1), fit = (warp - kFit0) >> 1;
+        if (fit < C::kGroups)
+            fit_tiles<HD, HELD, BF, MODE, 0>(P, w, smem, bar, tid, fit, mul);
         else
-            fit_tiles<HD, HELD, BF, MODE, 1>(P, w, smem, bar, tid, mul);
+            fit_tiles<HD, HELD, BF, MODE, 1>(P, w, smem, bar, tid, fit - C::kGroups, mul);
     } else if (warp >= kMma0) {
         const int t = warp - kMma0;
         const int n_mine = kAlternate ? (nt + 1 - t) / 2 : nt;
         if (n_mine > 0 && (t == 0 || two) && elect_one()) {
             constexpr int kBy = kAlternate ? 2 : 1;
-            const uint32_t idS = idesc_16(MB, kKeys, false), idO = idesc_16(MB, dsteps * 16, true);
+            const uint32_t idS = C::tile_of(idesc_16(MB, kKeys, false)), idO = C::tile_of(idesc_16(MB, dsteps * 16, true));
             constexpr uint64_t kSlotU = C::kSlotBytes >> 4;    // descriptors count 16 bytes
             const uint64_t dQ = sdesc_sw128(smem_u32(smem + M::q)) + (kAlternate ? 0 : t) * (C::kQBytes >> 4);
             const uint64_t dK = sdesc_sw128(smem_u32(smem + M::ring));
@@ -571,7 +605,7 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
                     if (!(ok = mma_wait(a.err, k_in + rk.slot, rk.phase) &&
                                (j < 0 || mma_wait(a.err, &bar.sfree[t], j & 1))))
                         break;
-                    mma_over_d<4, C::kChunkBytes>(cS, dQ, dK + rk.slot * kSlotU, idS, (dsteps + 3) / 4);
+                    mma_over_chunks<C::kQChunk, C::kChunkBytes>(cS, dQ, dK + rk.slot * kSlotU, idS, (dsteps + 3) / 4);
                     mma_commit(&bar.sfull[t]);
                     mma_commit(&bar.empty[0][rk.slot]);
                     rk.step(kBy, NR);

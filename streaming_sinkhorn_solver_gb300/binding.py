@@ -905,54 +905,81 @@ for _packed, _desc in ((_ROTATION, fs_rotation), (_CACHE, fs_cache), (_CACHE_ROW
     assert _packed.size == ctypes.sizeof(_desc)
 
 
-def _rows16(x, name: str):
-    """Refuses what is no (batch, n, heads, d) tensor of a 16-bit type on the GPU."""
-    import torch
-    if not _DTYPES:
+_TORCH = []
+
+
+def _with_torch():
+    """torch, and once the types' numbers (an import statement costs 0.4 us a call)."""
+    if not _TORCH:
+        import torch
         _DTYPES.update({torch.bfloat16: 0, torch.float16: 1})
+        _CACHE_DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2, torch.int8: 3})
+        _TORCH.append(torch)
+    return _TORCH[0]
+
+
+_CACHE_DTYPES = {}
+
+
+def _rows16(torch, x, name: str):
+    """The shape of x; refuses what is no (batch, n, heads, d) tensor of a 16-bit type on the GPU."""
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES or not x.is_cuda:
         raise TypeError(f"{name} must be a bfloat16 or float16 CUDA tensor")
-    if x.dim() != 4 or x.shape[3] < 1:
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected (batch, n, heads, d)")
+    shape = x.shape
+    if len(shape) != 4 or shape[3] < 1:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected (batch, n, heads, d)")
+    return shape
+
+
+def _result(torch, x, name: str, shape, like, stream):
+    """(a result, its strides): x, checked, or a new one."""
+    if x is not None:
+        return x, _att_strides(x, name, shape, like)
+    if stream is None:
+        x = torch.empty(shape, dtype=like.dtype, device=like.device)
+    else:
+        x = _att_empty(like, shape, like.dtype, stream)
+    _, n, heads, d = shape
+    return x, (n * heads * d, heads * d, d)
 
 
 def _rotate(fn: str, q, k, freqs, pos, interleaved, amplitude, q_out, k_out, stream) -> Tuple:
-    import torch
-    _rows16(q, "q")
-    batch, n, heads, d = q.shape
-    qs = _att_strides(q, "q", q.shape, q)
+    torch = _with_torch()
+    shape = batch, n, heads, d = _rows16(torch, q, "q")
+    qs = _att_strides(q, "q", shape, q)
     kv_heads, ks, kos, k_p, ko_p = 0, _NO_STRIDES, _NO_STRIDES, None, None
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise TypeError("k must be a tensor (batch, n, kv_heads, d) or None")
         kv_heads = k.shape[2]
-        ks = _att_strides(k, "k", (batch, n, kv_heads, d), q)
+        k_shape = (batch, n, kv_heads, d)
+        ks = _att_strides(k, "k", k_shape, q)
         k_p = k.data_ptr()
     elif k_out is not None:
         raise TypeError("k_out without k")
-    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
-        raise TypeError("freqs must be a float64 CUDA tensor (rotary_dim / 2,)")
-    half = freqs.shape[0]
-    freqs_p = _i_ptr(freqs, "freqs", (half,), torch.float64)
-    if not (isinstance(pos, torch.Tensor) and pos.is_cuda and pos.dtype == torch.int32):
+    if not isinstance(freqs, torch.Tensor) or freqs.dtype != torch.float64 or not freqs.is_cuda \
+            or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise TypeError("freqs must be a contiguous float64 CUDA tensor (rotary_dim / 2,)")
+    if not isinstance(pos, torch.Tensor) or pos.dtype != torch.int32 or not pos.is_cuda:
         raise TypeError("pos must be an int32 CUDA tensor")
-    if tuple(pos.shape) not in ((n,), (batch, n)):
+    if pos.shape == (batch, n):
+        step = pos.stride()
+    elif pos.shape == (n,):
+        step = (0, pos.stride(0))
+    else:
         raise ValueError(f"pos has shape {tuple(pos.shape)}, expected {(batch, n)} or {(n,)}")
-    step = pos.stride() if pos.dim() == 2 else (0, pos.stride(0))
-    q_out = _att_empty(q, q.shape, q.dtype, stream) if q_out is None else q_out
-    qos = _att_strides(q_out, "q_out", q.shape, q)
-    if kv_heads:
-        k_out = _att_empty(q, k.shape, q.dtype, stream) if k_out is None else k_out
-        kos = _att_strides(k_out, "k_out", k.shape, q)
+    q_out, qos = _result(torch, q_out, "q_out", shape, q, stream)
+    if k is not None:
+        k_out, kos = _result(torch, k_out, "k_out", k_shape, q, stream)
         ko_p = k_out.data_ptr()
-    elif k is not None and k_out is None:
-        k_out = _att_empty(q, k.shape, q.dtype, stream)
     r = fs_rotation()
-    _ROTATION.pack_into(r, 0, _DTYPES[q.dtype], heads, kv_heads, d, 2 * half,
+    _ROTATION.pack_into(r, 0, _DTYPES[q.dtype], heads, kv_heads, d, 2 * freqs.shape[0],
                         1 if interleaved else 0, batch, n, amplitude, 0, *qs, *ks, *qos, *kos,
-                        freqs_p, pos.data_ptr(), *step)
-    _raise(getattr(load_library(), fn)(ctypes.byref(r), q.data_ptr(), k_p, q_out.data_ptr(), ko_p,
-                                       _att_stream(stream, q)))
+                        freqs.data_ptr(), pos.data_ptr(), *step)
+    st = getattr(_lib or load_library(), fn)(r, q.data_ptr(), k_p, q_out.data_ptr(), ko_p,
+                                             _att_stream(stream, q))
+    if st:
+        _raise(st)
     return q_out, k_out
 
 
@@ -989,11 +1016,10 @@ class KVCache(NamedTuple):
 
 def fs_cache_new(pages: int, kv_heads: int, page_size: int, d: int, dtype, device="cuda") -> KVCache:
     """An empty cache (zeros) of `dtype`; in 8 bits its rows start at multiples of 16 bytes."""
-    import torch
-    held = _cache_dtypes()
-    if dtype not in held:
-        raise TypeError(f"dtype must be one of {', '.join(map(str, held))}")
-    eight = held[dtype] >= 2
+    torch = _with_torch()
+    if dtype not in _CACHE_DTYPES:
+        raise TypeError(f"dtype must be one of {', '.join(map(str, _CACHE_DTYPES))}")
+    eight = _CACHE_DTYPES[dtype] >= 2
     wide = (d + 15) // 16 * 16 if eight else d
 
     def rows():
@@ -1006,24 +1032,12 @@ def fs_cache_new(pages: int, kv_heads: int, page_size: int, d: int, dtype, devic
     return KVCache(rows(), rows(), *((scale(), scale()) if eight else ()))
 
 
-_CACHE_DTYPES = {}
-
-
-def _cache_dtypes():
-    import torch
-    if not _CACHE_DTYPES:
-        _CACHE_DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2,
-                              torch.int8: 3})
-    return _CACHE_DTYPES
-
-
-def _cache(cache, table, like) -> fs_cache:
+def _cache(torch, cache, table, like) -> fs_cache:
     """Checked description of a KVCache with its page table, for tensors on like's device."""
-    import torch
     k, v, k_scale, v_scale = cache
-    held = _cache_dtypes().get(getattr(k, "dtype", None))
-    if held is None or not isinstance(k, torch.Tensor) or k.device != like.device:
+    if not isinstance(k, torch.Tensor) or k.dtype not in _CACHE_DTYPES or k.device != like.device:
         raise TypeError(f"cache.k must be a 16-bit, float8_e4m3fn or int8 tensor on {like.device}")
+    held = _CACHE_DTYPES[k.dtype]
     shape = k.shape
     if len(shape) != 4:
         raise ValueError(f"cache.k has shape {tuple(shape)}, expected (pages, kv_heads, page_size, d)")
@@ -1032,26 +1046,28 @@ def _cache(cache, table, like) -> fs_cache:
     ks_p = vs_p = 0
     kss = vss = (0, 0)
     if held >= 2:
+        want = shape[:3]
         for x, name in ((k_scale, "cache.k_scale"), (v_scale, "cache.v_scale")):
-            if not (isinstance(x, torch.Tensor) and x.dtype == torch.float32 and x.device == k.device
-                    and x.shape == shape[:3]):
-                raise TypeError(f"{name} must be a float32 tensor of shape {tuple(shape[:3])} on {k.device}")
-            if shape[2] > 1 and x.stride(2) != 1:
+            if not isinstance(x, torch.Tensor) or x.dtype != torch.float32 or x.shape != want \
+                    or x.device != k.device:
+                raise TypeError(f"{name} must be a float32 tensor of shape {tuple(want)} on {k.device}")
+            if want[2] > 1 and x.stride(2) != 1:
                 raise TypeError(f"the tokens of {name} must be contiguous")
         ks_p, vs_p, kss, vss = k_scale.data_ptr(), v_scale.data_ptr(), k_scale.stride()[:2], v_scale.stride()[:2]
     elif k_scale is not None or v_scale is not None:
         raise TypeError("a cache in 16 bits has no scales")
-    if not (isinstance(table, torch.Tensor) and table.dtype == torch.int32 and table.device == k.device
-            and table.dim() == 2):
+    if not isinstance(table, torch.Tensor) or table.dtype != torch.int32 or table.device != k.device \
+            or table.dim() != 2:
         raise TypeError(f"table must be an int32 tensor (batch, pages of a sequence) on {k.device}")
-    if table.shape[0] != like.shape[0]:
+    rows, per = table.shape
+    if rows != like.shape[0]:
         raise ValueError(f"table has shape {tuple(table.shape)}, expected {like.shape[0]} rows")
-    if table.shape[1] > 1 and table.stride(1) != 1:
+    step, one = table.stride()
+    if per > 1 and one != 1:
         raise TypeError("the rows of table must be contiguous")
     c = fs_cache()
-    _CACHE.pack_into(c, 0, held, shape[1], shape[3], shape[2], shape[0], table.shape[0], table.shape[1],
-                     table.stride(0), k.data_ptr(), v.data_ptr(), ks_p, vs_p, *ks, *vs, *kss, *vss,
-                     table.data_ptr())
+    _CACHE.pack_into(c, 0, held, shape[1], shape[3], shape[2], shape[0], rows, per, step, k.data_ptr(),
+                     v.data_ptr(), ks_p, vs_p, *ks, *vs, *kss, *vss, table.data_ptr())
     return c
 
 
@@ -1065,22 +1081,22 @@ def fs_cache_write(cache: KVCache, table, positions, k, v, *, stream=None) -> No
                beyond the table or without a page are left out.  The rows that one call
                writes are distinct: of two tokens at one place, parts of either may be left.
     """
-    import torch
-    _rows16(k, "k")
-    batch, n, _, _ = k.shape
-    c = _cache(cache, table, k)
-    want = (batch, n, cache.k.shape[1], cache.k.shape[3])
+    torch = _with_torch()
+    batch, n, _, _ = _rows16(torch, k, "k")
+    c = _cache(torch, cache, table, k)
+    want = (batch, n, cache[0].shape[1], cache[0].shape[3])
     ks, vs = _att_strides(k, "k", want, k), _att_strides(v, "v", want, k)
-    if not (isinstance(positions, torch.Tensor) and positions.dtype == torch.int32
-            and positions.device == k.device and tuple(positions.shape) == (batch, n)):
+    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 \
+            or positions.device != k.device or positions.shape != (batch, n):
         raise TypeError(f"positions must be an int32 tensor of shape {(batch, n)} on {k.device}")
-    if n > 1 and positions.stride(1) != 1:
+    step, one = positions.stride()
+    if n > 1 and one != 1:
         raise TypeError("the rows of positions must be contiguous")
     r = fs_cache_rows()
-    _CACHE_ROWS.pack_into(r, 0, _DTYPES[k.dtype], 0, n, *ks, *vs, positions.data_ptr(),
-                          positions.stride(0))
-    _raise(load_library().fs_cache_write(ctypes.byref(c), ctypes.byref(r), k.data_ptr(), v.data_ptr(),
-                                         _att_stream(stream, k)))
+    _CACHE_ROWS.pack_into(r, 0, _DTYPES[k.dtype], 0, n, *ks, *vs, positions.data_ptr(), step)
+    st = (_lib or load_library()).fs_cache_write(c, r, k.data_ptr(), v.data_ptr(), _att_stream(stream, k))
+    if st:
+        _raise(st)
 
 
 def fs_cache_read(cache: KVCache, table, lens=None, n: Optional[int] = None, *, dtype=None, k=None,
@@ -1089,32 +1105,38 @@ def fs_cache_read(cache: KVCache, table, lens=None, n: Optional[int] = None, *, 
     (batch, n, kv_heads, d) for fs_cross_attention: new ones of `dtype` (None: the cache's,
     bfloat16 for 8 bits) or as given.  Zeros from lens[b] (int32 (batch,)) on and where
     there is no page."""
-    import torch
-    like = cache.k
+    torch = _with_torch()
+    like = cache[0]
     if not isinstance(like, torch.Tensor) or not like.is_cuda or like.dim() != 4:
         raise TypeError("cache.k must be a CUDA tensor (pages, kv_heads, page_size, d)")
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise TypeError("table must be an int32 tensor (batch, pages of a sequence)")
-    n = table.shape[1] * like.shape[2] if n is None else int(n)
+    _, heads, page, d = like.shape
+    batch, per = table.shape
+    n = per * page if n is None else int(n)
     if dtype is None:
         dtype = k.dtype if k is not None else like.dtype if like.element_size() == 2 else torch.bfloat16
-    if dtype not in (torch.bfloat16, torch.float16):
+    if dtype not in _DTYPES:
         raise TypeError("dtype must be bfloat16 or float16")
     if n < 0:
         raise ValueError(f"n={n}")
-    want = (table.shape[0], n, like.shape[1], like.shape[3])
-    k = _att_empty(like, want, dtype, stream) if k is None else k
-    v = _att_empty(like, want, dtype, stream) if v is None else v
-    _rows16(k, "k")
-    if k.dtype != dtype:
-        raise TypeError(f"k must be a {dtype} tensor")
-    c = _cache(cache, table, k)
-    ks, vs = _att_strides(k, "k", want, k), _att_strides(v, "v", want, k)
-    lens_p = 0 if lens is None else _i_ptr(lens, "lens", (table.shape[0],), torch.int32)
+    want = (batch, n, heads, d)
+    if k is None:
+        k = _att_empty(like, want, dtype, stream)
+        ks = (n * heads * d, heads * d, d)
+    else:
+        _rows16(torch, k, "k")
+        if k.dtype != dtype:
+            raise TypeError(f"k must be a {dtype} tensor")
+        ks = _att_strides(k, "k", want, k)
+    v, vs = _result(torch, v, "v", want, k, stream)
+    c = _cache(torch, cache, table, k)
+    lens_p = 0 if lens is None else _i_ptr(lens, "lens", (batch,), torch.int32)
     r = fs_cache_rows()
     _CACHE_ROWS.pack_into(r, 0, _DTYPES[dtype], 0, n, *ks, *vs, lens_p, 0)
-    _raise(load_library().fs_cache_read(ctypes.byref(c), ctypes.byref(r), k.data_ptr(), v.data_ptr(),
-                                        _att_stream(stream, k)))
+    st = (_lib or load_library()).fs_cache_read(c, r, k.data_ptr(), v.data_ptr(), _att_stream(stream, k))
+    if st:
+        _raise(st)
     return k, v
 
 
@@ -1133,26 +1155,26 @@ def fs_tree_attention(q, cache: KVCache, table, ctx_len, parents=None, *,
     scale         factor of the dot products, d ** -0.5 if None
     Positions beyond the table or without a page do not count.
     """
-    import torch
-    _rows16(q, "q")
-    batch, n, heads, d = q.shape
-    c = _cache(cache, table, q)
-    if cache.k.shape[3] != d:
-        raise ValueError(f"q has heads of {d}, the cache of {cache.k.shape[3]}")
-    qs = _att_strides(q, "q", q.shape, q)
+    torch = _with_torch()
+    shape = batch, n, heads, d = _rows16(torch, q, "q")
+    c = _cache(torch, cache, table, q)
+    if cache[0].shape[3] != d:
+        raise ValueError(f"q has heads of {d}, the cache of {cache[0].shape[3]}")
+    qs = _att_strides(q, "q", shape, q)
     ctx_p = _i_ptr(ctx_len, "ctx_len", (batch,), torch.int32)
     par_p = par_s = 0
     if parents is not None:
-        if not (isinstance(parents, torch.Tensor) and parents.dtype == torch.int32
-                and parents.device == q.device):
+        if not isinstance(parents, torch.Tensor) or parents.dtype != torch.int32 \
+                or parents.device != q.device:
             raise TypeError(f"parents must be an int32 tensor on {q.device}")
-        if tuple(parents.shape) not in ((n,), (batch, n)):
+        if parents.shape == (batch, n):
+            par_s = parents.stride(0)
+        elif parents.shape != (n,):
             raise ValueError(f"parents has shape {tuple(parents.shape)}, expected {(batch, n)} or {(n,)}")
         if n > 1 and parents.stride(-1) != 1:
             raise TypeError("the rows of parents must be contiguous")
-        par_p, par_s = parents.data_ptr(), parents.stride(0) if parents.dim() == 2 else 0
-    out = _att_empty(q, q.shape, q.dtype, stream) if out is None else out
-    os_ = _att_strides(out, "out", q.shape, q)
+        par_p = parents.data_ptr()
+    out, out_s = _result(torch, out, "out", shape, q, stream)
     rows = (batch, heads, n)
     if lse is None:
         lse = _att_empty(q, rows, torch.float32, stream)
@@ -1161,7 +1183,9 @@ def fs_tree_attention(q, cache: KVCache, table, ctx_len, parents=None, *,
         lse_p = _ptr(lse, "lse", rows)
     t = fs_tree()
     _TREE.pack_into(t, 0, _DTYPES[q.dtype], heads, n, d ** -0.5 if scale is None else scale, 0, *qs,
-                    *os_, ctx_p, par_p, par_s)
-    _raise(load_library().fs_tree_attention(ctypes.byref(c), ctypes.byref(t), q.data_ptr(),
-                                            out.data_ptr(), lse_p, _att_stream(stream, q)))
+                    *out_s, ctx_p, par_p, par_s)
+    st = (_lib or load_library()).fs_tree_attention(c, t, q.data_ptr(), out.data_ptr(), lse_p,
+                                                    _att_stream(stream, q))
+    if st:
+        _raise(st)
     return out, lse

@@ -5,9 +5,12 @@
 // into the operand registers of mma.sync (S = Q K^T with any 16 of the d elements in a
 // product, the same for both operands; O^T += V^T P^T, with P^T in S's own layout).
 //
-// A cache in 8 bits is widened to float16 in registers, which is exact: a lane's 16 bytes
-// of a key row are 4 products' worth of its operand, and of four value rows a byte permute
-// pairs two keys before they are widened.  Scales stay in float32:
+// A cache in 8 bits comes through a ring in shared memory that each warp keeps for itself,
+// two steps ahead by asynchronous copies, and is widened to float16 in registers, which is
+// exact: a lane's 16 bytes of a key row are 4 products' worth of its operand, and of four value
+// rows a byte permute pairs two keys before they are widened.  (Straight from memory, as the 16-bit
+// types come, the loads of a step waited for the page numbers and the products for the loads,
+// with registers for two blocks to an SM: half the speed.)  Scales stay in float32:
 //   x_ij = q_i . code_j (scale2 ks_j) + log2 vs_j,   P_ij = 2^{x_ij - ref_i},
 //   O_i = sum_j P_ij code_j,   sum_i = sum_j P_ij / vs_j,
 // so that the largest P of a row is the one that counts most in O, whatever the scales,
@@ -54,22 +57,6 @@ __device__ __forceinline__ void ld16(const uint8_t* p, bool on, uint32_t* x) {
                      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                      : "l"(p));
 }
-__device__ __forceinline__ void ld8(const uint8_t* p, bool on, uint32_t* x) {
-    x[0] = x[1] = 0;
-    if (on)
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-                     : "=r"(x[0]), "=r"(x[1])
-                     : "l"(p));
-}
-// 16 codes from element c on, zero from d on
-__device__ __forceinline__ void ld_codes16(const uint8_t* row, int c, int d, bool on, bool vec16, uint32_t* x) {
-    if (vec16) {
-        ld16(row + c, on && c < d, x);
-    } else {
-        ld8(row + c, on && c < d, x);
-        ld8(row + c + 8, on && c + 8 < d, x + 2);
-    }
-}
 
 // whether a register of the held type has an element that is not finite
 template <int HELD, bool BF>
@@ -83,9 +70,44 @@ __device__ __forceinline__ bool nonfinite(uint32_t w) {
     return (w & kExp) == kExp || ((w >> 16) & kExp) == kExp;
 }
 
-// RB: blocks of 8 query rows
-template <int HD, int RB>
-constexpr size_t kFewSmem = sizeof(float) * kWarps * 8 * RB * (HD + 2);
+__device__ __forceinline__ void cp16(uint32_t dst, const uint8_t* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const uint8_t* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const float* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0)
+                 : "memory");
+}
+
+// 8 bits, a warp's step of 32 keys in shared memory: codes of keys, of values, scales of both.
+// Rows of 128 bytes (two rows of 64 elements to one); the 16-byte unit u of row r lies where
+// the lanes that read at once (keys: two rows, half of each; values: two units of rows 2 t)
+// find theirs in different banks.
+template <int HD>
+struct Step {
+    static constexpr int kSteps = 3;
+    static constexpr int kRows = 32 * HD, kScales = 2 * 32 * 4;
+    static constexpr int kBytes = 2 * kRows + kScales;
+    __device__ static __forceinline__ int key_at(int r, int u) {
+        return HD == 128 ? 128 * r + 16 * (u ^ ((r & 1) << 2)) : value_at(r, u);
+    }
+    __device__ static __forceinline__ int value_at(int r, int u) {
+        return HD == 128 ? 128 * r + 16 * (u ^ (2 * (r >> 1 & 3)))
+                         : 128 * (r >> 1) + 16 * (((r & 1) * 4 + u) ^ (2 * (r >> 1 & 3)));
+    }
+};
+
+// RB: blocks of 8 query rows.  A warp's rows of O lie over its ring.
+template <int HD, int HELD, int RB>
+constexpr int kWarpBytes = HELD == HELD_16 || Step<HD>::kSteps * Step<HD>::kBytes < 4 * 8 * RB * HD
+                               ? 4 * 8 * RB * HD
+                               : Step<HD>::kSteps * Step<HD>::kBytes;
+template <int HD, int HELD, int RB>
+constexpr size_t kFewSmem = kWarps * (kWarpBytes<HD, HELD, RB> + sizeof(float) * 2 * 8 * RB);
 
 template <int HD, int HELD, bool BF, int RB>
 __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant__ FewArgs P) {
@@ -98,11 +120,12 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
     constexpr int VW = HD * EB / 32;                  // registers of a lane's part of a value row
     constexpr int NT = HD / 16;                       // O tiles: two elements of d to a lane
     constexpr int KB = !Q8 && HD == 64 ? 1 : 2, KEYS = 16 * KB;
+    constexpr int kWarpRows = kWarpBytes<HD, HELD, RB> / 4;     // floats from a warp's rows to the next's
     constexpr int RP = (RB + 1) / 2, ROWS = 8 * RB;
     constexpr float kShift = kProbShift<MB>;
     extern __shared__ float smem[];
     float* sO = smem;                                   // [warp][row][HD]
-    float* sRef = sO + kWarps * ROWS * HD;              // [warp][row]
+    float* sRef = sO + kWarps * kWarpRows;              // [warp][row]
     float* sSum = sRef + kWarps * ROWS;
     __shared__ int sParents[kv::kMaxTree];
     __shared__ uint32_t sTree[ROWS][kWords];
@@ -210,59 +233,148 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
     const uint8_t* kp = c.k.p + kh * c.k.head;
     const uint8_t* vp = c.v.p + kh * c.v.head;
 
-    for (int key = k0 + KEYS * warp; key < k1; key += KEYS * kWarps) {
-        // pages of each 8 of these keys (which none of them leaves), and what counts
-        int page[2 * KB];
-        uint32_t bits = 0;
+    // 8 bits: the ring, and what of the steps in it counts
+    using St = Step<HD>;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * 4 * kWarpRows;
+    uint32_t next_bits[St::kSteps - 1];
 #pragma unroll
-        for (int nb = 0; nb < 2 * KB; ++nb) {
-            const int at = key + 8 * nb;
-            page[nb] = at < k1 ? c.page_of(b, at) : -1;
-            if (page[nb] >= 0) bits |= (at + 8 <= k1 ? 255u : (1u << (k1 - at)) - 1u) << (8 * nb);
-        }
-        if (bits == 0) continue;
-        uint32_t k[2 * KB][U][4], v[KB][4][VW];
-        float ks[4 * KB], lv[4 * KB], iv[4 * KB];      // of keys 8 nb + 2 t + {0, 1}
+    for (int x = 0; x < St::kSteps - 1; ++x) next_bits[x] = 0;
+    int entry = -1;                       // of the step to be asked for, its keys 8 (lane & 3) on
+    const auto load_entry = [&](int key) {
+        const int i = (key + 8 * (lane & 3)) >> c.log_page;
+        int e = -1;
+        if (key < k1 && i < c.table_pages)
+            asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(e) : "l"(c.table + b * c.table_stride + i));
+        return e;
+    };
+    const auto ask = [&](int key, int stage) -> uint32_t {
+        const uint32_t to = ring + stage * St::kBytes;
+        const int left = k1 - (key + 8 * (lane & 3));
+        const bool on = (unsigned)entry < c.pages && left > 0;
+        const int held = on ? entry : -1;
+        entry = load_entry(key + KEYS * kWarps);
+        uint32_t bits = on && lane < 4 ? (left >= 8 ? 255u : (1u << left) - 1u) << (8 * lane) : 0u;
+        bits = __reduce_or_sync(0xffffffffu, bits);
+        constexpr int kUnits = HD / 16, kStep = 32 / kUnits;      // rows of an access
+        const int u = lane % kUnits;
 #pragma unroll
-        for (int nb = 0; nb < 2 * KB; ++nb) {
-            const int j = 8 * nb + g;
-            const bool on = (bits >> j) & 1u;
-            const uint8_t* p = kp + page[nb] * c.k.page + c.slot_of(key + j) * c.k.token;
+        for (int i = 0; i < 32 / kStep; ++i) {
+            const int pg = __shfl_sync(0xffffffffu, held, i * kStep / 8), r = i * kStep + lane / kUnits;
+            const bool there = bits >> r & 1u;
+            const int slot = c.slot_of(key + r);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (Q8)
-                    ld_codes16(p, PIECE * (t + 4 * u), a.d, on, c.vec16, k[nb][u]);
-                else
-                    ld16(p + 16 * (t + 4 * u), on && PIECE * (t + 4 * u) < a.d, k[nb][u]);
-            }
-        }
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int j = 16 * kb + 2 * t + (x & 1) + 8 * (x >> 1);
-                const bool on = (bits >> j) & 1u;
-                const uint8_t* p = vp + page[2 * kb + (x >> 1)] * c.v.page + c.slot_of(key + j) * c.v.token;
-                if (Q8) {
-                    if (HD == 128)
-                        ld_codes16(p, 16 * g, a.d, on, c.vec16, v[kb][x]);
-                    else
-                        ld8(p + 8 * g, on && 8 * g < a.d, v[kb][x]);
+            for (int v = 0; v < 2; ++v) {
+                const kv::Pool& p = v ? c.v : c.k;
+                const uint8_t* src = there ? (v ? vp : kp) + pg * p.page + slot * p.token + 16 * u : p.p;
+                const uint32_t dst = to + v * St::kRows + (v ? St::value_at(r, u) : St::key_at(r, u));
+                if (c.vec16) {
+                    cp16(dst, src, there && 16 * u < a.d);
                 } else {
-#pragma unroll
-                    for (int w = 0; w < HD / 64; ++w)
-                        ld16(p + 16 * g + 128 * w, on && 8 * g + 64 * w < a.d, v[kb][x] + 4 * w);
+                    const bool first = there && 16 * u < a.d, second = there && 16 * u + 8 < a.d;
+                    cp8(dst, first ? src : p.p, first);
+                    cp8(dst + 8, second ? src + 8 : p.p, second);
                 }
             }
-        if (Q8) {
+        }
+        const int pg = __shfl_sync(0xffffffffu, held, lane >> 3);
+        const bool there = bits >> lane & 1u;
+        const int slot = c.slot_of(key + lane);
+        cp4(to + 2 * St::kRows + 4 * lane, there ? c.k.scale + pg * c.k.s_page + kh * c.k.s_head + slot : c.k.scale,
+            there);
+        cp4(to + 2 * St::kRows + 4 * (32 + lane),
+            there ? c.v.scale + pg * c.v.s_page + kh * c.v.s_head + slot : c.v.scale, there);
+        return bits;
+    };
+    int stage = 0;
+    if (Q8) {
+        entry = load_entry(k0 + KEYS * warp);
 #pragma unroll
-            for (int e = 0; e < 4 * KB; ++e) {
-                const int nb = e >> 1, j = 8 * nb + 2 * t + (e & 1);
-                const bool on = (bits >> j) & 1u;
-                const int slot = c.slot_of(key + j);
-                ks[e] = on ? __ldg(c.k.scale + page[nb] * c.k.s_page + kh * c.k.s_head + slot) : 0.f;
-                lv[e] = on ? __ldg(c.v.scale + page[nb] * c.v.s_page + kh * c.v.s_head + slot) : 1.f;
+        for (int x = 0; x < St::kSteps - 1; ++x) {
+            const int key = k0 + KEYS * (warp + kWarps * x);
+            if (key < k1) next_bits[x] = ask(key, x);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    }
+
+    for (int key = k0 + KEYS * warp; key < k1; key += KEYS * kWarps) {
+        uint32_t bits = 0;
+        uint32_t k[2 * KB][U][4], v[KB][4][VW];
+        float ks[4 * KB], lv[4 * KB], iv[4 * KB];      // of keys 8 nb + 2 t + {0, 1}
+        const uint8_t* step = reinterpret_cast<const uint8_t*>(smem) + warp * 4 * kWarpRows + stage * St::kBytes;
+        if (Q8) {
+            __syncwarp();                 // the step before is done with
+            const int far = key + KEYS * kWarps * (St::kSteps - 1);
+            const int to = stage == 0 ? St::kSteps - 1 : stage - 1;
+            bits = next_bits[0];
+#pragma unroll
+            for (int x = 0; x + 1 < St::kSteps - 1; ++x) next_bits[x] = next_bits[x + 1];
+            next_bits[St::kSteps - 2] = far < k1 ? ask(far, to) : 0u;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            asm volatile("cp.async.wait_group %0;" ::"n"(St::kSteps - 1) : "memory");
+            __syncwarp();
+            stage = stage == St::kSteps - 1 ? 0 : stage + 1;
+            if (bits == 0) continue;
+#pragma unroll
+            for (int nb = 0; nb < 2 * KB; ++nb)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(step + St::key_at(8 * nb + g, t + 4 * u));
+                    k[nb][u][0] = x.x, k[nb][u][1] = x.y, k[nb][u][2] = x.z, k[nb][u][3] = x.w;
+                }
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int j = 16 * kb + 2 * t + (x & 1) + 8 * (x >> 1);
+                    const uint8_t* row = step + St::kRows;
+                    if (HD == 128) {
+                        const uint4 y = *reinterpret_cast<const uint4*>(row + St::value_at(j, g));
+                        v[kb][x][0] = y.x, v[kb][x][1] = y.y;
+                        v[kb][x][VW > 2 ? 2 : 0] = VW > 2 ? y.z : y.x;
+                        v[kb][x][VW > 2 ? 3 : 1] = VW > 2 ? y.w : y.y;
+                    } else {
+                        const uint2 y = *reinterpret_cast<const uint2*>(row + St::value_at(j, g >> 1) + 8 * (g & 1));
+                        v[kb][x][0] = y.x, v[kb][x][1] = y.y;
+                    }
+                }
+#pragma unroll
+            for (int nb = 0; nb < 2 * KB; ++nb) {
+                const float* s = reinterpret_cast<const float*>(step + 2 * St::kRows) + 8 * nb + 2 * t;
+                const float2 x = *reinterpret_cast<const float2*>(s), y = *reinterpret_cast<const float2*>(s + 32);
+                ks[2 * nb] = x.x, ks[2 * nb + 1] = x.y;
+                lv[2 * nb] = bits >> (8 * nb + 2 * t) & 1u ? y.x : 1.f;
+                lv[2 * nb + 1] = bits >> (8 * nb + 2 * t + 1) & 1u ? y.y : 1.f;
             }
+        } else {
+            // pages of each 8 of these keys (which none of them leaves), and what counts
+            int page[2 * KB];
+#pragma unroll
+            for (int nb = 0; nb < 2 * KB; ++nb) {
+                const int at = key + 8 * nb;
+                page[nb] = at < k1 ? c.page_of(b, at) : -1;
+                if (page[nb] >= 0) bits |= (at + 8 <= k1 ? 255u : (1u << (k1 - at)) - 1u) << (8 * nb);
+            }
+            if (bits == 0) continue;
+#pragma unroll
+            for (int nb = 0; nb < 2 * KB; ++nb) {
+                const int j = 8 * nb + g;
+                const bool on = (bits >> j) & 1u;
+                const uint8_t* p = kp + page[nb] * c.k.page + c.slot_of(key + j) * c.k.token;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    ld16(p + 16 * (t + 4 * u), on && PIECE * (t + 4 * u) < a.d, k[nb][u]);
+            }
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int j = 16 * kb + 2 * t + (x & 1) + 8 * (x >> 1);
+                    const bool on = (bits >> j) & 1u;
+                    const uint8_t* p = vp + page[2 * kb + (x >> 1)] * c.v.page + c.slot_of(key + j) * c.v.token;
+#pragma unroll
+                    for (int w = 0; w < (Q8 ? 0 : HD / 64); ++w)
+                        ld16(p + 16 * g + 128 * w, on && 8 * g + 64 * w < a.d, v[kb][x] + 4 * w);
+                }
         }
         float s[RP][2 * KB][4];
 #pragma unroll
@@ -421,6 +533,10 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
     }
 
     // each warp's rows, then their join
+    if (Q8) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         sum[rb] += __shfl_xor_sync(0xffffffffu, sum[rb], 1);
@@ -432,7 +548,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
 #pragma unroll
         for (int w = 0; w < NT; ++w) {
             const int col = Q8 ? HD / 8 * g + 2 * w : 8 * (g + 8 * (w >> 2)) + 2 * (w & 3);
-            float* p = sO + (size_t)(warp * ROWS + 8 * rb + 2 * t) * HD + col;
+            float* p = sO + warp * kWarpRows + (8 * rb + 2 * t) * HD + col;
             *reinterpret_cast<float2*>(p) = make_float2(o[rb][w][0], o[rb][w][2]);
             *reinterpret_cast<float2*>(p + HD) = make_float2(o[rb][w][1], o[rb][w][3]);
         }
@@ -467,7 +583,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
         for (int e = lane; e < P.dp; e += 32) {
             float x = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) x = fmaf(f[w], sO[(size_t)(w * ROWS + row) * HD + e], x);
+            for (int w = 0; w < kWarps; ++w) x = fmaf(f[w], sO[w * kWarpRows + row * HD + e], x);
             x = total == 0.f ? 0.f : x * inv;
             if (P.splits > 1)
                 part[e] = x;
@@ -499,7 +615,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
     // then a thread sums four elements of a row over them.
     constexpr int kSome = 256;
     constexpr int kQuads = HD / 4, kSums = ROWS * kQuads / (32 * kWarps);
-    static_assert(ROWS * kSome <= kWarps * ROWS * HD, "weights fit over the rows");
+    static_assert(ROWS * kSome <= kWarps * kWarpRows, "weights fit over the rows");
     float top[ROWS / kWarps], total[ROWS / kWarps];
 #pragma unroll
     for (int x = 0; x < ROWS / kWarps; ++x) {
@@ -577,10 +693,10 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
 template <int HD, int HELD, bool BF, int RB>
 cudaError_t launch(const FewArgs& p, cudaStream_t s) {
     static std::atomic<uint64_t> ready{0};    // devices whose shared-memory limit is raised
-    if (cudaError_t e = raise_smem(k_tree_few<HD, HELD, BF, RB>, kFewSmem<HD, RB>, ready); e != cudaSuccess)
+    if (cudaError_t e = raise_smem(k_tree_few<HD, HELD, BF, RB>, kFewSmem<HD, HELD, RB>, ready); e != cudaSuccess)
         return e;
     const unsigned blocks = (unsigned)((int64_t)p.a.c.B * p.a.c.G * p.groups * p.splits);
-    k_tree_few<HD, HELD, BF, RB><<<blocks, 32 * kWarps, kFewSmem<HD, RB>, s>>>(p);
+    k_tree_few<HD, HELD, BF, RB><<<blocks, 32 * kWarps, kFewSmem<HD, HELD, RB>, s>>>(p);
     count_launch();
     return cudaGetLastError();
 }
@@ -591,7 +707,7 @@ cudaError_t resident(int* blocks) {
     *blocks = held.load();
     if (*blocks > 0) return cudaSuccess;
     const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, k_tree_few<HD, HELD, BF, RB>,
-                                                                        32 * kWarps, kFewSmem<HD, RB>);
+                                                                        32 * kWarps, kFewSmem<HD, HELD, RB>);
     if (e == cudaSuccess) held.store(*blocks);
     return e;
 }

@@ -210,7 +210,10 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& P, const Share& w, uint
     constexpr int kSlots = C::Q8 ? C::kRaw : C::kRing;
     const Args& a = P.a;
     const int lane = threadIdx.x & 31;
-    const int rows = min(kKeys, 1 << a.c.log_page);            // of a copy
+    // A lane to each copy: rows of a page, 64 elements wide (16 bits), or scales.  One lane for
+    // all of them took 700 cycles a tile with pages of 64 and their scales, 1500 with pages of 16.
+    const int rows = min(kKeys, 1 << a.c.log_page), copies = kKeys / rows;
+    const int piece = lane & (copies - 1), part = lane / copies;
     const CUtensorMap* const map = KV ? &P.v : &P.k;
     const auto load_entry = [&](int j) {
         // of the tile's keys 8 (lane & 7) on
@@ -220,6 +223,10 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& P, const Share& w, uint
             asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(x) : "l"(a.c.table + w.b * a.c.table_stride + i));
         return x;
     };
+    const kv::Pool& scaled = part == 0 ? a.c.k : a.c.v;
+    const float* scale = scaled.scale + w.kh * scaled.s_head;
+    const int64_t s_page = scaled.s_page;
+    const uint32_t first_of = rows == 64 ? 1u : rows == 32 ? 0x11u : rows == 16 ? 0x55u : 0xffu;
     int entry = load_entry(0), entry2 = load_entry(1), bits = 0, asked = 0;
     const int mixed_from = w.mixed_from();
     Ring r;
@@ -243,45 +250,38 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& P, const Share& w, uint
                                                                        : &bar.full[KV][r.slot];
         uint32_t bytes = C::Q8 ? C::kRawBytes : C::kSlotBytes;
         if (KV == 0) {
-            // keys that count, 8 to a lane
-            const int left = w.end - key;
-            const uint32_t byte = !on ? 0u : left >= 8 ? 255u : (1u << left) - 1u;
-            const uint32_t lo = __reduce_or_sync(0xffffffffu, lane < 4 ? byte << (8 * lane) : 0u);
-            const uint32_t hi = __reduce_or_sync(0xffffffffu, lane >= 4 && lane < 8 ? byte << (8 * (lane - 4)) : 0u);
+            // keys that count: a bit for each 8, spread; the last of them may end among their 8
+            uint32_t lo = ((pages & 15u) * 0x00204081u & 0x01010101u) * 255u;
+            uint32_t hi = ((pages >> 4) * 0x00204081u & 0x01010101u) * 255u;
+            const int left = w.end - key0;
+            if (left < 32) lo &= (1u << left) - 1u;
+            if (left < 64) hi &= left <= 32 ? 0u : (1u << (left - 32)) - 1u;
             if (lane == 0)
                 *reinterpret_cast<uint2*>(reinterpret_cast<TileBits*>(smem + M::bits)[bits].counted) =
                     make_uint2(lo, hi);
             // scales, only where there is a page
-            if (C::Q8)
-                for (int c = 0; c < kKeys; c += rows) bytes += (pages >> (c >> 3) & 1) * 2 * 4 * rows;
+            if (C::Q8) bytes += 2 * 4 * rows * __popc(pages & first_of);
             if (++bits == C::kBits) bits = 0;
         }
+        const int pg = __shfl_sync(0xffffffffu, page, piece * rows >> 3);
+        const int slot = a.c.slot_of(key0 + piece * rows);
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
         __syncwarp();
-        if (elect_one()) mbar_arrive_expect_tx(full, bytes);
-        __syncwarp();
-        for (int c = 0; c < kKeys; c += rows) {
-            const int pg = __shfl_sync(0xffffffffu, page, c >> 3);
-            const int slot = a.c.slot_of(key0 + c);
-            if (elect_one()) {
-                if (C::Q8) {
-                    tma_load(smem + M::raw + (KV * C::kRaw + r.slot) * C::kRawBytes + c * HD, map, 0, slot, w.kh,
-                             pg, full);
-                    if (KV == 0 && (pages >> (c >> 3) & 1)) {
-                        float* s = reinterpret_cast<float*>(smem + M::raw_scale) + r.slot * 2 * kKeys + c;
-                        const kv::Pool &pk = a.c.k, &pv = a.c.v;
-                        bulk_g2s(s, pk.scale + pg * pk.s_page + w.kh * pk.s_head + slot, 4 * rows, full);
-                        bulk_g2s(s + kKeys, pv.scale + pg * pv.s_page + w.kh * pv.s_head + slot, 4 * rows, full);
-                    }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < C::kChunks; ++x)
-                        tma_load(smem + M::ring + (KV * C::kRing + r.slot) * C::kSlotBytes + x * C::kChunkBytes +
-                                     c * 128,
-                                 map, 64 * x, slot, w.kh, pg, full);
-                }
+        if (C::Q8) {
+            if (part == 0)
+                tma_load(smem + M::raw + (KV * C::kRaw + r.slot) * C::kRawBytes + piece * rows * HD, map, 0, slot,
+                         w.kh, pg, full);
+            if (KV == 0 && part < 2 && pages >> (piece * rows >> 3) & 1) {
+                float* s = reinterpret_cast<float*>(smem + M::raw_scale) + r.slot * 2 * kKeys + part * kKeys +
+                           piece * rows;
+                bulk_g2s(s, scale + pg * s_page + slot, 4 * rows, full);
             }
-            __syncwarp();
+        } else if (part < C::kChunks) {
+            tma_load(smem + M::ring + (KV * C::kRing + r.slot) * C::kSlotBytes + part * C::kChunkBytes +
+                         piece * rows * 128,
+                     map, 64 * part, slot, w.kh, pg, full);
         }
+        __syncwarp();
         r.step(1, kSlots);
     }
     if (w.nt <= kSlots) __syncthreads();
@@ -358,10 +358,10 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
             const bool scaled = KV == 0 && tid < kKeys;
             if (scaled) {
                 const float* s = reinterpret_cast<const float*>(smem + M::raw_scale) + from.slot * 2 * kKeys + tid;
-                if (tb.counted[tid >> 5] >> (tid & 31) & 1u) {
-                    ks = s[0];
-                    vs = s[kKeys];
-                }
+                const float k0 = s[0], v0 = s[kKeys];          // (anything where there is no page)
+                const bool on = tb.counted[tid >> 5] >> (tid & 31) & 1u;
+                ks = on ? k0 : 0.f;
+                vs = on ? v0 : 0.f;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.free_raw[KV][from.slot]);

@@ -24,6 +24,7 @@ struct RowsArgs {
 };
 
 constexpr int kThreads = 256;
+constexpr int kHeads = 4;       // heads of a token that a thread takes pieces of
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
@@ -95,40 +96,53 @@ __device__ __forceinline__ uint2 quantise(const uint4& x, float& scale) {
     return make_uint2(w[0], w[1]);
 }
 
+// A token's keys and values of up to kHeads heads to LANES lanes: one look at its page, and
+// all their loads under way together.
+struct Item {
+    int b, t, h0, heads;       // heads 0: none
+};
+template <int LANES>
+__device__ __forceinline__ Item item_of(const RowsArgs& P, unsigned items) {
+    constexpr unsigned kItems = kThreads / LANES;
+    const unsigned groups = (unsigned)(P.c.G + kHeads - 1) / kHeads;
+    const unsigned i = blockIdx.x * kItems + threadIdx.x / LANES;
+    const unsigned tok = i / groups, b = tok / (unsigned)P.n;
+    const int h0 = (int)(i - tok * groups) * kHeads;
+    return {(int)b, (int)(tok - b * (unsigned)P.n), h0, i < items ? min(kHeads, P.c.G - h0) : 0};
+}
+
 template <typename T, int HELD, int LANES>
-__global__ void __launch_bounds__(kThreads) k_write(const __grid_constant__ RowsArgs P, int64_t rows) {
+__global__ void __launch_bounds__(kThreads) k_write(const __grid_constant__ RowsArgs P, unsigned items) {
     const Cache& c = P.c;
     const int lane = threadIdx.x % LANES;
-    constexpr int kRows = kThreads / LANES;
-    // rows (b, t, head, key or value), a block's together
-    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
-        const int64_t r = r0 + threadIdx.x / LANES;
-        int pos = -1, page = -1, b = 0, t = 0, h = 0;
-        bool value = false;
-        if (r < rows) {
-            value = r & 1;
-            const int64_t x = r >> 1;
-            const int64_t tok = x / c.G;
-            h = (int)(x - tok * c.G);
-            b = (int)(tok / P.n);
-            t = (int)(tok - (int64_t)b * P.n);
-            pos = __ldg(P.at + b * P.at_stride + t);
-            if (pos >= 0) page = c.page_of(b, pos);
-        }
-        uint4 x = make_uint4(0, 0, 0, 0);
-        const View& from = value ? P.v : P.k;
-        if (page >= 0)
-            x = load_piece(static_cast<const uint16_t*>(from.p) + b * from.sb + t * from.st + h * from.sh,
-                           8 * lane, c.d, P.vec);
-        const Pool& to = value ? c.v : c.k;
-        const int slot = c.slot_of(pos);
+    Item it = item_of<LANES>(P, items);
+    int pos = -1, page = -1;
+    if (it.heads > 0) pos = __ldg(P.at + it.b * P.at_stride + it.t);
+    if (pos >= 0) page = c.page_of(it.b, pos);
+    if (page < 0) it.heads = 0;
+    const int slot = c.slot_of(pos);
+    uint4 x[2 * kHeads];
+#pragma unroll
+    for (int i = 0; i < 2 * kHeads; ++i) {
+        const View& from = i & 1 ? P.v : P.k;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (i >> 1 < it.heads)
+            x[i] = load_piece(static_cast<const uint16_t*>(from.p) + it.b * from.sb + it.t * from.st +
+                                  (it.h0 + (i >> 1)) * from.sh,
+                              8 * lane, c.d, P.vec);
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * kHeads; ++i) {
+        const Pool& to = i & 1 ? c.v : c.k;
+        const int h = it.h0 + (i >> 1);
+        const bool on = i >> 1 < it.heads;
         uint8_t* row = to.p + page * to.page + h * to.head + slot * to.token;
         if (HELD == HELD_16) {
-            if (page >= 0 && 8 * lane < c.d) *reinterpret_cast<uint4*>(row + 16 * lane) = x;
+            if (on && 8 * lane < c.d) *reinterpret_cast<uint4*>(row + 16 * lane) = x[i];
         } else {
             float scale;
-            const uint2 q = quantise<T, HELD, LANES>(x, scale);
-            if (page >= 0) {
+            const uint2 q = quantise<T, HELD, LANES>(x[i], scale);
+            if (on) {
                 if (8 * lane < c.d) *reinterpret_cast<uint2*>(row + 8 * lane) = q;
                 if (lane == 0) to.scale[page * to.s_page + h * to.s_head + slot] = scale;
             }
@@ -148,52 +162,57 @@ __device__ __forceinline__ uint4 values(const uint2& q, float scale) {
 }
 
 template <typename T, int HELD, int LANES>
-__global__ void __launch_bounds__(kThreads) k_read(const __grid_constant__ RowsArgs P, int64_t rows) {
+__global__ void __launch_bounds__(kThreads) k_read(const __grid_constant__ RowsArgs P, unsigned items) {
     const Cache& c = P.c;
     const int lane = threadIdx.x % LANES;
-    constexpr int kRows = kThreads / LANES;
-    for (int64_t r0 = (int64_t)blockIdx.x * kRows; r0 < rows; r0 += (int64_t)gridDim.x * kRows) {
-        const int64_t r = r0 + threadIdx.x / LANES;
-        if (r >= rows || 8 * lane >= c.d) continue;
-        const bool value = r & 1;
-        const int64_t x = r >> 1;
-        const int64_t tok = x / c.G;
-        const int h = (int)(x - tok * c.G);
-        const int b = (int)(tok / P.n);
-        const int t = (int)(tok - (int64_t)b * P.n);
-        const int page = P.at == nullptr || t < __ldg(P.at + b) ? c.page_of(b, t) : -1;
-        uint4 y = make_uint4(0, 0, 0, 0);
-        if (page >= 0) {
-            const Pool& from = value ? c.v : c.k;
-            const int slot = c.slot_of(t);
-            const uint8_t* row = from.p + page * from.page + h * from.head + slot * from.token;
-            if (HELD == HELD_16) {
-                y = __ldg(reinterpret_cast<const uint4*>(row) + lane);
-            } else {
-                const float scale = __ldg(from.scale + page * from.s_page + h * from.s_head + slot);
-                y = values<T, HELD>(__ldg(reinterpret_cast<const uint2*>(row) + lane), scale);
-            }
+    const Item it = item_of<LANES>(P, items);
+    if (it.heads == 0 || 8 * lane >= c.d) return;
+    const int page = P.at == nullptr || it.t < __ldg(P.at + it.b) ? c.page_of(it.b, it.t) : -1;
+    const int slot = c.slot_of(it.t);
+    uint4 y[2 * kHeads];
+    float scale[2 * kHeads];
+#pragma unroll
+    for (int i = 0; i < 2 * kHeads; ++i) {
+        const Pool& from = i & 1 ? c.v : c.k;
+        const int h = it.h0 + (i >> 1);
+        y[i] = make_uint4(0, 0, 0, 0);
+        scale[i] = 0.f;
+        if (page < 0 || i >> 1 >= it.heads) continue;
+        const uint8_t* row = from.p + page * from.page + h * from.head + slot * from.token;
+        if (HELD == HELD_16) {
+            y[i] = __ldg(reinterpret_cast<const uint4*>(row) + lane);
+        } else {
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(row) + lane);
+            y[i].x = q.x;
+            y[i].y = q.y;
+            scale[i] = __ldg(from.scale + page * from.s_page + h * from.s_head + slot);
         }
-        const View& to = value ? P.v : P.k;
-        uint16_t* out = static_cast<uint16_t*>(to.p) + b * to.sb + t * to.st + h * to.sh + 8 * lane;
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * kHeads; ++i) {
+        if (i >> 1 >= it.heads) continue;
+        const View& to = i & 1 ? P.v : P.k;
+        // (a row without a page: zero codes by a zero scale)
+        const uint4 o = HELD == HELD_16 ? y[i] : values<T, HELD>(make_uint2(y[i].x, y[i].y), scale[i]);
+        uint16_t* out = static_cast<uint16_t*>(to.p) + it.b * to.sb + it.t * to.st + (it.h0 + (i >> 1)) * to.sh +
+                        8 * lane;
         if (P.vec) {
-            *reinterpret_cast<uint4*>(out) = y;
+            *reinterpret_cast<uint4*>(out) = o;
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) out[k] = (uint16_t)(word(y, k >> 1) >> (16 * (k & 1)));
+            for (int k = 0; k < 8; ++k) out[k] = (uint16_t)(word(o, k >> 1) >> (16 * (k & 1)));
         }
     }
 }
 
 template <typename T, int HELD, int LANES>
 cudaError_t launch(const RowsArgs& p, bool write, cudaStream_t s) {
-    const int64_t rows = 2 * (int64_t)p.c.B * p.n * p.c.G;
-    const int64_t blocks = (rows * LANES + kThreads - 1) / kThreads;
-    const unsigned grid = (unsigned)std::min<int64_t>(blocks, 1 << 30);
+    const int64_t items = (int64_t)p.c.B * p.n * ((p.c.G + kHeads - 1) / kHeads);     // below 2^31
+    const unsigned grid = (unsigned)((items * LANES + kThreads - 1) / kThreads);
     if (write)
-        k_write<T, HELD, LANES><<<grid, kThreads, 0, s>>>(p, rows);
+        k_write<T, HELD, LANES><<<grid, kThreads, 0, s>>>(p, (unsigned)items);
     else
-        k_read<T, HELD, LANES><<<grid, kThreads, 0, s>>>(p, rows);
+        k_read<T, HELD, LANES><<<grid, kThreads, 0, s>>>(p, (unsigned)items);
     count_launch();
     return cudaGetLastError();
 }

@@ -1,15 +1,17 @@
 // Rotary positions of queries and keys, and their gradient (the same turned back).
 //
-// Bound by memory: every element is read and written once.  A block takes a few tokens:
-// first the sines and cosines of each into shared memory, where all their heads find
-// them, then the heads, 16 bytes an access.
+// Bound by memory: every element is read and written once.  A block takes up to 8 tokens:
+// first the frequencies, then the sines and cosines of each token into shared memory, where
+// all their heads find them, then the heads, 16 bytes an access.
 //
 // Angles.  A frequency is kept as a 64-bit fraction of a turn, F = frac(w / 2 pi) 2^64, so
 // that a position's angle is the low 64 bits of p F: whole turns fall away by themselves,
-// with no reduction and no double arithmetic per token, and a position of 2^31 is off by
+// with no reduction and no double arithmetic per token (5 operations of a type that this GPU
+// has next to no units for), and a position of 2^31 is off by
 // the rounding of w alone (2^-22 turns; float32 angles would be off by many).
 #include "fs_attn_host.cuh"
 
+#include <algorithm>
 #include <cmath>
 
 namespace fs {
@@ -19,7 +21,8 @@ namespace {
 
 using attn::View;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kTokens = 8;             // most tokens of a block
 constexpr int kMaxRotary = 512;
 
 struct Args {
@@ -51,17 +54,31 @@ __device__ __forceinline__ uint32_t pack(float x, float y) {
 template <typename T, bool PAIRS>
 __global__ void __launch_bounds__(kThreads) k_rotary(const __grid_constant__ Args P) {
     extern __shared__ float2 turn[];         // [tokens][half] amplitude (cos, sin)
+    __shared__ uint64_t step[kMaxRotary / 2];
+    __shared__ int32_t place[kTokens];
+    __shared__ int64_t at[kTokens][4];       // where a token's queries and keys begin: input, output
     const int64_t all = (int64_t)P.B * P.n;
     const int64_t first = (int64_t)blockIdx.x * P.tokens;
     const int count = (int)min((int64_t)P.tokens, all - first);
+    for (int i = threadIdx.x; i < P.half; i += kThreads) {
+        const double turns = __ldg(P.freqs + i) * 0.15915494309189533577;     // 1 / (2 pi)
+        step[i] = __double2ull_rz((turns - floor(turns)) * 0x1p64);
+    }
+    if (threadIdx.x < count) {
+        const unsigned tok = (unsigned)(first + threadIdx.x), b = tok / (unsigned)P.n;
+        const int64_t i = tok - b * (unsigned)P.n;
+        place[threadIdx.x] = __ldg(P.pos + b * P.pos_b + i * P.pos_t);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            at[threadIdx.x][k] = b * P.x[k].sb + i * P.x[k].st;
+            at[threadIdx.x][2 + k] = b * P.y[k].sb + i * P.y[k].st;
+        }
+    }
+    __syncthreads();
     for (int e = threadIdx.x; e < count * P.half; e += kThreads) {
         const int t = e / P.half, i = e - t * P.half;
-        const int64_t tok = first + t;
-        const int b = (int)(tok / P.n);
-        const int64_t p = __ldg(P.pos + b * P.pos_b + (tok - (int64_t)b * P.n) * P.pos_t);
-        const double turns = __ldg(P.freqs + i) * 0.15915494309189533577;     // 1 / (2 pi)
-        const uint64_t f = __double2ull_rz((turns - floor(turns)) * 0x1p64);
-        const int32_t top = (int32_t)(((uint64_t)p * f) >> 32);
+        const int64_t p = place[t];
+        const int32_t top = (int32_t)(((uint64_t)p * step[i]) >> 32);
         float sn, cs;
         sincospif((float)top * 0x1p-31f, &sn, &cs);
         turn[e] = make_float2(P.amplitude * cs, P.amplitude * (P.back ? -sn : sn));
@@ -69,53 +86,59 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const __grid_constant__ Arg
     __syncthreads();
     const int heads = P.heads[0] + P.heads[1];
     if (P.vec) {
-        // units of a head: the turned ones (8 elements, or 8 of each half), then copies of 8
+        // Units of a head: the turned ones (8 elements, or 8 of each half), then copies of 8.  A
+        // thread takes one of a head for kUnits tokens at a time, whose loads are under way together.
+        constexpr int kUnits = 4;
         const int turned = PAIRS ? P.half / 4 : P.half / 8;
         const int units = turned + (P.d - 2 * P.half) / 8;
-        for (int e = threadIdx.x; e < count * heads * units; e += kThreads) {
-            const int row = e / units, u = e - row * units;
-            const int t = row / heads;
-            int h = row - t * heads;
-            const int64_t tok = first + t;
-            const int b = (int)(tok / P.n);
-            const int64_t i = tok - (int64_t)b * P.n;
+        for (int e = threadIdx.x; e < heads * units; e += kThreads) {
+            int h = e / units;
+            const int u = e - h * units;
             const int which = h >= P.heads[0];
             if (which) h -= P.heads[0];
-            const View &from = P.x[which], &to = P.y[which];
-            const uint16_t* src = static_cast<const uint16_t*>(from.p) + b * from.sb + i * from.st + h * from.sh;
-            uint16_t* dst = static_cast<uint16_t*>(to.p) + b * to.sb + i * to.st + h * to.sh;
-            if (u >= turned) {
-                const int c = 2 * P.half + 8 * (u - turned);
-                *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
-                continue;
-            }
-            const float2* w = turn + t * P.half;
-            if (PAIRS) {
-                const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * u);
-                uint32_t o[4] = {x.x, x.y, x.z, x.w};
+            const bool turns = u < turned;
+            const int c = turns ? 8 * u : 2 * P.half + 8 * (u - turned);
+            const uint16_t* src = static_cast<const uint16_t*>(P.x[which].p) + h * P.x[which].sh + c;
+            uint16_t* dst = static_cast<uint16_t*>(P.y[which].p) + h * P.y[which].sh + c;
+            const float2* w = turn + (PAIRS ? 4 * u : 8 * u);
+            for (int t0 = 0; t0 < count; t0 += kUnits) {
+                uint4 x[kUnits], y[kUnits];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float a, c;
-                    unpack<T>(o[k], a, c);
-                    const float2 z = w[4 * u + k];
-                    o[k] = pack<T>(a * z.x - c * z.y, a * z.y + c * z.x);
+                for (int i = 0; i < kUnits; ++i) {
+                    if (t0 + i >= count) break;
+                    const uint16_t* p = src + at[t0 + i][which];
+                    x[i] = *reinterpret_cast<const uint4*>(p);
+                    if (!PAIRS && turns) y[i] = *reinterpret_cast<const uint4*>(p + P.half);
                 }
-                *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(o[0], o[1], o[2], o[3]);
-            } else {
-                const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * u);
-                const uint4 y = *reinterpret_cast<const uint4*>(src + P.half + 8 * u);
-                uint32_t o[4] = {x.x, x.y, x.z, x.w}, r[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float a0, a1, c0, c1;
-                    unpack<T>(o[k], a0, a1);
-                    unpack<T>(r[k], c0, c1);
-                    const float4 z = reinterpret_cast<const float4*>(w + 8 * u)[k];
-                    o[k] = pack<T>(a0 * z.x - c0 * z.y, a1 * z.z - c1 * z.w);
-                    r[k] = pack<T>(a0 * z.y + c0 * z.x, a1 * z.w + c1 * z.z);
+                for (int i = 0; i < kUnits; ++i) {
+                    if (t0 + i >= count) break;
+                    uint16_t* to = dst + at[t0 + i][2 + which];
+                    const float2* z0 = w + (t0 + i) * P.half;
+                    uint32_t o[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    if (turns && PAIRS) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float a, c1;
+                            unpack<T>(o[k], a, c1);
+                            const float2 z = z0[k];
+                            o[k] = pack<T>(a * z.x - c1 * z.y, a * z.y + c1 * z.x);
+                        }
+                    } else if (turns) {
+                        uint32_t r[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float a0, a1, c0, c1;
+                            unpack<T>(o[k], a0, a1);
+                            unpack<T>(r[k], c0, c1);
+                            const float4 z = reinterpret_cast<const float4*>(z0)[k];
+                            o[k] = pack<T>(a0 * z.x - c0 * z.y, a1 * z.z - c1 * z.w);
+                            r[k] = pack<T>(a0 * z.y + c0 * z.x, a1 * z.w + c1 * z.z);
+                        }
+                        *reinterpret_cast<uint4*>(to + P.half) = make_uint4(r[0], r[1], r[2], r[3]);
+                    }
+                    *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
-                *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(dst + P.half + 8 * u) = make_uint4(r[0], r[1], r[2], r[3]);
             }
         }
         return;
@@ -126,14 +149,10 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const __grid_constant__ Arg
         const int row = e / units, u = e - row * units;
         const int t = row / heads;
         int h = row - t * heads;
-        const int64_t tok = first + t;
-        const int b = (int)(tok / P.n);
-        const int64_t i = tok - (int64_t)b * P.n;
         const int which = h >= P.heads[0];
         if (which) h -= P.heads[0];
-        const View &from = P.x[which], &to = P.y[which];
-        const T* src = static_cast<const T*>(from.p) + b * from.sb + i * from.st + h * from.sh;
-        T* dst = static_cast<T*>(to.p) + b * to.sb + i * to.st + h * to.sh;
+        const T* src = static_cast<const T*>(P.x[which].p) + at[t][which] + h * P.x[which].sh;
+        T* dst = static_cast<T*>(P.y[which].p) + at[t][2 + which] + h * P.y[which].sh;
         if (u >= P.half) {
             dst[P.half + u] = src[P.half + u];
             continue;
@@ -212,7 +231,8 @@ fs_status rotary_entry(const fs_rotation* r, const void* q, const void* k, void*
     for (int w = 0; w < (r->kv_heads ? 2 : 1); ++w)
         p.vec = p.vec && attn::aligned16(p.x[w], p.B, p.n, p.heads[w]) &&
                 attn::aligned16(p.y[w], p.B, p.n, p.heads[w]);
-    p.tokens = tokens >= 4096 ? 4 : 1;
+    // the frequencies of a block's tokens are brought into shape once: as many as leave the GPU full
+    p.tokens = (int)std::min<int64_t>(kTokens, std::max<int64_t>(1, tokens / 1024));
     NvtxRange range(back ? "fs_rotary_grad" : "fs_rotary");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     FS_CUDA(r->dtype == FS_DTYPE_BF16 ? launch<__nv_bfloat16>(p, r->interleaved, s)

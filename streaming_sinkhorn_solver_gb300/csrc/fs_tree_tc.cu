@@ -377,8 +377,14 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
                 kv::widen4<kHeld>(x[i].z, y[4], y[5]);
                 kv::widen4<kHeld>(x[i].w, y[6], y[7]);
                 const uint32_t at = slot + (u >> 2) * C::kChunkBytes;
-                sts16(at + swz_offset(row, (u & 3) * 16), y[0], y[1], y[2], y[3]);
-                sts16(at + swz_offset(row, (u & 3) * 16 + 8), y[4], y[5], y[6], y[7]);
+                // the second 64 elements' lanes store their halves the other way round: the same
+                // units of both chunks are in the same banks
+                const bool turn = HD == 128 && u >= 4;
+                const int e = (u & 3) * 16 + (turn ? 8 : 0);
+                sts16(at + swz_offset(row, e), turn ? y[4] : y[0], turn ? y[5] : y[1], turn ? y[6] : y[2],
+                      turn ? y[7] : y[3]);
+                sts16(at + swz_offset(row, e ^ 8), turn ? y[0] : y[4], turn ? y[1] : y[5], turn ? y[2] : y[6],
+                      turn ? y[3] : y[7]);
             }
             if (scaled) {
                 TileScales& ts = reinterpret_cast<TileScales*>(smem + M::scales)[scales];

@@ -247,6 +247,13 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
             asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(e) : "l"(c.table + b * c.table_stride + i));
         return e;
     };
+    constexpr int kUnits = HD / 16, kStep = 32 / kUnits;      // of a row; rows of an access
+    const int unit = lane % kUnits;
+    const bool whole = c.vec16 && a.d == HD;
+    const int64_t k_off = (lane / kUnits) * c.k.token + 16 * unit, k_far = kStep * c.k.token;
+    const int64_t v_off = (lane / kUnits) * c.v.token + 16 * unit, v_far = kStep * c.v.token;
+    const float* k_scale = c.k.scale + kh * c.k.s_head;
+    const float* v_scale = c.v.scale + kh * c.v.s_head;
     const auto ask = [&](int key, int stage) -> uint32_t {
         const uint32_t to = ring + stage * St::kBytes;
         const int left = k1 - (key + 8 * (lane & 3));
@@ -255,9 +262,32 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
         entry = load_entry(key + KEYS * kWarps);
         uint32_t bits = on && lane < 4 ? (left >= 8 ? 255u : (1u << left) - 1u) << (8 * lane) : 0u;
         bits = __reduce_or_sync(0xffffffffu, bits);
-        constexpr int kUnits = HD / 16, kStep = 32 / kUnits;      // rows of an access
-        const int u = lane % kUnits;
+        if (bits == 0xffffffffu && whole) {
+            // All of them, in whole pieces: where each 8 begin comes from the lane that has their page.
+            // (The general case below takes 25 instructions a copy; the kernel was bound by them.)
+            const int slot0 = c.slot_of(key + 8 * (lane & 3));
+            const uint8_t* kb = kp + held * c.k.page + slot0 * c.k.token;
+            const uint8_t* vb = vp + held * c.v.page + slot0 * c.v.token;
 #pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint8_t* ks = reinterpret_cast<const uint8_t*>(
+                                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(kb), x)) + k_off;
+                const uint8_t* vs = reinterpret_cast<const uint8_t*>(
+                                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vb), x)) + v_off;
+#pragma unroll
+                for (int y = 0; y < 8 / kStep; ++y) {
+                    const int r = 8 * x + y * kStep + lane / kUnits;
+                    cp16(to + St::key_at(r, unit), ks + (y ? k_far : 0), true);
+                    cp16(to + St::kRows + St::value_at(r, unit), vs + (y ? v_far : 0), true);
+                }
+            }
+            const int pg = __shfl_sync(0xffffffffu, held, lane >> 3), slot = c.slot_of(key + lane);
+            cp4(to + 2 * St::kRows + 4 * lane, k_scale + pg * c.k.s_page + slot, true);
+            cp4(to + 2 * St::kRows + 4 * (32 + lane), v_scale + pg * c.v.s_page + slot, true);
+            return bits;
+        }
+        const int u = unit;
+#pragma unroll 1
         for (int i = 0; i < 32 / kStep; ++i) {
             const int pg = __shfl_sync(0xffffffffu, held, i * kStep / 8), r = i * kStep + lane / kUnits;
             const bool there = bits >> r & 1u;

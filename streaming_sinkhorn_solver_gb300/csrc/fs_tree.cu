@@ -9,17 +9,19 @@ namespace tree {
 namespace {
 
 // Splits of the keys of the few-row kernel.  A split costs its keys and a fixed part
-// (set-up, its share of the join) worth about 512 keys of 16 bits; blocks beyond the
-// resident ones wait for a whole turn.  The fewest splits of the least cost.
-int choose_few_splits(int64_t blocks, int m, int64_t resident) {
-    constexpr double kFixedKeys = 512.0;
+// (set-up, its share of the join) worth about 512 keys of 16 bits, 256 of 8; blocks beyond the
+// resident ones come as others end, between whole turns (sequences of one length) and none.  The
+// fewest splits of the least cost.
+int choose_few_splits(int64_t blocks, int m, int64_t resident, bool bytes) {
+    const double fixed = bytes ? 256.0 : 512.0;
     if (blocks > kCounters) return 1;
     const int64_t most = std::min<int64_t>((m + kFewKeys - 1) / kFewKeys, 4 * resident / blocks + 1);
     int best = 1;
     double least = 0.0;
     for (int64_t s = 1; s <= most; ++s) {
-        const double turns = (double)((blocks * s + resident - 1) / resident);
-        const double cost = turns * ((double)m / (double)s + kFixedKeys);
+        const double full = (double)(blocks * s) / (double)resident;
+        const double turns = full <= 1.0 ? 1.0 : 0.5 * (std::ceil(full) + full + 0.5);
+        const double cost = turns * ((double)m / (double)s + fixed);
         if (s == 1 || cost < 0.999 * least) {
             least = cost;
             best = (int)s;
@@ -106,7 +108,8 @@ fs_status tree_entry(const fs_cache* cache, const fs_tree* t, const void* q, voi
         p.row_blocks = per_head <= 8 ? 1 : 2;
         p.groups = (per_head + 8 * p.row_blocks - 1) / (8 * p.row_blocks);
         FS_CUDA(few_resident(a, p.row_blocks, &resident));
-        splits = choose_few_splits(B * a.c.G * p.groups, a.c.reach(), (int64_t)sms * resident);
+        splits = choose_few_splits(B * a.c.G * p.groups, a.c.reach(), (int64_t)sms * resident,
+                                   a.c.held != kv::HELD_16);
     } else {
         tc.groups = (per_head + 255) / 256;
         tc.o_vec = attn::aligned16(a.o, a.c.B, a.n, a.H);

@@ -5,7 +5,8 @@ Pairs of ordered point clouds (two noisy turns of a helix) are matched with
 queries are the points of one cloud, its keys and values those of the other, which has
 another length in every pair, and a learned bias by relative position knows that the
 clouds are ordered.  Training takes `fs_cross_attention` with its gradients; answering
-keeps the keys and values and asks for one point at a time.
+keeps the keys and values and asks for one point at a time, also from a cache in pages that
+holds them in 8 bits.
 
     python examples/distill_plan.py [--steps 300]
 """
@@ -96,6 +97,18 @@ class Model(torch.nn.Module):
         return self.o(CrossAttention.apply(q, k, v, self.bias.to(TYPE), how).flatten(-2).float())
 
 
+def held(k, v, lens, dtype=torch.float8_e4m3fn, page=16):
+    """The keys and values as a cache of `dtype` gives them back: what a server that holds
+    many clouds keeps of each, in half the memory."""
+    batch, m = k.shape[:2]
+    per = -(-m // page)
+    cache = fs.fs_cache_new(batch * per, KEY_HEADS, page, D, dtype)
+    table = torch.arange(batch * per, dtype=torch.int32, device="cuda").view(batch, per)
+    at = torch.arange(m, dtype=torch.int32, device="cuda").expand(batch, m)
+    fs.fs_cache_write(cache, table, torch.where(at < lens[:, None], at, -1), k, v)
+    return fs.fs_cache_read(cache, table, lens, m, dtype=k.dtype)
+
+
 def main(steps=300, batch=4, n=96, m=192, eps=0.05, report=True):
     """Trains and answers; returns the first loss, the last, and how far the answers of
     single points are from those of whole clouds."""
@@ -122,10 +135,12 @@ def main(steps=300, batch=4, n=96, m=192, eps=0.05, report=True):
             first = torch.full((batch,), i, dtype=torch.int32, device="cuda")
             answers.append(model.attend(model.queries(x[:, i:i + 1]), k, v, lens, first))
         apart = float((torch.cat(answers, 1) - whole).abs().max())
+        eight = model.attend(model.queries(x), *held(k, v, lens), lens)
     fs.fs_check()
     if report:
         print(f"loss {float(losses[0]):.5f} -> {float(losses[-1]):.5f}; "
-              f"one point at a time differs by {apart:.2g} at most")
+              f"one point at a time differs by {apart:.2g} at most, keys and values in 8 bits by "
+              f"{float((eight - whole).abs().max()):.2g}")
     return float(losses[0]), float(losses[-1]), apart
 
 

@@ -572,6 +572,18 @@ def test_a_run_of_them_together():
     assert bool(torch.isfinite(out).all())
 
 
+def test_the_example_holds_its_keys_in_8_bits():
+    import examples.distill_plan as example
+    k, v = (torch.randn(3, 50, example.KEY_HEADS, example.D, generator=gen(30)).bfloat16().cuda()
+            for _ in range(2))
+    lens = torch.tensor([50, 17, 33], dtype=torch.int32, device="cuda")
+    for x, y in zip((k, v), example.held(k, v, lens)):
+        code, scale = quantise(x, E4M3)
+        want = (code.float() * scale[..., None]).bfloat16()
+        for b in range(3):
+            assert torch.equal(y[b, :lens[b]].cpu(), want[b, :lens[b]]) and not y[b, lens[b]:].any()
+
+
 def test_refusals():
     q, cache, table, k, v = setting(15, 2, 3, [20, 30], 4, 2, 64, BF, E4M3, 16)
     q, table = q.cuda(), table.cuda()

@@ -317,7 +317,7 @@ fs_status fill_cache(int dev, Cache& c, const fs_cache* a, bool write) {
     FS_TRY(check_ptr(dev, a->table, a->batch * a->table_pages, "the page table"));
     c.table = a->table;
     c.table_stride = a->table_stride;
-    c.table_pages = (int)a->table_pages;
+    c.table_pages = a->pages ? (int)a->table_pages : 0;        // (no page: no position has one)
     c.pages = (unsigned)a->pages;
     c.log_page = 0;
     while (1 << c.log_page < a->page_size) ++c.log_page;

@@ -50,8 +50,18 @@ int choose_tc_splits(int64_t blocks, int m, int sms) {
     return best;
 }
 
-// Rows of a key head from which the tensor-core kernel takes a call.
-constexpr int kFewRows = 16;
+// Whether the few-row kernel takes a call: up to one block of 8 rows to a key head, in 16 bits only
+// where there is little to read (as far as the table reaches), and caches whose rows cannot be
+// copied by the page.  Measured (few rows, tensor cores): 8 key heads of 128, one sequence of 2000
+// keys, 4 rows: 10 us, 15 us in either type; 38 of 8192 keys, 4 rows: e4m3 119 us, 169, bfloat16
+// 240, 186; 19 of 4096, bfloat16, 318 MB: 68, 54; 12 rows: e4m3 47, 49, bfloat16 67, 55.  Heads
+// of 64 in bfloat16 part at 235 MB, of 128 at 105.
+bool few_rows(const Args& a) {
+    constexpr double kLittle = 128e6;
+    if (!tc_copies(a.c)) return true;
+    if (a.R * a.n > 8) return false;
+    return a.c.held != kv::HELD_16 || 4.0 * a.c.B * a.c.G * a.c.reach() * a.d <= kLittle;
+}
 
 fs_status tree_entry(const fs_cache* cache, const fs_tree* t, const void* q, void* out, float* lse,
                      void* stream) {
@@ -100,12 +110,12 @@ fs_status tree_entry(const fs_cache* cache, const fs_tree* t, const void* q, voi
     int sms = 0;
     FS_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     const int per_head = a.R * a.n;
-    const bool few = per_head <= kFewRows || !tc_copies(a.c);
+    const bool few = few_rows(a);
     TcArgs tc = {};
     int splits;
     if (few) {
         int resident = 0;
-        p.row_blocks = per_head <= 8 ? 1 : 2;
+        p.row_blocks = per_head <= 8 || a.c.held == kv::HELD_16 ? 1 : 2;
         p.groups = (per_head + 8 * p.row_blocks - 1) / (8 * p.row_blocks);
         FS_CUDA(few_resident(a, p.row_blocks, &resident));
         splits = choose_few_splits(B * a.c.G * p.groups, a.c.reach(), (int64_t)sms * resident,

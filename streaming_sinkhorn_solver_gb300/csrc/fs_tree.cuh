@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t tree_window8(const uint32_t* words, bool the
     return __funnelshift_r(words[w], w + 1 < kTreeWords ? words[w + 1] : 0u, at & 31);
 }
 
-// Few rows: row_blocks of 8 rows to a block (1 or 2), in `groups`.
+// Few rows: row_blocks of 8 rows to a block (1; in 8 bits or 2), in `groups`.
 struct FewArgs {
     Args a;
     Partials part;

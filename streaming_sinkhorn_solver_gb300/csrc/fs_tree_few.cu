@@ -742,12 +742,13 @@ cudaError_t resident(int* blocks) {
     return e;
 }
 
-// the kernel of a call, for `f` to run
+// the kernel of a call, for `f` to run; 16 bits in blocks of 8 rows
 template <int HD, int HELD, typename F>
 cudaError_t pick_rows(const Args& a, int row_blocks, F f) {
+    constexpr int kMost = HELD == HELD_16 ? 1 : 2;
     if (a.bf16)
-        return row_blocks == 1 ? f.template run<HD, HELD, true, 1>() : f.template run<HD, HELD, true, 2>();
-    return row_blocks == 1 ? f.template run<HD, HELD, false, 1>() : f.template run<HD, HELD, false, 2>();
+        return row_blocks == 1 ? f.template run<HD, HELD, true, 1>() : f.template run<HD, HELD, true, kMost>();
+    return row_blocks == 1 ? f.template run<HD, HELD, false, 1>() : f.template run<HD, HELD, false, kMost>();
 }
 template <int HD, typename F>
 cudaError_t pick_held(const Args& a, int row_blocks, F f) {

@@ -290,6 +290,9 @@ SIZES = [   # B, n, ctx, H, G, d, page
     (2, 40, [130, 64], 8, 1, 128, 128),
     (1, 100, [63], 6, 2, 32, 16),
     (1, 256, [70], 4, 2, 48, 64),
+    (2, 9, [70, 33], 8, 2, 8, 16),
+    (1, 5, [100], 16, 1, 24, 8),
+    (1, 3, [1500], 8, 1, 64, 1024),
 ]
 
 
@@ -570,6 +573,31 @@ def test_a_run_of_them_together():
             assert torch.equal(y[b, :lens[b]].cpu(), (code.float() * scale[..., None]).bfloat16())
     out, _ = fs.fs_cross_attention(tq, *back, kv_len=torch.tensor(lens, dtype=torch.int32).cuda())
     assert bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("held", [BF, E4M3])
+def test_nothing_to_do(held):
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    table = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    cache = fs.fs_cache_new(4, 2, 16, 64, held)
+    q = torch.ones(2, 3, 4, 64, dtype=BF, device="cuda")
+    k = q[:, :, :2]
+    fs.fs_cache_write(cache, table, torch.zeros(2, 0, dtype=torch.int32, device="cuda"), k[:, :0], k[:, :0])
+    assert not cache.k.float().any()
+    a, _ = fs.fs_cache_read(cache, table, n=0)
+    assert a.shape == (2, 0, 2, 64)
+    out, lse = fs.fs_tree_attention(q[:, :0], cache, table, lens)
+    assert out.shape == (2, 0, 4, 64) and lse.shape == (2, 4, 0)
+    out, _ = fs.fs_tree_attention(q[:0], cache, table[:0], lens[:0])
+    assert out.shape == (0, 3, 4, 64)
+    # a pool without pages
+    none = fs.fs_cache_new(0, 2, 16, 64, held)
+    fs.fs_cache_write(none, table, torch.zeros(2, 3, dtype=torch.int32, device="cuda"), k, k)
+    a, _ = fs.fs_cache_read(none, table)
+    assert a.shape == (2, 48, 2, 64) and not a.any()
+    for n in (1, 3):
+        out, lse = fs.fs_tree_attention(q.repeat(1, 1, 4, 1)[:, :n], none, table, lens + 20)
+        assert not out.any() and bool((lse == -math.inf).all())
 
 
 def test_the_example_holds_its_keys_in_8_bits():

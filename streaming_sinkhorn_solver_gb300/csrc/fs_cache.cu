@@ -41,6 +41,13 @@ __device__ __forceinline__ uint32_t word(const uint4& x, int k) {
     return k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w;
 }
 
+template <typename T>
+__device__ __forceinline__ constexpr uint32_t infinity_bits();
+template <>
+__device__ __forceinline__ constexpr uint32_t infinity_bits<__half>() { return 0x7c00u; }
+template <>
+__device__ __forceinline__ constexpr uint32_t infinity_bits<__nv_bfloat16>() { return 0x7f80u; }
+
 // Elements 8 lane .. 8 lane + 7 of a token's row, zero from d on.
 __device__ __forceinline__ uint4 load_piece(const uint16_t* row, int c, int d, bool vec) {
     uint4 x = make_uint4(0, 0, 0, 0);
@@ -58,40 +65,36 @@ __device__ __forceinline__ uint4 load_piece(const uint16_t* row, int c, int d, b
     return x;
 }
 
-// The 8-bit codes of a piece, and the row's scale (in every lane of the row).
-template <typename T, int HELD, int LANES>
-__device__ __forceinline__ uint2 quantise(const uint4& x, float& scale) {
-    float f[8];
-    uint32_t top = 0;        // largest magnitude by its bits: above infinity's for a NaN
+// Largest magnitude of a row, in every one of its lanes, as 16 bits: those of a type's
+// magnitudes are ordered as they are, infinities and NaN at the end.
+template <int LANES>
+__device__ __forceinline__ uint32_t row_top(const uint4& x) {
+    uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                          __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        f[k] = elem<T>(word(x, k >> 1), k & 1);
-        top = max(top, __float_as_uint(f[k]) & 0x7fffffffu);
-    }
-#pragma unroll
-    for (int o = LANES / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool fine = top < 0x7f800000u;
-    const float amax = fmaxf(__uint_as_float(top), kLeastMax);
-    constexpr float kTop = HELD == HELD_E4M3 ? kTopE4m3 : kTopI8;
-    const float up = __fdiv_rn(kTop, amax);
-    scale = fine ? __fdiv_rn(amax, kTop) : __uint_as_float(0x7fc00000u);
+    for (int o = LANES / 2; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return max(m & 0xffffu, m >> 16);
+}
+
+// The 8-bit codes of a piece of a row that `up` brings to the type's range; not fine: zeros.
+template <typename T, int HELD>
+__device__ __forceinline__ uint2 codes(const uint4& x, float up, bool fine) {
     uint32_t w[2] = {0, 0};
-    if (fine) {
+    if (!fine) return make_uint2(0, 0);
 #pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-            const float a = __fmul_rn(f[k], up), b = __fmul_rn(f[k + 1], up);
-            uint32_t two;
-            if (HELD == HELD_E4M3) {
-                uint16_t h;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
-                two = h;
-            } else {
-                const int ia = min(max(__float2int_rn(a), -127), 127);
-                const int ib = min(max(__float2int_rn(b), -127), 127);
-                two = (uint32_t)(ia & 255) | (uint32_t)(ib & 255) << 8;
-            }
-            w[k >> 2] |= two << (8 * (k & 2));
+    for (int k = 0; k < 8; k += 2) {
+        const float a = __fmul_rn(elem<T>(word(x, k >> 1), 0), up), b = __fmul_rn(elem<T>(word(x, k >> 1), 1), up);
+        uint32_t two;
+        if (HELD == HELD_E4M3) {
+            uint16_t h;
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
+            two = h;
+        } else {
+            const int ia = min(max(__float2int_rn(a), -127), 127);
+            const int ib = min(max(__float2int_rn(b), -127), 127);
+            two = (uint32_t)(ia & 255) | (uint32_t)(ib & 255) << 8;
         }
+        w[k >> 2] |= two << (8 * (k & 2));
     }
     return make_uint2(w[0], w[1]);
 }
@@ -131,21 +134,46 @@ __global__ void __launch_bounds__(kThreads) k_write(const __grid_constant__ Rows
                                   (it.h0 + (i >> 1)) * from.sh,
                               8 * lane, c.d, P.vec);
     }
+    // The quotients of all rows, each by a lane of its own: top / amax by lane r (or 2 r) of row
+    // r, amax / top by the same (or 2 r + 1), which writes it.  (Every lane dividing for every row
+    // took a third of the kernel's instructions, and those its time.)
+    static_assert(2 * kHeads == 8 && (LANES == 8 || LANES == 16), "lanes of the quotients");
+    uint32_t top[2 * kHeads];
+    float up = 0.f, scale = 0.f;
+    if (HELD != HELD_16) {
+        uint32_t mine = 0;
+        const int r = LANES == 16 ? lane >> 1 : lane;
+#pragma unroll
+        for (int i = 0; i < 2 * kHeads; ++i) {
+            top[i] = row_top<LANES>(x[i]);
+            mine = i == r ? top[i] : mine;
+        }
+        constexpr float kTop = HELD == HELD_E4M3 ? kTopE4m3 : kTopI8;
+        const float amax = fmaxf(elem<T>(mine, 0), kLeastMax);
+        if (LANES == 16) {
+            up = scale = __fdiv_rn(lane & 1 ? amax : kTop, lane & 1 ? kTop : amax);
+        } else {
+            up = __fdiv_rn(kTop, amax);
+            scale = __fdiv_rn(amax, kTop);
+        }
+        const int h = it.h0 + (r >> 1);
+        const Pool& to = r & 1 ? c.v : c.k;
+        if ((LANES == 8 || lane & 1) && r >> 1 < it.heads)
+            to.scale[page * to.s_page + h * to.s_head + slot] =
+                mine < infinity_bits<T>() ? scale : __uint_as_float(0x7fc00000u);
+    }
 #pragma unroll
     for (int i = 0; i < 2 * kHeads; ++i) {
         const Pool& to = i & 1 ? c.v : c.k;
         const int h = it.h0 + (i >> 1);
-        const bool on = i >> 1 < it.heads;
+        const bool on = i >> 1 < it.heads && 8 * lane < c.d;
         uint8_t* row = to.p + page * to.page + h * to.head + slot * to.token;
         if (HELD == HELD_16) {
-            if (on && 8 * lane < c.d) *reinterpret_cast<uint4*>(row + 16 * lane) = x[i];
+            if (on) *reinterpret_cast<uint4*>(row + 16 * lane) = x[i];
         } else {
-            float scale;
-            const uint2 q = quantise<T, HELD, LANES>(x[i], scale);
-            if (on) {
-                if (8 * lane < c.d) *reinterpret_cast<uint2*>(row + 8 * lane) = q;
-                if (lane == 0) to.scale[page * to.s_page + h * to.s_head + slot] = scale;
-            }
+            const float by = __shfl_sync(0xffffffffu, up, LANES == 16 ? 2 * i : i, LANES);
+            const uint2 q = codes<T, HELD>(x[i], by, top[i] < infinity_bits<T>());
+            if (on) *reinterpret_cast<uint2*>(row + 8 * lane) = q;
         }
     }
 }

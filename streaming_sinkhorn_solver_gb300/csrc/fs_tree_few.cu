@@ -720,11 +720,17 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
     }
 }
 
+// Raises the kernel's limit of shared memory: before its first launch, and before it is asked how
+// many blocks an SM holds.
+template <int HD, int HELD, bool BF, int RB>
+cudaError_t ready() {
+    static std::atomic<uint64_t> raised{0};   // devices
+    return raise_smem(k_tree_few<HD, HELD, BF, RB>, kFewSmem<HD, HELD, RB>, raised);
+}
+
 template <int HD, int HELD, bool BF, int RB>
 cudaError_t launch(const FewArgs& p, cudaStream_t s) {
-    static std::atomic<uint64_t> ready{0};    // devices whose shared-memory limit is raised
-    if (cudaError_t e = raise_smem(k_tree_few<HD, HELD, BF, RB>, kFewSmem<HD, HELD, RB>, ready); e != cudaSuccess)
-        return e;
+    if (cudaError_t e = ready<HD, HELD, BF, RB>(); e != cudaSuccess) return e;
     const unsigned blocks = (unsigned)((int64_t)p.a.c.B * p.a.c.G * p.groups * p.splits);
     k_tree_few<HD, HELD, BF, RB><<<blocks, 32 * kWarps, kFewSmem<HD, HELD, RB>, s>>>(p);
     count_launch();
@@ -736,8 +742,10 @@ cudaError_t resident(int* blocks) {
     static std::atomic<int> held{0};
     *blocks = held.load();
     if (*blocks > 0) return cudaSuccess;
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, k_tree_few<HD, HELD, BF, RB>,
-                                                                        32 * kWarps, kFewSmem<HD, HELD, RB>);
+    cudaError_t e = ready<HD, HELD, BF, RB>();
+    if (e == cudaSuccess)
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, k_tree_few<HD, HELD, BF, RB>, 32 * kWarps,
+                                                          kFewSmem<HD, HELD, RB>);
     if (e == cudaSuccess) held.store(*blocks);
     return e;
 }

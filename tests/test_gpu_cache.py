@@ -575,6 +575,25 @@ def test_a_run_of_them_together():
     assert bool(torch.isfinite(out).all())
 
 
+def test_the_first_call_of_a_process_is_like_the_others():
+    """Results do not depend on what ran before: the first call splits its keys as later ones do."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from tests.test_gpu_cache import *
+for held, d in ((E4M3, 64), (I8, 128), (BF, 64)):
+    q, cache, table, k, v = setting(14, 2, 1, [700, 300], 8, 2, d, BF, held, 16)
+    ctx = torch.tensor([700, 300], dtype=torch.int32).cuda()
+    a, b = (fs.fs_tree_attention(q.cuda(), cache, table.cuda(), ctx) for _ in range(2))
+    assert all(torch.equal(x, y) for x, y in zip(a, b)), (held, d)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
 @pytest.mark.parametrize("held", [BF, E4M3])
 def test_nothing_to_do(held):
     lens = torch.zeros(2, dtype=torch.int32, device="cuda")

@@ -3,6 +3,11 @@
 // Both are bound by memory alone: a row (one token of one key head, keys or values) is
 // taken by 8 or 16 lanes, 16 bytes of 16-bit elements each, so that its largest
 // magnitude is a few shuffles and nothing is read twice.
+//
+// Measured, 8 sequences of 4096 tokens, 8 heads of 128, bfloat16 to e4m3 and back: 78 us for both,
+// 5.2 TB/s (0.77 of the measured copy rate); 5 x 777 float16 tokens of 4 heads of 80 to int8
+// and 5 x 9001 back: 33 us, 2.7 TB/s (10 of a row's 16 lanes have elements, and many rows are
+// zeros behind a sequence's end).
 #include "fs_kv.cuh"
 
 #include <cmath>

@@ -1,7 +1,7 @@
 // Tree attention, few query rows per key head: bound by reading the cache once.
 //
 // As in the cross attention of few queries, the rows that share a key head are one tile of
-// 8 or 16, blocks split the keys, and a warp takes 32 keys at a time straight from memory
+// 8 (or 16, of 8-bit caches that have no copies by the page), blocks split the keys, and a warp takes 32 keys at a time straight from memory
 // into the operand registers of mma.sync (S = Q K^T with any 16 of the d elements in a
 // product, the same for both operands; O^T += V^T P^T, with P^T in S's own layout).
 //
@@ -16,6 +16,10 @@
 // so that the largest P of a row is the one that counts most in O, whatever the scales,
 // and float16 holds them all as it holds weights.  Queries in bfloat16 are multiplied by a
 // power of two for each row, which float16 then holds to all their bits.
+//
+// Measured, 8 key heads of 128, 4 rows: 38 sequences of 8192 e4m3 keys 126 us, 5.2 TB/s (0.77 of
+// the measured copy rate; DRAM at 66 % of its peak, issue slots at 47 %: the latency of a warp's
+// steps, with 8 warps to an SM); one sequence of 2000 bfloat16 keys 10 us, latency.
 #include "fs_tree.cuh"
 
 #include <type_traits>

@@ -56,16 +56,8 @@ __device__ __forceinline__ void tree_row(const int* parents, int t, uint32_t* wo
     }
 }
 // 32 keys from key `at` of the tree on (above -32), as a row sees them; the keys before
-// the tree too, where the row is there.  words: kTreeWords + 1 of them, the last zero.
+// the tree too, where the row is there.
 __device__ __forceinline__ uint32_t tree_window(const uint32_t* words, bool there, int at) {
-    if (!there) return 0;
-    if (at < 0) return at <= -32 ? 0xffffffffu : words[0] << -at | ((1u << -at) - 1u);
-    if (at >= kv::kMaxTree) return 0;
-    return __funnelshift_r(words[at >> 5], words[(at >> 5) + 1], at & 31);
-}
-
-// the same from words without the last, zero one
-__device__ __forceinline__ uint32_t tree_window8(const uint32_t* words, bool there, int at) {
     if (!there) return 0;
     if (at < 0) return at <= -32 ? 0xffffffffu : words[0] << -at | ((1u << -at) - 1u);
     if (at >= kv::kMaxTree) return 0;

@@ -35,7 +35,7 @@ using kv::HELD_E4M3;
 using kv::HELD_I8;
 
 constexpr int kWarps = 4;
-constexpr int kWords = kTreeWords + 1;
+constexpr int kWords = kTreeWords + 1;     // (odd: rows in banks of their own)
 
 template <bool BF>
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -164,7 +164,6 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
     if (threadIdx.x < ROWS) {
         const int row = group * ROWS + min((int)threadIdx.x, nrows - 1);
         tree_row(a.parents ? sParents : nullptr, row / a.R, sTree[threadIdx.x]);
-        sTree[threadIdx.x][kTreeWords] = 0;
     }
 
     // Row 8 rb + g of the tile: its queries as the products' operand

@@ -712,8 +712,8 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
                         const int tok = min(row_t + g + 8 * k, rows - 1) / a.R;
                         const uint32_t* words = sWords + (tok - tok0) * kTreeWords;
                         const bool there = words[tok >> 5] >> (tok & 31) & 1u;
-                        sees[0] &= tree_window8(words, there, key0 - ctx);
-                        sees[1] &= tree_window8(words, there, key0 + 32 - ctx);
+                        sees[0] &= tree_window(words, there, key0 - ctx);
+                        sees[1] &= tree_window(words, there, key0 + 32 - ctx);
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i)

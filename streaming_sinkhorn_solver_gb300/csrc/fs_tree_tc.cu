@@ -48,6 +48,9 @@ constexpr int kMma0 = kSoftWarps, kFit0 = kSoftWarps + 2;
 enum Mode : int { ROWS = 0, KEYS = 1, HALF = 2 };
 constexpr int kKeys = kTcKeys;
 constexpr float kRefSlack = 8.f;
+// values that may not be finite are looked through for that (whole numbers are)
+template <int HELD>
+constexpr bool kLooks = HELD != HELD_I8;
 // tiles that the tree's keys may lie in
 constexpr int kMixed = (kv::kMaxTree + kKeys - 2) / kKeys + 1;
 
@@ -105,8 +108,10 @@ struct TileScales {
 struct TcBars {
     uint64_t full[2][8], free_raw[2][8];     // copies landed; 8 bits: the ring they land in
     uint64_t ready[2][8], empty[2][8];       // 8 bits: widened tiles; operand tiles done with
-    // 16 bits: values of the tiles with keys of the tree (the block's last), each of which has
-    // barriers of its own: landed, and looked through
+    // Values of the tiles with keys of the tree (the block's last), each of which has barriers of its
+    // own: in 16 bits for having landed, and for having been looked through.  (The softmax does not
+    // wait for values otherwise: at the barrier of a slot that the other stream's tile had before,
+    // it could find that tile not there yet, take it for this one and read flags not written.)
     uint64_t last[kMixed], looked[kMixed];
     uint64_t sfull[2], sfree[2], pfull[2][2], pfree[2][2], drain[2];
     uint32_t tmem, pad;
@@ -358,7 +363,7 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
                     const int row = row0 + i * kStep;
                     const bool out = key0 + row >= w.end;
                     if (out) x[i] = make_uint4(0, 0, 0, 0);
-                    if (KV == 1 && HELD == HELD_E4M3 && look(x[i], key0, row, tb.poison_value))
+                    if (KV == 1 && kLooks<HELD> && look(x[i], key0, row, tb.poison_value))
                         x[i] = make_uint4(0, 0, 0, 0);
                 }
             }
@@ -419,7 +424,10 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
             before.step(kGroups, C::kRing);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(Q8 ? &bar.ready[KV][to.slot] : &bar.looked[j - mixed_from]);
+        if (lane == 0) {
+            if (Q8) mbar_arrive(&bar.ready[KV][to.slot]);
+            if (kLooks<HELD> && KV == 1 && mixed) mbar_arrive(&bar.looked[j - mixed_from]);
+        }
         if (Q8) from.step(kGroups, Q8 ? C::kRaw : 1);
         to.step(kGroups, C::kRing);
         scales += kGroups;
@@ -694,13 +702,13 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
             if (mixed || (counted.x & counted.y) != 0xffffffffu) {
                 uint32_t bad[2] = {0, 0};
                 if (mixed) {
-                    // the values' check comes with their tile
-                    if (!(ok = warp_wait(Q8 ? &bar.ready[1][tile % NR] : &bar.looked[tile - mixed_from],
-                                         Q8 ? tile / NR & 1 : 0, a.err, ERR_TIMEOUT_EPILOGUE)))
+                    // the values' check may come behind the scores
+                    if (kLooks<HELD> &&
+                        !(ok = warp_wait(&bar.looked[tile - mixed_from], 0, a.err, ERR_TIMEOUT_EPILOGUE)))
                         break;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        uint32_t f = HELD == HELD_I8 ? 0u : tb.poison_value[32 * x + lane];
+                        uint32_t f = kLooks<HELD> ? tb.poison_value[32 * x + lane] : 0u;
                         if (Q8) f |= tb.poison_scale[32 * x + lane];
                         bad[x] = __ballot_sync(0xffffffffu, f != 0);
                     }

@@ -501,8 +501,10 @@ fs_status fs_rotary_grad(const fs_rotation* rot, const void* dq, const void* dk,
  * amax = max(max |x_c|, 2^-80) and top = 448 (FS_DTYPE_E4M3) or 127 (FS_DTYPE_I8).
  * The value it stands for is code x scale.  A row with a NaN or an infinity gets
  * zero codes and a NaN scale: all of it is read as NaN.  A caller that writes
- * scales itself keeps them positive, 2^-89 at least.  FS_DTYPE_BF16 and
- * FS_DTYPE_F16 hold the rows as they are, without scales.
+ * scales itself keeps them positive, 2^-89 to 2^122 (fs_tree_attention takes a value
+ * scale beyond 2^-126 .. 2^126 as NaN); those of rows that nobody wrote may be anything as
+ * long as no token sees them.  FS_DTYPE_BF16 and FS_DTYPE_F16 hold the rows as they are,
+ * without scales.
  */
 typedef struct fs_cache {
     int32_t dtype;            /* fs_dtype: any of the four */

@@ -47,6 +47,16 @@ struct Cache {
 // Checks a description and fills `c`; `write`: its rows must not overlap.
 fs_status fill_cache(int dev, Cache& c, const fs_cache* cache, bool write);
 
+// The scales of a key and its value as a product's: the key's, and the value's logarithm.  A value
+// scale that no row has (not positive, infinite, NaN, beyond 2^+-126) makes the key's scale NaN,
+// and so every score with it: the rows that see the key are NaN, and the others never add
+// what it comes to.
+__device__ __forceinline__ void weigh(float k_scale, float v_scale, float& ks, float& lv) {
+    const bool fine = v_scale >= 0x1p-126f && v_scale <= 0x1p126f;
+    ks = fine ? k_scale : __uint_as_float(0x7fc00000u);
+    lv = fine ? lg2(v_scale) : 0.f;
+}
+
 // Four codes as two registers of two float16 values each, in their order; exact.
 template <int HELD>
 __device__ __forceinline__ void widen4(uint32_t x, uint32_t& lo, uint32_t& hi) {

@@ -11,10 +11,11 @@
 // rows a byte permute pairs two keys before they are widened.  (Straight from memory, as the 16-bit
 // types come, the loads of a step waited for the page numbers and the products for the loads,
 // with registers for two blocks to an SM: half the speed.)  Scales stay in float32:
-//   x_ij = q_i . code_j (scale2 ks_j) + log2 vs_j,   P_ij = 2^{x_ij - ref_i},
-//   O_i = sum_j P_ij code_j,   sum_i = sum_j P_ij / vs_j,
+//   w_ij = q_i . code_j (scale2 ks_j),   x_ij = w_ij + log2 vs_j,   P_ij = 2^{x_ij - ref_i},
+//   O_i = sum_j P_ij code_j,   sum_i = sum_j 2^{w_ij - ref_i},
 // so that the largest P of a row is the one that counts most in O, whatever the scales,
-// and float16 holds them all as it holds weights.  Queries in bfloat16 are multiplied by a
+// and float16 holds them all as it holds weights.  (The sum as that of P_ij / vs_j has the same
+// price, a reciprocal for an exponential, but takes 0 / vs_j from keys that a row does not see.)  Queries in bfloat16 are multiplied by a
 // power of two for each row, which float16 then holds to all their bits.
 //
 // Measured, 8 key heads of 128, 4 rows: 38 sequences of 8192 e4m3 keys 126 us, 5.2 TB/s (0.77 of
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
     for (int key = k0 + KEYS * warp; key < k1; key += KEYS * kWarps) {
         uint32_t bits = 0;
         uint32_t k[2 * KB][U][4], v[KB][4][VW];
-        float ks[4 * KB], lv[4 * KB], iv[4 * KB];      // of keys 8 nb + 2 t + {0, 1}
+        float ks[4 * KB], lv[4 * KB];                  // of keys 8 nb + 2 t + {0, 1}
         const uint8_t* step = reinterpret_cast<const uint8_t*>(smem) + warp * 4 * kWarpRows + stage * St::kBytes;
         if (Q8) {
             __syncwarp();                 // the step before is done with
@@ -374,9 +375,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
             for (int nb = 0; nb < 2 * KB; ++nb) {
                 const float* s = reinterpret_cast<const float*>(step + 2 * St::kRows) + 8 * nb + 2 * t;
                 const float2 x = *reinterpret_cast<const float2*>(s), y = *reinterpret_cast<const float2*>(s + 32);
-                ks[2 * nb] = x.x, ks[2 * nb + 1] = x.y;
-                lv[2 * nb] = bits >> (8 * nb + 2 * t) & 1u ? y.x : 1.f;
-                lv[2 * nb + 1] = bits >> (8 * nb + 2 * t + 1) & 1u ? y.y : 1.f;
+                kv::weigh(x.x, y.x, ks[2 * nb], lv[2 * nb]);
+                kv::weigh(x.y, y.y, ks[2 * nb + 1], lv[2 * nb + 1]);
             }
         } else {
             // pages of each 8 of these keys (which none of them leaves), and what counts
@@ -453,7 +453,6 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
                     bool bad = false;
 #pragma unroll
                     for (int w = 0; w < VW; ++w) bad |= nonfinite<HELD, BF>(v[kb][x][w]);
-                    if (Q8) bad |= !(lv[4 * kb + x] < INFINITY);
                     poison |= (uint32_t)bad << (4 * kb + x);
                 }
             poison |= __shfl_xor_sync(0xffffffffu, poison, 4);
@@ -466,15 +465,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
                     if (poison >> (4 * kb + x) & 1u) {
 #pragma unroll
                         for (int w = 0; w < VW; ++w) v[kb][x][w] = 0;
-                        if (Q8) lv[4 * kb + x] = 1.f;
                     }
-        }
-        if (Q8) {
-#pragma unroll
-            for (int e = 0; e < 4 * KB; ++e) {
-                iv[e] = __fdividef(1.f, lv[e]);
-                lv[e] = lg2(lv[e]);
-            }
         }
         // scores of row 8 rb + g and keys 8 nb + 2 t + {0, 1}
         uint32_t ph[RB][2 * KB], pl[RB][2 * KB];
@@ -482,17 +473,18 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
         bool moved = false;
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
-            float x[4 * KB], top = -INFINITY;
+            float x[4 * KB], w[4 * KB], top = -INFINITY;       // (16 bits: w is x)
             const uint32_t sees = bits & (mixed ? tree_window(words[rb], there[rb], key - ctx)
                                                 : there[rb] ? 0xffffffffu : 0u);
 #pragma unroll
             for (int e = 0; e < 4 * KB; ++e) {
                 const int j = 8 * (e >> 1) + 2 * t + (e & 1);
                 const float z = s[rb >> 1][e >> 1][2 * (rb & 1) + (e & 1)];
-                float y = Q8 ? fmaf(z * mul[rb], ks[e], lv[e]) : z * mul[rb];
+                float y = z * (Q8 ? mul[rb] * ks[e] : mul[rb]);
                 // bit 4 kb + x, e = 4 kb + 2 (nb & 1) + (e & 1) and x = (j & 1) + 2 (nb & 1)
                 if (poison >> e & 1u) y = __uint_as_float(0x7fc00000u);
-                x[e] = (sees >> j) & 1u ? y : -INFINITY;
+                w[e] = (sees >> j) & 1u ? y : -INFINITY;
+                x[e] = Q8 ? w[e] + lv[e] : w[e];
                 top = fmaxf(top, x[e]);
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -508,7 +500,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
 #pragma unroll
             for (int e = 0; e < 4 * KB; ++e) {
                 x[e] = ex2(x[e] - base);
-                sum[rb] = Q8 ? fmaf(x[e], iv[e], sum[rb]) : sum[rb] + x[e];
+                sum[rb] += Q8 ? ex2(w[e] - base) : x[e];
             }
 #pragma unroll
             for (int nb = 0; nb < 2 * KB; ++nb) {

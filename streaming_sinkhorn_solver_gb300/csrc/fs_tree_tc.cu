@@ -100,7 +100,7 @@ struct Tc {
 // What the softmax needs to know of a tile.
 struct TileBits {
     uint32_t counted[2];
-    uint8_t poison_scale[kKeys], poison_value[kKeys];    // of the tree's keys
+    uint8_t poison[kKeys];       // of the tree's keys
 };
 struct TileScales {
     float kc[kKeys], lv[kKeys], iv[kKeys];   // of the scores; log2 and inverse of the value scale
@@ -363,18 +363,16 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
                     const int row = row0 + i * kStep;
                     const bool out = key0 + row >= w.end;
                     if (out) x[i] = make_uint4(0, 0, 0, 0);
-                    if (KV == 1 && kLooks<HELD> && look(x[i], key0, row, tb.poison_value))
+                    if (KV == 1 && kLooks<HELD> && look(x[i], key0, row, tb.poison))
                         x[i] = make_uint4(0, 0, 0, 0);
                 }
             }
-            float ks = 0.f, vs = 0.f;
+            float ks = 0.f, vs = 0.f;              // (anything where there is no page)
             const bool scaled = KV == 0 && tid < kKeys;
             if (scaled) {
                 const float* s = reinterpret_cast<const float*>(smem + M::raw_scale) + from.slot * 2 * kKeys + tid;
-                const float k0 = s[0], v0 = s[kKeys];          // (anything where there is no page)
-                const bool on = tb.counted[tid >> 5] >> (tid & 31) & 1u;
-                ks = on ? k0 : 0.f;
-                vs = on ? v0 : 0.f;
+                ks = s[0];
+                vs = s[kKeys];
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.free_raw[KV][from.slot]);
@@ -401,12 +399,11 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
             }
             if (scaled) {
                 TileScales& ts = reinterpret_cast<TileScales*>(smem + M::scales)[scales];
-                const bool bad = mixed && key0 + tid >= w.ctx && !(vs < INFINITY);
-                const bool none = vs == 0.f || bad;            // (0: the key does not count)
-                ts.kc[tid] = ks * mul;
-                ts.lv[tid] = none ? 0.f : lg2(vs);
-                ts.iv[tid] = none ? 0.f : __fdividef(1.f, vs);
-                tb.poison_scale[tid] = bad;
+                float kc, lv;
+                kv::weigh(ks, vs, kc, lv);
+                ts.kc[tid] = kc * mul;
+                ts.lv[tid] = lv;
+                ts.iv[tid] = kc == kc ? __fdividef(1.f, vs) : 0.f;     // (what weigh refuses may have no inverse)
             }
         } else {
             if (!warp_wait(&bar.last[j - mixed_from], 0, a.err, ERR_TIMEOUT_PRODUCER)) return;
@@ -414,7 +411,7 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
             for (int i = 0; i < kMine; ++i) {
                 const int row = row0 + i * kStep;
                 const uint32_t at = slot + (u >> 3) * C::kChunkBytes + swz_offset(row, (u & 7) * 8);
-                const bool bad = look(lds16(at), key0, row, tb.poison_value);
+                const bool bad = look(lds16(at), key0, row, tb.poison);
                 if (bad || key0 + row >= w.end) sts16(at, 0, 0, 0, 0);
             }
         }
@@ -701,17 +698,11 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
             const bool mixed = tile >= mixed_from;
             if (mixed || (counted.x & counted.y) != 0xffffffffu) {
                 uint32_t bad[2] = {0, 0};
-                if (mixed) {
+                if (kLooks<HELD> && mixed) {
                     // the values' check may come behind the scores
-                    if (kLooks<HELD> &&
-                        !(ok = warp_wait(&bar.looked[tile - mixed_from], 0, a.err, ERR_TIMEOUT_EPILOGUE)))
-                        break;
+                    if (!(ok = warp_wait(&bar.looked[tile - mixed_from], 0, a.err, ERR_TIMEOUT_EPILOGUE))) break;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t f = kLooks<HELD> ? tb.poison_value[32 * x + lane] : 0u;
-                        if (Q8) f |= tb.poison_scale[32 * x + lane];
-                        bad[x] = __ballot_sync(0xffffffffu, f != 0);
-                    }
+                    for (int x = 0; x < 2; ++x) bad[x] = __ballot_sync(0xffffffffu, tb.poison[32 * x + lane] != 0);
                 }
 #pragma unroll
                 for (int k = 0; k < kLaneRows; ++k) {

@@ -1,0 +1,99 @@
+"""Tree attention at the ends of its range: keys that no row or not every row sees.  Bounds as in
+kv_ref."""
+import math
+
+import pytest
+import torch
+
+from streaming_sinkhorn_solver_gb300 import binding as fs
+from tests.kv_ref import quantise, tree64
+from tests.test_gpu_cache import BF, E4M3, HALF, I8, NAN, check, gen, random_parents, setting, within
+
+pytestmark = pytest.mark.gpu
+EIGHT = [E4M3, I8]
+
+
+def values_of(x, held):
+    """What rows x stand for in a cache, float64."""
+    if held in (BF, HALF):
+        return x.double()
+    code, scale = quantise(x, held)
+    return code.double() * scale.double()[..., None]
+
+
+def attend(q, cache, table, ctx, parents):
+    got = fs.fs_tree_attention(q.cuda(), cache, table.cuda(), torch.tensor(ctx, dtype=torch.int32).cuda(),
+                               None if parents is None else parents.cuda())
+    fs.fs_check()
+    return got
+
+
+# --- keys that a row does not see ----------------------------------------------
+
+@pytest.mark.parametrize("held", [BF, *EIGHT])
+@pytest.mark.parametrize("n,d", [(1, 64), (2, 128), (3, 72), (9, 128), (20, 64), (40, 128)])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_absent_tokens_beside_rows_that_are_not_numbers(held, n, d, which):
+    """A NaN row of the context: the tokens that are there see it, padding does not."""
+    ctx = [300, 77]
+    q, cache, table, k, v = setting(n + d, 2, n, ctx, 8, 2, d, BF, held, 16)
+    rows = torch.ones(2, 1, 2, d, dtype=BF)
+    rows[0] = NAN
+    at = torch.tensor([[40], [-1]], dtype=torch.int32)
+    one = torch.ones_like(rows)
+    fs.fs_cache_write(cache, table.cuda(), at.cuda(), *((rows.cuda(), one.cuda()) if which == "k"
+                                                        else (one.cuda(), rows.cuda())))
+    parents = random_parents(gen(n), 2, n)
+    parents[:, -1] = -2
+    out, lse = attend(q, cache, table, ctx, parents)
+    assert not out[:, -1].any() and bool((lse[:, :, -1] == -math.inf).all())
+    assert bool(torch.isnan(out[0, :-1]).all())
+    want = tree64(q[1:], k[1:], v[1:], torch.ones(k.shape[:2], dtype=torch.bool)[1:], ctx[1:], parents[1:],
+                  weights=HALF if held in EIGHT else None)
+    within(out[1:], want["out"], want["tol"]["out"], "out")
+    within(lse[1:], want["lse"], want["tol"]["lse"], "lse")
+
+
+@pytest.mark.parametrize("held", EIGHT)
+@pytest.mark.parametrize("n,H,G,d", [(2, 4, 2, 64), (3, 4, 4, 128), (5, 8, 2, 72), (12, 8, 2, 128), (40, 4, 2, 64),
+                                     (50, 8, 2, 128)])
+@pytest.mark.parametrize("fill", [0.0, 1e-40, -1.0, -1e-40, 3e38, math.inf, NAN])
+def test_scales_of_slots_that_were_never_written(held, n, H, G, d, fill):
+    """Padding's tokens are left out of the write: their slots' scales may be anything."""
+    ctx = [100, 61]
+    gone = max(1, n // 4)
+    g = gen(n + d)
+    page, per = 16, -(-(max(ctx) + n) // 16)
+    cache = fs.KVCache(*(torch.zeros(2 * per, G, page, d, dtype=torch.int8, device="cuda").view(held)
+                         for _ in range(2)),
+                       *(torch.full((2 * per, G, page), fill, device="cuda") for _ in range(2)))
+    table = torch.randperm(2 * per, generator=g).int().view(2, per)
+    x, y = (torch.randn(2, per * page, G, d, generator=g).bfloat16() for _ in range(2))
+    at = torch.arange(per * page, dtype=torch.int32).expand(2, -1).clone()
+    for b in range(2):
+        at[b, ctx[b] + n - gone:] = -1
+    fs.fs_cache_write(cache, table.cuda(), at.cuda(), x.cuda(), y.cuda())
+    q = (2 * torch.randn(2, n, H, d, generator=g)).bfloat16()
+    parents = random_parents(g, 2, n, absent=gone)
+    check(q, cache, table, values_of(x, held), values_of(y, held), ctx, parents)
+
+
+@pytest.mark.parametrize("held", EIGHT)
+@pytest.mark.parametrize("n,H", [(4, 2), (40, 8)])
+@pytest.mark.parametrize("scale", [0.0, 1e-40, -1.0, 3e38, math.inf])
+def test_value_scales_that_are_none(held, n, H, scale):
+    """A value scale that no row can have: NaN for the tokens that see it, nothing for others."""
+    ctx = [100, 61]
+    q, cache, table, k, v = setting(8, 2, n, ctx, H, 2, 64, BF, held, 16)
+    bad = n // 2
+    for b in range(2):
+        p = ctx[b] + bad
+        cache.v_scale[int(table[b, p // 16]), :, p % 16] = scale
+    parents = torch.full((2, n), -1, dtype=torch.int32)
+    parents[:, -1] = bad
+    out, lse = attend(q, cache, table, ctx, parents)
+    others = [t for t in range(n - 1) if t != bad]
+    want = tree64(q, k, v, torch.ones(k.shape[:2], dtype=torch.bool), ctx, parents, weights=HALF)
+    within(out[:, others], want["out"][:, others], want["tol"]["out"][:, others], "out")
+    within(lse[:, :, others], want["lse"][:, :, others], want["tol"]["lse"][:, :, others], "lse")
+    assert bool(torch.isnan(out[:, [bad, n - 1]]).all())

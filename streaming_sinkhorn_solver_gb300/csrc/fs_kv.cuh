@@ -51,10 +51,26 @@ fs_status fill_cache(int dev, Cache& c, const fs_cache* cache, bool write);
 // scale that no row has (not positive, infinite, NaN, beyond 2^+-126) makes the key's scale NaN,
 // and so every score with it: the rows that see the key are NaN, and the others never add
 // what it comes to.
+__device__ __forceinline__ bool weighable(float v_scale) { return v_scale >= 0x1p-126f && v_scale <= 0x1p126f; }
 __device__ __forceinline__ void weigh(float k_scale, float v_scale, float& ks, float& lv) {
-    const bool fine = v_scale >= 0x1p-126f && v_scale <= 0x1p126f;
+    const bool fine = weighable(v_scale);
     ks = fine ? k_scale : __uint_as_float(0x7fc00000u);
     lv = fine ? lg2(v_scale) : 0.f;
+}
+
+// Beside 8-bit values a row's reference is a whole number: value scales far apart bring it, and what it
+// moves by, to 200, where float32 would round to 2^-17.
+// x 2^y for a sum x of exponentials whose reference moves by -y; y may be below float32's exponents
+// and x as much above 1: the factor goes in by halves.
+__device__ __forceinline__ float moved_sum(float x, float y) {
+    const float half = ex2(0.5f * y);
+    return x * half * half;
+}
+
+// ref + log2(total), the exponent of total first: ref and it may be 120 and all but cancel.
+__device__ __forceinline__ float log_sum(float ref, float total) {
+    const int e = min(max((__float_as_int(total) >> 23) - 127, -126), 126);
+    return (ref + (float)e) + lg2(total * __int_as_float((127 - e) << 23));
 }
 
 // Four codes as two registers of two float16 values each, in their order; exact.

@@ -14,7 +14,9 @@
 //   w_ij = q_i . code_j (scale2 ks_j),   x_ij = w_ij + log2 vs_j,   P_ij = 2^{x_ij - ref_i},
 //   O_i = sum_j P_ij code_j,   sum_i = sum_j 2^{w_ij - ref_i},
 // so that the largest P of a row is the one that counts most in O, whatever the scales,
-// and float16 holds them all as it holds weights.  (The sum as that of P_ij / vs_j has the same
+// and float16 holds them all as it holds weights.  The sum's terms are up to 2^8 / vs_j, 2^97 for the
+// least scale that a row can have, and the one of the reference is 1 / vs, 2^-122 or more: float32
+// holds them all.  (The sum as that of P_ij / vs_j has the same
 // price, a reciprocal for an exponential, but takes 0 / vs_j from keys that a row does not see.)  Queries in bfloat16 are multiplied by a
 // power of two for each row, which float16 then holds to all their bits.
 //
@@ -491,8 +493,11 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             alpha[rb] = 1.f;
             if (top > ref[rb] + 8.f) {
-                if (ref[rb] != -INFINITY) alpha[rb] = ex2(ref[rb] - top);
-                sum[rb] *= alpha[rb];
+                if (Q8) top = ceilf(top);
+                if (ref[rb] != -INFINITY) {
+                    alpha[rb] = ex2(ref[rb] - top);
+                    sum[rb] = Q8 ? kv::moved_sum(sum[rb], ref[rb] - top) : sum[rb] * alpha[rb];
+                }
                 ref[rb] = top;
                 moved |= alpha[rb] != 1.f;
             }
@@ -598,11 +603,14 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
         float total = 0.f, f[kWarps];
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            f[w] = ex2(sRef[w * ROWS + row] - base);
-            total = fmaf(f[w], sSum[w * ROWS + row], total);
+            const float by = sRef[w * ROWS + row] - base;
+            f[w] = ex2(by);
+            total = Q8 ? total + kv::moved_sum(sSum[w * ROWS + row], by) : fmaf(f[w], sSum[w * ROWS + row], total);
         }
         const float inv = total == 0.f ? 0.f : 1.f / total;
-        const float lse2 = total == 0.f ? -INFINITY : top - kShift + lg2(total);
+        const float lse2 = total == 0.f ? -INFINITY
+                           : Q8         ? kv::log_sum(top - kShift, total)
+                                        : top - kShift + lg2(total);
         T* out = out_row(row);
         float* part = P.part.out + (split * P.part.rows + at) * P.dp;
         for (int e = lane; e < P.dp; e += 32) {

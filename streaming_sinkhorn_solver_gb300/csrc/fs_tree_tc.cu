@@ -14,6 +14,9 @@
 // float16 (exact).  Scales stay in float32:
 //   x_ij = q_i . code_j (scale2 ks_j) + log2 vs_j,   P_ij = 2^{x_ij - ref_i},
 //   O_i = sum_j P_ij code_j,   sum_i = sum_j P_ij / vs_j.
+// Where the scales are so far apart that P_ij could be below float32's numbers and P_ij / vs_j still
+// count (rows of zeros, whose scale is 2^-89, beside others), the sum is that of the terms'
+// own exponentials, 2^{x_ij - log2 vs_j - ref_i}.
 // Queries in bfloat16 become float16 for that, the block's multiplied by one power of two that
 // brings the largest to 2^14: what the others lose, 2^-25 at most, is 2^-39 of it.
 //
@@ -104,6 +107,7 @@ struct TileBits {
 };
 struct TileScales {
     float kc[kKeys], lv[kKeys], iv[kKeys];   // of the scores; log2 and inverse of the value scale
+    int apart, pad[3];                       // the tile's sums are formed without iv, which is 0
 };
 struct TcBars {
     uint64_t full[2][8], free_raw[2][8];     // copies landed; 8 bits: the ring they land in
@@ -334,6 +338,7 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
     int scales = j_at % C::kScales, bits = j_at % C::kBits;
     Ring before;               // the tile before this one: they are handed on in their order
     if (kGroups > 1 && group == 0) before.step(1, C::kRing);
+    int most = -(1 << 10);     // exponent of the value scales of the tiles so far that go to the same stream
     // pieces of a row are in neighbouring lanes
     const auto look = [&](const uint4& x, int key0, int row, uint8_t* flags) {
         uint32_t bad = key0 + row >= w.ctx && nonfinite16<HELD, BF>(x);
@@ -367,12 +372,13 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
                         x[i] = make_uint4(0, 0, 0, 0);
                 }
             }
-            float ks = 0.f, vs = 0.f;              // (anything where there is no page)
+            float ks = 0.f, vs = 0.f, vs2 = 0.f;   // (anything where there is no page)
             const bool scaled = KV == 0 && tid < kKeys;
             if (scaled) {
                 const float* s = reinterpret_cast<const float*>(smem + M::raw_scale) + from.slot * 2 * kKeys + tid;
                 ks = s[0];
                 vs = s[kKeys];
+                vs2 = s[kKeys + (tid ^ 32) - tid];         // the other 32 keys', which both warps look at
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.free_raw[KV][from.slot]);
@@ -403,7 +409,18 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
                 kv::weigh(ks, vs, kc, lv);
                 ts.kc[tid] = kc * mul;
                 ts.lv[tid] = lv;
-                ts.iv[tid] = kc == kc ? __fdividef(1.f, vs) : 0.f;     // (what weigh refuses may have no inverse)
+                // P / vs is lost where P < 2^-126: 2^-62 of the sum at most while the scales are within 2^64 of
+                // the largest so far, which a reference may be from.  The tree's keys, which not every row
+                // sees, have no say in how others are summed.
+                const bool on = kv::weighable(vs) && tb.counted[tid >> 5] >> lane & 1u;
+                const bool on2 = kv::weighable(vs2) && tb.counted[tid >> 5 ^ 1] >> lane & 1u;
+                const int e = __float_as_int(vs) >> 23, e2 = __float_as_int(vs2) >> 23;
+                const int least = __reduce_min_sync(0xffffffffu, min(on ? e : 1 << 10, on2 ? e2 : 1 << 10));
+                const int top = __reduce_max_sync(0xffffffffu, max(on ? e : -(1 << 10), on2 ? e2 : -(1 << 10)));
+                if (!mixed) most = max(most, top);
+                const bool apart = mixed || most - least > 64;
+                ts.iv[tid] = apart || !kv::weighable(vs) ? 0.f : __fdividef(1.f, vs);
+                if (tid == 0) ts.apart = apart;
             }
         } else {
             if (!warp_wait(&bar.last[j - mixed_from], 0, a.err, ERR_TIMEOUT_PRODUCER)) return;
@@ -750,9 +767,12 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     float alpha = 1.f;
                     if (top > ref[k] + kRefSlack) {
+                        if (Q8) top = ceilf(top);
                         // (up to its first counted key a row's sum and O are zero)
-                        if (ref[k] != -INFINITY) alpha = ex2(ref[k] - top);
-                        sum[k] *= alpha;
+                        if (ref[k] != -INFINITY) {
+                            alpha = ex2(ref[k] - top);
+                            sum[k] = Q8 ? kv::moved_sum(sum[k], ref[k] - top) : sum[k] * alpha;
+                        }
                         ref[k] = top;
                     }
                     const float x = __shfl_sync(0xffffffffu, alpha, 4 * (lane & 7));
@@ -785,6 +805,19 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
             uint64_t s[kLaneRows];
 #pragma unroll
             for (int k = 0; k < kLaneRows; ++k) s[k] = 0;
+            if (Q8 && ts.apart) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 l = *reinterpret_cast<const float2*>(ts.lv + 8 * i + 2 * t4);
+#pragma unroll
+                    for (int k = 0; k < kLaneRows; ++k) {
+                        const float* x = v + 32 * (k >> 1) + 4 * i + 2 * (k & 1);
+                        float e0, e1;
+                        upk(add2(pk(x[0] - l.x, x[1] - l.y), base2[k]), e0, e1);
+                        s[k] = add2(s[k], pk(ex2(e0), ex2(e1)));
+                    }
+                }
+            }
             uint32_t p[8 * kLaneRows];         // p[16 h + 2 i + (k & 1)]
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -852,8 +885,9 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
             total = 0.f;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                f[x] = ex2(join[128 * x + r] - base);
-                total = fmaf(f[x], join[256 + 128 * x + r], total);
+                const float by = join[128 * x + r] - base, part = join[256 + 128 * x + r];
+                f[x] = ex2(by);
+                total = Q8 ? total + kv::moved_sum(part, by) : fmaf(f[x], part, total);
             }
             c0 = t ? (dsteps + 1) / 2 * 16 : 0;
             c1 = t ? dsteps * 16 : (dsteps + 1) / 2 * 16;
@@ -862,7 +896,9 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
         const float inv = none ? 0.f : 1.f / total;
         const int64_t row = ((int64_t)b * a.H + head) * a.n + tok;
         if (live && (!kAlternate || t == 0)) {
-            const float lse2 = none ? -INFINITY : top - kProbShift<MB> + lg2(total);
+            const float lse2 = none ? -INFINITY
+                               : Q8 ? kv::log_sum(top - kProbShift<MB>, total)
+                                    : top - kProbShift<MB> + lg2(total);
             if (P.splits > 1)
                 P.part.lse2[split * P.part.rows + row] = lse2;
             else

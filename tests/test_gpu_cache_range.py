@@ -1,5 +1,5 @@
-"""Tree attention at the ends of its range: keys that no row or not every row sees.  Bounds as in
-kv_ref."""
+"""Tree attention at the ends of its range: keys that no row or not every row sees,
+scales of very different sizes.  Bounds as in kv_ref."""
 import math
 
 import pytest
@@ -97,3 +97,47 @@ def test_value_scales_that_are_none(held, n, H, scale):
     within(out[:, others], want["out"][:, others], want["tol"]["out"][:, others], "out")
     within(lse[:, :, others], want["lse"][:, :, others], want["tol"]["lse"][:, :, others], "lse")
     assert bool(torch.isnan(out[:, [bad, n - 1]]).all())
+
+
+# --- scales of very different sizes -----------------------------------
+
+@pytest.mark.parametrize("held", EIGHT)
+@pytest.mark.parametrize("n,H,G,d", [(1, 4, 2, 64), (2, 8, 2, 128), (20, 4, 2, 64), (20, 4, 2, 128), (40, 4, 2, 128),
+                                     (90, 4, 2, 64)])
+@pytest.mark.parametrize("ctx", [37, 700])
+@pytest.mark.parametrize("size", [2.0 ** 60, 2.0 ** 119])
+@pytest.mark.parametrize("order", ["first", "last", "between", "mixed"])
+def test_rows_of_zeros_beside_large_ones(held, n, H, G, d, ctx, size, order):
+    """Every key counts in the sum by its score alone, whatever its value: rows of zeros (held at
+    2^-80) beside values of 2^60 and of 2^119, all of one weight."""
+    q, cache, table, k, v = setting(n, 1, n, [ctx], H, G, d, BF, held, 16)
+    m = ctx + n
+    g = gen(m)
+    rows = torch.randn(1, m, G, d, generator=g).clamp(-4, 4) * size
+    small = {"first": torch.arange(m) >= 3, "last": torch.arange(m) < ctx - 2,
+             "between": torch.arange(m) % 7 != 3, "mixed": torch.rand(m, generator=g) < 0.5}[order]
+    rows[:, small] = 0
+    vv, kk = rows.bfloat16(), torch.zeros(1, m, G, d, dtype=BF)
+    fs.fs_cache_write(cache, table.cuda(), torch.arange(m, dtype=torch.int32)[None].cuda(), kk.cuda(), vv.cuda())
+    k[:, :m], v[:, :m] = values_of(kk, held), values_of(vv, held)
+    check(q, cache, table, k, v, [ctx])
+
+
+@pytest.mark.parametrize("held", EIGHT)
+@pytest.mark.parametrize("n", [1, 20, 40, 100])
+def test_weights_of_rows_that_end_small(held, n):
+    """The large values come with scores that leave them next to no weight: rows of zeros and of
+    small values have it all."""
+    ctx = 200
+    q, cache, table, k, v = setting(n, 1, n, [ctx], 4, 2, 64, BF, held, 16)
+    m = ctx + n
+    g = gen(m)
+    q = torch.ones_like(q)
+    kk = torch.randn(1, m, 2, 64, generator=g).bfloat16()
+    vv = torch.randn(1, m, 2, 64, generator=g).bfloat16()
+    vv[:, ::3] = 0
+    vv[:, 5] *= 2.0 ** 118
+    kk[:, 5] = -12.0                 # 96 below the others: 2^-138 of their weight
+    fs.fs_cache_write(cache, table.cuda(), torch.arange(m, dtype=torch.int32)[None].cuda(), kk.cuda(), vv.cuda())
+    k[:, :m], v[:, :m] = values_of(kk, held), values_of(vv, held)
+    check(q, cache, table, k, v, [ctx])

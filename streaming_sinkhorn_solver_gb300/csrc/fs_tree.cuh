@@ -33,6 +33,23 @@ __device__ __forceinline__ int context(const Args& a, int b) {
     return l < 0 ? 0 : min(l, a.c.reach());
 }
 
+// 2^n, -126 <= n <= 127
+__device__ __forceinline__ float two_to(int n) { return __int_as_float((127 + n) << 23); }
+
+// Queries in bfloat16 beside an 8-bit cache become float16, each row times the power of two that
+// brings its largest finite magnitude to [2^14, 2^15): float16 holds elements from 2^-31 of that on to all
+// their bits, others to 2^-39 of it.  (One power for a block of rows left nothing of a row
+// beside one 2^40 times as large.)
+// top: the larger of it and two bfloat16 magnitudes
+__device__ __forceinline__ uint32_t finite_top(uint32_t top, uint32_t w) {
+    const uint32_t l = w & 0x7fffu, h = w >> 16 & 0x7fffu;
+    return max(top, max(l < 0x7f80u ? l : 0u, h < 0x7f80u ? h : 0u));
+}
+__device__ __forceinline__ int query_shift(uint32_t top) { return min(14 + 127 - (int)(top >> 7), 126); }
+__device__ __forceinline__ uint32_t shifted_pair(uint32_t w, float up) {
+    return attn::pack16<false>(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+}
+
 // What a token of the tree sees of it: bit u for token u, none if it is not there.
 constexpr int kTreeWords = kv::kMaxTree / 32;
 // parents: in shared memory, or nullptr for a chain

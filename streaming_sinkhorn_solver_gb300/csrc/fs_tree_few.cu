@@ -17,8 +17,8 @@
 // and float16 holds them all as it holds weights.  The sum's terms are up to 2^8 / vs_j, 2^97 for the
 // least scale that a row can have, and the one of the reference is 1 / vs, 2^-122 or more: float32
 // holds them all.  (The sum as that of P_ij / vs_j has the same
-// price, a reciprocal for an exponential, but takes 0 / vs_j from keys that a row does not see.)  Queries in bfloat16 are multiplied by a
-// power of two for each row, which float16 then holds to all their bits.
+// price, a reciprocal for an exponential, but takes 0 / vs_j from keys that a row does not see.)  Queries in bfloat16 become
+// float16, each row times a power of two (query_shift).
 //
 // Measured, 8 key heads of 128, 4 rows: 38 sequences of 8192 e4m3 keys 126 us, 5.2 TB/s (0.77 of
 // the measured copy rate; DRAM at 66 % of its peak, issue slots at 47 %: the latency of a warp's
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
 
     // Row 8 rb + g of the tile: its queries as the products' operand
     uint32_t q[RB][U][4 * (Q8 ? 2 : 1)];
-    float mul[RB];                        // scale2, times what the row was divided by
+    float mul[RB];                        // scale2, over what the row was multiplied by
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         const int row = group * ROWS + min(8 * rb + g, nrows - 1);
@@ -194,27 +194,19 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
                 }
             }
         if (Q8 && BF) {
-            // the row's largest magnitude to [1, 2), then float16
             uint32_t top = 0;
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    top = max(top, max(q[rb][u][k] & 0x7fffu, q[rb][u][k] >> 16 & 0x7fffu));
+                for (int k = 0; k < 8; ++k) top = finite_top(top, q[rb][u][k]);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int ex = top >> 7;          // biased exponent; 0 and 255 are left alone
-            const int by = ex == 0 || ex == 255 ? 127 : min(ex, 253);
-            const float down = __uint_as_float((uint32_t)(254 - by) << 23);
-            mul[rb] = a.scale2 * __uint_as_float((uint32_t)by << 23);
+            const int up = query_shift(top);
+            mul[rb] = a.scale2 * two_to(-up);
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t w = q[rb][u][k];
-                    q[rb][u][k] = pack16<false>(__uint_as_float(w << 16) * down,
-                                                __uint_as_float(w & 0xffff0000u) * down);
-                }
+                for (int k = 0; k < 8; ++k) q[rb][u][k] = shifted_pair(q[rb][u][k], two_to(up));
         }
     }
     __syncthreads();

@@ -17,8 +17,8 @@
 // Where the scales are so far apart that P_ij could be below float32's numbers and P_ij / vs_j still
 // count (rows of zeros, whose scale is 2^-89, beside others), the sum is that of the terms'
 // own exponentials, 2^{x_ij - log2 vs_j - ref_i}.
-// Queries in bfloat16 become float16 for that, the block's multiplied by one power of two that
-// brings the largest to 2^14: what the others lose, 2^-25 at most, is 2^-39 of it.
+// Queries in bfloat16 become float16 for that, each row times a power of two (query_shift) that its
+// scores are divided by.
 //
 // A softmax thread holds 16 keys of each of 4 rows (the 16 x 256-bit form of TMEM loads), not
 // a row: the scales of its keys are then 24 loads of 8 bytes instead of 48 of 16 that
@@ -135,8 +135,8 @@ struct Smem {
     static constexpr int parents = join;                                      // (done with before the join)
     static constexpr int bars = join + (C::kAlternate ? 4 * 4 * 128 : 4 * kv::kMaxTree);
     static_assert(4 * 4 * 128 >= 4 * kv::kMaxTree, "parents");
-    static constexpr int top = bars + (int)sizeof(TcBars);                    // of the queries, by warps
-    static constexpr int bytes = top + 4 * kSoftWarps;
+    static constexpr int down = bars + (int)sizeof(TcBars);                   // [row]: what scores are multiplied by
+    static constexpr int bytes = down + (C::Q8 ? 4 * C::kRows : 0);
     static_assert(bits % 16 == 0 && bars % 8 == 0, "alignment");
     static_assert(1024 + bytes <= kSmemLimit, "shared memory");
 };
@@ -206,9 +206,6 @@ __device__ __forceinline__ bool nonfinite16(const uint4& x) {
     }
     return bad;
 }
-
-// 2^n, -126 <= n <= 127
-__device__ __forceinline__ float two_to(int n) { return __int_as_float((127 + n) << 23); }
 
 // A block's share of the work.
 struct Share {
@@ -313,7 +310,7 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& P, const Share& w, uint
 // operand tile.  16 bits: of the values, tiles with keys of the tree are looked through.
 template <int HD, int HELD, bool BF, int MODE, int KV>
 __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8_t* smem, TcBars& bar, int tid,
-                                          int group, float mul) {
+                                          int group) {
     using C = Tc<HD, HELD, MODE>;
     using M = Smem<HD, HELD, MODE>;
     constexpr bool Q8 = C::Q8;
@@ -407,7 +404,7 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
                 TileScales& ts = reinterpret_cast<TileScales*>(smem + M::scales)[scales];
                 float kc, lv;
                 kv::weigh(ks, vs, kc, lv);
-                ts.kc[tid] = kc * mul;
+                ts.kc[tid] = kc * a.scale2;
                 ts.lv[tid] = lv;
                 // P / vs is lost where P < 2^-126: 2^-62 of the sum at most while the scales are within 2^64 of
                 // the largest so far, which a reference may be from.  The tree's keys, which not every row
@@ -468,7 +465,7 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     TcBars& bar = *reinterpret_cast<TcBars*>(smem + M::bars);
     uint32_t* sWords = reinterpret_cast<uint32_t*>(smem + M::words);
-    uint32_t* sTop = reinterpret_cast<uint32_t*>(smem + M::top);
+    float* sDown = reinterpret_cast<float*>(smem + M::down);
     int* sParents = reinterpret_cast<int*>(smem + M::parents);
 
     int blk = blockIdx.x;
@@ -496,7 +493,6 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
     const auto warps_of = [&](int t) {
         return min(4, (rows - row0 - (kAlternate ? 0 : 128 * t) + kQuarter - 1) / kQuarter);
     };
-    float mul = a.scale2;
 
     if (warp >= kCopy) {
         // Their barriers are their own until the block meets: they start their copies before
@@ -528,7 +524,7 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
         constexpr int kPieces = HD / 8;        // of a row, in neighbouring lanes
         constexpr int kMine = C::kRows * kPieces / kSoftThreads, kStep = kSoftThreads / kPieces;
         const int u = threadIdx.x % kPieces;
-        uint32_t x[kMine][4], top = 0;
+        uint32_t x[kMine][4];
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int all = row0 + threadIdx.x / kPieces + i * kStep;
@@ -550,28 +546,18 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
             }
         }
         if (Q8 && BF) {
-            // The largest finite magnitude of the block to [2^14, 2^15), then float16.
 #pragma unroll
-            for (int i = 0; i < kMine; ++i)
+            for (int i = 0; i < kMine; ++i) {
+                uint32_t top = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t l = x[i][k] & 0x7fffu, h = x[i][k] >> 16 & 0x7fffu;
-                    top = max(top, max(l < 0x7f80u ? l : 0u, h < 0x7f80u ? h : 0u));
-                }
-            top = __reduce_max_sync(0xffffffffu, top);
-            if (lane == 0) sTop[warp] = top;
-            named_sync(1, kSoftThreads);
+                for (int k = 0; k < 4; ++k) top = finite_top(top, x[i][k]);
 #pragma unroll
-            for (int k = 0; k < kSoftWarps; ++k) top = max(top, sTop[k]);
-            // times 2^(14 + 127 - exponent), in two factors that float32 holds
-            const int up = 14 + 127 - (int)(top >> 7);
-            const float f0 = two_to(up / 2), f1 = two_to(up - up / 2);
+                for (int o = kPieces / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int up = query_shift(top);
+                if (u == 0) sDown[threadIdx.x / kPieces + i * kStep] = two_to(-up);
 #pragma unroll
-            for (int i = 0; i < kMine; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    x[i][k] = pack16<false>(__uint_as_float(x[i][k] << 16) * f0 * f1,
-                                            __uint_as_float(x[i][k] & 0xffff0000u) * f0 * f1);
+                for (int k = 0; k < 4; ++k) x[i][k] = shifted_pair(x[i][k], two_to(up));
+            }
         }
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
@@ -609,18 +595,11 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
     const uint32_t tmem = bar.tmem;
 
     if (warp >= kFit0) {
-        if (Q8 && BF) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int k = 0; k < kSoftWarps; ++k) top = max(top, sTop[k]);
-            const int down = (int)(top >> 7) - 14 - 127;
-            mul = mul * two_to(down / 2) * two_to(down - down / 2);
-        }
         const int tid = (threadIdx.x - 32 * kFit0) & (kFitters - 1), fit = (warp - kFit0) >> 1;
         if (fit < C::kGroups)
-            fit_tiles<HD, HELD, BF, MODE, 0>(P, w, smem, bar, tid, fit, mul);
+            fit_tiles<HD, HELD, BF, MODE, 0>(P, w, smem, bar, tid, fit);
         else
-            fit_tiles<HD, HELD, BF, MODE, 1>(P, w, smem, bar, tid, fit - C::kGroups, mul);
+            fit_tiles<HD, HELD, BF, MODE, 1>(P, w, smem, bar, tid, fit - C::kGroups);
     } else if (warp >= kMma0) {
         const int t = warp - kMma0;
         const int n_mine = kAlternate ? (nt + 1 - t) / 2 : nt;
@@ -669,7 +648,12 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
         const int n_mine = quarter >= warps_of(t) ? 0 : kAlternate ? (nt + 1 - t) / 2 : nt;
         const int g = lane >> 2, t4 = lane & 3;
         const int row_t = row0 + (kAlternate ? 0 : 128 * t) + quarter * kQuarter;    // the warp's first row
+        const float mul = a.scale2;                  // (8 bits: with the keys' scales)
         const uint64_t mul2 = pk(mul, mul);
+        float down[kLaneRows];                       // of the rows' queries
+#pragma unroll
+        for (int k = 0; k < kLaneRows; ++k)
+            down[k] = Q8 && BF ? sDown[(kAlternate ? 0 : 128 * t) + quarter * kQuarter + g + 8 * k] : 1.f;
         // of rows g + 8 k of the warp; a lane's part of the sum
         float ref[kLaneRows], sum[kLaneRows];
 #pragma unroll
@@ -709,7 +693,9 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
 #pragma unroll
                     for (int k = 0; k < kLaneRows; ++k) {
                         float* x = v + 32 * (k >> 1) + 4 * i + 2 * (k & 1);
-                        upk(fma2(pk(x[0], x[1]), kc[Q8 ? i : 0], lv[Q8 ? i : 0]), x[0], x[1]);
+                        uint64_t f = kc[Q8 ? i : 0];
+                        if (BF) f = mul2f(f, pk(down[k], down[k]));
+                        upk(fma2(pk(x[0], x[1]), f, lv[Q8 ? i : 0]), x[0], x[1]);
                     }
             }
             const bool mixed = tile >= mixed_from;

@@ -1,5 +1,5 @@
 """Tree attention at the ends of its range: keys that no row or not every row sees,
-scales of very different sizes.  Bounds as in kv_ref."""
+scales and queries of very different sizes.  Bounds as in kv_ref."""
 import math
 
 import pytest
@@ -99,7 +99,7 @@ def test_value_scales_that_are_none(held, n, H, scale):
     assert bool(torch.isnan(out[:, [bad, n - 1]]).all())
 
 
-# --- scales of very different sizes -----------------------------------
+# --- scales and queries of very different sizes -----------------------------------
 
 @pytest.mark.parametrize("held", EIGHT)
 @pytest.mark.parametrize("n,H,G,d", [(1, 4, 2, 64), (2, 8, 2, 128), (20, 4, 2, 64), (20, 4, 2, 128), (40, 4, 2, 128),
@@ -141,3 +141,40 @@ def test_weights_of_rows_that_end_small(held, n):
     fs.fs_cache_write(cache, table.cuda(), torch.arange(m, dtype=torch.int32)[None].cuda(), kk.cuda(), vv.cuda())
     k[:, :m], v[:, :m] = values_of(kk, held), values_of(vv, held)
     check(q, cache, table, k, v, [ctx])
+
+
+@pytest.mark.parametrize("held", EIGHT)
+@pytest.mark.parametrize("n,H,d", [(2, 8, 64), (20, 8, 64), (20, 8, 128), (30, 8, 128), (70, 8, 64), (70, 8, 128)])
+@pytest.mark.parametrize("size", [45, 100, -45, -120])
+def test_one_large_query_leaves_its_neighbours(held, n, H, d, size):
+    """Queries of one token, or of one head, times 2^size: no other row notices."""
+    ctx = [150]
+    q, cache, table, k, v = setting(n, 1, n, ctx, H, 2, d, BF, held, 16)
+    q[0, n // 2] *= 2.0 ** size
+    check(q, cache, table, k, v, ctx)
+    # one head of a token; what others get is as without it
+    q, *_ = setting(n, 1, n, ctx, H, 2, d, BF, held, 16)
+    a, la = attend(q, cache, table, ctx, None)
+    q[0, n // 2, 1] *= 2.0 ** size
+    b, lb = attend(q, cache, table, ctx, None)
+    a[0, n // 2, 1] = b[0, n // 2, 1] = 0
+    la[0, 1, n // 2] = lb[0, 1, n // 2] = 0
+    assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("held", EIGHT)
+@pytest.mark.parametrize("n", [1, 20])
+def test_small_elements_of_a_query(held, n):
+    """Elements 2^-26 of a row's largest that meet the only large elements of the keys."""
+    ctx = [150]
+    q, cache, table, k, v = setting(n, 1, n, ctx, 4, 2, 64, BF, held, 16)
+    m = ctx[0] + n
+    g = gen(m)
+    q[..., 1:] *= 2.0 ** -26
+    q[..., 0] = 1.0
+    kk = (torch.randn(1, m, 2, 64, generator=g) * 2.0 ** 24).bfloat16()
+    kk[..., 0] = 0
+    vv = torch.randn(1, m, 2, 64, generator=g).bfloat16()
+    fs.fs_cache_write(cache, table.cuda(), torch.arange(m, dtype=torch.int32)[None].cuda(), kk.cuda(), vv.cuda())
+    k[:, :m], v[:, :m] = values_of(kk, held), values_of(vv, held)
+    check(q, cache, table, k, v, ctx)

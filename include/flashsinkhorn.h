@@ -461,8 +461,10 @@ fs_status fs_cross_attention_grad(const fs_attention* at, const void* q, const v
  *     amplitude (x cos(p w_i) - y sin(p w_i),  x sin(p w_i) + y cos(p w_i)),
  * w_i = freqs[i] (radians a position; longer contexts take other freqs and
  * amplitude), the rest of the head is copied.  p w_i is reduced in whole numbers
- * of 2^-64 turns, so far positions lose nothing (freqs as large as they like);
- * products are float32, results rounded once.  A result may be its own input.
+ * of 2^-64 turns: at any position the angle is off by 2^-31 turns at most, for |w_i| up
+ * to 2^40, before it becomes a float32 fraction of half a turn.  Pairs whose w_i is not
+ * finite are NaN.  Products are float32, results rounded once.  A result may be its own
+ * input.
  * fs_rotary_grad -- the gradient: the same turned back, of dq, dk (arguments in
  * the places of q, k; results in those of q_out, k_out, with their strides).
  * k and k_out may be NULL (kv_heads 0): queries alone.  FS_ERR_INVALID_ARG as

@@ -8,9 +8,10 @@
 //
 // Angles.  A frequency is kept as a 64-bit fraction of a turn, F = frac(w / 2 pi) 2^64, so
 // that a position's angle is the low 64 bits of p F: whole turns fall away by themselves,
-// with no reduction and no double arithmetic per token (5 operations of a type that this GPU
-// has next to no units for), and a position of 2^31 is off by
-// the rounding of w alone (2^-22 turns; float32 angles would be off by many).
+// with no reduction and no double arithmetic per token (a type that this GPU has next to no
+// units for).  w / 2 pi is formed in two doubles, as one would be off by 2^-53 of it, which at
+// position 2^31 is 2^-22 turns for each turn a position and many for a w of 10^6.  So is F by
+// half of 2^-64 for |w| below 2^40, and a position's angle by 2^-32 turns, cut from p F.
 #include "fs_attn_host.cuh"
 
 #include <algorithm>
@@ -52,19 +53,25 @@ __device__ __forceinline__ uint32_t pack(float x, float y) {
     return (uint32_t)*reinterpret_cast<const uint16_t*>(&b) << 16 | *reinterpret_cast<const uint16_t*>(&a);
 }
 
+// x less whole numbers, in 2^-64
+__device__ __forceinline__ uint64_t fraction(double x) { return (uint64_t)__double2ll_rn((x - rint(x)) * 0x1p64); }
+
 // PAIRS: neighbours (2 i, 2 i + 1) are pairs, else (i, i + half)
 template <typename T, bool PAIRS>
 __global__ void __launch_bounds__(kThreads) k_rotary(const __grid_constant__ Args P) {
-    extern __shared__ float2 turn[];         // [tokens][half] amplitude (cos, sin)
+    extern __shared__ __align__(16) float2 turn[];     // [tokens][half] amplitude (cos, sin)
     __shared__ uint64_t step[kMaxRotary / 2];
+    __shared__ float amplitude[kMaxRotary / 2];        // NaN for a frequency that is not finite
     __shared__ int32_t place[kTokens];
     __shared__ int64_t at[kTokens][4];       // where a token's queries and keys begin: input, output
     const int64_t all = (int64_t)P.B * P.n;
     const int64_t first = (int64_t)blockIdx.x * P.tokens;
     const int count = (int)min((int64_t)P.tokens, all - first);
     for (int i = threadIdx.x; i < P.half; i += kThreads) {
-        const double turns = __ldg(P.freqs + i) * 0.15915494309189533577;     // 1 / (2 pi)
-        step[i] = __double2ull_rz((turns - floor(turns)) * 0x1p64);
+        constexpr double kHigh = 0x1.45f306dc9c883p-3, kLow = -0x1.6b01ec5417056p-57;      // 1 / 2 pi
+        const double w = __ldg(P.freqs + i), turns = w * kHigh;
+        step[i] = fraction(turns) + fraction(fma(w, kLow, fma(w, kHigh, -turns)));
+        amplitude[i] = isfinite(w) ? P.amplitude : __int_as_float(0x7fc00000);
     }
     if (threadIdx.x < count) {
         const unsigned tok = (unsigned)(first + threadIdx.x), b = tok / (unsigned)P.n;
@@ -83,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const __grid_constant__ Arg
         const int32_t top = (int32_t)(((uint64_t)p * step[i]) >> 32);
         float sn, cs;
         sincospif((float)top * 0x1p-31f, &sn, &cs);
-        turn[e] = make_float2(P.amplitude * cs, P.amplitude * (P.back ? -sn : sn));
+        turn[e] = make_float2(amplitude[i] * cs, amplitude[i] * (P.back ? -sn : sn));
     }
     __syncthreads();
     const int heads = P.heads[0] + P.heads[1];

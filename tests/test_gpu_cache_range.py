@@ -1,12 +1,13 @@
-"""Tree attention at the ends of its range: keys that no row or not every row sees,
-scales and queries of very different sizes.  Bounds as in kv_ref."""
+"""Tree attention and rotary positions at the ends of their ranges: keys that no row or not every row
+sees, scales and queries of very different sizes, far angles.  Bounds as in kv_ref."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
 
 from streaming_sinkhorn_solver_gb300 import binding as fs
-from tests.kv_ref import quantise, tree64
+from tests.kv_ref import quantise, rotary64, tree64
 from tests.test_gpu_cache import BF, E4M3, HALF, I8, NAN, check, gen, random_parents, setting, within
 
 pytestmark = pytest.mark.gpu
@@ -178,3 +179,54 @@ def test_small_elements_of_a_query(held, n):
     fs.fs_cache_write(cache, table.cuda(), torch.arange(m, dtype=torch.int32)[None].cuda(), kk.cuda(), vv.cuda())
     k[:, :m], v[:, :m] = values_of(kk, held), values_of(vv, held)
     check(q, cache, table, k, v, ctx)
+
+
+# --- angles -------------------------------------------------------------------
+
+TURN = Fraction("0.159154943091895335768883763372514362034459645740456448747667344058896797634226535")    # 1 / 2 pi
+
+
+def exact_rotary(x, freqs, pos, interleaved, back):
+    """(result, bound) of rotary64, its angles from whole numbers.  Beside a float32 angle's bound
+    the 2^-32 turns that a position's angle is cut at: 2 pi 2^-32, within its margin."""
+    half = freqs.numel()
+    turns = torch.tensor([[[float((int(p) * Fraction(float(w)) * TURN) % 1) for w in freqs] for p in row]
+                          for row in pos], dtype=torch.float64)
+    near = turns * (2 * math.pi)
+    want, tol = rotary64(x, torch.ones(half, dtype=torch.float64), torch.zeros_like(pos), interleaved, 1.0, back)
+    c, s = torch.cos(near)[:, :, None], torch.sin(near)[:, :, None] * (-1.0 if back else 1.0)
+    at = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else (slice(0, half), slice(half, 2 * half))
+    a, b = x.double()[..., at[0]], x.double()[..., at[1]]
+    want[..., at[0]], want[..., at[1]] = a * c - b * s, a * s + b * c
+    u = torch.finfo(x.dtype).eps / 2
+    tol[..., at[0]] = tol[..., at[1]] = 2.0 ** -21 * (a.abs() + b.abs())
+    tol[..., :2 * half] += u * want[..., :2 * half].abs() + 2.0 ** -25
+    return want, tol
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d", [16, 17])
+def test_rotary_of_frequencies_of_any_size(interleaved, d):
+    g = gen(d)
+    w = torch.tensor([1e6 + 0.3, 1e9, -3.7e5, 2.0 ** 40 - 1.5, 1e-9, -1e-12, 6.283185307179586, 0.0],
+                     dtype=torch.float64)
+    pos = torch.tensor([[0, 1, -1, 10 ** 6, 2 ** 31 - 1, -(2 ** 31), 123456789]], dtype=torch.int32)
+    q = torch.randn(1, 7, 3, d, generator=g).half()
+    for fn, back in ((fs.fs_rotary, False), (fs.fs_rotary_grad, True)):
+        got, _ = fn(q.cuda(), None, w.cuda(), pos.cuda(), interleaved=interleaved)
+        within(got, *exact_rotary(q, w, pos, interleaved, back), "rotary")
+
+
+@pytest.mark.parametrize("d", [16, 21])
+@pytest.mark.parametrize("bad", [NAN, math.inf, -math.inf])
+def test_rotary_of_frequencies_that_are_not_numbers(d, bad):
+    g = gen(d)
+    w = torch.tensor([1.0, bad, 0.01, 0.001], dtype=torch.float64)
+    pos = torch.tensor([[0, 1, 2, 3]], dtype=torch.int32)
+    q = torch.randn(1, 4, 2, d, generator=g).bfloat16()
+    got = fs.fs_rotary(q.cuda(), None, w.cuda(), pos.cuda())[0].cpu()
+    assert bool(torch.isnan(got[..., [1, 5]]).all())
+    w[1] = 0.1
+    fine = fs.fs_rotary(q.cuda(), None, w.cuda(), pos.cuda())[0].cpu()
+    rest = [c for c in range(d) if c not in (1, 5)]
+    assert torch.equal(got[..., rest], fine[..., rest])

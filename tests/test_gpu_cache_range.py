@@ -1,5 +1,6 @@
 """Tree attention and rotary positions at the ends of their ranges: keys that no row or not every row
-sees, scales and queries of very different sizes, far angles.  Bounds as in kv_ref."""
+sees, scales and queries of very different sizes, far angles; short
+last blocks, padded rows.  Bounds as in kv_ref."""
 import math
 from fractions import Fraction
 
@@ -230,3 +231,56 @@ def test_rotary_of_frequencies_that_are_not_numbers(d, bad):
     fine = fs.fs_rotary(q.cuda(), None, w.cuda(), pos.cuda())[0].cpu()
     rest = [c for c in range(d) if c not in (1, 5)]
     assert torch.equal(got[..., rest], fine[..., rest])
+
+
+# --- ends of blocks, rows that are padded ----------------------------------------
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("B,n,H,G,d,rotary,skew", [
+    (1, 8197, 2, 1, 32, 32, False), (3, 2777, 3, 1, 40, 16, False), (1, 2051, 2, 2, 24, 16, False),
+    (1, 3001, 2, 1, 17, 8, False), (2, 4103, 2, 1, 16, 16, True), (1, 6149, 1, 0, 9, 2, False)])
+def test_rotary_of_blocks_that_end_short(interleaved, B, n, H, G, d, rotary, skew):
+    """Several tokens to a block, the last block with fewer; rows that take 16-byte accesses and others."""
+    g = gen(n)
+    q, k = (torch.randn(B, n, h, d, generator=g).bfloat16() for h in (H, G))
+    pos = torch.randint(0, 100000, (B, n), generator=g, dtype=torch.int32)
+    w = torch.from_numpy(fs.fs_rotary_frequencies(rotary))
+
+    def there(x):
+        if not skew:
+            return x.cuda()
+        y = torch.zeros(*x.shape[:3], d + 3, dtype=BF, device="cuda")[..., 1:d + 1]
+        y.copy_(x)
+        return y
+
+    for fn, back in ((fs.fs_rotary, False), (fs.fs_rotary_grad, True)):
+        got = fn(there(q), there(k) if G else None, w.cuda(), pos.cuda(), interleaved=interleaved)
+        for x, y in zip((q, k), got):
+            if y is not None:
+                within(y, *rotary64(x, w, pos, interleaved, 1.0, back), "rotary")
+
+
+@pytest.mark.parametrize("held", EIGHT)
+@pytest.mark.parametrize("dtype", [BF, HALF])
+@pytest.mark.parametrize("B,n,ctx,H,G,d,page", [
+    (2, 9, [70, 33], 8, 2, 8, 16), (1, 40, [200], 4, 1, 24, 8), (2, 27, [333, 90], 10, 2, 72, 16),
+    (1, 100, [190], 4, 2, 72, 64), (1, 60, [1000], 8, 1, 104, 32), (2, 2, [300, 9], 4, 2, 72, 16)])
+def test_rows_that_are_padded_to_whole_pieces(held, dtype, B, n, ctx, H, G, d, page):
+    """Heads of no multiple of 16, as fs_cache_new lays them out: the padding of the rows may hold anything."""
+    g = gen(n + d)
+    per = -(-(max(ctx) + n) // page)
+    cache = fs.fs_cache_new(B * per + 1, G, page, d, held)
+    wide = cache.k.stride(2)
+    for x in (cache.k, cache.v):
+        x.as_strided((B * per + 1, G, page, wide), x.stride()).view(torch.int8).fill_(0x7f)
+    for x in (cache.k_scale, cache.v_scale):
+        x.fill_(NAN)
+    table = torch.randperm(B * per + 1, generator=g)[:B * per].int().view(B, per)
+    k, v = (torch.randn(B, per * page, G, d, generator=g).to(dtype) for _ in range(2))
+    at = torch.arange(per * page, dtype=torch.int32).expand(B, -1).clone()
+    for b in range(B):
+        at[b, ctx[b] + n:] = -1
+    fs.fs_cache_write(cache, table.cuda(), at.cuda(), k.cuda(), v.cuda())
+    q = (2 * torch.randn(B, n, H, d, generator=g)).to(dtype)
+    parents = random_parents(gen(n), B, n, absent=n // 5)
+    check(q, cache, table, values_of(k, held), values_of(v, held), ctx, parents)

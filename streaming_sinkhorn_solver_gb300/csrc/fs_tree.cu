@@ -50,17 +50,20 @@ int choose_tc_splits(int64_t blocks, int m, int sms) {
     return best;
 }
 
-// Whether the few-row kernel takes a call: up to one block of 8 rows to a key head, in 16 bits only
-// where there is little to read (as far as the table reaches), and caches whose rows cannot be
-// copied by the page.  Measured (few rows, tensor cores): 8 key heads of 128, one sequence of 2000
-// keys, 4 rows: 10 us, 15 us in either type; 38 of 8192 keys, 4 rows: e4m3 119 us, 169, bfloat16
-// 240, 186; 19 of 4096, bfloat16, 318 MB: 68, 54; 12 rows: e4m3 47, 49, bfloat16 67, 55.  Heads
-// of 64 in bfloat16 part at 235 MB, of 128 at 105.
+// Whether the few-row kernel takes a call: caches whose rows cannot be copied by the page, and up to
+// one block of 8 rows to a key head, in 16 bits and heads above 64 only where there is little to read.
+// The table's reach stands for the lengths, which are on the GPU.
+// Measured with 4 rows on each of 8 key heads (few rows, tensor cores), us:
+//   bfloat16 heads of 128: 34 MB 15, 16; 67 MB 24, 22; 134 MB 38, 30; 319 MB 71, 54; 1275 MB 240, 188
+//   bfloat16 heads of 64:  34 MB 14, 15; 67 MB 22, 18; 134 MB 34, 35; 319 MB 59, 59; 1275 MB 199, 203
+//   e4m3 of 128, 64, as many keys: 34 MB 14, 19 and 14, 21; 319 MB 40, 51 and 44, 82; 1275 MB 117, 172
+//   and 129, 293
+// (Beyond 8 rows, where a cache would be read twice: 12 rows of heads of 128, e4m3 47, 49, bfloat16 67, 55.)
 bool few_rows(const Args& a) {
-    constexpr double kLittle = 128e6;
+    constexpr double kLittle = 48e6;
     if (!tc_copies(a.c)) return true;
     if (a.R * a.n > 8) return false;
-    return a.c.held != kv::HELD_16 || 4.0 * a.c.B * a.c.G * a.c.reach() * a.d <= kLittle;
+    return a.c.held != kv::HELD_16 || a.d <= 64 || 4.0 * a.c.B * a.c.G * a.c.reach() * a.d <= kLittle;
 }
 
 fs_status tree_entry(const fs_cache* cache, const fs_tree* t, const void* q, void* out, float* lse,
@@ -143,7 +146,6 @@ fs_status tree_entry(const fs_cache* cache, const fs_tree* t, const void* q, voi
     if (few) {
         p.part = part;
         p.splits = splits;
-        p.dp = a.d;
         p.counters = c.ws->counters;
         FS_CUDA(launch_few(p, c.stream));
     } else {

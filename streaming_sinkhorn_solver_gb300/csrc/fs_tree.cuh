@@ -87,7 +87,6 @@ struct FewArgs {
     Args a;
     Partials part;
     int splits, groups, row_blocks;
-    int dp;                // elements of a partial row: d, a multiple of 8
     unsigned* counters;    // [batch x key heads x groups], zero between calls
 };
 constexpr int kFewKeys = 128;          // the splits are whole multiples of these keys

@@ -604,15 +604,15 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
                            : Q8         ? kv::log_sum(top - kShift, total)
                                         : top - kShift + lg2(total);
         T* out = out_row(row);
-        float* part = P.part.out + (split * P.part.rows + at) * P.dp;
-        for (int e = lane; e < P.dp; e += 32) {
+        float* part = P.part.out + (split * P.part.rows + at) * a.d;
+        for (int e = lane; e < a.d; e += 32) {
             float x = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) x = fmaf(f[w], sO[w * kWarpRows + row * HD + e], x);
             x = total == 0.f ? 0.f : x * inv;
             if (P.splits > 1)
                 part[e] = x;
-            else if (e < a.d)
+            else
                 out[e] = from_f<T>(x);
         }
         if (lane == 0) {
@@ -680,9 +680,9 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
         for (int x = 0; x < kSums; ++x) {
             const int e = threadIdx.x + x * 32 * kWarps, row = e / kQuads, col = 4 * (e % kQuads);
             if (row >= nrows || col >= a.d) continue;
-            const float* src = P.part.out + (s0 * P.part.rows + place(row)) * P.dp + col;
+            const float* src = P.part.out + (s0 * P.part.rows + place(row)) * a.d + col;
             const float* w = sO + row * kSome;
-            const int64_t step = P.part.rows * P.dp;
+            const int64_t step = P.part.rows * a.d;
 #pragma unroll 16
             for (int i = 0; i < some; ++i) {
                 const float4 y = *reinterpret_cast<const float4*>(src + i * step);
@@ -710,8 +710,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_tree_few(const __grid_constant_
         const float inv = sSum[row] == 0.f ? 0.f : 1.f / sSum[row];
         const float y[4] = {acc[x].x * inv, acc[x].y * inv, acc[x].z * inv, acc[x].w * inv};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (col + i < a.d) out[i] = from_f<T>(y[i]);
+        for (int i = 0; i < 4; ++i) out[i] = from_f<T>(y[i]);
     }
 }
 

@@ -38,7 +38,7 @@ __device__ __forceinline__ float two_to(int n) { return __int_as_float((127 + n)
 
 // Queries in bfloat16 beside an 8-bit cache become float16, each row times the power of two that
 // brings its largest finite magnitude to [2^14, 2^15): float16 holds elements from 2^-31 of that on to all
-// their bits, others to 2^-39 of it.  (One power for a block of rows left nothing of a row
+// their bits, others to 2^-39 of it.  (One power for a block of any rows left nothing of a row
 // beside one 2^40 times as large.)
 // top: the larger of it and two bfloat16 magnitudes
 __device__ __forceinline__ uint32_t finite_top(uint32_t top, uint32_t w) {

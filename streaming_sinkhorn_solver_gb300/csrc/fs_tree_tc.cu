@@ -16,9 +16,9 @@
 //   O_i = sum_j P_ij code_j,   sum_i = sum_j P_ij / vs_j.
 // Where the scales are so far apart that P_ij could be below float32's numbers and P_ij / vs_j still
 // count (rows of zeros, whose scale is 2^-89, beside others), the sum is that of the terms'
-// own exponentials, 2^{x_ij - log2 vs_j - ref_i}.
-// Queries in bfloat16 become float16 for that, each row times a power of two (query_shift) that its
-// scores are divided by.
+// own exponentials, 2^{x_ij - log2 vs_j - ref_i}: those tiles are weighed by a loop of their own.
+// Queries in bfloat16 become float16 for that, times a power of two (query_shift) that their scores are
+// divided by: one for the block where its rows are alike, else one for each.
 //
 // A softmax thread holds 16 keys of each of 4 rows (the 16 x 256-bit form of TMEM loads), not
 // a row: the scales of its keys are then 24 loads of 8 bytes instead of 48 of 16 that
@@ -107,7 +107,7 @@ struct TileBits {
 };
 struct TileScales {
     float kc[kKeys], lv[kKeys], iv[kKeys];   // of the scores; log2 and inverse of the value scale
-    int apart, pad[3];                       // the tile's sums are formed without iv, which is 0
+    int odd[2], pad[2];                      // of 32 keys each: scales apart, or keys of the tree
 };
 struct TcBars {
     uint64_t full[2][8], free_raw[2][8];     // copies landed; 8 bits: the ring they land in
@@ -135,7 +135,8 @@ struct Smem {
     static constexpr int parents = join;                                      // (done with before the join)
     static constexpr int bars = join + (C::kAlternate ? 4 * 4 * 128 : 4 * kv::kMaxTree);
     static_assert(4 * 4 * 128 >= 4 * kv::kMaxTree, "parents");
-    static constexpr int down = bars + (int)sizeof(TcBars);                   // [row]: what scores are multiplied by
+    static constexpr int shift = bars + (int)sizeof(TcBars);                  // of the queries, by warps: [most, least]
+    static constexpr int down = shift + 2 * 4 * kSoftWarps;                   // [row]: what scores are multiplied by
     static constexpr int bytes = down + (C::Q8 ? 4 * C::kRows : 0);
     static_assert(bits % 16 == 0 && bars % 8 == 0, "alignment");
     static_assert(1024 + bytes <= kSmemLimit, "shared memory");
@@ -205,6 +206,18 @@ __device__ __forceinline__ bool nonfinite16(const uint4& x) {
         }
     }
     return bad;
+}
+
+// Queries in bfloat16 beside an 8-bit cache: rows whose largest elements are within 2^12 of the block's
+// take its power of two, which their scores are divided by with the keys' scales; in a block with
+// others each row has its own, and its scores take a factor more.
+__device__ __forceinline__ bool apart_rows(int most, int least) { return most - least > 12; }
+__device__ __forceinline__ void block_shift(const int* shift, int& most, int& least) {
+#pragma unroll
+    for (int k = 0; k < kSoftWarps; ++k) {
+        most = max(most, shift[k]);
+        least = min(least, shift[kSoftWarps + k]);
+    }
 }
 
 // A block's share of the work.
@@ -310,7 +323,7 @@ __device__ __forceinline__ void copy_tiles(const TcArgs& P, const Share& w, uint
 // operand tile.  16 bits: of the values, tiles with keys of the tree are looked through.
 template <int HD, int HELD, bool BF, int MODE, int KV>
 __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8_t* smem, TcBars& bar, int tid,
-                                          int group) {
+                                          int group, float mul) {
     using C = Tc<HD, HELD, MODE>;
     using M = Smem<HD, HELD, MODE>;
     constexpr bool Q8 = C::Q8;
@@ -335,7 +348,6 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
     int scales = j_at % C::kScales, bits = j_at % C::kBits;
     Ring before;               // the tile before this one: they are handed on in their order
     if (kGroups > 1 && group == 0) before.step(1, C::kRing);
-    int most = -(1 << 10);     // exponent of the value scales of the tiles so far that go to the same stream
     // pieces of a row are in neighbouring lanes
     const auto look = [&](const uint4& x, int key0, int row, uint8_t* flags) {
         uint32_t bad = key0 + row >= w.ctx && nonfinite16<HELD, BF>(x);
@@ -369,13 +381,14 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
                         x[i] = make_uint4(0, 0, 0, 0);
                 }
             }
-            float ks = 0.f, vs = 0.f, vs2 = 0.f;   // (anything where there is no page)
+            float ks = 0.f, vs = 0.f;              // (anything where there is no page)
+            uint32_t counted = 0;
             const bool scaled = KV == 0 && tid < kKeys;
             if (scaled) {
                 const float* s = reinterpret_cast<const float*>(smem + M::raw_scale) + from.slot * 2 * kKeys + tid;
                 ks = s[0];
                 vs = s[kKeys];
-                vs2 = s[kKeys + (tid ^ 32) - tid];         // the other 32 keys', which both warps look at
+                counted = tb.counted[tid >> 5];
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.free_raw[KV][from.slot]);
@@ -404,20 +417,15 @@ __device__ __forceinline__ void fit_tiles(const TcArgs& P, const Share& w, uint8
                 TileScales& ts = reinterpret_cast<TileScales*>(smem + M::scales)[scales];
                 float kc, lv;
                 kv::weigh(ks, vs, kc, lv);
-                ts.kc[tid] = kc * a.scale2;
+                ts.kc[tid] = kc * mul;
                 ts.lv[tid] = lv;
-                // P / vs is lost where P < 2^-126: 2^-62 of the sum at most while the scales are within 2^64 of
-                // the largest so far, which a reference may be from.  The tree's keys, which not every row
-                // sees, have no say in how others are summed.
-                const bool on = kv::weighable(vs) && tb.counted[tid >> 5] >> lane & 1u;
-                const bool on2 = kv::weighable(vs2) && tb.counted[tid >> 5 ^ 1] >> lane & 1u;
-                const int e = __float_as_int(vs) >> 23, e2 = __float_as_int(vs2) >> 23;
-                const int least = __reduce_min_sync(0xffffffffu, min(on ? e : 1 << 10, on2 ? e2 : 1 << 10));
-                const int top = __reduce_max_sync(0xffffffffu, max(on ? e : -(1 << 10), on2 ? e2 : -(1 << 10)));
-                if (!mixed) most = max(most, top);
-                const bool apart = mixed || most - least > 64;
-                ts.iv[tid] = apart || !kv::weighable(vs) ? 0.f : __fdividef(1.f, vs);
-                if (tid == 0) ts.apart = apart;
+                ts.iv[tid] = kv::weighable(vs) ? __fdividef(1.f, vs) : 0.f;
+                // P / vs is lost where P < 2^-126: 2^-62 of the sum at most while all scales so far, which a
+                // reference may be from, are 2^-48 to 2^16.  The tree's keys, which not every row sees, have
+                // no say in how others are summed.
+                const bool on = counted >> lane & 1u;
+                const bool odd = mixed || __any_sync(0xffffffffu, on && !(vs >= 0x1p-48f && vs <= 0x1p16f));
+                if (lane == 0) ts.odd[tid >> 5] = odd;
             }
         } else {
             if (!warp_wait(&bar.last[j - mixed_from], 0, a.err, ERR_TIMEOUT_PRODUCER)) return;
@@ -465,6 +473,7 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     TcBars& bar = *reinterpret_cast<TcBars*>(smem + M::bars);
     uint32_t* sWords = reinterpret_cast<uint32_t*>(smem + M::words);
+    int* sShift = reinterpret_cast<int*>(smem + M::shift);
     float* sDown = reinterpret_cast<float*>(smem + M::down);
     int* sParents = reinterpret_cast<int*>(smem + M::parents);
 
@@ -546,6 +555,7 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
             }
         }
         if (Q8 && BF) {
+            int up[kMine], most = -126, least = 126;
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
                 uint32_t top = 0;
@@ -553,10 +563,24 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
                 for (int k = 0; k < 4; ++k) top = finite_top(top, x[i][k]);
 #pragma unroll
                 for (int o = kPieces / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const int up = query_shift(top);
-                if (u == 0) sDown[threadIdx.x / kPieces + i * kStep] = two_to(-up);
+                up[i] = query_shift(top);
+                least = min(least, up[i]);
+                if (top != 0) most = max(most, up[i]);         // (rows of zeros take any)
+            }
+            least = __reduce_min_sync(0xffffffffu, least);
+            most = __reduce_max_sync(0xffffffffu, most);
+            if (lane == 0) {
+                sShift[warp] = most;
+                sShift[kSoftWarps + warp] = least;
+            }
+            named_sync(1, kSoftThreads);
+            block_shift(sShift, most, least);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[i][k] = shifted_pair(x[i][k], two_to(up));
+            for (int i = 0; i < kMine; ++i) {
+                const int more = apart_rows(most, least) ? min(up[i] - least, 126) : 0;
+                if (u == 0) sDown[threadIdx.x / kPieces + i * kStep] = two_to(-more);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[i][k] = shifted_pair(x[i][k], two_to(least + more));
             }
         }
 #pragma unroll
@@ -595,11 +619,17 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
     const uint32_t tmem = bar.tmem;
 
     if (warp >= kFit0) {
+        float mul = a.scale2;
+        if (Q8 && BF) {
+            int most = -126, least = 126;
+            block_shift(sShift, most, least);
+            mul *= two_to(-least);
+        }
         const int tid = (threadIdx.x - 32 * kFit0) & (kFitters - 1), fit = (warp - kFit0) >> 1;
         if (fit < C::kGroups)
-            fit_tiles<HD, HELD, BF, MODE, 0>(P, w, smem, bar, tid, fit);
+            fit_tiles<HD, HELD, BF, MODE, 0>(P, w, smem, bar, tid, fit, mul);
         else
-            fit_tiles<HD, HELD, BF, MODE, 1>(P, w, smem, bar, tid, fit - C::kGroups);
+            fit_tiles<HD, HELD, BF, MODE, 1>(P, w, smem, bar, tid, fit - C::kGroups, mul);
     } else if (warp >= kMma0) {
         const int t = warp - kMma0;
         const int n_mine = kAlternate ? (nt + 1 - t) / 2 : nt;
@@ -650,10 +680,13 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
         const int row_t = row0 + (kAlternate ? 0 : 128 * t) + quarter * kQuarter;    // the warp's first row
         const float mul = a.scale2;                  // (8 bits: with the keys' scales)
         const uint64_t mul2 = pk(mul, mul);
-        float down[kLaneRows];                       // of the rows' queries
-#pragma unroll
-        for (int k = 0; k < kLaneRows; ++k)
-            down[k] = Q8 && BF ? sDown[(kAlternate ? 0 : 128 * t) + quarter * kQuarter + g + 8 * k] : 1.f;
+        bool factors = false;                        // of the rows' scores
+        if (Q8 && BF) {
+            int most = -126, least = 126;
+            block_shift(sShift, most, least);
+            factors = apart_rows(most, least);
+        }
+        const float* down = sDown + (kAlternate ? 0 : 128 * t) + quarter * kQuarter + g;
         // of rows g + 8 k of the warp; a lane's part of the sum
         float ref[kLaneRows], sum[kLaneRows];
 #pragma unroll
@@ -661,12 +694,12 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
             ref[k] = -INFINITY;
             sum[k] = 0.f;
         }
-        bool ok = true;
-        for (int j = 0; j < n_mine; ++j) {
-            const int tile = kAlternate ? 2 * j + t : j;
+        // A tile of the stream, scored: P and the sums; false if a wait ran out.  Beside an 8-bit cache `plain`
+        // takes tiles whose keys all rows see, in blocks without factors and with scales near one another.
+        bool apart = false;                          // scales that were not, so far
+        const auto weigh_tile = [&](auto plain, int j, int tile) -> bool {
+            constexpr bool kPlain = decltype(plain)::value;
             const int key0 = (t0 + tile) * kKeys;
-            if (!(ok = warp_wait(&bar.sfull[t], j & 1, a.err, ERR_TIMEOUT_EPILOGUE))) break;
-            tc_fence_after();
             // v[32 h + 4 i + e]: column 8 i + 2 t4 + (e & 1) of row g + 8 (2 h + (e >> 1))
             float v[16 * kLaneRows];
             tmem_ld16x64(tS, v);
@@ -687,23 +720,32 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.sfree[t]);
+            if (Q8 && BF && !kPlain && factors) {
+#pragma unroll
+                for (int k = 0; k < kLaneRows; ++k) {
+                    const float f = down[8 * k];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float* x = v + 32 * (k >> 1) + 4 * i + 2 * (k & 1);
+                        upk(mul2f(pk(x[0], x[1]), pk(f, f)), x[0], x[1]);
+                    }
+                }
+            }
             if (Q8) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
                     for (int k = 0; k < kLaneRows; ++k) {
                         float* x = v + 32 * (k >> 1) + 4 * i + 2 * (k & 1);
-                        uint64_t f = kc[Q8 ? i : 0];
-                        if (BF) f = mul2f(f, pk(down[k], down[k]));
-                        upk(fma2(pk(x[0], x[1]), f, lv[Q8 ? i : 0]), x[0], x[1]);
+                        upk(fma2(pk(x[0], x[1]), kc[Q8 ? i : 0], lv[Q8 ? i : 0]), x[0], x[1]);
                     }
             }
-            const bool mixed = tile >= mixed_from;
+            const bool mixed = !kPlain && tile >= mixed_from;
             if (mixed || (counted.x & counted.y) != 0xffffffffu) {
                 uint32_t bad[2] = {0, 0};
                 if (kLooks<HELD> && mixed) {
                     // the values' check may come behind the scores
-                    if (!(ok = warp_wait(&bar.looked[tile - mixed_from], 0, a.err, ERR_TIMEOUT_EPILOGUE))) break;
+                    if (!warp_wait(&bar.looked[tile - mixed_from], 0, a.err, ERR_TIMEOUT_EPILOGUE)) return false;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) bad[x] = __ballot_sync(0xffffffffu, tb.poison[32 * x + lane] != 0);
                 }
@@ -766,8 +808,8 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
                 }
                 if (__any_sync(0xffffffffu, f != 1.f)) {
                     // O is still once the products of tile j - 1 are done (j > 0 here)
-                    if (!(ok = warp_wait(&bar.pfree[t][buf ^ 1], ((j - 1) >> 1) & 1, a.err, ERR_TIMEOUT_EPILOGUE)))
-                        break;
+                    if (!warp_wait(&bar.pfree[t][buf ^ 1], ((j - 1) >> 1) & 1, a.err, ERR_TIMEOUT_EPILOGUE))
+                        return false;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < dsteps * 16; c += 16) {
@@ -791,7 +833,7 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
             uint64_t s[kLaneRows];
 #pragma unroll
             for (int k = 0; k < kLaneRows; ++k) s[k] = 0;
-            if (Q8 && ts.apart) {
+            if (Q8 && !kPlain && apart) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float2 l = *reinterpret_cast<const float2*>(ts.lv + 8 * i + 2 * t4);
@@ -807,7 +849,7 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
             uint32_t p[8 * kLaneRows];         // p[16 h + 2 i + (k & 1)]
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint64_t iv = Q8 ? *reinterpret_cast<const uint64_t*>(ts.iv + 8 * i + 2 * t4) : 0;
+                const uint64_t iv = Q8 && (kPlain || !apart) ? *reinterpret_cast<const uint64_t*>(ts.iv + 8 * i + 2 * t4) : 0;
 #pragma unroll
                 for (int k = 0; k < kLaneRows; ++k) {
                     const float* x = v + 32 * (k >> 1) + 4 * i + 2 * (k & 1);
@@ -832,6 +874,32 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
                 upk(s[k], f0, f1);
                 sum[k] += f0 + f1;
             }
+            return true;
+        };
+        // Beside an 8-bit cache the plain tiles, as long as they come, then the others, in two loops.  (All
+        // in one, or each of two bodies by a test in one loop, took the registers that keep a tile's stages
+        // side by side: 19 x 64 tokens, 4096 e4m3 keys 125 and 105 us for 101, 32 x 16 tokens 167 for
+        // 159.)
+        bool ok = true;
+        int j = 0;
+        const auto odd = [&](int tile) {
+            const int2 x = *reinterpret_cast<const int2*>(
+                reinterpret_cast<const TileScales*>(smem + M::scales)[tile % C::kScales].odd);
+            return __any_sync(0xffffffffu, (x.x | x.y) != 0) != 0;
+        };
+        for (; Q8 && !factors && j < n_mine; ++j) {
+            const int tile = kAlternate ? 2 * j + t : j;
+            if (!(ok = warp_wait(&bar.sfull[t], j & 1, a.err, ERR_TIMEOUT_EPILOGUE))) break;
+            if (odd(tile)) break;
+            tc_fence_after();
+            if (!(ok = weigh_tile(std::integral_constant<bool, Q8>(), j, tile))) break;
+        }
+        for (; j < n_mine && ok; ++j) {
+            const int tile = kAlternate ? 2 * j + t : j;
+            if (!(ok = warp_wait(&bar.sfull[t], j & 1, a.err, ERR_TIMEOUT_EPILOGUE))) break;
+            tc_fence_after();
+            if (Q8) apart = apart || odd(tile);
+            ok = weigh_tile(std::false_type(), j, tile);
         }
         if (n_mine > 0 && ok) {
             const int j = n_mine - 1;

@@ -165,6 +165,31 @@ def test_one_large_query_leaves_its_neighbours(held, n, H, d, size):
 
 
 @pytest.mark.parametrize("held", EIGHT)
+@pytest.mark.parametrize("dtype", [BF, HALF])
+@pytest.mark.parametrize("n,H,G,d", [(1, 8, 2, 128), (20, 8, 2, 64), (20, 8, 2, 128), (30, 8, 2, 64), (30, 8, 2, 128),
+                                     (70, 8, 2, 64), (70, 8, 2, 128)])
+@pytest.mark.parametrize("first", [0, 500])
+def test_large_queries_and_scales_apart_over_many_tiles(held, dtype, n, H, G, d, first):
+    """Both at once, from some tile on, with a tree and padding: every loop of a block, one after the other."""
+    ctx = [900, 333]
+    q, cache, table, k, v = setting(n, 2, n, ctx, H, G, d, dtype, held, 32)
+    g = gen(n + first)
+    m = max(ctx) + n
+    if dtype == BF:
+        q[0, n // 3, 1] *= 2.0 ** 50
+    kk, vv = (torch.randn(2, m, G, d, generator=g).to(dtype) for _ in range(2))
+    vv[:, first::5] = 0
+    if dtype == BF:
+        vv[:, first + 3::7] *= 2.0 ** 40
+    at = torch.arange(m, dtype=torch.int32).expand(2, m).clone()
+    for b in range(2):
+        at[b, ctx[b] + n:] = -1
+    fs.fs_cache_write(cache, table.cuda(), at.cuda(), kk.cuda(), vv.cuda())
+    k[:, :m], v[:, :m] = values_of(kk, held), values_of(vv, held)
+    check(q, cache, table, k, v, ctx, random_parents(g, 2, n, absent=n // 8))
+
+
+@pytest.mark.parametrize("held", EIGHT)
 @pytest.mark.parametrize("n", [1, 20])
 def test_small_elements_of_a_query(held, n):
     """Elements 2^-26 of a row's largest that meet the only large elements of the keys."""

@@ -519,7 +519,9 @@ typedef struct fs_cache {
     int64_t table_stride;     /* from one row to the next */
     void *k, *v;              /* rows at page s[0] + head s[1] + token s[2], s = k_stride, v_stride */
     float *k_scale, *v_scale; /* 8 bits: scales at page s[0] + head s[1] + token; else ignored */
-    int64_t k_stride[3], v_stride[3]; /* rows start at multiples of 16 bytes, in 8 bits of 8 */
+    int64_t k_stride[3], v_stride[3]; /* rows start at multiples of 16 bytes, in 8 bits of 8; of
+                                 16 there too serves trees of more than 8 rows a key head, which
+                                 otherwise read the cache once for every 16 of them */
     int64_t k_scale_stride[2], v_scale_stride[2];
     const int32_t* table;     /* batch rows of table_pages */
 } fs_cache;
@@ -539,16 +541,16 @@ typedef struct fs_cache_rows {
  * fs_cache_write -- writes token t of sequence b at position at[b][t]; tokens at
  * negative positions, beyond the table or without a page are left out, and every
  * other row of the cache is left as it is.  The rows that a call writes are
- * distinct: of two tokens at one place, parts of either may be left there.
- * Captured as fs_rotary.
+ * distinct: of two tokens at one place, parts of either may be left there.  k and v lie
+ * outside the cache.  Captured as fs_rotary.
  */
 fs_status fs_cache_write(const fs_cache* cache, const fs_cache_rows* rows, const void* k,
                          const void* v, void* stream);
 
 /*
- * fs_cache_read -- positions 0 .. n - 1 of every sequence, rounded once to
- * rows->dtype, as the k and v of fs_cross_attention; zeros from at[b] on (at NULL:
- * none) and where there is no page.  Captured as fs_rotary.
+ * fs_cache_read -- positions 0 .. n - 1 of every sequence, in 8 bits code x scale in
+ * float32 and then rows->dtype, as the k and v of fs_cross_attention; zeros from at[b]
+ * on (at NULL: none) and where there is no page.  Captured as fs_rotary.
  */
 fs_status fs_cache_read(const fs_cache* cache, const fs_cache_rows* rows, void* k, void* v,
                         void* stream);
@@ -567,13 +569,19 @@ fs_status fs_cache_read(const fs_cache* cache, const fs_cache_rows* rows, void* 
  * ctx_len is taken into [0, table_pages x page_size]; positions beyond the table do
  * not count.  Keys and values that a token does not see never reach its results,
  * whatever they hold; of the tree's own values that it sees, one that is not finite
- * makes the whole of its row NaN.
+ * makes the whole of its row NaN, lse too, as does any value with a NaN scale.
  *
  * out (batch x n x heads x d) of the type of q, lse float32 (batch x heads x n),
  * contiguous.  Numerics as fs_cross_attention; a cache in 8 bits is multiplied as
  * float16 holds its codes (exactly), keys' scales enter the scores, values' the
- * weights, in float32.  Bitwise deterministic.  Captured as fs_cross_attention;
- * errors as there.
+ * weights, in float32.  Weights are rounded once to the type of the products (float16
+ * for a cache in 8 bits); up to 8 rows (n x heads / kv_heads) of a bfloat16 cache keep
+ * them in two parts, for heads above 64 while the tables of all sequences reach no
+ * further than 48 MB of keys and values.  Queries in bfloat16 become float16 beside a cache in 8 bits:
+ * exactly, but for elements below 2^-18 of the largest of their row, which are off by up
+ * to 2^-27 of that.  Bitwise deterministic.  Captured as fs_cross_attention; errors as
+ * there.  The kernel and how its keys are split go by what the table can hold, not by
+ * ctx_len, which is on the GPU: a table no wider than the longest sequence serves best.
  */
 typedef struct fs_tree {
     int32_t dtype;            /* fs_dtype of q and out: FS_DTYPE_BF16 or FS_DTYPE_F16, and that of

@@ -1007,7 +1007,8 @@ def fs_rotary_grad(dq, dk, freqs, pos, *, interleaved: bool = False, amplitude: 
 class KVCache(NamedTuple):
     """Keys and values in pages: k and v (pages, kv_heads, page_size, d), bfloat16, float16,
     float8_e4m3fn or int8; 8-bit ones with float32 scales (pages, kv_heads, page_size).  Any
-    strides whose rows start at multiples of 16 bytes (8 bits: of 8)."""
+    strides whose rows start at multiples of 16 bytes (8 bits: of 8; of 16 there too, as
+    fs_cache_new has them, spares trees of many tokens reading the cache several times)."""
     k: object
     v: object
     k_scale: object = None
@@ -1080,6 +1081,7 @@ def fs_cache_write(cache: KVCache, table, positions, k, v, *, stream=None) -> No
     positions  int32 (batch, n): where each token goes; tokens with a negative position,
                beyond the table or without a page are left out.  The rows that one call
                writes are distinct: of two tokens at one place, parts of either may be left.
+    k and v lie outside the cache.
     """
     torch = _with_torch()
     batch, n, _, _ = _rows16(torch, k, "k")
@@ -1103,8 +1105,8 @@ def fs_cache_read(cache: KVCache, table, lens=None, n: Optional[int] = None, *, 
                   v=None, stream=None) -> Tuple:
     """Positions 0 .. n - 1 (None: all that the table has) of every sequence as k and v
     (batch, n, kv_heads, d) for fs_cross_attention: new ones of `dtype` (None: the cache's,
-    bfloat16 for 8 bits) or as given.  Zeros from lens[b] (int32 (batch,)) on and where
-    there is no page."""
+    bfloat16 for 8 bits) or as given; in 8 bits code x scale in float32, then rounded.  Zeros
+    from lens[b] (int32 (batch,)) on and where there is no page."""
     torch = _with_torch()
     like = cache[0]
     if not isinstance(like, torch.Tensor) or not like.is_cuda or like.dim() != 4:
@@ -1153,7 +1155,8 @@ def fs_tree_attention(q, cache: KVCache, table, ctx_len, parents=None, *,
                   chain does not end in -1 (-2, for padding) is not there: out 0, lse -inf.
                   None: a chain of tokens; n = 1 is ordinary decoding.
     scale         factor of the dot products, d ** -0.5 if None
-    Positions beyond the table or without a page do not count.
+    Positions beyond the table or without a page do not count.  A table no wider than the longest
+    sequence serves best: kernel and splits go by what it can hold.
     """
     torch = _with_torch()
     shape = batch, n, heads, d = _rows16(torch, q, "q")

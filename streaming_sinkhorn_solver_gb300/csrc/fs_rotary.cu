@@ -3,8 +3,8 @@
 // Bound by memory: every element is read and written once.  A block takes up to 8 tokens:
 // first the frequencies, then the sines and cosines of each token into shared memory, where
 // all their heads find them, then the heads, 16 bytes an access.  Measured: 2 x 8192 tokens of
-// 40 heads of 128, bfloat16: 57 us, 5.8 TB/s (0.86 of the measured copy rate); 3 x 2777 tokens of
-// 28 heads of 80, pairs of neighbours, half of the head, with the gradient: 34 us, 4.4 TB/s.
+// 40 heads of 128, bfloat16: 58 us, 5.7 TB/s (0.85 of the measured copy rate); 3 x 2777 tokens of
+// 28 heads of 80, pairs of neighbours, half of the head, with the gradient: 35 us, 4.3 TB/s.
 //
 // Angles.  A frequency is kept as a 64-bit fraction of a turn, F = frac(w / 2 pi) 2^64, so
 // that a position's angle is the low 64 bits of p F: whole turns fall away by themselves,

@@ -20,8 +20,8 @@
 // price, a reciprocal for an exponential, but takes 0 / vs_j from keys that a row does not see.)  Queries in bfloat16 become
 // float16, each row times a power of two (query_shift).
 //
-// Measured, 8 key heads of 128, 4 rows: 38 sequences of 8192 e4m3 keys 126 us, 5.2 TB/s (0.77 of
-// the measured copy rate; DRAM at 66 % of its peak, issue slots at 47 %: the latency of a warp's
+// Measured, 8 key heads of 128, 4 rows: 38 sequences of 8192 e4m3 keys 117 to 120 us, 5.5 TB/s (0.81
+// of the measured copy rate; DRAM at 69 % of its peak, issue slots at 47 %: the latency of a warp's
 // steps, with 8 warps to an SM); one sequence of 2000 bfloat16 keys 10 us, latency.
 #include "fs_tree.cuh"
 

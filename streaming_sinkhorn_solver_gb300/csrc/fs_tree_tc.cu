@@ -24,13 +24,16 @@
 // a row: the scales of its keys are then 24 loads of 8 bytes instead of 48 of 16 that
 // every lane reads alike, which took most of the shared memory's time.
 //
+// Weights go into the products in one 16-bit part: TMEM has no columns for a second.
+//
 // Bound: in 16 bits by memory with 64 rows (DRAM at 81 % of its peak), with 256 by the chain of
-// products and softmax (the tensor pipe is busy for 47 %).  In 8 bits a tile takes as long as one of
-// 16 bits, 0.75 us, with half the bytes: a tile is copied, widened, multiplied, weighed and
-// multiplied again, each by other warps that wait for the last ones.
+// products and softmax (the tensor pipe is busy for 47 %).  In 8 bits a tile takes nearly as long as
+// one of 16 bits, 0.7 us, with half the bytes: a tile is copied, widened, multiplied, weighed and
+// multiplied again, each by other warps that wait for the last ones; with 256 rows the weighing alone
+// is the longest.
 // Measured, 8 key heads of 128, 32 heads: 19 x 16 tokens, 8192 keys: bfloat16 99 us, 6.5 TB/s
-// (0.96 of the measured copy rate), e4m3 95 us, 3.5 TB/s; 19 x 64 tokens, 4096 bfloat16 keys: 73 us,
-// 1110 TFLOP/s and 4.7 TB/s.
+// (0.96 of the measured copy rate), e4m3 92 us, 3.6 TB/s; 19 x 64 tokens, 4096 keys: bfloat16 72 us,
+// 1130 TFLOP/s and 4.8 TB/s, e4m3 101 us, 804 TFLOP/s.
 #include "fs_tree.cuh"
 
 #include <type_traits>

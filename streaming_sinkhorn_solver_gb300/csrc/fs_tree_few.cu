@@ -16,8 +16,8 @@
 // so that the largest P of a row is the one that counts most in O, whatever the scales,
 // and float16 holds them all as it holds weights.  The sum's terms are up to 2^8 / vs_j, 2^97 for the
 // least scale that a row can have, and the one of the reference is 1 / vs, 2^-122 or more: float32
-// holds them all.  (The sum as that of P_ij / vs_j has the same
-// price, a reciprocal for an exponential, but takes 0 / vs_j from keys that a row does not see.)  Queries in bfloat16 become
+// holds them all.  (The sum as that of P_ij / vs_j has the same price, a reciprocal for an
+// exponential, but takes 0 / vs_j from keys that a row does not see.)  Queries in bfloat16 become
 // float16, each row times a power of two (query_shift).
 //
 // Measured, 8 key heads of 128, 4 rows: 38 sequences of 8192 e4m3 keys 117 to 120 us, 5.5 TB/s (0.81

@@ -852,7 +852,8 @@ __global__ void __launch_bounds__(Tc<HD, HELD, MODE>::kThreads, 1) k_tree_tc(con
             uint32_t p[8 * kLaneRows];         // p[16 h + 2 i + (k & 1)]
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint64_t iv = Q8 && (kPlain || !apart) ? *reinterpret_cast<const uint64_t*>(ts.iv + 8 * i + 2 * t4) : 0;
+                const uint64_t iv =
+                    Q8 && (kPlain || !apart) ? *reinterpret_cast<const uint64_t*>(ts.iv + 8 * i + 2 * t4) : 0;
 #pragma unroll
                 for (int k = 0; k < kLaneRows; ++k) {
                     const float* x = v + 32 * (k >> 1) + 4 * i + 2 * (k & 1);
